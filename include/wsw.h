@@ -5,8 +5,9 @@
  * The calls cover the memory-bound mat-vec y = W.x that streams every weight byte
  * once per decoded token, the block quantizer that turns the activation into int8
  * blocks with absmax scales in front of the quantized mat-vec, the grouped MoE
- * form of that mat-vec, the one-pass q8_0 KV-cache dequantizer and the
- * small-batch prefill GEMM.  Each call is one or more hand-written CUDA kernels.
+ * form of that mat-vec, the one-pass q8_0 KV-cache dequantizer, the small-batch prefill
+ * GEMM, attention, and the operators of a decode step around a paged KV cache.  Each call
+ * is one or more hand-written CUDA kernels.
  *
  * Sources (web pages, cited by title and section):
  *   [P1] "vulkan : dequant q8_0 KV once in coopmat1" (llama.cpp pull request)
@@ -435,6 +436,211 @@ int wsw_attn_prefill_q8_0(const uint16_t *q, const int8_t *kq, const uint16_t *k
  */
 int wsw_gemm_bf16(const uint16_t *W, int64_t M, int64_t K, int64_t ld, const uint16_t *X,
                   int64_t N, int64_t ldx, float *Y, void *stream, const wsw_launch_opts *opts);
+
+/* ------------------------------------------------------------------------------------
+ * A decode step around a paged KV cache.  Requests of different lengths share one pool of
+ * pages; a block table lists each request's pages in order.  wsw_kv_page_plan gives the
+ * step's new tokens their pages, positions and cache slots, wsw_rope_kv_write rotates q
+ * and k and writes K and V there, wsw_attn_paged_decode attends, and wsw_token_logprobs
+ * reads the lm_head's rows.  Lengths, tables and slots stay on the device, so that a step
+ * can be captured in a CUDA graph and replayed while they change.
+ */
+
+/* Element types of the calls below. */
+typedef enum wsw_dtype {
+    WSW_F32 = 0,
+    WSW_F16 = 1,  /* IEEE binary16 */
+    WSW_BF16 = 2,
+    WSW_Q8_0 = 3  /* int8 codes, one binary16 scale per 32 values (caches only) */
+} wsw_dtype;
+
+/*
+ * A paged KV cache.  Position p of a request lives in its page table[p / page_size] at
+ * offset p % page_size; a slot is page * page_size + offset.  The row of KV head h there is
+ * the head_dim elements at k + page * page_stride + offset * pos_stride + h * head_stride
+ * (v likewise); both orders of positions and heads inside a page, and K and V interleaved
+ * in one buffer, are strides.  q8_0 rows are int8 codes with head_dim / 32 binary16 scales
+ * at kd (vd) + page * d_page_stride + offset * d_pos_stride + h * d_head_stride, as
+ * wsw_quantize_q8 (block 32) writes them.
+ *
+ *   k, v         16-byte aligned; strides multiples of 16 bytes.
+ *   kd, vd       NULL unless dtype is WSW_Q8_0; base and strides multiples of
+ *                head_dim / 16 bytes.
+ *   page_size    a power of two, at most 65536.
+ *   head_dim     64, 128 or 256;  heads <= 65535;  1 <= num_pages < 2^31.
+ *   dtype        WSW_F16, WSW_BF16 or WSW_Q8_0.
+ * A null pointer, a size below 1 or a negative stride is WSW_ERR_INVALID_ARG, a type or
+ * size beyond these limits WSW_ERR_UNSUPPORTED.
+ */
+typedef struct wsw_kv_cache {
+    void *k, *v;
+    uint16_t *kd, *vd;
+    int64_t num_pages, page_size, heads, head_dim;
+    int64_t page_stride, pos_stride, head_stride;       /* elements of k and v */
+    int64_t d_page_stride, d_pos_stride, d_head_stride; /* elements of kd and vd */
+    int32_t dtype;                                      /* a wsw_dtype */
+} wsw_kv_cache;
+
+/*
+ * wsw_kv_page_plan -- block table and slot map of a step from the requests' lengths.
+ * Request r holds seq_len[r] cached tokens and adds new_len[r] (0 is fine); its new pages
+ * come from the list of free pages, in request order:
+ *   cu[r]        = sum of new_len before r;  need(r) = ceil((seq_len + new_len) / page_size)
+ *                  - ceil(seq_len / page_size);  off(r) = sum of need before r
+ *   table[r][j]  = free_pages[head + off(r) + j - ceil(seq_len / page_size)] for each new j
+ *   token cu[r] + i:  position = seq_len[r] + i,
+ *                     slot = table[r][position / page_size] * page_size + position % page_size
+ *   len_out[r]   = seq_len[r] + new_len[r];  head_out = head + pages taken
+ * A request that cannot be served keeps its length and takes no page, its tokens get
+ * position and slot -1, and a bit of *err_flag is set: 1 (bit 0) a negative length (it
+ * has no tokens); 2 more than max_pages pages (or 2^31 positions); 4 tokens beyond `tokens` (cu is cut there);
+ * 8 the free list ran out (the requests before it are served, it and those after it that
+ * need a page are not).  Tokens from cu[requests] to `tokens` get -1 and -1; a token whose
+ * table entry is negative gets slot -1.  Table entries other than the new ones are left
+ * as they are.
+ *
+ *   seq_len, new_len  int32 [requests].
+ *   free_pages        int32 [n_free]; head: int32 [1], the next free entry (outside
+ *                     [0, n_free]: nothing is free).
+ *   table             int32 [requests][table_stride], max_pages entries used of each row.
+ *   positions, slots  int32 and int64 [tokens];  cu int32 [requests + 1].
+ *   len_out, head_out may be seq_len and head themselves: every length is read before
+ *                     one is written.
+ *   err_flag          int32 [1] or NULL; bits are ORed in, never cleared.
+ *   requests <= 16384, page_size a power of two <= 65536, tokens and max_pages < 2^31
+ *   (WSW_ERR_UNSUPPORTED otherwise).  requests == 0 plans no token.
+ */
+int wsw_kv_page_plan(const int32_t *seq_len, const int32_t *new_len, int64_t requests, const int32_t *free_pages,
+                     int64_t n_free, const int32_t *head, int64_t page_size, int32_t *table, int64_t max_pages,
+                     int64_t table_stride, int64_t tokens, int32_t *positions, int64_t *slots, int32_t *cu,
+                     int32_t *len_out, int32_t *head_out, int32_t *err_flag, void *stream,
+                     const wsw_launch_opts *opts);
+
+/* How wsw_rope_table scales the frequencies f_i = theta^(-2 i / rot_dim) for contexts
+ * `factor` times as long as the `original` one. */
+typedef enum wsw_rope_scaling {
+    WSW_ROPE_PLAIN = 0,
+    WSW_ROPE_LINEAR = 1,  /* f_i / factor */
+    WSW_ROPE_NTK = 2,     /* theta * factor^(rot_dim / (rot_dim - 2)) in place of theta */
+    WSW_ROPE_BY_PARTS = 3 /* between f_i / factor for pairs that turn at most once over
+                             `original` positions and f_i for those that turn 32 times or
+                             more, linear in the turns (NTK-by-parts of "YaRN: Efficient
+                             Context Window Extension of Large Language Models", section
+                             3.2); cos and sin times 0.1 ln(factor) + 1 (section 3.3) */
+} wsw_rope_scaling;
+
+/*
+ * wsw_rope_table -- host: the per-pair frequencies of wsw_rope_kv_write in fractions of a
+ * turn, turns[i] = round(2^64 * f_i / (2 pi)), and the factor on cos and sin.  A
+ * position's angle is then the exact 64-bit product position * turns[i] modulo one turn,
+ * as good at position 2^30 as at 1.
+ *   freqs    NULL, or rot_dim / 2 radians per position of the caller's own, in [0, 2 pi):
+ *            they are taken as given and theta, scaling, factor, original ignored.
+ *   turns    host uint64 [rot_dim / 2];  mscale: host float.
+ * WSW_ERR_INVALID_ARG: rot_dim not a positive even number (<= 256; > 2 for NTK),
+ * theta <= 1, factor < 1, original < 1 (BY_PARTS), or a frequency outside [0, 2 pi).
+ */
+int wsw_rope_table(int64_t rot_dim, double theta, int32_t scaling, double factor, int64_t original,
+                   const double *freqs, uint64_t *turns, float *mscale);
+
+/*
+ * wsw_rope_kv_write -- rotary positions of q and k, and the write of k and v into the
+ * paged cache, in one pass.  Pair i < rot_dim / 2 of a head is (x[i], x[i + rot_dim / 2]),
+ * or (x[2 i], x[2 i + 1]) with interleaved = 1; with angle a = positions[t] * 2 pi *
+ * turns[i] / 2^64 it becomes
+ *   mscale * (x0 cos a - x1 sin a, x1 cos a + x0 sin a);
+ * the dimensions from rot_dim on are copied.  q goes to q_out, k and v to the row of
+ * slots[t] in the cache, rounded once to its type (q8_0: by wsw_quantize_q8's rule).
+ * A token with a negative position is padding: its q_out row is zero and nothing is
+ * cached.  One with a negative slot is rotated and not cached; a slot outside the cache
+ * is treated so too and sets bit 0 of *err_flag.  Two tokens of one call must not share
+ * a slot.
+ *
+ *   q         `dtype` [tokens][q_heads][head_dim] with the given token and head strides
+ *             (elements), unit stride in head_dim; k and v likewise with cache->heads heads:
+ *             views of one fused QKV row or separate tensors.
+ *   dtype     WSW_F32, WSW_F16 or WSW_BF16, of q, k, v and q_out.  16-byte aligned bases
+ *             and strides give the widest loads; others take narrower ones.
+ *   turns     device uint64 [rot_dim / 2] (from wsw_rope_table);  rot_dim even, <= head_dim.
+ *   q_out     `dtype` [tokens][q_heads][head_dim], packed; it may be q itself only when q is
+ *             packed, too.
+ *   positions int32 [tokens];  slots int64 [tokens].
+ * q_heads may be 0.  tokens == 0 does nothing.
+ */
+int wsw_rope_kv_write(const void *q, const void *k, const void *v, int32_t dtype, int64_t tokens, int64_t q_heads,
+                      int64_t q_tok_stride, int64_t q_head_stride, int64_t k_tok_stride, int64_t k_head_stride,
+                      int64_t v_tok_stride, int64_t v_head_stride, const uint64_t *turns, int64_t rot_dim,
+                      float mscale, int32_t interleaved, const int32_t *positions, const int64_t *slots,
+                      void *q_out, const wsw_kv_cache *cache, int32_t *err_flag, void *stream,
+                      const wsw_launch_opts *opts);
+
+/*
+ * wsw_attn_paged_decode -- attention of one new token per request over a paged cache.
+ * For request r with n = lens[r] cached tokens (the new one, at position n - 1, among
+ * them), query head a = h * group + g of KV head h and every position p that it sees
+ * (max(0, n - window) <= p < n; window = 0: all p < n):
+ *   x_p  = scale * q[r][a] . K(h, p);  x_p = softcap * tanh(x_p / softcap) if softcap > 0
+ *   x_p -= slopes[a] * (n - 1 - p)     if slopes != NULL
+ *   out[r][a] = sum_p exp(x_p - m) V(h, p) / sum_p exp(x_p - m);  lse[r][a] = ln sum_p exp(x_p)
+ * K(h, p) and V(h, p) are the cached rows; a q8_0 value is binary16(scale * code), the
+ * value wsw_dequant_q8_0_kv writes.  A request of length 0 (an unused row of a padded
+ * batch) gets out = 0 and lse = -inf.  Positions past lens[r] in a page are never used.
+ *
+ * Scores, the softmax's maximum and sum, and the value sums are fp32.  The products run
+ * on tensor cores in the cache's 16-bit type (binary16 for q8_0); q and the softmax
+ * weights enter as a high part plus a residual in that type, so that they keep about 22
+ * bits (binary16) or 16 bits (bf16; a bf16 q is exact).
+ *
+ *   q, out    `dtype` (WSW_F32, WSW_F16 or WSW_BF16) [requests][q_heads][head_dim], packed,
+ *             16-byte aligned; q_heads = group * cache->heads, any group >= 1.
+ *   table     int32 [requests][table_stride], max_pages entries of each row used.  An
+ *             entry outside [0, num_pages) hides its positions and sets bit 0 of *err_flag.
+ *   lens      int32 [requests]; below 0 or above max_pages * page_size is cut to that
+ *             range and sets bit 1.
+ *   lse       fp32 [requests][q_heads] or NULL;  slopes fp32 [q_heads] or NULL.
+ *   scale     finite; softcap finite, >= 0;  0 <= window < 2^31.
+ *   ws        device workspace of ws_bytes >= wsw_attn_paged_decode_workspace_bytes(...)
+ *             bytes, 16-byte aligned, zero-filled before its first use and then reused:
+ *             its arrival counters are zero again after every call.  Two calls in flight
+ *             at once need two workspaces.
+ *   requests <= 65535 and requests * q_heads < 2^31;  max_pages * page_size < 2^31.
+ * One launch; results depend on the arguments alone, not on the launch or the device.
+ */
+size_t wsw_attn_paged_decode_workspace_bytes(int64_t requests, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t requests, int64_t q_heads,
+                          const wsw_kv_cache *cache, const int32_t *table, int64_t max_pages, int64_t table_stride,
+                          const int32_t *lens, float scale, float softcap, int64_t window, const float *slopes,
+                          void *out, float *lse, int32_t *err_flag, void *ws, size_t ws_bytes, void *stream,
+                          const wsw_launch_opts *opts);
+
+/*
+ * wsw_token_logprobs -- what a step answers with, in one pass over its logits: for each row
+ * x of `vocab` logits, y = scale * x, and its token t,
+ *   lse = ln sum_j exp(y_j);  logprob = y_t - lse;  entropy = -sum_j p_j ln p_j, p = exp(y - lse)
+ *   rank = number of j with x_j > x_t, or x_j = x_t and j < t (0: the most likely token)
+ *   top_id[i], top_logprob[i], i < top: the i-th largest x_j (ties: the lower j first), y_j - lse
+ * -inf logits (forbidden tokens) have probability 0.  A row of nothing but -inf has
+ * lse = -inf, entropy = 0 and every log probability -inf.  A NaN or +inf logit makes the
+ * row's fp32 results NaN (its ids stay within [-1, vocab)).  A token outside [0, vocab)
+ * gets logprob NaN and rank -1.
+ *
+ *   logits   `dtype` (WSW_F32, WSW_F16 or WSW_BF16) [rows][ld], ld >= vocab, aligned to
+ *            its element.
+ *   tokens   int32 [rows], or NULL with logprob and rank NULL.
+ *   scale    finite, > 0 (1 / temperature).
+ *   top      0 .. 32, at most vocab; with 0 top_logprob and top_id may be NULL.
+ *   logprob, lse, entropy fp32 [rows];  rank int32 [rows];  top_logprob fp32 and top_id
+ *            int32 [rows][top].
+ *   ws       device workspace of ws_bytes >= wsw_token_logprobs_workspace_bytes(...) bytes
+ *            (0: none needed, ws may be NULL), 16-byte aligned, zero-filled before its
+ *            first use and then reused, as the attention's.
+ *   1 <= vocab < 2^31;  rows < 2^31.  rows == 0 does nothing.
+ */
+size_t wsw_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top);
+int wsw_token_logprobs(const void *logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                       const int32_t *tokens, float scale, int32_t top, float *logprob, int32_t *rank, float *lse,
+                       float *entropy, float *top_logprob, int32_t *top_id, void *ws, size_t ws_bytes, void *stream,
+                       const wsw_launch_opts *opts);
 
 /*
  * wsw_bounded_wait_check -- run the bounded mbarrier wait of the tensor-core kernels

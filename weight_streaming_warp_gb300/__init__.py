@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -21,7 +22,9 @@ __all__ = [
     "gemv_bf16_chain", "gemv_q8_0", "quantize_gemv_q8_0", "moe_gemv_q8_0", "dequant_q8_0_kv", "gemm_bf16",
     "upload_padded", "status_string", "abi_version", "moe_workspace_bytes", "gemv_bf16_plan",
     "bounded_wait_check", "attn_decode_f16", "attn_decode_workspace_bytes", "attn_prefill_f16",
-    "attn_prefill_q8_0", "attn_prefill_q8_0_workspace_bytes",
+    "attn_prefill_q8_0", "attn_prefill_q8_0_workspace_bytes", "PagedKV", "KvPlan", "kv_page_plan", "RopeTable",
+    "rope_table", "rope_kv_write", "attn_paged_decode", "attn_paged_decode_workspace_bytes", "TokenLogprobs",
+    "token_logprobs", "token_logprobs_out", "token_logprobs_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -50,6 +53,14 @@ class _CLink(ctypes.Structure):
 class _CPlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("load_bytes", "rows_per_warp", "pdl", "ctas", "threads",
                                                "log2_segments", "x_in_smem", "l2_prefetch_steps")]
+
+
+class _CKv(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "kd", "vd")]
+                + [(n, ctypes.c_int64) for n in ("num_pages", "page_size", "heads", "head_dim", "page_stride",
+                                                 "pos_stride", "head_stride", "d_page_stride", "d_pos_stride",
+                                                 "d_head_stride")]
+                + [("dtype", ctypes.c_int32)])
 
 
 @dataclass
@@ -105,6 +116,22 @@ def load():
     L.wsw_attn_prefill_q8_0.argtypes = [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _f32, _i64, _p,
                                         ctypes.c_size_t, _p, _p, _p]
     L.wsw_attn_prefill_q8_0.restype = ctypes.c_int
+    L.wsw_kv_page_plan.argtypes = [_p, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p,
+                                   _p]
+    L.wsw_rope_table.argtypes = [_i64, ctypes.c_double, _i32, ctypes.c_double, _i64, _p, _p, _p]
+    L.wsw_rope_kv_write.argtypes = [_p, _p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _p, _i64, _f32,
+                                    _i32, _p, _p, _p, _p, _p, _p, _p]
+    L.wsw_attn_paged_decode_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
+    L.wsw_attn_paged_decode_workspace_bytes.restype = ctypes.c_size_t
+    L.wsw_attn_paged_decode.argtypes = [_p, _i32, _i64, _i64, _p, _p, _i64, _i64, _p, _f32, _f32, _i64, _p, _p, _p, _p,
+                                        _p, ctypes.c_size_t, _p, _p]
+    L.wsw_token_logprobs_workspace_bytes.argtypes = [_i64, _i64, _i64]
+    L.wsw_token_logprobs_workspace_bytes.restype = ctypes.c_size_t
+    L.wsw_token_logprobs.argtypes = [_p, _i32, _i64, _i64, _i64, _p, _f32, _i32, _p, _p, _p, _p, _p, _p, _p,
+                                     ctypes.c_size_t, _p, _p]
+    for f in ("wsw_kv_page_plan", "wsw_rope_table", "wsw_rope_kv_write", "wsw_attn_paged_decode",
+              "wsw_token_logprobs"):
+        getattr(L, f).restype = ctypes.c_int
     for f in ("wsw_quantize_q8", "wsw_gemv_bf16", "wsw_gemv_bf16_chain", "wsw_gemv_q8_0", "wsw_quantize_gemv_q8_0",
               "wsw_moe_gemv_q8_0", "wsw_dequant_q8_0_kv", "wsw_gemm_bf16", "wsw_gemv_bf16_plan",
               "wsw_bounded_wait_check", "wsw_attn_decode_f16", "wsw_attn_prefill_f16"):
@@ -408,6 +435,262 @@ def attn_prefill_q8_0(q, kq, kd, vq, vd, window, scale=None, out=None, ws=None, 
                                         depth, heads, group, nq, hd, float(scale), int(window), ws.data_ptr(),
                                         ws.numel(), y.data_ptr(), _stream(), _opts(opts)), "attn_prefill_q8_0")
     return y
+
+
+# ------------------------------------------------- a step around a paged KV cache ----
+
+_FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # wsw_dtype
+_CACHES = {torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
+
+
+def _float_dev(t, name):
+    code = _FLOATS.get(t.dtype) if isinstance(t, torch.Tensor) and t.is_cuda else None
+    if code is None:
+        raise WswError("%s must be a CUDA tensor of float32, float16 or bfloat16" % name)
+    return code
+
+
+def _packed(t, dtype, name, shape=None):
+    """The address of a contiguous device tensor."""
+    _dev(t, dtype, name)
+    if not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+        raise WswError("%s must be contiguous%s" % (name, "" if shape is None else " of shape %s" % (shape,)))
+    return t.data_ptr()
+
+
+class PagedKV:
+    """A paged KV cache of one layer: pages shared by all requests.  k and v: fp16, bf16 or
+    (q8_0) int8, [pages][page_size][heads][head_dim] (layout "nhd") or
+    [pages][heads][page_size][head_dim] ("hnd"), any strides but unit in head_dim and the
+    same for both; kd and vd: the q8_0 scales, fp16, head_dim / 32 in the last dimension.
+    page_size a power of two, head_dim 64, 128 or 256.  The object holds the tensors."""
+
+    def __init__(self, k, v, kd=None, vd=None, layout="nhd"):
+        if layout not in ("nhd", "hnd"):
+            raise WswError("layout must be 'nhd' or 'hnd'")
+        dtype = _CACHES.get(k.dtype) if isinstance(k, torch.Tensor) and k.is_cuda else None
+        if dtype is None:
+            raise WswError("k must be a CUDA tensor of float16, bfloat16 or int8")
+        _dev(v, k.dtype, "v")
+        if k.dim() != 4 or k.stride(3) != 1 or k.shape != v.shape or k.stride() != v.stride():
+            raise WswError("k and v must be 4-D views of equal shape and strides, unit in head_dim")
+        pos, head = (1, 2) if layout == "nhd" else (2, 1)
+        c = _CKv(k.data_ptr(), v.data_ptr(), None, None, k.shape[0], k.shape[pos], k.shape[head], k.shape[3],
+                 k.stride(0), k.stride(pos), k.stride(head), 0, 0, 0, dtype)
+        if dtype == 3:
+            _dev(kd, torch.float16, "kd")
+            _dev(vd, torch.float16, "vd")
+            if (tuple(kd.shape) != tuple(k.shape[:3]) + (k.shape[3] // 32,) or kd.shape != vd.shape
+                    or kd.stride() != vd.stride() or kd.stride(3) != 1):
+                raise WswError("kd and vd must be [..][head_dim / 32] views with equal strides, unit in the last")
+            c.kd, c.vd = kd.data_ptr(), vd.data_ptr()
+            c.d_page_stride, c.d_pos_stride, c.d_head_stride = kd.stride(0), kd.stride(pos), kd.stride(head)
+        elif kd is not None or vd is not None:
+            raise WswError("kd and vd belong to an int8 cache")
+        self.k, self.v, self.kd, self.vd, self.layout = k, v, kd, vd, layout
+        self.num_pages, self.page_size, self.heads, self.head_dim = k.shape[0], k.shape[pos], k.shape[head], k.shape[3]
+        self._c = c
+        self._ref = ctypes.addressof(c)
+
+
+class KvPlan(NamedTuple):
+    positions: torch.Tensor  # int32 [tokens]
+    slots: torch.Tensor      # int64 [tokens]
+    cu: torch.Tensor         # int32 [requests + 1]
+    seq_len: torch.Tensor    # int32 [requests], with the new tokens
+    head: torch.Tensor       # int32 [1]
+
+
+def kv_page_plan(seq_len, new_len, free_pages, head, table, page_size, tokens, out=None, err_flag=None, opts=None):
+    """Pages, positions and cache slots of a step's new tokens, on the device.  Request r
+    has seq_len[r] cached tokens and adds new_len[r]; the pages that it opens are taken
+    from free_pages[head ..] and written into its row of table (int32 [requests][max_pages],
+    updated in place).  `tokens` is the room for the step's tokens: rows beyond their sum
+    get position and slot -1, as do the tokens of a request that does not fit (err_flag,
+    an int32 device tensor, tells why: wsw.h).  Returns a KvPlan; out = such a tuple of
+    tensors to fill, in which seq_len and head may be the arguments themselves."""
+    n = seq_len.shape[0]
+    _packed(seq_len, torch.int32, "seq_len")
+    _packed(new_len, torch.int32, "new_len", (n,))
+    _packed(free_pages, torch.int32, "free_pages")
+    _packed(head, torch.int32, "head", (1,))
+    _dev(table, torch.int32, "table")
+    if table.dim() != 2 or table.shape[0] != n or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise WswError("table must be [requests][max_pages] with unit stride in max_pages")
+    if out is None:
+        dev = seq_len.device
+        out = KvPlan(torch.empty(tokens, dtype=torch.int32, device=dev),
+                     torch.empty(tokens, dtype=torch.int64, device=dev),
+                     torch.empty(n + 1, dtype=torch.int32, device=dev), torch.empty_like(seq_len),
+                     torch.empty_like(head))
+    else:
+        out = KvPlan(*out)
+    err = _packed(err_flag, torch.int32, "err_flag") if err_flag is not None else None
+    _check(load().wsw_kv_page_plan(
+        seq_len.data_ptr(), new_len.data_ptr(), n, free_pages.data_ptr(), free_pages.shape[0], head.data_ptr(),
+        page_size, table.data_ptr(), table.shape[1], max(table.stride(0), table.shape[1]) if n > 1 else table.shape[1],
+        tokens, _packed(out.positions, torch.int32, "positions", (tokens,)),
+        _packed(out.slots, torch.int64, "slots", (tokens,)), _packed(out.cu, torch.int32, "cu", (n + 1,)),
+        _packed(out.seq_len, torch.int32, "seq_len (out)", (n,)), _packed(out.head, torch.int32, "head (out)", (1,)),
+        err, _stream(), _opts(opts)), "kv_page_plan")
+    return out
+
+
+class RopeTable(NamedTuple):
+    turns: torch.Tensor  # int64 (the bits of uint64) [rot_dim / 2]: turns per position, times 2^64
+    mscale: float
+    rot_dim: int
+
+
+_ROPE_SCALING = {None: 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
+def rope_table(rot_dim, theta=10000.0, scaling=None, factor=1.0, original=0, freqs=None, device="cuda"):
+    """The frequencies of rope_kv_write, made once per model: theta^(-2 i / rot_dim), scaled
+    for contexts `factor` times the `original` length by "linear", "ntk" or "by_parts"
+    (wsw.h), or freqs, the caller's own rot_dim / 2 radians per position."""
+    if scaling not in _ROPE_SCALING:
+        raise WswError("scaling must be one of None, 'linear', 'ntk', 'by_parts'")
+    turns = (ctypes.c_uint64 * max(rot_dim // 2, 1))()
+    mscale = ctypes.c_float()
+    arr = None
+    if freqs is not None:
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != rot_dim // 2:
+            raise WswError("freqs must have rot_dim / 2 values")
+        arr = (ctypes.c_double * len(freqs))(*freqs)
+    _check(load().wsw_rope_table(rot_dim, theta, _ROPE_SCALING[scaling], factor, original, arr, turns,
+                                 ctypes.byref(mscale)), "rope_table")
+    t = torch.tensor([v - (1 << 64) if v >> 63 else v for v in turns], dtype=torch.int64)
+    return RopeTable(t.to(device), mscale.value, rot_dim)
+
+
+def _rows3(t, name, tokens, heads, hd):
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != hd or (heads is not None and t.shape[1] != heads) or (
+            t.stride(2) != 1 and hd > 1):
+        raise WswError("%s must be a [tokens][heads][head_dim] view with unit stride in head_dim" % name)
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def rope_kv_write(q, k, v, rope, positions, slots, kv, interleaved=False, out=None, err_flag=None, opts=None):
+    """Rotates q [tokens][q_heads][head_dim] and k [tokens][kv_heads][head_dim] by their
+    positions and writes k and v into the cache at their slots, in one pass; returns the
+    rotated q (packed, q's dtype; out = the tensor to fill).  q, k, v: fp32, fp16 or bf16
+    views with any token and head strides, for instance of one fused QKV row.  rope: a
+    RopeTable; positions int32 and slots int64 [tokens], as kv_page_plan gives them.
+    interleaved: pairs (2 i, 2 i + 1) instead of (i, i + rot_dim / 2)."""
+    code = _float_dev(q, "q")
+    _dev(k, q.dtype, "k")
+    _dev(v, q.dtype, "v")
+    n, heads, hd = q.shape
+    if hd != kv.head_dim:
+        raise WswError("q must have the cache's head_dim")
+    qp, qt, qh = _rows3(q, "q", n, None, hd)
+    kp, kt, kh = _rows3(k, "k", n, kv.heads, hd)
+    vp, vt, vh = _rows3(v, "v", n, kv.heads, hd)
+    if out is None:
+        out = torch.empty((n, heads, hd), dtype=q.dtype, device=q.device)
+    err = _packed(err_flag, torch.int32, "err_flag") if err_flag is not None else None
+    _check(load().wsw_rope_kv_write(
+        qp, kp, vp, code, n, heads, qt, qh, kt, kh, vt, vh, rope.turns.data_ptr(), rope.rot_dim, rope.mscale,
+        int(bool(interleaved)), _packed(positions, torch.int32, "positions", (n,)),
+        _packed(slots, torch.int64, "slots", (n,)), _packed(out, q.dtype, "out", (n, heads, hd)), kv._ref, err,
+        _stream(), _opts(opts)), "rope_kv_write")
+    return out
+
+
+def attn_paged_decode_workspace_bytes(requests, q_heads, kv_heads, head_dim) -> int:
+    return int(load().wsw_attn_paged_decode_workspace_bytes(requests, q_heads, kv_heads, head_dim))
+
+
+def attn_paged_decode(q, kv, table, lens, scale=None, softcap=0.0, window=0, slopes=None, out=None, lse=None,
+                      err_flag=None, ws=None, opts=None):
+    """Attention of one new token per request over the paged cache kv (a PagedKV).
+    q [requests][q_heads][head_dim] (contiguous, fp32, fp16 or bf16; q_heads a multiple of
+    the cache's heads); table int32 [requests][max_pages]; lens int32 [requests], the
+    cached tokens with the new one.  scale defaults to 1 / sqrt(head_dim); softcap > 0
+    caps the scores by softcap * tanh(score / softcap); window > 0 shows only the last
+    `window` positions; slopes fp32 [q_heads] subtracts slope * distance.  Returns out
+    (q's dtype); lse, an fp32 [requests][q_heads] tensor, receives the log of the sum of
+    exponentials.  A request of length 0 gives zeros and -inf.  ws: a uint8 device tensor
+    of at least attn_paged_decode_workspace_bytes(...) bytes, zero-filled before its first
+    use (every call leaves it ready for the next), allocated if None."""
+    code = _float_dev(q, "q")
+    if q.dim() != 3 or not q.is_contiguous():
+        raise WswError("q must be a contiguous [requests][q_heads][head_dim] tensor")
+    n, heads, hd = q.shape
+    if hd != kv.head_dim or heads % kv.heads != 0:
+        raise WswError("q must have the cache's head_dim and a multiple of its heads")
+    _dev(table, torch.int32, "table")
+    if table.dim() != 2 or table.shape[0] != n or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise WswError("table must be [requests][max_pages] with unit stride in max_pages")
+    if scale is None:
+        scale = 1.0 / float(hd) ** 0.5
+    if out is None:
+        out = torch.empty_like(q)
+    if ws is None:
+        ws = torch.zeros(attn_paged_decode_workspace_bytes(n, heads, kv.heads, hd), dtype=torch.uint8,
+                         device=q.device)
+    _check(load().wsw_attn_paged_decode(
+        q.data_ptr(), code, n, heads, kv._ref, table.data_ptr(), table.shape[1],
+        max(table.stride(0), table.shape[1]) if n > 1 else table.shape[1], _packed(lens, torch.int32, "lens", (n,)),
+        scale, softcap, window, _packed(slopes, torch.float32, "slopes", (heads,)) if slopes is not None else None,
+        _packed(out, q.dtype, "out", (n, heads, hd)),
+        _packed(lse, torch.float32, "lse", (n, heads)) if lse is not None else None,
+        _packed(err_flag, torch.int32, "err_flag") if err_flag is not None else None, ws.data_ptr(), ws.numel(),
+        _stream(), _opts(opts)), "attn_paged_decode")
+    return out
+
+
+class TokenLogprobs(NamedTuple):
+    logprob: Optional[torch.Tensor]  # fp32 [rows] (None without tokens)
+    rank: Optional[torch.Tensor]     # int32 [rows]
+    lse: torch.Tensor                # fp32 [rows]
+    entropy: torch.Tensor            # fp32 [rows]
+    top_logprob: torch.Tensor        # fp32 [rows][top]
+    top_id: torch.Tensor             # int32 [rows][top]
+
+
+def token_logprobs_workspace_bytes(rows, vocab, top) -> int:
+    return int(load().wsw_token_logprobs_workspace_bytes(rows, vocab, top))
+
+
+def token_logprobs_out(rows, top, tokens=True, device="cuda") -> TokenLogprobs:
+    """Tensors for token_logprobs to fill."""
+    f = lambda *s: torch.empty(s, dtype=torch.float32, device=device)  # noqa: E731
+    i = lambda *s: torch.empty(s, dtype=torch.int32, device=device)  # noqa: E731
+    return TokenLogprobs(f(rows) if tokens else None, i(rows) if tokens else None, f(rows), f(rows), f(rows, top),
+                         i(rows, top))
+
+
+def token_logprobs(logits, tokens=None, top=0, scale=1.0, out=None, ws=None, opts=None):
+    """Per row of logits [rows][vocab] (fp32, fp16 or bf16, any row stride), with y = scale *
+    logits: the log probability and rank of its token (int32 [rows], or None), the log of
+    the sum of exponentials, the entropy, and the `top` (at most 32) most likely tokens
+    with their log probabilities, equal ones by the lower id.  Returns a TokenLogprobs
+    (out = one to fill).  ws: a uint8 device tensor of at least
+    token_logprobs_workspace_bytes(...) bytes, zero-filled before its first use, allocated
+    if None."""
+    code = _float_dev(logits, "logits")
+    rows, vocab, ld = _rowmajor(logits, "logits")
+    if out is None:
+        out = token_logprobs_out(rows, top, tokens is not None, logits.device)
+    need = token_logprobs_workspace_bytes(rows, vocab, top)
+    if ws is None and need:
+        ws = torch.zeros(need, dtype=torch.uint8, device=logits.device)
+    tp = lp = rp = None
+    if tokens is not None:
+        tp = _packed(tokens, torch.int32, "tokens", (rows,))
+        lp = _packed(out.logprob, torch.float32, "logprob", (rows,))
+        rp = _packed(out.rank, torch.int32, "rank", (rows,))
+    _check(load().wsw_token_logprobs(
+        logits.data_ptr(), code, rows, vocab, ld, tp, scale, top, lp, rp, _packed(out.lse, torch.float32, "lse", (rows,)),
+        _packed(out.entropy, torch.float32, "entropy", (rows,)),
+        _packed(out.top_logprob, torch.float32, "top_logprob", (rows, top)) if top else None,
+        _packed(out.top_id, torch.int32, "top_id", (rows, top)) if top else None,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, _stream(), _opts(opts)),
+        "token_logprobs")
+    return out
 
 
 def upload_padded(W: torch.Tensor, ld: int, device=None) -> torch.Tensor:

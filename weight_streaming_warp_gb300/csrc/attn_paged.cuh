@@ -1,0 +1,815 @@
+// attn_paged.cuh -- attention of one new token per request over a paged KV cache.
+//
+//   y_p = scale q . K_p (capped by softcap tanh(. / softcap), minus slope (n - 1 - p))
+//   out = sum_p 2^(y_p - m) V_p / sum_p 2^(y_p - m), y in log2 units, m = max_p y_p
+//
+// Bound: every seen K and V byte once (2 head_dim values per position and KV head) against
+// 2 * group multiply-adds per value; HBM bandwidth for any group up to 16.  So the layout of
+// the work is about keeping loads in flight on every SM whatever the requests' lengths:
+//  * One list of tiles.  A tile is 16 positions of one pair (request, KV head); the tiles of
+//    all pairs, in order, are cut into equal runs for 152 CTAs and those into equal runs for
+//    their warps.  Nothing is launched per request and no SM waits for a long one; lengths are
+//    read on the device, each CTA scanning them once.
+//  * Each warp streams its run through a private ring of shared-memory stages with cp.async,
+//    across pair boundaries without a drain, and keeps its own softmax (running maximum, sum,
+//    value sums) in registers: no block barrier until its run ends.
+//  * A pair that lies in one warp's run is written by that warp.  Otherwise the warps leave
+//    (m, l, sums) records, the CTA joins its own, and when a pair spans CTAs the last of them to
+//    arrive (a counter in the workspace) joins theirs, in tile order, so that results do not
+//    depend on timing.  A CTA has at most two pairs that it shares with others.
+//
+// Products on m16n8k16 tensor-core tiles with fp32 sums.  Up to eight query heads of a KV head
+// share a 16-row operand as high parts (rows 0..7) and residuals (8..15) of q and of the
+// weights; 9 to 16 take 16 rows and a second product for the residuals; more take several
+// passes over the pair.  The weights are scaled by 2^kShift: their residuals stay above
+// binary16's subnormals.  q8_0 rows stay codes in shared memory and become binary16(scale *
+// code) in registers, the value the one-pass dequantizer writes.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv_cache.cuh"
+
+namespace wsw {
+namespace paged {
+
+constexpr int kTile = 16;      // positions per tile
+constexpr int kCtas = 152;     // runs of the tile list: one CTA per SM of a 152-SM part
+constexpr float kShift = 8.f;  // log2 of the weights' scale
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kSmemMax = 226 * 1024;
+
+struct Args {
+    const void *q;
+    void *out;
+    float *lse;
+    const float *slopes;
+    const int32_t *table, *lens;
+    int32_t *err;
+    unsigned *cnt;  // [kCtas] arrival counters (zero between calls), by a pair's first CTA
+    float *rec;     // [kCtas][2][rows][D + 4] what a CTA leaves of its shared pairs
+    float *wrec;    // [kCtas][warps][rows][D + 4] what a warp leaves of its first pair
+    KvView kv;
+    int64_t table_stride;
+    float scale2;     // scale log2 e
+    float cap_in;     // scale / softcap, 0: not capped
+    float cap_out;    // softcap log2 e
+    int requests, q_heads, group, passes;  // passes = ceil(group / rows)
+    int max_len, window;                   // window > 0
+    int dtype;                             // of q and out
+};
+
+// Shape of one variant: cache type, head_dim, query rows (8 or 16).
+template <int CT, int D, int RT>
+struct Cfg {
+    static constexpr bool q8 = CT == WSW_Q8_0;
+    static constexpr int warps = D == 256 ? 4 : 8;
+    static constexpr int threads = warps * 32;
+    static constexpr int row_bytes = q8 ? D : 2 * D;
+    static constexpr int pieces = row_bytes / 16;      // 16-byte pieces of a row
+    static constexpr int scale_bytes = q8 ? D / 16 : 0;
+    static constexpr int kv_bytes = kTile * row_bytes;  // K (or V) rows of a tile
+    static constexpr int stage = 2 * kv_bytes + 2 * kTile * scale_bytes;
+    static constexpr int ksteps = D / 16;
+    static constexpr bool q_smem = D == 256;            // q's high parts: registers if they fit
+    static constexpr int qfrag = ksteps * 512;          // bytes of one warp's A fragments
+    static constexpr int q_bytes = (q_smem ? qfrag : 0) + (RT == 16 ? qfrag : 0);
+    static constexpr int fit = (kSmemMax - warps * q_bytes) / (warps * stage);
+    static constexpr int stages = fit < 6 ? fit : 6;
+    static constexpr int ring = stages * stage;
+    static constexpr int smem = warps * (ring + q_bytes);
+    static constexpr int rec = D + 4;                   // floats: m, l, 2 pad, sums
+    static_assert(stages >= 2 && RT * rec * 4 <= ring && ring % 16 == 0, "ring");
+};
+
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// copies of 16 (or 4, 8) bytes that write zeros and read nothing when !valid
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+template <int B>
+__device__ __forceinline__ void cp_small(uint32_t dst, const void *src, bool valid) {
+    if constexpr (B == 16) cp16(dst, src, valid);
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(valid ? B : 0)
+                     : "memory");
+}
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(p) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(p) : "memory");
+}
+template <int CT>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (CT == WSW_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                     "{%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                     "{%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// (x, y) as a pair of 16-bit values, and what the rounding left of each as another pair
+template <int CT>
+__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+    if constexpr (CT == WSW_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(x - bf16lo(hi), y - bf16hi(hi));
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        const float2 f = __half22float2(h);
+        const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    }
+}
+// Two codes, bytes `sel` picks from w (biased by 128), times the scales in d: 0x6400 + u is
+// 1024 + u in binary16, so both steps before the product are exact.
+__device__ __forceinline__ uint32_t dequant2(uint32_t biased, uint32_t sel, __half2 d) {
+    const uint32_t h = __byte_perm(biased, 0x64646464u, sel);
+    const uint32_t bias = 0x64806480u;  // 1152
+    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&bias)), d);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ float2 load_q2(const Args &a, int64_t i) {
+    if (a.dtype == WSW_F32) return reinterpret_cast<const float2 *>(a.q)[i >> 1];
+    const uint32_t u = reinterpret_cast<const uint32_t *>(a.q)[i >> 1];
+    if (a.dtype == WSW_BF16) return make_float2(bf16lo(u), bf16hi(u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+__device__ __forceinline__ void store_out4(const Args &a, int64_t i, float4 v) {
+    if (a.dtype == WSW_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i) = v;
+    } else if (a.dtype == WSW_BF16) {
+        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = *reinterpret_cast<uint2 *>(h);
+    } else {
+        __half2 h[2] = {__floats2half2_rn(v.x, v.y), __floats2half2_rn(v.z, v.w)};
+        *reinterpret_cast<uint2 *>(static_cast<__half *>(a.out) + i) = *reinterpret_cast<uint2 *>(h);
+    }
+}
+__device__ __forceinline__ void store_out2(const Args &a, int64_t i, float x, float y) {
+    if (a.dtype == WSW_F32) {
+        *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + i) = make_float2(x, y);
+    } else if (a.dtype == WSW_BF16) {
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = __floats2bfloat162_rn(x, y);
+    } else {
+        *reinterpret_cast<__half2 *>(static_cast<__half *>(a.out) + i) = __floats2half2_rn(x, y);
+    }
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
+}
+// weight of a record with maximum m against the common maximum
+__device__ __forceinline__ float weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
+
+// Where a warp is in the tile list: request, head and pass, tile of the pair.
+struct Cursor {
+    int64_t g;   // index in the list
+    int r, hp, t, nt;
+    int start, len;  // seen positions are [start, len)
+};
+// A piece of a pair left as a record: the pair, its first tile's index and its tile count.
+struct Piece {
+    int64_t pstart;
+    int r, hp, nt;  // r = -1: none
+};
+
+__device__ __forceinline__ int clipped_len(const Args &a, int r) {
+    const int n = a.lens[r];
+    return n < 0 ? 0 : n > a.max_len ? a.max_len : n;
+}
+__device__ __forceinline__ int tiles_of(const Args &a, int len) {
+    const int seen = len < a.window ? len : a.window;
+    return seen / kTile + (seen % kTile != 0);
+}
+__device__ __forceinline__ void set_request(const Args &a, Cursor &c, int r) {
+    c.r = r;
+    c.len = clipped_len(a, r);
+    c.nt = tiles_of(a, c.len);
+    c.start = c.len > a.window ? c.len - a.window : 0;
+}
+// The next tile of the list; the caller knows that there is one.
+__device__ __forceinline__ void advance(const Args &a, Cursor &c) {
+    ++c.g;
+    if (++c.t < c.nt) return;
+    c.t = 0;
+    if (++c.hp < a.kv.heads * a.passes) return;
+    c.hp = 0;
+    int r = c.r;
+    do set_request(a, c, ++r);
+    while (c.nt == 0 && r + 1 < a.requests);
+}
+
+template <int CT, int D, int RT>
+__global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(const __grid_constant__ Args a) {
+    using C = Cfg<CT, D, RT>;
+    constexpr int W = C::warps, NT = C::threads;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int64_t scan[W + 1];
+    __shared__ int64_t run_off[W];     // of each warp's first tile in its request
+    __shared__ int run_req[W];
+    __shared__ Piece pieces[2 * W];
+    __shared__ uint32_t seen_mask[W][C::stages];
+    __shared__ int last[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cta = blockIdx.x;
+    const int HP = a.kv.heads * a.passes;
+    if (tid < 2 * W) pieces[tid].r = -1;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // ---- the tile list: each thread counts a run of requests, a scan places the runs
+    const int per = (a.requests + NT - 1) / NT;
+    const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
+    int64_t mine = 0;
+    bool cut_len = false;
+    for (int r = r0; r < r1; ++r) {
+        const int n = a.lens[r];
+        cut_len |= n < 0 || n > a.max_len;
+        mine += static_cast<int64_t>(tiles_of(a, n < 0 ? 0 : n > a.max_len ? a.max_len : n)) * HP;
+    }
+    if (cut_len && cta == 0 && a.err) atomicOr(a.err, 2);
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(WSW_FULL_MASK, upto, d);
+        if (lane >= d) upto += y;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    int64_t total = 0, before = upto - mine;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    const int64_t run = max((total + kCtas - 1) / kCtas, static_cast<int64_t>(W));  // tiles per CTA
+    const int64_t b = min(cta * run, total), e = min(b + run, total);
+    const int64_t n_cta = e - b;
+    for (int w = 0; w < W; ++w) {
+        const int64_t s = b + n_cta * w / W;
+        if (s < before || s >= before + mine) continue;
+        int64_t at = before;
+        for (int r = r0; r < r1; ++r) {
+            const int64_t n = static_cast<int64_t>(tiles_of(a, clipped_len(a, r))) * HP;
+            if (s < at + n) {
+                run_req[w] = r;
+                run_off[w] = s - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    // requests that see nothing
+    for (int r = cta; r < a.requests; r += gridDim.x) {
+        if (a.lens[r] > 0 && a.max_len > 0) continue;
+        for (int i = tid; i < a.q_heads * (D / 4); i += NT)
+            store_out4(a, (static_cast<int64_t>(r) * a.q_heads) * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+        if (a.lse)
+            for (int i = tid; i < a.q_heads; i += NT) a.lse[static_cast<int64_t>(r) * a.q_heads + i] = -INFINITY;
+    }
+    __syncthreads();
+    if (n_cta == 0) return;
+
+    const int64_t wb = b + n_cta * warp / W, we = b + n_cta * (warp + 1) / W;
+    int todo = static_cast<int>(we - wb);     // tiles left to use
+    int to_issue = todo;
+    unsigned char *ring = smem + warp * C::ring;
+    const uint32_t ring_s = smem_addr(ring);
+    unsigned char *qsm = smem + W * C::ring + warp * C::q_bytes;
+    uint4 *q_hi_sm = reinterpret_cast<uint4 *>(qsm);
+    uint4 *q_lo_sm = reinterpret_cast<uint4 *>(qsm + (C::q_smem ? C::qfrag : 0));
+
+    if (todo > 0) {
+        Cursor uc;  // the tile in use
+        set_request(a, uc, run_req[warp]);
+        uc.g = wb;
+        uc.hp = static_cast<int>(run_off[warp] / uc.nt);
+        uc.t = static_cast<int>(run_off[warp] - static_cast<int64_t>(uc.hp) * uc.nt);
+        Cursor ic = uc;  // the next tile to copy
+        const int page_mask = (1 << a.kv.page_shift) - 1;
+
+        // lane i < 16 holds the page of position i of the next tile to copy, loaded a step ahead
+        int next_page = -1, next_pos = 0;
+        auto look_up = [&]() {
+            const int p = ic.start + ic.t * kTile + (lane & 15);
+            next_pos = p;
+            next_page = p < ic.len ? a.table[ic.r * a.table_stride + (p >> a.kv.page_shift)] : -1;
+        };
+        look_up();
+        int ist = 0;
+        auto issue = [&]() {
+            if (to_issue > 0) {
+                --to_issue;
+                const bool in = next_pos < ic.len;
+                const bool ok = in && static_cast<unsigned>(next_page) < static_cast<unsigned>(a.kv.num_pages);
+                const uint32_t valid = __ballot_sync(WSW_FULL_MASK, ok) & 0xffffu;
+                if (in && !ok && a.err) atomicOr(a.err, 1);
+                const int64_t page = ok ? next_page : 0, off = ok ? next_pos & page_mask : 0;
+                const int64_t at = page * a.kv.page_stride + off * a.kv.pos_stride;
+                const int h = ic.hp / a.passes;
+                const unsigned char *kb = a.kv.k + h * a.kv.head_stride, *vb = a.kv.v + h * a.kv.head_stride;
+                const uint32_t stg = ring_s + ist * C::stage;
+                constexpr int kRows = 32 / C::pieces;  // rows per round of the warp
+                const int c = lane % C::pieces, rr = lane / C::pieces;
+#pragma unroll
+                for (int i = 0; i < kTile / kRows; ++i) {
+                    const int row = i * kRows + rr;
+                    const int64_t o = __shfl_sync(WSW_FULL_MASK, at, row);
+                    const bool v = (valid >> row) & 1;
+                    const int sw = C::pieces >= 8 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
+                    const uint32_t dst = stg + row * C::row_bytes + sw * 16;
+                    cp16(dst, kb + o + c * 16, v);
+                    cp16(dst + C::kv_bytes, vb + o + c * 16, v);
+                }
+                if constexpr (C::q8) {  // lanes 0..15: K scales, 16..31: V scales
+                    const int64_t dat = page * a.kv.d_page_stride + off * a.kv.d_pos_stride + h * a.kv.d_head_stride;
+                    cp_small<C::scale_bytes>(stg + 2 * C::kv_bytes + lane * C::scale_bytes,
+                                             (lane < 16 ? a.kv.kd : a.kv.vd) + dat, ok);
+                }
+                if (lane == 0) seen_mask[warp][ist] = valid;
+                if (++ist == C::stages) ist = 0;
+                if (to_issue > 0) {
+                    advance(a, ic);
+                    look_up();
+                }
+            }
+            cp_commit();  // one group per step, empty past the end
+        };
+#pragma unroll
+        for (int i = 0; i < C::stages - 1; ++i) issue();
+
+        const int gq = lane >> 2, tq = lane & 3;
+        uint32_t qa[C::q_smem ? 1 : C::ksteps][4];
+        float m[RT / 8], l[RT / 8], slope[RT / 8];
+        float o[D / 8][4];
+        bool q_lo = false;   // RT 16: q has residuals
+        int t_first = 0;     // first tile of the piece
+        bool fresh = true;   // a new pair begins
+        bool first_piece = true;
+        int rst = 0;
+        const int mi = lane >> 3, mr = lane & 7;
+
+        for (; todo > 0; --todo) {
+            if (fresh) {
+                fresh = false;
+                t_first = uc.t;
+                const int h = uc.hp / a.passes, g0 = (uc.hp - h * a.passes) * RT;
+                const int64_t head0 = static_cast<int64_t>(uc.r) * a.q_heads + h * a.group + g0;
+                bool some = false;
+#pragma unroll
+                for (int kt = 0; kt < C::ksteps; ++kt) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {       // the fragment's two column halves
+                        // natural order for 16-bit rows; for q8_0 lane tq owns dimensions
+                        // tq D / 4 ..., four of them per step
+                        const int d = C::q8 ? tq * (D / 4) + 4 * kt + 2 * x : 16 * kt + 8 * x + 2 * tq;
+#pragma unroll
+                        for (int y = 0; y < RT / 8; ++y) {
+                            const int row = gq + 8 * y;
+                            float2 v = make_float2(0.f, 0.f);
+                            if (g0 + row < a.group) v = load_q2(a, (head0 + row) * D + d);
+                            uint32_t vh, vl;
+                            split<CT>(v.x, v.y, vh, vl);
+                            if constexpr (RT == 8) {
+                                hi[2 * x] = vh;
+                                hi[2 * x + 1] = vl;
+                            } else {
+                                hi[2 * x + y] = vh;
+                                lo[2 * x + y] = vl;
+                                some |= (vl & 0x7fff7fffu) != 0;
+                            }
+                        }
+                    }
+                    if constexpr (C::q_smem) q_hi_sm[kt * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) qa[kt][i] = hi[i];
+                    }
+                    if constexpr (RT == 16) q_lo_sm[kt * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                if constexpr (RT == 16) q_lo = __any_sync(WSW_FULL_MASK, some);
+#pragma unroll
+                for (int y = 0; y < RT / 8; ++y) {
+                    m[y] = -INFINITY;
+                    l[y] = 0.f;
+                    const int row = g0 + gq + 8 * y;
+                    slope[y] = a.slopes && row < a.group ? a.slopes[h * a.group + row] * kLog2e : 0.f;
+                }
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+            }
+            __syncwarp();  // every lane is done reading the stage that the next copy reuses
+            issue();
+            cp_wait<C::stages - 1>();
+            __syncwarp();  // the tile's pieces copied by every lane are visible
+            const uint32_t stg = ring_s + rst * C::stage;
+            const unsigned char *stg_p = ring + rst * C::stage;
+            const uint32_t valid = seen_mask[warp][rst];
+            if (++rst == C::stages) rst = 0;
+
+            // ---- scores of 16 positions, two blocks of 8
+            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            auto score = [&](int kt, const uint32_t (&kb)[4]) {  // kb: block 0's two registers, block 1's
+                uint32_t qf[4];
+                if constexpr (C::q_smem) {
+                    const uint4 u = q_hi_sm[kt * 32 + lane];
+                    qf[0] = u.x; qf[1] = u.y; qf[2] = u.z; qf[3] = u.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qf[i] = qa[kt][i];
+                }
+                mma<CT>(sc[0], qf, kb[0], kb[1]);
+                mma<CT>(sc[1], qf, kb[2], kb[3]);
+                if constexpr (RT == 16) {
+                    if (q_lo) {
+                        const uint4 u = q_lo_sm[kt * 32 + lane];
+                        const uint32_t ql[4] = {u.x, u.y, u.z, u.w};
+                        mma<CT>(sc[0], ql, kb[0], kb[1]);
+                        mma<CT>(sc[1], ql, kb[2], kb[3]);
+                    }
+                }
+            };
+            if constexpr (!C::q8) {
+                const int pos = 8 * (mi >> 1) + mr;
+#pragma unroll
+                for (int kt = 0; kt < C::ksteps; ++kt) {
+                    uint32_t kb[4];
+                    const int ch = 2 * kt + (mi & 1);
+                    ldsm4(kb, stg + pos * C::row_bytes + ((ch ^ (pos & 7)) << 4));
+                    score(kt, kb);
+                }
+            } else {
+                constexpr int kVec = D / 64;  // 16-byte pieces per lane and row
+                uint32_t w[2][4 * kVec];
+                __half2 ds[2][D == 256 ? 2 : 1];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int row = 8 * n + gq;
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) {
+                        const int ch = tq * kVec + i;
+                        const int sw = C::pieces >= 8 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
+                        const uint4 u = *reinterpret_cast<const uint4 *>(stg_p + row * C::row_bytes + sw * 16);
+                        w[n][4 * i] = u.x ^ 0x80808080u;
+                        w[n][4 * i + 1] = u.y ^ 0x80808080u;
+                        w[n][4 * i + 2] = u.z ^ 0x80808080u;
+                        w[n][4 * i + 3] = u.w ^ 0x80808080u;
+                    }
+                    const __half *sp = reinterpret_cast<const __half *>(stg_p + 2 * C::kv_bytes + row * C::scale_bytes);
+                    if constexpr (D == 64) ds[n][0] = __half2half2(sp[tq >> 1]);
+                    else if constexpr (D == 128) ds[n][0] = __half2half2(sp[tq]);
+                    else {
+                        ds[n][0] = __half2half2(sp[2 * tq]);
+                        ds[n][1] = __half2half2(sp[2 * tq + 1]);
+                    }
+                }
+#pragma unroll
+                for (int kt = 0; kt < C::ksteps; ++kt) {
+                    const int bl = D == 256 ? kt >> 3 : 0;
+                    const uint32_t kb[4] = {dequant2(w[0][kt], 0x4140, ds[0][bl]), dequant2(w[0][kt], 0x4342, ds[0][bl]),
+                                            dequant2(w[1][kt], 0x4140, ds[1][bl]), dequant2(w[1][kt], 0x4342, ds[1][bl])};
+                    score(kt, kb);
+                }
+            }
+
+            // ---- softmax: lane (gq, tq) holds positions 8 n + 2 tq + {0, 1} of rows gq, gq + 8
+            const int p0 = uc.start + uc.t * kTile;
+            uint32_t ph[4], pl[4];
+            float al[RT / 8];
+#pragma unroll
+            for (int y = 0; y < RT / 8; ++y) {
+                float s[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int pi = 8 * n + 2 * tq + j;
+                        float x = RT == 8 ? sc[n][j] + sc[n][2 + j] : sc[n][2 * y + j];
+                        x = a.cap_in != 0.f ? a.cap_out * tanhf(x * a.cap_in) : x * a.scale2;
+                        if (a.slopes) x = fmaf(-slope[y], static_cast<float>(uc.len - 1 - (p0 + pi)), x);
+                        s[2 * n + j] = (valid >> pi) & 1 ? x : -INFINITY;
+                    }
+                float mt = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+                mt = fmaxf(mt, __shfl_xor_sync(WSW_FULL_MASK, mt, 1));
+                mt = fmaxf(mt, __shfl_xor_sync(WSW_FULL_MASK, mt, 2));
+                const float mn = fmaxf(m[y], mt);
+                const bool none = mn == -INFINITY;
+                al[y] = none ? 1.f : ex2(m[y] - mn);
+                m[y] = mn;
+                float p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = none ? 0.f : ex2(s[i] - (mn - kShift));
+                l[y] = l[y] * al[y] + ((p[0] + p[1]) + (p[2] + p[3]));
+                if constexpr (RT == 8) {
+                    split<CT>(p[0], p[1], ph[0], ph[1]);
+                    split<CT>(p[2], p[3], ph[2], ph[3]);
+                } else {
+                    split<CT>(p[0], p[1], ph[y], pl[y]);
+                    split<CT>(p[2], p[3], ph[2 + y], pl[2 + y]);
+                }
+            }
+            if (__any_sync(WSW_FULL_MASK, al[0] != 1.f || al[RT / 8 - 1] != 1.f)) {
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    o[n][0] *= al[0];
+                    o[n][1] *= al[0];
+                    o[n][2] *= al[RT / 8 - 1];
+                    o[n][3] *= al[RT / 8 - 1];
+                }
+            }
+
+            // ---- value sums
+            auto add = [&](int n, uint32_t b0, uint32_t b1) {
+                mma<CT>(o[n], ph, b0, b1);
+                if constexpr (RT == 16) mma<CT>(o[n], pl, b0, b1);
+            };
+            const int vpos = 8 * (mi & 1) + mr;
+            if constexpr (!C::q8) {
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    uint32_t vb[4];
+                    const int ch = 2 * j + (mi >> 1);
+                    ldsm4_t(vb, stg + C::kv_bytes + vpos * C::row_bytes + ((ch ^ (vpos & 7)) << 4));
+                    add(2 * j, vb[0], vb[1]);
+                    add(2 * j + 1, vb[2], vb[3]);
+                }
+            } else {
+                // a transposed 16-bit matrix element is a pair of codes: dimensions 16 c + 2 i and
+                // + 1 of one position.  Bytes 0 and 2 of a register are the even dimension at
+                // positions 2 tq and 2 tq + 1, bytes 1 and 3 the odd one: two column blocks.
+                const unsigned char *vs = stg_p + 2 * C::kv_bytes + kTile * C::scale_bytes;
+                constexpr int kBl = D / 32;
+                __half dv[4][kBl];  // scales of positions 2 tq, 2 tq + 1, 8 + 2 tq, 9 + 2 tq
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 8 * (i >> 1) + 2 * tq + (i & 1);
+                    const __half *sp = reinterpret_cast<const __half *>(vs + row * C::scale_bytes);
+                    if constexpr (kBl == 2) {
+                        const uint32_t u = *reinterpret_cast<const uint32_t *>(sp);
+                        *reinterpret_cast<uint32_t *>(dv[i]) = u;
+                    } else if constexpr (kBl == 4) {
+                        *reinterpret_cast<uint2 *>(dv[i]) = *reinterpret_cast<const uint2 *>(sp);
+                    } else {
+                        *reinterpret_cast<uint4 *>(dv[i]) = *reinterpret_cast<const uint4 *>(sp);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kBl; ++j) {
+                    uint32_t vb[4];
+                    const int ch = 2 * j + (mi >> 1);
+                    const int sw = C::pieces >= 8 ? ch ^ (vpos & 7) : ch ^ ((vpos >> 1) & 3);
+                    ldsm4_t(vb, stg + C::kv_bytes + vpos * C::row_bytes + (sw << 4));
+                    const __half2 d0 = __halves2half2(dv[0][j], dv[1][j]), d1 = __halves2half2(dv[2][j], dv[3][j]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vb[i] ^= 0x80808080u;
+#pragma unroll
+                    for (int pc = 0; pc < 2; ++pc) {
+                        add(4 * j + 2 * pc, dequant2(vb[2 * pc], 0x4240, d0), dequant2(vb[2 * pc + 1], 0x4240, d1));
+                        add(4 * j + 2 * pc + 1, dequant2(vb[2 * pc], 0x4341, d0), dequant2(vb[2 * pc + 1], 0x4341, d1));
+                    }
+                }
+            }
+
+            // ---- the end of the pair, or of the run
+            const bool pair_end = uc.t == uc.nt - 1;
+            if (!pair_end && todo > 1) {
+                ++uc.t;
+                ++uc.g;
+                continue;
+            }
+            fresh = true;
+            const int h = uc.hp / a.passes, g0 = (uc.hp - h * a.passes) * RT;
+            const bool whole = pair_end && t_first == 0;
+            float *rec = nullptr;
+            if (!whole) {
+                if (todo == 1) {  // the run's last piece: into the ring, which no copy uses any more
+                    cp_wait<0>();
+                    __syncwarp();
+                    rec = reinterpret_cast<float *>(ring);
+                } else {
+                    rec = a.wrec + static_cast<int64_t>(cta * W + warp) * RT * C::rec;
+                }
+                if (lane == 0) pieces[2 * warp + (todo == 1)] = Piece{uc.g - uc.t, uc.r, uc.hp, uc.nt};
+            }
+#pragma unroll
+            for (int y = 0; y < RT / 8; ++y) {
+                l[y] += __shfl_xor_sync(WSW_FULL_MASK, l[y], 1);
+                l[y] += __shfl_xor_sync(WSW_FULL_MASK, l[y], 2);
+                const int row = gq + 8 * y;
+                if (g0 + row >= a.group) continue;
+                const int64_t head = static_cast<int64_t>(uc.r) * a.q_heads + h * a.group + g0 + row;
+                const float inv = l[y] == 0.f ? 0.f : 1.f / l[y];
+                auto val = [&](int n, int x) { return RT == 8 ? o[n][x] + o[n][2 + x] : o[n][2 * y + x]; };
+                float *rr = whole ? nullptr : rec + row * C::rec;
+                if (tq == 0) {
+                    if (whole) {
+                        if (a.lse) a.lse[head] = lse_of(m[y], l[y]);
+                    } else {
+                        rr[0] = m[y];
+                        rr[1] = l[y];
+                    }
+                }
+                if constexpr (!C::q8) {
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        const int d = 8 * n + 2 * tq;
+                        if (whole) store_out2(a, head * D + d, val(n, 0) * inv, val(n, 1) * inv);
+                        else *reinterpret_cast<float2 *>(rr + 4 + d) = make_float2(val(n, 0), val(n, 1));
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < D / 8; n += 2) {
+                        const int d = 8 * n + 4 * tq;
+                        const float4 v = make_float4(val(n, 0), val(n + 1, 0), val(n, 1), val(n + 1, 1));
+                        if (whole) store_out4(a, head * D + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                        else *reinterpret_cast<float4 *>(rr + 4 + d) = v;
+                    }
+                }
+            }
+            first_piece = false;
+            if (todo > 1) {
+                // advance() is safe: there is another tile
+                advance(a, uc);
+            }
+        }
+        (void)first_piece;
+        cp_wait<0>();
+    }
+    __syncthreads();
+
+    // ---- join the warps' records, pair by pair in tile order
+    constexpr int kCols = D / 4;
+    int nshared = 0;
+    Piece shared_pair[2];
+    for (int i = 0; i < 2 * W;) {
+        const Piece pc = pieces[i];
+        if (pc.r < 0) {
+            ++i;
+            continue;
+        }
+        int j = i + 1;
+        while (j < 2 * W && (pieces[j].r < 0 || (pieces[j].r == pc.r && pieces[j].hp == pc.hp))) ++j;
+        const bool complete = pc.pstart >= b && pc.pstart + pc.nt <= e;
+        const int h = pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
+        const int rows = min(RT, a.group - g0);
+        float *dst = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec;
+        for (int u = tid; u < rows * kCols; u += NT) {
+            const int row = u / kCols, c4 = u - row * kCols;
+            float mx = -INFINITY;
+            for (int k = i; k < j; ++k) {
+                if (pieces[k].r < 0) continue;
+                const float *r = (k & 1 ? reinterpret_cast<const float *>(smem + (k >> 1) * C::ring)
+                                        : a.wrec + static_cast<int64_t>(cta * W + (k >> 1)) * RT * C::rec) + row * C::rec;
+                mx = fmaxf(mx, r[0]);
+            }
+            float l = 0.f;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = i; k < j; ++k) {
+                if (pieces[k].r < 0) continue;
+                const float *r = (k & 1 ? reinterpret_cast<const float *>(smem + (k >> 1) * C::ring)
+                                        : a.wrec + static_cast<int64_t>(cta * W + (k >> 1)) * RT * C::rec) + row * C::rec;
+                const float f = weight(r[0], mx);
+                const float4 x = *reinterpret_cast<const float4 *>(r + 4 + 4 * c4);
+                l = fmaf(r[1], f, l);
+                s.x = fmaf(x.x, f, s.x);
+                s.y = fmaf(x.y, f, s.y);
+                s.z = fmaf(x.z, f, s.z);
+                s.w = fmaf(x.w, f, s.w);
+            }
+            if (complete) {
+                const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
+                if (c4 == 0 && a.lse) a.lse[head] = lse_of(mx, l);
+            } else {
+                float *r = dst + row * C::rec;
+                *reinterpret_cast<float4 *>(r + 4 + 4 * c4) = s;
+                if (c4 == 0) {
+                    r[0] = mx;
+                    r[1] = l;
+                }
+            }
+        }
+        if (!complete && nshared < 2) shared_pair[nshared++] = pc;
+        i = j;
+    }
+    if (nshared == 0) return;
+
+    // ---- pairs shared with other CTAs: the last to arrive joins their records.  The block
+    // barrier orders this CTA's records before thread 0's arrival, whose release publishes
+    // them; its acquire, and the barrier after it, order the reads after every arrival.
+    __syncthreads();
+    if (tid < nshared) {
+        const Piece pc = shared_pair[tid];
+        const int64_t f = pc.pstart / run, t = (pc.pstart + pc.nt - 1) / run;
+        unsigned old;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.cnt + f) : "memory");
+        last[tid] = old == static_cast<unsigned>(t - f);
+    }
+    __syncthreads();
+    for (int sp = 0; sp < nshared; ++sp) {
+        if (!last[sp]) continue;
+        const Piece pc = shared_pair[sp];
+        const int f = static_cast<int>(pc.pstart / run), n = static_cast<int>((pc.pstart + pc.nt - 1) / run) - f + 1;
+        const int h = pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
+        const int rows = min(RT, a.group - g0);
+        // threads (slice, row, column): the records are dealt to the slices, then the slices
+        // are joined in order
+        int slices = NT / (rows * kCols);
+        if (slices < 1) slices = 1;
+        float *part = reinterpret_cast<float *>(smem);  // [slices * rows * kCols][6]
+        for (int u = tid; u < slices * rows * kCols; u += NT) {
+            const int sl = u / (rows * kCols), v = u - sl * rows * kCols;
+            const int row = v / kCols, c4 = v - row * kCols;
+            float mx = -INFINITY, l = 0.f;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int k = sl; k < n; k += slices) {
+                // the first CTA holds the pair's beginning as its second shared pair
+                const float *r = a.rec + (static_cast<int64_t>(f + k) * 2 + (k == 0)) * RT * C::rec + row * C::rec;
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(r));
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(r + 4 + 4 * c4));
+                const float mn = fmaxf(mx, ml.x);
+                const float fo = weight(mx, mn), fn = weight(ml.x, mn);
+                mx = mn;
+                l = l * fo + ml.y * fn;
+                s.x = s.x * fo + x.x * fn;
+                s.y = s.y * fo + x.y * fn;
+                s.z = s.z * fo + x.z * fn;
+                s.w = s.w * fo + x.w * fn;
+            }
+            float *w = part + u * 6;
+            w[0] = mx; w[1] = l; w[2] = s.x; w[3] = s.y; w[4] = s.z; w[5] = s.w;
+        }
+        __syncthreads();
+        for (int u = tid; u < rows * kCols; u += NT) {
+            const int row = u / kCols, c4 = u - row * kCols;
+            float mx = -INFINITY;
+            for (int sl = 0; sl < slices; ++sl) mx = fmaxf(mx, part[(sl * rows * kCols + u) * 6]);
+            float l = 0.f, s[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int sl = 0; sl < slices; ++sl) {
+                const float *w = part + (sl * rows * kCols + u) * 6;
+                const float fn = weight(w[0], mx);
+                l = fmaf(w[1], fn, l);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] = fmaf(w[2 + i], fn, s[i]);
+            }
+            const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            store_out4(a, head * D + 4 * c4, make_float4(s[0] * inv, s[1] * inv, s[2] * inv, s[3] * inv));
+            if (c4 == 0 && a.lse) a.lse[head] = lse_of(mx, l);
+        }
+        if (tid == 0) a.cnt[f] = 0u;  // ready for the next call
+        __syncthreads();
+    }
+}
+
+template <int CT>
+cudaError_t launch_type(const Args &a, int rows, cudaStream_t s, bool pdl, int ctas);
+
+template <int CT, int D, int RT>
+cudaError_t launch_one(const Args &a, cudaStream_t s, bool pdl, int ctas) {
+    using C = Cfg<CT, D, RT>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attn_paged_kernel<CT, D, RT>), C::smem);
+    if (e != cudaSuccess) return e;
+    return launch(attn_paged_kernel<CT, D, RT>, dim3(ctas), dim3(C::threads), C::smem, s, pdl, a);
+}
+
+#define WSW_PAGED_TYPE(CT)                                                                       \
+    template <>                                                                                  \
+    cudaError_t launch_type<CT>(const Args &a, int rows, cudaStream_t s, bool pdl, int ctas) {   \
+        switch (a.kv.head_dim * 2 + (rows == 16)) {                                              \
+            case 128: return launch_one<CT, 64, 8>(a, s, pdl, ctas);                             \
+            case 129: return launch_one<CT, 64, 16>(a, s, pdl, ctas);                            \
+            case 256: return launch_one<CT, 128, 8>(a, s, pdl, ctas);                            \
+            case 257: return launch_one<CT, 128, 16>(a, s, pdl, ctas);                           \
+            case 512: return launch_one<CT, 256, 8>(a, s, pdl, ctas);                            \
+            default: return launch_one<CT, 256, 16>(a, s, pdl, ctas);                            \
+        }                                                                                        \
+    }
+
+}  // namespace paged
+}  // namespace wsw

@@ -1,0 +1,317 @@
+// rope_kv.cu -- rotary positions of q and k fused with the write of k and v into the paged
+// KV cache, and the host table of frequencies.
+//
+// Pair (x0, x1) of a head at position p turns by the angle a = p f:
+//   (x0, x1) -> m (x0 cos a - x1 sin a, x1 cos a + x0 sin a)
+// ("RoFormer: Enhanced Transformer with Rotary Position Embedding", section 3.4.2), f from
+// the table, m its attention factor.
+//
+// Angles: p f in fp32 is off by p f 2^-24 radians, 0.06 at p = 10^6 and f = 1.  The table
+// holds f in fractions of a turn as 64-bit fixed point, so p * turns modulo 2^64 drops the
+// whole turns exactly; its top 32 bits (2^-32 of a turn) go to sincospi.  One 64-bit
+// integer product replaces an FP64 one, which this part runs at a sixtieth of fp32's rate.
+// Each (token, pair) is computed once per CTA and shared by all heads through shared memory.
+//
+// Work: a thread owns 8 consecutive dimensions of one row (a row: one head of one token);
+// for the half layout it loads its 8 partners too, which its own warp's neighbours have
+// just brought into L1.  Bytes decide: q, k and v once in, q out, k and v out.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "kv_cache.cuh"
+#include "q8_math.cuh"
+
+namespace wsw {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTile = 4;  // tokens per CTA
+
+struct RopeArgs {
+    const void *q, *k, *v;
+    int64_t qts, qhs, kts, khs, vts, vhs;  // token and head strides, elements
+    const uint64_t *turns;
+    const int32_t *positions;
+    const int64_t *slots;
+    void *q_out;
+    int32_t *err;
+    KvView kv;
+    int64_t tokens;
+    float mscale;
+    int q_heads, rot, interleaved, tile;
+    int lane_shift;  // log2(head_dim / 8): threads per row
+    bool vec;        // q, k, v rows 16-byte aligned
+    bool vec_out;    // q_out 16-byte aligned
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    return make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
+}
+
+// 8 consecutive values; plain loads, as the call may write q in place
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]) {
+    if (vec) {
+        alignas(16) T t[8];
+        uint4 *u = reinterpret_cast<uint4 *>(t);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(p)[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_f(t[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_f(p[i]);
+    }
+}
+
+__device__ __forceinline__ void store8(float *p, bool vec, const float (&x)[8]) {
+    if (vec) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = x[i];
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, bool vec, const float (&x)[8]) {
+    const uint4 u = pack8<T>(x);
+    if (vec) {
+        *reinterpret_cast<uint4 *>(p) = u;
+    } else {
+        const T *t = reinterpret_cast<const T *>(&u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = t[i];
+    }
+}
+
+template <typename T, int CT>
+__global__ void __launch_bounds__(kThreads) rope_kv_kernel(const RopeArgs a) {
+    __shared__ float2 cs[kMaxTile * 128];  // (m cos, m sin) of each token and pair
+    const int tid = threadIdx.x;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tile;
+    const int tile = static_cast<int>(a.tokens - t0 < a.tile ? a.tokens - t0 : a.tile);
+    const int half = a.rot >> 1;
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int i = tid; i < tile * half; i += kThreads) {
+        const int tt = i / half;
+        const int32_t p = a.positions[t0 + tt];
+        const uint64_t turn = static_cast<uint64_t>(p < 0 ? 0 : p) * a.turns[i - tt * half];
+        // the top 32 bits as a signed fraction: half turns in [-1, 1)
+        const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
+        float s, c;
+        sincospif(x, &s, &c);
+        cs[i] = make_float2(a.mscale * c, a.mscale * s);
+    }
+    __syncthreads();
+
+    const int lanes = 1 << a.lane_shift, D = lanes * 8;
+    const int rows = a.q_heads + 2 * a.kv.heads;
+    const int units = tile * rows << a.lane_shift;
+    for (int base = blockIdx.y * kThreads; base < units; base += gridDim.y * kThreads) {
+        const int u = base + tid;
+        const bool active = u < units;  // a row's lanes are all active or all idle
+        const int row = active ? u >> a.lane_shift : 0;
+        const int tt = row / rows, h = row - tt * rows;
+        const int d0 = (u & (lanes - 1)) * 8;
+        const int64_t t = t0 + tt;
+        const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + a.kv.heads;
+        const int kh = is_v ? h - a.q_heads - a.kv.heads : h - a.q_heads;
+        const T *src;
+        if (is_q) src = static_cast<const T *>(a.q) + t * a.qts + h * a.qhs;
+        else if (is_v) src = static_cast<const T *>(a.v) + t * a.vts + kh * a.vhs;
+        else src = static_cast<const T *>(a.k) + t * a.kts + kh * a.khs;
+        const int32_t pos = a.positions[t];
+        float x[8];
+        if (active && pos >= 0) {
+            load8(src + d0, a.vec, x);
+            if (!is_v && d0 < a.rot) {
+                const float2 *w = cs + tt * half;
+                if (a.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (d0 + 2 * i >= a.rot) break;
+                        const float2 z = w[(d0 >> 1) + i];
+                        const float x0 = x[2 * i], x1 = x[2 * i + 1];
+                        x[2 * i] = x0 * z.x - x1 * z.y;
+                        x[2 * i + 1] = x1 * z.x + x0 * z.y;
+                    }
+                } else if ((half & 7) == 0) {
+                    const bool lo = d0 < half;
+                    float y[8];
+                    load8(src + (lo ? d0 + half : d0 - half), a.vec, y);
+                    w += lo ? d0 : d0 - half;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 z = w[i];
+                        x[i] = x[i] * z.x + y[i] * (lo ? -z.y : z.y);
+                    }
+                } else {  // the halves do not meet at a multiple of 8: partners one by one
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int d = d0 + i;
+                        if (d >= a.rot) break;
+                        const bool lo = d < half;
+                        const float y = to_f(src[lo ? d + half : d - half]);
+                        const float2 z = w[lo ? d : d - half];
+                        x[i] = x[i] * z.x + y * (lo ? -z.y : z.y);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = 0.f;  // padding
+        }
+        __syncwarp();  // a row in place: its partners are read before it is written
+        int64_t where = -1, dwhere = 0;
+        if (active && !is_q && pos >= 0) {
+            const int64_t slot = a.slots[t];
+            const int64_t page = slot >> a.kv.page_shift;
+            if (slot >= 0 && page < a.kv.num_pages) {
+                const int64_t off = slot & ((int64_t(1) << a.kv.page_shift) - 1);
+                where = page * a.kv.page_stride + off * a.kv.pos_stride + kh * a.kv.head_stride;
+                dwhere = page * a.kv.d_page_stride + off * a.kv.d_pos_stride + kh * a.kv.d_head_stride;
+            } else if (slot >= 0 && a.err) {
+                atomicOr(a.err, 1);
+            }
+        }
+        if constexpr (CT == WSW_Q8_0) {
+            const float amax = q8m::block_amax<32>(x);  // every lane of the warp
+            if (where >= 0) {
+                const float d = q8m::scale(amax);
+                uint32_t codes[2];
+                q8m::codes(x, amax, d, codes);
+                *reinterpret_cast<uint2 *>((is_v ? a.kv.v : a.kv.k) + where + d0) = make_uint2(codes[0], codes[1]);
+                if ((d0 & 31) == 0)
+                    reinterpret_cast<__half *>((is_v ? a.kv.vd : a.kv.kd) + dwhere)[d0 >> 5] = __float2half_rn(d);
+            }
+        } else if (where >= 0) {
+            unsigned char *dst = (is_v ? a.kv.v : a.kv.k) + where + d0 * 2;
+            if constexpr (CT == WSW_F16) *reinterpret_cast<uint4 *>(dst) = pack8<__half>(x);
+            else *reinterpret_cast<uint4 *>(dst) = pack8<__nv_bfloat16>(x);
+        }
+        if (active && is_q) store8(static_cast<T *>(a.q_out) + (t * a.q_heads + h) * D + d0, a.vec_out, x);
+    }
+}
+
+template <typename T>
+cudaError_t launch_rope(const RopeArgs &a, int cache_type, dim3 grid, cudaStream_t s, bool pdl) {
+    if (cache_type == WSW_F16) return launch(rope_kv_kernel<T, WSW_F16>, grid, dim3(kThreads), 0, s, pdl, a);
+    if (cache_type == WSW_BF16) return launch(rope_kv_kernel<T, WSW_BF16>, grid, dim3(kThreads), 0, s, pdl, a);
+    return launch(rope_kv_kernel<T, WSW_Q8_0>, grid, dim3(kThreads), 0, s, pdl, a);
+}
+
+}  // namespace
+}  // namespace wsw
+
+extern "C" int wsw_rope_table(int64_t rot_dim, double theta, int32_t scaling, double factor, int64_t original,
+                              const double *freqs, uint64_t *turns, float *mscale) {
+    constexpr double kTwoPi = 6.283185307179586476925;
+    if (!turns || !mscale || rot_dim < 2 || rot_dim > 256 || (rot_dim & 1)) return WSW_ERR_INVALID_ARG;
+    if (freqs) {
+        scaling = WSW_ROPE_PLAIN;
+    } else {
+        if (scaling < WSW_ROPE_PLAIN || scaling > WSW_ROPE_BY_PARTS || !std::isfinite(theta) || !(theta > 1))
+            return WSW_ERR_INVALID_ARG;
+        if (scaling != WSW_ROPE_PLAIN && (!std::isfinite(factor) || !(factor >= 1))) return WSW_ERR_INVALID_ARG;
+        if (scaling == WSW_ROPE_NTK && rot_dim <= 2) return WSW_ERR_INVALID_ARG;
+        if (scaling == WSW_ROPE_BY_PARTS && original < 1) return WSW_ERR_INVALID_ARG;
+        if (scaling == WSW_ROPE_NTK) theta *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+    }
+    for (int64_t i = 0; i < rot_dim / 2; ++i) {
+        double f = freqs ? freqs[i] : std::pow(theta, -2.0 * static_cast<double>(i) / static_cast<double>(rot_dim));
+        if (scaling == WSW_ROPE_LINEAR) f /= factor;
+        if (scaling == WSW_ROPE_BY_PARTS) {
+            const double t = (static_cast<double>(original) * f / kTwoPi - 1.0) / 31.0;  // turns: 1 .. 32
+            const double keep = t < 0 ? 0 : t > 1 ? 1 : t;
+            f = keep * f + (1 - keep) * f / factor;
+        }
+        if (!(f >= 0 && f < kTwoPi)) return WSW_ERR_INVALID_ARG;
+        // f / 2 pi < 1, and 2^64 - 2048 is the largest double below 2^64
+        const double x = std::nearbyint(std::ldexp(f / kTwoPi, 64));
+        turns[i] = x < 18446744073709549568.0 ? static_cast<uint64_t>(x) : 18446744073709549568ull;
+    }
+    *mscale = scaling == WSW_ROPE_BY_PARTS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return WSW_OK;
+}
+
+extern "C" int wsw_rope_kv_write(const void *q, const void *k, const void *v, int32_t dtype, int64_t tokens,
+                                 int64_t q_heads, int64_t q_tok_stride, int64_t q_head_stride, int64_t k_tok_stride,
+                                 int64_t k_head_stride, int64_t v_tok_stride, int64_t v_head_stride,
+                                 const uint64_t *turns, int64_t rot_dim, float mscale, int32_t interleaved,
+                                 const int32_t *positions, const int64_t *slots, void *q_out,
+                                 const wsw_kv_cache *cache, int32_t *err_flag, void *stream,
+                                 const wsw_launch_opts *opts) {
+    using namespace wsw;
+    Opts o;
+    int st = resolve_opts(opts, &o);
+    if (st != WSW_OK) return st;
+    RopeArgs a;
+    st = check_kv_cache(cache, &a.kv);
+    if (st != WSW_OK) return st;
+    if (dtype != WSW_F32 && dtype != WSW_F16 && dtype != WSW_BF16) return WSW_ERR_UNSUPPORTED;
+    if (tokens < 0 || q_heads < 0 || rot_dim < 0 || rot_dim > a.kv.head_dim || (rot_dim & 1) ||
+        (interleaved != 0 && interleaved != 1) || !std::isfinite(mscale) || q_tok_stride < 0 || q_head_stride < 0 ||
+        k_tok_stride < 0 || k_head_stride < 0 || v_tok_stride < 0 || v_head_stride < 0)
+        return WSW_ERR_INVALID_ARG;
+    if (tokens >= (int64_t(1) << 31) || q_heads > 65535) return WSW_ERR_UNSUPPORTED;
+    if (tokens == 0) return WSW_OK;
+    if (!k || !v || !positions || !slots || (q_heads > 0 && (!q || !q_out)) || (rot_dim > 0 && !turns))
+        return WSW_ERR_INVALID_ARG;
+    const int64_t esize = dtype == WSW_F32 ? 4 : 2;
+    const uintptr_t in = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+                         (q_heads > 0 ? reinterpret_cast<uintptr_t>(q) : 0);
+    const uintptr_t strides = static_cast<uintptr_t>(k_tok_stride | k_head_stride | v_tok_stride | v_head_stride |
+                                                     (q_heads > 0 ? q_tok_stride | q_head_stride : 0)) * esize;
+    const uintptr_t qo = q_heads > 0 ? reinterpret_cast<uintptr_t>(q_out) : 0;
+    if (((in | qo) & (esize - 1)) || (reinterpret_cast<uintptr_t>(positions) & 3) ||
+        (reinterpret_cast<uintptr_t>(slots) & 7) || (reinterpret_cast<uintptr_t>(turns) & 7) ||
+        (reinterpret_cast<uintptr_t>(err_flag) & 3))
+        return WSW_ERR_MISALIGNED;
+    DeviceInfo di;
+    if (!device_info(&di, &st)) return st;
+    a.q = q; a.k = k; a.v = v;
+    a.qts = q_tok_stride; a.qhs = q_head_stride;
+    a.kts = k_tok_stride; a.khs = k_head_stride;
+    a.vts = v_tok_stride; a.vhs = v_head_stride;
+    a.turns = turns;
+    a.positions = positions;
+    a.slots = slots;
+    a.q_out = q_out;
+    a.err = err_flag;
+    a.tokens = tokens;
+    a.mscale = mscale;
+    a.q_heads = static_cast<int>(q_heads);
+    a.rot = static_cast<int>(rot_dim);
+    a.interleaved = interleaved;
+    a.lane_shift = a.kv.head_dim == 64 ? 3 : a.kv.head_dim == 128 ? 4 : 5;
+    a.vec = ((in | strides) & 15) == 0;
+    a.vec_out = (qo & 15) == 0;
+    const int64_t passes = (((q_heads + 2 * a.kv.heads) << a.lane_shift) + kThreads - 1) / kThreads;  // of one token
+    a.tile = tokens >= 2048 ? kMaxTile : 1;
+    const int64_t slabs = tokens >= 2048 ? 1 : passes;
+    const dim3 grid(static_cast<unsigned>((tokens + a.tile - 1) / a.tile),
+                    static_cast<unsigned>(slabs < 65535 ? slabs : 65535));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (dtype == WSW_F32) e = launch_rope<float>(a, cache->dtype, grid, s, o.pdl);
+    else if (dtype == WSW_F16) e = launch_rope<__half>(a, cache->dtype, grid, s, o.pdl);
+    else e = launch_rope<__nv_bfloat16>(a, cache->dtype, grid, s, o.pdl);
+    return e == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
+}
