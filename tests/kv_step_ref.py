@@ -98,16 +98,17 @@ def attend(q, k, v, scale, softcap=0.0, slopes=None, distance=None):
 
 
 def logprobs(x, token, scale, top):
-    """One row in float64: (logprob, rank, lse, entropy, top ids, top logprobs)."""
+    """One row in float64: (logprob, rank, lse, entropy, top ids, top logprobs, ln S), with
+    S = sum exp(y - max y): the probabilities come from y - max y, which stays exact where
+    lse itself is huge (a row at the type's lowest value)."""
     y = x * scale
     m = y.max()
     order = np.lexsort((np.arange(len(x)), -x))[:top]
+    rank = int((x > x[token]).sum() + (x[:token] == x[token]).sum())
     if m == -np.inf:
-        return -np.inf, int((x > x[token]).sum() + (x[:token] == x[token]).sum()), -np.inf, 0.0, order, np.full(
-            top, -np.inf)
-    lse = m + math.log(np.exp(y - m).sum())
-    lp = y - lse
+        return -np.inf, rank, -np.inf, 0.0, order, np.full(top, -np.inf), 0.0
+    ln_s = math.log(np.exp(y - m).sum())
+    lp = (y - m) - ln_s
     p = np.exp(lp)
     ent = -(p[p > 0] * lp[p > 0]).sum()
-    rank = int((x > x[token]).sum() + (x[:token] == x[token]).sum())
-    return lp[token], rank, lse, ent, order, lp[order]
+    return lp[token], rank, m + ln_s, ent, order, lp[order], ln_s

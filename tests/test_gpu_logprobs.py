@@ -34,7 +34,7 @@ def _check(wsw, logits, tokens, top, scale, ws=None, opts=None):
     for i in range(rows):
         t = 0 if tokens is None else tokens[i]
         inside = 0 <= t < vocab
-        lp, rank, lse, ent, order, best = ref.logprobs(x[i], t if inside else 0, scale, top)
+        lp, rank, lse, ent, order, best, ln_s = ref.logprobs(x[i], t if inside else 0, scale, top)
         assert np.array_equal(ids[i], order), i
         if tokens is not None:
             assert int(r.rank[i]) == (rank if inside else -1)
@@ -44,7 +44,6 @@ def _check(wsw, logits, tokens, top, scale, ws=None, opts=None):
                 assert float(r.logprob[i]) == -math.inf
             continue
         m = x[i].max() * scale
-        ln_s = lse - m
         assert abs(got["lse"][i] - lse) <= s_rel + 3 * EPS * (abs(lse) + abs(ln_s) + abs(m)), i
         mean = abs(ln_s - ent)
         assert abs(got["entropy"][i] - ent) <= s_rel * (1 + 2 * mean) + 3 * EPS * (abs(ln_s) + mean), i

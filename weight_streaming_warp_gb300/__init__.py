@@ -515,7 +515,7 @@ def kv_page_plan(seq_len, new_len, free_pages, head, table, page_size, tokens, o
     _packed(free_pages, torch.int32, "free_pages")
     _packed(head, torch.int32, "head", (1,))
     _dev(table, torch.int32, "table")
-    if table.dim() != 2 or table.shape[0] != n or (table.shape[1] > 1 and table.stride(1) != 1):
+    if table.dim() != 2 or table.shape[0] != n or (table.numel() > n and table.stride(1) != 1):
         raise WswError("table must be [requests][max_pages] with unit stride in max_pages")
     if out is None:
         dev = seq_len.device
@@ -622,7 +622,7 @@ def attn_paged_decode(q, kv, table, lens, scale=None, softcap=0.0, window=0, slo
     if hd != kv.head_dim or heads % kv.heads != 0:
         raise WswError("q must have the cache's head_dim and a multiple of its heads")
     _dev(table, torch.int32, "table")
-    if table.dim() != 2 or table.shape[0] != n or (table.shape[1] > 1 and table.stride(1) != 1):
+    if table.dim() != 2 or table.shape[0] != n or (table.numel() > n and table.stride(1) != 1):
         raise WswError("table must be [requests][max_pages] with unit stride in max_pages")
     if scale is None:
         scale = 1.0 / float(hd) ** 0.5

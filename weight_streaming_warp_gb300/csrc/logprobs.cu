@@ -453,7 +453,10 @@ void split_rows(int64_t rows, int64_t vocab, int *splits, int *chunk) {
     *splits = static_cast<int>((vocab + ch - 1) / ch);
 }
 int record_floats(int64_t top) { return static_cast<int>(4 + 2 * ((top + 1) / 2 * 2)); }
-size_t counter_bytes(int64_t rows) { return static_cast<size_t>((rows * 4 + 15) / 16 * 16); }
+// Rows are split only while there are at most kTargetCtas / 2 of them.  The counters' place does
+// not depend on the sizes: one workspace serves calls of different sizes in turn.
+constexpr size_t kCounterBytes = 1024;
+static_assert(kTargetCtas / 2 * 4 <= kCounterBytes, "counters");
 
 }  // namespace
 }  // namespace wsw
@@ -465,7 +468,7 @@ extern "C" size_t wsw_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab
     int splits, chunk;
     split_rows(rows, vocab, &splits, &chunk);
     if (splits == 1) return 0;
-    return counter_bytes(rows) + static_cast<size_t>(rows) * splits * record_floats(top) * 4;
+    return kCounterBytes + static_cast<size_t>(rows) * splits * record_floats(top) * 4;
 }
 
 extern "C" int wsw_token_logprobs(const void *logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
@@ -502,7 +505,7 @@ extern "C" int wsw_token_logprobs(const void *logits, int32_t dtype, int64_t row
     a.logprob = logprob; a.lse = lse; a.entropy = entropy; a.top_logprob = top_logprob;
     a.rank = rank; a.top_id = top_id;
     a.cnt = static_cast<unsigned *>(ws);
-    a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + (need ? counter_bytes(rows) : 0));
+    a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + (need ? kCounterBytes : 0));
     a.ld = ld; a.rows = rows;
     a.scale = scale;
     a.c = scale * kLog2e;
