@@ -78,9 +78,12 @@ struct Cfg {
     static constexpr int fit = (kSmemMax - warps * q_bytes) / (warps * stage);
     static constexpr int stages = fit < 6 ? fit : 6;
     static constexpr int ring = stages * stage;
-    static constexpr int smem = warps * (ring + q_bytes);
+    // the joins at the end keep weights where q was, or behind the rings
+    static constexpr int smem = warps * (ring + q_bytes) + (q_bytes == 0 ? 2048 : 0);
     static constexpr int rec = D + 4;                   // floats: m, l, 2 pad, sums
     static_assert(stages >= 2 && RT * rec * 4 <= ring && ring % 16 == 0, "ring");
+    static_assert((2 * warps + 2) * RT * 4 <= 2048 && smem <= kSmemMax + 1024, "joins");
+    static_assert(2 * kCtas * RT * 4 + (threads > RT * D / 4 ? threads : RT * D / 4) * 16 <= warps * ring, "joins");
 };
 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -151,12 +154,6 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t biased, uint32_t sel, __ha
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-__device__ __forceinline__ float2 load_q2(const Args &a, int64_t i) {
-    if (a.dtype == WSW_F32) return reinterpret_cast<const float2 *>(a.q)[i >> 1];
-    const uint32_t u = reinterpret_cast<const uint32_t *>(a.q)[i >> 1];
-    if (a.dtype == WSW_BF16) return make_float2(bf16lo(u), bf16hi(u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-}
 __device__ __forceinline__ void store_out4(const Args &a, int64_t i, float4 v) {
     if (a.dtype == WSW_F32) {
         *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i) = v;
@@ -378,37 +375,69 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 const int h = uc.hp / a.passes, g0 = (uc.hp - h * a.passes) * RT;
                 const int64_t head0 = static_cast<int64_t>(uc.r) * a.q_heads + h * a.group + g0;
                 bool some = false;
+                // every load of a batch is issued before the first is used
+                constexpr int kB = C::ksteps < 8 ? C::ksteps : 8;
 #pragma unroll
-                for (int kt = 0; kt < C::ksteps; ++kt) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {       // the fragment's two column halves
+                for (int k0 = 0; k0 < C::ksteps; k0 += kB) {
+                    float2 qv[kB][2][RT / 8];
+                    auto at = [&](int kt, int x, int row) -> int64_t {
                         // natural order for 16-bit rows; for q8_0 lane tq owns dimensions
                         // tq D / 4 ..., four of them per step
-                        const int d = C::q8 ? tq * (D / 4) + 4 * kt + 2 * x : 16 * kt + 8 * x + 2 * tq;
+                        const int d = C::q8 ? tq * (D / 4) + 4 * (k0 + kt) + 2 * x : 16 * (k0 + kt) + 8 * x + 2 * tq;
+                        return ((head0 + row) * D + d) >> 1;
+                    };
+                    if (a.dtype == WSW_F32) {
 #pragma unroll
-                        for (int y = 0; y < RT / 8; ++y) {
-                            const int row = gq + 8 * y;
-                            float2 v = make_float2(0.f, 0.f);
-                            if (g0 + row < a.group) v = load_q2(a, (head0 + row) * D + d);
-                            uint32_t vh, vl;
-                            split<CT>(v.x, v.y, vh, vl);
-                            if constexpr (RT == 8) {
-                                hi[2 * x] = vh;
-                                hi[2 * x + 1] = vl;
-                            } else {
-                                hi[2 * x + y] = vh;
-                                lo[2 * x + y] = vl;
-                                some |= (vl & 0x7fff7fffu) != 0;
-                            }
+                        for (int i = 0; i < kB * 2 * (RT / 8); ++i) {
+                            const int kt = i / (RT / 4), x = (i / (RT / 8)) & 1, y = i % (RT / 8);
+                            qv[kt][x][y] = g0 + gq + 8 * y < a.group
+                                               ? reinterpret_cast<const float2 *>(a.q)[at(kt, x, gq + 8 * y)]
+                                               : make_float2(0.f, 0.f);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kB * 2 * (RT / 8); ++i) {
+                            const int kt = i / (RT / 4), x = (i / (RT / 8)) & 1, y = i % (RT / 8);
+                            qv[kt][x][y].x = __uint_as_float(
+                                g0 + gq + 8 * y < a.group
+                                    ? reinterpret_cast<const uint32_t *>(a.q)[at(kt, x, gq + 8 * y)] : 0u);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kB * 2 * (RT / 8); ++i) {
+                            float2 &v = qv[i / (RT / 4)][(i / (RT / 8)) & 1][i % (RT / 8)];
+                            const uint32_t u = __float_as_uint(v.x);
+                            v = a.dtype == WSW_BF16 ? make_float2(bf16lo(u), bf16hi(u))
+                                                    : __half22float2(*reinterpret_cast<const __half2 *>(&u));
                         }
                     }
-                    if constexpr (C::q_smem) q_hi_sm[kt * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) qa[kt][i] = hi[i];
+                    for (int j = 0; j < kB; ++j) {
+                        const int kt = k0 + j;
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {  // the fragment's two column halves
+#pragma unroll
+                            for (int y = 0; y < RT / 8; ++y) {
+                                const float2 v = qv[j][x][y];
+                                uint32_t vh, vl;
+                                split<CT>(v.x, v.y, vh, vl);
+                                if constexpr (RT == 8) {
+                                    hi[2 * x] = vh;
+                                    hi[2 * x + 1] = vl;
+                                } else {
+                                    hi[2 * x + y] = vh;
+                                    lo[2 * x + y] = vl;
+                                    some |= (vl & 0x7fff7fffu) != 0;
+                                }
+                            }
+                        }
+                        if constexpr (C::q_smem) q_hi_sm[kt * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) qa[kt][i] = hi[i];
+                        }
+                        if constexpr (RT == 16) q_lo_sm[kt * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    if constexpr (RT == 16) q_lo_sm[kt * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 if constexpr (RT == 16) q_lo = __any_sync(WSW_FULL_MASK, some);
 #pragma unroll
@@ -660,10 +689,13 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     }
     __syncthreads();
 
-    // ---- join the warps' records, pair by pair in tile order
+    // ---- join the warps' records, pair by pair in tile order: the weights of a pair's
+    // records first, then independent sums
     constexpr int kCols = D / 4;
+    float *wgt = reinterpret_cast<float *>(smem + W * C::ring);  // [2 W][RT] weights, then [2][RT] m, l
+    float *joined = wgt + 2 * W * RT;
     int nshared = 0;
-    Piece shared_pair[2];
+    Piece shared_a, shared_b;
     for (int i = 0; i < 2 * W;) {
         const Piece pc = pieces[i];
         if (pc.r < 0) {
@@ -675,30 +707,47 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         const bool complete = pc.pstart >= b && pc.pstart + pc.nt <= e;
         const int h = pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
         const int rows = min(RT, a.group - g0);
+        auto record = [&](int k) -> const float * {
+            return k & 1 ? reinterpret_cast<const float *>(smem + (k >> 1) * C::ring)
+                         : a.wrec + static_cast<int64_t>(cta * W + (k >> 1)) * RT * C::rec;
+        };
+        if (tid < 32) {  // lane: row (of 16) and one of two interleaved runs of the records
+            const int row = lane & 15;
+            float mx = -INFINITY, l = 0.f;
+            if (row < rows)
+                for (int k = i + (lane >> 4); k < j; k += 2)
+                    if (pieces[k].r >= 0) mx = fmaxf(mx, record(k)[row * C::rec]);
+            mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, 16));
+            if (row < rows)
+                for (int k = i + (lane >> 4); k < j; k += 2) {
+                    if (pieces[k].r < 0) continue;
+                    const float *r = record(k) + row * C::rec;
+                    const float f = weight(r[0], mx);
+                    wgt[k * RT + row] = f;
+                    l = fmaf(r[1], f, l);
+                }
+            l += __shfl_xor_sync(WSW_FULL_MASK, l, 16);
+            if (lane < rows) {
+                joined[row] = mx;
+                joined[RT + row] = l;
+            }
+        }
+        __syncthreads();
         float *dst = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec;
         for (int u = tid; u < rows * kCols; u += NT) {
             const int row = u / kCols, c4 = u - row * kCols;
-            float mx = -INFINITY;
-            for (int k = i; k < j; ++k) {
-                if (pieces[k].r < 0) continue;
-                const float *r = (k & 1 ? reinterpret_cast<const float *>(smem + (k >> 1) * C::ring)
-                                        : a.wrec + static_cast<int64_t>(cta * W + (k >> 1)) * RT * C::rec) + row * C::rec;
-                mx = fmaxf(mx, r[0]);
-            }
-            float l = 0.f;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
             for (int k = i; k < j; ++k) {
                 if (pieces[k].r < 0) continue;
-                const float *r = (k & 1 ? reinterpret_cast<const float *>(smem + (k >> 1) * C::ring)
-                                        : a.wrec + static_cast<int64_t>(cta * W + (k >> 1)) * RT * C::rec) + row * C::rec;
-                const float f = weight(r[0], mx);
-                const float4 x = *reinterpret_cast<const float4 *>(r + 4 + 4 * c4);
-                l = fmaf(r[1], f, l);
+                const float f = wgt[k * RT + row];
+                const float4 x = *reinterpret_cast<const float4 *>(record(k) + row * C::rec + 4 + 4 * c4);
                 s.x = fmaf(x.x, f, s.x);
                 s.y = fmaf(x.y, f, s.y);
                 s.z = fmaf(x.z, f, s.z);
                 s.w = fmaf(x.w, f, s.w);
             }
+            const float mx = joined[row], l = joined[RT + row];
             if (complete) {
                 const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -707,23 +756,25 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             } else {
                 float *r = dst + row * C::rec;
                 *reinterpret_cast<float4 *>(r + 4 + 4 * c4) = s;
-                if (c4 == 0) {
-                    r[0] = mx;
-                    r[1] = l;
-                }
+                if (c4 == 0) *reinterpret_cast<float2 *>(r) = make_float2(mx, l);
             }
         }
-        if (!complete && nshared < 2) shared_pair[nshared++] = pc;
+        if (!complete) {
+            if (nshared == 0) shared_a = pc;
+            else shared_b = pc;
+            ++nshared;
+        }
+        __syncthreads();  // the weights' place is free again
         i = j;
     }
     if (nshared == 0) return;
 
-    // ---- pairs shared with other CTAs: the last to arrive joins their records.  The block
-    // barrier orders this CTA's records before thread 0's arrival, whose release publishes
-    // them; its acquire, and the barrier after it, order the reads after every arrival.
-    __syncthreads();
+    // ---- pairs shared with other CTAs (at most two): the last to arrive joins their records.
+    // The block barrier above orders this CTA's records before thread 0's arrival, whose
+    // release publishes them; its acquire, and the barrier after it, order the reads below
+    // after every arrival.
     if (tid < nshared) {
-        const Piece pc = shared_pair[tid];
+        const Piece pc = tid == 0 ? shared_a : shared_b;
         const int64_t f = pc.pstart / run, t = (pc.pstart + pc.nt - 1) / run;
         unsigned old;
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.cnt + f) : "memory");
@@ -732,55 +783,77 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     __syncthreads();
     for (int sp = 0; sp < nshared; ++sp) {
         if (!last[sp]) continue;
-        const Piece pc = shared_pair[sp];
+        const Piece pc = sp == 0 ? shared_a : shared_b;
         const int f = static_cast<int>(pc.pstart / run), n = static_cast<int>((pc.pstart + pc.nt - 1) / run) - f + 1;
         const int h = pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
         const int rows = min(RT, a.group - g0);
-        // threads (slice, row, column): the records are dealt to the slices, then the slices
-        // are joined in order
-        int slices = NT / (rows * kCols);
-        if (slices < 1) slices = 1;
-        float *part = reinterpret_cast<float *>(smem);  // [slices * rows * kCols][6]
-        for (int u = tid; u < slices * rows * kCols; u += NT) {
-            const int sl = u / (rows * kCols), v = u - sl * rows * kCols;
-            const int row = v / kCols, c4 = v - row * kCols;
-            float mx = -INFINITY, l = 0.f;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int k = sl; k < n; k += slices) {
-                // the first CTA holds the pair's beginning as its second shared pair
-                const float *r = a.rec + (static_cast<int64_t>(f + k) * 2 + (k == 0)) * RT * C::rec + row * C::rec;
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(r));
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(r + 4 + 4 * c4));
-                const float mn = fmaxf(mx, ml.x);
-                const float fo = weight(mx, mn), fn = weight(ml.x, mn);
-                mx = mn;
-                l = l * fo + ml.y * fn;
-                s.x = s.x * fo + x.x * fn;
-                s.y = s.y * fo + x.y * fn;
-                s.z = s.z * fo + x.z * fn;
-                s.w = s.w * fo + x.w * fn;
-            }
-            float *w = part + u * 6;
-            w[0] = mx; w[1] = l; w[2] = s.x; w[3] = s.y; w[4] = s.z; w[5] = s.w;
+        // record k: CTA f + k's; the first CTA holds the pair's beginning as its second pair
+        auto record = [&](int k) -> const float * {
+            return a.rec + (static_cast<int64_t>(f + k) * 2 + (k == 0)) * RT * C::rec;
+        };
+        float *w = reinterpret_cast<float *>(smem);             // [n][RT] maxima, then weights
+        float *lw = w + kCtas * RT;                             // [n][RT] sums
+        float *part = lw + kCtas * RT;                          // [slices][rows][D]
+        for (int u = tid; u < n * RT; u += NT) {
+            const int k = u / RT, row = u - k * RT;
+            if (row >= rows) continue;
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(record(k) + row * C::rec));
+            w[u] = ml.x;
+            lw[u] = ml.y;
         }
         __syncthreads();
-        for (int u = tid; u < rows * kCols; u += NT) {
-            const int row = u / kCols, c4 = u - row * kCols;
-            float mx = -INFINITY;
-            for (int sl = 0; sl < slices; ++sl) mx = fmaxf(mx, part[(sl * rows * kCols + u) * 6]);
-            float l = 0.f, s[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int sl = 0; sl < slices; ++sl) {
-                const float *w = part + (sl * rows * kCols + u) * 6;
-                const float fn = weight(w[0], mx);
-                l = fmaf(w[1], fn, l);
+        for (int row = warp; row < rows; row += W) {
+            float mx = -INFINITY, l = 0.f;
+            for (int k = lane; k < n; k += 32) mx = fmaxf(mx, w[k * RT + row]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = fmaf(w[2 + i], fn, s[i]);
+            for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
+            for (int k = lane; k < n; k += 32) {
+                const float g = weight(w[k * RT + row], mx);
+                w[k * RT + row] = g;
+                l = fmaf(lw[k * RT + row], g, l);
+            }
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(WSW_FULL_MASK, l, d);
+            __syncwarp();
+            if (lane == 0) {
+                lw[row] = l;  // record 0's sums have been read
+                const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
+                if (a.lse) a.lse[head] = lse_of(mx, l);
+            }
+        }
+        __syncthreads();
+        // the records are dealt to slices of the block, whose sums are then added in order
+        const int units = rows * kCols;
+        const int slices = NT / units > 1 ? NT / units : 1;
+        for (int u = tid; u < slices * units; u += NT) {
+            const int sl = u / units, v = u - sl * units;
+            const int row = v / kCols, c4 = v - row * kCols;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 16
+            for (int k = sl; k < n; k += slices) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(record(k) + row * C::rec + 4 + 4 * c4));
+                const float g = w[k * RT + row];
+                s.x = fmaf(x.x, g, s.x);
+                s.y = fmaf(x.y, g, s.y);
+                s.z = fmaf(x.z, g, s.z);
+                s.w = fmaf(x.w, g, s.w);
+            }
+            *reinterpret_cast<float4 *>(part + u * 4) = s;
+        }
+        __syncthreads();
+        for (int u = tid; u < units; u += NT) {
+            const int row = u / kCols, c4 = u - row * kCols;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int sl = 0; sl < slices; ++sl) {
+                const float4 x = *reinterpret_cast<const float4 *>(part + (sl * units + u) * 4);
+                s.x += x.x;
+                s.y += x.y;
+                s.z += x.z;
+                s.w += x.w;
             }
             const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            store_out4(a, head * D + 4 * c4, make_float4(s[0] * inv, s[1] * inv, s[2] * inv, s[3] * inv));
-            if (c4 == 0 && a.lse) a.lse[head] = lse_of(mx, l);
+            const float inv = lw[row] == 0.f ? 0.f : 1.f / lw[row];
+            store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
         }
         if (tid == 0) a.cnt[f] = 0u;  // ready for the next call
         __syncthreads();
