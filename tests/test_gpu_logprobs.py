@@ -180,4 +180,4 @@ def test_workspace_reuse_options_and_streams():
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(x, y) for x, y in zip(a, c))
     torch.cuda.synchronize()
-    assert int(ws[:8].view(torch.int32).abs().sum()) == 0, "counters left nonzero"
+    assert int(ws[:2048].view(torch.int32).abs().sum()) == 0, "counters left nonzero"

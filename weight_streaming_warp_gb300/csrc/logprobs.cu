@@ -11,10 +11,11 @@
 // maximum reaches the token's logit.
 //
 // Top k: only values above a threshold that is never above the k-th best of what was seen
-// enter a candidate buffer in shared memory.  The first threshold is the k-th largest of
-// the 256 threads' maxima over the first tile (k distinct values are at least as large),
-// which leaves about k candidates of 8192.  Between tiles the buffer is cut to its k best
-// keys once it holds more than kKeep, which raises the threshold.  Keys are 64 bits, the
+// enter a candidate buffer in shared memory.  The first threshold is the k-th largest of the
+// maxima of 32 groups of threads over the first tile (k distinct values are at least as
+// large), which leaves k to some tens of candidates.  After the first tile, and
+// later once it holds more than kKeep, the buffer is cut to its k best keys, which raises the
+// threshold to the k-th best value so far.  Keys are 64 bits, the
 // value's order-preserving bits over the complemented index, so that they are distinct and
 // equal values rank by index.  A tile that overflows the buffer (a long run of equal or
 // rising values) is read again in pieces that cannot.
@@ -37,8 +38,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kUnroll = 4;      // 16-byte vectors per thread and tile
 constexpr int kCap = 1024;      // candidate buffer
-constexpr int kKeep = 256;      // cut the buffer between tiles beyond this
-constexpr int kTargetCtas = 304;
+constexpr int kKeep = 96;       // cut the buffer between tiles beyond this
+constexpr int kLook = 2;        // look at the buffer every so many tiles
+constexpr int kTargetCtas = 608;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct LpArgs {
@@ -77,11 +79,24 @@ __device__ __forceinline__ uint64_t key_of(float x, int i) {
     return (static_cast<uint64_t>(ord(x)) << 32) | static_cast<uint32_t>(~i);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// two fp32 values in one register pair, for the packed arithmetic
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
     static constexpr int kVec = 4;
+    static constexpr uint32_t kLow = 0xff800000u;  // -inf in every element of a word
     __device__ static float get(const float *p, int64_t i) { return p[i]; }
     __device__ static void unpack(const uint4 &u, float (&x)[4]) {
         x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
@@ -90,6 +105,7 @@ struct Elem<float> {
 template <>
 struct Elem<__half> {
     static constexpr int kVec = 8;
+    static constexpr uint32_t kLow = 0xfc00fc00u;
     __device__ static float get(const __half *p, int64_t i) { return __half2float(p[i]); }
     __device__ static void unpack(const uint4 &u, float (&x)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -104,6 +120,7 @@ struct Elem<__half> {
 template <>
 struct Elem<__nv_bfloat16> {
     static constexpr int kVec = 8;
+    static constexpr uint32_t kLow = 0xff80ff80u;
     __device__ static float get(const __nv_bfloat16 *p, int64_t i) { return __bfloat162float(p[i]); }
     __device__ static void unpack(const uint4 &u, float (&x)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -114,6 +131,12 @@ struct Elem<__nv_bfloat16> {
         }
     }
 };
+
+// the least value above x (above -inf: -FLT_MAX; above +inf: nothing, NaN)
+__device__ __forceinline__ float above(float x) {
+    if (x == 0.f) return __uint_as_float(1u);
+    return x < INFINITY ? __uint_as_float(__float_as_uint(x) + (x > 0.f ? 1 : -1)) : NAN;
+}
 
 // Running sums of one thread, then of larger sets.  m >= -FLT_MAX, so that x - m is never
 // (-inf) - (-inf).
@@ -138,7 +161,7 @@ __device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
 struct Shared {
     uint64_t buf[kCap];
     uint64_t best[kMaxTop];
-    float mx[kThreads];
+    float group[kMaxTop];
     Sums sums[kWarps];
     int count[kWarps];
     int n;         // candidates in buf (may pass kCap: then the tile is read again)
@@ -146,18 +169,22 @@ struct Shared {
     int last;
 };
 
-// The k-th largest of n distinct-by-index values v (ties ordered by index), 1 <= k <= n: every
-// thread calls it; the result goes to sm.thr.
-__device__ __forceinline__ void kth_of_maxima(Shared &sm, int k) {
+// A value that at least k <= 32 of the block's values reach, from the threads' maxima: the k-th
+// largest maximum of 32 groups of eight threads.  Every thread calls it and gets it.
+__device__ __forceinline__ float reached_by(Shared &sm, float mx, int k) {
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
+    if ((threadIdx.x & 7) == 0) sm.group[threadIdx.x >> 3] = mx;
     __syncthreads();
-    const float own = sm.mx[threadIdx.x];
-    int above = 0;
-    for (int i = 0; i < kThreads; ++i) {
-        const float o = sm.mx[i];
-        above += o > own || (o == own && i < static_cast<int>(threadIdx.x));
+    const int lane = threadIdx.x & 31;
+    const float own = sm.group[lane];
+    int larger = 0;
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) {
+        const float o = sm.group[j];
+        larger += o > own || (o == own && j < lane);
     }
-    if (above == k - 1) sm.thr = own;
-    __syncthreads();
+    return __shfl_sync(WSW_FULL_MASK, own, __ffs(__ballot_sync(WSW_FULL_MASK, larger == k - 1)) - 1);
 }
 
 // Cut the buffer to its k best keys, in order, and set the threshold.  Every thread calls it.
@@ -240,7 +267,7 @@ __device__ __forceinline__ void finish(const LpArgs &a, Shared &sm, int64_t row,
 template <typename T>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     constexpr int V = Elem<T>::kVec;
-    constexpr int kTile = kThreads * kUnroll * V;  // values per tile
+    constexpr int kTile = kThreads * kUnroll * V;  // values per tile (4096 or 8192)
     __shared__ Shared sm;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x / a.splits;
@@ -248,121 +275,165 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     pdl_launch_dependents();
     pdl_wait();
     const T *x = static_cast<const T *>(a.x) + row * a.ld;
-    // positions of 16-byte vectors: the row's first `lead` values come before the first one.
-    // Vector v covers values lead + v V ...; v = -1 and the last one may be partial.
-    const int lead = static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T));
-    const int64_t begin = static_cast<int64_t>(split) * a.chunk;  // in values, before the shift by lead
-    const int lo = begin == 0 ? 0 : static_cast<int>(min(begin + lead, static_cast<int64_t>(a.vocab)));
-    const int hi = static_cast<int>(min(begin + a.chunk + lead, static_cast<int64_t>(a.vocab)));
+    // The row as 16-byte vectors: `lead` values come before the first.  The split takes the
+    // vectors of [lo, hi); the first split also the values before them, the last one those
+    // after the last whole vector: at most V - 1 each, one for each of the first threads.
+    const int lead = min(static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)), a.vocab);
+    const int64_t begin = lead + static_cast<int64_t>(split) * a.chunk;
+    const int whole = lead + (a.vocab - lead) / V * V;  // end of the last whole vector
+    const int lo = static_cast<int>(min(begin, static_cast<int64_t>(whole)));
+    const int hi = static_cast<int>(min(begin + a.chunk, static_cast<int64_t>(whole)));
     const float c = a.c;
     const int k = a.top;
 
+    uint4 raw[kUnroll];
+    auto fetch = [&](int tile0) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int at = tile0 + (u * kThreads + tid) * V;
+            raw[u] = make_uint4(Elem<T>::kLow, Elem<T>::kLow, Elem<T>::kLow, Elem<T>::kLow);
+            if (at < hi) raw[u] = __ldg(reinterpret_cast<const uint4 *>(x + at));
+        }
+    };
+    fetch(lo);
+
+    // rank: x_j >= xt for j < t, x_j >= the next value for j > t; NaN: nothing counts.  A vector
+    // that holds t counts as after it; its equal values before t are added here.
     const int t = a.tokens ? a.tokens[row] : -1;
     const bool has_t = t >= 0 && t < a.vocab;
-    const float xt = has_t ? Elem<T>::get(x, t) : INFINITY;  // nothing is above it, so nothing is counted
-    Sums s{-FLT_MAX, 0.f, 0.f};
+    const float xt = has_t ? Elem<T>::get(x, t) : NAN;
+    const float xt_next = above(xt);
     int count = 0;
+    if (tid == 64 && has_t && t >= lo && t < hi)
+        for (int i = lo + (t - lo) / V * V; i < t; ++i) count += Elem<T>::get(x, i) == xt;
+    Sums s{-FLT_MAX, 0.f, 0.f};
     if (tid == 0) {
         sm.n = 0;
         sm.thr = -INFINITY;
     }
+    __syncthreads();
+    {
+        int i = -1;
+        if (split == 0 && tid < lead) i = tid;
+        if (split == a.splits - 1 && tid >= 32 && tid - 32 < a.vocab - whole) i = whole + tid - 32;
+        if (i >= 0) {
+            const float v = Elem<T>::get(x, i);
+            count += v >= (i < t ? xt : xt_next);
+            if (!(v == -INFINITY)) {
+                s.m = fmaxf(v, -FLT_MAX);
+                s.s = v != v || v == INFINITY ? NAN : 1.f;
+            }
+            if (k > 0) push(sm, key_of(v, i));
+        }
+    }
+    const uint64_t c2 = f2(c, c);
 
-    // Each tile covers values [tile0, tile0 + kTile) with tile0 congruent to lead modulo V; the
-    // first starts at or before lo.
-    const int tile_first = lo - (((lo - lead) % V + V) % V);
+    int since = 0, filled = 0;  // tiles since the buffer was looked at, candidates known then
+    int group0 = lo;
     bool first = true;
-    for (int64_t tile0 = tile_first; tile0 < hi; tile0 += kTile) {
+    for (int tile0 = lo; tile0 < hi; tile0 += kTile) {
         float v[kUnroll][V];
         float vm[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int64_t at = tile0 + (static_cast<int64_t>(u) * kThreads + tid) * V;
-            if (at >= lo && at + V <= hi) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(x + at));
-                Elem<T>::unpack(w, v[u]);
-            } else {
+            Elem<T>::unpack(raw[u], v[u]);
+            const int at = tile0 + (u * kThreads + tid) * V;
+            const float tq = at >= hi ? NAN : at + V <= t ? xt : xt_next;
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[u][i] = at + i >= lo && at + i < hi ? Elem<T>::get(x, at + i) : -INFINITY;
-            }
+            for (int i = 0; i < V; ++i) count += v[u][i] >= tq;
         }
+        if (tile0 + kTile < hi) fetch(tile0 + kTile);  // in flight during this tile's arithmetic
         float tm = -INFINITY;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            vm[u] = v[u][0];
+            vm[u] = fmaxf(v[u][0], v[u][1]);
 #pragma unroll
-            for (int i = 1; i < V; ++i) vm[u] = fmaxf(vm[u], v[u][i]);
+            for (int i = 2; i < V; i += 2) vm[u] = max3(vm[u], v[u][i], v[u][i + 1]);
             tm = fmaxf(tm, vm[u]);
         }
         if (tm > s.m) raise(s, tm, c);
+        const uint64_t nm2 = f2(-s.m, -s.m);
+        uint64_t ss = 0ull, ee = 0ull;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = max_nan((v[u][i] - s.m) * c, -200.f);  // 2^-200 is 0, and 0 times -200 too
-                const float e = ex2(d);
-                s.s += e;
-                s.e = fmaf(e, d, s.e);
+            for (int i = 0; i < V; i += 2) {
+                uint64_t d2 = f2(v[u][i], v[u][i + 1]);
+                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d2) : "l"(nm2));
+                asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d2) : "l"(c2));
+                float d0, d1;
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d2));
+                d0 = max_nan(d0, -200.f);  // 2^-200 is 0, and 0 times -200 too
+                d1 = max_nan(d1, -200.f);
+                const uint64_t e2 = f2(ex2(d0), ex2(d1));
+                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(ss) : "l"(e2));
+                asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(ee) : "l"(e2), "l"(f2(d0, d1)));
             }
-        if (tm >= xt) {
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int64_t at = tile0 + (static_cast<int64_t>(u) * kThreads + tid) * V;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    count += at + i >= lo && at + i < hi && (v[u][i] > xt || (v[u][i] == xt && at + i < t));
-            }
+        {
+            float x0, x1;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(ss));
+            s.s += x0 + x1;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(ee));
+            s.e += x0 + x1;
         }
-        if (k > 0) {
-            if (first) {
-                sm.mx[tid] = tm;
-                kth_of_maxima(sm, k);
-            }
-            const float thr = sm.thr;
-            int filled = 0;
-            if (first ? tm >= thr : tm > thr) {
+        if (k == 0) continue;
+        // first tile: everything that reaches the bound; then only what beats the k-th best
+        const float thr = first ? reached_by(sm, tm, k) : above(sm.thr);
+        if (tm >= thr) {
+            // few vectors get here: they are read again, so that this code stays small
+            unsigned hits = 0;
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int64_t at = tile0 + (static_cast<int64_t>(u) * kThreads + tid) * V;
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (at + i >= lo && at + i < hi && (first ? v[u][i] >= thr : v[u][i] > thr))
-                            filled = push(sm, key_of(v[u][i], static_cast<int>(at) + i));
+            for (int u = 0; u < kUnroll; ++u) hits |= static_cast<unsigned>(vm[u] >= thr) << u;
+#pragma unroll 1
+            while (hits) {
+                const int u = __ffs(hits) - 1;
+                hits &= hits - 1;
+                const int at = tile0 + (u * kThreads + tid) * V;
+                if (at >= hi) break;
+#pragma unroll 1
+                for (int i = 0; i < V; ++i) {
+                    const float y = Elem<T>::get(x, at + i);
+                    if (y >= thr) filled = push(sm, key_of(y, at + i));
                 }
             }
-            // one answer for the whole block; inside, nobody pushes until all have read sm.n
-            const bool over = __syncthreads_or(filled > kKeep);
-            const int n = over ? sm.n : 0;
-            if (n > kCap) {
-                // too many: drop this tile's candidates and take the tile again in pieces of
-                // kCap - kMaxTop values, cutting after each
+        }
+        if (!first && ++since < kLook && tile0 + kTile < hi) continue;
+        // one answer for the whole block; inside, nobody pushes until all have read sm.n
+        const bool over = __syncthreads_or(filled > kKeep) || first;
+        const int n = over ? sm.n : 0;
+        const int group_end = min(tile0 + kTile, hi);
+        if (n > kCap) {
+            // too many: drop the candidates of the tiles since the last look and take those
+            // values again in pieces of kCap - kMaxTop, cutting after each
+            __syncthreads();
+            if (tid == 0) {
+                int kept = 0;
+                for (int i = 0; i < kCap; ++i) {
+                    const int idx = static_cast<int>(~static_cast<uint32_t>(sm.buf[i]));
+                    if (idx < group0 || idx >= group_end) sm.buf[kept++] = sm.buf[i];
+                }
+                sm.n = kept;
+            }
+            __syncthreads();
+            cut(sm, k);
+#pragma unroll 1
+            for (int p = group0; p < group_end; p += kCap - kMaxTop) {
+                const uint64_t floor = sm.n == k ? sm.best[k - 1] : 0;
+                const int end = min(p + (kCap - kMaxTop), group_end);
                 __syncthreads();
-                if (tid == 0) {
-                    int kept = 0;
-                    for (int i = 0; i < kCap && !first; ++i) {
-                        const int idx = static_cast<int>(~static_cast<uint32_t>(sm.buf[i]));
-                        if (idx < tile0) sm.buf[kept++] = sm.buf[i];
-                    }
-                    sm.n = kept;
+                for (int i = p + tid; i < end; i += kThreads) {
+                    const uint64_t key = key_of(Elem<T>::get(x, i), i);
+                    if (key > floor) push(sm, key);
                 }
                 __syncthreads();
                 cut(sm, k);
-                for (int64_t p = tile0; p < tile0 + kTile; p += kCap - kMaxTop) {
-                    const uint64_t floor = sm.n == k ? sm.best[k - 1] : 0;
-                    const int64_t end = min(p + (kCap - kMaxTop), tile0 + kTile);
-                    __syncthreads();
-                    for (int64_t i = p + tid; i < end; i += kThreads)
-                        if (i >= lo && i < hi) {
-                            const uint64_t key = key_of(Elem<T>::get(x, i), static_cast<int>(i));
-                            if (key > floor) push(sm, key);
-                        }
-                    __syncthreads();
-                    cut(sm, k);
-                }
-            } else if (over) {
-                cut(sm, k);
             }
-            first = false;
+        } else if (over) {
+            cut(sm, k);
         }
+        first = false;
+        since = filled = 0;
+        group0 = tile0 + kTile;
     }
     if (k > 0) {
         __syncthreads();
@@ -401,30 +472,33 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
         count += __float_as_int(r.w);
     }
     if (k > 0) {
-        // the same selection over the splits' keys
+        // The splits' keys are in order.  A key that k of them reach: the k-th largest of the
+        // splits' best, or with fewer splits the least of their ceil(k / splits)-th.
+        auto key_at = [&](int sp, int i) {
+            return __ldcg(reinterpret_cast<const uint64_t *>(recs + static_cast<int64_t>(sp) * a.rec + 4) + i);
+        };
+        const int depth = (k + a.splits - 1) / a.splits, keys = a.splits * k;
         if (tid == 0) {
             sm.n = 0;
             sm.thr = -INFINITY;
         }
-        const int keys = a.splits * k;
-        float tm = -INFINITY;
-        for (int i = tid; i < keys; i += kThreads) {
-            const int sp = i / k;
-            const uint64_t key =
-                __ldcg(reinterpret_cast<const uint64_t *>(recs + static_cast<int64_t>(sp) * a.rec + 4) + (i - sp * k));
-            if (key >> 32 > 1) tm = fmaxf(tm, unord(static_cast<uint32_t>(key >> 32)));
+        for (int i = tid; i < a.splits; i += kThreads) sm.buf[i] = key_at(i, depth - 1);
+        __syncthreads();
+        for (int i = tid; i < a.splits; i += kThreads) {
+            const uint64_t own = sm.buf[i];
+            int more = 0;  // ties (absent keys are 0) by index
+            for (int j = 0; j < a.splits; ++j) more += sm.buf[j] > own || (sm.buf[j] == own && j < i);
+            if (more == min(k, a.splits) - 1) sm.best[0] = own;
         }
-        sm.mx[tid] = tm;
-        kth_of_maxima(sm, k);
-        const uint64_t thr = static_cast<uint64_t>(ord(sm.thr)) << 32;
+        __syncthreads();
+        const uint64_t thr = sm.best[0];
         for (int base = 0; base < keys; base += kCap - kMaxTop) {
             const int end = min(base + kCap - kMaxTop, keys);
             const uint64_t floor = base > 0 && sm.n == k ? sm.best[k - 1] : 0;
             __syncthreads();
             for (int i = base + tid; i < end; i += kThreads) {
                 const int sp = i / k;
-                const uint64_t key = __ldcg(
-                    reinterpret_cast<const uint64_t *>(recs + static_cast<int64_t>(sp) * a.rec + 4) + (i - sp * k));
+                const uint64_t key = key_at(sp, i - sp * k);
                 if (key >= thr && key > floor) push(sm, key);
             }
             __syncthreads();
@@ -455,7 +529,7 @@ void split_rows(int64_t rows, int64_t vocab, int *splits, int *chunk) {
 int record_floats(int64_t top) { return static_cast<int>(4 + 2 * ((top + 1) / 2 * 2)); }
 // Rows are split only while there are at most kTargetCtas / 2 of them.  The counters' place does
 // not depend on the sizes: one workspace serves calls of different sizes in turn.
-constexpr size_t kCounterBytes = 1024;
+constexpr size_t kCounterBytes = 2048;
 static_assert(kTargetCtas / 2 * 4 <= kCounterBytes, "counters");
 
 }  // namespace
