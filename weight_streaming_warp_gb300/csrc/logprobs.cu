@@ -11,14 +11,14 @@
 // maximum reaches the token's logit.
 //
 // Top k: only values above a threshold that is never above the k-th best of what was seen
-// enter a candidate buffer in shared memory.  The first threshold is the k-th largest of the
+// are kept, their whole 16-byte vector at first, in shared memory.  The first threshold is the k-th largest of the
 // maxima of 32 groups of threads over the first tile (k distinct values are at least as
-// large), which leaves k to some tens of candidates.  After the first tile, and
-// later once it holds more than kKeep, the buffer is cut to its k best keys, which raises the
-// threshold to the k-th best value so far.  Keys are 64 bits, the
+// large), which leaves k to some tens of candidates a tile.  Once
+// there are more than kKeep vectors, their values become keys and the keys are cut to the k
+// best, which raises the threshold to the k-th best value so far.  Keys are 64 bits, the
 // value's order-preserving bits over the complemented index, so that they are distinct and
-// equal values rank by index.  A tile that overflows the buffer (a long run of equal or
-// rising values) is read again in pieces that cannot.
+// equal values rank by index.  Tiles that bring too many vectors (a long run of equal or
+// rising values) are read again in pieces that cannot.
 //
 // Rows are split over CTAs when there are few; each split leaves (m, S, E, count, k keys) in
 // the workspace and the row's last CTA joins them in a fixed order.
@@ -33,13 +33,15 @@
 namespace wsw {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kUnroll = 4;      // 16-byte vectors per thread and tile
-constexpr int kCap = 1024;      // candidate buffer
-constexpr int kKeep = 96;       // cut the buffer between tiles beyond this
-constexpr int kLook = 2;        // look at the buffer every so many tiles
+constexpr int kCap = 1024;      // keys
+constexpr int kVecs = 112;      // candidate vectors: at most 8 keys each, beside k and the row's ends
+constexpr int kKeep = 28;       // make keys of them beyond this
+constexpr int kLook = 2;        // look at their number every so many tiles
+static_assert(kVecs * 8 + kMaxTop + 16 <= kCap, "keys");
 constexpr int kTargetCtas = 608;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -105,6 +107,10 @@ struct Elem<float> {
 template <>
 struct Elem<__half> {
     static constexpr int kVec = 8;
+    static constexpr bool kBf16 = false;
+    using Pair = __half2;
+    __device__ static Pair pair(float x) { return __float2half2_rn(x); }
+    __device__ static float2 floats(Pair p) { return __half22float2(p); }
     static constexpr uint32_t kLow = 0xfc00fc00u;
     __device__ static float get(const __half *p, int64_t i) { return __half2float(p[i]); }
     __device__ static void unpack(const uint4 &u, float (&x)[8]) {
@@ -120,6 +126,10 @@ struct Elem<__half> {
 template <>
 struct Elem<__nv_bfloat16> {
     static constexpr int kVec = 8;
+    static constexpr bool kBf16 = true;
+    using Pair = __nv_bfloat162;
+    __device__ static Pair pair(float x) { return __float2bfloat162_rn(x); }
+    __device__ static float2 floats(Pair p) { return __bfloat1622float2(p); }
     static constexpr uint32_t kLow = 0xff80ff80u;
     __device__ static float get(const __nv_bfloat16 *p, int64_t i) { return __bfloat162float(p[i]); }
     __device__ static void unpack(const uint4 &u, float (&x)[8]) {
@@ -132,11 +142,74 @@ struct Elem<__nv_bfloat16> {
     }
 };
 
+// unpack's inverse (exact: the values came from it)
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&x)[Elem<T>::kVec]) {
+    if constexpr (sizeof(T) == 4) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (Elem<T>::kBf16) {
+                w[i] = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
+            } else {
+                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 // the least value above x (above -inf: -FLT_MAX; above +inf: nothing, NaN)
 __device__ __forceinline__ float above(float x) {
     if (x == 0.f) return __uint_as_float(1u);
     return x < INFINITY ? __uint_as_float(__float_as_uint(x) + (x > 0.f ? 1 : -1)) : NAN;
 }
+
+// the same among T's values, for an x that is one
+template <typename T>
+__device__ __forceinline__ float above_in(float x) {
+    if constexpr (sizeof(T) == 4) {
+        return above(x);
+    } else {
+        if (!(x < INFINITY)) return NAN;
+        constexpr bool bf = Elem<T>::kBf16;
+        if (x == 0.f) return bf ? __uint_as_float(1u << 16) : __half2float(__ushort_as_half(1));
+        const uint16_t b = bf ? __float_as_uint(x) >> 16 : __half_as_ushort(__float2half_rn(x));
+        const uint16_t n = static_cast<uint16_t>(b + (x > 0.f ? 1 : -1));
+        return bf ? __uint_as_float(static_cast<uint32_t>(n) << 16) : __half2float(__ushort_as_half(n));
+    }
+}
+
+// Counts a tile's values from a bound up.  16-bit values are compared and counted in pairs (at
+// most 16 of each half: exact); the bound is one of their type's values, or NaN for nothing.
+template <typename T>
+struct Counter {
+    using Pair = typename Elem<T>::Pair;
+    Pair n = Elem<T>::pair(0.f);
+    __device__ static Pair bound(float b) { return Elem<T>::pair(b); }
+    __device__ void add(const uint4 &raw, const float (&)[8], Pair b) {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n = __hadd2(n, __hge2(*reinterpret_cast<const Pair *>(&w[i]), b));
+    }
+    __device__ int total() const {
+        const float2 f = Elem<T>::floats(n);
+        return static_cast<int>(f.x + f.y);
+    }
+};
+template <>
+struct Counter<float> {
+    int n = 0;
+    __device__ static float bound(float b) { return b; }
+    __device__ void add(const uint4 &, const float (&x)[4], float b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += x[i] >= b;
+    }
+    __device__ int total() const { return n; }
+};
 
 // Running sums of one thread, then of larger sets.  m >= -FLT_MAX, so that x - m is never
 // (-inf) - (-inf).
@@ -159,22 +232,25 @@ __device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
 }
 
 struct Shared {
+    uint4 vec[kVecs];
+    int vec_at[kVecs];
+    int nvec;      // may pass kVecs: then the tiles are read again
     uint64_t buf[kCap];
     uint64_t best[kMaxTop];
     float group[kMaxTop];
     Sums sums[kWarps];
     int count[kWarps];
-    int n;         // candidates in buf (may pass kCap: then the tile is read again)
+    int n;         // keys in buf
     float thr;
     int last;
 };
 
 // A value that at least k <= 32 of the block's values reach, from the threads' maxima: the k-th
-// largest maximum of 32 groups of eight threads.  Every thread calls it and gets it.
+// largest maximum of 32 groups of neighbouring threads.  Every thread calls it and gets it.
 __device__ __forceinline__ float reached_by(Shared &sm, float mx, int k) {
 #pragma unroll
-    for (int d = 4; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
-    if ((threadIdx.x & 7) == 0) sm.group[threadIdx.x >> 3] = mx;
+    for (int d = kThreads / 64; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
+    if (threadIdx.x % (kThreads / 32) == 0) sm.group[threadIdx.x / (kThreads / 32)] = mx;
     __syncthreads();
     const int lane = threadIdx.x & 31;
     const float own = sm.group[lane];
@@ -189,10 +265,11 @@ __device__ __forceinline__ float reached_by(Shared &sm, float mx, int k) {
 
 // Cut the buffer to its k best keys, in order, and set the threshold.  Every thread calls it.
 __device__ __forceinline__ void cut(Shared &sm, int k) {
-    const int n = min(sm.n, kCap);
+    const int n = sm.n;
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t own = sm.buf[i];
         int above = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) above += sm.buf[j] > own;
         if (above < k) sm.best[above] = own;
     }
@@ -206,11 +283,21 @@ __device__ __forceinline__ void cut(Shared &sm, int k) {
     __syncthreads();
 }
 
-// Returns how many candidates there are now (beyond kCap they are dropped).
-__device__ __forceinline__ int push(Shared &sm, uint64_t key) {
-    const int at = atomicAdd(&sm.n, 1);
-    if (at < kCap) sm.buf[at] = key;
-    return at + 1;
+__device__ __forceinline__ void push(Shared &sm, uint64_t key) { sm.buf[atomicAdd(&sm.n, 1)] = key; }
+
+// The candidate vectors' values from thr up become keys; then the keys are cut.  Every thread
+// calls it, with the vectors written before a barrier.
+template <typename T>
+__device__ __forceinline__ void take_vectors(Shared &sm, float thr, int k) {
+    constexpr int V = Elem<T>::kVec;
+    const int n = sm.nvec * V;
+    for (int e = threadIdx.x; e < n; e += kThreads) {
+        const float y = Elem<T>::get(reinterpret_cast<const T *>(sm.vec), e);
+        if (y >= thr) push(sm, key_of(y, sm.vec_at[e / V] + e % V));
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sm.nvec = 0;
+    cut(sm, k);
 }
 
 // The block's sums and count, valid in thread 0.
@@ -265,7 +352,7 @@ __device__ __forceinline__ void finish(const LpArgs &a, Shared &sm, int64_t row,
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) logprobs_kernel(const LpArgs a) {
     constexpr int V = Elem<T>::kVec;
     constexpr int kTile = kThreads * kUnroll * V;  // values per tile (4096 or 8192)
     __shared__ Shared sm;
@@ -303,12 +390,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     const bool has_t = t >= 0 && t < a.vocab;
     const float xt = has_t ? Elem<T>::get(x, t) : NAN;
     const float xt_next = above(xt);
+    const auto ge_t = Counter<T>::bound(xt), gt_t = Counter<T>::bound(above_in<T>(xt)), none = Counter<T>::bound(NAN);
     int count = 0;
     if (tid == 64 && has_t && t >= lo && t < hi)
         for (int i = lo + (t - lo) / V * V; i < t; ++i) count += Elem<T>::get(x, i) == xt;
     Sums s{-FLT_MAX, 0.f, 0.f};
     if (tid == 0) {
-        sm.n = 0;
+        sm.n = sm.nvec = 0;
         sm.thr = -INFINITY;
     }
     __syncthreads();
@@ -331,17 +419,18 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
     int since = 0, filled = 0;  // tiles since the buffer was looked at, candidates known then
     int group0 = lo;
     bool first = true;
+    float thr = -INFINITY;
     for (int tile0 = lo; tile0 < hi; tile0 += kTile) {
         float v[kUnroll][V];
         float vm[kUnroll];
+        Counter<T> counted;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             Elem<T>::unpack(raw[u], v[u]);
             const int at = tile0 + (u * kThreads + tid) * V;
-            const float tq = at >= hi ? NAN : at + V <= t ? xt : xt_next;
-#pragma unroll
-            for (int i = 0; i < V; ++i) count += v[u][i] >= tq;
+            counted.add(raw[u], v[u], at >= hi ? none : at + V <= t ? ge_t : gt_t);
         }
+        count += counted.total();
         if (tile0 + kTile < hi) fetch(tile0 + kTile);  // in flight during this tile's arithmetic
         float tm = -INFINITY;
 #pragma unroll
@@ -377,67 +466,56 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LpArgs a) {
             s.e += x0 + x1;
         }
         if (k == 0) continue;
-        // first tile: everything that reaches the bound; then only what beats the k-th best
-        const float thr = first ? reached_by(sm, tm, k) : above(sm.thr);
+        // what reaches the first tile's bound; after a cut, only what beats the k-th best
+        if (first) thr = reached_by(sm, tm, k);
         if (tm >= thr) {
-            // few vectors get here: they are read again, so that this code stays small
-            unsigned hits = 0;
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) hits |= static_cast<unsigned>(vm[u] >= thr) << u;
-#pragma unroll 1
-            while (hits) {
-                const int u = __ffs(hits) - 1;
-                hits &= hits - 1;
+            for (int u = 0; u < kUnroll; ++u) {
                 const int at = tile0 + (u * kThreads + tid) * V;
-                if (at >= hi) break;
-#pragma unroll 1
-                for (int i = 0; i < V; ++i) {
-                    const float y = Elem<T>::get(x, at + i);
-                    if (y >= thr) filled = push(sm, key_of(y, at + i));
-                }
+                if (!(vm[u] >= thr) || at >= hi) continue;
+                filled = atomicAdd(&sm.nvec, 1);
+                if (filled >= kVecs) continue;
+                sm.vec[filled] = pack<T>(v[u]);
+                sm.vec_at[filled] = at;
             }
         }
         if (!first && ++since < kLook && tile0 + kTile < hi) continue;
-        // one answer for the whole block; inside, nobody pushes until all have read sm.n
-        const bool over = __syncthreads_or(filled > kKeep) || first;
-        const int n = over ? sm.n : 0;
+        // one answer for the whole block; inside, nobody adds vectors until all have read sm.nvec
+        const bool over = __syncthreads_or(filled > kKeep || (first && k > 8));
         const int group_end = min(tile0 + kTile, hi);
-        if (n > kCap) {
-            // too many: drop the candidates of the tiles since the last look and take those
-            // values again in pieces of kCap - kMaxTop, cutting after each
+        if (over && sm.nvec > kVecs) {
+            // too many: take the values of the tiles since the last look again, in pieces that
+            // fit, cutting after each
             __syncthreads();
-            if (tid == 0) {
-                int kept = 0;
-                for (int i = 0; i < kCap; ++i) {
-                    const int idx = static_cast<int>(~static_cast<uint32_t>(sm.buf[i]));
-                    if (idx < group0 || idx >= group_end) sm.buf[kept++] = sm.buf[i];
-                }
-                sm.n = kept;
-            }
-            __syncthreads();
+            if (tid == 0) sm.nvec = 0;
             cut(sm, k);
 #pragma unroll 1
             for (int p = group0; p < group_end; p += kCap - kMaxTop) {
                 const uint64_t floor = sm.n == k ? sm.best[k - 1] : 0;
                 const int end = min(p + (kCap - kMaxTop), group_end);
-                __syncthreads();
+                float mx = -INFINITY;
+                for (int i = p + tid; i < end; i += kThreads) mx = fmaxf(mx, Elem<T>::get(x, i));
+                const uint64_t bound = static_cast<uint64_t>(ord(reached_by(sm, mx, k))) << 32;
                 for (int i = p + tid; i < end; i += kThreads) {
                     const uint64_t key = key_of(Elem<T>::get(x, i), i);
-                    if (key > floor) push(sm, key);
+                    if (key >= bound && key > floor) push(sm, key);
                 }
                 __syncthreads();
                 cut(sm, k);
             }
+            group0 = group_end;
+            thr = above(sm.thr);
         } else if (over) {
-            cut(sm, k);
+            take_vectors<T>(sm, thr, k);
+            group0 = group_end;
+            thr = above(sm.thr);
         }
         first = false;
         since = filled = 0;
-        group0 = tile0 + kTile;
     }
     if (k > 0) {
         __syncthreads();
-        cut(sm, k);
+        take_vectors<T>(sm, thr, k);
     }
     s = block_sums(sm, s, count, c);
     if (tid == 0) {
