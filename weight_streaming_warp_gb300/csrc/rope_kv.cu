@@ -27,7 +27,7 @@ namespace wsw {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 4;  // tokens per CTA
+constexpr int kMaxTile = 2;  // tokens per CTA
 
 struct RopeArgs {
     const void *q, *k, *v;
@@ -100,77 +100,98 @@ __device__ __forceinline__ void store8(T *p, bool vec, const float (&x)[8]) {
     }
 }
 
+// Where pair p's (cos, sin) sits among a token's: neighbouring lanes read neighbouring places at
+// every step of their loops (a plain order is an eight-way bank conflict).
+__device__ __forceinline__ int place(int p, int half, int group) {
+    return group == 8 ? (p & 7) * (half >> 3) + (p >> 3) : group == 4 ? (p & 3) * ((half + 3) >> 2) + (p >> 2) : p;
+}
+
 template <typename T, int CT>
 __global__ void __launch_bounds__(kThreads) rope_kv_kernel(const RopeArgs a) {
-    __shared__ float2 cs[kMaxTile * 128];  // (m cos, m sin) of each token and pair
+    __shared__ float2 cs[kMaxTile][128 + 4];  // (m cos, m sin) of each token and pair
+    __shared__ int32_t pos_sm[kMaxTile];
+    __shared__ int64_t slot_sm[kMaxTile];
     const int tid = threadIdx.x;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tile;
     const int tile = static_cast<int>(a.tokens - t0 < a.tile ? a.tokens - t0 : a.tile);
     const int half = a.rot >> 1;
+    const int group = a.interleaved ? 4 : (half & 7) == 0 ? 8 : 1;
     pdl_launch_dependents();
     pdl_wait();
     for (int i = tid; i < tile * half; i += kThreads) {
-        const int tt = i / half;
+        const int tt = i / half, pair = i - tt * half;
         const int32_t p = a.positions[t0 + tt];
-        const uint64_t turn = static_cast<uint64_t>(p < 0 ? 0 : p) * a.turns[i - tt * half];
+        const uint64_t turn = static_cast<uint64_t>(p < 0 ? 0 : p) * a.turns[pair];
         // the top 32 bits as a signed fraction: half turns in [-1, 1)
         const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
         float s, c;
         sincospif(x, &s, &c);
-        cs[i] = make_float2(a.mscale * c, a.mscale * s);
+        cs[tt][place(pair, half, group)] = make_float2(a.mscale * c, a.mscale * s);
+    }
+    if (tid < tile) {
+        pos_sm[tid] = a.positions[t0 + tid];
+        slot_sm[tid] = a.slots[t0 + tid];
     }
     __syncthreads();
 
     const int lanes = 1 << a.lane_shift, D = lanes * 8;
     const int rows = a.q_heads + 2 * a.kv.heads;
-    const int units = tile * rows << a.lane_shift;
-    for (int base = blockIdx.y * kThreads; base < units; base += gridDim.y * kThreads) {
-        const int u = base + tid;
-        const bool active = u < units;  // a row's lanes are all active or all idle
-        const int row = active ? u >> a.lane_shift : 0;
-        const int tt = row / rows, h = row - tt * rows;
-        const int d0 = (u & (lanes - 1)) * 8;
-        const int64_t t = t0 + tt;
+    const int d0 = (tid & (lanes - 1)) * 8;
+    const int step = static_cast<int>(gridDim.y * kThreads) >> a.lane_shift;  // rows per round of the grid's y
+    const int step_t = step / rows, step_h = step - step_t * rows;
+    int row = static_cast<int>(blockIdx.y * kThreads + tid) >> a.lane_shift;
+    int tt = row / rows, h = row - tt * rows;
+    const int total = tile * rows;
+    const int warp_row = row - ((tid & 31) >> a.lane_shift);  // the warp's first row: a uniform loop
+    for (int base = warp_row; base < total; base += step) {
+        const bool active = tt < tile;  // a row's lanes are all active or all idle
+        const int64_t t = t0 + (active ? tt : 0);
         const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + a.kv.heads;
         const int kh = is_v ? h - a.q_heads - a.kv.heads : h - a.q_heads;
         const T *src;
         if (is_q) src = static_cast<const T *>(a.q) + t * a.qts + h * a.qhs;
         else if (is_v) src = static_cast<const T *>(a.v) + t * a.vts + kh * a.vhs;
         else src = static_cast<const T *>(a.k) + t * a.kts + kh * a.khs;
-        const int32_t pos = a.positions[t];
+        const int32_t pos = active ? pos_sm[tt] : -1;
         float x[8];
-        if (active && pos >= 0) {
+        if (pos >= 0) {
             load8(src + d0, a.vec, x);
             if (!is_v && d0 < a.rot) {
-                const float2 *w = cs + tt * half;
-                if (a.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (d0 + 2 * i >= a.rot) break;
-                        const float2 z = w[(d0 >> 1) + i];
-                        const float x0 = x[2 * i], x1 = x[2 * i + 1];
-                        x[2 * i] = x0 * z.x - x1 * z.y;
-                        x[2 * i + 1] = x1 * z.x + x0 * z.y;
-                    }
-                } else if ((half & 7) == 0) {
+                const float2 *w = cs[tt];
+                if (group == 8) {
                     const bool lo = d0 < half;
                     float y[8];
                     load8(src + (lo ? d0 + half : d0 - half), a.vec, y);
-                    w += lo ? d0 : d0 - half;
+                    w += (lo ? d0 : d0 - half) >> 3;
+                    const int stride = half >> 3;
+                    const float sign = lo ? -1.f : 1.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float2 z = w[i];
-                        x[i] = x[i] * z.x + y[i] * (lo ? -z.y : z.y);
+                        const float2 z = w[i * stride];
+                        x[i] = fmaf(x[i], z.x, y[i] * (sign * z.y));
+                    }
+                } else if (group == 4) {
+                    w += d0 >> 3;
+                    const int stride = (half + 3) >> 2;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (d0 + 2 * i >= a.rot) break;
+                        const float2 z = w[i * stride];
+                        const float x0 = x[2 * i], x1 = x[2 * i + 1];
+                        x[2 * i] = fmaf(x0, z.x, -x1 * z.y);
+                        x[2 * i + 1] = fmaf(x1, z.x, x0 * z.y);
                     }
                 } else {  // the halves do not meet at a multiple of 8: partners one by one
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
                         const int d = d0 + i;
                         if (d >= a.rot) break;
                         const bool lo = d < half;
-                        const float y = to_f(src[lo ? d + half : d - half]);
+                        const float y = to_f(src[lo ? d + half : d - half]), own = to_f(src[d]);
                         const float2 z = w[lo ? d : d - half];
-                        x[i] = x[i] * z.x + y * (lo ? -z.y : z.y);
+                        const float turned = fmaf(own, z.x, y * (lo ? -z.y : z.y));
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = j == i ? turned : x[j];
                     }
                 }
             }
@@ -180,8 +201,8 @@ __global__ void __launch_bounds__(kThreads) rope_kv_kernel(const RopeArgs a) {
         }
         __syncwarp();  // a row in place: its partners are read before it is written
         int64_t where = -1, dwhere = 0;
-        if (active && !is_q && pos >= 0) {
-            const int64_t slot = a.slots[t];
+        if (!is_q && pos >= 0) {
+            const int64_t slot = slot_sm[tt];
             const int64_t page = slot >> a.kv.page_shift;
             if (slot >= 0 && page < a.kv.num_pages) {
                 const int64_t off = slot & ((int64_t(1) << a.kv.page_shift) - 1);
@@ -207,6 +228,12 @@ __global__ void __launch_bounds__(kThreads) rope_kv_kernel(const RopeArgs a) {
             else *reinterpret_cast<uint4 *>(dst) = pack8<__nv_bfloat16>(x);
         }
         if (active && is_q) store8(static_cast<T *>(a.q_out) + (t * a.q_heads + h) * D + d0, a.vec_out, x);
+        tt += step_t;
+        h += step_h;
+        if (h >= rows) {
+            h -= rows;
+            ++tt;
+        }
     }
 }
 
@@ -304,8 +331,8 @@ extern "C" int wsw_rope_kv_write(const void *q, const void *k, const void *v, in
     a.vec = ((in | strides) & 15) == 0;
     a.vec_out = (qo & 15) == 0;
     const int64_t passes = (((q_heads + 2 * a.kv.heads) << a.lane_shift) + kThreads - 1) / kThreads;  // of one token
-    a.tile = tokens >= 2048 ? kMaxTile : 1;
-    const int64_t slabs = tokens >= 2048 ? 1 : passes;
+    a.tile = tokens >= 1024 ? kMaxTile : 1;
+    const int64_t slabs = tokens >= 1024 ? 1 : passes;
     const dim3 grid(static_cast<unsigned>((tokens + a.tile - 1) / a.tile),
                     static_cast<unsigned>(slabs < 65535 ? slabs : 65535));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
