@@ -162,7 +162,8 @@ def _opts(opts):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The current stream's handle (torch's raw accessor: a Stream object costs 3 us to make)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dev(t: torch.Tensor, dtype, name):
@@ -452,10 +453,27 @@ def _float_dev(t, name):
 
 def _packed(t, dtype, name, shape=None):
     """The address of a contiguous device tensor."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     _dev(t, dtype, name)
-    if not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
-        raise WswError("%s must be contiguous%s" % (name, "" if shape is None else " of shape %s" % (shape,)))
-    return t.data_ptr()
+    raise WswError("%s must be contiguous%s" % (name, "" if shape is None else " of shape %s" % (shape,)))
+
+
+def _table(t, n):
+    """(address, pages per row, row stride) of a block table of n requests."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda):
+        _dev(t, torch.int32, "table")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != n:
+        raise WswError("table must be [requests][max_pages]")
+    width = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), width, width
+    row, unit = t.stride()
+    if (width > 1 and unit != 1) or (n > 1 and row < width):
+        raise WswError("table must have unit stride in max_pages and rows that do not overlap")
+    return t.data_ptr(), width, max(row, width)
 
 
 class PagedKV:
@@ -509,30 +527,26 @@ def kv_page_plan(seq_len, new_len, free_pages, head, table, page_size, tokens, o
     get position and slot -1, as do the tokens of a request that does not fit (err_flag,
     an int32 device tensor, tells why: wsw.h).  Returns a KvPlan; out = such a tuple of
     tensors to fill, in which seq_len and head may be the arguments themselves."""
-    n = seq_len.shape[0]
-    _packed(seq_len, torch.int32, "seq_len")
-    _packed(new_len, torch.int32, "new_len", (n,))
-    _packed(free_pages, torch.int32, "free_pages")
-    _packed(head, torch.int32, "head", (1,))
-    _dev(table, torch.int32, "table")
-    if table.dim() != 2 or table.shape[0] != n or (table.numel() > n and table.stride(1) != 1):
-        raise WswError("table must be [requests][max_pages] with unit stride in max_pages")
+    sp = _packed(seq_len, torch.int32, "seq_len")
+    n = seq_len.numel()
+    tp, width, row = _table(table, n)
     if out is None:
         dev = seq_len.device
         out = KvPlan(torch.empty(tokens, dtype=torch.int32, device=dev),
                      torch.empty(tokens, dtype=torch.int64, device=dev),
                      torch.empty(n + 1, dtype=torch.int32, device=dev), torch.empty_like(seq_len),
                      torch.empty_like(head))
-    else:
+    elif type(out) is not KvPlan:
         out = KvPlan(*out)
-    err = _packed(err_flag, torch.int32, "err_flag") if err_flag is not None else None
+    positions, slots, cu, lens, head_out = out
     _check(load().wsw_kv_page_plan(
-        seq_len.data_ptr(), new_len.data_ptr(), n, free_pages.data_ptr(), free_pages.shape[0], head.data_ptr(),
-        page_size, table.data_ptr(), table.shape[1], max(table.stride(0), table.shape[1]) if n > 1 else table.shape[1],
-        tokens, _packed(out.positions, torch.int32, "positions", (tokens,)),
-        _packed(out.slots, torch.int64, "slots", (tokens,)), _packed(out.cu, torch.int32, "cu", (n + 1,)),
-        _packed(out.seq_len, torch.int32, "seq_len (out)", (n,)), _packed(out.head, torch.int32, "head (out)", (1,)),
-        err, _stream(), _opts(opts)), "kv_page_plan")
+        sp, _packed(new_len, torch.int32, "new_len", (n,)), n, _packed(free_pages, torch.int32, "free_pages"),
+        free_pages.numel(), _packed(head, torch.int32, "head", (1,)), page_size, tp, width, row, tokens,
+        _packed(positions, torch.int32, "positions", (tokens,)), _packed(slots, torch.int64, "slots", (tokens,)),
+        _packed(cu, torch.int32, "cu", (n + 1,)), _packed(lens, torch.int32, "seq_len (out)", (n,)),
+        _packed(head_out, torch.int32, "head (out)", (1,)),
+        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag"), _stream(), _opts(opts)),
+        "kv_page_plan")
     return out
 
 
@@ -565,11 +579,16 @@ def rope_table(rot_dim, theta=10000.0, scaling=None, factor=1.0, original=0, fre
     return RopeTable(t.to(device), mscale.value, rot_dim)
 
 
-def _rows3(t, name, tokens, heads, hd):
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != hd or (heads is not None and t.shape[1] != heads) or (
-            t.stride(2) != 1 and hd > 1):
-        raise WswError("%s must be a [tokens][heads][head_dim] view with unit stride in head_dim" % name)
-    return t.data_ptr(), t.stride(0), t.stride(1)
+def _rows3(t, dtype, name, shape):
+    """(address, token stride, head stride) of a [tokens][heads][head_dim] view."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda):
+        _dev(t, dtype, name)
+    if t.shape != shape:
+        raise WswError("%s must have shape %s" % (name, shape))
+    tok, head, unit = t.stride()
+    if unit != 1:
+        raise WswError("%s must have unit stride in head_dim" % name)
+    return t.data_ptr(), tok, head
 
 
 def rope_kv_write(q, k, v, rope, positions, slots, kv, interleaved=False, out=None, err_flag=None, opts=None):
@@ -580,22 +599,23 @@ def rope_kv_write(q, k, v, rope, positions, slots, kv, interleaved=False, out=No
     RopeTable; positions int32 and slots int64 [tokens], as kv_page_plan gives them.
     interleaved: pairs (2 i, 2 i + 1) instead of (i, i + rot_dim / 2)."""
     code = _float_dev(q, "q")
-    _dev(k, q.dtype, "k")
-    _dev(v, q.dtype, "v")
-    n, heads, hd = q.shape
+    if q.dim() != 3:
+        raise WswError("q must be a [tokens][q_heads][head_dim] view")
+    dtype, shape = q.dtype, q.shape
+    n, heads, hd = shape
     if hd != kv.head_dim:
         raise WswError("q must have the cache's head_dim")
-    qp, qt, qh = _rows3(q, "q", n, None, hd)
-    kp, kt, kh = _rows3(k, "k", n, kv.heads, hd)
-    vp, vt, vh = _rows3(v, "v", n, kv.heads, hd)
+    qp, qt, qh = _rows3(q, dtype, "q", shape)
+    kp, kt, kh = _rows3(k, dtype, "k", (n, kv.heads, hd))
+    vp, vt, vh = _rows3(v, dtype, "v", (n, kv.heads, hd))
     if out is None:
-        out = torch.empty((n, heads, hd), dtype=q.dtype, device=q.device)
-    err = _packed(err_flag, torch.int32, "err_flag") if err_flag is not None else None
+        out = torch.empty((n, heads, hd), dtype=dtype, device=q.device)
     _check(load().wsw_rope_kv_write(
         qp, kp, vp, code, n, heads, qt, qh, kt, kh, vt, vh, rope.turns.data_ptr(), rope.rot_dim, rope.mscale,
-        int(bool(interleaved)), _packed(positions, torch.int32, "positions", (n,)),
-        _packed(slots, torch.int64, "slots", (n,)), _packed(out, q.dtype, "out", (n, heads, hd)), kv._ref, err,
-        _stream(), _opts(opts)), "rope_kv_write")
+        1 if interleaved else 0, _packed(positions, torch.int32, "positions", (n,)),
+        _packed(slots, torch.int64, "slots", (n,)), _packed(out, dtype, "out", shape), kv._ref,
+        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag"), _stream(), _opts(opts)),
+        "rope_kv_write")
     return out
 
 
@@ -618,12 +638,11 @@ def attn_paged_decode(q, kv, table, lens, scale=None, softcap=0.0, window=0, slo
     code = _float_dev(q, "q")
     if q.dim() != 3 or not q.is_contiguous():
         raise WswError("q must be a contiguous [requests][q_heads][head_dim] tensor")
-    n, heads, hd = q.shape
+    shape = q.shape
+    n, heads, hd = shape
     if hd != kv.head_dim or heads % kv.heads != 0:
         raise WswError("q must have the cache's head_dim and a multiple of its heads")
-    _dev(table, torch.int32, "table")
-    if table.dim() != 2 or table.shape[0] != n or (table.numel() > n and table.stride(1) != 1):
-        raise WswError("table must be [requests][max_pages] with unit stride in max_pages")
+    tp, width, row = _table(table, n)
     if scale is None:
         scale = 1.0 / float(hd) ** 0.5
     if out is None:
@@ -632,13 +651,12 @@ def attn_paged_decode(q, kv, table, lens, scale=None, softcap=0.0, window=0, slo
         ws = torch.zeros(attn_paged_decode_workspace_bytes(n, heads, kv.heads, hd), dtype=torch.uint8,
                          device=q.device)
     _check(load().wsw_attn_paged_decode(
-        q.data_ptr(), code, n, heads, kv._ref, table.data_ptr(), table.shape[1],
-        max(table.stride(0), table.shape[1]) if n > 1 else table.shape[1], _packed(lens, torch.int32, "lens", (n,)),
-        scale, softcap, window, _packed(slopes, torch.float32, "slopes", (heads,)) if slopes is not None else None,
-        _packed(out, q.dtype, "out", (n, heads, hd)),
-        _packed(lse, torch.float32, "lse", (n, heads)) if lse is not None else None,
-        _packed(err_flag, torch.int32, "err_flag") if err_flag is not None else None, ws.data_ptr(), ws.numel(),
-        _stream(), _opts(opts)), "attn_paged_decode")
+        q.data_ptr(), code, n, heads, kv._ref, tp, width, row, _packed(lens, torch.int32, "lens", (n,)), scale, softcap,
+        window, None if slopes is None else _packed(slopes, torch.float32, "slopes", (heads,)),
+        _packed(out, q.dtype, "out", shape),
+        None if lse is None else _packed(lse, torch.float32, "lse", (n, heads)),
+        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag"),
+        _packed(ws, torch.uint8, "ws"), ws.numel(), _stream(), _opts(opts)), "attn_paged_decode")
     return out
 
 
@@ -675,21 +693,25 @@ def token_logprobs(logits, tokens=None, top=0, scale=1.0, out=None, ws=None, opt
     rows, vocab, ld = _rowmajor(logits, "logits")
     if out is None:
         out = token_logprobs_out(rows, top, tokens is not None, logits.device)
-    need = token_logprobs_workspace_bytes(rows, vocab, top)
-    if ws is None and need:
-        ws = torch.zeros(need, dtype=torch.uint8, device=logits.device)
-    tp = lp = rp = None
+    logprob, rank, lse, entropy, top_logprob, top_id = out
+    tp = lp = rp = bp = ip = wp = None
     if tokens is not None:
         tp = _packed(tokens, torch.int32, "tokens", (rows,))
-        lp = _packed(out.logprob, torch.float32, "logprob", (rows,))
-        rp = _packed(out.rank, torch.int32, "rank", (rows,))
+        lp = _packed(logprob, torch.float32, "logprob", (rows,))
+        rp = _packed(rank, torch.int32, "rank", (rows,))
+    if top:
+        bp = _packed(top_logprob, torch.float32, "top_logprob", (rows, top))
+        ip = _packed(top_id, torch.int32, "top_id", (rows, top))
+    if ws is None:
+        need = token_logprobs_workspace_bytes(rows, vocab, top)
+        if need:
+            ws = torch.zeros(need, dtype=torch.uint8, device=logits.device)
+    if ws is not None:
+        wp = _packed(ws, torch.uint8, "ws")
     _check(load().wsw_token_logprobs(
-        logits.data_ptr(), code, rows, vocab, ld, tp, scale, top, lp, rp, _packed(out.lse, torch.float32, "lse", (rows,)),
-        _packed(out.entropy, torch.float32, "entropy", (rows,)),
-        _packed(out.top_logprob, torch.float32, "top_logprob", (rows, top)) if top else None,
-        _packed(out.top_id, torch.int32, "top_id", (rows, top)) if top else None,
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, _stream(), _opts(opts)),
-        "token_logprobs")
+        logits.data_ptr(), code, rows, vocab, ld, tp, scale, top, lp, rp, _packed(lse, torch.float32, "lse", (rows,)),
+        _packed(entropy, torch.float32, "entropy", (rows,)), bp, ip, wp, 0 if wp is None else ws.numel(), _stream(),
+        _opts(opts)), "token_logprobs")
     return out
 
 
