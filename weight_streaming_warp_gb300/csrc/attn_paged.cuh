@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     __shared__ int64_t run_off[W];     // of each warp's first tile in its request
     __shared__ int run_req[W];
     __shared__ Piece pieces[2 * W];
+    __shared__ float2 piece_ml[2 * W][RT];  // (m, l) of each piece's rows
     __shared__ uint32_t seen_mask[W][C::stages];
     __shared__ int last[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -307,41 +308,75 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         Cursor ic = uc;  // the next tile to copy
         const int page_mask = (1 << a.kv.page_shift) - 1;
 
-        // lane i < 16 holds the page of position i of the next tile to copy, loaded a step ahead
-        int next_page = -1, next_pos = 0;
+        // The request's page numbers from wbase on, 64 of them over the lanes, loaded well before
+        // their copies: a table read on the way to each copy would double its latency.
+        int wreq = -1, wbase = 0, win0 = -1, win1 = -1;
+        auto entries = [&](int i) {  // page numbers i + lane
+            i += lane;
+            return i <= (ic.len - 1) >> a.kv.page_shift ? a.table[ic.r * a.table_stride + i] : -1;
+        };
         auto look_up = [&]() {
-            const int p = ic.start + ic.t * kTile + (lane & 15);
-            next_pos = p;
-            next_page = p < ic.len ? a.table[ic.r * a.table_stride + (p >> a.kv.page_shift)] : -1;
+            const int i0 = (ic.start + ic.t * kTile) >> a.kv.page_shift;
+            if (ic.r != wreq || i0 < wbase || i0 >= wbase + 64) {
+                wreq = ic.r;
+                wbase = i0;
+                win0 = entries(wbase);
+                win1 = entries(wbase + 32);
+            } else if (i0 >= wbase + 32) {
+                wbase += 32;
+                win0 = win1;
+                win1 = entries(wbase + 32);
+            }
         };
         look_up();
         int ist = 0;
         auto issue = [&]() {
             if (to_issue > 0) {
                 --to_issue;
-                const bool in = next_pos < ic.len;
-                const bool ok = in && static_cast<unsigned>(next_page) < static_cast<unsigned>(a.kv.num_pages);
+                const int p0 = ic.start + ic.t * kTile, p = p0 + (lane & 15);
+                const int rel = (p >> a.kv.page_shift) - wbase;
+                const int pg0 = __shfl_sync(WSW_FULL_MASK, win0, rel & 31), pg1 = __shfl_sync(WSW_FULL_MASK, win1, rel & 31);
+                const int page = rel < 32 ? pg0 : pg1;
+                const bool in = p < ic.len;
+                const bool ok = in && static_cast<unsigned>(page) < static_cast<unsigned>(a.kv.num_pages);
                 const uint32_t valid = __ballot_sync(WSW_FULL_MASK, ok) & 0xffffu;
                 if (in && !ok && a.err) atomicOr(a.err, 1);
-                const int64_t page = ok ? next_page : 0, off = ok ? next_pos & page_mask : 0;
-                const int64_t at = page * a.kv.page_stride + off * a.kv.pos_stride;
-                const int h = ic.hp / a.passes;
+                const int64_t at = ok ? page * a.kv.page_stride + (p & page_mask) * a.kv.pos_stride : 0;
+                const int h = a.passes == 1 ? ic.hp : ic.hp / a.passes;
                 const unsigned char *kb = a.kv.k + h * a.kv.head_stride, *vb = a.kv.v + h * a.kv.head_stride;
                 const uint32_t stg = ring_s + ist * C::stage;
                 constexpr int kRows = 32 / C::pieces;  // rows per round of the warp
                 const int c = lane % C::pieces, rr = lane / C::pieces;
-#pragma unroll
-                for (int i = 0; i < kTile / kRows; ++i) {
-                    const int row = i * kRows + rr;
-                    const int64_t o = __shfl_sync(WSW_FULL_MASK, at, row);
-                    const bool v = (valid >> row) & 1;
+                auto swizzled = [&](int row) {
                     const int sw = C::pieces >= 8 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
-                    const uint32_t dst = stg + row * C::row_bytes + sw * 16;
-                    cp16(dst, kb + o + c * 16, v);
-                    cp16(dst + C::kv_bytes, vb + o + c * 16, v);
+                    return stg + row * C::row_bytes + sw * 16;
+                };
+                if (valid == 0xffffu && (p0 & page_mask) + kTile - 1 <= page_mask) {
+                    // the whole tile in one page: its rows are pos_stride apart
+                    const int64_t o = __shfl_sync(WSW_FULL_MASK, at, 0) + rr * a.kv.pos_stride + c * 16;
+                    const unsigned char *kp = kb + o, *vp = vb + o;
+#pragma unroll
+                    for (int i = 0; i < kTile / kRows; ++i) {
+                        const uint32_t dst = swizzled(i * kRows + rr);
+                        cp16(dst, kp, true);
+                        cp16(dst + C::kv_bytes, vp, true);
+                        kp += kRows * a.kv.pos_stride;
+                        vp += kRows * a.kv.pos_stride;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kTile / kRows; ++i) {
+                        const int row = i * kRows + rr;
+                        const int64_t o = __shfl_sync(WSW_FULL_MASK, at, row);
+                        const bool v = (valid >> row) & 1;
+                        const uint32_t dst = swizzled(row);
+                        cp16(dst, kb + o + c * 16, v);
+                        cp16(dst + C::kv_bytes, vb + o + c * 16, v);
+                    }
                 }
                 if constexpr (C::q8) {  // lanes 0..15: K scales, 16..31: V scales
-                    const int64_t dat = page * a.kv.d_page_stride + off * a.kv.d_pos_stride + h * a.kv.d_head_stride;
+                    const int64_t dat = ok ? page * a.kv.d_page_stride + (p & page_mask) * a.kv.d_pos_stride +
+                                                 h * a.kv.d_head_stride : 0;
                     cp_small<C::scale_bytes>(stg + 2 * C::kv_bytes + lane * C::scale_bytes,
                                              (lane < 16 ? a.kv.kd : a.kv.vd) + dat, ok);
                 }
@@ -461,6 +496,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 
             // ---- scores of 16 positions, two blocks of 8
             float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            float sd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // the odd steps: a second chain
             auto score = [&](int kt, const uint32_t (&kb)[4]) {  // kb: block 0's two registers, block 1's
                 uint32_t qf[4];
                 if constexpr (C::q_smem) {
@@ -470,14 +506,15 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 #pragma unroll
                     for (int i = 0; i < 4; ++i) qf[i] = qa[kt][i];
                 }
-                mma<CT>(sc[0], qf, kb[0], kb[1]);
-                mma<CT>(sc[1], qf, kb[2], kb[3]);
+                float (&s0)[4] = kt & 1 ? sd[0] : sc[0], (&s1)[4] = kt & 1 ? sd[1] : sc[1];
+                mma<CT>(s0, qf, kb[0], kb[1]);
+                mma<CT>(s1, qf, kb[2], kb[3]);
                 if constexpr (RT == 16) {
                     if (q_lo) {
                         const uint4 u = q_lo_sm[kt * 32 + lane];
                         const uint32_t ql[4] = {u.x, u.y, u.z, u.w};
-                        mma<CT>(sc[0], ql, kb[0], kb[1]);
-                        mma<CT>(sc[1], ql, kb[2], kb[3]);
+                        mma<CT>(s0, ql, kb[0], kb[1]);
+                        mma<CT>(s1, ql, kb[2], kb[3]);
                     }
                 }
             };
@@ -522,6 +559,12 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                                             dequant2(w[1][kt], 0x4140, ds[1][bl]), dequant2(w[1][kt], 0x4342, ds[1][bl])};
                     score(kt, kb);
                 }
+            }
+
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sc[0][i] += sd[0][i];
+                sc[1][i] += sd[1][i];
             }
 
             // ---- softmax: lane (gq, tq) holds positions 8 n + 2 tq + {0, 1} of rows gq, gq + 8
@@ -654,12 +697,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 auto val = [&](int n, int x) { return RT == 8 ? o[n][x] + o[n][2 + x] : o[n][2 * y + x]; };
                 float *rr = whole ? nullptr : rec + row * C::rec;
                 if (tq == 0) {
-                    if (whole) {
-                        if (a.lse) a.lse[head] = lse_of(m[y], l[y]);
-                    } else {
-                        rr[0] = m[y];
-                        rr[1] = l[y];
-                    }
+                    if (!whole) piece_ml[2 * warp + (todo == 1)][row] = make_float2(m[y], l[y]);
+                    else if (a.lse) a.lse[head] = lse_of(m[y], l[y]);
                 }
                 if constexpr (!C::q8) {
 #pragma unroll
@@ -696,56 +735,52 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     float *joined = wgt + 2 * W * RT;
     int nshared = 0;
     Piece shared_a, shared_b;
-    for (int i = 0; i < 2 * W;) {
+    // a lane for each piece: the pieces of a pair are neighbours
+    const bool have = lane < 2 * W && pieces[lane < 2 * W ? lane : 0].r >= 0;
+    const int64_t key = have ? pieces[lane].pstart : -1;
+    uint32_t left = __ballot_sync(WSW_FULL_MASK, have);
+    while (left) {
+        const int i = __ffs(left) - 1;
+        const uint32_t set = left & __ballot_sync(WSW_FULL_MASK, key == __shfl_sync(WSW_FULL_MASK, key, i));
+        left &= ~set;
         const Piece pc = pieces[i];
-        if (pc.r < 0) {
-            ++i;
-            continue;
-        }
-        int j = i + 1;
-        while (j < 2 * W && (pieces[j].r < 0 || (pieces[j].r == pc.r && pieces[j].hp == pc.hp))) ++j;
         const bool complete = pc.pstart >= b && pc.pstart + pc.nt <= e;
         const int h = pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
         const int rows = min(RT, a.group - g0);
-        auto record = [&](int k) -> const float * {
-            return k & 1 ? reinterpret_cast<const float *>(smem + (k >> 1) * C::ring)
-                         : a.wrec + static_cast<int64_t>(cta * W + (k >> 1)) * RT * C::rec;
-        };
-        if (tid < 32) {  // lane: row (of 16) and one of two interleaved runs of the records
-            const int row = lane & 15;
+        if (tid < rows) {
+            float2 ml[2 * W];
             float mx = -INFINITY, l = 0.f;
-            if (row < rows)
-                for (int k = i + (lane >> 4); k < j; k += 2)
-                    if (pieces[k].r >= 0) mx = fmaxf(mx, record(k)[row * C::rec]);
-            mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, 16));
-            if (row < rows)
-                for (int k = i + (lane >> 4); k < j; k += 2) {
-                    if (pieces[k].r < 0) continue;
-                    const float *r = record(k) + row * C::rec;
-                    const float f = weight(r[0], mx);
-                    wgt[k * RT + row] = f;
-                    l = fmaf(r[1], f, l);
-                }
-            l += __shfl_xor_sync(WSW_FULL_MASK, l, 16);
-            if (lane < rows) {
-                joined[row] = mx;
-                joined[RT + row] = l;
+#pragma unroll
+            for (int k = 0; k < 2 * W; ++k) {
+                ml[k] = (set >> k) & 1 ? piece_ml[k][tid] : make_float2(-INFINITY, 0.f);
+                mx = fmaxf(mx, ml[k].x);
             }
+#pragma unroll
+            for (int k = 0; k < 2 * W; ++k) {
+                const float f = weight(ml[k].x, mx);
+                wgt[k * RT + tid] = f;
+                l = fmaf(ml[k].y, f, l);
+            }
+            joined[tid] = mx;
+            joined[RT + tid] = l;
         }
         __syncthreads();
         float *dst = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec;
         for (int u = tid; u < rows * kCols; u += NT) {
             const int row = u / kCols, c4 = u - row * kCols;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = i; k < j; ++k) {
-                if (pieces[k].r < 0) continue;
+            auto add = [&](int k, const float *r) {
                 const float f = wgt[k * RT + row];
-                const float4 x = *reinterpret_cast<const float4 *>(record(k) + row * C::rec + 4 + 4 * c4);
+                const float4 x = *reinterpret_cast<const float4 *>(r + row * C::rec + 4 + 4 * c4);
                 s.x = fmaf(x.x, f, s.x);
                 s.y = fmaf(x.y, f, s.y);
                 s.z = fmaf(x.z, f, s.z);
                 s.w = fmaf(x.w, f, s.w);
+            };
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if ((set >> (2 * w)) & 1) add(2 * w, a.wrec + static_cast<int64_t>(cta * W + w) * RT * C::rec);
+                if ((set >> (2 * w + 1)) & 1) add(2 * w + 1, reinterpret_cast<const float *>(smem + w * C::ring));
             }
             const float mx = joined[row], l = joined[RT + row];
             if (complete) {
@@ -765,7 +800,6 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             ++nshared;
         }
         __syncthreads();  // the weights' place is free again
-        i = j;
     }
     if (nshared == 0) return;
 
@@ -794,6 +828,23 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         float *w = reinterpret_cast<float *>(smem);             // [n][RT] maxima, then weights
         float *lw = w + kCtas * RT;                             // [n][RT] sums
         float *part = lw + kCtas * RT;                          // [slices][rows][D]
+        // the records are dealt to slices of the block, whose sums are then added in order; the
+        // first ones are on their way while the weights are made
+        const int units = rows * kCols;
+        const int slices = NT / units > 1 ? NT / units : 1;
+        constexpr int kAhead = 16;
+        float4 xa[kAhead];
+        {
+            const int sl = tid / units, v = tid - sl * units;
+            const float *r0 = record(0) + v / kCols * C::rec + 4 + 4 * (v % kCols);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int k = sl + i * slices;
+                xa[i] = sl < slices && k < n
+                            ? __ldcg(reinterpret_cast<const float4 *>(r0 + (record(k) - record(0))))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
         for (int u = tid; u < n * RT; u += NT) {
             const int k = u / RT, row = u - k * RT;
             if (row >= rows) continue;
@@ -822,22 +873,27 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             }
         }
         __syncthreads();
-        // the records are dealt to slices of the block, whose sums are then added in order
-        const int units = rows * kCols;
-        const int slices = NT / units > 1 ? NT / units : 1;
         for (int u = tid; u < slices * units; u += NT) {
             const int sl = u / units, v = u - sl * units;
             const int row = v / kCols, c4 = v - row * kCols;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 16
-            for (int k = sl; k < n; k += slices) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(record(k) + row * C::rec + 4 + 4 * c4));
+            auto add = [&](int k, float4 x) {
                 const float g = w[k * RT + row];
                 s.x = fmaf(x.x, g, s.x);
                 s.y = fmaf(x.y, g, s.y);
                 s.z = fmaf(x.z, g, s.z);
                 s.w = fmaf(x.w, g, s.w);
+            };
+            int k = sl;
+            if (u == tid) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (sl + i * slices < n) add(sl + i * slices, xa[i]);
+                k += kAhead * slices;
             }
+#pragma unroll 8
+            for (; k < n; k += slices)
+                add(k, __ldcg(reinterpret_cast<const float4 *>(record(k) + row * C::rec + 4 + 4 * c4)));
             *reinterpret_cast<float4 *>(part + u * 4) = s;
         }
         __syncthreads();
