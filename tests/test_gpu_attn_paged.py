@@ -236,7 +236,7 @@ def test_options_repeats_streams_and_graphs_change_no_bit():
         b, lb = c.run(ws=ws, opts=opts)
         assert torch.equal(a, b) and torch.equal(la, lb)
     torch.cuda.synchronize()
-    assert int(ws[:1024].view(torch.int32).abs().sum()) == 0, "counters left nonzero"
+    assert int(ws[:2048].view(torch.int32).abs().sum()) == 0, "counters left nonzero"
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):

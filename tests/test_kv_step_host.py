@@ -84,9 +84,9 @@ def test_attention_refusals(lib):
     assert _attn(lib, n=0, q=None) == 0
     wb = lib.wsw_attn_paged_decode_workspace_bytes
     # counters, and 132 floats per query row for two records of each of 152 CTAs and one of each warp
-    assert wb(1, 32, 4, 128) == 1024 + 152 * 10 * 8 * 132 * 4
-    assert wb(64, 40, 4, 128) == 1024 + 152 * 10 * 16 * 132 * 4
-    assert wb(64, 40, 4, 256) == 1024 + 152 * 6 * 16 * 260 * 4
+    assert wb(1, 32, 4, 128) == 2048 + 152 * 14 * 8 * 132 * 4
+    assert wb(64, 40, 4, 128) == 2048 + 152 * 14 * 16 * 132 * 4
+    assert wb(64, 40, 4, 256) == 2048 + 152 * 6 * 16 * 260 * 4
     assert wb(1, 30, 4, 128) == 0 and wb(1, 32, 4, 96) == 0
 
 

@@ -6,15 +6,16 @@
 namespace wsw {
 namespace paged {
 
-template <> cudaError_t launch_type<WSW_F16>(const Args &, int, cudaStream_t, bool, int);
-template <> cudaError_t launch_type<WSW_BF16>(const Args &, int, cudaStream_t, bool, int);
-template <> cudaError_t launch_type<WSW_Q8_0>(const Args &, int, cudaStream_t, bool, int);
+template <> cudaError_t launch_type<WSW_F16>(const Args &, int, cudaStream_t, bool, int64_t);
+template <> cudaError_t launch_type<WSW_BF16>(const Args &, int, cudaStream_t, bool, int64_t);
+template <> cudaError_t launch_type<WSW_Q8_0>(const Args &, int, cudaStream_t, bool, int64_t);
 
 namespace {
-constexpr size_t kCounterBytes = 1024;  // kCtas counters, padded
+constexpr size_t kCounterBytes = 2048;
+static_assert(3 * kCtas * 4 <= kCounterBytes, "counters");
 // groups of up to 8 query heads keep their residuals in the other 8 rows of a 16-row tile
 int rows_of(int64_t group) { return group <= 8 ? 8 : 16; }
-int warps_of(int64_t head_dim) { return head_dim == 256 ? 4 : 8; }
+int warps_of(int64_t head_dim) { return head_dim == 256 ? 4 : 12; }  // at most
 size_t record_bytes(int rows, int64_t head_dim) { return static_cast<size_t>(rows) * (head_dim + 4) * 4; }
 }  // namespace
 }  // namespace paged
@@ -85,16 +86,13 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
     a.cnt = reinterpret_cast<unsigned *>(w);
     a.rec = reinterpret_cast<float *>(w + kCounterBytes);
     a.wrec = a.rec + static_cast<size_t>(kCtas) * 2 * record_bytes(rows, cache->head_dim) / 4;
-    // no more CTAs than the longest possible lists fill
+    // tiles of the longest possible lists
     const int64_t seen = a.max_len < a.window ? a.max_len : a.window;
     const int64_t tiles = requests * cache->heads * a.passes * ((seen + kTile - 1) / kTile);
-    const int64_t warps = warps_of(cache->head_dim);
-    int64_t ctas = (tiles + warps - 1) / warps;
-    ctas = ctas < 1 ? 1 : ctas > kCtas ? kCtas : ctas;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (cache->dtype == WSW_F16) e = launch_type<WSW_F16>(a, rows, s, o.pdl, static_cast<int>(ctas));
-    else if (cache->dtype == WSW_BF16) e = launch_type<WSW_BF16>(a, rows, s, o.pdl, static_cast<int>(ctas));
-    else e = launch_type<WSW_Q8_0>(a, rows, s, o.pdl, static_cast<int>(ctas));
+    if (cache->dtype == WSW_F16) e = launch_type<WSW_F16>(a, rows, s, o.pdl, tiles);
+    else if (cache->dtype == WSW_BF16) e = launch_type<WSW_BF16>(a, rows, s, o.pdl, tiles);
+    else e = launch_type<WSW_Q8_0>(a, rows, s, o.pdl, tiles);
     return e == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
 }

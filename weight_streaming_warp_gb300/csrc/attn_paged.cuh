@@ -9,14 +9,18 @@
 //  * One list of tiles.  A tile is 16 positions of one pair (request, KV head); the tiles of
 //    all pairs, in order, are cut into equal runs for 152 CTAs and those into equal runs for
 //    their warps.  Nothing is launched per request and no SM waits for a long one; lengths are
-//    read on the device, each CTA scanning them once.
+//    read on the device, each CTA scanning them once.  A cut that falls into a pair of at most
+//    kWhole tiles moves to the nearer end of it: sharing a pair between CTAs costs 4 us at its
+//    end, as much as so many tiles.
 //  * Each warp streams its run through a private ring of shared-memory stages with cp.async,
 //    across pair boundaries without a drain, and keeps its own softmax (running maximum, sum,
 //    value sums) in registers: no block barrier until its run ends.
 //  * A pair that lies in one warp's run is written by that warp.  Otherwise the warps leave
-//    (m, l, sums) records, the CTA joins its own, and when a pair spans CTAs the last of them to
-//    arrive (a counter in the workspace) joins theirs, in tile order, so that results do not
-//    depend on timing.  A CTA has at most two pairs that it shares with others.
+//    (m, l, sums) records, the CTA joins its own, and when a pair spans CTAs the last of each
+//    group of kGroup CTAs to arrive (a counter in the workspace) joins the group's records, and
+//    the last group's CTA the groups', always in tile order, so that results do not depend on
+//    timing.  (One CTA joining 38 records of eight rows took 7 us, 147 records 15 us: 42 bytes
+//    a nanosecond of one SM's loads.)  A CTA has at most two pairs that it shares with others.
 //
 // Products on m16n8k16 tensor-core tiles with fp32 sums.  Up to eight query heads of a KV head
 // share a 16-row operand as high parts (rows 0..7) and residuals (8..15) of q and of the
@@ -35,6 +39,8 @@ namespace wsw {
 namespace paged {
 
 constexpr int kTile = 16;      // positions per tile
+constexpr int kWhole = 32;     // pairs of up to so many tiles stay in one CTA
+constexpr int kGroup = 8;      // CTAs whose records are joined first
 constexpr int kCtas = 152;     // runs of the tile list: one CTA per SM of a 152-SM part
 constexpr float kShift = 8.f;  // log2 of the weights' scale
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -47,7 +53,9 @@ struct Args {
     const float *slopes;
     const int32_t *table, *lens;
     int32_t *err;
-    unsigned *cnt;  // [kCtas] arrival counters (zero between calls), by a pair's first CTA
+    // arrival counters, zero between calls: [kCtas][2] of a pair within a group of CTAs, by its
+    // record there, then [kCtas] of a pair's groups, by its first CTA
+    unsigned *cnt;
     float *rec;     // [kCtas][2][rows][D + 4] what a CTA leaves of its shared pairs
     float *wrec;    // [kCtas][warps][rows][D + 4] what a warp leaves of its first pair
     KvView kv;
@@ -64,7 +72,7 @@ struct Args {
 template <int CT, int D, int RT>
 struct Cfg {
     static constexpr bool q8 = CT == WSW_Q8_0;
-    static constexpr int warps = D == 256 ? 4 : 8;
+    static constexpr int warps = D == 256 ? 4 : q8 && RT == 8 ? 12 : 8;
     static constexpr int threads = warps * 32;
     static constexpr int row_bytes = q8 ? D : 2 * D;
     static constexpr int pieces = row_bytes / 16;      // 16-byte pieces of a row
@@ -79,11 +87,11 @@ struct Cfg {
     static constexpr int stages = fit < 6 ? fit : 6;
     static constexpr int ring = stages * stage;
     // the joins at the end keep weights where q was, or behind the rings
-    static constexpr int smem = warps * (ring + q_bytes) + (q_bytes == 0 ? 2048 : 0);
+    static constexpr int smem = warps * (ring + q_bytes) + (q_bytes == 0 ? 4096 : 0);
     static constexpr int rec = D + 4;                   // floats: m, l, 2 pad, sums
     static_assert(stages >= 2 && RT * rec * 4 <= ring && ring % 16 == 0, "ring");
-    static_assert((2 * warps + 2) * RT * 4 <= 2048 && smem <= kSmemMax + 1024, "joins");
-    static_assert(2 * kCtas * RT * 4 + (threads > RT * D / 4 ? threads : RT * D / 4) * 16 <= warps * ring, "joins");
+    static_assert(2 * warps <= 32 && 3 * 2 * warps * RT * 4 <= 4096 && smem <= kSmemMax + 3072, "joins");
+    static_assert(2 * 19 * RT * 4 + (threads > RT * D / 4 ? threads : RT * D / 4) * 16 <= warps * ring, "joins");
 };
 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -262,23 +270,40 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    const int64_t run = max((total + kCtas - 1) / kCtas, static_cast<int64_t>(W));  // tiles per CTA
-    const int64_t b = min(cta * run, total), e = min(b + run, total);
-    const int64_t n_cta = e - b;
-    for (int w = 0; w < W; ++w) {
-        const int64_t s = b + n_cta * w / W;
-        if (s < before || s >= before + mine) continue;
+    const int64_t run = max(total < 0x7fffffff ? static_cast<int64_t>((static_cast<uint32_t>(total) + kCtas - 1) / kCtas)
+                                               : (total + kCtas - 1) / kCtas,
+                            static_cast<int64_t>(W));  // tiles per CTA
+    // the request that holds tile s, for the thread whose requests do
+    auto locate = [&](int64_t s, int &req, int64_t &off) {
+        if (s < before || s >= before + mine) return;
         int64_t at = before;
+#pragma unroll 1
         for (int r = r0; r < r1; ++r) {
             const int64_t n = static_cast<int64_t>(tiles_of(a, clipped_len(a, r))) * HP;
             if (s < at + n) {
-                run_req[w] = r;
-                run_off[w] = s - at;
-                break;
+                req = r;
+                off = s - at;
+                return;
             }
             at += n;
         }
-    }
+    };
+    const int64_t raw_b = min(cta * run, total), raw_e = min(raw_b + run, total);
+    locate(raw_b, run_req[0], run_off[0]);
+    locate(raw_e, run_req[1], run_off[1]);
+    __syncthreads();
+    auto snapped = [&](int64_t s, int i) -> int64_t {
+        if (s >= total || s == 0) return s;
+        const int nt = tiles_of(a, clipped_len(a, run_req[i]));
+        if (nt > kWhole) return s;
+        const int t = run_off[i] < 0x7fffffff ? static_cast<int>(run_off[i]) % nt : static_cast<int>(run_off[i] % nt);
+        return s - t + (2 * t > nt ? nt : 0);
+    };
+    const int64_t b = snapped(raw_b, 0), e = snapped(raw_e, 1);
+    const int64_t n_cta = e - b;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < W; ++w) locate(b + n_cta * w / W, run_req[w], run_off[w]);
     // requests that see nothing
     for (int r = cta; r < a.requests; r += gridDim.x) {
         if (a.lens[r] > 0 && a.max_len > 0) continue;
@@ -385,6 +410,15 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 if (to_issue > 0) {
                     advance(a, ic);
                     look_up();
+                    if (ic.t == 0) {  // a new pair: its queries on their way to L1
+                        const int hn = a.passes == 1 ? ic.hp : ic.hp / a.passes, gn = (ic.hp - hn * a.passes) * RT;
+                        const int esize = a.dtype == WSW_F32 ? 4 : 2;
+                        const int bytes = min(RT, a.group - gn) * D * esize;
+                        const unsigned char *qp = static_cast<const unsigned char *>(a.q) +
+                            ((static_cast<int64_t>(ic.r) * a.q_heads + hn * a.group + gn) * D) * esize;
+                        for (int i = lane * 128; i < bytes; i += 32 * 128)
+                            asm volatile("prefetch.global.L1 [%0];" ::"l"(qp + i));
+                    }
                 }
             }
             cp_commit();  // one group per step, empty past the end
@@ -731,47 +765,67 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     // ---- join the warps' records, pair by pair in tile order: the weights of a pair's
     // records first, then independent sums
     constexpr int kCols = D / 4;
-    float *wgt = reinterpret_cast<float *>(smem + W * C::ring);  // [2 W][RT] weights, then [2][RT] m, l
-    float *joined = wgt + 2 * W * RT;
-    int nshared = 0;
-    Piece shared_a, shared_b;
+    float *wgt = reinterpret_cast<float *>(smem + W * C::ring);  // [2 W][RT] weights, then [2 W][RT] (m, l)
+    float2 *joined = reinterpret_cast<float2 *>(wgt + 2 * W * RT);
+    __shared__ uint32_t pair_set[2 * W];  // each pair's pieces, and its first one
+    __shared__ int pair_first[2 * W];
     // a lane for each piece: the pieces of a pair are neighbours
     const bool have = lane < 2 * W && pieces[lane < 2 * W ? lane : 0].r >= 0;
     const int64_t key = have ? pieces[lane].pstart : -1;
-    uint32_t left = __ballot_sync(WSW_FULL_MASK, have);
-    while (left) {
-        const int i = __ffs(left) - 1;
-        const uint32_t set = left & __ballot_sync(WSW_FULL_MASK, key == __shfl_sync(WSW_FULL_MASK, key, i));
-        left &= ~set;
-        const Piece pc = pieces[i];
-        const bool complete = pc.pstart >= b && pc.pstart + pc.nt <= e;
-        const int h = pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
-        const int rows = min(RT, a.group - g0);
-        if (tid < rows) {
-            float2 ml[2 * W];
-            float mx = -INFINITY, l = 0.f;
+    const uint32_t all = __ballot_sync(WSW_FULL_MASK, have);
+    const uint32_t below = all & ((1u << lane) - 1);
+    const int64_t key_below = __shfl_sync(WSW_FULL_MASK, key, below ? 31 - __clz(below) : lane);
+    const bool is_first = have && !(below && key == key_below);
+    const uint32_t firsts = __ballot_sync(WSW_FULL_MASK, is_first);
+    const int pairs = __popc(firsts);
+    const bool open = is_first && !(key >= b && key + pieces[lane < 2 * W ? lane : 0].nt <= e);
+    const uint32_t open_set = __ballot_sync(WSW_FULL_MASK, open);  // pairs shared with other CTAs: at most two
+    if (warp == 0 && is_first) {
+        const uint32_t later = lane == 31 ? 0 : firsts & ~((2u << lane) - 1);
+        const int j = __popc(firsts & ((1u << lane) - 1));
+        pair_set[j] = all & ~((1u << lane) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : 0xffffffffu);
+        pair_first[j] = lane;
+    }
+    __syncthreads();
+    for (int u = tid; u < pairs * RT; u += NT) {
+        const int j = u / RT, row = u - j * RT;
+        const uint32_t set = pair_set[j];
+        float2 ml[2 * W];
+        float mx = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int k = 0; k < 2 * W; ++k) {
-                ml[k] = (set >> k) & 1 ? piece_ml[k][tid] : make_float2(-INFINITY, 0.f);
-                mx = fmaxf(mx, ml[k].x);
-            }
+        for (int k = 0; k < 2 * W; ++k) ml[k] = (set >> k) & 1 ? piece_ml[k][row] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int k = 0; k < 2 * W; ++k) {
-                const float f = weight(ml[k].x, mx);
-                wgt[k * RT + tid] = f;
-                l = fmaf(ml[k].y, f, l);
-            }
-            joined[tid] = mx;
-            joined[RT + tid] = l;
+        for (int k = 0; k < 2 * W; ++k) mx = fmaxf(mx, ml[k].x);
+#pragma unroll
+        for (int k = 0; k < 2 * W; ++k) {
+            const float f = weight(ml[k].x, mx);
+            if ((set >> k) & 1) wgt[k * RT + row] = f;
+            l = fmaf(ml[k].y, f, l);
         }
-        __syncthreads();
-        float *dst = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec;
-        for (int u = tid; u < rows * kCols; u += NT) {
-            const int row = u / kCols, c4 = u - row * kCols;
+        joined[j * RT + row] = make_float2(mx, l);
+    }
+    __syncthreads();
+    // a thread keeps its place in the records and takes the pairs in turn; the records of the
+    // warps' first pieces are in the workspace: all on their way at once
+    constexpr int kUnits = RT * kCols, kTurns = NT / kUnits > 1 ? NT / kUnits : 1;
+    for (int u = tid; u < kTurns * kUnits; u += NT) {
+        const int v = u % kUnits, row = v / kCols, c4 = v % kCols;
+        const int at = row * C::rec + 4 + 4 * c4;
+        float4 xf[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            xf[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if ((all >> (2 * w)) & 1)
+                xf[w] = *reinterpret_cast<const float4 *>(a.wrec + static_cast<int64_t>(cta * W + w) * RT * C::rec + at);
+        }
+#pragma unroll 1
+        for (int j = u / kUnits; j < pairs; j += kTurns) {
+            const Piece pc = pieces[pair_first[j]];
+            const int h = pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
+            if (g0 + row >= a.group) continue;
+            const uint32_t set = pair_set[j];
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            auto add = [&](int k, const float *r) {
-                const float f = wgt[k * RT + row];
-                const float4 x = *reinterpret_cast<const float4 *>(r + row * C::rec + 4 + 4 * c4);
+            auto add = [&](float f, float4 x) {
                 s.x = fmaf(x.x, f, s.x);
                 s.y = fmaf(x.y, f, s.y);
                 s.z = fmaf(x.z, f, s.z);
@@ -779,164 +833,181 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             };
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                if ((set >> (2 * w)) & 1) add(2 * w, a.wrec + static_cast<int64_t>(cta * W + w) * RT * C::rec);
-                if ((set >> (2 * w + 1)) & 1) add(2 * w + 1, reinterpret_cast<const float *>(smem + w * C::ring));
+                if ((set >> (2 * w)) & 1) add(wgt[2 * w * RT + row], xf[w]);
+                if ((set >> (2 * w + 1)) & 1)
+                    add(wgt[(2 * w + 1) * RT + row],
+                        *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * C::ring) + at));
             }
-            const float mx = joined[row], l = joined[RT + row];
-            if (complete) {
+            const float2 ml = joined[j * RT + row];
+            if (pc.pstart >= b && pc.pstart + pc.nt <= e) {
                 const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
                 store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
-                if (c4 == 0 && a.lse) a.lse[head] = lse_of(mx, l);
+                if (c4 == 0 && a.lse) a.lse[head] = lse_of(ml.x, ml.y);
             } else {
-                float *r = dst + row * C::rec;
-                *reinterpret_cast<float4 *>(r + 4 + 4 * c4) = s;
-                if (c4 == 0) *reinterpret_cast<float2 *>(r) = make_float2(mx, l);
+                float *r = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec;
+                *reinterpret_cast<float4 *>(r + at) = s;
+                if (c4 == 0) *reinterpret_cast<float2 *>(r + row * C::rec) = ml;
             }
         }
-        if (!complete) {
-            if (nshared == 0) shared_a = pc;
-            else shared_b = pc;
-            ++nshared;
-        }
-        __syncthreads();  // the weights' place is free again
     }
+    const int nshared = __popc(open_set);
+    Piece shared_a = pieces[0], shared_b = pieces[0];
+    if (nshared > 0) shared_a = pieces[__ffs(open_set) - 1];
+    if (nshared > 1) shared_b = pieces[31 - __clz(open_set)];
+    __syncthreads();
     if (nshared == 0) return;
 
-    // ---- pairs shared with other CTAs (at most two): the last to arrive joins their records.
+    // ---- pairs shared with other CTAs (at most two): first the group's CTAs, then the groups.
     // The block barrier above orders this CTA's records before thread 0's arrival, whose
     // release publishes them; its acquire, and the barrier after it, order the reads below
     // after every arrival.
+    auto arrive = [](unsigned *cnt, int expected) {
+        unsigned old;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(cnt) : "memory");
+        const bool is_last = old == static_cast<unsigned>(expected - 1);
+        if (is_last) *cnt = 0u;  // ready for the next call
+        return is_last;
+    };
+    const int group0 = cta / kGroup * kGroup;  // the group's first CTA
+    auto first_cta = [&](const Piece &pc) { return static_cast<int>(pc.pstart / run); };
+    auto last_cta = [&](const Piece &pc) { return static_cast<int>((pc.pstart + pc.nt - 1) / run); };
     if (tid < nshared) {
         const Piece pc = tid == 0 ? shared_a : shared_b;
-        const int64_t f = pc.pstart / run, t = (pc.pstart + pc.nt - 1) / run;
-        unsigned old;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.cnt + f) : "memory");
-        last[tid] = old == static_cast<unsigned>(t - f);
+        const int f = first_cta(pc), c0 = max(f, group0), c1 = min(last_cta(pc), group0 + kGroup - 1);
+        last[tid] = arrive(a.cnt + 2 * c0 + (c0 == f), c1 - c0 + 1);
     }
     __syncthreads();
     for (int sp = 0; sp < nshared; ++sp) {
         if (!last[sp]) continue;
         const Piece pc = sp == 0 ? shared_a : shared_b;
-        const int f = static_cast<int>(pc.pstart / run), n = static_cast<int>((pc.pstart + pc.nt - 1) / run) - f + 1;
+        const int f = first_cta(pc), t = last_cta(pc);
         const int h = pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
         const int rows = min(RT, a.group - g0);
-        // record k: CTA f + k's; the first CTA holds the pair's beginning as its second pair
-        auto record = [&](int k) -> const float * {
-            return a.rec + (static_cast<int64_t>(f + k) * 2 + (k == 0)) * RT * C::rec;
-        };
-        float *w = reinterpret_cast<float *>(smem);             // [n][RT] maxima, then weights
-        float *lw = w + kCtas * RT;                             // [n][RT] sums
-        float *part = lw + kCtas * RT;                          // [slices][rows][D]
-        // the records are dealt to slices of the block, whose sums are then added in order; the
-        // first ones are on their way while the weights are made
-        const int units = rows * kCols;
-        const int slices = NT / units > 1 ? NT / units : 1;
-        constexpr int kAhead = 16;
-        float4 xa[kAhead];
-        {
-            const int sl = tid / units, v = tid - sl * units;
-            const float *r0 = record(0) + v / kCols * C::rec + 4 + 4 * (v % kCols);
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int k = sl + i * slices;
-                xa[i] = sl < slices && k < n
-                            ? __ldcg(reinterpret_cast<const float4 *>(r0 + (record(k) - record(0))))
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-        }
-        for (int u = tid; u < n * RT; u += NT) {
-            const int k = u / RT, row = u - k * RT;
-            if (row >= rows) continue;
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(record(k) + row * C::rec));
-            w[u] = ml.x;
-            lw[u] = ml.y;
-        }
-        __syncthreads();
-        for (int row = warp; row < rows; row += W) {
-            float mx = -INFINITY, l = 0.f;
-            for (int k = lane; k < n; k += 32) mx = fmaxf(mx, w[k * RT + row]);
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
-            for (int k = lane; k < n; k += 32) {
-                const float g = weight(w[k * RT + row], mx);
-                w[k * RT + row] = g;
-                l = fmaf(lw[k * RT + row], g, l);
-            }
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(WSW_FULL_MASK, l, d);
-            __syncwarp();
-            if (lane == 0) {
-                lw[row] = l;  // record 0's sums have been read
-                const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
-                if (a.lse) a.lse[head] = lse_of(mx, l);
-            }
-        }
-        __syncthreads();
-        for (int u = tid; u < slices * units; u += NT) {
-            const int sl = u / units, v = u - sl * units;
-            const int row = v / kCols, c4 = v - row * kCols;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            auto add = [&](int k, float4 x) {
-                const float g = w[k * RT + row];
-                s.x = fmaf(x.x, g, s.x);
-                s.y = fmaf(x.y, g, s.y);
-                s.z = fmaf(x.z, g, s.z);
-                s.w = fmaf(x.w, g, s.w);
+        const int groups = t / kGroup - f / kGroup + 1;
+        // level 0: the group's CTAs; level 1: the groups, each at its first CTA's record
+#pragma unroll 1
+        for (int level = 0; level < 2; ++level) {
+            const int c0 = level == 0 ? max(f, group0) : f;
+            const int n = level == 0 ? min(t, group0 + kGroup - 1) - c0 + 1 : groups;
+            const bool final = level == 1 || groups == 1;
+            // record k; a pair begins in its first CTA's second record
+            auto record = [&](int k) -> float * {
+                const int c = level == 0 ? c0 + k : k == 0 ? f : (f / kGroup + k) * kGroup;
+                return a.rec + (static_cast<int64_t>(c) * 2 + (c == f)) * RT * C::rec;
             };
-            int k = sl;
-            if (u == tid) {
+            constexpr int kMost = (kCtas + kGroup - 1) / kGroup;         // records: 19
+            static_assert(kGroup <= kMost, "records");
+            float *w = reinterpret_cast<float *>(smem);             // [n][RT] maxima, then weights
+            float *lw = w + kMost * RT;                             // [n][RT] sums
+            float *part = lw + kMost * RT;                          // [slices][rows][D]
+            // the records are dealt to slices of the block, whose sums are then added in order;
+            // a thread's are on their way while the weights are made
+            const int units = rows * kCols;
+            const int slices = NT / units > 1 ? NT / units : 1;
+            for (int u = tid; u < n * RT; u += NT) {
+                const int k = u / RT, row = u - k * RT;
+                if (row >= rows) continue;
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(record(k) + row * C::rec));
+                w[u] = ml.x;
+                lw[u] = ml.y;
+            }
+            float4 xa[kMost];
+            auto fetch = [&](int u) {
+                const int sl = u / units, v = u - sl * units;
+                const int at = v / kCols * C::rec + 4 + 4 * (v % kCols);
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i)
-                    if (sl + i * slices < n) add(sl + i * slices, xa[i]);
-                k += kAhead * slices;
+                for (int i = 0; i < kMost; ++i)
+                    if (sl < slices && sl + i * slices < n)
+                        xa[i] = __ldcg(reinterpret_cast<const float4 *>(record(sl + i * slices) + at));
+            };
+            fetch(tid);
+            __syncthreads();
+            if (tid < rows) {
+                float mx = -INFINITY, l = 0.f;
+#pragma unroll 4
+                for (int k = 0; k < n; ++k) mx = fmaxf(mx, w[k * RT + tid]);
+#pragma unroll 4
+                for (int k = 0; k < n; ++k) {
+                    const float g = weight(w[k * RT + tid], mx);
+                    w[k * RT + tid] = g;
+                    l = fmaf(lw[k * RT + tid], g, l);
+                }
+                lw[tid] = l;                 // record 0's have been read
+                lw[RT + tid] = mx;
             }
-#pragma unroll 8
-            for (; k < n; k += slices)
-                add(k, __ldcg(reinterpret_cast<const float4 *>(record(k) + row * C::rec + 4 + 4 * c4)));
-            *reinterpret_cast<float4 *>(part + u * 4) = s;
-        }
-        __syncthreads();
-        for (int u = tid; u < units; u += NT) {
-            const int row = u / kCols, c4 = u - row * kCols;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int sl = 0; sl < slices; ++sl) {
-                const float4 x = *reinterpret_cast<const float4 *>(part + (sl * units + u) * 4);
-                s.x += x.x;
-                s.y += x.y;
-                s.z += x.z;
-                s.w += x.w;
+            __syncthreads();
+            for (int u = tid; u < slices * units; u += NT) {
+                if (u != tid) fetch(u);
+                const int sl = u / units, row = (u - sl * units) / kCols;
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kMost; ++i) {
+                    const int k = sl + i * slices;
+                    if (k >= n) break;
+                    const float g = w[k * RT + row];
+                    s.x = fmaf(xa[i].x, g, s.x);
+                    s.y = fmaf(xa[i].y, g, s.y);
+                    s.z = fmaf(xa[i].z, g, s.z);
+                    s.w = fmaf(xa[i].w, g, s.w);
+                }
+                *reinterpret_cast<float4 *>(part + u * 4) = s;
             }
-            const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
-            const float inv = lw[row] == 0.f ? 0.f : 1.f / lw[row];
-            store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
+            __syncthreads();
+            for (int u = tid; u < units; u += NT) {
+                const int row = u / kCols, c4 = u - row * kCols;
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int sl = 0; sl < slices; ++sl) {
+                    const float4 x = *reinterpret_cast<const float4 *>(part + (sl * units + u) * 4);
+                    s.x += x.x;
+                    s.y += x.y;
+                    s.z += x.z;
+                    s.w += x.w;
+                }
+                const float l = lw[row], mx = lw[RT + row];
+                if (final) {
+                    const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
+                    if (c4 == 0 && a.lse) a.lse[head] = lse_of(mx, l);
+                } else {
+                    float *r = record(0) + row * C::rec;
+                    *reinterpret_cast<float4 *>(r + 4 + 4 * c4) = s;
+                    if (c4 == 0) *reinterpret_cast<float2 *>(r) = make_float2(mx, l);
+                }
+            }
+            __syncthreads();
+            if (final) break;
+            if (tid == 0) last[sp] = arrive(a.cnt + 2 * kCtas + f, groups);
+            __syncthreads();
+            if (!last[sp]) break;
         }
-        if (tid == 0) a.cnt[f] = 0u;  // ready for the next call
-        __syncthreads();
     }
 }
 
 template <int CT>
-cudaError_t launch_type(const Args &a, int rows, cudaStream_t s, bool pdl, int ctas);
+cudaError_t launch_type(const Args &a, int rows, cudaStream_t s, bool pdl, int64_t tiles);
 
 template <int CT, int D, int RT>
-cudaError_t launch_one(const Args &a, cudaStream_t s, bool pdl, int ctas) {
+cudaError_t launch_one(const Args &a, cudaStream_t s, bool pdl, int64_t tiles) {
     using C = Cfg<CT, D, RT>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attn_paged_kernel<CT, D, RT>), C::smem);
     if (e != cudaSuccess) return e;
-    return launch(attn_paged_kernel<CT, D, RT>, dim3(ctas), dim3(C::threads), C::smem, s, pdl, a);
+    // no more CTAs than `tiles`, the most that there can be, fill
+    const int64_t want = (tiles + C::warps - 1) / C::warps, ctas = want < 1 ? 1 : want > kCtas ? kCtas : want;
+    return launch(attn_paged_kernel<CT, D, RT>, dim3(static_cast<unsigned>(ctas)), dim3(C::threads), C::smem, s, pdl, a);
 }
 
 #define WSW_PAGED_TYPE(CT)                                                                       \
     template <>                                                                                  \
-    cudaError_t launch_type<CT>(const Args &a, int rows, cudaStream_t s, bool pdl, int ctas) {   \
+    cudaError_t launch_type<CT>(const Args &a, int rows, cudaStream_t s, bool pdl, int64_t tiles) {   \
         switch (a.kv.head_dim * 2 + (rows == 16)) {                                              \
-            case 128: return launch_one<CT, 64, 8>(a, s, pdl, ctas);                             \
-            case 129: return launch_one<CT, 64, 16>(a, s, pdl, ctas);                            \
-            case 256: return launch_one<CT, 128, 8>(a, s, pdl, ctas);                            \
-            case 257: return launch_one<CT, 128, 16>(a, s, pdl, ctas);                           \
-            case 512: return launch_one<CT, 256, 8>(a, s, pdl, ctas);                            \
-            default: return launch_one<CT, 256, 16>(a, s, pdl, ctas);                            \
+            case 128: return launch_one<CT, 64, 8>(a, s, pdl, tiles);                             \
+            case 129: return launch_one<CT, 64, 16>(a, s, pdl, tiles);                            \
+            case 256: return launch_one<CT, 128, 8>(a, s, pdl, tiles);                            \
+            case 257: return launch_one<CT, 128, 16>(a, s, pdl, tiles);                           \
+            case 512: return launch_one<CT, 256, 8>(a, s, pdl, tiles);                            \
+            default: return launch_one<CT, 256, 16>(a, s, pdl, tiles);                            \
         }                                                                                        \
     }
 
