@@ -78,6 +78,8 @@ def test_attention_refusals(lib):
     assert _attn(lib, ts=4) == INVALID  # a row shorter than max_pages
     assert _attn(lib, n=70000) == UNSUPPORTED and _attn(lib, window=1 << 31) == UNSUPPORTED
     assert _attn(lib, pages=1 << 28, ts=1 << 28) == UNSUPPORTED  # 2^32 positions
+    big = _cache(page_size=65536, heads=64)
+    assert _attn(lib, cache=big, heads=64, n=60000, pages=1024, ts=1024) == UNSUPPORTED  # 2^34 tiles
     assert _attn(lib, q=None) == INVALID and _attn(lib, ws=None) == INVALID and _attn(lib, table=None) == INVALID
     assert _attn(lib, q=P(4104)) == MISALIGNED and _attn(lib, lens=P(4097)) == MISALIGNED
     assert _attn(lib, wsn=1000) == WORKSPACE

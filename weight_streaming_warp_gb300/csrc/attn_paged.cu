@@ -61,8 +61,6 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
         return WSW_ERR_MISALIGNED;
     if (ws_bytes < wsw_attn_paged_decode_workspace_bytes(requests, q_heads, cache->heads, cache->head_dim))
         return WSW_ERR_WORKSPACE;
-    DeviceInfo di;
-    if (!device_info(&di, &st)) return st;
     a.q = q;
     a.out = out;
     a.lse = lse;
@@ -89,6 +87,9 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
     // tiles of the longest possible lists
     const int64_t seen = a.max_len < a.window ? a.max_len : a.window;
     const int64_t tiles = requests * cache->heads * a.passes * ((seen + kTile - 1) / kTile);
+    if (tiles >= lim - 65536) return WSW_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
+    DeviceInfo di;
+    if (!device_info(&di, &st)) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (cache->dtype == WSW_F16) e = launch_type<WSW_F16>(a, rows, s, o.pdl, tiles);

@@ -40,7 +40,7 @@ namespace paged {
 
 constexpr int kTile = 16;      // positions per tile
 constexpr int kWhole = 32;     // pairs of up to so many tiles stay in one CTA
-constexpr int kGroup = 8;      // CTAs whose records are joined first
+constexpr int kGroup = 12;     // CTAs whose records are joined first
 constexpr int kCtas = 152;     // runs of the tile list: one CTA per SM of a 152-SM part
 constexpr float kShift = 8.f;  // log2 of the weights' scale
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -91,7 +91,7 @@ struct Cfg {
     static constexpr int rec = D + 4;                   // floats: m, l, 2 pad, sums
     static_assert(stages >= 2 && RT * rec * 4 <= ring && ring % 16 == 0, "ring");
     static_assert(2 * warps <= 32 && 3 * 2 * warps * RT * 4 <= 4096 && smem <= kSmemMax + 3072, "joins");
-    static_assert(2 * 19 * RT * 4 + (threads > RT * D / 4 ? threads : RT * D / 4) * 16 <= warps * ring, "joins");
+    static_assert(2 * 14 * RT * 4 + (threads > RT * D / 4 ? threads : RT * D / 4) * 16 <= warps * ring, "joins");
 };
 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -162,25 +162,18 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t biased, uint32_t sel, __ha
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-__device__ __forceinline__ void store_out4(const Args &a, int64_t i, float4 v) {
-    if (a.dtype == WSW_F32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i) = v;
-    } else if (a.dtype == WSW_BF16) {
-        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = *reinterpret_cast<uint2 *>(h);
-    } else {
-        __half2 h[2] = {__floats2half2_rn(v.x, v.y), __floats2half2_rn(v.z, v.w)};
-        *reinterpret_cast<uint2 *>(static_cast<__half *>(a.out) + i) = *reinterpret_cast<uint2 *>(h);
-    }
+// (x, y) in the output's 16-bit type
+__device__ __forceinline__ uint32_t pack16(int dtype, float x, float y) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    const __half2 h = __floats2half2_rn(x, y);
+    return dtype == WSW_BF16 ? *reinterpret_cast<const uint32_t *>(&b) : *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ void store_out2(const Args &a, int64_t i, float x, float y) {
-    if (a.dtype == WSW_F32) {
-        *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + i) = make_float2(x, y);
-    } else if (a.dtype == WSW_BF16) {
-        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = __floats2bfloat162_rn(x, y);
-    } else {
-        *reinterpret_cast<__half2 *>(static_cast<__half *>(a.out) + i) = __floats2half2_rn(x, y);
-    }
+__device__ __forceinline__ void store_out4(const Args &a, int64_t i, float4 v) {
+    if (a.dtype == WSW_F32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i) = v;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + i) =
+            make_uint2(pack16(a.dtype, v.x, v.y), pack16(a.dtype, v.z, v.w));
 }
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
@@ -190,13 +183,13 @@ __device__ __forceinline__ float weight(float m, float mx) { return m == -INFINI
 
 // Where a warp is in the tile list: request, head and pass, tile of the pair.
 struct Cursor {
-    int64_t g;   // index in the list
+    int g;       // index in the list
     int r, hp, t, nt;
     int start, len;  // seen positions are [start, len)
 };
 // A piece of a pair left as a record: the pair, its first tile's index and its tile count.
 struct Piece {
-    int64_t pstart;
+    int pstart;
     int r, hp, nt;  // r = -1: none
 };
 
@@ -231,9 +224,11 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     using C = Cfg<CT, D, RT>;
     constexpr int W = C::warps, NT = C::threads;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int64_t scan[W + 1];
-    __shared__ int64_t run_off[W];     // of each warp's first tile in its request
-    __shared__ int run_req[W];
+    __shared__ int scan[W];
+    struct Place {
+        int req, off, nt;  // a tile's request, its index there, the tiles of a pair there
+    };
+    __shared__ Place cut[2], place[W];  // of the CTA's cuts, of the warps' first tiles
     __shared__ Piece pieces[2 * W];
     __shared__ float2 piece_ml[2 * W][RT];  // (m, l) of each piece's rows
     __shared__ uint32_t seen_mask[W][C::stages];
@@ -245,78 +240,79 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     pdl_launch_dependents();
     pdl_wait();
 
-    // ---- the tile list: each thread counts a run of requests, a scan places the runs
+    // ---- the tile list (below 2^31 tiles): each thread counts a run of requests, a scan
+    // places the runs
     const int per = (a.requests + NT - 1) / NT;
     const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
-    int64_t mine = 0;
+    int mine = 0, nt0 = 0;  // nt0: of request r0
     bool cut_len = false;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-        const int n = a.lens[r];
-        cut_len |= n < 0 || n > a.max_len;
-        mine += static_cast<int64_t>(tiles_of(a, n < 0 ? 0 : n > a.max_len ? a.max_len : n)) * HP;
+        const int n = a.lens[r], clipped = min(max(n, 0), a.max_len);
+        cut_len |= n != clipped;
+        const int nt = tiles_of(a, clipped);
+        if (r == r0) nt0 = nt;
+        mine += nt * HP;
     }
     if (cut_len && cta == 0 && a.err) atomicOr(a.err, 2);
-    int64_t upto = mine;
+    int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(WSW_FULL_MASK, upto, d);
+        const int y = __shfl_up_sync(WSW_FULL_MASK, upto, d);
         if (lane >= d) upto += y;
     }
     if (lane == 31) scan[warp] = upto;
     __syncthreads();
-    int64_t total = 0, before = upto - mine;
+    int total = 0, before = upto - mine;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    const int64_t run = max(total < 0x7fffffff ? static_cast<int64_t>((static_cast<uint32_t>(total) + kCtas - 1) / kCtas)
-                                               : (total + kCtas - 1) / kCtas,
-                            static_cast<int64_t>(W));  // tiles per CTA
-    // the request that holds tile s, for the thread whose requests do
-    auto locate = [&](int64_t s, int &req, int64_t &off) {
+    const int run = max((total + kCtas - 1) / kCtas, W);  // tiles per CTA
+    // the place of tile s, from the thread whose requests hold it
+    auto locate = [&](int s, Place &p) {
         if (s < before || s >= before + mine) return;
-        int64_t at = before;
+        int at = before, r = r0, nt = nt0;
 #pragma unroll 1
-        for (int r = r0; r < r1; ++r) {
-            const int64_t n = static_cast<int64_t>(tiles_of(a, clipped_len(a, r))) * HP;
-            if (s < at + n) {
-                req = r;
-                off = s - at;
-                return;
-            }
-            at += n;
+        while (s >= at + nt * HP) {
+            at += nt * HP;
+            nt = tiles_of(a, clipped_len(a, ++r));
         }
+        p = Place{r, s - at, nt};
     };
-    const int64_t raw_b = min(cta * run, total), raw_e = min(raw_b + run, total);
-    locate(raw_b, run_req[0], run_off[0]);
-    locate(raw_e, run_req[1], run_off[1]);
+    const int raw_b = static_cast<int>(min(static_cast<int64_t>(cta) * run, static_cast<int64_t>(total)));
+    const int raw_e = static_cast<int>(min(static_cast<int64_t>(cta + 1) * run, static_cast<int64_t>(total)));
+    locate(raw_b, cut[0]);
+    locate(raw_e, cut[1]);
     __syncthreads();
-    auto snapped = [&](int64_t s, int i) -> int64_t {
-        if (s >= total || s == 0) return s;
-        const int nt = tiles_of(a, clipped_len(a, run_req[i]));
-        if (nt > kWhole) return s;
-        const int t = run_off[i] < 0x7fffffff ? static_cast<int>(run_off[i]) % nt : static_cast<int>(run_off[i] % nt);
-        return s - t + (2 * t > nt ? nt : 0);
+    auto snapped = [&](int s, const Place &p) {
+        if (s >= total || s == 0 || p.nt > kWhole) return s;
+        const int t = p.off % p.nt;
+        return s - t + (2 * t > p.nt ? p.nt : 0);
     };
-    const int64_t b = snapped(raw_b, 0), e = snapped(raw_e, 1);
-    const int64_t n_cta = e - b;
-    __syncthreads();
+    const int b = snapped(raw_b, cut[0]), e = snapped(raw_e, cut[1]);
+    const int n_cta = e - b;
+    auto first_tile = [&](int w) { return b + static_cast<int>(static_cast<int64_t>(n_cta) * w / W); };
+    if (before < e && before + mine > b) {
 #pragma unroll 1
-    for (int w = 0; w < W; ++w) locate(b + n_cta * w / W, run_req[w], run_off[w]);
+        for (int w = 0; w < W; ++w) locate(first_tile(w), place[w]);
+    }
     // requests that see nothing
+#pragma unroll 1
     for (int r = cta; r < a.requests; r += gridDim.x) {
-        if (a.lens[r] > 0 && a.max_len > 0) continue;
-        for (int i = tid; i < a.q_heads * (D / 4); i += NT)
-            store_out4(a, (static_cast<int64_t>(r) * a.q_heads) * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
-        if (a.lse)
-            for (int i = tid; i < a.q_heads; i += NT) a.lse[static_cast<int64_t>(r) * a.q_heads + i] = -INFINITY;
+        if (clipped_len(a, r) > 0) continue;
+        const int64_t head = static_cast<int64_t>(r) * a.q_heads;
+#pragma unroll 1
+        for (int i = tid; i < a.q_heads * (D / 4); i += NT) store_out4(a, head * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll 1
+        for (int i = tid; a.lse && i < a.q_heads; i += NT) a.lse[head + i] = -INFINITY;
     }
     __syncthreads();
     if (n_cta == 0) return;
 
-    const int64_t wb = b + n_cta * warp / W, we = b + n_cta * (warp + 1) / W;
-    int todo = static_cast<int>(we - wb);     // tiles left to use
+    const int wb = first_tile(warp), we = first_tile(warp + 1);
+    int todo = we - wb;     // tiles left to use
     int to_issue = todo;
     unsigned char *ring = smem + warp * C::ring;
     const uint32_t ring_s = smem_addr(ring);
@@ -326,10 +322,11 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 
     if (todo > 0) {
         Cursor uc;  // the tile in use
-        set_request(a, uc, run_req[warp]);
+        const Place at_first = place[warp];
+        set_request(a, uc, at_first.req);
         uc.g = wb;
-        uc.hp = static_cast<int>(run_off[warp] / uc.nt);
-        uc.t = static_cast<int>(run_off[warp] - static_cast<int64_t>(uc.hp) * uc.nt);
+        uc.hp = at_first.off / uc.nt;
+        uc.t = at_first.off - uc.hp * uc.nt;
         Cursor ic = uc;  // the next tile to copy
         const int page_mask = (1 << a.kv.page_shift) - 1;
 
@@ -423,9 +420,6 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             }
             cp_commit();  // one group per step, empty past the end
         };
-#pragma unroll
-        for (int i = 0; i < C::stages - 1; ++i) issue();
-
         const int gq = lane >> 2, tq = lane & 3;
         uint32_t qa[C::q_smem ? 1 : C::ksteps][4];
         float m[RT / 8], l[RT / 8], slope[RT / 8];
@@ -433,11 +427,15 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         bool q_lo = false;   // RT 16: q has residuals
         int t_first = 0;     // first tile of the piece
         bool fresh = true;   // a new pair begins
-        bool first_piece = true;
         int rst = 0;
         const int mi = lane >> 3, mr = lane & 7;
 
-        for (; todo > 0; --todo) {
+        // the first turns only fill the ring
+#pragma unroll 1
+        for (int fill = 1 - C::stages; todo > 0; todo -= fill >= 0, ++fill) {
+            __syncwarp();  // every lane is done reading the stage that the next copy reuses
+            issue();
+            if (fill < 0) continue;
             if (fresh) {
                 fresh = false;
                 t_first = uc.t;
@@ -519,8 +517,6 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
             }
-            __syncwarp();  // every lane is done reading the stage that the next copy reuses
-            issue();
             cp_wait<C::stages - 1>();
             __syncwarp();  // the tile's pieces copied by every lane are visible
             const uint32_t stg = ring_s + rst * C::stage;
@@ -734,30 +730,37 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                     if (!whole) piece_ml[2 * warp + (todo == 1)][row] = make_float2(m[y], l[y]);
                     else if (a.lse) a.lse[head] = lse_of(m[y], l[y]);
                 }
-                if constexpr (!C::q8) {
+                // lane tq's dimensions: 2 tq, 2 tq + 1 of every eight, or (q8_0) 4 tq .. 4 tq + 3 of sixteen
+                if (!whole || a.dtype == WSW_F32) {
+                    float *dst = whole ? static_cast<float *>(a.out) + head * D : rr + 4;
+                    const float f = whole ? inv : 1.f;
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        const int d = 8 * n + 2 * tq;
-                        if (whole) store_out2(a, head * D + d, val(n, 0) * inv, val(n, 1) * inv);
-                        else *reinterpret_cast<float2 *>(rr + 4 + d) = make_float2(val(n, 0), val(n, 1));
+                    for (int n = 0; n < D / 8; n += C::q8 ? 2 : 1) {
+                        if constexpr (C::q8)
+                            *reinterpret_cast<float4 *>(dst + 8 * n + 4 * tq) =
+                                make_float4(val(n, 0) * f, val(n + 1, 0) * f, val(n, 1) * f, val(n + 1, 1) * f);
+                        else
+                            *reinterpret_cast<float2 *>(dst + 8 * n + 2 * tq) = make_float2(val(n, 0) * f, val(n, 1) * f);
                     }
                 } else {
+                    uint16_t *dst = static_cast<uint16_t *>(a.out) + head * D;
 #pragma unroll
-                    for (int n = 0; n < D / 8; n += 2) {
-                        const int d = 8 * n + 4 * tq;
-                        const float4 v = make_float4(val(n, 0), val(n + 1, 0), val(n, 1), val(n + 1, 1));
-                        if (whole) store_out4(a, head * D + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                        else *reinterpret_cast<float4 *>(rr + 4 + d) = v;
+                    for (int n = 0; n < D / 8; n += C::q8 ? 2 : 1) {
+                        if constexpr (C::q8)
+                            *reinterpret_cast<uint2 *>(dst + 8 * n + 4 * tq) =
+                                make_uint2(pack16(a.dtype, val(n, 0) * inv, val(n + 1, 0) * inv),
+                                           pack16(a.dtype, val(n, 1) * inv, val(n + 1, 1) * inv));
+                        else
+                            *reinterpret_cast<uint32_t *>(dst + 8 * n + 2 * tq) =
+                                pack16(a.dtype, val(n, 0) * inv, val(n, 1) * inv);
                     }
                 }
             }
-            first_piece = false;
             if (todo > 1) {
                 // advance() is safe: there is another tile
                 advance(a, uc);
             }
         }
-        (void)first_piece;
         cp_wait<0>();
     }
     __syncthreads();
@@ -771,10 +774,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     __shared__ int pair_first[2 * W];
     // a lane for each piece: the pieces of a pair are neighbours
     const bool have = lane < 2 * W && pieces[lane < 2 * W ? lane : 0].r >= 0;
-    const int64_t key = have ? pieces[lane].pstart : -1;
+    const int key = have ? pieces[lane].pstart : -1;
     const uint32_t all = __ballot_sync(WSW_FULL_MASK, have);
     const uint32_t below = all & ((1u << lane) - 1);
-    const int64_t key_below = __shfl_sync(WSW_FULL_MASK, key, below ? 31 - __clz(below) : lane);
+    const int key_below = __shfl_sync(WSW_FULL_MASK, key, below ? 31 - __clz(below) : lane);
     const bool is_first = have && !(below && key == key_below);
     const uint32_t firsts = __ballot_sync(WSW_FULL_MASK, is_first);
     const int pairs = __popc(firsts);
@@ -870,8 +873,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         return is_last;
     };
     const int group0 = cta / kGroup * kGroup;  // the group's first CTA
-    auto first_cta = [&](const Piece &pc) { return static_cast<int>(pc.pstart / run); };
-    auto last_cta = [&](const Piece &pc) { return static_cast<int>((pc.pstart + pc.nt - 1) / run); };
+    auto first_cta = [&](const Piece &pc) { return pc.pstart / run; };
+    auto last_cta = [&](const Piece &pc) { return (pc.pstart + pc.nt - 1) / run; };
     if (tid < nshared) {
         const Piece pc = tid == 0 ? shared_a : shared_b;
         const int f = first_cta(pc), c0 = max(f, group0), c1 = min(last_cta(pc), group0 + kGroup - 1);
@@ -896,7 +899,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 const int c = level == 0 ? c0 + k : k == 0 ? f : (f / kGroup + k) * kGroup;
                 return a.rec + (static_cast<int64_t>(c) * 2 + (c == f)) * RT * C::rec;
             };
-            constexpr int kMost = (kCtas + kGroup - 1) / kGroup;         // records: 19
+            constexpr int kMost = (kCtas + kGroup - 1) / kGroup + 1;     // groups: a pair may touch one more
             static_assert(kGroup <= kMost, "records");
             float *w = reinterpret_cast<float *>(smem);             // [n][RT] maxima, then weights
             float *lw = w + kMost * RT;                             // [n][RT] sums
@@ -913,33 +916,39 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 lw[u] = ml.y;
             }
             float4 xa[kMost];
+            const float *second = record(1);  // from the second on the records are evenly spaced
+            const int64_t apart = static_cast<int64_t>(level == 0 ? 2 : 2 * kGroup) * RT * C::rec;
             auto fetch = [&](int u) {
                 const int sl = u / units, v = u - sl * units;
                 const int at = v / kCols * C::rec + 4 + 4 * (v % kCols);
+                const float *r = second + at + (sl - 1) * apart;
 #pragma unroll
-                for (int i = 0; i < kMost; ++i)
+                for (int i = 0; i < kMost; ++i, r += slices * apart)
                     if (sl < slices && sl + i * slices < n)
-                        xa[i] = __ldcg(reinterpret_cast<const float4 *>(record(sl + i * slices) + at));
+                        xa[i] = __ldcg(reinterpret_cast<const float4 *>(i == 0 && sl == 0 ? record(0) + at : r));
             };
-            fetch(tid);
-            __syncthreads();
-            if (tid < rows) {
-                float mx = -INFINITY, l = 0.f;
+#pragma unroll 1
+            for (int u = tid; u - tid < slices * units; u += NT) {
+                fetch(u);
+                if (u == tid) {
+                    __syncthreads();
+                    if (tid < rows) {
+                        float mx = -INFINITY, l = 0.f;
 #pragma unroll 4
-                for (int k = 0; k < n; ++k) mx = fmaxf(mx, w[k * RT + tid]);
+                        for (int k = 0; k < n; ++k) mx = fmaxf(mx, w[k * RT + tid]);
 #pragma unroll 4
-                for (int k = 0; k < n; ++k) {
-                    const float g = weight(w[k * RT + tid], mx);
-                    w[k * RT + tid] = g;
-                    l = fmaf(lw[k * RT + tid], g, l);
+                        for (int k = 0; k < n; ++k) {
+                            const float g = weight(w[k * RT + tid], mx);
+                            w[k * RT + tid] = g;
+                            l = fmaf(lw[k * RT + tid], g, l);
+                        }
+                        lw[tid] = l;  // record 0's have been read
+                        lw[RT + tid] = mx;
+                    }
+                    __syncthreads();
                 }
-                lw[tid] = l;                 // record 0's have been read
-                lw[RT + tid] = mx;
-            }
-            __syncthreads();
-            for (int u = tid; u < slices * units; u += NT) {
-                if (u != tid) fetch(u);
                 const int sl = u / units, row = (u - sl * units) / kCols;
+                if (sl >= slices) continue;
                 float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < kMost; ++i) {
@@ -954,6 +963,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 *reinterpret_cast<float4 *>(part + u * 4) = s;
             }
             __syncthreads();
+#pragma unroll 1
             for (int u = tid; u < units; u += NT) {
                 const int row = u / kCols, c4 = u - row * kCols;
                 float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
