@@ -57,7 +57,7 @@ struct Args {
     // record there, then [kCtas] of a pair's groups, by its first CTA
     unsigned *cnt;
     float *rec;     // [kCtas][2][rows][D + 4] what a CTA leaves of its shared pairs
-    float *wrec;    // [kCtas][warps][rows][D + 4] what a warp leaves of its first pair
+    float *wrec;    // [kCtas][warps][rows][D (+ 4)] what a warp leaves of its first pair
     KvView kv;
     int64_t table_stride;
     float scale2;     // scale log2 e
@@ -88,10 +88,12 @@ struct Cfg {
     static constexpr int ring = stages * stage;
     // the joins at the end keep weights where q was, or behind the rings
     static constexpr int smem = warps * (ring + q_bytes) + (q_bytes == 0 ? 4096 : 0);
-    static constexpr int rec = D + 4;                   // floats: m, l, 2 pad, sums
-    static_assert(stages >= 2 && RT * rec * 4 <= ring && ring % 16 == 0, "ring");
+    static constexpr int rec = D + 4;                   // floats of a CTA's record row: m, l, 2 pad, sums
+    // of a warp's: sums, padded against bank conflicts if two records fit into the warp's ring
+    static constexpr int srec = 2 * RT * (D + 4) * 4 <= ring ? D + 4 : D;
+    static_assert(stages >= 2 && 2 * RT * srec * 4 <= ring && ring % 16 == 0, "ring");
     static_assert(2 * warps <= 32 && 3 * 2 * warps * RT * 4 <= 4096 && smem <= kSmemMax + 3072, "joins");
-    static_assert(2 * 14 * RT * 4 + (threads > RT * D / 4 ? threads : RT * D / 4) * 16 <= warps * ring, "joins");
+    static_assert(2 * 14 * RT * 4 + RT * 8 <= warps * ring, "joins");
 };
 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                         vp += kRows * a.kv.pos_stride;
                     }
                 } else {
-#pragma unroll
+#pragma unroll 2
                     for (int i = 0; i < kTile / kRows; ++i) {
                         const int row = i * kRows + rr;
                         const int64_t o = __shfl_sync(WSW_FULL_MASK, at, row);
@@ -427,6 +429,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         bool q_lo = false;   // RT 16: q has residuals
         int t_first = 0;     // first tile of the piece
         bool fresh = true;   // a new pair begins
+        bool first_left = false;  // the first piece is in the workspace
         int rst = 0;
         const int mi = lane >> 3, mr = lane & 7;
 
@@ -712,7 +715,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                     __syncwarp();
                     rec = reinterpret_cast<float *>(ring);
                 } else {
-                    rec = a.wrec + static_cast<int64_t>(cta * W + warp) * RT * C::rec;
+                    rec = a.wrec + static_cast<int64_t>(cta * W + warp) * RT * C::srec;
+                    first_left = true;
                 }
                 if (lane == 0) pieces[2 * warp + (todo == 1)] = Piece{uc.g - uc.t, uc.r, uc.hp, uc.nt};
             }
@@ -723,36 +727,36 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 const int row = gq + 8 * y;
                 if (g0 + row >= a.group) continue;
                 const int64_t head = static_cast<int64_t>(uc.r) * a.q_heads + h * a.group + g0 + row;
-                const float inv = l[y] == 0.f ? 0.f : 1.f / l[y];
-                auto val = [&](int n, int x) { return RT == 8 ? o[n][x] + o[n][2 + x] : o[n][2 * y + x]; };
-                float *rr = whole ? nullptr : rec + row * C::rec;
+                const float inv = l[y] == 0.f ? 0.f : 1.f / l[y], f = whole ? inv : 1.f;
+                float v[D / 8][2];
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) v[n][x] = (RT == 8 ? o[n][x] + o[n][2 + x] : o[n][2 * y + x]) * f;
                 if (tq == 0) {
                     if (!whole) piece_ml[2 * warp + (todo == 1)][row] = make_float2(m[y], l[y]);
                     else if (a.lse) a.lse[head] = lse_of(m[y], l[y]);
                 }
                 // lane tq's dimensions: 2 tq, 2 tq + 1 of every eight, or (q8_0) 4 tq .. 4 tq + 3 of sixteen
                 if (!whole || a.dtype == WSW_F32) {
-                    float *dst = whole ? static_cast<float *>(a.out) + head * D : rr + 4;
-                    const float f = whole ? inv : 1.f;
+                    float *dst = whole ? static_cast<float *>(a.out) + head * D : rec + row * C::srec;
+                    dst += C::q8 ? 4 * tq : 2 * tq;
 #pragma unroll
                     for (int n = 0; n < D / 8; n += C::q8 ? 2 : 1) {
                         if constexpr (C::q8)
-                            *reinterpret_cast<float4 *>(dst + 8 * n + 4 * tq) =
-                                make_float4(val(n, 0) * f, val(n + 1, 0) * f, val(n, 1) * f, val(n + 1, 1) * f);
+                            *reinterpret_cast<float4 *>(dst + 8 * n) = make_float4(v[n][0], v[n + 1][0], v[n][1], v[n + 1][1]);
                         else
-                            *reinterpret_cast<float2 *>(dst + 8 * n + 2 * tq) = make_float2(val(n, 0) * f, val(n, 1) * f);
+                            *reinterpret_cast<float2 *>(dst + 8 * n) = make_float2(v[n][0], v[n][1]);
                     }
                 } else {
-                    uint16_t *dst = static_cast<uint16_t *>(a.out) + head * D;
+                    uint16_t *dst = static_cast<uint16_t *>(a.out) + head * D + (C::q8 ? 4 * tq : 2 * tq);
 #pragma unroll
                     for (int n = 0; n < D / 8; n += C::q8 ? 2 : 1) {
                         if constexpr (C::q8)
-                            *reinterpret_cast<uint2 *>(dst + 8 * n + 4 * tq) =
-                                make_uint2(pack16(a.dtype, val(n, 0) * inv, val(n + 1, 0) * inv),
-                                           pack16(a.dtype, val(n, 1) * inv, val(n + 1, 1) * inv));
+                            *reinterpret_cast<uint2 *>(dst + 8 * n) =
+                                make_uint2(pack16(a.dtype, v[n][0], v[n + 1][0]), pack16(a.dtype, v[n][1], v[n + 1][1]));
                         else
-                            *reinterpret_cast<uint32_t *>(dst + 8 * n + 2 * tq) =
-                                pack16(a.dtype, val(n, 0) * inv, val(n, 1) * inv);
+                            *reinterpret_cast<uint32_t *>(dst + 8 * n) = pack16(a.dtype, v[n][0], v[n][1]);
                     }
                 }
             }
@@ -761,7 +765,16 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 advance(a, uc);
             }
         }
-        cp_wait<0>();
+        // the first piece's record joins the last one's in the ring
+        if (first_left) {
+            __syncwarp();
+            const float4 *src = reinterpret_cast<const float4 *>(a.wrec + static_cast<int64_t>(cta * W + warp) * RT * C::srec);
+            float4 *dst = reinterpret_cast<float4 *>(ring) + RT * C::srec / 4;
+            constexpr int kPer = RT * C::srec / 4 / 32;  // whole rounds of the warp
+#pragma unroll 8
+            for (int i = 0; i < kPer; ++i) dst[i * 32 + lane] = src[i * 32 + lane];
+            if (lane < RT * C::srec / 4 - kPer * 32) dst[kPer * 32 + lane] = src[kPer * 32 + lane];
+        }
     }
     __syncthreads();
 
@@ -776,70 +789,68 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     const bool have = lane < 2 * W && pieces[lane < 2 * W ? lane : 0].r >= 0;
     const int key = have ? pieces[lane].pstart : -1;
     const uint32_t all = __ballot_sync(WSW_FULL_MASK, have);
-    const uint32_t below = all & ((1u << lane) - 1);
+    const uint32_t upto_me = (2u << lane) - 1, below = all & (upto_me >> 1);
     const int key_below = __shfl_sync(WSW_FULL_MASK, key, below ? 31 - __clz(below) : lane);
     const bool is_first = have && !(below && key == key_below);
-    const uint32_t firsts = __ballot_sync(WSW_FULL_MASK, is_first);
+    const uint32_t firsts = __ballot_sync(WSW_FULL_MASK, is_first), later = firsts & ~upto_me;
     const int pairs = __popc(firsts);
     const bool open = is_first && !(key >= b && key + pieces[lane < 2 * W ? lane : 0].nt <= e);
     const uint32_t open_set = __ballot_sync(WSW_FULL_MASK, open);  // pairs shared with other CTAs: at most two
+    const int my_first = 31 - __clz((firsts & upto_me) | 1u), my_pair = __popc(firsts & upto_me) - 1;
+    const uint32_t set = all & ~((1u << my_first) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : 0xffffffffu);
+    const int my_last = set ? 31 - __clz(set) : lane;  // of this lane's pair
     if (warp == 0 && is_first) {
-        const uint32_t later = lane == 31 ? 0 : firsts & ~((2u << lane) - 1);
-        const int j = __popc(firsts & ((1u << lane) - 1));
-        pair_set[j] = all & ~((1u << lane) - 1) & (later ? (1u << (__ffs(later) - 1)) - 1 : 0xffffffffu);
-        pair_first[j] = lane;
+        pair_set[my_pair] = set;
+        pair_first[my_pair] = lane;
     }
-    __syncthreads();
-    for (int u = tid; u < pairs * RT; u += NT) {
-        const int j = u / RT, row = u - j * RT;
-        const uint32_t set = pair_set[j];
-        float2 ml[2 * W];
-        float mx = -INFINITY, l = 0.f;
+    // a warp for each row: maximum and sum along the neighbours of a pair (a lane without a
+    // piece counts as its pair's, with no weight)
+    const int run_key = have ? key : key_below;
+#pragma unroll 1
+    for (int row = warp; row < RT; row += W) {
+        const float2 ml = have ? piece_ml[lane < 2 * W ? lane : 0][row] : make_float2(-INFINITY, 0.f);
+        float mx = ml.x;
 #pragma unroll
-        for (int k = 0; k < 2 * W; ++k) ml[k] = (set >> k) & 1 ? piece_ml[k][row] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int k = 0; k < 2 * W; ++k) mx = fmaxf(mx, ml[k].x);
-#pragma unroll
-        for (int k = 0; k < 2 * W; ++k) {
-            const float f = weight(ml[k].x, mx);
-            if ((set >> k) & 1) wgt[k * RT + row] = f;
-            l = fmaf(ml[k].y, f, l);
+        for (int d = 1; d < 2 * W; d <<= 1) {
+            const float y = __shfl_up_sync(WSW_FULL_MASK, mx, d);
+            const int k = __shfl_up_sync(WSW_FULL_MASK, run_key, d);
+            if (lane >= d && k == run_key) mx = fmaxf(mx, y);
         }
-        joined[j * RT + row] = make_float2(mx, l);
+        mx = __shfl_sync(WSW_FULL_MASK, mx, my_last);
+        const float f = weight(ml.x, mx);
+        float l = ml.y * f;
+#pragma unroll
+        for (int d = 1; d < 2 * W; d <<= 1) {
+            const float y = __shfl_up_sync(WSW_FULL_MASK, l, d);
+            const int k = __shfl_up_sync(WSW_FULL_MASK, run_key, d);
+            if (lane >= d && k == run_key) l += y;
+        }
+        l = __shfl_sync(WSW_FULL_MASK, l, my_last);
+        if (have) wgt[lane * RT + row] = f;
+        if (is_first) joined[my_pair * RT + row] = make_float2(mx, l);
     }
     __syncthreads();
-    // a thread keeps its place in the records and takes the pairs in turn; the records of the
-    // warps' first pieces are in the workspace: all on their way at once
+    // a thread keeps its place in the records and takes the pairs in turn
     constexpr int kUnits = RT * kCols, kTurns = NT / kUnits > 1 ? NT / kUnits : 1;
+#pragma unroll 1
     for (int u = tid; u < kTurns * kUnits; u += NT) {
         const int v = u % kUnits, row = v / kCols, c4 = v % kCols;
-        const int at = row * C::rec + 4 + 4 * c4;
-        float4 xf[W];
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            xf[w] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if ((all >> (2 * w)) & 1)
-                xf[w] = *reinterpret_cast<const float4 *>(a.wrec + static_cast<int64_t>(cta * W + w) * RT * C::rec + at);
-        }
 #pragma unroll 1
         for (int j = u / kUnits; j < pairs; j += kTurns) {
             const Piece pc = pieces[pair_first[j]];
-            const int h = pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
+            const int h = a.passes == 1 ? pc.hp : pc.hp / a.passes, g0 = (pc.hp - h * a.passes) * RT;
             if (g0 + row >= a.group) continue;
-            const uint32_t set = pair_set[j];
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            auto add = [&](float f, float4 x) {
+#pragma unroll 4
+            for (uint32_t m = pair_set[j]; m; m &= m - 1) {
+                const int k = __ffs(m) - 1;
+                const float f = wgt[k * RT + row];
+                const float4 x = *reinterpret_cast<const float4 *>(
+                    reinterpret_cast<const float *>(smem + (k >> 1) * C::ring) + ((k & 1 ? 0 : RT) + row) * C::srec + 4 * c4);
                 s.x = fmaf(x.x, f, s.x);
                 s.y = fmaf(x.y, f, s.y);
                 s.z = fmaf(x.z, f, s.z);
                 s.w = fmaf(x.w, f, s.w);
-            };
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                if ((set >> (2 * w)) & 1) add(wgt[2 * w * RT + row], xf[w]);
-                if ((set >> (2 * w + 1)) & 1)
-                    add(wgt[(2 * w + 1) * RT + row],
-                        *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * C::ring) + at));
             }
             const float2 ml = joined[j * RT + row];
             if (pc.pstart >= b && pc.pstart + pc.nt <= e) {
@@ -848,9 +859,9 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
                 if (c4 == 0 && a.lse) a.lse[head] = lse_of(ml.x, ml.y);
             } else {
-                float *r = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec;
-                *reinterpret_cast<float4 *>(r + at) = s;
-                if (c4 == 0) *reinterpret_cast<float2 *>(r + row * C::rec) = ml;
+                float *r = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec + row * C::rec;
+                *reinterpret_cast<float4 *>(r + 4 + 4 * c4) = s;
+                if (c4 == 0) *reinterpret_cast<float2 *>(r) = ml;
             }
         }
     }
@@ -899,91 +910,66 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 const int c = level == 0 ? c0 + k : k == 0 ? f : (f / kGroup + k) * kGroup;
                 return a.rec + (static_cast<int64_t>(c) * 2 + (c == f)) * RT * C::rec;
             };
-            constexpr int kMost = (kCtas + kGroup - 1) / kGroup + 1;     // groups: a pair may touch one more
-            static_assert(kGroup <= kMost, "records");
-            float *w = reinterpret_cast<float *>(smem);             // [n][RT] maxima, then weights
-            float *lw = w + kMost * RT;                             // [n][RT] sums
-            float *part = lw + kMost * RT;                          // [slices][rows][D]
-            // the records are dealt to slices of the block, whose sums are then added in order;
-            // a thread's are on their way while the weights are made
-            const int units = rows * kCols;
-            const int slices = NT / units > 1 ? NT / units : 1;
+            constexpr int kMost = (kCtas + kGroup - 1) / kGroup + 1;  // groups: a pair may touch one more
+            float *w = reinterpret_cast<float *>(smem);               // [n][RT] maxima, then weights
+            float *lw = w + kMost * RT;                               // [n][RT] sums
+            float2 *jn = reinterpret_cast<float2 *>(lw + kMost * RT);  // [RT] joined (m, l)
+            const int apart = (level == 0 ? 2 : 2 * kGroup) * RT * C::rec;  // from the second record on
+            const float *r0 = record(0), *r1 = record(1);
             for (int u = tid; u < n * RT; u += NT) {
-                const int k = u / RT, row = u - k * RT;
-                if (row >= rows) continue;
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(record(k) + row * C::rec));
+                const int k = u / RT, row = u % RT;
+                const float *r = (k == 0 ? r0 : r1 + (k - 1) * apart) + row * C::rec;
+                const float2 ml = row < rows ? __ldcg(reinterpret_cast<const float2 *>(r)) : make_float2(-INFINITY, 0.f);
                 w[u] = ml.x;
                 lw[u] = ml.y;
             }
-            float4 xa[kMost];
-            const float *second = record(1);  // from the second on the records are evenly spaced
-            const int64_t apart = static_cast<int64_t>(level == 0 ? 2 : 2 * kGroup) * RT * C::rec;
-            auto fetch = [&](int u) {
-                const int sl = u / units, v = u - sl * units;
-                const int at = v / kCols * C::rec + 4 + 4 * (v % kCols);
-                const float *r = second + at + (sl - 1) * apart;
-#pragma unroll
-                for (int i = 0; i < kMost; ++i, r += slices * apart)
-                    if (sl < slices && sl + i * slices < n)
-                        xa[i] = __ldcg(reinterpret_cast<const float4 *>(i == 0 && sl == 0 ? record(0) + at : r));
-            };
 #pragma unroll 1
-            for (int u = tid; u - tid < slices * units; u += NT) {
-                fetch(u);
+            for (int u = tid; u - tid < kUnits; u += NT) {
+                const int row = u / kCols, c4 = u % kCols, at = row * C::rec + 4 + 4 * c4;
+                float4 xa[kMost];  // on their way while the weights are made
+#pragma unroll
+                for (int k = 0; k < kMost; ++k)
+                    if (k < n && row < rows)
+                        xa[k] = __ldcg(reinterpret_cast<const float4 *>(k == 0 ? r0 + at : r1 + at + (k - 1) * apart));
                 if (u == tid) {
                     __syncthreads();
                     if (tid < rows) {
                         float mx = -INFINITY, l = 0.f;
-#pragma unroll 4
+#pragma unroll 1
                         for (int k = 0; k < n; ++k) mx = fmaxf(mx, w[k * RT + tid]);
-#pragma unroll 4
+#pragma unroll 1
                         for (int k = 0; k < n; ++k) {
                             const float g = weight(w[k * RT + tid], mx);
                             w[k * RT + tid] = g;
                             l = fmaf(lw[k * RT + tid], g, l);
                         }
-                        lw[tid] = l;  // record 0's have been read
-                        lw[RT + tid] = mx;
+                        jn[tid] = make_float2(mx, l);
                     }
                     __syncthreads();
                 }
-                const int sl = u / units, row = (u - sl * units) / kCols;
-                if (sl >= slices) continue;
+                if (row >= rows) continue;
                 float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < kMost; ++i) {
-                    const int k = sl + i * slices;
+                for (int k = 0; k < kMost; ++k) {
                     if (k >= n) break;
                     const float g = w[k * RT + row];
-                    s.x = fmaf(xa[i].x, g, s.x);
-                    s.y = fmaf(xa[i].y, g, s.y);
-                    s.z = fmaf(xa[i].z, g, s.z);
-                    s.w = fmaf(xa[i].w, g, s.w);
+                    s.x = fmaf(xa[k].x, g, s.x);
+                    s.y = fmaf(xa[k].y, g, s.y);
+                    s.z = fmaf(xa[k].z, g, s.z);
+                    s.w = fmaf(xa[k].w, g, s.w);
                 }
-                *reinterpret_cast<float4 *>(part + u * 4) = s;
-            }
-            __syncthreads();
-#pragma unroll 1
-            for (int u = tid; u < units; u += NT) {
-                const int row = u / kCols, c4 = u - row * kCols;
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int sl = 0; sl < slices; ++sl) {
-                    const float4 x = *reinterpret_cast<const float4 *>(part + (sl * units + u) * 4);
-                    s.x += x.x;
-                    s.y += x.y;
-                    s.z += x.z;
-                    s.w += x.w;
-                }
-                const float l = lw[row], mx = lw[RT + row];
+                const float2 ml = jn[row];
                 if (final) {
                     const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
                     store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
-                    if (c4 == 0 && a.lse) a.lse[head] = lse_of(mx, l);
+                    if (c4 == 0 && a.lse) a.lse[head] = lse_of(ml.x, ml.y);
                 } else {
-                    float *r = record(0) + row * C::rec;
-                    *reinterpret_cast<float4 *>(r + 4 + 4 * c4) = s;
-                    if (c4 == 0) *reinterpret_cast<float2 *>(r) = make_float2(mx, l);
+                    // the group's record takes the place of its first CTA's: this thread has read
+                    // what it writes, and everyone the (m, l)
+                    float *r = record(0);
+                    *reinterpret_cast<float4 *>(r + at) = s;
+                    if (c4 == 0) *reinterpret_cast<float2 *>(r + row * C::rec) = ml;
                 }
             }
             __syncthreads();
