@@ -12,8 +12,12 @@
 // One launch of one cluster: every CTA scans all the requests into its own shared memory
 // (no exchange, no workspace), a cluster barrier puts every length read before the first
 // write, so that the new lengths may overwrite the old, and the CTAs share the writes.
-// Tokens find their request by binary search in shared memory, four consecutive ones per
-// thread with one search.
+// The sums saturate just beyond what can be served, so they fit in 32 bits whatever the
+// lengths.  A thread takes four consecutive tokens (one while there are threads for all): one binary search in shared memory (a
+// search for each token made 130000 tokens of 1000 requests bound by instructions, 18 us), one
+// table read for each page that they touch.
+#include <atomic>
+
 #include "common.cuh"
 
 namespace wsw {
@@ -33,54 +37,66 @@ struct PlanArgs {
     int requests, n_free, shift, max_pages, tokens;
 };
 
-__device__ __forceinline__ int64_t pages_of(int64_t len, int shift) {
-    return (len + (int64_t(1) << shift) - 1) >> shift;
+// pages of `len` < 2^31 positions
+__device__ __forceinline__ int pages_of(int len, int shift) {
+    return static_cast<int>((static_cast<unsigned>(len) + (1u << shift) - 1) >> shift);
 }
 
-// Exclusive prefix of v over the block's threads, and the block's total.  Every thread
-// calls it; sm holds 33 values.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sm, int64_t *total) {
+// a + b, at most cap < 2^31 (a, b <= cap)
+__device__ __forceinline__ int add_sat(int a, int b, int cap) {
+    const unsigned s = static_cast<unsigned>(a) + static_cast<unsigned>(b);
+    return s < static_cast<unsigned>(cap) ? static_cast<int>(s) : cap;
+}
+
+// Exclusive saturating prefix of v <= cap over the block's threads, and the block's total.
+// Every thread calls it; sm holds 33 values.
+__device__ __forceinline__ int block_scan(int v, int cap, int *sm, int *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int64_t x = v;
+    int x = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(WSW_FULL_MASK, x, d);
-        if (lane >= d) x += y;
+        const int y = __shfl_up_sync(WSW_FULL_MASK, x, d);
+        if (lane >= d) x = add_sat(x, y, cap);
     }
     if (lane == 31) sm[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int64_t w = lane < warps ? sm[lane] : 0;
-        const int64_t own = w;
+        int w = lane < warps ? sm[lane] : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(WSW_FULL_MASK, w, d);
-            if (lane >= d) w += y;
+            const int y = __shfl_up_sync(WSW_FULL_MASK, w, d);
+            if (lane >= d) w = add_sat(w, y, cap);
         }
-        sm[lane] = w - own;
-        if (lane == 31) sm[32] = w;
+        sm[lane + 1] = w;
+        if (lane == 0) sm[0] = 0;
     }
     __syncthreads();
     *total = sm[32];
-    const int64_t before = sm[warp] + x - v;
+    const int x_before = __shfl_up_sync(WSW_FULL_MASK, x, 1);
+    const int before = add_sat(sm[warp], lane ? x_before : 0, cap);
     __syncthreads();  // sm may be reused
     return before;
 }
 
-// The last i with a[i] <= x, for a[0] <= x (a is ascending, n entries).
-__device__ __forceinline__ int find(const int32_t *a, int n, int x) {
-    int lo = 0, hi = n;  // a[lo] <= x < a[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a[mid] <= x) lo = mid;
-        else hi = mid;
-    }
-    return lo;
+// The last i with a[i] <= x[j] for each of N values (a is ascending, n entries, a[0] <= x)
+template <int N>
+__device__ __forceinline__ void find(const int32_t *a, int n, const int (&x)[N], int (&at)[N]) {
+    int top = 1;
+    while (top < n) top <<= 1;
+#pragma unroll
+    for (int j = 0; j < N; ++j) at[j] = 0;
+#pragma unroll 1
+    for (int step = top >> 1; step > 0; step >>= 1)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int i = at[j] + step;
+            if (i < n && a[i] <= x[j]) at[j] = i;
+        }
 }
 
 __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
     extern __shared__ int32_t sm[];
-    __shared__ int64_t scan_sm[33];
+    __shared__ int scan_sm[33];
     __shared__ int used_sm, err_sm;
     const int R = a.requests, tid = threadIdx.x, nt = blockDim.x;
     int32_t *cu = sm;             // [R + 1] tokens before each request, cut at a.tokens
@@ -93,51 +109,52 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
     pdl_wait();
 
     const int head = *a.head;
-    const int64_t avail = head < 0 || head > a.n_free ? 0 : a.n_free - head;
+    const int avail = head < 0 || head > a.n_free ? 0 : a.n_free - head;
     // a thread takes `per` consecutive requests
     const int per = (R + nt - 1) / nt;
     const int r0 = min(tid * per, R), r1 = min(r0 + per, R);
-    int err = 0;
-    int64_t sum = 0;
-    for (int r = r0; r < r1; ++r) {
+    const int tok_cap = a.tokens + 1, page_cap = avail + 1;  // < 2^31: what does not fit any more
+    int err = 0, sum = 0;
+    for (int r = tid; r < R; r += nt) {
         const int s = a.seq[r], n = a.add[r];
         const bool bad = s < 0 || n < 0;
         if (bad) err |= 1;
         len[r] = bad ? -1 : s;
         off[r] = bad ? 0 : n;  // the new length, until the page scan replaces it
-        sum += bad ? 0 : n;
     }
-    int64_t total;
-    int64_t at = block_scan(sum, scan_sm, &total);
+    __syncthreads();
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) sum = add_sat(sum, min(off[r], tok_cap), tok_cap);
+    int total;
+    int at = block_scan(sum, tok_cap, scan_sm, &total);
     sum = 0;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
         const int n = off[r], s = len[r];
-        cu[r] = static_cast<int32_t>(at < a.tokens ? at : a.tokens);
-        at += n;
-        int64_t need = 0;
+        cu[r] = min(at, a.tokens);
+        at = add_sat(at, min(n, tok_cap), tok_cap);
+        int need = 0;
         if (s >= 0) {
-            const int64_t want = pages_of(int64_t(s) + n, a.shift);
-            if (want > a.max_pages || int64_t(s) + n > 0x7fffffff) { err |= 2; len[r] = -1; }
+            if (n > 0x7fffffff - s || pages_of(s + n, a.shift) > a.max_pages) { err |= 2; len[r] = -1; }
             else if (at > a.tokens) { err |= 4; len[r] = -1; }
-            else need = want - pages_of(s, a.shift);
+            else need = pages_of(s + n, a.shift) - pages_of(s, a.shift);
         }
-        off[r] = static_cast<int32_t>(need);  // at most max_pages
-        sum += need;
+        off[r] = need;  // at most max_pages
+        sum = add_sat(sum, min(need, page_cap), page_cap);
     }
-    if (tid == 0) cu[R] = static_cast<int32_t>(total < a.tokens ? total : a.tokens);
-    int64_t before = block_scan(sum, scan_sm, &total), used = 0;
+    if (tid == 0) cu[R] = min(total, a.tokens);
+    int before = block_scan(sum, page_cap, scan_sm, &total), used = 0;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-        const int need = off[r];
+        const int need = min(off[r], page_cap), after = add_sat(before, need, page_cap);
         if (need > 0) {
-            if (before + need > avail) { err |= 8; len[r] = -1; }
-            else used = before + need;
+            if (after > avail) { err |= 8; len[r] = -1; }
+            else used = after;
         }
-        // past the end of the free list the exact offset does not matter
-        off[r] = static_cast<int32_t>(before < 0x7fffffff ? before : 0x7fffffff);
-        before += need;
+        off[r] = before;
+        before = after;
     }
-    if (tid == 0) off[R] = 0x7fffffff;
-    if (used > 0) atomicMax(&used_sm, static_cast<int>(used));  // served requests come first
+    if (used > 0) atomicMax(&used_sm, used);  // served requests come first
     if (err) atomicOr(&err_sm, err);
     __syncthreads();
     if (ncta > 1) {  // every CTA of the cluster has read its lengths
@@ -159,43 +176,80 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
         if (len[r] >= 0) a.len_out[r] = len[r] + (cu[r + 1] - cu[r]);
         else if (a.len_out != a.seq) a.len_out[r] = a.seq[r];
     }
-    for (int i = first; i < granted; i += step) {
-        const int r = find(off, R, i);
-        const int64_t j = pages_of(len[r], a.shift) + (i - off[r]);
-        a.table[r * a.table_stride + j] = a.free_pages[head + i];
+    // four places of the thread at a time, their searches and reads in flight together
+    const int rounds = (granted + 4 * step - 1) / (4 * step);
+#pragma unroll 1
+    for (int k = 0; k < rounds; ++k) {
+        int i[4], r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) i[j] = min(first + (4 * k + j) * step, granted - 1);  // the last one again
+        find(off, R, i, r);
+        int32_t page[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) page[j] = a.free_pages[head + i[j]];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            a.table[r[j] * a.table_stride + pages_of(len[r[j]], a.shift) + (i[j] - off[r[j]])] = page[j];
     }
     const int filled = cu[R];
-    for (int64_t t0 = int64_t(first) * 4; t0 < a.tokens; t0 += int64_t(step) * 4) {
-        int32_t pos[4];
+    const int group = a.tokens > step ? 4 : 1;
+    const bool wide = group == 4 && ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0;
+#pragma unroll 1
+    for (int64_t base = group * static_cast<int64_t>(first); base < a.tokens; base += group * static_cast<int64_t>(step)) {
+        const int t0 = static_cast<int>(base);
+        const int x[1] = {t0};
+        int at0[1];
+        find(cu, R > 0 ? R : 1, x, at0);
+        int r = at0[0], end = t0 < filled ? cu[r + 1] : 0, page = -1, page_key = -1;
+        int pos[4];
         int64_t slot[4];
-        int r = t0 < filled ? find(cu, R, static_cast<int>(t0)) : R;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t t = t0 + i;
+            const int t = t0 + i;
             pos[i] = -1;
             slot[i] = -1;
-            if (t >= filled) continue;
-            while (t >= cu[r + 1]) ++r;  // cu[R] = filled > t
-            if (len[r] < 0) continue;
-            const int p = len[r] + static_cast<int>(t - cu[r]);
-            const int have = static_cast<int>(pages_of(len[r], a.shift)), j = p >> a.shift;
-            const int page = j < have ? a.table[r * a.table_stride + j] : a.free_pages[head + off[r] + (j - have)];
-            pos[i] = p;
-            if (page >= 0) slot[i] = (int64_t(page) << a.shift) + (p & ((1 << a.shift) - 1));
+            if (i >= group || t >= filled) continue;
+            while (t >= end) {  // cu[R] = filled > t
+                end = cu[++r + 1];
+                page_key = -1;
+            }
+            const int s = len[r];
+            if (s < 0) continue;
+            pos[i] = s + (t - cu[r]);
+            const int q = pos[i] >> a.shift;
+            if (q != page_key) {
+                const int have = pages_of(s, a.shift);
+                page = q < have ? a.table[r * a.table_stride + q] : a.free_pages[head + off[r] + (q - have)];
+                page_key = q;
+            }
+            if (page >= 0) slot[i] = (int64_t(page) << a.shift) + (pos[i] & ((1 << a.shift) - 1));
         }
-        if (t0 + 4 <= a.tokens && ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0) {
+        if (wide && t0 + 4 <= a.tokens) {
             *reinterpret_cast<int4 *>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
             reinterpret_cast<longlong2 *>(a.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
             reinterpret_cast<longlong2 *>(a.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (t0 + i < a.tokens) {
+                if (i < group && t0 + i < a.tokens) {
                     a.positions[t0 + i] = pos[i];
                     a.slots[t0 + i] = slot[i];
                 }
         }
     }
+}
+
+// More than eight CTAs in a cluster are an option of the kernel, set once per device.
+cudaError_t cluster_of_16(const void *kernel) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load() & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
 }
 
 }  // namespace
@@ -216,7 +270,7 @@ extern "C" int wsw_kv_page_plan(const int32_t *seq_len, const int32_t *new_len, 
         return WSW_ERR_INVALID_ARG;
     if (requests > 0 && (!seq_len || !new_len || !len_out || (max_pages > 0 && !table))) return WSW_ERR_INVALID_ARG;
     constexpr int64_t lim = int64_t(1) << 31;
-    if (requests > kMaxRequests || n_free >= lim || tokens >= lim || max_pages >= lim || page_size > 65536 ||
+    if (requests > kMaxRequests || tokens >= lim - 1 || n_free >= lim - 1 || max_pages >= lim || page_size > 65536 ||
         (page_size & (page_size - 1)))
         return WSW_ERR_UNSUPPORTED;
     const uintptr_t al = reinterpret_cast<uintptr_t>(seq_len) | reinterpret_cast<uintptr_t>(new_len) |
@@ -242,8 +296,13 @@ extern "C" int wsw_kv_page_plan(const int32_t *seq_len, const int32_t *new_len, 
     if (e != cudaSuccess) return WSW_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    const unsigned ncta = tokens > 8192 ? 8 : 1;
-    const int64_t want = requests > (tokens + 3) / 4 ? requests : (tokens + 3) / 4;
+    // one CTA while its threads see few tokens each, else the largest cluster
+    const unsigned ncta = tokens > 2048 ? 16 : 1;
+    if (ncta > 8) {
+        e = cluster_of_16(reinterpret_cast<const void *>(kv_plan_kernel));
+        if (e != cudaSuccess) return WSW_ERR_CUDA;
+    }
+    const int64_t want = requests > tokens / ncta ? requests : tokens / ncta;
     cfg.gridDim = dim3(ncta);
     cfg.blockDim = dim3(want > 512 ? kThreads : want > 128 ? 512 : 128);
     cfg.dynamicSmemBytes = smem;
