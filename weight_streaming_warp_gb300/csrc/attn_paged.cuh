@@ -6,11 +6,11 @@
 // Bound: every seen K and V byte once (2 head_dim values per position and KV head) against
 // 2 * group multiply-adds per value; HBM bandwidth for any group up to 16.  So the layout of
 // the work is about keeping loads in flight on every SM whatever the requests' lengths:
-//  * One list of tiles.  A tile is 16 positions of one pair (request, KV head); the tiles of
+//  * One list of tiles.  A tile is 16 (q8_0: 32) positions of one pair (request, KV head); the tiles of
 //    all pairs, in order, are cut into equal runs for 152 CTAs and those into equal runs for
 //    their warps.  Nothing is launched per request and no SM waits for a long one; lengths are
 //    read on the device, each CTA scanning them once.  A cut that falls into a pair of at most
-//    kWhole tiles moves to the nearer end of it: sharing a pair between CTAs costs 4 us at its
+//    kWhole positions moves to the nearer end of it: sharing a pair between CTAs costs 4 us at its
 //    end, as much as so many tiles.
 //  * Each warp streams its run through a private ring of shared-memory stages with cp.async,
 //    across pair boundaries without a drain, and keeps its own softmax (running maximum, sum,
@@ -19,14 +19,15 @@
 //    (m, l, sums) records, the CTA joins its own, and when a pair spans CTAs the last of each
 //    group of kGroup CTAs to arrive (a counter in the workspace) joins the group's records, and
 //    the last group's CTA the groups', always in tile order, so that results do not depend on
-//    timing.  (One CTA joining 38 records of eight rows took 7 us, 147 records 15 us: 42 bytes
-//    a nanosecond of one SM's loads.)  A CTA has at most two pairs that it shares with others.
+//    timing.  (One CTA joining 147 records of eight rows took 15 us: 42 bytes a nanosecond of
+//    one SM's loads.)  A CTA has at most two pairs that it shares with others.
 //
 // Products on m16n8k16 tensor-core tiles with fp32 sums.  Up to eight query heads of a KV head
 // share a 16-row operand as high parts (rows 0..7) and residuals (8..15) of q and of the
 // weights; 9 to 16 take 16 rows and a second product for the residuals; more take several
-// passes over the pair.  The weights are scaled by 2^kShift: their residuals stay above
-// binary16's subnormals.  q8_0 rows stay codes in shared memory and become binary16(scale *
+// passes over the pair.  The maximum in use is raised, and the sums rescaled, only when a tile
+// exceeds it by more than kLazy; the weights, then up to 2^(kLazy + kShift), stay in binary16's
+// range and their residuals above its subnormals.  q8_0 rows stay codes in shared memory and become binary16(scale *
 // code) in registers, the value the one-pass dequantizer writes.
 #pragma once
 
@@ -38,11 +39,11 @@
 namespace wsw {
 namespace paged {
 
-constexpr int kTile = 16;      // positions per tile
-constexpr int kWhole = 32;     // pairs of up to so many tiles stay in one CTA
+constexpr int kWhole = 512;    // pairs of up to so many positions stay in one CTA
+constexpr float kLazy = 8.f;   // log2: the running maximum may lag by so much
 constexpr int kGroup = 12;     // CTAs whose records are joined first
 constexpr int kCtas = 152;     // runs of the tile list: one CTA per SM of a 152-SM part
-constexpr float kShift = 8.f;  // log2 of the weights' scale
+constexpr float kShift = 4.f;  // log2 of the weights' scale
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kSmemMax = 226 * 1024;
 
@@ -72,13 +73,18 @@ struct Args {
 template <int CT, int D, int RT>
 struct Cfg {
     static constexpr bool q8 = CT == WSW_Q8_0;
+    // q8_0 is bound by the instructions that turn codes into values: tiles of 32 positions share
+    // the bookkeeping and the softmax's reductions among more of them, and the smaller rows
+    // leave room for 12 warps (32 x 32768 positions, group 8: 16-position tiles 150 us, 32
+    // with 8, 10, 12 warps 126, 147, 124 us)
     static constexpr int warps = D == 256 ? 4 : q8 && RT == 8 ? 12 : 8;
     static constexpr int threads = warps * 32;
     static constexpr int row_bytes = q8 ? D : 2 * D;
     static constexpr int pieces = row_bytes / 16;      // 16-byte pieces of a row
     static constexpr int scale_bytes = q8 ? D / 16 : 0;
-    static constexpr int kv_bytes = kTile * row_bytes;  // K (or V) rows of a tile
-    static constexpr int stage = 2 * kv_bytes + 2 * kTile * scale_bytes;
+    static constexpr int tile = q8 && D <= 128 ? 32 : 16;           // positions
+    static constexpr int kv_bytes = tile * row_bytes;   // K (or V) rows of a tile
+    static constexpr int stage = 2 * kv_bytes + 2 * tile * scale_bytes;
     static constexpr int ksteps = D / 16;
     static constexpr bool q_smem = D == 256;            // q's high parts: registers if they fit
     static constexpr int qfrag = ksteps * 512;          // bytes of one warp's A fragments
@@ -93,7 +99,7 @@ struct Cfg {
     static constexpr int srec = 2 * RT * (D + 4) * 4 <= ring ? D + 4 : D;
     static_assert(stages >= 2 && 2 * RT * srec * 4 <= ring && ring % 16 == 0, "ring");
     static_assert(2 * warps <= 32 && 3 * 2 * warps * RT * 4 <= 4096 && smem <= kSmemMax + 3072, "joins");
-    static_assert(2 * 14 * RT * 4 + RT * 8 <= warps * ring, "joins");
+    static_assert(40 * RT * 4 + RT * 8 <= warps * ring, "joins");
 };
 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -199,17 +205,20 @@ __device__ __forceinline__ int clipped_len(const Args &a, int r) {
     const int n = a.lens[r];
     return n < 0 ? 0 : n > a.max_len ? a.max_len : n;
 }
+template <int T>
 __device__ __forceinline__ int tiles_of(const Args &a, int len) {
     const int seen = len < a.window ? len : a.window;
-    return seen / kTile + (seen % kTile != 0);
+    return seen / T + (seen % T != 0);
 }
+template <int T>
 __device__ __forceinline__ void set_request(const Args &a, Cursor &c, int r) {
     c.r = r;
     c.len = clipped_len(a, r);
-    c.nt = tiles_of(a, c.len);
+    c.nt = tiles_of<T>(a, c.len);
     c.start = c.len > a.window ? c.len - a.window : 0;
 }
 // The next tile of the list; the caller knows that there is one.
+template <int T>
 __device__ __forceinline__ void advance(const Args &a, Cursor &c) {
     ++c.g;
     if (++c.t < c.nt) return;
@@ -217,14 +226,14 @@ __device__ __forceinline__ void advance(const Args &a, Cursor &c) {
     if (++c.hp < a.kv.heads * a.passes) return;
     c.hp = 0;
     int r = c.r;
-    do set_request(a, c, ++r);
+    do set_request<T>(a, c, ++r);
     while (c.nt == 0 && r + 1 < a.requests);
 }
 
 template <int CT, int D, int RT>
 __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(const __grid_constant__ Args a) {
     using C = Cfg<CT, D, RT>;
-    constexpr int W = C::warps, NT = C::threads;
+    constexpr int W = C::warps, NT = C::threads, T = C::tile;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int scan[W];
     struct Place {
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     for (int r = r0; r < r1; ++r) {
         const int n = a.lens[r], clipped = min(max(n, 0), a.max_len);
         cut_len |= n != clipped;
-        const int nt = tiles_of(a, clipped);
+        const int nt = tiles_of<T>(a, clipped);
         if (r == r0) nt0 = nt;
         mine += nt * HP;
     }
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 #pragma unroll 1
         while (s >= at + nt * HP) {
             at += nt * HP;
-            nt = tiles_of(a, clipped_len(a, ++r));
+            nt = tiles_of<T>(a, clipped_len(a, ++r));
         }
         p = Place{r, s - at, nt};
     };
@@ -289,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     locate(raw_e, cut[1]);
     __syncthreads();
     auto snapped = [&](int s, const Place &p) {
-        if (s >= total || s == 0 || p.nt > kWhole) return s;
+        if (s >= total || s == 0 || p.nt > kWhole / T) return s;
         const int t = p.off % p.nt;
         return s - t + (2 * t > p.nt ? p.nt : 0);
     };
@@ -325,7 +334,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     if (todo > 0) {
         Cursor uc;  // the tile in use
         const Place at_first = place[warp];
-        set_request(a, uc, at_first.req);
+        set_request<T>(a, uc, at_first.req);
         uc.g = wb;
         uc.hp = at_first.off / uc.nt;
         uc.t = at_first.off - uc.hp * uc.nt;
@@ -340,7 +349,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             return i <= (ic.len - 1) >> a.kv.page_shift ? a.table[ic.r * a.table_stride + i] : -1;
         };
         auto look_up = [&]() {
-            const int i0 = (ic.start + ic.t * kTile) >> a.kv.page_shift;
+            const int i0 = (ic.start + ic.t * T) >> a.kv.page_shift;
             if (ic.r != wreq || i0 < wbase || i0 >= wbase + 64) {
                 wreq = ic.r;
                 wbase = i0;
@@ -357,13 +366,14 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         auto issue = [&]() {
             if (to_issue > 0) {
                 --to_issue;
-                const int p0 = ic.start + ic.t * kTile, p = p0 + (lane & 15);
+                constexpr uint32_t kAll = T == 32 ? 0xffffffffu : (1u << (T & 31)) - 1;
+                const int p0 = ic.start + ic.t * T, p = p0 + (lane & (T - 1));
                 const int rel = (p >> a.kv.page_shift) - wbase;
                 const int pg0 = __shfl_sync(WSW_FULL_MASK, win0, rel & 31), pg1 = __shfl_sync(WSW_FULL_MASK, win1, rel & 31);
                 const int page = rel < 32 ? pg0 : pg1;
                 const bool in = p < ic.len;
                 const bool ok = in && static_cast<unsigned>(page) < static_cast<unsigned>(a.kv.num_pages);
-                const uint32_t valid = __ballot_sync(WSW_FULL_MASK, ok) & 0xffffu;
+                const uint32_t valid = __ballot_sync(WSW_FULL_MASK, ok) & kAll;
                 if (in && !ok && a.err) atomicOr(a.err, 1);
                 const int64_t at = ok ? page * a.kv.page_stride + (p & page_mask) * a.kv.pos_stride : 0;
                 const int h = a.passes == 1 ? ic.hp : ic.hp / a.passes;
@@ -375,12 +385,12 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                     const int sw = C::pieces >= 8 ? c ^ (row & 7) : c ^ ((row >> 1) & 3);
                     return stg + row * C::row_bytes + sw * 16;
                 };
-                if (valid == 0xffffu && (p0 & page_mask) + kTile - 1 <= page_mask) {
+                if (valid == kAll && (p0 & page_mask) + T - 1 <= page_mask) {
                     // the whole tile in one page: its rows are pos_stride apart
                     const int64_t o = __shfl_sync(WSW_FULL_MASK, at, 0) + rr * a.kv.pos_stride + c * 16;
                     const unsigned char *kp = kb + o, *vp = vb + o;
 #pragma unroll
-                    for (int i = 0; i < kTile / kRows; ++i) {
+                    for (int i = 0; i < T / kRows; ++i) {
                         const uint32_t dst = swizzled(i * kRows + rr);
                         cp16(dst, kp, true);
                         cp16(dst + C::kv_bytes, vp, true);
@@ -389,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                     }
                 } else {
 #pragma unroll 2
-                    for (int i = 0; i < kTile / kRows; ++i) {
+                    for (int i = 0; i < T / kRows; ++i) {
                         const int row = i * kRows + rr;
                         const int64_t o = __shfl_sync(WSW_FULL_MASK, at, row);
                         const bool v = (valid >> row) & 1;
@@ -398,7 +408,13 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                         cp16(dst + C::kv_bytes, vb + o + c * 16, v);
                     }
                 }
-                if constexpr (C::q8) {  // lanes 0..15: K scales, 16..31: V scales
+                if constexpr (C::q8 && T == 32) {  // a lane for each position's scales
+                    const int64_t dat = ok ? page * a.kv.d_page_stride + (p & page_mask) * a.kv.d_pos_stride +
+                                                 h * a.kv.d_head_stride : 0;
+                    const uint32_t dst = stg + 2 * C::kv_bytes + lane * C::scale_bytes;
+                    cp_small<C::scale_bytes>(dst, a.kv.kd + dat, ok);
+                    cp_small<C::scale_bytes>(dst + T * C::scale_bytes, a.kv.vd + dat, ok);
+                } else if constexpr (C::q8) {  // lanes 0..15: K scales, 16..31: V scales
                     const int64_t dat = ok ? page * a.kv.d_page_stride + (p & page_mask) * a.kv.d_pos_stride +
                                                  h * a.kv.d_head_stride : 0;
                     cp_small<C::scale_bytes>(stg + 2 * C::kv_bytes + lane * C::scale_bytes,
@@ -407,7 +423,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 if (lane == 0) seen_mask[warp][ist] = valid;
                 if (++ist == C::stages) ist = 0;
                 if (to_issue > 0) {
-                    advance(a, ic);
+                    advance<T>(a, ic);
                     look_up();
                     if (ic.t == 0) {  // a new pair: its queries on their way to L1
                         const int hn = a.passes == 1 ? ic.hp : ic.hp / a.passes, gn = (ic.hp - hn * a.passes) * RT;
@@ -527,11 +543,12 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             const uint32_t valid = seen_mask[warp][rst];
             if (++rst == C::stages) rst = 0;
 
-            // ---- scores of 16 positions, two blocks of 8
-            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            float sd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // the odd steps: a second chain
-            auto score = [&](int kt, const uint32_t (&kb)[4]) {  // kb: block 0's two registers, block 1's
-                uint32_t qf[4];
+            // ---- scores, in blocks of 8 positions
+            constexpr int NB = T / 8;
+            float sc[NB][4];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+            auto q_frag = [&](int kt, uint32_t (&qf)[4]) {
                 if constexpr (C::q_smem) {
                     const uint4 u = q_hi_sm[kt * 32 + lane];
                     qf[0] = u.x; qf[1] = u.y; qf[2] = u.z; qf[3] = u.w;
@@ -539,76 +556,79 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 #pragma unroll
                     for (int i = 0; i < 4; ++i) qf[i] = qa[kt][i];
                 }
-                float (&s0)[4] = kt & 1 ? sd[0] : sc[0], (&s1)[4] = kt & 1 ? sd[1] : sc[1];
-                mma<CT>(s0, qf, kb[0], kb[1]);
-                mma<CT>(s1, qf, kb[2], kb[3]);
+            };
+            // d += q_kt K^T for one block, its two registers b0 and b1
+            auto score = [&](float (&d)[4], int kt, uint32_t b0, uint32_t b1) {
+                uint32_t qf[4];
+                q_frag(kt, qf);
+                mma<CT>(d, qf, b0, b1);
                 if constexpr (RT == 16) {
                     if (q_lo) {
                         const uint4 u = q_lo_sm[kt * 32 + lane];
                         const uint32_t ql[4] = {u.x, u.y, u.z, u.w};
-                        mma<CT>(s0, ql, kb[0], kb[1]);
-                        mma<CT>(s1, ql, kb[2], kb[3]);
+                        mma<CT>(d, ql, b0, b1);
                     }
                 }
             };
             if constexpr (!C::q8) {
+                static_assert(C::q8 || NB == 2, "blocks");
+                float sd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // the odd steps: a second chain
                 const int pos = 8 * (mi >> 1) + mr;
 #pragma unroll
                 for (int kt = 0; kt < C::ksteps; ++kt) {
                     uint32_t kb[4];
                     const int ch = 2 * kt + (mi & 1);
                     ldsm4(kb, stg + pos * C::row_bytes + ((ch ^ (pos & 7)) << 4));
-                    score(kt, kb);
+                    score(kt & 1 ? sd[0] : sc[0], kt, kb[0], kb[1]);
+                    score(kt & 1 ? sd[1] : sc[1], kt, kb[2], kb[3]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sc[0][i] += sd[0][i];
+                    sc[1][i] += sd[1][i];
                 }
             } else {
                 constexpr int kVec = D / 64;  // 16-byte pieces per lane and row
-                uint32_t w[2][4 * kVec];
-                __half2 ds[2][D == 256 ? 2 : 1];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < NB; ++n) {
+                    uint32_t w[4 * kVec];
+                    __half2 ds[D == 256 ? 2 : 1];
                     const int row = 8 * n + gq;
 #pragma unroll
                     for (int i = 0; i < kVec; ++i) {
                         const int ch = tq * kVec + i;
                         const int sw = C::pieces >= 8 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
                         const uint4 u = *reinterpret_cast<const uint4 *>(stg_p + row * C::row_bytes + sw * 16);
-                        w[n][4 * i] = u.x ^ 0x80808080u;
-                        w[n][4 * i + 1] = u.y ^ 0x80808080u;
-                        w[n][4 * i + 2] = u.z ^ 0x80808080u;
-                        w[n][4 * i + 3] = u.w ^ 0x80808080u;
+                        w[4 * i] = u.x ^ 0x80808080u;
+                        w[4 * i + 1] = u.y ^ 0x80808080u;
+                        w[4 * i + 2] = u.z ^ 0x80808080u;
+                        w[4 * i + 3] = u.w ^ 0x80808080u;
                     }
                     const __half *sp = reinterpret_cast<const __half *>(stg_p + 2 * C::kv_bytes + row * C::scale_bytes);
-                    if constexpr (D == 64) ds[n][0] = __half2half2(sp[tq >> 1]);
-                    else if constexpr (D == 128) ds[n][0] = __half2half2(sp[tq]);
+                    if constexpr (D == 64) ds[0] = __half2half2(sp[tq >> 1]);
+                    else if constexpr (D == 128) ds[0] = __half2half2(sp[tq]);
                     else {
-                        ds[n][0] = __half2half2(sp[2 * tq]);
-                        ds[n][1] = __half2half2(sp[2 * tq + 1]);
+                        ds[0] = __half2half2(sp[2 * tq]);
+                        ds[1] = __half2half2(sp[2 * tq + 1]);
+                    }
+#pragma unroll
+                    for (int kt = 0; kt < C::ksteps; ++kt) {
+                        const int bl = D == 256 ? kt >> 3 : 0;
+                        score(sc[n], kt, dequant2(w[kt], 0x4140, ds[bl]), dequant2(w[kt], 0x4342, ds[bl]));
                     }
                 }
-#pragma unroll
-                for (int kt = 0; kt < C::ksteps; ++kt) {
-                    const int bl = D == 256 ? kt >> 3 : 0;
-                    const uint32_t kb[4] = {dequant2(w[0][kt], 0x4140, ds[0][bl]), dequant2(w[0][kt], 0x4342, ds[0][bl]),
-                                            dequant2(w[1][kt], 0x4140, ds[1][bl]), dequant2(w[1][kt], 0x4342, ds[1][bl])};
-                    score(kt, kb);
-                }
-            }
-
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sc[0][i] += sd[0][i];
-                sc[1][i] += sd[1][i];
             }
 
             // ---- softmax: lane (gq, tq) holds positions 8 n + 2 tq + {0, 1} of rows gq, gq + 8
-            const int p0 = uc.start + uc.t * kTile;
-            uint32_t ph[4], pl[4];
+            const int p0 = uc.start + uc.t * T;
+            uint32_t ph[NB / 2][4], pl[NB / 2][4];
             float al[RT / 8];
+            bool raised = false;
 #pragma unroll
             for (int y = 0; y < RT / 8; ++y) {
-                float s[4];
+                float s[2 * NB];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int pi = 8 * n + 2 * tq + j;
@@ -617,26 +637,27 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                         if (a.slopes) x = fmaf(-slope[y], static_cast<float>(uc.len - 1 - (p0 + pi)), x);
                         s[2 * n + j] = (valid >> pi) & 1 ? x : -INFINITY;
                     }
-                float mt = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+                float mt = s[0];
+#pragma unroll
+                for (int i = 1; i < 2 * NB; ++i) mt = fmaxf(mt, s[i]);
                 mt = fmaxf(mt, __shfl_xor_sync(WSW_FULL_MASK, mt, 1));
                 mt = fmaxf(mt, __shfl_xor_sync(WSW_FULL_MASK, mt, 2));
-                const float mn = fmaxf(m[y], mt);
-                const bool none = mn == -INFINITY;
-                al[y] = none ? 1.f : ex2(m[y] - mn);
-                m[y] = mn;
-                float p[4];
+                const bool raise = mt > m[y] + kLazy;  // m = -inf: by anything visible
+                al[y] = raise ? ex2(m[y] - mt) : 1.f;
+                raised |= raise;
+                if (raise) m[y] = mt;
+                const float ref = m[y] == -INFINITY ? 0.f : m[y] - kShift;  // nothing seen yet: all weights 0
+                float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = none ? 0.f : ex2(s[i] - (mn - kShift));
-                l[y] = l[y] * al[y] + ((p[0] + p[1]) + (p[2] + p[3]));
-                if constexpr (RT == 8) {
-                    split<CT>(p[0], p[1], ph[0], ph[1]);
-                    split<CT>(p[2], p[3], ph[2], ph[3]);
-                } else {
-                    split<CT>(p[0], p[1], ph[y], pl[y]);
-                    split<CT>(p[2], p[3], ph[2 + y], pl[2 + y]);
+                for (int n = 0; n < NB; ++n) {
+                    const float p_0 = ex2(s[2 * n] - ref), p_1 = ex2(s[2 * n + 1] - ref);
+                    sum += p_0 + p_1;
+                    if constexpr (RT == 8) split<CT>(p_0, p_1, ph[n / 2][2 * (n & 1)], ph[n / 2][2 * (n & 1) + 1]);
+                    else split<CT>(p_0, p_1, ph[n / 2][2 * (n & 1) + y], pl[n / 2][2 * (n & 1) + y]);
                 }
+                l[y] = fmaf(l[y], al[y], sum);
             }
-            if (__any_sync(WSW_FULL_MASK, al[0] != 1.f || al[RT / 8 - 1] != 1.f)) {
+            if (__any_sync(WSW_FULL_MASK, raised)) {
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n) {
                     o[n][0] *= al[0];
@@ -646,54 +667,52 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 }
             }
 
-            // ---- value sums
-            auto add = [&](int n, uint32_t b0, uint32_t b1) {
-                mma<CT>(o[n], ph, b0, b1);
-                if constexpr (RT == 16) mma<CT>(o[n], pl, b0, b1);
-            };
-            const int vpos = 8 * (mi & 1) + mr;
-            if constexpr (!C::q8) {
+            // ---- value sums, 16 positions at a time
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    uint32_t vb[4];
-                    const int ch = 2 * j + (mi >> 1);
-                    ldsm4_t(vb, stg + C::kv_bytes + vpos * C::row_bytes + ((ch ^ (vpos & 7)) << 4));
-                    add(2 * j, vb[0], vb[1]);
-                    add(2 * j + 1, vb[2], vb[3]);
-                }
-            } else {
-                // a transposed 16-bit matrix element is a pair of codes: dimensions 16 c + 2 i and
-                // + 1 of one position.  Bytes 0 and 2 of a register are the even dimension at
-                // positions 2 tq and 2 tq + 1, bytes 1 and 3 the odd one: two column blocks.
-                const unsigned char *vs = stg_p + 2 * C::kv_bytes + kTile * C::scale_bytes;
-                constexpr int kBl = D / 32;
-                __half dv[4][kBl];  // scales of positions 2 tq, 2 tq + 1, 8 + 2 tq, 9 + 2 tq
+            for (int t16 = 0; t16 < T / 16; ++t16) {
+                auto add = [&](int n, uint32_t b0, uint32_t b1) {
+                    mma<CT>(o[n], ph[t16], b0, b1);
+                    if constexpr (RT == 16) mma<CT>(o[n], pl[t16], b0, b1);
+                };
+                const int vpos = 16 * t16 + 8 * (mi & 1) + mr;
+                if constexpr (!C::q8) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 8 * (i >> 1) + 2 * tq + (i & 1);
-                    const __half *sp = reinterpret_cast<const __half *>(vs + row * C::scale_bytes);
-                    if constexpr (kBl == 2) {
-                        const uint32_t u = *reinterpret_cast<const uint32_t *>(sp);
-                        *reinterpret_cast<uint32_t *>(dv[i]) = u;
-                    } else if constexpr (kBl == 4) {
-                        *reinterpret_cast<uint2 *>(dv[i]) = *reinterpret_cast<const uint2 *>(sp);
-                    } else {
-                        *reinterpret_cast<uint4 *>(dv[i]) = *reinterpret_cast<const uint4 *>(sp);
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t vb[4];
+                        const int ch = 2 * j + (mi >> 1);
+                        ldsm4_t(vb, stg + C::kv_bytes + vpos * C::row_bytes + ((ch ^ (vpos & 7)) << 4));
+                        add(2 * j, vb[0], vb[1]);
+                        add(2 * j + 1, vb[2], vb[3]);
                     }
-                }
+                } else {
+                    // a transposed 16-bit matrix element is a pair of codes: dimensions 16 c + 2 i and
+                    // + 1 of one position.  Bytes 0 and 2 of a register are the even dimension at
+                    // positions 2 tq and 2 tq + 1, bytes 1 and 3 the odd one: two column blocks.
+                    const unsigned char *vs = stg_p + 2 * C::kv_bytes + T * C::scale_bytes;
+                    constexpr int kBl = D / 32;
+                    __half dv[4][kBl];  // scales of positions 2 tq, 2 tq + 1, 8 + 2 tq, 9 + 2 tq
 #pragma unroll
-                for (int j = 0; j < kBl; ++j) {
-                    uint32_t vb[4];
-                    const int ch = 2 * j + (mi >> 1);
-                    const int sw = C::pieces >= 8 ? ch ^ (vpos & 7) : ch ^ ((vpos >> 1) & 3);
-                    ldsm4_t(vb, stg + C::kv_bytes + vpos * C::row_bytes + (sw << 4));
-                    const __half2 d0 = __halves2half2(dv[0][j], dv[1][j]), d1 = __halves2half2(dv[2][j], dv[3][j]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = 16 * t16 + 8 * (i >> 1) + 2 * tq + (i & 1);
+                        const __half *sp = reinterpret_cast<const __half *>(vs + row * C::scale_bytes);
+                        if constexpr (kBl == 2) *reinterpret_cast<uint32_t *>(dv[i]) = *reinterpret_cast<const uint32_t *>(sp);
+                        else if constexpr (kBl == 4) *reinterpret_cast<uint2 *>(dv[i]) = *reinterpret_cast<const uint2 *>(sp);
+                        else *reinterpret_cast<uint4 *>(dv[i]) = *reinterpret_cast<const uint4 *>(sp);
+                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) vb[i] ^= 0x80808080u;
+                    for (int j = 0; j < kBl; ++j) {
+                        uint32_t vb[4];
+                        const int ch = 2 * j + (mi >> 1);
+                        const int sw = C::pieces >= 8 ? ch ^ (vpos & 7) : ch ^ ((vpos >> 1) & 3);
+                        ldsm4_t(vb, stg + C::kv_bytes + vpos * C::row_bytes + (sw << 4));
+                        const __half2 d0 = __halves2half2(dv[0][j], dv[1][j]), d1 = __halves2half2(dv[2][j], dv[3][j]);
 #pragma unroll
-                    for (int pc = 0; pc < 2; ++pc) {
-                        add(4 * j + 2 * pc, dequant2(vb[2 * pc], 0x4240, d0), dequant2(vb[2 * pc + 1], 0x4240, d1));
-                        add(4 * j + 2 * pc + 1, dequant2(vb[2 * pc], 0x4341, d0), dequant2(vb[2 * pc + 1], 0x4341, d1));
+                        for (int i = 0; i < 4; ++i) vb[i] ^= 0x80808080u;
+#pragma unroll
+                        for (int pc = 0; pc < 2; ++pc) {
+                            add(4 * j + 2 * pc, dequant2(vb[2 * pc], 0x4240, d0), dequant2(vb[2 * pc + 1], 0x4240, d1));
+                            add(4 * j + 2 * pc + 1, dequant2(vb[2 * pc], 0x4341, d0), dequant2(vb[2 * pc + 1], 0x4341, d1));
+                        }
                     }
                 }
             }
@@ -762,7 +781,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             }
             if (todo > 1) {
                 // advance() is safe: there is another tile
-                advance(a, uc);
+                advance<T>(a, uc);
             }
         }
         // the first piece's record joins the last one's in the ring
@@ -910,54 +929,55 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 const int c = level == 0 ? c0 + k : k == 0 ? f : (f / kGroup + k) * kGroup;
                 return a.rec + (static_cast<int64_t>(c) * 2 + (c == f)) * RT * C::rec;
             };
-            constexpr int kMost = (kCtas + kGroup - 1) / kGroup + 1;  // groups: a pair may touch one more
-            float *w = reinterpret_cast<float *>(smem);               // [n][RT] maxima, then weights
-            float *lw = w + kMost * RT;                               // [n][RT] sums
-            float2 *jn = reinterpret_cast<float2 *>(lw + kMost * RT);  // [RT] joined (m, l)
+            constexpr int kMost = kGroup > (kCtas + kGroup - 1) / kGroup + 1 ? kGroup : (kCtas + kGroup - 1) / kGroup + 1;
+            static_assert(kMost <= 64, "records");
+            constexpr int kAhead = kMost < 20 ? kMost : 20;  // of a thread's records on their way at once
+            float *w = reinterpret_cast<float *>(smem);                // [kMost][RT] weights
+            float2 *jn = reinterpret_cast<float2 *>(w + kMost * RT);   // [RT] joined (m, l)
             const int apart = (level == 0 ? 2 : 2 * kGroup) * RT * C::rec;  // from the second record on
             const float *r0 = record(0), *r1 = record(1);
-            for (int u = tid; u < n * RT; u += NT) {
-                const int k = u / RT, row = u % RT;
-                const float *r = (k == 0 ? r0 : r1 + (k - 1) * apart) + row * C::rec;
-                const float2 ml = row < rows ? __ldcg(reinterpret_cast<const float2 *>(r)) : make_float2(-INFINITY, 0.f);
-                w[u] = ml.x;
-                lw[u] = ml.y;
-            }
+            auto part = [&](int k, int at) { return (k == 0 ? r0 : r1 + (k - 1) * apart) + at; };
 #pragma unroll 1
             for (int u = tid; u - tid < kUnits; u += NT) {
                 const int row = u / kCols, c4 = u % kCols, at = row * C::rec + 4 + 4 * c4;
-                float4 xa[kMost];  // on their way while the weights are made
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int k0 = 0; k0 < n; k0 += kAhead) {
+                    float4 xa[kAhead];
 #pragma unroll
-                for (int k = 0; k < kMost; ++k)
-                    if (k < n && row < rows)
-                        xa[k] = __ldcg(reinterpret_cast<const float4 *>(k == 0 ? r0 + at : r1 + at + (k - 1) * apart));
-                if (u == tid) {
-                    __syncthreads();
-                    if (tid < rows) {
-                        float mx = -INFINITY, l = 0.f;
+                    for (int k = 0; k < kAhead; ++k)
+                        if (k0 + k < n && row < rows) xa[k] = __ldcg(reinterpret_cast<const float4 *>(part(k0 + k, at)));
+                    if (u == tid && k0 == 0) {  // meanwhile the weights, a warp for each row
 #pragma unroll 1
-                        for (int k = 0; k < n; ++k) mx = fmaxf(mx, w[k * RT + tid]);
-#pragma unroll 1
-                        for (int k = 0; k < n; ++k) {
-                            const float g = weight(w[k * RT + tid], mx);
-                            w[k * RT + tid] = g;
-                            l = fmaf(lw[k * RT + tid], g, l);
+                        for (int wr = warp; wr < rows; wr += W) {
+                            const float2 none = make_float2(-INFINITY, 0.f);
+                            const float2 x = lane < n ? __ldcg(reinterpret_cast<const float2 *>(part(lane, wr * C::rec))) : none;
+                            const float2 y = lane + 32 < n
+                                ? __ldcg(reinterpret_cast<const float2 *>(part(lane + 32, wr * C::rec))) : none;
+                            float mx = fmaxf(x.x, y.x);
+#pragma unroll
+                            for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
+                            const float fx = weight(x.x, mx), fy = weight(y.x, mx);
+                            float l = fmaf(x.y, fx, y.y * fy);
+#pragma unroll
+                            for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(WSW_FULL_MASK, l, d);
+                            if (lane < n) w[lane * RT + wr] = fx;
+                            if (lane + 32 < n) w[(lane + 32) * RT + wr] = fy;
+                            if (lane == 0) jn[wr] = make_float2(mx, l);
                         }
-                        jn[tid] = make_float2(mx, l);
+                        __syncthreads();
                     }
-                    __syncthreads();
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) {
+                        if (k0 + k >= n || row >= rows) break;
+                        const float g = w[(k0 + k) * RT + row];
+                        s.x = fmaf(xa[k].x, g, s.x);
+                        s.y = fmaf(xa[k].y, g, s.y);
+                        s.z = fmaf(xa[k].z, g, s.z);
+                        s.w = fmaf(xa[k].w, g, s.w);
+                    }
                 }
                 if (row >= rows) continue;
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < kMost; ++k) {
-                    if (k >= n) break;
-                    const float g = w[k * RT + row];
-                    s.x = fmaf(xa[k].x, g, s.x);
-                    s.y = fmaf(xa[k].y, g, s.y);
-                    s.z = fmaf(xa[k].z, g, s.z);
-                    s.w = fmaf(xa[k].w, g, s.w);
-                }
                 const float2 ml = jn[row];
                 if (final) {
                     const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
