@@ -79,6 +79,16 @@ __device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]) {
     }
 }
 
+// 4 consecutive values of an aligned row
+template <typename T>
+__device__ __forceinline__ void load4(const T *p, float (&x)[4]) {
+    alignas(16) T t[4];
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(t) = *reinterpret_cast<const uint4 *>(p);
+    else *reinterpret_cast<uint2 *>(t) = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = to_f(t[i]);
+}
+
 __device__ __forceinline__ void store8(float *p, bool vec, const float (&x)[8]) {
     if (vec) {
         reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -183,7 +193,20 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kv_kernel(const RopeArgs a) 
                         x[2 * i] = fmaf(x0, z.x, -x1 * z.y);
                         x[2 * i + 1] = fmaf(x1, z.x, x0 * z.y);
                     }
-                } else {  // the halves do not meet at a multiple of 8: partners one by one
+                } else if ((half & 3) == 0 && a.vec) {  // partners four by four
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int d = d0 + 4 * c;
+                        if (d >= a.rot) break;
+                        const bool lo = d < half;
+                        float y[4];
+                        load4(src + (lo ? d + half : d - half), y);
+                        const float2 *z = w + (lo ? d : d - half);
+                        const float sign = lo ? -1.f : 1.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[4 * c + i] = fmaf(x[4 * c + i], z[i].x, y[i] * (sign * z[i].y));
+                    }
+                } else {  // the halves do not meet at a multiple of 4: partners one by one
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
                         const int d = d0 + i;
