@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) logprobs_ker
         }
         if (!first && ++since < kLook && tile0 + kTile < hi) continue;
         // one answer for the whole block; inside, nobody adds vectors until all have read sm.nvec
-        const bool over = __syncthreads_or(filled > kKeep || (first && k > 8));
+        // (a large k's bound is loose: it is cut after the first of several tiles)
+        const bool over = __syncthreads_or(filled > kKeep || (first && k > 8 && tile0 + 2 * kTile < hi));
         const int group_end = min(tile0 + kTile, hi);
         if (over && sm.nvec > kVecs) {
             // too many: take the values of the tiles since the last look again, in pieces that
@@ -573,12 +574,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) logprobs_ker
         for (int base = 0; base < keys; base += kCap - kMaxTop) {
             const int end = min(base + kCap - kMaxTop, keys);
             const uint64_t floor = base > 0 && sm.n == k ? sm.best[k - 1] : 0;
-            __syncthreads();
-            for (int i = base + tid; i < end; i += kThreads) {
-                const int sp = i / k;
-                const uint64_t key = key_at(sp, i - sp * k);
-                if (key >= thr && key > floor) push(sm, key);
+            constexpr int kEach = (kCap - kMaxTop + kThreads - 1) / kThreads;
+            uint64_t got[kEach];  // a thread's keys, on their way together
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                const int i = base + tid + j * kThreads, sp = i / k;
+                got[j] = i < end ? key_at(sp, i - sp * k) : 0;
             }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kEach; ++j)
+                if (base + tid + j * kThreads < end && got[j] >= thr && got[j] > floor) push(sm, got[j]);
             __syncthreads();
             cut(sm, k);
         }
