@@ -84,9 +84,9 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
     a.cnt = reinterpret_cast<unsigned *>(w);
     a.rec = reinterpret_cast<float *>(w + kCounterBytes);
     a.wrec = a.rec + static_cast<size_t>(kCtas) * 2 * record_bytes(rows, cache->head_dim) / 4;
-    // tiles of the longest possible lists
+    // the longest possible list
     const int64_t seen = a.max_len < a.window ? a.max_len : a.window;
-    const int64_t tiles = requests * cache->heads * a.passes * ((seen + 15) / 16);
+    const int64_t tiles = requests * cache->heads * a.passes * ((seen + 15) / 16 + kPair);
     if (tiles >= lim - 65536) return WSW_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
     DeviceInfo di;
     if (!device_info(&di, &st)) return st;

@@ -11,7 +11,9 @@
 //    their warps.  Nothing is launched per request and no SM waits for a long one; lengths are
 //    read on the device, each CTA scanning them once.  A cut that falls into a pair of at most
 //    kWhole positions moves to the nearer end of it: sharing a pair between CTAs costs 4 us at its
-//    end, as much as so many tiles.
+//    end, as much as so many tiles.  In long lists a pair counts kPair tiles more than it has:
+//    its queries, its end and its last, partial tile cost a warp about as much (256 x 512
+//    positions of 8 heads: the CTAs with the most pairs took 66 us, the median 46).
 //  * Each warp streams its run through a private ring of shared-memory stages with cp.async,
 //    across pair boundaries without a drain, and keeps its own softmax (running maximum, sum,
 //    value sums) in registers: no block barrier until its run ends.
@@ -40,6 +42,7 @@ namespace wsw {
 namespace paged {
 
 constexpr int kWhole = 512;    // pairs of up to so many positions stay in one CTA
+constexpr int kPair = 4;       // tiles that the beginning and end of a pair count for
 constexpr float kLazy = 8.f;   // log2: the running maximum may lag by so much
 constexpr int kGroup = 12;     // CTAs whose records are joined first
 constexpr int kCtas = 152;     // runs of the tile list: one CTA per SM of a 152-SM part
@@ -191,11 +194,11 @@ __device__ __forceinline__ float weight(float m, float mx) { return m == -INFINI
 
 // Where a warp is in the tile list: request, head and pass, tile of the pair.
 struct Cursor {
-    int g;       // index in the list
+    int g;       // its place in the list, in tiles and the pairs' extra counts before them
     int r, hp, t, nt;
     int start, len;  // seen positions are [start, len)
 };
-// A piece of a pair left as a record: the pair, its first tile's index and its tile count.
+// A piece of a pair left as a record: the pair, its first tile's place and its tile count.
 struct Piece {
     int pstart;
     int r, hp, nt;  // r = -1: none
@@ -219,10 +222,11 @@ __device__ __forceinline__ void set_request(const Args &a, Cursor &c, int r) {
 }
 // The next tile of the list; the caller knows that there is one.
 template <int T>
-__device__ __forceinline__ void advance(const Args &a, Cursor &c) {
+__device__ __forceinline__ void advance(const Args &a, Cursor &c, int extra) {
     ++c.g;
     if (++c.t < c.nt) return;
     c.t = 0;
+    c.g += extra;
     if (++c.hp < a.kv.heads * a.passes) return;
     c.hp = 0;
     int r = c.r;
@@ -235,9 +239,9 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     using C = Cfg<CT, D, RT>;
     constexpr int W = C::warps, NT = C::threads, T = C::tile;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int scan[W];
+    __shared__ int2 scan[W];
     struct Place {
-        int req, off, nt;  // a tile's request, its index there, the tiles of a pair there
+        int req, off, nt;  // a request, the place in its part of the list, its pairs' tiles
     };
     __shared__ Place cut[2], place[W];  // of the CTA's cuts, of the warps' first tiles
     __shared__ Piece pieces[2 * W];
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     // places the runs
     const int per = (a.requests + NT - 1) / NT;
     const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
-    int mine = 0, nt0 = 0;  // nt0: of request r0
+    int mine = 0, mine_n = 0, nt0 = 0;  // tiles, pairs; nt0: of request r0
     bool cut_len = false;
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
@@ -264,30 +268,45 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         const int nt = tiles_of<T>(a, clipped);
         if (r == r0) nt0 = nt;
         mine += nt * HP;
+        mine_n += nt > 0 ? HP : 0;
     }
     if (cut_len && cta == 0 && a.err) atomicOr(a.err, 2);
-    int upto = mine;
+    int upto = mine, upto_n = mine_n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(WSW_FULL_MASK, upto, d);
-        if (lane >= d) upto += y;
+        const int y = __shfl_up_sync(WSW_FULL_MASK, upto, d), y_n = __shfl_up_sync(WSW_FULL_MASK, upto_n, d);
+        if (lane >= d) {
+            upto += y;
+            upto_n += y_n;
+        }
     }
-    if (lane == 31) scan[warp] = upto;
+    if (lane == 31) scan[warp] = make_int2(upto, upto_n);
     __syncthreads();
-    int total = 0, before = upto - mine;
+    int total = 0, total_n = 0, before = upto - mine, before_n = upto_n - mine_n;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
+        const int2 x = scan[w];
+        if (w < warp) {
+            before += x.x;
+            before_n += x.y;
+        }
+        total += x.x;
+        total_n += x.y;
     }
-    const int run = max((total + kCtas - 1) / kCtas, W);  // tiles per CTA
-    // the place of tile s, from the thread whose requests hold it
+    // a few tiles for each warp at least: there latency counts, not balance
+    const int extra = total >= 4 * kCtas * W ? kPair : 0;
+    mine += extra * mine_n;
+    before += extra * before_n;
+    total += extra * total_n;
+    const int run = max((total + kCtas - 1) / kCtas, W);  // of a CTA
+    auto counted = [&](int nt) { return nt > 0 ? nt + extra : 0; };  // a pair's length in the list
+    // what the list has at s, from the thread whose requests hold it
     auto locate = [&](int s, Place &p) {
         if (s < before || s >= before + mine) return;
         int at = before, r = r0, nt = nt0;
 #pragma unroll 1
-        while (s >= at + nt * HP) {
-            at += nt * HP;
+        while (s >= at + counted(nt) * HP) {
+            at += counted(nt) * HP;
             nt = tiles_of<T>(a, clipped_len(a, ++r));
         }
         p = Place{r, s - at, nt};
@@ -299,8 +318,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     __syncthreads();
     auto snapped = [&](int s, const Place &p) {
         if (s >= total || s == 0 || p.nt > kWhole / T) return s;
-        const int t = p.off % p.nt;
-        return s - t + (2 * t > p.nt ? p.nt : 0);
+        const int n = counted(p.nt), t = p.off % n;
+        return s - t + (2 * t > n ? n : 0);
     };
     const int b = snapped(raw_b, cut[0]), e = snapped(raw_e, cut[1]);
     const int n_cta = e - b;
@@ -323,21 +342,23 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     if (n_cta == 0) return;
 
     const int wb = first_tile(warp), we = first_tile(warp + 1);
-    int todo = we - wb;     // tiles left to use
-    int to_issue = todo;
     unsigned char *ring = smem + warp * C::ring;
     const uint32_t ring_s = smem_addr(ring);
     unsigned char *qsm = smem + W * C::ring + warp * C::q_bytes;
     uint4 *q_hi_sm = reinterpret_cast<uint4 *>(qsm);
     uint4 *q_lo_sm = reinterpret_cast<uint4 *>(qsm + (C::q_smem ? C::qfrag : 0));
 
-    if (todo > 0) {
+    if (wb < we) {
         Cursor uc;  // the tile in use
         const Place at_first = place[warp];
         set_request<T>(a, uc, at_first.req);
-        uc.g = wb;
-        uc.hp = at_first.off / uc.nt;
-        uc.t = at_first.off - uc.hp * uc.nt;
+        {
+            const int n = counted(uc.nt);
+            uc.hp = at_first.off / n;
+            const int in = at_first.off - uc.hp * n;
+            uc.t = max(in - extra, 0);
+            uc.g = wb - in + extra + uc.t;  // we or beyond: no tile here
+        }
         Cursor ic = uc;  // the next tile to copy
         const int page_mask = (1 << a.kv.page_shift) - 1;
 
@@ -364,8 +385,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         look_up();
         int ist = 0;
         auto issue = [&]() {
-            if (to_issue > 0) {
-                --to_issue;
+            if (ic.g < we) {
                 constexpr uint32_t kAll = T == 32 ? 0xffffffffu : (1u << (T & 31)) - 1;
                 const int p0 = ic.start + ic.t * T, p = p0 + (lane & (T - 1));
                 const int rel = (p >> a.kv.page_shift) - wbase;
@@ -422,8 +442,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 }
                 if (lane == 0) seen_mask[warp][ist] = valid;
                 if (++ist == C::stages) ist = 0;
-                if (to_issue > 0) {
-                    advance<T>(a, ic);
+                if (ic.g + 1 + (ic.t == ic.nt - 1 ? extra : 0) >= we) {
+                    ic.g = we;
+                } else {
+                    advance<T>(a, ic, extra);
                     look_up();
                     if (ic.t == 0) {  // a new pair: its queries on their way to L1
                         const int hn = a.passes == 1 ? ic.hp : ic.hp / a.passes, gn = (ic.hp - hn * a.passes) * RT;
@@ -451,7 +473,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 
         // the first turns only fill the ring
 #pragma unroll 1
-        for (int fill = 1 - C::stages; todo > 0; todo -= fill >= 0, ++fill) {
+        for (int fill = 1 - C::stages; uc.g < we; ++fill) {
             __syncwarp();  // every lane is done reading the stage that the next copy reuses
             issue();
             if (fill < 0) continue;
@@ -718,8 +740,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             }
 
             // ---- the end of the pair, or of the run
-            const bool pair_end = uc.t == uc.nt - 1;
-            if (!pair_end && todo > 1) {
+            const bool pair_end = uc.t == uc.nt - 1, run_end = uc.g + 1 + (pair_end ? extra : 0) >= we;
+            if (!pair_end && !run_end) {
                 ++uc.t;
                 ++uc.g;
                 continue;
@@ -729,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
             const bool whole = pair_end && t_first == 0;
             float *rec = nullptr;
             if (!whole) {
-                if (todo == 1) {  // the run's last piece: into the ring, which no copy uses any more
+                if (run_end) {  // the run's last piece: into the ring, which no copy uses any more
                     cp_wait<0>();
                     __syncwarp();
                     rec = reinterpret_cast<float *>(ring);
@@ -737,7 +759,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                     rec = a.wrec + static_cast<int64_t>(cta * W + warp) * RT * C::srec;
                     first_left = true;
                 }
-                if (lane == 0) pieces[2 * warp + (todo == 1)] = Piece{uc.g - uc.t, uc.r, uc.hp, uc.nt};
+                if (lane == 0) pieces[2 * warp + run_end] = Piece{uc.g - uc.t, uc.r, uc.hp, uc.nt};
             }
 #pragma unroll
             for (int y = 0; y < RT / 8; ++y) {
@@ -753,7 +775,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 #pragma unroll
                     for (int x = 0; x < 2; ++x) v[n][x] = (RT == 8 ? o[n][x] + o[n][2 + x] : o[n][2 * y + x]) * f;
                 if (tq == 0) {
-                    if (!whole) piece_ml[2 * warp + (todo == 1)][row] = make_float2(m[y], l[y]);
+                    if (!whole) piece_ml[2 * warp + run_end][row] = make_float2(m[y], l[y]);
                     else if (a.lse) a.lse[head] = lse_of(m[y], l[y]);
                 }
                 // lane tq's dimensions: 2 tq, 2 tq + 1 of every eight, or (q8_0) 4 tq .. 4 tq + 3 of sixteen
@@ -779,10 +801,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                     }
                 }
             }
-            if (todo > 1) {
-                // advance() is safe: there is another tile
-                advance<T>(a, uc);
-            }
+            if (run_end) break;
+            advance<T>(a, uc, extra);
         }
         // the first piece's record joins the last one's in the ring
         if (first_left) {
