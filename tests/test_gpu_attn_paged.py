@@ -156,6 +156,19 @@ def test_ragged_batches():
     Case(wsw, [2000, 0, 1, 2000], kvh=4, group=16, d=256, cache="bf16", q="bf16").check()
 
 
+@pytest.mark.parametrize("seed", range(6))
+def test_lists_of_long_and_short_requests(seed):
+    """Lists long enough for every rule of their cutting: pairs shared by many CTAs, cuts near
+    a long pair's ends, short pairs kept whole, requests of no tokens between them."""
+    wsw = need_gpu()
+    g = np.random.default_rng(100 + seed)
+    lens = [int(math.exp(x)) for x in g.uniform(0, math.log(9000), 24)] + [int(g.integers(5000, 16000)), 0]
+    g.shuffle(lens)
+    cache, q = [("fp16", "fp32"), ("q8_0", "fp32"), ("bf16", "bf16")][seed % 3]
+    Case(wsw, lens, kvh=[3, 4, 8][seed // 2], group=[4, 8, 10][(seed // 3) % 3], cache=cache, q=q,
+         page=[16, 64, 8][seed % 3], nhd=seed % 2 == 0, seed=seed).check()
+
+
 @pytest.mark.parametrize("window", [1, 15, 16, 100, 5000])
 def test_windows(window):
     wsw = need_gpu()

@@ -316,10 +316,14 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     locate(raw_b, cut[0]);
     locate(raw_e, cut[1]);
     __syncthreads();
+    // a cut just inside a long pair moves to its end, too: a CTA that shares two pairs with
+    // others ends with two joins, worth some 20 tiles
+    const int margin = min(run / 8, 16);
     auto snapped = [&](int s, const Place &p) {
-        if (s >= total || s == 0 || p.nt > kWhole / T) return s;
+        if (s >= total || s == 0) return s;
         const int n = counted(p.nt), t = p.off % n;
-        return s - t + (2 * t > n ? n : 0);
+        if (p.nt <= kWhole / T) return s - t + (2 * t > n ? n : 0);
+        return t <= margin ? s - t : n - t <= margin ? s - t + n : s;
     };
     const int b = snapped(raw_b, cut[0]), e = snapped(raw_e, cut[1]);
     const int n_cta = e - b;
@@ -923,8 +927,15 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         return is_last;
     };
     const int group0 = cta / kGroup * kGroup;  // the group's first CTA
-    auto first_cta = [&](const Piece &pc) { return pc.pstart / run; };
-    auto last_cta = [&](const Piece &pc) { return (pc.pstart + pc.nt - 1) / run; };
+    // the CTAs of a long pair's first and last tiles, by the cuts as they were moved
+    auto first_cta = [&](const Piece &pc) {
+        const int c = pc.pstart / run;
+        return c + ((c + 1) * run - (pc.pstart - extra) <= margin);
+    };
+    auto last_cta = [&](const Piece &pc) {
+        const int end = pc.pstart + pc.nt, c = (end - 1) / run;
+        return c - (end - c * run <= margin);
+    };
     if (tid < nshared) {
         const Piece pc = tid == 0 ? shared_a : shared_b;
         const int f = first_cta(pc), c0 = max(f, group0), c1 = min(last_cta(pc), group0 + kGroup - 1);
