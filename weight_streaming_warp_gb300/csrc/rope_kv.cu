@@ -63,19 +63,29 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
 }
 
+// the two values of a word
+__device__ __forceinline__ float2 two(uint32_t u, __half) { return __half22float2(*reinterpret_cast<const __half2 *>(&u)); }
+__device__ __forceinline__ float2 two(uint32_t u, __nv_bfloat16) { return make_float2(bf16lo(u), bf16hi(u)); }
+
 // 8 consecutive values; plain loads, as the call may write q in place
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]) {
-    if (vec) {
-        alignas(16) T t[8];
-        uint4 *u = reinterpret_cast<uint4 *>(t);
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(p)[i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_f(t[i]);
-    } else {
+    if (!vec) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = to_f(p[i]);
+    } else if constexpr (sizeof(T) == 4) {
+        const float4 u = reinterpret_cast<const float4 *>(p)[0], v = reinterpret_cast<const float4 *>(p)[1];
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = two(w[i], T());
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
     }
 }
 
@@ -116,10 +126,11 @@ __device__ __forceinline__ int place(int p, int half, int group) {
     return group == 8 ? (p & 7) * (half >> 3) + (p >> 3) : group == 4 ? (p & 3) * ((half + 3) >> 2) + (p >> 2) : p;
 }
 
-// Eight CTAs on an SM: the copy is bound by the loads in flight, so threads count for more than
-// registers (8191 bf16 tokens of 48 heads: 50 us at 32 registers, 56 at 40, 74 at 56).
+// One CTA for a token or two.  It is bound by the loads in flight, so threads count for more
+// than registers: 8191 tokens of 48 heads, fp32 into binary16, 66 us with 6 CTAs on an SM and 69
+// with 8; bf16 with pairs 20 apart, 56 and 52 us.
 template <typename T, int CT>
-__global__ void __launch_bounds__(kThreads, 8) rope_kv_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 8) rope_kv_kernel(const RopeArgs a) {
     __shared__ float2 cs[kMaxTile][128 + 4];  // (m cos, m sin) of each token and pair
     __shared__ int32_t pos_sm[kMaxTile];
     __shared__ int64_t slot_sm[kMaxTile];
@@ -268,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kv_kernel(const RopeArgs a) 
 // partner's values are the neighbour's slot.  The next token's angles are computed beside
 // this one's rows.
 constexpr int kRing = 4;
-constexpr int kStreamCtas = 3;  // on an SM: 8191 bf16 tokens of 48 heads 46.2 us, with 4, 5, 6 CTAs 47.8, 49.5, 54.1 us
+constexpr int kStreamCtas = 3;  // on an SM: 8191 bf16 tokens of 48 heads 40 us, with 4 and 5 CTAs 45 and 59 us
 
 template <typename T, int CT>
 __global__ void __launch_bounds__(kThreads, kStreamCtas) rope_stream_kernel(const RopeArgs a) {
@@ -287,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) rope_stream_kernel(cons
     const int rows = a.q_heads + 2 * a.kv.heads;
     const int d0 = (tid & (lanes - 1)) * 8;
     const int rp = kThreads >> a.lane_shift, rs = tid >> a.lane_shift;  // rows a round, this thread's
-    const int rounds = (rows + rp - 1) / rp;
     const int stride = gridDim.x;
     const int count = static_cast<int>((a.tokens - blockIdx.x + stride - 1) / stride);  // this CTA's tokens
     const bool turns = d0 < a.rot, lo = d0 < half;
@@ -296,26 +306,32 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) rope_stream_kernel(cons
     pdl_launch_dependents();
     pdl_wait();
 
-    int pi = 0, pj = 0, ps = 0;  // the next row to copy: token, round, slot
+    // the next row to copy: tokens left, its row, its slot, and that token's rows
+    int p_left = count, ph = rs;
+    const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(&ring[0][tid * kV]));
+    constexpr uint32_t kSlot = kThreads * kV * 16;
+    uint32_t p_slot = ring_s;
+    const T *pq = static_cast<const T *>(a.q) + blockIdx.x * a.qts + d0;
+    const T *pk = static_cast<const T *>(a.k) + blockIdx.x * a.kts + d0;
+    const T *pv = static_cast<const T *>(a.v) + blockIdx.x * a.vts + d0;
     auto issue = [&]() {
-        if (pi < count) {
-            const int h = pj * rp + rs;
-            if (h < rows) {
-                const int64_t t = token(pi);
-                const int kh = h - a.q_heads;
-                const T *src = kh < 0 ? static_cast<const T *>(a.q) + t * a.qts + h * a.qhs
-                               : kh < a.kv.heads ? static_cast<const T *>(a.k) + t * a.kts + kh * a.khs
-                                                 : static_cast<const T *>(a.v) + t * a.vts + (kh - a.kv.heads) * a.vhs;
-                const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&ring[ps][tid * kV]));
+        if (p_left > 0) {
+            if (ph < rows) {
+                const int kh = ph - a.q_heads, vh = kh - a.kv.heads;
+                const T *src = kh < 0 ? pq + ph * a.qhs : vh < 0 ? pk + kh * a.khs : pv + vh * a.vhs;
 #pragma unroll
                 for (int i = 0; i < kV; ++i)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i),
-                                 "l"(reinterpret_cast<const uint4 *>(src + d0) + i) : "memory");
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(p_slot + 16 * i),
+                                 "l"(reinterpret_cast<const uint4 *>(src) + i) : "memory");
             }
-            if (++ps == kRing) ps = 0;
-            if (++pj == rounds) {
-                pj = 0;
-                ++pi;
+            p_slot = p_slot == ring_s + (kRing - 1) * kSlot ? ring_s : p_slot + kSlot;
+            ph += rp;
+            if (ph - rs >= rows) {  // the next token
+                ph = rs;
+                --p_left;
+                pq += stride * a.qts;
+                pk += stride * a.kts;
+                pv += stride * a.vts;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -371,7 +387,10 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) rope_stream_kernel(cons
             if (group == 8) {
                 const int at = (lo ? d0 : d0 - half) >> 3, st = half >> 3;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) z[k] = c[at + k * st];
+                for (int k = 0; k < 8; ++k) {
+                    z[k] = c[at + k * st];
+                    z[k].y = lo ? -z[k].y : z[k].y;
+                }
             } else {
                 const int st = (half + 3) >> 2;
 #pragma unroll
@@ -380,12 +399,11 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) rope_stream_kernel(cons
         }
         T *ob = static_cast<T *>(a.q_out) + token(i) * a.q_heads * D + d0;
 #pragma unroll 1
-        for (int j = 0; j < rounds; ++j) {
+        for (int h = rs; h - rs < rows; h += rp) {
             __syncwarp();  // the slot that the next copy takes has been read, by the partners too
             issue();
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
             __syncwarp();
-            const int h = j * rp + rs;
             const bool active = h < rows;  // a row's lanes are all active or all idle
             const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + a.kv.heads;
             const int kh = is_v ? h - a.q_heads - a.kv.heads : h - a.q_heads;
@@ -398,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) rope_stream_kernel(cons
                         float y[8];
                         load8(own + partner * 8, true, y);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = fmaf(x[k], z[k].x, y[k] * (lo ? -z[k].y : z[k].y));
+                        for (int k = 0; k < 8; ++k) x[k] = fmaf(x[k], z[k].x, y[k] * z[k].y);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -544,8 +562,8 @@ extern "C" int wsw_rope_kv_write(const void *q, const void *k, const void *v, in
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     // The streaming form wants aligned rows, pairs that fall into whole vectors, and a few tokens
-    // for each CTA.  8191 tokens of 48 heads, streaming and plain form: bf16 46 and 50 us, fp32
-    // into q8_0 63 and 67 us; fp32 into a 16-bit cache 70 and 65 us, so that one stays plain.
+    // for each CTA.  8191 tokens of 48 heads, streaming and plain form: bf16 40 and 50 us, fp32
+    // into q8_0 60 and 67 us; fp32 into a 16-bit cache 69 and 66 us, so that one stays plain.
     const bool heavy = dtype != WSW_F32 || cache->dtype == WSW_Q8_0;
     if (tokens >= 1024 && heavy && a.vec && a.vec_out && (interleaved || (rot_dim & 15) == 0)) {
         const dim3 all(static_cast<unsigned>(tokens < kStreamCtas * di.sm_count ? tokens : kStreamCtas * di.sm_count));
