@@ -584,7 +584,8 @@ int wsw_rope_kv_write(const void *q, const void *k, const void *v, int32_t dtype
  *   out[r][a] = sum_p exp(x_p - m) V(h, p) / sum_p exp(x_p - m);  lse[r][a] = ln sum_p exp(x_p)
  * K(h, p) and V(h, p) are the cached rows; a q8_0 value is binary16(scale * code), the
  * value wsw_dequant_q8_0_kv writes.  A request of length 0 (an unused row of a padded
- * batch) gets out = 0 and lse = -inf.  Positions past lens[r] in a page are never used.
+ * batch) gets out = 0 and lse = -inf, as does one whose seen scores are all -inf.
+ * Positions past lens[r] in a page are never used.
  *
  * Scores, the softmax's maximum and sum, and the value sums are fp32.  The products run
  * on tensor cores in the cache's 16-bit type (binary16 for q8_0); q and the softmax

