@@ -637,7 +637,7 @@ int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t requests, int64_
  *   ws       device workspace of ws_bytes >= wsw_token_logprobs_workspace_bytes(...) bytes
  *            (0: none needed, ws may be NULL), 16-byte aligned, zero-filled before its
  *            first use and then reused, as the attention's.
- *   1 <= vocab < 2^31;  rows < 2^31.  rows == 0 does nothing.
+ *   1 <= vocab < 2^31 - 65536;  rows < 2^31.  rows == 0 does nothing.
  */
 size_t wsw_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top);
 int wsw_token_logprobs(const void *logits, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,

@@ -83,6 +83,21 @@ def test_scales_and_the_best_token(x, scale):
     assert torch.equal(r.logprob, r.top_logprob[:, 0])
 
 
+@pytest.mark.parametrize("x", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("top", [1, 5, 20])
+@pytest.mark.parametrize("rows", [1, 700])
+def test_the_rows_last_values_tie_with_earlier_ones(x, top, rows):
+    """The row's end, which no whole 16-byte vector holds, ranks after every equal value."""
+    wsw = need_gpu()
+    vocab = 33001
+    lg = -1.0 - torch.rand(rows, vocab, generator=torch.Generator().manual_seed(8))
+    lg[:, 100: 100 + top - 1] = 5.0
+    lg[:, 2000:2400] = 2.0  # enough candidates for a cut before the tie is read
+    lg[:, 30000] = 3.0
+    lg[:, vocab - 1] = 3.0
+    _check(wsw, lg.to(DT[x]).cuda(), [vocab - 1] * rows, top, 1.0)
+
+
 @pytest.mark.parametrize("offset,ld", [(0, 3001), (1, 3001), (3, 3007), (5, 4096)])
 @pytest.mark.parametrize("x", ["fp32", "fp16"])
 def test_strides_and_alignment(offset, ld, x):

@@ -288,6 +288,14 @@ __device__ __forceinline__ void cut(Shared &sm, int k) {
     __syncthreads();
 }
 
+// The least value that can still be among the k best, from a cut and with [.., end) behind: one above
+// the k-th best, but its equal where that one is of the row's last few values, which are read first
+// and rank after an equal value before them.
+__device__ __forceinline__ float after_cut(const Shared &sm, int end, int k) {
+    if (sm.n == k && static_cast<int>(~static_cast<uint32_t>(sm.best[k - 1])) >= end) return sm.thr;
+    return above(sm.thr);
+}
+
 __device__ __forceinline__ void push(Shared &sm, uint64_t key) { sm.buf[atomicAdd(&sm.n, 1)] = key; }
 
 // The candidate vectors' values from thr up become keys; then the keys are cut.  Every thread
@@ -510,11 +518,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) logprobs_ker
                 cut(sm, k);
             }
             group0 = group_end;
-            thr = above(sm.thr);
+            thr = after_cut(sm, group_end, k);
         } else if (over) {
             take_vectors<T>(sm, thr, k);
             group0 = group_end;
-            thr = above(sm.thr);
+            thr = after_cut(sm, group_end, k);
         }
         first = false;
         since = filled = 0;
