@@ -98,6 +98,26 @@ def test_the_rows_last_values_tie_with_earlier_ones(x, top, rows):
     _check(wsw, lg.to(DT[x]).cuda(), [vocab - 1] * rows, top, 1.0)
 
 
+@pytest.mark.parametrize("x", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("top", [1, 8, 32])
+@pytest.mark.parametrize("rows", [2, 320])
+@pytest.mark.parametrize("kind", ["islands", "drift", "steps"])
+def test_uneven_rows_overflow_the_candidates(x, top, rows, kind):
+    """Parts of a row far above what came before: more candidates at once than are kept."""
+    wsw = need_gpu()
+    vocab = 40009
+    lg = torch.randn(rows, vocab, generator=torch.Generator().manual_seed(10)) * 2.5
+    if kind == "islands":
+        lg[:, 9000:11000] += 5.0
+        lg[:, 26001:26002] = 40.0
+        lg[:, 33333:40009] += 9.0
+    elif kind == "drift":
+        lg += torch.linspace(0, 20, vocab)
+    else:
+        lg = torch.arange(vocab).div(1500, rounding_mode="floor").float().expand(rows, vocab).clone()
+    _check(wsw, lg.to(DT[x]).cuda(), [(1237 * i) % vocab for i in range(rows)], top, 1.0)
+
+
 @pytest.mark.parametrize("offset,ld", [(0, 3001), (1, 3001), (3, 3007), (5, 4096)])
 @pytest.mark.parametrize("x", ["fp32", "fp16"])
 def test_strides_and_alignment(offset, ld, x):

@@ -17,15 +17,18 @@
 // there are more than kKeep vectors, their values become keys and the keys are cut to the k
 // best, which raises the threshold to the k-th best value so far.  Keys are 64 bits, the
 // value's order-preserving bits over the complemented index, so that they are distinct and
-// equal values rank by index.  Tiles that bring too many vectors (a long run of equal or
-// rising values) are read again in pieces that cannot.
+// equal values rank by index.  Tiles that bring too many vectors (logits that rise along the row, or a
+// part of the vocabulary well above the rest) are read again, against a new bound from
+// their own groups' maxima (2047 x 50021 bf16, 5 alternatives, a tenth of the row raised by two
+// deviations: 226 us when they were read in pieces of 992 values with a cut each, 92 so).
 //
 // Rows are split over CTAs when there are few; each split leaves (m, S, E, count, k keys) in
 // the workspace and the row's last CTA joins them in a fixed order.
 //
 // Bound: the logits once, but a bf16 logit's arithmetic costs more issue slots than its two
-// bytes cost of HBM's time.  2047 rows of 50021: bf16 66 us with 5 alternatives (3.1 TB/s, 66% of
-// the issue slots) and 47 us with none, fp32 77 and 70 us (5.3 and 5.8 TB/s).  One row of 152064 fp32
+// bytes cost of HBM's time.  2047 rows of 50021: bf16 63 us with 5 alternatives (3.3 TB/s) and
+// 47 us with none, fp32 75 and 70 us (5.4 and 5.8 TB/s); sorted rows, the worst order, take 145 us
+// (bf16, rising).  One row of 152064 fp32
 // values: 11 us with 20 alternatives, 4.4 us with none; 64 rows with 8: 18 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,9 +47,11 @@ constexpr int kMaxTop = 32;
 constexpr int kUnroll = 4;      // 16-byte vectors per thread and tile
 constexpr int kCap = 1024;      // keys
 constexpr int kVecs = 112;      // candidate vectors: at most 8 keys each, beside k and the row's ends
-constexpr int kKeep = 28;       // make keys of them beyond this
+constexpr int kKeep = 20;       // make keys of them beyond this
 constexpr int kLook = 2;        // look at their number every so many tiles
-static_assert(kVecs * 8 + kMaxTop + 16 <= kCap, "keys");
+constexpr int kPiece = 224;     // values of a piece
+constexpr int kThin = 96;       // keys that are worth thinning before a cut
+static_assert(kVecs * 8 + kMaxTop + 16 <= kCap && kPiece + kMaxTop + 16 <= kCap, "keys");
 constexpr int kTargetCtas = 608;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -298,18 +303,90 @@ __device__ __forceinline__ float after_cut(const Shared &sm, int end, int k) {
 
 __device__ __forceinline__ void push(Shared &sm, uint64_t key) { sm.buf[atomicAdd(&sm.n, 1)] = key; }
 
-// The candidate vectors' values from thr up become keys; then the keys are cut.  Every thread
-// calls it, with the vectors written before a barrier.
+// The keys of buf that can be among the k best, by the k-th largest of 32 groups' maxima: some 30
+// of any number of distinct values, so that the cut's n * n stays small.  Every thread calls it.
+__device__ __forceinline__ void thin(Shared &sm, int n, int k) {
+    uint64_t own[kCap / kThreads];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kCap / kThreads; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        own[j] = i < n ? sm.buf[i] : 0;
+        if (own[j]) mx = fmaxf(mx, unord(static_cast<uint32_t>(own[j] >> 32)));
+    }
+    const uint64_t least = static_cast<uint64_t>(ord(reached_by(sm, mx, k))) << 32;  // a barrier: all have read buf
+    if (threadIdx.x == 0) sm.n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kCap / kThreads; ++j)
+        if (own[j] && own[j] >= least) push(sm, own[j]);
+    __syncthreads();
+}
+
+// The candidates' values from thr up become keys, and the keys are cut.  When there were too many
+// vectors for their place, the values [from, end) of the row are read again: those that the k-th
+// largest of 32 groups' maxima reaches, which some tens do in any order of distinct values; what
+// many equal ones still overflow goes in pieces that cannot, a cut before each.  Every thread calls it
+// after a barrier behind the candidates.
 template <typename T>
-__device__ __forceinline__ void take_vectors(Shared &sm, float thr, int k) {
+__device__ __forceinline__ void select(Shared &sm, const T *x, int from, int end, float thr, int k) {
     constexpr int V = Elem<T>::kVec;
-    const int n = sm.nvec * V;
-    for (int e = threadIdx.x; e < n; e += kThreads) {
-        const float y = Elem<T>::get(reinterpret_cast<const T *>(sm.vec), e);
-        if (y >= thr) push(sm, key_of(y, sm.vec_at[e / V] + e % V));
+    const int tid = threadIdx.x, n0 = sm.n, nvec = sm.nvec;
+    if (nvec <= kVecs) {
+        for (int e = tid; e < nvec * V; e += kThreads) {
+            const float y = Elem<T>::get(reinterpret_cast<const T *>(sm.vec), e);
+            if (y >= thr) push(sm, key_of(y, sm.vec_at[e / V] + e % V));
+        }
+    } else {
+        const int nv = (end - from) / V;
+        float mx = -INFINITY;
+        float v[V];
+#pragma unroll 2
+        for (int i = tid; i < nv; i += kThreads) {
+            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(x + from) + i), v);
+#pragma unroll
+            for (int u = 0; u < V; ++u) mx = fmaxf(mx, v[u]);
+        }
+        const float bound = fmaxf(thr, reached_by(sm, mx, k));  // a barrier: all have read sm.n, sm.nvec
+        bool full = !(mx >= bound);
+#pragma unroll 1
+        for (int i = tid; i < nv && !full; i += kThreads) {
+            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(x + from) + i), v);
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                if (!(v[u] >= bound)) continue;
+                const int to = atomicAdd(&sm.n, 1);
+                full = to >= kCap;
+                if (!full) sm.buf[to] = key_of(v[u], from + i * V + u);
+            }
+        }
+        __syncthreads();
+        if (sm.n > kCap) {
+            __syncthreads();
+            if (tid == 0) sm.n = n0;
+#pragma unroll 1
+            for (int p = from; p < end; p += kPiece) {
+                __syncthreads();
+                cut(sm, k);
+                const uint64_t floor = sm.n == k ? sm.best[k - 1] : 0;
+                const int pe = min(p + kPiece, end);
+                mx = -INFINITY;
+                for (int i = p + tid; i < pe; i += kThreads) mx = fmaxf(mx, Elem<T>::get(x, i));
+                const uint64_t least = static_cast<uint64_t>(ord(reached_by(sm, mx, k))) << 32;
+                for (int i = p + tid; i < pe; i += kThreads) {
+                    const uint64_t key = key_of(Elem<T>::get(x, i), i);
+                    if (key >= least && key > floor) push(sm, key);
+                }
+            }
+        }
     }
     __syncthreads();
-    if (threadIdx.x == 0) sm.nvec = 0;
+    const int n = sm.n;
+    if (n > kThin) {
+        __syncthreads();
+        thin(sm, n, k);
+    }
+    if (tid == 0) sm.nvec = 0;
     cut(sm, k);
 }
 
@@ -493,43 +570,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) logprobs_ker
             }
         }
         if (!first && ++since < kLook && tile0 + kTile < hi) continue;
-        // one answer for the whole block; inside, nobody adds vectors until all have read sm.nvec
-        // (a large k's bound is loose: it is cut after the first of several tiles)
-        const bool over = __syncthreads_or(filled > kKeep || (first && k > 8 && tile0 + 2 * kTile < hi));
-        const int group_end = min(tile0 + kTile, hi);
-        if (over && sm.nvec > kVecs) {
-            // too many: take the values of the tiles since the last look again, in pieces that
-            // fit, cutting after each
-            __syncthreads();
-            if (tid == 0) sm.nvec = 0;
-            cut(sm, k);
-#pragma unroll 1
-            for (int p = group0; p < group_end; p += kCap - kMaxTop) {
-                const uint64_t floor = sm.n == k ? sm.best[k - 1] : 0;
-                const int end = min(p + (kCap - kMaxTop), group_end);
-                float mx = -INFINITY;
-                for (int i = p + tid; i < end; i += kThreads) mx = fmaxf(mx, Elem<T>::get(x, i));
-                const uint64_t bound = static_cast<uint64_t>(ord(reached_by(sm, mx, k))) << 32;
-                for (int i = p + tid; i < end; i += kThreads) {
-                    const uint64_t key = key_of(Elem<T>::get(x, i), i);
-                    if (key >= bound && key > floor) push(sm, key);
-                }
-                __syncthreads();
-                cut(sm, k);
-            }
-            group0 = group_end;
-            thr = after_cut(sm, group_end, k);
-        } else if (over) {
-            take_vectors<T>(sm, thr, k);
-            group0 = group_end;
-            thr = after_cut(sm, group_end, k);
+        // one answer for the whole block (a large k's bound is loose: it is cut after the first of
+        // several tiles)
+        const bool last = tile0 + kTile >= hi;
+        if (__syncthreads_or(filled > kKeep || last || (first && k > 8))) {
+            const int end = min(tile0 + kTile, hi);
+            select(sm, x, group0, end, thr, k);
+            group0 = end;
+            thr = after_cut(sm, end, k);
         }
         first = false;
         since = filled = 0;
     }
-    if (k > 0) {
+    if (k > 0 && lo >= hi) {
         __syncthreads();
-        take_vectors<T>(sm, thr, k);
+        cut(sm, k);
     }
     s = block_sums(sm, s, count, c);
     if (tid == 0) {
