@@ -194,6 +194,26 @@ def test_large_scores_stay_finite():
     Case(wsw, [500, 1000], qsigma=40.0).check()
 
 
+@pytest.mark.parametrize("q", ["fp32", "bf16"])
+@pytest.mark.parametrize("cache,d", [("fp16", 128), ("q8_0", 64), ("fp16", 256), ("bf16", 128), ("q8_0", 128)])
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 1e6, 1e30])
+@pytest.mark.parametrize("softcap", [0.0, 2.0])
+def test_queries_of_any_size(q, cache, d, size, softcap):
+    """q far outside binary16's range, the scale the other way: ordinary scores."""
+    wsw = need_gpu()
+    Case(wsw, [70, 3], group=10, d=d, q=q, cache=cache, qsigma=size).check(scale=1 / (math.sqrt(d) * size),
+                                                                         softcap=softcap)
+
+
+def test_a_zero_query_and_one_of_another_size_share_a_head():
+    wsw = need_gpu()
+    c = Case(wsw, [300, 17, 1], group=4)
+    c.q[:, 0] = 0.0
+    c.q[:, 1] *= 2.0 ** 30
+    c.q[:, 6] *= 2.0 ** -40
+    c.check(scale=2.0 ** -30)
+
+
 def test_bad_pages_are_hidden_and_flagged():
     wsw = need_gpu()
     c = Case(wsw, [100, 64, 40], page=16)

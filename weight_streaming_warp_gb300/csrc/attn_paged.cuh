@@ -28,14 +28,16 @@
 // Measured, 4 KV heads of 128: 64 requests of up to 8192 positions, bf16, group 10, 111 us
 // (4.9 TB/s, bound by latency with 8 warps on an SM); 32 of up to 32768, q8_0, group 8, 120 us (4.9
 // TB/s, bound by instructions); the same in bf16 180 us (6.1 TB/s); one of 32768 binary16 positions, group 8,
-// 24 us, of which 8 us are the two levels of joins; three short ones (head_dim 64) 8.5 us.
+// 24 us, of which 8 us are the two levels of joins; three short ones (head_dim 64) 8.7 us.
 //
 // Products on m16n8k16 tensor-core tiles with fp32 sums.  Up to eight query heads of a KV head
 // share a 16-row operand as high parts (rows 0..7) and residuals (8..15) of q and of the
 // weights; 9 to 16 take 16 rows and a second product for the residuals; more take several
 // passes over the pair.  The maximum in use is raised, and the sums rescaled, only when a tile
 // exceeds it by more than kLazy; the weights, then up to 2^(kLazy + kShift), stay in binary16's
-// range and their residuals above its subnormals.  q8_0 rows stay codes in shared memory and become binary16(scale *
+// range (a weight is off by 2^-22 of itself or 2^-32 of the largest).  A query row enters
+// binary16 times the power of two that brings its largest value to 2^14 .. 2^15, so that any fp32
+// or bf16 row keeps 22 bits.  q8_0 rows stay codes in shared memory and become binary16(scale *
 // code) in registers, the value the one-pass dequantizer writes.
 #pragma once
 
@@ -52,7 +54,7 @@ constexpr int kPair = 4;       // tiles that the beginning and end of a pair cou
 constexpr float kLazy = 8.f;   // log2: the running maximum may lag by so much
 constexpr int kGroup = 12;     // CTAs whose records are joined first
 constexpr int kCtas = 152;     // runs of the tile list: one CTA per SM of a 152-SM part
-constexpr float kShift = 4.f;  // log2 of the weights' scale
+constexpr float kShift = 7.f;  // log2 of the weights' scale
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kSmemMax = 226 * 1024;
 
@@ -473,6 +475,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         const int gq = lane >> 2, tq = lane & 3;
         uint32_t qa[C::q_smem ? 1 : C::ksteps][4];
         float m[RT / 8], l[RT / 8], slope[RT / 8];
+        float unit[RT / 8];  // of a score's product sum, over softcap if that is used (not bf16)
         float o[D / 8][4];
         bool q_lo = false;   // RT 16: q has residuals
         int t_first = 0;     // first tile of the piece
@@ -495,9 +498,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 bool some = false;
                 // every load of a batch is issued before the first is used
                 constexpr int kB = C::ksteps < 8 ? C::ksteps : 8;
-#pragma unroll
-                for (int k0 = 0; k0 < C::ksteps; k0 += kB) {
-                    float2 qv[kB][2][RT / 8];
+                float2 qv[kB][2][RT / 8];
+                auto load = [&](int k0) {
                     auto at = [&](int kt, int x, int row) -> int64_t {
                         // natural order for 16-bit rows; for q8_0 lane tq owns dimensions
                         // tq D / 4 ..., four of them per step
@@ -528,6 +530,38 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                                                     : __half22float2(*reinterpret_cast<const __half2 *>(&u));
                         }
                     }
+                };
+                float up[RT / 8];
+#pragma unroll
+                for (int y = 0; y < RT / 8; ++y) {
+                    up[y] = 1.f;  // bf16 has fp32's range
+                    unit[y] = a.cap_in != 0.f ? a.cap_in : a.scale2;
+                }
+                if constexpr (CT != WSW_BF16) {
+                    float top[RT / 8];
+#pragma unroll
+                    for (int y = 0; y < RT / 8; ++y) top[y] = 0.f;
+#pragma unroll 1
+                    for (int k0 = 0; k0 < C::ksteps; k0 += kB) {
+                        load(k0);
+#pragma unroll
+                        for (int i = 0; i < kB * 2 * (RT / 8); ++i) {
+                            const float2 v = qv[i / (RT / 4)][(i / (RT / 8)) & 1][i % (RT / 8)];
+                            top[i % (RT / 8)] = fmaxf(top[i % (RT / 8)], fmaxf(fabsf(v.x), fabsf(v.y)));
+                        }
+                    }
+#pragma unroll
+                    for (int y = 0; y < RT / 8; ++y) {
+                        top[y] = fmaxf(top[y], __shfl_xor_sync(WSW_FULL_MASK, top[y], 1));
+                        top[y] = fmaxf(top[y], __shfl_xor_sync(WSW_FULL_MASK, top[y], 2));
+                        const int e = max(static_cast<int>(__float_as_uint(top[y]) >> 23), 15);
+                        up[y] = __uint_as_float((268u - e) << 23);           // 2^(14 - (e - 127))
+                        unit[y] *= __uint_as_float((e - 14u) << 23);         // its inverse
+                    }
+                }
+#pragma unroll
+                for (int k0 = 0; k0 < C::ksteps; k0 += kB) {
+                    if (CT == WSW_BF16 || C::ksteps > kB) load(k0);
 #pragma unroll
                     for (int j = 0; j < kB; ++j) {
                         const int kt = k0 + j;
@@ -538,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                             for (int y = 0; y < RT / 8; ++y) {
                                 const float2 v = qv[j][x][y];
                                 uint32_t vh, vl;
-                                split<CT>(v.x, v.y, vh, vl);
+                                split<CT>(v.x * up[y], v.y * up[y], vh, vl);
                                 if constexpr (RT == 8) {
                                     hi[2 * x] = vh;
                                     hi[2 * x + 1] = vl;
@@ -665,7 +699,12 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                     for (int j = 0; j < 2; ++j) {
                         const int pi = 8 * n + 2 * tq + j;
                         float x = RT == 8 ? sc[n][j] + sc[n][2 + j] : sc[n][2 * y + j];
-                        x = a.cap_in != 0.f ? a.cap_out * tanhf(x * a.cap_in) : x * a.scale2;
+                        if constexpr (CT == WSW_BF16) {
+                            x = a.cap_in != 0.f ? a.cap_out * tanhf(x * a.cap_in) : x * a.scale2;
+                        } else {
+                            x *= unit[y];
+                            if (a.cap_in != 0.f) x = a.cap_out * tanhf(x);
+                        }
                         if (a.slopes) x = fmaf(-slope[y], static_cast<float>(uc.len - 1 - (p0 + pi)), x);
                         s[2 * n + j] = (valid >> pi) & 1 ? x : -INFINITY;
                     }
