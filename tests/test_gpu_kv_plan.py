@@ -117,3 +117,12 @@ def test_strided_table_and_graph_replay():
         assert np.array_equal(out[0].cpu().numpy(), pos) and np.array_equal(out[1].cpu().numpy(), slot), step
         assert np.array_equal(lens.cpu().numpy(), hl) and int(head) == hh
     assert np.array_equal(table.cpu().numpy(), ht) and int(big[:, 10:].max()) == -1
+
+
+def test_slots_past_32_bits():
+    wsw = need_gpu()
+    seq, add = np.array([70000, 0, 65535]), np.array([3, 2, 2])
+    table = np.full((3, 3), -1)
+    table[0, :2], table[2, 0] = [1 << 30, (1 << 31) - 1], (1 << 31) - 2
+    want = _check(wsw, seq, add, np.array([1 << 29, (1 << 31) - 3]), table, 65536, 8)
+    assert want[6] == 0 and want[2].max() > 1 << 46

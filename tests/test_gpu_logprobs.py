@@ -216,3 +216,12 @@ def test_workspace_reuse_options_and_streams():
     assert all(torch.equal(x, y) for x, y in zip(a, c))
     torch.cuda.synchronize()
     assert int(ws[:2048].view(torch.int32).abs().sum()) == 0, "counters left nonzero"
+
+
+def test_rows_past_32_bits():
+    wsw = need_gpu()
+    ld = (1 << 31) + 4096  # elements between rows
+    buf = torch.empty(2 * ld, dtype=torch.bfloat16, device="cuda")
+    view = buf.view(2, ld)[:, :20001]
+    view.copy_(_normal(11, 2, 20001, "bf16"))
+    _check(wsw, view, [5, 20000], 8, 1.0)

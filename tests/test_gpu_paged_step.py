@@ -102,3 +102,33 @@ def test_a_server_out_of_pages_reports_it(example):
     assert int(s.err) == 8  # the third request got no page
     assert s.lens.tolist() == [1, 1, 0] and s.plan.slots.tolist()[2] == -1
     assert (s.attn[0][2] == 0).all()
+
+
+@pytest.mark.parametrize("cache,pages", [("fp16", 17000), ("q8_0", 33500)])
+def test_a_cache_whose_offsets_pass_32_bits(cache, pages):
+    """Rows written and read past 2^32 bytes (and 2^31 elements) of each buffer equal those of a small cache."""
+    wsw = need_gpu()
+    page, h, d, n, length = 256, 4, 128, 3, 300
+    g = torch.Generator().manual_seed(3)
+    code = torch.int8 if cache == "q8_0" else torch.float16
+
+    def make(count):
+        kv = [torch.empty((count, page, h, d), dtype=code, device="cuda") for _ in range(2)]
+        sc = [torch.empty((count, page, h, d // 32), dtype=torch.float16, device="cuda") for _ in range(2)]
+        return wsw.PagedKV(*kv, *(sc if cache == "q8_0" else (None, None)))
+    rope = wsw.rope_table(d)
+    x = torch.randn(n * length, 3 * h, d, generator=g).cuda()
+    q, k, v = x.split([h, h, h], 1)
+    pos = torch.arange(length).repeat(n)
+    r = torch.arange(n).repeat_interleave(length)
+    res = []
+    for count, ids in ((6, torch.arange(6)), (pages, torch.tensor([0, pages - 1, pages // 2, pages - 2, 1, pages - 3]))):
+        kv = make(count)
+        table = ids.view(3, 2).to(torch.int32)
+        slots = table[r, pos // page].long() * page + pos % page
+        turned = wsw.rope_kv_write(q, k, v, rope, pos.to(torch.int32).cuda(), slots.cuda(), kv)
+        lens = torch.full((n,), length, dtype=torch.int32, device="cuda")
+        res.append((turned, wsw.attn_paged_decode(turned[length - 1::length].contiguous(), kv, table.cuda(), lens)))
+        del kv
+    assert res[1][1].isfinite().all()
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
