@@ -128,6 +128,21 @@ def test_types_widths_and_pairings(x, cache, d, rot, interleaved):
     _check(wsw, x, cache, 37, 6, 2, d, rot, interleaved, nhd=interleaved)
 
 
+@pytest.mark.parametrize("x,cache", [("bf16", "bf16"), ("fp16", "q8_0"), ("fp32", "q8_0"), ("fp32", "fp16")])
+@pytest.mark.parametrize("hq,h,d,rot,interleaved", [
+    (20, 4, 128, 128, False), (20, 2, 128, 96, True), (40, 4, 64, 64, False), (8, 2, 256, 256, False), (24, 1, 128, 40, False),
+    (1, 1, 64, 64, False), (1, 1, 128, 40, True), (3, 1, 128, 128, False), (8, 2, 64, 32, False), (2, 1, 256, 64, True)])
+@pytest.mark.parametrize("tokens", [1024, 2435])
+def test_prompts_of_many_and_few_heads(x, cache, hq, h, d, rot, interleaved, tokens):
+    wsw = need_gpu()
+    g = torch.Generator().manual_seed(tokens)
+    slots = torch.randperm(-(-tokens // 16) * 16 + 32, generator=g)[:tokens]
+    positions = torch.randint(0, 100000, (tokens,), generator=g)
+    unused = torch.rand(tokens, generator=g) < 0.05
+    slots[unused], positions[unused] = -1, -1
+    _check(wsw, x, cache, tokens, hq, h, d, rot, interleaved, nhd=tokens == 1024, slots=slots, positions=positions)
+
+
 @pytest.mark.parametrize("tokens", [1, 2, 255, 2047, 2049, 4099])
 def test_token_counts(tokens):
     wsw = need_gpu()

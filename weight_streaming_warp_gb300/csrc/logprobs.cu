@@ -7,8 +7,8 @@
 //
 // One pass: a thread keeps a running maximum m, S and E in fp32 over its vectors (kept in
 // the log2 domain, e = 2^((x - m) scale log2 e)); when m grows by D (log2 units), S and E
-// become f S and f (E - D S), f = 2^-D.  The rank is a count, taken only in vectors whose
-// maximum reaches the token's logit.
+// become f S and f (E - D S), f = 2^-D.  The rank is a count of the values
+// that reach the token's logit, 16-bit ones compared and counted in pairs.
 //
 // Top k: only values above a threshold that is never above the k-th best of what was seen
 // are kept, their whole 16-byte vector at first, in shared memory.  The first threshold is the k-th largest of the

@@ -30,7 +30,7 @@ namespace wsw {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 2;  // tokens per CTA
+constexpr int kMaxTile = 8;  // tokens per CTA
 
 struct RopeArgs {
     const void *q, *k, *v;
@@ -129,7 +129,7 @@ __device__ __forceinline__ int place(int p, int half, int group) {
     return group == 8 ? (p & 7) * (half >> 3) + (p >> 3) : group == 4 ? (p & 3) * ((half + 3) >> 2) + (p >> 2) : p;
 }
 
-// One CTA for a token or two.  It is bound by the loads in flight, so threads count for more
+// One CTA for a few tokens.  It is bound by the loads in flight, so threads count for more
 // than registers: 8191 tokens of 48 heads, fp32 into binary16, 66 us with 6 CTAs on an SM and 69
 // with 8; bf16 with pairs 20 apart, 56 and 52 us.
 template <typename T, int CT>
@@ -564,18 +564,27 @@ extern "C" int wsw_rope_kv_write(const void *q, const void *k, const void *v, in
     const int64_t passes = (((q_heads + 2 * a.kv.heads) << a.lane_shift) + kThreads - 1) / kThreads;  // of one token
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    // The streaming form wants aligned rows, pairs that fall into whole vectors, and a few tokens
-    // for each CTA.  8191 tokens of 48 heads, streaming and plain form: bf16 40 and 50 us, fp32
-    // into q8_0 60 and 67 us; fp32 into a 16-bit cache 69 and 66 us, so that one stays plain.
+    // The streaming form wants aligned rows, pairs that fall into whole vectors, a few tokens for
+    // each CTA and enough of each token for its threads.  8191 tokens of 48 heads, streaming and
+    // plain form: bf16 40 and 50 us, fp32 into q8_0 60 and 67 us; fp32 into a 16-bit cache 69 and 66
+    // us, so that one stays plain.  bf16 rows of 128: 24 a token 29.2 and 30.5 us, 12 21.2 and
+    // 18.3, 3 19.0 and 8.3.
+    const int64_t vectors = (q_heads + 2 * a.kv.heads) << a.lane_shift;  // 8 values, of one token
     const bool heavy = dtype != WSW_F32 || cache->dtype == WSW_Q8_0;
-    if (tokens >= 1024 && heavy && a.vec && a.vec_out && (interleaved || (rot_dim & 15) == 0)) {
+    if (tokens >= 1024 && heavy && vectors >= 384 && a.vec && a.vec_out && (interleaved || (rot_dim & 15) == 0)) {
         const dim3 all(static_cast<unsigned>(tokens < kStreamCtas * di.sm_count ? tokens : kStreamCtas * di.sm_count));
         if (dtype == WSW_F32) e = launch_stream<float>(a, cache->dtype, all, s, o.pdl);
         else if (dtype == WSW_F16) e = launch_stream<__half>(a, cache->dtype, all, s, o.pdl);
         else e = launch_stream<__nv_bfloat16>(a, cache->dtype, all, s, o.pdl);
         return e == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
     }
-    a.tile = tokens >= 1024 ? kMaxTile : 1;
+    // Tokens of a CTA: two, or so many that its threads have three vectors each (8191 bf16 tokens of 3
+    // rows: 10.0 us with 2, 8.3 with 8), while there are two CTAs for each of 152 SMs (1024 tokens of
+    // 12 rows: 4.4 us with 2, 6.0 with 8).
+    int64_t tile = 3 * kThreads / vectors;
+    if (tile > tokens / 304) tile = tokens / 304;
+    if (tile > kMaxTile) tile = kMaxTile;
+    a.tile = tokens < 1024 ? 1 : tile < 2 ? 2 : static_cast<int>(tile);
     const int64_t slabs = tokens >= 1024 ? 1 : passes;
     const dim3 grid(static_cast<unsigned>((tokens + a.tile - 1) / a.tile),
                     static_cast<unsigned>(slabs < 65535 ? slabs : 65535));
