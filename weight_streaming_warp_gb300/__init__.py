@@ -610,9 +610,10 @@ def rope_kv_write(q, k, v, rope, positions, slots, kv, interleaved=False, out=No
     vp, vt, vh = _rows3(v, dtype, "v", (n, kv.heads, hd))
     if out is None:
         out = torch.empty((n, heads, hd), dtype=dtype, device=q.device)
+    rot = rope.rot_dim
     _check(load().wsw_rope_kv_write(
-        qp, kp, vp, code, n, heads, qt, qh, kt, kh, vt, vh, rope.turns.data_ptr(), rope.rot_dim, rope.mscale,
-        1 if interleaved else 0, _packed(positions, torch.int32, "positions", (n,)),
+        qp, kp, vp, code, n, heads, qt, qh, kt, kh, vt, vh, _packed(rope.turns, torch.int64, "rope.turns", (rot // 2,)),
+        rot, rope.mscale, 1 if interleaved else 0, _packed(positions, torch.int32, "positions", (n,)),
         _packed(slots, torch.int64, "slots", (n,)), _packed(out, dtype, "out", shape), kv._ref,
         None if err_flag is None else _packed(err_flag, torch.int32, "err_flag"), _stream(), _opts(opts)),
         "rope_kv_write")
