@@ -1,9 +1,8 @@
 // abi.cu -- status strings, device queries and option handling for libwsw.so.
-#include <map>
 #include <mutex>
-#include <utility>
 
 #include "common.cuh"
+#include "smem_grant.h"
 
 namespace wsw {
 
@@ -76,21 +75,12 @@ int resolve_opts(const wsw_launch_opts *o, Opts *out) {
 }
 
 cudaError_t ensure_smem(const void *kernel, int bytes) {
-    static std::map<std::pair<const void *, int>, int> granted;
+    static SmemGrants grants;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        auto it = granted.find({kernel, dev});
-        if (it != granted.end() && it->second >= bytes) return cudaSuccess;
-    }
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) {
-        std::lock_guard<std::mutex> lk(g_mu);
-        int &g = granted[{kernel, dev}];
-        if (g < bytes) g = bytes;
-    }
-    return e;
+    return static_cast<cudaError_t>(grants.ensure(kernel, dev, bytes, [kernel](int n) {
+        return static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, n));
+    }));
 }
 
 int load_width(const void *base, int64_t pitch_bytes, int cap) {
