@@ -166,6 +166,10 @@ def _stream():
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
 def _dev(t: torch.Tensor, dtype, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise WswError("%s must be a CUDA tensor" % name)
@@ -444,26 +448,45 @@ _FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # wsw_dtype
 _CACHES = {torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
 
 
+def _home(t, name):
+    """The device index of a call's first tensor.  It is the current device, whose stream the launch
+    takes; the call's other tensors have to lie there, too."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise WswError("%s must be a CUDA tensor" % name)
+    if dev != _current_device():
+        raise WswError("%s is on cuda:%d, which is not the current device" % (name, dev))
+    return dev
+
+
 def _float_dev(t, name):
+    """(type code, device index) of a call's first tensor."""
     code = _FLOATS.get(t.dtype) if isinstance(t, torch.Tensor) and t.is_cuda else None
     if code is None:
         raise WswError("%s must be a CUDA tensor of float32, float16 or bfloat16" % name)
-    return code
+    return code, _home(t, name)
 
 
-def _packed(t, dtype, name, shape=None):
-    """The address of a contiguous device tensor."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+def _on(t, dtype, name, dev):
+    """What is wrong with a tensor that is not `dtype` on device `dev`."""
+    _dev(t, dtype, name)
+    if t.get_device() != dev:
+        raise WswError("%s is on cuda:%d, the call's device is cuda:%d" % (name, t.get_device(), dev))
+
+
+def _packed(t, dtype, name, dev, shape=None):
+    """The address of a contiguous tensor of device `dev`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
             and (shape is None or t.shape == shape)):
         return t.data_ptr()
-    _dev(t, dtype, name)
+    _on(t, dtype, name, dev)
     raise WswError("%s must be contiguous%s" % (name, "" if shape is None else " of shape %s" % (shape,)))
 
 
-def _table(t, n):
+def _table(t, n, dev):
     """(address, pages per row, row stride) of a block table of n requests."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda):
-        _dev(t, torch.int32, "table")
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev):
+        _on(t, torch.int32, "table", dev)
     shape = t.shape
     if len(shape) != 2 or shape[0] != n:
         raise WswError("table must be [requests][max_pages]")
@@ -476,12 +499,19 @@ def _table(t, n):
     return t.data_ptr(), width, max(row, width)
 
 
+def _cache(kv, dev):
+    """The address of a PagedKV's description for a call on device `dev`."""
+    if kv._device != dev:
+        raise WswError("the cache is on cuda:%d, the call's device is cuda:%d" % (kv._device, dev))
+    return kv._ref
+
+
 class PagedKV:
     """A paged KV cache of one layer: pages shared by all requests.  k and v: fp16, bf16 or
     (q8_0) int8, [pages][page_size][heads][head_dim] (layout "nhd") or
     [pages][heads][page_size][head_dim] ("hnd"), any strides but unit in head_dim and the
     same for both; kd and vd: the q8_0 scales, fp16, head_dim / 32 in the last dimension.
-    page_size a power of two, head_dim 64, 128 or 256.  The object holds the tensors."""
+    page_size a power of two, head_dim 64, 128 or 256, all on one device.  The object holds the tensors."""
 
     def __init__(self, k, v, kd=None, vd=None, layout="nhd"):
         if layout not in ("nhd", "hnd"):
@@ -507,6 +537,10 @@ class PagedKV:
             raise WswError("kd and vd belong to an int8 cache")
         self.k, self.v, self.kd, self.vd, self.layout = k, v, kd, vd, layout
         self.num_pages, self.page_size, self.heads, self.head_dim = k.shape[0], k.shape[pos], k.shape[head], k.shape[3]
+        self._device = k.get_device()
+        for t, name in ((v, "v"), (kd, "kd"), (vd, "vd")):
+            if t is not None and t.get_device() != self._device:
+                raise WswError("%s must be on k's device" % name)
         self._c = c
         self._ref = ctypes.addressof(c)
 
@@ -527,25 +561,27 @@ def kv_page_plan(seq_len, new_len, free_pages, head, table, page_size, tokens, o
     get position and slot -1, as do the tokens of a request that does not fit (err_flag,
     an int32 device tensor, tells why: wsw.h).  Returns a KvPlan; out = such a tuple of
     tensors to fill, in which seq_len and head may be the arguments themselves."""
-    sp = _packed(seq_len, torch.int32, "seq_len")
+    dev = _home(seq_len, "seq_len")
+    sp = _packed(seq_len, torch.int32, "seq_len", dev)
     n = seq_len.numel()
-    tp, width, row = _table(table, n)
+    tp, width, row = _table(table, n, dev)
     if out is None:
-        dev = seq_len.device
-        out = KvPlan(torch.empty(tokens, dtype=torch.int32, device=dev),
-                     torch.empty(tokens, dtype=torch.int64, device=dev),
-                     torch.empty(n + 1, dtype=torch.int32, device=dev), torch.empty_like(seq_len),
+        where = seq_len.device
+        out = KvPlan(torch.empty(tokens, dtype=torch.int32, device=where),
+                     torch.empty(tokens, dtype=torch.int64, device=where),
+                     torch.empty(n + 1, dtype=torch.int32, device=where), torch.empty_like(seq_len),
                      torch.empty_like(head))
     elif type(out) is not KvPlan:
         out = KvPlan(*out)
     positions, slots, cu, lens, head_out = out
     _check(load().wsw_kv_page_plan(
-        sp, _packed(new_len, torch.int32, "new_len", (n,)), n, _packed(free_pages, torch.int32, "free_pages"),
-        free_pages.numel(), _packed(head, torch.int32, "head", (1,)), page_size, tp, width, row, tokens,
-        _packed(positions, torch.int32, "positions", (tokens,)), _packed(slots, torch.int64, "slots", (tokens,)),
-        _packed(cu, torch.int32, "cu", (n + 1,)), _packed(lens, torch.int32, "seq_len (out)", (n,)),
-        _packed(head_out, torch.int32, "head (out)", (1,)),
-        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag"), _stream(), _opts(opts)),
+        sp, _packed(new_len, torch.int32, "new_len", dev, (n,)), n,
+        _packed(free_pages, torch.int32, "free_pages", dev), free_pages.numel(),
+        _packed(head, torch.int32, "head", dev, (1,)), page_size, tp, width, row, tokens,
+        _packed(positions, torch.int32, "positions", dev, (tokens,)),
+        _packed(slots, torch.int64, "slots", dev, (tokens,)), _packed(cu, torch.int32, "cu", dev, (n + 1,)),
+        _packed(lens, torch.int32, "seq_len (out)", dev, (n,)), _packed(head_out, torch.int32, "head (out)", dev, (1,)),
+        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag", dev), _stream(), _opts(opts)),
         "kv_page_plan")
     return out
 
@@ -579,10 +615,10 @@ def rope_table(rot_dim, theta=10000.0, scaling=None, factor=1.0, original=0, fre
     return RopeTable(t.to(device), mscale.value, rot_dim)
 
 
-def _rows3(t, dtype, name, shape):
+def _rows3(t, dtype, name, dev, shape):
     """(address, token stride, head stride) of a [tokens][heads][head_dim] view."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda):
-        _dev(t, dtype, name)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev):
+        _on(t, dtype, name, dev)
     if t.shape != shape:
         raise WswError("%s must have shape %s" % (name, shape))
     tok, head, unit = t.stride()
@@ -598,24 +634,25 @@ def rope_kv_write(q, k, v, rope, positions, slots, kv, interleaved=False, out=No
     views with any token and head strides, for instance of one fused QKV row.  rope: a
     RopeTable; positions int32 and slots int64 [tokens], as kv_page_plan gives them.
     interleaved: pairs (2 i, 2 i + 1) instead of (i, i + rot_dim / 2)."""
-    code = _float_dev(q, "q")
+    code, dev = _float_dev(q, "q")
     if q.dim() != 3:
         raise WswError("q must be a [tokens][q_heads][head_dim] view")
     dtype, shape = q.dtype, q.shape
     n, heads, hd = shape
     if hd != kv.head_dim:
         raise WswError("q must have the cache's head_dim")
-    qp, qt, qh = _rows3(q, dtype, "q", shape)
-    kp, kt, kh = _rows3(k, dtype, "k", (n, kv.heads, hd))
-    vp, vt, vh = _rows3(v, dtype, "v", (n, kv.heads, hd))
+    qp, qt, qh = _rows3(q, dtype, "q", dev, shape)
+    kp, kt, kh = _rows3(k, dtype, "k", dev, (n, kv.heads, hd))
+    vp, vt, vh = _rows3(v, dtype, "v", dev, (n, kv.heads, hd))
     if out is None:
         out = torch.empty((n, heads, hd), dtype=dtype, device=q.device)
     rot = rope.rot_dim
     _check(load().wsw_rope_kv_write(
-        qp, kp, vp, code, n, heads, qt, qh, kt, kh, vt, vh, _packed(rope.turns, torch.int64, "rope.turns", (rot // 2,)),
-        rot, rope.mscale, 1 if interleaved else 0, _packed(positions, torch.int32, "positions", (n,)),
-        _packed(slots, torch.int64, "slots", (n,)), _packed(out, dtype, "out", shape), kv._ref,
-        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag"), _stream(), _opts(opts)),
+        qp, kp, vp, code, n, heads, qt, qh, kt, kh, vt, vh,
+        _packed(rope.turns, torch.int64, "rope.turns", dev, (rot // 2,)), rot, rope.mscale, 1 if interleaved else 0,
+        _packed(positions, torch.int32, "positions", dev, (n,)), _packed(slots, torch.int64, "slots", dev, (n,)),
+        _packed(out, dtype, "out", dev, shape), _cache(kv, dev),
+        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag", dev), _stream(), _opts(opts)),
         "rope_kv_write")
     return out
 
@@ -636,14 +673,14 @@ def attn_paged_decode(q, kv, table, lens, scale=None, softcap=0.0, window=0, slo
     exponentials.  A request of length 0 gives zeros and -inf.  ws: a uint8 device tensor
     of at least attn_paged_decode_workspace_bytes(...) bytes, zero-filled before its first
     use (every call leaves it ready for the next), allocated if None."""
-    code = _float_dev(q, "q")
+    code, dev = _float_dev(q, "q")
     if q.dim() != 3 or not q.is_contiguous():
         raise WswError("q must be a contiguous [requests][q_heads][head_dim] tensor")
     shape = q.shape
     n, heads, hd = shape
     if hd != kv.head_dim or heads % kv.heads != 0:
         raise WswError("q must have the cache's head_dim and a multiple of its heads")
-    tp, width, row = _table(table, n)
+    tp, width, row = _table(table, n, dev)
     if scale is None:
         scale = 1.0 / float(hd) ** 0.5
     if out is None:
@@ -652,12 +689,12 @@ def attn_paged_decode(q, kv, table, lens, scale=None, softcap=0.0, window=0, slo
         ws = torch.zeros(attn_paged_decode_workspace_bytes(n, heads, kv.heads, hd), dtype=torch.uint8,
                          device=q.device)
     _check(load().wsw_attn_paged_decode(
-        q.data_ptr(), code, n, heads, kv._ref, tp, width, row, _packed(lens, torch.int32, "lens", (n,)), scale, softcap,
-        window, None if slopes is None else _packed(slopes, torch.float32, "slopes", (heads,)),
-        _packed(out, q.dtype, "out", shape),
-        None if lse is None else _packed(lse, torch.float32, "lse", (n, heads)),
-        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag"),
-        _packed(ws, torch.uint8, "ws"), ws.numel(), _stream(), _opts(opts)), "attn_paged_decode")
+        q.data_ptr(), code, n, heads, _cache(kv, dev), tp, width, row, _packed(lens, torch.int32, "lens", dev, (n,)),
+        scale, softcap, window, None if slopes is None else _packed(slopes, torch.float32, "slopes", dev, (heads,)),
+        _packed(out, q.dtype, "out", dev, shape),
+        None if lse is None else _packed(lse, torch.float32, "lse", dev, (n, heads)),
+        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag", dev),
+        _packed(ws, torch.uint8, "ws", dev), ws.numel(), _stream(), _opts(opts)), "attn_paged_decode")
     return out
 
 
@@ -690,29 +727,29 @@ def token_logprobs(logits, tokens=None, top=0, scale=1.0, out=None, ws=None, opt
     (out = one to fill).  ws: a uint8 device tensor of at least
     token_logprobs_workspace_bytes(...) bytes, zero-filled before its first use, allocated
     if None."""
-    code = _float_dev(logits, "logits")
+    code, dev = _float_dev(logits, "logits")
     rows, vocab, ld = _rowmajor(logits, "logits")
     if out is None:
         out = token_logprobs_out(rows, top, tokens is not None, logits.device)
     logprob, rank, lse, entropy, top_logprob, top_id = out
     tp = lp = rp = bp = ip = wp = None
     if tokens is not None:
-        tp = _packed(tokens, torch.int32, "tokens", (rows,))
-        lp = _packed(logprob, torch.float32, "logprob", (rows,))
-        rp = _packed(rank, torch.int32, "rank", (rows,))
+        tp = _packed(tokens, torch.int32, "tokens", dev, (rows,))
+        lp = _packed(logprob, torch.float32, "logprob", dev, (rows,))
+        rp = _packed(rank, torch.int32, "rank", dev, (rows,))
     if top:
-        bp = _packed(top_logprob, torch.float32, "top_logprob", (rows, top))
-        ip = _packed(top_id, torch.int32, "top_id", (rows, top))
+        bp = _packed(top_logprob, torch.float32, "top_logprob", dev, (rows, top))
+        ip = _packed(top_id, torch.int32, "top_id", dev, (rows, top))
     if ws is None:
         need = token_logprobs_workspace_bytes(rows, vocab, top)
         if need:
             ws = torch.zeros(need, dtype=torch.uint8, device=logits.device)
     if ws is not None:
-        wp = _packed(ws, torch.uint8, "ws")
+        wp = _packed(ws, torch.uint8, "ws", dev)
     _check(load().wsw_token_logprobs(
-        logits.data_ptr(), code, rows, vocab, ld, tp, scale, top, lp, rp, _packed(lse, torch.float32, "lse", (rows,)),
-        _packed(entropy, torch.float32, "entropy", (rows,)), bp, ip, wp, 0 if wp is None else ws.numel(), _stream(),
-        _opts(opts)), "token_logprobs")
+        logits.data_ptr(), code, rows, vocab, ld, tp, scale, top, lp, rp,
+        _packed(lse, torch.float32, "lse", dev, (rows,)), _packed(entropy, torch.float32, "entropy", dev, (rows,)), bp, ip,
+        wp, 0 if wp is None else ws.numel(), _stream(), _opts(opts)), "token_logprobs")
     return out
 
 
