@@ -531,9 +531,10 @@ typedef enum wsw_rope_scaling {
 
 /*
  * wsw_rope_table -- host: the per-pair frequencies of wsw_rope_kv_write in fractions of a
- * turn, turns[i] = round(2^64 * f_i / (2 pi)), and the factor on cos and sin.  A
- * position's angle is then the exact 64-bit product position * turns[i] modulo one turn,
- * as good at position 2^30 as at 1.
+ * turn, turns[i] = round(2^64 * f_i / (2 pi)) with f_i carried to some 100 bits, and the
+ * factor on cos and sin.  A position's angle is then the exact 64-bit product position *
+ * turns[i] modulo one turn: the table's rounding makes it wrong by position * 2^-65 turns at
+ * most, 7e-10 radians at position 2^31.
  *   freqs    NULL, or rot_dim / 2 radians per position of the caller's own, in [0, 2 pi):
  *            they are taken as given and theta, scaling, factor, original ignored.
  *   turns    host uint64 [rot_dim / 2];  mscale: host float.

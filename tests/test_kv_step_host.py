@@ -155,3 +155,45 @@ def test_binding_refuses_host_tensors():
                  lambda: wsw.kv_page_plan(torch.zeros(2, dtype=torch.int32), None, None, None, None, 16, 4)):
         with pytest.raises(wsw.WswError):
             call()
+
+
+# 2 pi to 60 digits
+TWO_PI = "6.28318530717958647692528676655900576839433879875021164194989"
+
+
+@pytest.mark.parametrize("rot,theta,scaling,factor,original", [
+    (128, 10000.0, None, 1.0, 0), (256, 1e6, None, 1.0, 0), (2, 100.0, None, 1.0, 0), (64, 500000.0, "linear", 8.0, 0),
+    (96, 1234.5, "linear", 3.7, 0), (128, 10000.0, "ntk", 4.0, 0), (4, 10000.0, "ntk", 2.5, 0), (250, 1e6, "ntk", 16.0, 0),
+    (128, 10000.0, "by_parts", 4.0, 32768), (256, 1e6, "by_parts", 40.0, 4096), (64, 1.0000001, None, 1.0, 0),
+    (128, 1e300, None, 1.0, 0),
+    (6, 1e308, "ntk", 1e100, 0)])
+def test_rope_table_against_40_digits(lib, rot, theta, scaling, factor, original):
+    """The table is the definition's turns rounded to whole 2^-64 turns, so that position times
+    turns is off by half a position 2^-64 turns: 7e-10 radians at position 2^31.  (Frequencies in
+    doubles are off by f 2^-53 or more: 3e-7 radians there.)"""
+    import decimal
+    with decimal.localcontext(decimal.Context(prec=50)):
+        D = decimal.Decimal
+        two_pi, unit = D(TWO_PI), D(2) ** 64
+        t = wsw.rope_table(rot, theta, scaling, factor, original, device="cpu")
+        got = [int(x) for x in t.turns.numpy().view(np.uint64)]
+        for i in range(rot // 2):
+            base = D(theta) * (D(factor) ** (D(rot) / D(rot - 2)) if scaling == "ntk" else 1)
+            f = base ** (D(-2 * i) / D(rot))
+            if scaling == "linear":
+                f /= D(factor)
+            if scaling == "by_parts":
+                keep = min(max((D(original) * f / two_pi - 1) / 31, D(0)), D(1))
+                f = keep * f + (1 - keep) * f / D(factor)
+            # beside the rounding, 2^-90 of the value for the way there
+            assert abs(got[i] - f / two_pi * unit) <= D(0.5) + D(2) ** -90 * unit, i
+
+
+def test_own_frequencies_against_40_digits(lib):
+    import decimal
+    f = [6.28, 1.0, 0.3, 1e-3, 1e-9, 2.0 ** -60, 5e-324, 0.0]
+    t = wsw.rope_table(16, freqs=f, device="cpu")
+    with decimal.localcontext(decimal.Context(prec=50)):
+        D = decimal.Decimal
+        for got, want in zip(t.turns.numpy().view(np.uint64), f):
+            assert abs(int(got) - D(want) / D(TWO_PI) * D(2) ** 64) <= D(0.5) + D(2) ** -26

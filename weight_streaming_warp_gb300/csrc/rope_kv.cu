@@ -1,5 +1,5 @@
 // rope_kv.cu -- rotary positions of q and k fused with the write of k and v into the paged
-// KV cache, and the host table of frequencies.
+// KV cache (the host table of frequencies: rope_table.cu).
 //
 // Pair (x0, x1) of a head at position p turns by the angle a = p f:
 //   (x0, x1) -> m (x0 cos a - x1 sin a, x1 cos a + x0 sin a)
@@ -477,37 +477,6 @@ cudaError_t launch_rope(const RopeArgs &a, int cache_type, dim3 grid, cudaStream
 
 }  // namespace
 }  // namespace wsw
-
-extern "C" int wsw_rope_table(int64_t rot_dim, double theta, int32_t scaling, double factor, int64_t original,
-                              const double *freqs, uint64_t *turns, float *mscale) {
-    constexpr double kTwoPi = 6.283185307179586476925;
-    if (!turns || !mscale || rot_dim < 2 || rot_dim > 256 || (rot_dim & 1)) return WSW_ERR_INVALID_ARG;
-    if (freqs) {
-        scaling = WSW_ROPE_PLAIN;
-    } else {
-        if (scaling < WSW_ROPE_PLAIN || scaling > WSW_ROPE_BY_PARTS || !std::isfinite(theta) || !(theta > 1))
-            return WSW_ERR_INVALID_ARG;
-        if (scaling != WSW_ROPE_PLAIN && (!std::isfinite(factor) || !(factor >= 1))) return WSW_ERR_INVALID_ARG;
-        if (scaling == WSW_ROPE_NTK && rot_dim <= 2) return WSW_ERR_INVALID_ARG;
-        if (scaling == WSW_ROPE_BY_PARTS && original < 1) return WSW_ERR_INVALID_ARG;
-        if (scaling == WSW_ROPE_NTK) theta *= std::pow(factor, rot_dim / (rot_dim - 2.0));
-    }
-    for (int64_t i = 0; i < rot_dim / 2; ++i) {
-        double f = freqs ? freqs[i] : std::pow(theta, -2.0 * static_cast<double>(i) / static_cast<double>(rot_dim));
-        if (scaling == WSW_ROPE_LINEAR) f /= factor;
-        if (scaling == WSW_ROPE_BY_PARTS) {
-            const double t = (static_cast<double>(original) * f / kTwoPi - 1.0) / 31.0;  // turns: 1 .. 32
-            const double keep = t < 0 ? 0 : t > 1 ? 1 : t;
-            f = keep * f + (1 - keep) * f / factor;
-        }
-        if (!(f >= 0 && f < kTwoPi)) return WSW_ERR_INVALID_ARG;
-        // f / 2 pi < 1, and 2^64 - 2048 is the largest double below 2^64
-        const double x = std::nearbyint(std::ldexp(f / kTwoPi, 64));
-        turns[i] = x < 18446744073709549568.0 ? static_cast<uint64_t>(x) : 18446744073709549568ull;
-    }
-    *mscale = scaling == WSW_ROPE_BY_PARTS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
-    return WSW_OK;
-}
 
 extern "C" int wsw_rope_kv_write(const void *q, const void *k, const void *v, int32_t dtype, int64_t tokens,
                                  int64_t q_heads, int64_t q_tok_stride, int64_t q_head_stride, int64_t k_tok_stride,
