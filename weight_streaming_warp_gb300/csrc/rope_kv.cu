@@ -8,7 +8,9 @@
 //
 // Angles: p f in fp32 is off by p f 2^-24 radians, 0.06 at p = 10^6 and f = 1.  The table
 // holds f in fractions of a turn as 64-bit fixed point, so p * turns modulo 2^64 drops the
-// whole turns exactly; its top 32 bits (2^-32 of a turn) go to sincospi.  One 64-bit
+// whole turns exactly.  Its top 24 bits are an fp32 value for sincospi; the next 32, an angle d below
+// 4e-7, turn the result once more by first order (cos d = 1 - 7e-14): all 32 bits in one
+// rounded fp32 value were off by 9e-8 radians.  One 64-bit
 // integer product replaces an FP64 one, which this part runs at a sixtieth of fp32's rate.
 // Each (token, pair) is computed once per CTA and shared by all heads through shared memory.
 //
@@ -123,6 +125,16 @@ __device__ __forceinline__ void store8(T *p, bool vec, const float (&x)[8]) {
     }
 }
 
+// (cos, sin) of a position's angle, `turns` of a pair's 2^-64 turns each
+__device__ __forceinline__ float2 cos_sin(int32_t position, uint64_t turns) {
+    const uint64_t turn = static_cast<uint64_t>(position < 0 ? 0 : position) * turns;
+    const int32_t top = static_cast<int32_t>(turn >> 32) & ~0xff;  // a signed fraction: half turns in [-1, 1)
+    const float d = static_cast<float>(static_cast<uint32_t>(turn >> 8)) * 8.7196712e-17f;  // pi 2^-55
+    float s, c;
+    sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+    return make_float2(fmaf(-s, d, c), fmaf(c, d, s));
+}
+
 // Where pair p's (cos, sin) sits among a token's: neighbouring lanes read neighbouring places at
 // every step of their loops (a plain order is an eight-way bank conflict).
 __device__ __forceinline__ int place(int p, int half, int group) {
@@ -146,13 +158,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 8) rope_kv_kern
     pdl_wait();
     for (int i = tid; i < tile * half; i += kThreads) {
         const int tt = i / half, pair = i - tt * half;
-        const int32_t p = a.positions[t0 + tt];
-        const uint64_t turn = static_cast<uint64_t>(p < 0 ? 0 : p) * a.turns[pair];
-        // the top 32 bits as a signed fraction: half turns in [-1, 1)
-        const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31
-        float s, c;
-        sincospif(x, &s, &c);
-        cs[tt][place(pair, half, group)] = make_float2(a.mscale * c, a.mscale * s);
+        const float2 z = cos_sin(a.positions[t0 + tt], a.turns[pair]);
+        cs[tt][place(pair, half, group)] = make_float2(a.mscale * z.x, a.mscale * z.y);
     }
     if (tid < tile) {
         pos_sm[tid] = a.positions[t0 + tid];
@@ -354,12 +361,8 @@ __global__ void __launch_bounds__(kThreads, kStreamCtas) rope_stream_kernel(cons
             if (tid == kThreads - 1) slot_ahead = a.slots[token(i + 1)];
         }
         if (tid < half) {
-            const uint64_t at = static_cast<uint64_t>(p < 0 ? 0 : p) * turn;
-            // the top 32 bits as a signed fraction: half turns in [-1, 1)
-            const float x = static_cast<float>(static_cast<int32_t>(at >> 32)) * 4.656612873077393e-10f;  // 2^-31
-            float s, c;
-            sincospif(x, &s, &c);
-            cs[i & 1][place(tid, half, group)] = make_float2(a.mscale * c, a.mscale * s);
+            const float2 z = cos_sin(p, turn);
+            cs[i & 1][place(tid, half, group)] = make_float2(a.mscale * z.x, a.mscale * z.y);
         }
         if (tid == kThreads - 1) {
             Token w{-1, 0, p};
