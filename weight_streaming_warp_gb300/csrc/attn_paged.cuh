@@ -34,8 +34,9 @@
 // share a 16-row operand as high parts (rows 0..7) and residuals (8..15) of q and of the
 // weights; 9 to 16 take 16 rows and a second product for the residuals; more take several
 // passes over the pair.  The maximum in use is raised, and the sums rescaled, only when a tile
-// exceeds it by more than kLazy; the weights, then up to 2^(kLazy + kShift), stay in binary16's
-// range (a weight is off by 2^-22 of itself or 2^-32 of the largest).  A query row enters
+// exceeds it by more than kLazy; binary16 weights, then up to 2^(kLazy + shift), stay in its
+// range (a weight is off by 2^-22 of itself or 2^-32 of the largest).  bf16 weights end at 1 there:
+// a value sum overflows where the sum of the values themselves would.  A query row enters
 // binary16 times the power of two that brings its largest value to 2^14 .. 2^15, so that any fp32
 // or bf16 row keeps 22 bits.  q8_0 rows stay codes in shared memory and become binary16(scale *
 // code) in registers, the value the one-pass dequantizer writes.
@@ -54,7 +55,6 @@ constexpr int kPair = 4;       // tiles that the beginning and end of a pair cou
 constexpr float kLazy = 8.f;   // log2: the running maximum may lag by so much
 constexpr int kGroup = 12;     // CTAs whose records are joined first
 constexpr int kCtas = 152;     // runs of the tile list: one CTA per SM of a 152-SM part
-constexpr float kShift = 7.f;  // log2 of the weights' scale
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kSmemMax = 226 * 1024;
 
@@ -105,6 +105,7 @@ struct Cfg {
     static constexpr int ring = stages * stage;
     // the joins at the end keep weights where q was, or behind the rings
     static constexpr int smem = warps * (ring + q_bytes) + (q_bytes == 0 ? 4096 : 0);
+    static constexpr float shift = CT == WSW_BF16 ? -kLazy : 7.f;  // log2 of the weights' scale
     static constexpr int rec = D + 4;                   // floats of a CTA's record row: m, l, 2 pad, sums
     // of a warp's: sums, padded against bank conflicts if two records fit into the warp's ring
     static constexpr int srec = 2 * RT * (D + 4) * 4 <= ring ? D + 4 : D;
@@ -194,8 +195,8 @@ __device__ __forceinline__ void store_out4(const Args &a, int64_t i, float4 v) {
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + i) =
             make_uint2(pack16(a.dtype, v.x, v.y), pack16(a.dtype, v.z, v.w));
 }
-__device__ __forceinline__ float lse_of(float m, float l) {
-    return l == 0.f ? -INFINITY : (m + log2f(l) - kShift) * kLn2;
+__device__ __forceinline__ float lse_of(float m, float l, float shift) {
+    return l == 0.f ? -INFINITY : (m + log2f(l) - shift) * kLn2;
 }
 // weight of a record with maximum m against the common maximum
 __device__ __forceinline__ float weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 al[y] = raise ? ex2(m[y] - mt) : 1.f;
                 raised |= raise;
                 if (raise) m[y] = mt;
-                const float ref = m[y] == -INFINITY ? 0.f : m[y] - kShift;  // nothing seen yet: all weights 0
+                const float ref = m[y] == -INFINITY ? 0.f : m[y] - C::shift;  // nothing seen yet: all weights 0
                 float sum = 0.f;
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
@@ -825,7 +826,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                     for (int x = 0; x < 2; ++x) v[n][x] = (RT == 8 ? o[n][x] + o[n][2 + x] : o[n][2 * y + x]) * f;
                 if (tq == 0) {
                     if (!whole) piece_ml[2 * warp + run_end][row] = make_float2(m[y], l[y]);
-                    else if (a.lse) a.lse[head] = lse_of(m[y], l[y]);
+                    else if (a.lse) a.lse[head] = lse_of(m[y], l[y], C::shift);
                 }
                 // lane tq's dimensions: 2 tq, 2 tq + 1 of every eight, or (q8_0) 4 tq .. 4 tq + 3 of sixteen
                 if (!whole || a.dtype == WSW_F32) {
@@ -945,7 +946,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
                 const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
                 store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
-                if (c4 == 0 && a.lse) a.lse[head] = lse_of(ml.x, ml.y);
+                if (c4 == 0 && a.lse) a.lse[head] = lse_of(ml.x, ml.y, C::shift);
             } else {
                 float *r = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec + row * C::rec;
                 *reinterpret_cast<float4 *>(r + 4 + 4 * c4) = s;
@@ -1059,7 +1060,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                     const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
                     const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
                     store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
-                    if (c4 == 0 && a.lse) a.lse[head] = lse_of(ml.x, ml.y);
+                    if (c4 == 0 && a.lse) a.lse[head] = lse_of(ml.x, ml.y, C::shift);
                 } else {
                     // the group's record takes the place of its first CTA's: this thread has read
                     // what it writes, and everyone the (m, l)
