@@ -45,7 +45,7 @@ def calls(monkeypatch):
             return lambda *a: made.append(name) or 0
 
     monkeypatch.setattr(wsw, "load", Library)
-    monkeypatch.setattr(wsw, "_stream", lambda: 0)
+    monkeypatch.setattr(wsw, "_raw_stream", lambda device: 0)
     monkeypatch.setattr(wsw, "_current_device", lambda: 0)
     return made
 

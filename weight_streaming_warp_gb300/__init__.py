@@ -31,6 +31,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libwsw.so")
 _lib = None
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # none in a torch without CUDA
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _i64, _i32, _p, _f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
 
 
@@ -163,11 +165,7 @@ def _opts(opts):
 
 def _stream():
     """The current stream's handle (torch's raw accessor: a Stream object costs 3 us to make)."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-
-
-def _current_device():
-    return torch._C._cuda_getDevice()
+    return _raw_stream(_current_device())
 
 
 def _dev(t: torch.Tensor, dtype, name):
@@ -445,26 +443,28 @@ def attn_prefill_q8_0(q, kq, kd, vq, vd, window, scale=None, out=None, ws=None, 
 # ------------------------------------------------- a step around a paged KV cache ----
 
 _FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # wsw_dtype
+_I32, _I64, _F32, _U8, _Tensor = torch.int32, torch.int64, torch.float32, torch.uint8, torch.Tensor
 _CACHES = {torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}
 
 
 def _home(t, name):
     """The device index of a call's first tensor.  It is the current device, whose stream the launch
     takes; the call's other tensors have to lie there, too."""
-    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    dev = t.get_device() if isinstance(t, _Tensor) else -1
     if dev < 0:
         raise WswError("%s must be a CUDA tensor" % name)
-    if dev != _current_device():
-        raise WswError("%s is on cuda:%d, which is not the current device" % (name, dev))
-    return dev
+    if dev == _current_device():
+        return dev
+    raise WswError("%s is on cuda:%d, which is not the current device" % (name, dev))
 
 
 def _float_dev(t, name):
     """(type code, device index) of a call's first tensor."""
-    code = _FLOATS.get(t.dtype) if isinstance(t, torch.Tensor) and t.is_cuda else None
-    if code is None:
+    code = _FLOATS.get(t.dtype) if isinstance(t, _Tensor) else None
+    if code is None or not t.is_cuda:
         raise WswError("%s must be a CUDA tensor of float32, float16 or bfloat16" % name)
-    return code, _home(t, name)
+    dev = t.get_device()
+    return code, dev if dev == _current_device() else _home(t, name)
 
 
 def _on(t, dtype, name, dev):
@@ -476,7 +476,7 @@ def _on(t, dtype, name, dev):
 
 def _packed(t, dtype, name, dev, shape=None):
     """The address of a contiguous tensor of device `dev`."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
             and (shape is None or t.shape == shape)):
         return t.data_ptr()
     _on(t, dtype, name, dev)
@@ -485,8 +485,8 @@ def _packed(t, dtype, name, dev, shape=None):
 
 def _table(t, n, dev):
     """(address, pages per row, row stride) of a block table of n requests."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev):
-        _on(t, torch.int32, "table", dev)
+    if not (isinstance(t, _Tensor) and t.dtype is _I32 and t.get_device() == dev):
+        _on(t, _I32, "table", dev)
     shape = t.shape
     if len(shape) != 2 or shape[0] != n:
         raise WswError("table must be [requests][max_pages]")
@@ -499,11 +499,8 @@ def _table(t, n, dev):
     return t.data_ptr(), width, max(row, width)
 
 
-def _cache(kv, dev):
-    """The address of a PagedKV's description for a call on device `dev`."""
-    if kv._device != dev:
-        raise WswError("the cache is on cuda:%d, the call's device is cuda:%d" % (kv._device, dev))
-    return kv._ref
+def _elsewhere(kv, dev):
+    raise WswError("the cache is on cuda:%d, the call's device is cuda:%d" % (kv._device, dev))
 
 
 class PagedKV:
@@ -562,7 +559,7 @@ def kv_page_plan(seq_len, new_len, free_pages, head, table, page_size, tokens, o
     an int32 device tensor, tells why: wsw.h).  Returns a KvPlan; out = such a tuple of
     tensors to fill, in which seq_len and head may be the arguments themselves."""
     dev = _home(seq_len, "seq_len")
-    sp = _packed(seq_len, torch.int32, "seq_len", dev)
+    sp = _packed(seq_len, _I32, "seq_len", dev)
     n = seq_len.numel()
     tp, width, row = _table(table, n, dev)
     if out is None:
@@ -575,13 +572,13 @@ def kv_page_plan(seq_len, new_len, free_pages, head, table, page_size, tokens, o
         out = KvPlan(*out)
     positions, slots, cu, lens, head_out = out
     _check(load().wsw_kv_page_plan(
-        sp, _packed(new_len, torch.int32, "new_len", dev, (n,)), n,
-        _packed(free_pages, torch.int32, "free_pages", dev), free_pages.numel(),
-        _packed(head, torch.int32, "head", dev, (1,)), page_size, tp, width, row, tokens,
-        _packed(positions, torch.int32, "positions", dev, (tokens,)),
-        _packed(slots, torch.int64, "slots", dev, (tokens,)), _packed(cu, torch.int32, "cu", dev, (n + 1,)),
-        _packed(lens, torch.int32, "seq_len (out)", dev, (n,)), _packed(head_out, torch.int32, "head (out)", dev, (1,)),
-        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag", dev), _stream(), _opts(opts)),
+        sp, _packed(new_len, _I32, "new_len", dev, (n,)), n,
+        _packed(free_pages, _I32, "free_pages", dev), free_pages.numel(),
+        _packed(head, _I32, "head", dev, (1,)), page_size, tp, width, row, tokens,
+        _packed(positions, _I32, "positions", dev, (tokens,)),
+        _packed(slots, _I64, "slots", dev, (tokens,)), _packed(cu, _I32, "cu", dev, (n + 1,)),
+        _packed(lens, _I32, "seq_len (out)", dev, (n,)), _packed(head_out, _I32, "head (out)", dev, (1,)),
+        None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _raw_stream(dev), _opts(opts)),
         "kv_page_plan")
     return out
 
@@ -617,7 +614,7 @@ def rope_table(rot_dim, theta=10000.0, scaling=None, factor=1.0, original=0, fre
 
 def _rows3(t, dtype, name, dev, shape):
     """(address, token stride, head stride) of a [tokens][heads][head_dim] view."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev):
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev):
         _on(t, dtype, name, dev)
     if t.shape != shape:
         raise WswError("%s must have shape %s" % (name, shape))
@@ -641,18 +638,20 @@ def rope_kv_write(q, k, v, rope, positions, slots, kv, interleaved=False, out=No
     n, heads, hd = shape
     if hd != kv.head_dim:
         raise WswError("q must have the cache's head_dim")
-    qp, qt, qh = _rows3(q, dtype, "q", dev, shape)
+    qt, qh, unit = q.stride()
+    if unit != 1:
+        raise WswError("q must have unit stride in head_dim")
     kp, kt, kh = _rows3(k, dtype, "k", dev, (n, kv.heads, hd))
     vp, vt, vh = _rows3(v, dtype, "v", dev, (n, kv.heads, hd))
     if out is None:
         out = torch.empty((n, heads, hd), dtype=dtype, device=q.device)
     rot = rope.rot_dim
     _check(load().wsw_rope_kv_write(
-        qp, kp, vp, code, n, heads, qt, qh, kt, kh, vt, vh,
-        _packed(rope.turns, torch.int64, "rope.turns", dev, (rot // 2,)), rot, rope.mscale, 1 if interleaved else 0,
-        _packed(positions, torch.int32, "positions", dev, (n,)), _packed(slots, torch.int64, "slots", dev, (n,)),
-        _packed(out, dtype, "out", dev, shape), _cache(kv, dev),
-        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag", dev), _stream(), _opts(opts)),
+        q.data_ptr(), kp, vp, code, n, heads, qt, qh, kt, kh, vt, vh,
+        _packed(rope.turns, _I64, "rope.turns", dev, (rot // 2,)), rot, rope.mscale, 1 if interleaved else 0,
+        _packed(positions, _I32, "positions", dev, (n,)), _packed(slots, _I64, "slots", dev, (n,)),
+        _packed(out, dtype, "out", dev, shape), kv._ref if kv._device == dev else _elsewhere(kv, dev),
+        None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _raw_stream(dev), _opts(opts)),
         "rope_kv_write")
     return out
 
@@ -689,12 +688,13 @@ def attn_paged_decode(q, kv, table, lens, scale=None, softcap=0.0, window=0, slo
         ws = torch.zeros(attn_paged_decode_workspace_bytes(n, heads, kv.heads, hd), dtype=torch.uint8,
                          device=q.device)
     _check(load().wsw_attn_paged_decode(
-        q.data_ptr(), code, n, heads, _cache(kv, dev), tp, width, row, _packed(lens, torch.int32, "lens", dev, (n,)),
-        scale, softcap, window, None if slopes is None else _packed(slopes, torch.float32, "slopes", dev, (heads,)),
+        q.data_ptr(), code, n, heads, kv._ref if kv._device == dev else _elsewhere(kv, dev), tp, width, row,
+        _packed(lens, _I32, "lens", dev, (n,)), scale, softcap, window,
+        None if slopes is None else _packed(slopes, _F32, "slopes", dev, (heads,)),
         _packed(out, q.dtype, "out", dev, shape),
-        None if lse is None else _packed(lse, torch.float32, "lse", dev, (n, heads)),
-        None if err_flag is None else _packed(err_flag, torch.int32, "err_flag", dev),
-        _packed(ws, torch.uint8, "ws", dev), ws.numel(), _stream(), _opts(opts)), "attn_paged_decode")
+        None if lse is None else _packed(lse, _F32, "lse", dev, (n, heads)),
+        None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev),
+        _packed(ws, _U8, "ws", dev), ws.numel(), _raw_stream(dev), _opts(opts)), "attn_paged_decode")
     return out
 
 
@@ -734,22 +734,22 @@ def token_logprobs(logits, tokens=None, top=0, scale=1.0, out=None, ws=None, opt
     logprob, rank, lse, entropy, top_logprob, top_id = out
     tp = lp = rp = bp = ip = wp = None
     if tokens is not None:
-        tp = _packed(tokens, torch.int32, "tokens", dev, (rows,))
-        lp = _packed(logprob, torch.float32, "logprob", dev, (rows,))
-        rp = _packed(rank, torch.int32, "rank", dev, (rows,))
+        tp = _packed(tokens, _I32, "tokens", dev, (rows,))
+        lp = _packed(logprob, _F32, "logprob", dev, (rows,))
+        rp = _packed(rank, _I32, "rank", dev, (rows,))
     if top:
-        bp = _packed(top_logprob, torch.float32, "top_logprob", dev, (rows, top))
-        ip = _packed(top_id, torch.int32, "top_id", dev, (rows, top))
+        bp = _packed(top_logprob, _F32, "top_logprob", dev, (rows, top))
+        ip = _packed(top_id, _I32, "top_id", dev, (rows, top))
     if ws is None:
         need = token_logprobs_workspace_bytes(rows, vocab, top)
         if need:
             ws = torch.zeros(need, dtype=torch.uint8, device=logits.device)
     if ws is not None:
-        wp = _packed(ws, torch.uint8, "ws", dev)
+        wp = _packed(ws, _U8, "ws", dev)
     _check(load().wsw_token_logprobs(
         logits.data_ptr(), code, rows, vocab, ld, tp, scale, top, lp, rp,
-        _packed(lse, torch.float32, "lse", dev, (rows,)), _packed(entropy, torch.float32, "entropy", dev, (rows,)), bp, ip,
-        wp, 0 if wp is None else ws.numel(), _stream(), _opts(opts)), "token_logprobs")
+        _packed(lse, _F32, "lse", dev, (rows,)), _packed(entropy, _F32, "entropy", dev, (rows,)), bp, ip,
+        wp, 0 if wp is None else ws.numel(), _raw_stream(dev), _opts(opts)), "token_logprobs")
     return out
 
 
