@@ -1,8 +1,10 @@
 """Paged decode attention at the ends of its types' ranges, against the formula in 64 bits (the
 inputs, bounds and check of test_gpu_attn_paged)."""
+import numpy as np
 import pytest
 import torch
 
+import kv_step_ref as ref
 from helpers import need_gpu
 from test_gpu_attn_paged import Case
 
@@ -17,3 +19,26 @@ def test_bf16_values_near_the_largest(d, group, q):
     c.kv.v.copy_(c.kv.v.double() * 2.0 ** 122)
     c.vals[1] *= 2.0 ** 122
     c.check()
+
+
+@pytest.mark.parametrize("cache,page", [("fp16", 8), ("q8_0", 16)])
+def test_the_last_positions_that_there_can_be(cache, page):
+    """Lengths just below 2^31 - 4096.  The window keeps the work small; the block table is as long
+    as the length."""
+    wsw = need_gpu()
+    pages = ((1 << 31) - 4096) // page
+    length, window, kvh, group, d = pages * page - 3, 100, 2, 4, 128
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").remainder_(3)[None]
+    c = Case(wsw, [3 * page], kvh=kvh, group=group, cache=cache, page=page, extra=0, seed=page)
+    c.lens_d.fill_(length)
+    c.table_d = table
+    out, lse = c.run(window=window)
+    p = np.arange(length - window, length)
+    rows = p // page % 3 * page + p % page
+    want, wl, mag, terms = ref.attend(c.q[0].double().numpy(), c.vals[0][rows], c.vals[1][rows], d ** -0.5)
+    # test_gpu_attn_paged's bounds, with its bf16 terms
+    e = terms * (2.0 ** -17 + (d / 16 + 2) * 2.0 ** -23) + 2.0 ** -22
+    lim = mag * (2 * e + 2.0 ** -17 + 8 * 2.0 ** -23) + 2.0 ** -24 * np.abs(want) + 2.0 ** -25
+    assert (np.abs(out[0].double().cpu().numpy() - want) <= lim).all()
+    lim = e + 2.0 ** -22 + 8 * 2.0 ** -23 + 2.0 ** -22 * np.abs(wl)
+    assert (np.abs(lse[0].double().cpu().numpy() - wl) <= lim).all()

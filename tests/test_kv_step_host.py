@@ -197,3 +197,14 @@ def test_own_frequencies_against_40_digits(lib):
         D = decimal.Decimal
         for got, want in zip(t.turns.numpy().view(np.uint64), f):
             assert abs(int(got) - D(want) / D(TWO_PI) * D(2) ** 64) <= D(0.5) + D(2) ** -26
+
+
+def test_attention_refuses_tables_that_reach_two_to_the_31(lib):
+    """Tiles and windows of the table run past the last position: 2^31 - 4096 of them at most."""
+    most = (1 << 31) - 4096
+    for page, pages in ((1, most + 1), (1, (1 << 31) - 1), (8, (1 << 28) - 1), (16, (1 << 27) - 255), (4096, 1 << 19)):
+        assert pages * page > most
+        assert _attn(lib, cache=_cache(page_size=page), pages=pages, ts=pages, window=1) == UNSUPPORTED
+    for page, pages in ((1, most), (16, (1 << 27) - 256), (4096, (1 << 19) - 1)):  # the next refusal, as they pass this one
+        assert pages * page <= most
+        assert _attn(lib, cache=_cache(page_size=page), pages=pages, ts=pages, window=1, q=None) == INVALID
