@@ -507,8 +507,8 @@ typedef struct wsw_kv_cache {
  *   len_out, head_out may be seq_len and head themselves: every length is read before
  *                     one is written.
  *   err_flag          int32 [1] or NULL; bits are ORed in, never cleared.
- *   requests <= 16384, page_size a power of two <= 65536, tokens and max_pages < 2^31
- *   (WSW_ERR_UNSUPPORTED otherwise).  requests == 0 plans no token.
+ *   requests <= 16384, page_size a power of two <= 65536, tokens <= 2^31 - 2^20, n_free <
+ *   2^31 - 1, max_pages < 2^31 (WSW_ERR_UNSUPPORTED otherwise).  requests == 0 plans no token.
  */
 int wsw_kv_page_plan(const int32_t *seq_len, const int32_t *new_len, int64_t requests, const int32_t *free_pages,
                      int64_t n_free, const int32_t *head, int64_t page_size, int32_t *table, int64_t max_pages,

@@ -208,3 +208,13 @@ def test_attention_refuses_tables_that_reach_two_to_the_31(lib):
     for page, pages in ((1, most), (16, (1 << 27) - 256), (4096, (1 << 19) - 1)):  # the next refusal, as they pass this one
         assert pages * page <= most
         assert _attn(lib, cache=_cache(page_size=page), pages=pages, ts=pages, window=1, q=None) == INVALID
+
+
+def test_plan_refuses_tokens_that_reach_two_to_the_31(lib):
+    """Threads step in rounds of up to 65536 places past the last token: 2^31 - 2^20 at most."""
+    def plan(tokens, seq=A):
+        return lib.wsw_kv_page_plan(seq, A, 4, A, 8, A, 16, A, 8, 8, tokens, A, A, A, A, A, None, None, None)
+    most = (1 << 31) - (1 << 20)
+    for tokens in (most + 1, (1 << 31) - 3, (1 << 31) - 2):
+        assert plan(tokens) == UNSUPPORTED
+    assert plan(most, seq=P(4097)) == MISALIGNED  # the next refusal

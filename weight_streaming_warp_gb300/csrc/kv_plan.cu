@@ -271,7 +271,11 @@ extern "C" int wsw_kv_page_plan(const int32_t *seq_len, const int32_t *new_len, 
         return WSW_ERR_INVALID_ARG;
     if (requests > 0 && (!seq_len || !new_len || !len_out || (max_pages > 0 && !table))) return WSW_ERR_INVALID_ARG;
     constexpr int64_t lim = int64_t(1) << 31;
-    if (requests > kMaxRequests || tokens >= lim - 1 || n_free >= lim - 1 || max_pages >= lim || page_size > 65536 ||
+    // threads step in rounds of up to 4 * 16 * kThreads places, the last one past the tokens and the new pages
+    // (no more than the tokens): it stays below 2^31
+    constexpr int64_t most = lim - (int64_t(1) << 20);
+    static_assert(4 * 16 * kThreads < (1 << 20), "rounds");
+    if (requests > kMaxRequests || tokens > most || n_free >= lim - 1 || max_pages >= lim || page_size > 65536 ||
         (page_size & (page_size - 1)))
         return WSW_ERR_UNSUPPORTED;
     const uintptr_t al = reinterpret_cast<uintptr_t>(seq_len) | reinterpret_cast<uintptr_t>(new_len) |
