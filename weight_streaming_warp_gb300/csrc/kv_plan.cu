@@ -9,16 +9,16 @@
 // Two exclusive scans over the requests, then independent writes; the bytes (16 per
 // request, 12 per token) are a few hundred nanoseconds of HBM time at any size served, so
 // the launch and the dependent steps (lengths, two scans, table entry, slot) are the time.
-// One launch of one cluster: every CTA scans all the requests into its own shared memory
-// (no exchange, no workspace), a cluster barrier puts every length read before the first
-// write, so that the new lengths may overwrite the old, and the CTAs share the writes.
+// One launch of one cluster, of 16 CTAs where the device holds one, else 8: every CTA scans all the
+// requests into its own shared memory (no exchange, no workspace), a cluster barrier puts every
+// length read before the first write, so that the new lengths may overwrite the old (a call whose
+// lengths go elsewhere takes the same form), and the CTAs share the writes.
 // The sums saturate just beyond what can be served, so they fit in 32 bits whatever the
 // lengths.  A thread takes four consecutive tokens (one while there are threads for all): one binary search in shared memory (a
 // search for each token made 130000 tokens of 1000 requests bound by instructions, 18 us), one
 // table read for each page that they touch.  64 requests of one token each take 3.9 us, 130000
 // tokens of 1000 requests 10.5 us (clusters of 8 CTAs 13.7 us).
-#include <atomic>
-
+#include "cluster_choice.h"
 #include "common.cuh"
 
 namespace wsw {
@@ -240,17 +240,37 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
     }
 }
 
-// More than eight CTAs in a cluster are an option of the kernel, set once per device.
-cudaError_t cluster_of_16(const void *kernel) {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+constexpr int kMaxSmem = (3 * kMaxRequests + 2) * 4;
+
+// Sets the kernel's options on the current device, once, and says how many CTAs a cluster can have.
+cudaError_t cluster_ctas(int device, unsigned *ctas) {
+    static ClusterChoice choice;
+    const void *kernel = reinterpret_cast<const void *>(kv_plan_kernel);
+    const cudaError_t e = ensure_smem(kernel, kMaxSmem);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (done.load() & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) done.fetch_or(bit);
-    return e;
+    *ctas = choice.of(device, [kernel] {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 16;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kMaxSmem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        return clusters > 0;
+    });
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -297,16 +317,11 @@ extern "C" int wsw_kv_page_plan(const int32_t *seq_len, const int32_t *new_len, 
     a.shift = 0;
     while ((int64_t(1) << a.shift) < page_size) ++a.shift;
     const int smem = static_cast<int>((3 * requests + 2) * 4);
-    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kv_plan_kernel), smem);
-    if (e != cudaSuccess) return WSW_ERR_CUDA;
+    unsigned ncta = 1;
+    if (cluster_ctas(di.device, &ncta) != cudaSuccess) return WSW_ERR_CUDA;
+    if (tokens <= 2048) ncta = 1;  // while its threads see few tokens each, else the largest cluster
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    // one CTA while its threads see few tokens each, else the largest cluster
-    const unsigned ncta = tokens > 2048 ? 16 : 1;
-    if (ncta > 8) {
-        e = cluster_of_16(reinterpret_cast<const void *>(kv_plan_kernel));
-        if (e != cudaSuccess) return WSW_ERR_CUDA;
-    }
     const int64_t want = requests > tokens / ncta ? requests : tokens / ncta;
     cfg.gridDim = dim3(ncta);
     cfg.blockDim = dim3(want > 512 ? kThreads : want > 128 ? 512 : 128);
