@@ -592,7 +592,8 @@ int wsw_rope_kv_write(const void *q, const void *k, const void *v, int32_t dtype
  * on tensor cores in the cache's 16-bit type (binary16 for q8_0); q and the softmax
  * weights enter as a high part plus a residual in that type, so that they keep about 22
  * bits (binary16; a query row times a power of two of its own, so any finite row; a weight
- * is off by 2^-22 of itself or 2^-32 of the row's largest) or 16 bits (bf16; a bf16 q is exact).
+ * is off by 2^-22 of itself or 2^-32 of the row's largest) or 16 bits (bf16 under 16-bit
+ * queries, which are exact).  Under fp32 queries over bf16 they are three parts, exact.
  *
  *   q, out    `dtype` (WSW_F32, WSW_F16 or WSW_BF16) [requests][q_heads][head_dim], packed,
  *             16-byte aligned; q_heads = group * cache->heads, any group >= 1.

@@ -6,9 +6,10 @@
 namespace wsw {
 namespace paged {
 
-template <> cudaError_t launch_type<WSW_F16>(const Args &, int, cudaStream_t, bool, int64_t);
-template <> cudaError_t launch_type<WSW_BF16>(const Args &, int, cudaStream_t, bool, int64_t);
-template <> cudaError_t launch_type<WSW_Q8_0>(const Args &, int, cudaStream_t, bool, int64_t);
+template <> cudaError_t launch_type<WSW_F16, false>(const Args &, int, cudaStream_t, bool, int64_t);
+template <> cudaError_t launch_type<WSW_BF16, false>(const Args &, int, cudaStream_t, bool, int64_t);
+template <> cudaError_t launch_type<WSW_BF16, true>(const Args &, int, cudaStream_t, bool, int64_t);
+template <> cudaError_t launch_type<WSW_Q8_0, false>(const Args &, int, cudaStream_t, bool, int64_t);
 
 namespace {
 constexpr size_t kCounterBytes = 2048;
@@ -95,8 +96,9 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
     if (!device_info(&di, &st)) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (cache->dtype == WSW_F16) e = launch_type<WSW_F16>(a, rows, s, o.pdl, tiles);
-    else if (cache->dtype == WSW_BF16) e = launch_type<WSW_BF16>(a, rows, s, o.pdl, tiles);
-    else e = launch_type<WSW_Q8_0>(a, rows, s, o.pdl, tiles);
+    if (cache->dtype == WSW_F16) e = launch_type<WSW_F16, false>(a, rows, s, o.pdl, tiles);
+    else if (cache->dtype == WSW_Q8_0) e = launch_type<WSW_Q8_0, false>(a, rows, s, o.pdl, tiles);
+    else if (dtype == WSW_F32) e = launch_type<WSW_BF16, true>(a, rows, s, o.pdl, tiles);
+    else e = launch_type<WSW_BF16, false>(a, rows, s, o.pdl, tiles);
     return e == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
 }

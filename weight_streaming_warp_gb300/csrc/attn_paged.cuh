@@ -38,7 +38,10 @@
 // range (a weight is off by 2^-22 of itself or 2^-32 of the largest).  bf16 weights end at 1 there:
 // a value sum overflows where the sum of the values themselves would.  A query row enters
 // binary16 times the power of two that brings its largest value to 2^14 .. 2^15, so that any fp32
-// or bf16 row keeps 22 bits.  q8_0 rows stay codes in shared memory and become binary16(scale *
+// or bf16 row keeps 22 bits.  Over bf16 pages two parts are 16 bits, enough for a 16-bit result and
+// exact for a 16-bit q; under fp32 queries q and the weights are three parts, exact, with one product more
+// each (with two: results off by 4e-6.  32 x 32768, group 8: 175 us, with two parts 181; 64 ragged of group
+// 10 126 and 113, three short ones 10.3 and 9.3 us).  q8_0 rows stay codes in shared memory and become binary16(scale *
 // code) in registers, the value the one-pass dequantizer writes.
 #pragma once
 
@@ -80,8 +83,9 @@ struct Args {
     int dtype;                             // of q and out
 };
 
-// Shape of one variant: cache type, head_dim, query rows (8 or 16).
-template <int CT, int D, int RT>
+// Shape of one variant: cache type, head_dim, query rows (8 or 16), third parts of q and the weights
+// (bf16 pages under fp32 queries).
+template <int CT, int D, int RT, bool X3>
 struct Cfg {
     static constexpr bool q8 = CT == WSW_Q8_0;
     // q8_0 is bound by the instructions that turn codes into values: tiles of 32 positions share
@@ -99,7 +103,8 @@ struct Cfg {
     static constexpr int ksteps = D / 16;
     static constexpr bool q_smem = D == 256;            // q's high parts: registers if they fit
     static constexpr int qfrag = ksteps * 512;          // bytes of one warp's A fragments
-    static constexpr int q_bytes = (q_smem ? qfrag : 0) + (RT == 16 ? qfrag : 0);
+    static constexpr int xfrag = X3 && q_smem ? ksteps * RT * 32 : 0;  // of q's third parts: as q's high parts
+    static constexpr int q_bytes = (q_smem ? qfrag : 0) + (RT == 16 ? qfrag : 0) + xfrag;
     static constexpr int fit = (kSmemMax - warps * q_bytes) / (warps * stage);
     static constexpr int stages = fit < 6 ? fit : 6;
     static constexpr int ring = stages * stage;
@@ -152,6 +157,16 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same with an operand of third parts: rows 0..7 alone where the other rows are residuals
+template <int CT, int RT>
+__device__ __forceinline__ void mma_third(float (&d)[4], const uint32_t (&t)[RT / 4], uint32_t b0, uint32_t b1) {
+    if constexpr (RT == 8) {
+        const uint32_t a[4] = {t[0], 0u, t[1], 0u};
+        mma<CT>(d, a, b0, b1);
+    } else {
+        mma<CT>(d, t, b0, b1);
+    }
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -172,6 +187,14 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
         const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
         lo = *reinterpret_cast<const uint32_t *>(&l);
     }
+}
+// (x, y) as three pairs of bf16, exact: each cut leaves the bits that the next ones take
+__device__ __forceinline__ void split3(float x, float y, uint32_t &hi, uint32_t &lo, uint32_t &third) {
+    hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+    x -= bf16lo(hi);
+    y -= bf16hi(hi);
+    lo = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+    third = __byte_perm(__float_as_uint(x - bf16lo(lo)), __float_as_uint(y - bf16hi(lo)), 0x7632);
 }
 // Two codes, bytes `sel` picks from w (biased by 128), times the scales in d: 0x6400 + u is
 // 1024 + u in binary16, so both steps before the product are exact.
@@ -243,9 +266,9 @@ __device__ __forceinline__ void advance(const Args &a, Cursor &c, int extra) {
     while (c.nt == 0 && r + 1 < a.requests);
 }
 
-template <int CT, int D, int RT>
-__global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(const __grid_constant__ Args a) {
-    using C = Cfg<CT, D, RT>;
+template <int CT, int D, int RT, bool X3>
+__global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_kernel(const __grid_constant__ Args a) {
+    using C = Cfg<CT, D, RT, X3>;
     constexpr int W = C::warps, NT = C::threads, T = C::tile;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int2 scan[W];
@@ -360,6 +383,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     unsigned char *qsm = smem + W * C::ring + warp * C::q_bytes;
     uint4 *q_hi_sm = reinterpret_cast<uint4 *>(qsm);
     uint4 *q_lo_sm = reinterpret_cast<uint4 *>(qsm + (C::q_smem ? C::qfrag : 0));
+    uint32_t *q_third_sm = reinterpret_cast<uint32_t *>(qsm + C::q_bytes - C::xfrag);
 
     if (wb < we) {
         Cursor uc;  // the tile in use
@@ -475,6 +499,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
         };
         const int gq = lane >> 2, tq = lane & 3;
         uint32_t qa[C::q_smem ? 1 : C::ksteps][4];
+        uint32_t q3[X3 && !C::q_smem ? C::ksteps : 1][RT / 4];  // third parts, of rows 0..7 (and 8..15)
         float m[RT / 8], l[RT / 8], slope[RT / 8];
         float unit[RT / 8];  // of a score's product sum, over softcap if that is used (not bf16)
         float o[D / 8][4];
@@ -566,14 +591,15 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 #pragma unroll
                     for (int j = 0; j < kB; ++j) {
                         const int kt = k0 + j;
-                        uint32_t hi[4], lo[4];
+                        uint32_t hi[4], lo[4], third[RT / 4];
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {  // the fragment's two column halves
 #pragma unroll
                             for (int y = 0; y < RT / 8; ++y) {
                                 const float2 v = qv[j][x][y];
                                 uint32_t vh, vl;
-                                split<CT>(v.x * up[y], v.y * up[y], vh, vl);
+                                if constexpr (X3) split3(v.x, v.y, vh, vl, third[x * (RT / 8) + y]);
+                                else split<CT>(v.x * up[y], v.y * up[y], vh, vl);
                                 if constexpr (RT == 8) {
                                     hi[2 * x] = vh;
                                     hi[2 * x + 1] = vl;
@@ -590,6 +616,13 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                             for (int i = 0; i < 4; ++i) qa[kt][i] = hi[i];
                         }
                         if constexpr (RT == 16) q_lo_sm[kt * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        if constexpr (X3) {
+#pragma unroll
+                            for (int i = 0; i < RT / 4; ++i) {
+                                if constexpr (C::q_smem) q_third_sm[(kt * (RT / 4) + i) * 32 + lane] = third[i];
+                                else q3[kt][i] = third[i];
+                            }
+                        }
                     }
                 }
                 if constexpr (RT == 16) q_lo = __any_sync(WSW_FULL_MASK, some);
@@ -635,6 +668,12 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                         const uint32_t ql[4] = {u.x, u.y, u.z, u.w};
                         mma<CT>(d, ql, b0, b1);
                     }
+                }
+                if constexpr (X3) {
+                    uint32_t t[RT / 4];
+#pragma unroll
+                    for (int i = 0; i < RT / 4; ++i) t[i] = C::q_smem ? q_third_sm[(kt * (RT / 4) + i) * 32 + lane] : q3[C::q_smem ? 0 : kt][i];
+                    mma_third<CT, RT>(d, t, b0, b1);
                 }
             };
             if constexpr (!C::q8) {
@@ -688,7 +727,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
 
             // ---- softmax: lane (gq, tq) holds positions 8 n + 2 tq + {0, 1} of rows gq, gq + 8
             const int p0 = uc.start + uc.t * T;
-            uint32_t ph[NB / 2][4], pl[NB / 2][4];
+            uint32_t ph[NB / 2][4], pl[NB / 2][4], pt[NB / 2][RT / 4];
             float al[RT / 8];
             bool raised = false;
 #pragma unroll
@@ -724,8 +763,9 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 for (int n = 0; n < NB; ++n) {
                     const float p_0 = ex2(s[2 * n] - ref), p_1 = ex2(s[2 * n + 1] - ref);
                     sum += p_0 + p_1;
-                    if constexpr (RT == 8) split<CT>(p_0, p_1, ph[n / 2][2 * (n & 1)], ph[n / 2][2 * (n & 1) + 1]);
-                    else split<CT>(p_0, p_1, ph[n / 2][2 * (n & 1) + y], pl[n / 2][2 * (n & 1) + y]);
+                    uint32_t &hi = ph[n / 2][2 * (n & 1) + y], &lo = RT == 8 ? ph[n / 2][2 * (n & 1) + 1] : pl[n / 2][2 * (n & 1) + y];
+                    if constexpr (X3) split3(p_0, p_1, hi, lo, pt[n / 2][(n & 1) * (RT / 8) + y]);
+                    else split<CT>(p_0, p_1, hi, lo);
                 }
                 l[y] = fmaf(l[y], al[y], sum);
             }
@@ -745,6 +785,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
                 auto add = [&](int n, uint32_t b0, uint32_t b1) {
                     mma<CT>(o[n], ph[t16], b0, b1);
                     if constexpr (RT == 16) mma<CT>(o[n], pl[t16], b0, b1);
+                    if constexpr (X3) mma_third<CT, RT>(o[n], pt[t16], b0, b1);
                 };
                 const int vpos = 16 * t16 + 8 * (mi & 1) + mr;
                 if constexpr (!C::q8) {
@@ -1078,30 +1119,31 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT>::threads, 1) attn_paged_kernel(
     }
 }
 
-template <int CT>
+template <int CT, bool X3>
 cudaError_t launch_type(const Args &a, int rows, cudaStream_t s, bool pdl, int64_t tiles);
 
-template <int CT, int D, int RT>
+template <int CT, int D, int RT, bool X3>
 cudaError_t launch_one(const Args &a, cudaStream_t s, bool pdl, int64_t tiles) {
-    using C = Cfg<CT, D, RT>;
-    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attn_paged_kernel<CT, D, RT>), C::smem);
+    using C = Cfg<CT, D, RT, X3>;
+    const auto kernel = attn_paged_kernel<CT, D, RT, X3>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), C::smem);
     if (e != cudaSuccess) return e;
     // no more CTAs than `tiles`, the most that there can be, fill
     const int64_t want = (tiles + C::warps - 1) / C::warps, ctas = want < 1 ? 1 : want > kCtas ? kCtas : want;
-    return launch(attn_paged_kernel<CT, D, RT>, dim3(static_cast<unsigned>(ctas)), dim3(C::threads), C::smem, s, pdl, a);
+    return launch(kernel, dim3(static_cast<unsigned>(ctas)), dim3(C::threads), C::smem, s, pdl, a);
 }
 
-#define WSW_PAGED_TYPE(CT)                                                                       \
-    template <>                                                                                  \
-    cudaError_t launch_type<CT>(const Args &a, int rows, cudaStream_t s, bool pdl, int64_t tiles) {   \
-        switch (a.kv.head_dim * 2 + (rows == 16)) {                                              \
-            case 128: return launch_one<CT, 64, 8>(a, s, pdl, tiles);                             \
-            case 129: return launch_one<CT, 64, 16>(a, s, pdl, tiles);                            \
-            case 256: return launch_one<CT, 128, 8>(a, s, pdl, tiles);                            \
-            case 257: return launch_one<CT, 128, 16>(a, s, pdl, tiles);                           \
-            case 512: return launch_one<CT, 256, 8>(a, s, pdl, tiles);                            \
-            default: return launch_one<CT, 256, 16>(a, s, pdl, tiles);                            \
-        }                                                                                        \
+#define WSW_PAGED_TYPE(CT, X3)                                                                       \
+    template <>                                                                                      \
+    cudaError_t launch_type<CT, X3>(const Args &a, int rows, cudaStream_t s, bool pdl, int64_t tiles) {   \
+        switch (a.kv.head_dim * 2 + (rows == 16)) {                                                  \
+            case 128: return launch_one<CT, 64, 8, X3>(a, s, pdl, tiles);                             \
+            case 129: return launch_one<CT, 64, 16, X3>(a, s, pdl, tiles);                            \
+            case 256: return launch_one<CT, 128, 8, X3>(a, s, pdl, tiles);                            \
+            case 257: return launch_one<CT, 128, 16, X3>(a, s, pdl, tiles);                           \
+            case 512: return launch_one<CT, 256, 8, X3>(a, s, pdl, tiles);                            \
+            default: return launch_one<CT, 256, 16, X3>(a, s, pdl, tiles);                            \
+        }                                                                                            \
     }
 
 }  // namespace paged

@@ -4,6 +4,6 @@
 
 namespace wsw {
 namespace paged {
-WSW_PAGED_TYPE(WSW_BF16)
+WSW_PAGED_TYPE(WSW_BF16, false)
 }  // namespace paged
 }  // namespace wsw

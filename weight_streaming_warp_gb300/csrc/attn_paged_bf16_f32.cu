@@ -1,0 +1,9 @@
+// attn_paged_bf16_f32.cu -- the paged decode attention over bf16 pages (one translation unit per
+// cache type: they compile side by side).
+#include "attn_paged.cuh"
+
+namespace wsw {
+namespace paged {
+WSW_PAGED_TYPE(WSW_BF16, true)
+}  // namespace paged
+}  // namespace wsw

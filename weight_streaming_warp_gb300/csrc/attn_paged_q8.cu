@@ -4,6 +4,6 @@
 
 namespace wsw {
 namespace paged {
-WSW_PAGED_TYPE(WSW_Q8_0)
+WSW_PAGED_TYPE(WSW_Q8_0, false)
 }  // namespace paged
 }  // namespace wsw
