@@ -42,3 +42,12 @@ def test_the_last_positions_that_there_can_be(cache, page):
     assert (np.abs(out[0].double().cpu().numpy() - want) <= lim).all()
     lim = e + 2.0 ** -22 + 8 * 2.0 ** -23 + 2.0 ** -22 * np.abs(wl)
     assert (np.abs(lse[0].double().cpu().numpy() - wl) <= lim).all()
+
+
+@pytest.mark.parametrize("cache,q", [("fp16", "fp32"), ("bf16", "fp32"), ("bf16", "bf16"), ("q8_0", "fp16")])
+@pytest.mark.parametrize("softcap", [1e38, 3e38])
+def test_a_cap_near_the_largest_number_is_none(cache, q, softcap):
+    wsw = need_gpu()
+    c = Case(wsw, [1, 40, 300], cache=cache, q=q)
+    for got, want in zip(c.run(softcap=softcap), c.run()):
+        assert torch.equal(got, want)

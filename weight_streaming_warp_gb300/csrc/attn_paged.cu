@@ -1,4 +1,5 @@
 // attn_paged.cu -- host entry of the paged decode attention (kernel: attn_paged.cuh).
+#include <cfloat>
 #include <cmath>
 
 #include "attn_paged.cuh"
@@ -74,8 +75,12 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
     a.err = err_flag;
     a.table_stride = table_stride;
     a.scale2 = scale * kLog2e;
-    a.cap_in = softcap > 0.f ? scale / softcap : 0.f;
-    a.cap_out = softcap * kLog2e;
+    // A cap so large that softcap log2 e or scale / softcap leaves fp32's normal range bends only scores of
+    // |q . K| above 2^114: none.  (As a cap, inf * tanh(0) made every result NaN.)
+    const float in = softcap > 0.f ? scale / softcap : 0.f;
+    const bool capped = std::isfinite(softcap * kLog2e) && std::fabs(in) >= FLT_MIN;
+    a.cap_in = capped ? in : 0.f;
+    a.cap_out = capped ? softcap * kLog2e : 0.f;
     a.requests = static_cast<int>(requests);
     a.q_heads = static_cast<int>(q_heads);
     a.group = static_cast<int>(q_heads / cache->heads);
