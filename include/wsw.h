@@ -602,7 +602,7 @@ int wsw_rope_kv_write(const void *q, const void *k, const void *v, int32_t dtype
  *   lens      int32 [requests]; below 0 or above max_pages * page_size is cut to that
  *             range and sets bit 1.
  *   lse       fp32 [requests][q_heads] or NULL;  slopes fp32 [q_heads] or NULL.
- *   scale     finite; softcap finite, >= 0;  0 <= window < 2^31.
+ *   scale     scale * log2(e) finite in fp32; softcap finite, >= 0;  0 <= window < 2^31.
  *   ws        device workspace of ws_bytes >= wsw_attn_paged_decode_workspace_bytes(...)
  *             bytes, 16-byte aligned, zero-filled before its first use and then reused:
  *             its arrival counters are zero again after every call.  Two calls in flight
@@ -633,7 +633,7 @@ int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t requests, int64_
  *   logits   `dtype` (WSW_F32, WSW_F16 or WSW_BF16) [rows][ld], ld >= vocab, aligned to
  *            its element.
  *   tokens   int32 [rows], or NULL with logprob and rank NULL.
- *   scale    finite, > 0 (1 / temperature).
+ *   scale    > 0 (1 / temperature), scale * log2(e) finite in fp32.
  *   top      0 .. 32, at most vocab; with 0 top_logprob and top_id may be NULL.
  *   logprob, lse, entropy fp32 [rows];  rank int32 [rows];  top_logprob fp32 and top_id
  *            int32 [rows][top].

@@ -218,3 +218,14 @@ def test_plan_refuses_tokens_that_reach_two_to_the_31(lib):
     for tokens in (most + 1, (1 << 31) - 3, (1 << 31) - 2):
         assert plan(tokens) == UNSUPPORTED
     assert plan(most, seq=P(4097)) == MISALIGNED  # the next refusal
+
+
+def test_scales_whose_log2_form_overflows_are_refused(lib):
+    """scale * log2 e has to be finite, too: 0 times an infinite one is NaN."""
+    for scale in (3.4e38, -3.4e38, 2.4e38):
+        assert _attn(lib, scale=scale) == INVALID
+    assert _attn(lib, scale=2.3e38, lens=P(4097)) == MISALIGNED and _attn(lib, scale=-2.3e38, lens=P(4097)) == MISALIGNED
+
+    def lp(scale, x=A):
+        return lib.wsw_token_logprobs(x, 0, 2, 100, 100, A, scale, 5, A, A, A, A, A, A, None, 0, None, None)
+    assert lp(3.4e38) == INVALID and lp(2.4e38) == INVALID and lp(2.3e38, x=P(4098)) == MISALIGNED

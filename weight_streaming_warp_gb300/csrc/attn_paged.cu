@@ -49,7 +49,7 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
     if (st != WSW_OK) return st;
     if (dtype != WSW_F32 && dtype != WSW_F16 && dtype != WSW_BF16) return WSW_ERR_UNSUPPORTED;
     if (requests < 0 || q_heads < 1 || q_heads % a.kv.heads != 0 || max_pages < 0 || table_stride < max_pages ||
-        !std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
+        !std::isfinite(scale * kLog2e) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
         return WSW_ERR_INVALID_ARG;
     constexpr int64_t lim = int64_t(1) << 31;
     // Positions and page numbers are 32 bits: a tile's positions and a window of 64 + 32 table entries run

@@ -706,7 +706,7 @@ extern "C" int wsw_token_logprobs(const void *logits, int32_t dtype, int64_t row
     int st = resolve_opts(opts, &o);
     if (st != WSW_OK) return st;
     if (dtype != WSW_F32 && dtype != WSW_F16 && dtype != WSW_BF16) return WSW_ERR_UNSUPPORTED;
-    if (rows < 0 || vocab < 1 || ld < vocab || !std::isfinite(scale) || !(scale > 0.f) || top < 0 || top > vocab)
+    if (rows < 0 || vocab < 1 || ld < vocab || !std::isfinite(scale * kLog2e) || !(scale > 0.f) || top < 0 || top > vocab)
         return WSW_ERR_INVALID_ARG;
     constexpr int64_t lim = int64_t(1) << 31;
     if (top > kMaxTop || vocab >= lim - 65536 || rows >= lim) return WSW_ERR_UNSUPPORTED;
