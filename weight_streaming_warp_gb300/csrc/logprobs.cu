@@ -3,7 +3,8 @@
 //
 //   y_j = scale x_j;  lse = ln sum exp(y_j);  logprob = y_t - lse
 //   entropy = ln S - E / S with S = sum e_j, E = sum e_j (y_j - m), e_j = exp(y_j - m)
-//   (-sum p ln p with p = e / S; it stays exact for a peaked row, where both terms are small)
+//   (-sum p ln p with p = e / S; a peaked row's terms are both small, which leaves an absolute error of
+//   about 2^-24: what of S - 1 is below that is lost in S)
 //
 // One pass: a thread keeps a running maximum m, S and E in fp32 over its vectors (kept in
 // the log2 domain, e = 2^((x - m) scale log2 e)); when m grows by D (log2 units), S and E
@@ -668,7 +669,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) logprobs_ker
     finish(a, sm, row, xt);
 }
 
-// Splits of a row: about kTargetCtas CTAs over all rows, each of 4096 values or more.
+// Splits of a row: about kTargetCtas CTAs over all rows, each of 4096 values or more.  From 305 rows on
+// each is one CTA's.  Rows of 152064 bf16 values, one CTA each and split over 1824 CTAs: with 5 alternatives 305
+// rows 42 and 39 us, 400 44 and 47, 608 51 and 60, 912 69 and 79; without them 33 and 28, 35 and 33, 43 and 44, 60
+// and 61 us.
 void split_rows(int64_t rows, int64_t vocab, int *splits, int *chunk) {
     int64_t n = kTargetCtas / rows;
     const int64_t most = (vocab + 4095) / 4096;

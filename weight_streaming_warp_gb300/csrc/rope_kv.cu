@@ -538,9 +538,10 @@ extern "C" int wsw_rope_kv_write(const void *q, const void *k, const void *v, in
     cudaError_t e;
     // The streaming form wants aligned rows, pairs that fall into whole vectors, a few tokens for
     // each CTA and enough of each token for its threads.  8191 tokens of 48 heads, streaming and
-    // plain form: bf16 40 and 50 us, fp32 into q8_0 60 and 67 us; fp32 into a 16-bit cache 69 and 66
-    // us, so that one stays plain.  bf16 rows of 128: 24 a token 29.2 and 30.5 us, 12 21.2 and
-    // 18.3, 3 19.0 and 8.3.
+    // plain form: bf16 41 and 55 us, fp32 into q8_0 61 and 70 us; fp32 into a 16-bit cache 69 and 66
+    // us, so that one stays plain.  bf16 rows of 128: 24 a token 29.1 and 31.8 us, 12 21.2 and
+    // 18.3, 3 19.0 and 8.3.  1024 and 1500 tokens of 48 heads: bf16 6.8 and 10.7, 10.3 and 14.5 us, fp32 into
+    // q8_0 12.4 and 13.9, 15.4 and 16.3 us; of 24 rows 5.4 and 6.4, 7.0 and 7.7 us.
     const int64_t vectors = (q_heads + 2 * a.kv.heads) << a.lane_shift;  // 8 values, of one token
     const bool heavy = dtype != WSW_F32 || cache->dtype == WSW_Q8_0;
     if (tokens >= 1024 && heavy && vectors >= 384 && a.vec && a.vec_out && (interleaved || (rot_dim & 15) == 0)) {
