@@ -607,7 +607,8 @@ int wsw_rope_kv_write(const void *q, const void *k, const void *v, int32_t dtype
  *             bytes, 16-byte aligned, zero-filled before its first use and then reused:
  *             its arrival counters are zero again after every call.  Two calls in flight
  *             at once need two workspaces.
- *   requests <= 65535 and requests * q_heads < 2^31;  max_pages * page_size <= 2^31 - 4096;
+ *   requests <= 65535, requests * q_heads < 2^31 and q_heads * head_dim / 4 <= 2^31 - 4096;
+ *   max_pages * page_size <= 2^31 - 4096;
  *   requests * kv heads * ceil(max_pages * page_size / 16) < 2^31 (with more than 16
  *   query heads per KV head, times ceil(group / 16); with a window, min(window, ...)).
  * One launch; results depend on the arguments alone, not on the launch or the device.

@@ -229,3 +229,11 @@ def test_scales_whose_log2_form_overflows_are_refused(lib):
     def lp(scale, x=A):
         return lib.wsw_token_logprobs(x, 0, 2, 100, 100, A, scale, 5, A, A, A, A, A, A, None, 0, None, None)
     assert lp(3.4e38) == INVALID and lp(2.4e38) == INVALID and lp(2.3e38, x=P(4098)) == MISALIGNED
+
+
+def test_attention_refuses_rows_beyond_32_bits(lib):
+    """The zeros of a request of no tokens are counted in vectors of four with 32 bits."""
+    one = _cache(heads=1, head_dim=256, pos_stride=256, head_stride=256)
+    most = ((1 << 31) - 4096) // 64
+    assert _attn(lib, cache=one, n=1, heads=most + 1) == UNSUPPORTED
+    assert _attn(lib, cache=one, n=1, heads=most, q=None) == INVALID  # the next refusal

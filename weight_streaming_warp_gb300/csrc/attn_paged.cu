@@ -55,7 +55,7 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
     // Positions and page numbers are 32 bits: a tile's positions and a window of 64 + 32 table entries run
     // past the last position (page_size 1: an entry's number past 2^31 - 1 was read at a negative offset).
     constexpr int64_t most = lim - 4096;
-    if (requests > 65535 || requests * q_heads >= lim || max_pages > most || (max_pages << a.kv.page_shift) > most ||
+    if (requests > 65535 || requests * q_heads >= lim || q_heads * (a.kv.head_dim / 4) > most || max_pages > most || (max_pages << a.kv.page_shift) > most ||
         window >= lim)
         return WSW_ERR_UNSUPPORTED;
     if (requests == 0) return WSW_OK;
