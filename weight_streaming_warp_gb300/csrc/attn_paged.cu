@@ -52,11 +52,12 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
         !std::isfinite(scale * kLog2e) || !std::isfinite(softcap) || softcap < 0.f || window < 0)
         return WSW_ERR_INVALID_ARG;
     constexpr int64_t lim = int64_t(1) << 31;
-    // Positions and page numbers are 32 bits: a tile's positions and a window of 64 + 32 table entries run
-    // past the last position (page_size 1: an entry's number past 2^31 - 1 was read at a negative offset).
+    // Positions and page numbers are 32 bits: a tile's positions and a window of 64 + 32 table entries run past
+    // the last position (page_size 1: an entry's number past 2^31 - 1 was read at a negative offset), a step of
+    // the CTA past a row's last vector of four.
     constexpr int64_t most = lim - 4096;
-    if (requests > 65535 || requests * q_heads >= lim || q_heads * (a.kv.head_dim / 4) > most || max_pages > most || (max_pages << a.kv.page_shift) > most ||
-        window >= lim)
+    if (requests > 65535 || q_heads >= lim || requests * q_heads >= lim || q_heads * (a.kv.head_dim / 4) > most ||
+        max_pages > most || (max_pages << a.kv.page_shift) > most || window >= lim)
         return WSW_ERR_UNSUPPORTED;
     if (requests == 0) return WSW_OK;
     if (!q || !out || !lens || !ws || (max_pages > 0 && !table)) return WSW_ERR_INVALID_ARG;

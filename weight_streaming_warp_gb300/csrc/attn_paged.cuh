@@ -672,7 +672,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                 if constexpr (X3) {
                     uint32_t t[RT / 4];
 #pragma unroll
-                    for (int i = 0; i < RT / 4; ++i) t[i] = C::q_smem ? q_third_sm[(kt * (RT / 4) + i) * 32 + lane] : q3[C::q_smem ? 0 : kt][i];
+                    for (int i = 0; i < RT / 4; ++i) {
+                        if constexpr (C::q_smem) t[i] = q_third_sm[(kt * (RT / 4) + i) * 32 + lane];
+                        else t[i] = q3[kt][i];
+                    }
                     mma_third<CT, RT>(d, t, b0, b1);
                 }
             };
@@ -763,7 +766,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                 for (int n = 0; n < NB; ++n) {
                     const float p_0 = ex2(s[2 * n] - ref), p_1 = ex2(s[2 * n + 1] - ref);
                     sum += p_0 + p_1;
-                    uint32_t &hi = ph[n / 2][2 * (n & 1) + y], &lo = RT == 8 ? ph[n / 2][2 * (n & 1) + 1] : pl[n / 2][2 * (n & 1) + y];
+                    uint32_t &hi = ph[n / 2][2 * (n & 1) + y];
+                    uint32_t &lo = RT == 8 ? ph[n / 2][2 * (n & 1) + 1] : pl[n / 2][2 * (n & 1) + y];
                     if constexpr (X3) split3(p_0, p_1, hi, lo, pt[n / 2][(n & 1) * (RT / 8) + y]);
                     else split<CT>(p_0, p_1, hi, lo);
                 }
