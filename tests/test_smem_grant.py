@@ -18,7 +18,7 @@ int main() {
     using namespace std::chrono_literals;
     static int kernel;
     wsw::SmemGrants grants;
-    std::atomic<int> limit{0}, sets{0};  // the limit as the driver would hold it
+    std::atomic<int> limit{0}, sets{0};  // the limit as CUDA would hold it
     std::promise<void> inside, go;
     std::thread small([&] {
         grants.ensure(&kernel, 0, 20, [&](int n) {
