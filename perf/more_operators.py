@@ -44,10 +44,10 @@ def listed():
         {"name": "beam 60 x 10 x 50021 bf16", "op": "beam", "requests": 60, "beams": 10, "vocab": 50021, "x": "bf16",
          "scale": 1.25, "ends": 0, "masked": False},
         # the survivors of four requests' beams, one layer
-        {"name": "fork 4 x 4, 1000 cached", "op": "fork", "groups": 4, "beams": 4, "cached": 1000, "page": 16,
+        {"name": "fork 4 x 4 of 1000", "op": "fork", "groups": 4, "beams": 4, "cached": 1000, "page": 16,
          "kv_heads": 4, "dim": 128, "cache": "fp16", "nhd": True, "layers": 1},
         # a server's beams at depth, four layers of large pages
-        {"name": "fork 64 x 8, 8192 cached", "op": "fork", "groups": 64, "beams": 8, "cached": 8192, "page": 64,
+        {"name": "fork 64 x 8 of 8192", "op": "fork", "groups": 64, "beams": 8, "cached": 8192, "page": 64,
          "kv_heads": 4, "dim": 128, "cache": "bf16", "nhd": False, "layers": 4},
         # after a fork: the pages of the beams that were dropped go back to the free list
         {"name": "free 64 rows of 8192", "op": "compact", "rows": 64, "cached": 8192, "page": 16, "kv_heads": 4,
