@@ -649,6 +649,95 @@ int wsw_token_logprobs(const void *logits, int32_t dtype, int64_t rows, int64_t 
                        float *entropy, float *top_logprob, int32_t *top_id, void *ws, size_t ws_bytes, void *stream,
                        const wsw_launch_opts *opts);
 
+/* ------------------------------------------------------------------------------------
+ * Rows that continue one prompt (beams, parallel samples, a shared system prompt).  Their
+ * block tables list the same pages for what they have in common.
+ */
+
+/*
+ * wsw_kv_page_fork -- block table rows of a step's children from their parents'.  With
+ * n = seq_len[parent[i]], row i of the new table lists the pages of its parent:
+ *   table_out[i][j] = table[parent[i]][j] for j < ceil(n / page_size);  len_out[i] = n
+ * Full pages are shared.  A partly filled last page (n % page_size > 0) stays with the lowest
+ * child of its row; each other child takes a fresh page in its place, the k-th of them in row
+ * order free_pages[head + k], and leaves a copy for wsw_kv_page_copy:
+ *   src[k] = the parent's last page, dst[k] = the fresh one, fill[k] = n % page_size
+ *   *count = number of copies;  *head_out = head + *count
+ * Entries of the new rows from their pages on become -1 as far as any row of `table` reaches.
+ * A partly filled last page has to be its row's alone, as this call leaves it.  What no row
+ * lists any more goes back to the free list by wsw_kv_page_compact.
+ *
+ *   parent      int32 [children]: a row of `table`, or -1 for an empty row (length 0).
+ *   seq_len     int32 [requests], the old rows' lengths; their pages lie in `table`, int32
+ *               [requests][table_stride], max_pages entries of each row used.
+ *   table_out   int32 [children][out_stride]; table itself (out_stride = table_stride) or
+ *               elsewhere (WSW_ERR_INVALID_ARG if they overlap otherwise).
+ *   len_out     int32 [children] and head_out int32 [1]; they may be seq_len and head.
+ *   src, dst, fill  int32 [children], the first *count entries written; count int32 [1].
+ *   free_pages, head  as wsw_kv_page_plan's.
+ *   err_flag    int32 [1] or NULL; bits are ORed in: 1 (bit 0) a parent outside [-1, requests),
+ *               2 a parent of negative length or more than max_pages pages, 8 the free list
+ *               ran out.  The rows concerned are empty.
+ *   children, requests <= 8192;  n_free < 2^31 - 1;  max_pages <= 2^31 - 2^20;  page_size a
+ *   power of two <= 65536.
+ */
+int wsw_kv_page_fork(const int32_t *parent, int64_t children, const int32_t *seq_len, int64_t requests,
+                     const int32_t *free_pages, int64_t n_free, const int32_t *head, int64_t page_size,
+                     const int32_t *table, int64_t max_pages, int64_t table_stride, int32_t *table_out,
+                     int64_t out_stride, int32_t *len_out, int32_t *head_out, int32_t *src, int32_t *dst,
+                     int32_t *fill, int32_t *count, int32_t *err_flag, void *stream, const wsw_launch_opts *opts);
+
+/*
+ * wsw_kv_page_copy -- copy pages within every one of `n_caches` caches (the layers of a
+ * model): for e < *count, the first fill[e] positions of page src[e] to page dst[e], K, V and
+ * scales.  A copy from or to a page outside a cache is left out there and sets bit 0 of
+ * *err_flag.  The other positions of dst[e] stay as they are.
+ *
+ *   src, dst    int32 [copies];  fill int32 [copies] (cut to [0, page_size]) or NULL: whole
+ *               pages.  No page may be the dst of two copies, or the dst of one and the src of
+ *               another.
+ *   count       int32 [1], cut to [0, copies].
+ *   caches      host array of pointers; page_size equal in all, the rest their own.
+ *   copies < 2^31;  n_caches <= 65536.  One launch for each 32 caches.
+ */
+int wsw_kv_page_copy(const int32_t *src, const int32_t *dst, const int32_t *fill, const int32_t *count,
+                     int64_t copies, const wsw_kv_cache *const *caches, int64_t n_caches, int32_t *err_flag,
+                     void *stream, const wsw_launch_opts *opts);
+
+/*
+ * wsw_kv_page_compact -- the free list from what the rows list, and live pages moved together.
+ * A page is live if a row lists it (among its first ceil(seq_len / page_size) entries) or
+ * held[p] is not 0.  With N live pages, the k-th live page >= N that is not held moves to the
+ * k-th page below N that is not live, both counted in ascending order, for k < max_moves:
+ *   src[k], dst[k]  that move, for wsw_kv_page_copy (whole pages);  *count = number of moves
+ *   table_out       the rows' used entries with the moved pages' new numbers
+ *   free_pages      [N .. num_pages - 1]: the pages that are not live then, ascending;
+ *   *head = N
+ * max_moves = 0 only frees: no table is written, src and dst may be NULL.  Pages that a row
+ * of no table lists, but that have to stay (a prefix kept for later), are `held`; they never
+ * move.  One call sees all the rows that use the pool.
+ *
+ *   seq_len     int32 [requests];  table int32 [requests][table_stride].
+ *   held        uint8 [num_pages] or NULL.
+ *   table_out   int32 [requests][out_stride]; table itself (equal strides) or elsewhere; entries
+ *               past a row's pages are not written.
+ *   free_pages  int32 [num_pages]; entries before *head are left as they are.
+ *   src, dst    int32 [max_moves];  count, head int32 [1].
+ *   err_flag    int32 [1] or NULL; bits are ORed in: 1 (bit 0) an entry outside [0, num_pages) (it
+ *               lists nothing and stays as it is), 2 a length that is negative or needs more than
+ *               max_pages entries (the row lists nothing).
+ *   ws          device workspace of ws_bytes >= wsw_kv_page_compact_workspace_bytes(num_pages),
+ *               16-byte aligned, overwritten.
+ *   requests <= 65535;  num_pages <= 2^26;  max_pages <= 2^31 - 2^20;  page_size a power of two
+ *   <= 65536;  max_moves < 2^31.
+ */
+size_t wsw_kv_page_compact_workspace_bytes(int64_t num_pages);
+int wsw_kv_page_compact(const int32_t *seq_len, int64_t requests, const int32_t *table, int64_t max_pages,
+                        int64_t table_stride, int64_t page_size, int64_t num_pages, const uint8_t *held,
+                        int64_t max_moves, int32_t *table_out, int64_t out_stride, int32_t *free_pages,
+                        int32_t *head, int32_t *src, int32_t *dst, int32_t *count, int32_t *err_flag, void *ws,
+                        size_t ws_bytes, void *stream, const wsw_launch_opts *opts);
+
 /*
  * wsw_bounded_wait_check -- run the bounded mbarrier wait of the tensor-core kernels
  * on its own, one thread of one CTA.  The library has no device-side fault injection:

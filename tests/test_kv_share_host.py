@@ -1,0 +1,96 @@
+"""What the calls for rows that share pages refuse on the host, before anything is launched."""
+import ctypes
+
+import pytest
+
+import weight_streaming_warp_gb300 as wsw
+
+INVALID, MISALIGNED, UNSUPPORTED, WORKSPACE = 1, 2, 3, 4
+P, N = ctypes.c_void_p, None
+A = P(4096)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from weight_streaming_warp_gb300 import build
+    build.build()
+    return wsw.load()
+
+
+def _fork(lib, **change):
+    a = dict(parent=P(1 << 20), children=4, seq=P(2 << 20), requests=4, free=A, n_free=8, head=A, page=16,
+             table=P(3 << 20), width=8, stride=8, out=P(4 << 20), out_stride=8, lens=P(5 << 20), head_out=A, src=A, dst=A,
+             fill=A, count=A, err=N)
+    a.update(change)
+    return lib.wsw_kv_page_fork(*a.values(), None, None)
+
+
+def test_fork_rejects_on_host(lib):
+    for name in ("parent", "seq", "free", "head", "table", "out", "lens", "head_out", "src", "dst", "fill", "count"):
+        assert _fork(lib, **{name: N}) == INVALID, name
+        assert _fork(lib, **{name: P((6 << 20) + 2)}) == MISALIGNED, name
+    assert _fork(lib, err=P(4098)) == MISALIGNED
+    for change in ({"children": -1}, {"requests": -1}, {"n_free": -1}, {"width": -1}, {"page": 0}, {"stride": 7},
+                   {"out_stride": 7}):
+        assert _fork(lib, **change) == INVALID, change
+    for change in ({"children": 8193}, {"requests": 8193}, {"page": 48}, {"page": 1 << 17}, {"n_free": (1 << 31) - 1},
+                   {"width": 1 << 31, "stride": 1 << 31, "out_stride": 1 << 31}, {"stride": 1 << 50},
+                   {"out_stride": 1 << 50}):
+        assert _fork(lib, **change) == UNSUPPORTED, change
+    # the new table overlaps the old one, but is not the old one; the lengths likewise
+    assert _fork(lib, out=P((3 << 20) + 4)) == INVALID
+    assert _fork(lib, out=P(3 << 20), out_stride=9) == INVALID
+    assert _fork(lib, out=P((3 << 20) - 4 * 8 * 4 + 4)) == INVALID
+    assert _fork(lib, lens=P((2 << 20) + 4)) == INVALID
+
+
+def _cache(**change):
+    c = dict(k=4096, v=4096, kd=None, vd=None, num_pages=8, page_size=16, heads=2, head_dim=64, page_stride=2048,
+             pos_stride=128, head_stride=64, d_page_stride=0, d_pos_stride=0, d_head_stride=0, dtype=1)
+    c.update(change)
+    return wsw._CKv(**c)
+
+
+def _copy(lib, *caches, src=A, dst=A, fill=A, count=A, copies=4, n=None, err=N):
+    refs = (P * max(1, len(caches)))(*[ctypes.addressof(c) if c else None for c in caches])
+    return lib.wsw_kv_page_copy(src, dst, fill, count, copies, refs, len(caches) if n is None else n, err, None, None)
+
+
+def test_copy_rejects_on_host(lib):
+    ok = _cache()
+    assert _copy(lib) == 0 and _copy(lib, ok, copies=0, src=N, dst=N, count=N) == 0
+    for name in ("src", "dst", "count"):
+        assert _copy(lib, ok, **{name: N}) == INVALID
+        assert _copy(lib, ok, **{name: P(4098)}) == MISALIGNED
+    assert _copy(lib, ok, fill=P(4097)) == MISALIGNED and _copy(lib, ok, err=P(4097)) == MISALIGNED
+    assert _copy(lib, ok, copies=-1) == INVALID and _copy(lib, ok, n=-1) == INVALID
+    assert _copy(lib, ok, copies=1 << 31) == UNSUPPORTED
+    assert _copy(lib, ok, _cache(page_size=8)) == INVALID  # one block table, one page size
+    assert _copy(lib, ok, None) == INVALID
+    assert _copy(lib, ok, _cache(k=4104)) == MISALIGNED
+    assert _copy(lib, ok, _cache(head_dim=96)) == UNSUPPORTED
+    assert _copy(lib, ok, _cache(dtype=3)) == INVALID  # q8_0 without scales
+    assert lib.wsw_kv_page_copy(A, A, N, A, 4, None, 1, N, None, None) == INVALID
+
+
+def _compact(lib, **change):
+    a = dict(seq=A, requests=4, table=P(3 << 20), width=8, stride=8, page=16, pool=100, held=N, moves=5, out=P(4 << 20),
+             out_stride=8, free=A, head=A, src=A, dst=A, count=A, err=N, ws=A, ws_bytes=1 << 20)
+    a.update(change)
+    return lib.wsw_kv_page_compact(*a.values(), None, None)
+
+
+def test_compact_rejects_on_host(lib):
+    for name in ("seq", "table", "out", "free", "head", "src", "dst", "count", "ws"):
+        assert _compact(lib, **{name: N}) == INVALID, name
+    for name in ("seq", "table", "out", "free", "head", "src", "dst", "count", "err", "ws"):
+        assert _compact(lib, **{name: P((6 << 20) + 2)}) == MISALIGNED, name
+    for change in ({"requests": -1}, {"width": -1}, {"stride": 7}, {"out_stride": 7}, {"page": 0}, {"pool": 0},
+                   {"moves": -1}, {"out": P((3 << 20) + 4)}, {"out": P(3 << 20), "out_stride": 9}):
+        assert _compact(lib, **change) == INVALID, change
+    for change in ({"requests": 65536}, {"page": 24}, {"page": 1 << 17}, {"pool": (1 << 26) + 1}, {"moves": 1 << 31},
+                   {"stride": 1 << 50}, {"width": 1 << 31, "stride": 1 << 31, "out_stride": 1 << 31}):
+        assert _compact(lib, **change) == UNSUPPORTED, change
+    need = lib.wsw_kv_page_compact_workspace_bytes
+    assert need(0) == 0 and need((1 << 26) + 1) == 0 and need(100) >= 100 + 400
+    assert _compact(lib, ws_bytes=need(100) - 1) == WORKSPACE

@@ -24,7 +24,8 @@ __all__ = [
     "bounded_wait_check", "attn_decode_f16", "attn_decode_workspace_bytes", "attn_prefill_f16",
     "attn_prefill_q8_0", "attn_prefill_q8_0_workspace_bytes", "PagedKV", "KvPlan", "kv_page_plan", "RopeTable",
     "rope_table", "rope_kv_write", "attn_paged_decode", "attn_paged_decode_workspace_bytes", "TokenLogprobs",
-    "token_logprobs", "token_logprobs_out", "token_logprobs_workspace_bytes",
+    "token_logprobs", "token_logprobs_out", "token_logprobs_workspace_bytes", "PageCopies", "KvFork", "kv_page_fork",
+    "kv_page_copy", "KvCompact", "kv_page_compact", "kv_page_compact_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -131,7 +132,14 @@ def load():
     L.wsw_token_logprobs_workspace_bytes.restype = ctypes.c_size_t
     L.wsw_token_logprobs.argtypes = [_p, _i32, _i64, _i64, _i64, _p, _f32, _i32, _p, _p, _p, _p, _p, _p, _p,
                                      ctypes.c_size_t, _p, _p]
-    for f in ("wsw_kv_page_plan", "wsw_rope_table", "wsw_rope_kv_write", "wsw_attn_paged_decode",
+    L.wsw_kv_page_fork.argtypes = [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p,
+                                   _p, _p, _p, _p]
+    L.wsw_kv_page_copy.argtypes = [_p, _p, _p, _p, _i64, _p, _i64, _p, _p, _p]
+    L.wsw_kv_page_compact_workspace_bytes.argtypes = [_i64]
+    L.wsw_kv_page_compact_workspace_bytes.restype = ctypes.c_size_t
+    L.wsw_kv_page_compact.argtypes = [_p, _i64, _p, _i64, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p,
+                                      _p, ctypes.c_size_t, _p, _p]
+    for f in ("wsw_kv_page_fork", "wsw_kv_page_copy", "wsw_kv_page_compact", "wsw_kv_page_plan", "wsw_rope_table", "wsw_rope_kv_write", "wsw_attn_paged_decode",
               "wsw_token_logprobs"):
         getattr(L, f).restype = ctypes.c_int
     for f in ("wsw_quantize_q8", "wsw_gemv_bf16", "wsw_gemv_bf16_chain", "wsw_gemv_q8_0", "wsw_quantize_gemv_q8_0",
@@ -750,6 +758,126 @@ def token_logprobs(logits, tokens=None, top=0, scale=1.0, out=None, ws=None, opt
         logits.data_ptr(), code, rows, vocab, ld, tp, scale, top, lp, rp,
         _packed(lse, _F32, "lse", dev, (rows,)), _packed(entropy, _F32, "entropy", dev, (rows,)), bp, ip,
         wp, 0 if wp is None else ws.numel(), _raw_stream(dev), _opts(opts)), "token_logprobs")
+    return out
+
+
+# ------------------------------------------------------ rows that continue one prompt ----
+
+class PageCopies(NamedTuple):
+    """Copies of pages for kv_page_copy; the first `count` of them are there."""
+    src: torch.Tensor             # int32 [most]
+    dst: torch.Tensor             # int32 [most]
+    fill: Optional[torch.Tensor]  # int32 [most] positions of each, or None: whole pages
+    count: torch.Tensor           # int32 [1]
+
+
+class KvFork(NamedTuple):
+    table: torch.Tensor    # int32 [children][max_pages]
+    seq_len: torch.Tensor  # int32 [children]
+    head: torch.Tensor     # int32 [1]
+    copies: PageCopies     # room for one of each child
+
+
+def _page_copies(n, device, fill):
+    i = lambda m: torch.empty(m, dtype=torch.int32, device=device)  # noqa: E731
+    return PageCopies(i(n), i(n), i(n) if fill else None, i(1))
+
+
+def kv_page_fork(parent, seq_len, free_pages, head, table, page_size, out=None, err_flag=None, opts=None):
+    """Block table rows of children (beams, samples) from their parents' rows: row i continues
+    row parent[i] (int32 [children]; -1: an empty row) of table, whose lengths are seq_len.
+    Full pages are shared; all but a row's lowest child get a page from free_pages[head ..]
+    for a partly filled last page, and an entry in copies, which kv_page_copy carries out
+    before the next tokens are written.  Returns a KvFork; out = one to fill, in which table,
+    seq_len and head may be the arguments themselves.  err_flag: wsw.h."""
+    dev = _home(parent, "parent")
+    pp = _packed(parent, _I32, "parent", dev)
+    n = parent.numel()
+    sp = _packed(seq_len, _I32, "seq_len", dev)
+    rows = seq_len.numel()
+    tp, width, row = _table(table, rows, dev)
+    if out is None:
+        out = KvFork(table.new_full((n, width), -1), torch.empty_like(parent), torch.empty_like(head),
+                     _page_copies(n, parent.device, True))
+    op, out_width, out_row = _table(out.table, n, dev)
+    if out_width != width:
+        raise WswError("the new table must have as many entries in a row as the old one")
+    c = out.copies
+    _check(load().wsw_kv_page_fork(
+        pp, n, sp, rows, _packed(free_pages, _I32, "free_pages", dev), free_pages.numel(),
+        _packed(head, _I32, "head", dev, (1,)), page_size, tp, width, row, op, out_row,
+        _packed(out.seq_len, _I32, "seq_len (out)", dev, (n,)), _packed(out.head, _I32, "head (out)", dev, (1,)),
+        _packed(c.src, _I32, "copies.src", dev, (n,)), _packed(c.dst, _I32, "copies.dst", dev, (n,)),
+        _packed(c.fill, _I32, "copies.fill", dev, (n,)), _packed(c.count, _I32, "copies.count", dev, (1,)),
+        None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _raw_stream(dev), _opts(opts)),
+        "kv_page_fork")
+    return out
+
+
+def kv_page_copy(copies, caches, err_flag=None, opts=None):
+    """Carries out copies (a PageCopies, as kv_page_fork and kv_page_compact give them) in each
+    of caches, the PagedKV of every layer that shares the block table, in one launch for up to 32
+    of them.  A copy that names a page outside a cache is left out there (err_flag, bit 0)."""
+    dev = _home(copies.src, "copies.src")
+    sp = _packed(copies.src, _I32, "copies.src", dev)
+    n = copies.src.numel()
+    caches = (caches,) if isinstance(caches, PagedKV) else caches
+    for kv in caches:
+        if kv._device != dev:
+            _elsewhere(kv, dev)
+    refs = (_p * max(len(caches), 1))(*[kv._ref for kv in caches])
+    _check(load().wsw_kv_page_copy(
+        sp, _packed(copies.dst, _I32, "copies.dst", dev, (n,)),
+        None if copies.fill is None else _packed(copies.fill, _I32, "copies.fill", dev, (n,)),
+        _packed(copies.count, _I32, "copies.count", dev, (1,)), n, refs, len(caches),
+        None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _raw_stream(dev), _opts(opts)),
+        "kv_page_copy")
+
+
+class KvCompact(NamedTuple):
+    table: torch.Tensor       # int32 [requests][max_pages]
+    free_pages: torch.Tensor  # int32 [num_pages]: the free ones from head on
+    head: torch.Tensor        # int32 [1]
+    copies: PageCopies        # room for max_moves whole pages
+
+
+def kv_page_compact_workspace_bytes(num_pages) -> int:
+    return int(load().wsw_kv_page_compact_workspace_bytes(num_pages))
+
+
+def kv_page_compact(seq_len, table, page_size, num_pages, held=None, max_moves=0, out=None, err_flag=None, ws=None,
+                    opts=None):
+    """The free list of a pool of num_pages pages from what the rows of table list (and held,
+    uint8 [num_pages], marks): with max_moves = 0 it only frees what no row lists any more; else
+    up to max_moves live pages behind the others also move into the gaps, the table follows and
+    copies names the pages, which kv_page_copy has to copy before the cache is used again.
+    Returns a KvCompact, whose table is `table` itself, updated in place; out = one to fill, in
+    which table may lie elsewhere.  ws: a uint8 device tensor of at least
+    kv_page_compact_workspace_bytes(num_pages) bytes, allocated if None."""
+    dev = _home(seq_len, "seq_len")
+    sp = _packed(seq_len, _I32, "seq_len", dev)
+    n = seq_len.numel()
+    tp, width, row = _table(table, n, dev)
+    if out is None:
+        out = KvCompact(table, torch.full((num_pages,), -1, dtype=torch.int32, device=seq_len.device),
+                        torch.empty(1, dtype=torch.int32, device=seq_len.device),
+                        _page_copies(max_moves, seq_len.device, False))
+    op, out_width, out_row = _table(out.table, n, dev)
+    if out_width != width:
+        raise WswError("the new table must have as many entries in a row as the old one")
+    c = out.copies
+    if c.fill is not None:
+        raise WswError("whole pages move: copies.fill must be None")
+    if ws is None:
+        ws = torch.empty(kv_page_compact_workspace_bytes(num_pages), dtype=torch.uint8, device=seq_len.device)
+    _check(load().wsw_kv_page_compact(
+        sp, n, tp, width, row, page_size, num_pages,
+        None if held is None else _packed(held, _U8, "held", dev, (num_pages,)), max_moves, op, out_row,
+        _packed(out.free_pages, _I32, "free_pages", dev, (num_pages,)), _packed(out.head, _I32, "head", dev, (1,)),
+        _packed(c.src, _I32, "copies.src", dev, (max_moves,)), _packed(c.dst, _I32, "copies.dst", dev, (max_moves,)),
+        _packed(c.count, _I32, "copies.count", dev, (1,)),
+        None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _packed(ws, _U8, "ws", dev), ws.numel(),
+        _raw_stream(dev), _opts(opts)), "kv_page_compact")
     return out
 
 

@@ -18,8 +18,7 @@
 // search for each token made 130000 tokens of 1000 requests bound by instructions, 18 us), one
 // table read for each page that they touch.  64 requests of one token each take 3.9 us, 130000
 // tokens of 1000 requests 10.5 us (clusters of 8 CTAs 13.7 us).
-#include "cluster_choice.h"
-#include "common.cuh"
+#include "kv_rows.cuh"
 
 namespace wsw {
 namespace {
@@ -37,47 +36,6 @@ struct PlanArgs {
     int64_t table_stride;
     int requests, n_free, shift, max_pages, tokens;
 };
-
-// pages of `len` < 2^31 positions
-__device__ __forceinline__ int pages_of(int len, int shift) {
-    return static_cast<int>((static_cast<unsigned>(len) + (1u << shift) - 1) >> shift);
-}
-
-// a + b, at most cap < 2^31 (a, b <= cap)
-__device__ __forceinline__ int add_sat(int a, int b, int cap) {
-    const unsigned s = static_cast<unsigned>(a) + static_cast<unsigned>(b);
-    return s < static_cast<unsigned>(cap) ? static_cast<int>(s) : cap;
-}
-
-// Exclusive saturating prefix of v <= cap over the block's threads, and the block's total.
-// Every thread calls it; sm holds 33 values.
-__device__ __forceinline__ int block_scan(int v, int cap, int *sm, int *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(WSW_FULL_MASK, x, d);
-        if (lane >= d) x = add_sat(x, y, cap);
-    }
-    if (lane == 31) sm[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int w = lane < warps ? sm[lane] : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(WSW_FULL_MASK, w, d);
-            if (lane >= d) w = add_sat(w, y, cap);
-        }
-        sm[lane + 1] = w;
-        if (lane == 0) sm[0] = 0;
-    }
-    __syncthreads();
-    *total = sm[32];
-    const int x_before = __shfl_up_sync(WSW_FULL_MASK, x, 1);
-    const int before = add_sat(sm[warp], lane ? x_before : 0, cap);
-    __syncthreads();  // sm may be reused
-    return before;
-}
 
 // The last i with a[i] <= x[j] for each of N values (a is ascending, n entries, a[0] <= x)
 template <int N>
@@ -159,8 +117,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
     if (err) atomicOr(&err_sm, err);
     __syncthreads();
     if (ncta > 1) {  // every CTA of the cluster has read its lengths
-        asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        cluster_barrier();
     }
     const int granted = used_sm;
 
@@ -242,37 +199,6 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const PlanArgs a) {
 
 constexpr int kMaxSmem = (3 * kMaxRequests + 2) * 4;
 
-// Sets the kernel's options on the current device, once, and says how many CTAs a cluster can have.
-cudaError_t cluster_ctas(int device, unsigned *ctas) {
-    static ClusterChoice choice;
-    const void *kernel = reinterpret_cast<const void *>(kv_plan_kernel);
-    const cudaError_t e = ensure_smem(kernel, kMaxSmem);
-    if (e != cudaSuccess) return e;
-    *ctas = choice.of(device, [kernel] {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-            cudaGetLastError();
-            return false;
-        }
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 16;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.gridDim = dim3(16);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kMaxSmem;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            return false;
-        }
-        return clusters > 0;
-    });
-    return cudaSuccess;
-}
-
 }  // namespace
 }  // namespace wsw
 
@@ -317,25 +243,14 @@ extern "C" int wsw_kv_page_plan(const int32_t *seq_len, const int32_t *new_len, 
     a.shift = 0;
     while ((int64_t(1) << a.shift) < page_size) ++a.shift;
     const int smem = static_cast<int>((3 * requests + 2) * 4);
+    static ClusterChoice choice;
     unsigned ncta = 1;
-    if (cluster_ctas(di.device, &ncta) != cudaSuccess) return WSW_ERR_CUDA;
+    if (cluster_ctas(choice, reinterpret_cast<const void *>(kv_plan_kernel), kThreads, kMaxSmem, di.device, &ncta) !=
+        cudaSuccess)
+        return WSW_ERR_CUDA;
     if (tokens <= 2048) ncta = 1;  // while its threads see few tokens each, else the largest cluster
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
     const int64_t want = requests > tokens / ncta ? requests : tokens / ncta;
-    cfg.gridDim = dim3(ncta);
-    cfg.blockDim = dim3(want > 512 ? kThreads : want > 128 ? 512 : 128);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.attrs = attr;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ncta;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
-    if (o.pdl) {
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
-        cfg.numAttrs = 2;
-    }
-    return cudaLaunchKernelEx(&cfg, kv_plan_kernel, a) == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
+    const cudaError_t e = launch_cluster(kv_plan_kernel, ncta, ncta, want > 512 ? kThreads : want > 128 ? 512 : 128, smem,
+                                         static_cast<cudaStream_t>(stream), o.pdl, a);
+    return e == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
 }
