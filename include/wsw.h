@@ -739,6 +739,42 @@ int wsw_kv_page_compact(const int32_t *seq_len, int64_t requests, const int32_t 
                         size_t ws_bytes, void *stream, const wsw_launch_opts *opts);
 
 /*
+ * wsw_beam_select -- the next beams of every request from the logits of all its beams, in one
+ * pass.  With x[b] the row of beam b (row request * beams + b of the logits), y = scale * x,
+ *   s[b][j] = scores[b] + y[b][j] - ln sum_i exp(y[b][i])
+ * The candidates (b, j) with finite s are taken in descending order of s, equal ones by the
+ * lower b, then the lower j, until `beams` of them do not end: those are the next beams, in that
+ * order.  A candidate ends if its token is one of end_tokens; it is reported as an ended one
+ * if fewer than `beams` candidates come before it.
+ *   parent[i], token[i], score[i]   of the i-th next beam of a request: the row of the logits that
+ *                      it continues, its token, its s rounded to fp32
+ *   end_parent, end_token, end_score   the same of the ended ones, in order
+ * Places without a candidate hold -1, -1 and -inf.  A forbidden token (logit -inf), a beam whose
+ * score is not finite, and every beam whose row holds a NaN or +inf have no candidates.
+ * Sums are fp32 within a thread and 64 bits above, scores are compared in 64 bits: s is off by
+ * some 1e-7, differences between the beams of a request by some 1e-8.  parent is what
+ * wsw_kv_page_fork takes.
+ *
+ *   logits      `dtype` (WSW_F32, WSW_F16 or WSW_BF16) [requests * beams][ld], ld >= vocab,
+ *               aligned to its element.
+ *   scores      fp32 [requests][beams]: the beams' log probabilities so far (-inf: no beam).
+ *   end_tokens  host int32 [n_ends].
+ *   scale       > 0 (1 / temperature), scale * log2(e) finite in fp32.
+ *   parent, token int32 and score fp32 [requests][beams];  end_parent, end_token and
+ *               end_score likewise (all NULL is fine without end tokens).
+ *   ws          device workspace of ws_bytes >= wsw_beam_select_workspace_bytes(...) bytes,
+ *               16-byte aligned, zero-filled before its first use and then reused, as
+ *               wsw_attn_paged_decode's.
+ *   requests <= 16384;  beams <= 32;  n_ends <= 8;  beams * (1 + n_ends) <= 32;
+ *   1 <= vocab < 2^31 - 65536.  requests == 0 does nothing.
+ */
+size_t wsw_beam_select_workspace_bytes(int64_t requests, int64_t beams, int64_t vocab, int64_t n_ends);
+int wsw_beam_select(const void *logits, int32_t dtype, int64_t requests, int64_t beams, int64_t vocab, int64_t ld,
+                    const float *scores, const int32_t *end_tokens, int64_t n_ends, float scale, int32_t *parent,
+                    int32_t *token, float *score, int32_t *end_parent, int32_t *end_token, float *end_score, void *ws,
+                    size_t ws_bytes, void *stream, const wsw_launch_opts *opts);
+
+/*
  * wsw_bounded_wait_check -- run the bounded mbarrier wait of the tensor-core kernels
  * on its own, one thread of one CTA.  The library has no device-side fault injection:
  * this call is how the give-up path of a wait is exercised on a GPU.

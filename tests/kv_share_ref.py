@@ -92,7 +92,7 @@ def attend(q, k, v, scale, softcap=0.0, slopes=None, distance=None):
 
 def beam(logits, scores, ends, scale=1.0):
     """One request in float64: logits [beams][vocab], scores [beams].  Returns ([(beam, token, score)] of the next
-    beams, the same of the ended candidates, all candidates' scores in order)."""
+    beams, the same of the ended candidates, the scores in order up to the first that was not taken)."""
     beams, vocab = logits.shape
     total = np.full((beams, vocab), -np.inf)
     for b in range(beams):
@@ -113,4 +113,4 @@ def beam(logits, scores, ends, scale=1.0):
                 ended.append(c)
         else:
             nxt.append(c)
-    return nxt, ended, flat[order[: 4 * beams + 4]]
+    return nxt, ended, flat[order[: rank + 1]]

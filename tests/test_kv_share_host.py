@@ -94,3 +94,31 @@ def test_compact_rejects_on_host(lib):
     need = lib.wsw_kv_page_compact_workspace_bytes
     assert need(0) == 0 and need((1 << 26) + 1) == 0 and need(100) >= 100 + 400
     assert _compact(lib, ws_bytes=need(100) - 1) == WORKSPACE
+
+
+def _beam(lib, **change):
+    a = dict(logits=A, dtype=0, requests=2, beams=4, vocab=1000, ld=1000, scores=A, ends=(ctypes.c_int32 * 1)(5), n_ends=1,
+             scale=ctypes.c_float(1.0), parent=A, token=A, score=A, end_parent=A, end_token=A, end_score=A, ws=A,
+             ws_bytes=1 << 24)
+    a.update(change)
+    return lib.wsw_beam_select(*a.values(), None, None)
+
+
+def test_beam_select_rejects_on_host(lib):
+    for name in ("logits", "scores", "ends", "parent", "token", "score", "end_parent", "end_token", "end_score", "ws"):
+        assert _beam(lib, **{name: N}) == INVALID, name
+    assert _beam(lib, end_parent=N, end_token=N, end_score=N) == INVALID  # there is an end token
+    for name in ("logits", "scores", "parent", "token", "score", "end_parent", "end_token", "end_score", "ws"):
+        assert _beam(lib, **{name: P((1 << 20) + 2)}) == MISALIGNED, name
+    assert _beam(lib, logits=P(4097), dtype=1) == MISALIGNED
+    for change in ({"requests": -1}, {"beams": 0}, {"vocab": 0}, {"ld": 999}, {"n_ends": -1}, {"scale": ctypes.c_float(0)},
+                   {"scale": ctypes.c_float(-1)}, {"scale": ctypes.c_float(float("nan"))},
+                   {"scale": ctypes.c_float(3e38)}):
+        assert _beam(lib, **change) == INVALID, change
+    for change in ({"dtype": 3}, {"requests": 16385}, {"beams": 33, "n_ends": 0}, {"beams": 17}, {"n_ends": 9, "beams": 1},
+                   {"vocab": (1 << 31) - 65536, "ld": 1 << 31}):
+        assert _beam(lib, **change) == UNSUPPORTED, change
+    need = lib.wsw_beam_select_workspace_bytes
+    assert need(0, 4, 10, 0) == 0 and need(1, 33, 10, 0) == 0 and need(1, 16, 1000, 2) == 0
+    assert _beam(lib, ws_bytes=need(2, 4, 1000, 1) - 1) == WORKSPACE
+    assert _beam(lib, requests=0, logits=N, ws=N) == 0

@@ -25,7 +25,8 @@ __all__ = [
     "attn_prefill_q8_0", "attn_prefill_q8_0_workspace_bytes", "PagedKV", "KvPlan", "kv_page_plan", "RopeTable",
     "rope_table", "rope_kv_write", "attn_paged_decode", "attn_paged_decode_workspace_bytes", "TokenLogprobs",
     "token_logprobs", "token_logprobs_out", "token_logprobs_workspace_bytes", "PageCopies", "KvFork", "kv_page_fork",
-    "kv_page_copy", "KvCompact", "kv_page_compact", "kv_page_compact_workspace_bytes",
+    "kv_page_copy", "KvCompact", "kv_page_compact", "kv_page_compact_workspace_bytes", "BeamStep", "beam_select",
+    "beam_select_out", "beam_select_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -139,7 +140,11 @@ def load():
     L.wsw_kv_page_compact_workspace_bytes.restype = ctypes.c_size_t
     L.wsw_kv_page_compact.argtypes = [_p, _i64, _p, _i64, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p,
                                       _p, ctypes.c_size_t, _p, _p]
-    for f in ("wsw_kv_page_fork", "wsw_kv_page_copy", "wsw_kv_page_compact", "wsw_kv_page_plan", "wsw_rope_table", "wsw_rope_kv_write", "wsw_attn_paged_decode",
+    L.wsw_beam_select_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
+    L.wsw_beam_select_workspace_bytes.restype = ctypes.c_size_t
+    L.wsw_beam_select.argtypes = [_p, _i32, _i64, _i64, _i64, _i64, _p, _p, _i64, _f32, _p, _p, _p, _p, _p, _p, _p,
+                                  ctypes.c_size_t, _p, _p]
+    for f in ("wsw_beam_select", "wsw_kv_page_fork", "wsw_kv_page_copy", "wsw_kv_page_compact", "wsw_kv_page_plan", "wsw_rope_table", "wsw_rope_kv_write", "wsw_attn_paged_decode",
               "wsw_token_logprobs"):
         getattr(L, f).restype = ctypes.c_int
     for f in ("wsw_quantize_q8", "wsw_gemv_bf16", "wsw_gemv_bf16_chain", "wsw_gemv_q8_0", "wsw_quantize_gemv_q8_0",
@@ -878,6 +883,57 @@ def kv_page_compact(seq_len, table, page_size, num_pages, held=None, max_moves=0
         _packed(c.count, _I32, "copies.count", dev, (1,)),
         None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _packed(ws, _U8, "ws", dev), ws.numel(),
         _raw_stream(dev), _opts(opts)), "kv_page_compact")
+    return out
+
+
+class BeamStep(NamedTuple):
+    parent: torch.Tensor      # int32 [requests][beams]: rows of the logits
+    token: torch.Tensor       # int32 [requests][beams]
+    score: torch.Tensor       # fp32 [requests][beams]
+    end_parent: torch.Tensor  # the same of the candidates that end
+    end_token: torch.Tensor
+    end_score: torch.Tensor
+
+
+def beam_select_workspace_bytes(requests, beams, vocab, ends=0) -> int:
+    return int(load().wsw_beam_select_workspace_bytes(requests, beams, vocab, ends))
+
+
+def beam_select_out(requests, beams, device="cuda") -> BeamStep:
+    """Tensors for beam_select to fill."""
+    return BeamStep(*[torch.empty((requests, beams), dtype=t, device=device) for t in (_I32, _I32, _F32) * 2])
+
+
+def beam_select(logits, scores, end_tokens=(), scale=1.0, out=None, ws=None, opts=None):
+    """The next beams of every request.  logits [requests * beams][vocab] (fp32, fp16 or bf16, any
+    row stride), scores fp32 [requests][beams] the beams' log probabilities so far (-inf: no
+    beam).  Of all candidates (beam, token), ranked by score + log softmax(scale * logits), the first
+    `beams` whose token is not one of end_tokens (at most 8) are the next beams; those that
+    end and have fewer than `beams` before them are reported beside them.  beams * (1 + number of
+    end tokens) <= 32.  Returns a BeamStep (out = one to fill), -1 and -inf where there are fewer
+    candidates; its parent, flattened, is kv_page_fork's.  ws: a uint8 device tensor of at
+    least beam_select_workspace_bytes(...) bytes, zero-filled before its first use, allocated if
+    None."""
+    code, dev = _float_dev(logits, "logits")
+    rows, vocab, ld = _rowmajor(logits, "logits")
+    sp = _packed(scores, _F32, "scores", dev)
+    shape = scores.shape
+    if len(shape) != 2 or shape[0] * shape[1] != rows:
+        raise WswError("scores must be [requests][beams], logits [requests * beams][vocab]")
+    n, beams = shape
+    ends = (_i32 * len(end_tokens))(*end_tokens) if end_tokens else None
+    if out is None:
+        out = beam_select_out(n, beams, logits.device)
+    if ws is None:
+        ws = torch.zeros(beam_select_workspace_bytes(n, beams, vocab, len(end_tokens)), dtype=torch.uint8,
+                         device=logits.device)
+    parent, token, score, end_parent, end_token, end_score = out
+    _check(load().wsw_beam_select(
+        logits.data_ptr(), code, n, beams, vocab, ld, sp, ends, len(end_tokens), scale,
+        _packed(parent, _I32, "parent", dev, shape), _packed(token, _I32, "token", dev, shape),
+        _packed(score, _F32, "score", dev, shape), _packed(end_parent, _I32, "end_parent", dev, shape),
+        _packed(end_token, _I32, "end_token", dev, shape), _packed(end_score, _F32, "end_score", dev, shape),
+        _packed(ws, _U8, "ws", dev), ws.numel(), _raw_stream(dev), _opts(opts)), "beam_select")
     return out
 
 
