@@ -775,6 +775,40 @@ int wsw_beam_select(const void *logits, int32_t dtype, int64_t requests, int64_t
                     size_t ws_bytes, void *stream, const wsw_launch_opts *opts);
 
 /*
+ * wsw_attn_paged_prefix -- wsw_attn_paged_decode for a batch in which groups of requests share a
+ * long prefix, whose K and V are read once for all requests of a group.  Group g is the
+ * requests cu_groups[g] <= r < cu_groups[g + 1]; the first prefix_len[g] positions of all of them
+ * hold the same keys and values (in the same pages, as wsw_kv_page_fork leaves them, or in
+ * copies).  Results are those of wsw_attn_paged_decode without a window: each request sees all its
+ * lens[r] positions.  The prefix is read through the table row of the group's first request
+ * with lens[r] >= prefix_len[g]; a shorter request (or an unused row of length 0), a group of
+ * one request, and a request outside all groups are attended as wsw_attn_paged_decode does.
+ *
+ * A prefix's products run on the tensor cores with fp32 sums.  Under 16-bit queries the softmax
+ * weights are rounded to the cache's 16-bit type (binary16 for q8_0), 2^-9 (bf16) or 2^-12 of each
+ * at most on average half of that; under fp32 queries they and q keep 22 bits over binary16 and q8_0 and
+ * all 24 over bf16, as there.
+ *
+ *   cu_groups   int32 [groups + 1], ascending within [0, requests];  prefix_len int32 [groups], within
+ *               [0, max_pages * page_size].  A bound that is not is moved to the nearest one that is,
+ *               and sets bit 2 of *err_flag; bits 0 and 1 as wsw_attn_paged_decode's.
+ *   head_dim    64 or 128.
+ *   ws          device workspace of ws_bytes >= wsw_attn_paged_prefix_workspace_bytes(...) bytes,
+ *               16-byte aligned, zero-filled before its first use and then reused, as
+ *               wsw_attn_paged_decode's.
+ *   1 <= groups <= 16384;  requests * q_heads <= 2^30;
+ *   kv heads * (requests * group / 128 + groups) * (max_pages * page_size / 64 + 2) < 2^31 - 65536.
+ *   Other arguments and limits as wsw_attn_paged_decode.  Four launches.
+ */
+size_t wsw_attn_paged_prefix_workspace_bytes(int64_t requests, int64_t groups, int64_t q_heads, int64_t kv_heads,
+                                             int64_t head_dim);
+int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t requests, int64_t q_heads, const wsw_kv_cache *cache,
+                          const int32_t *table, int64_t max_pages, int64_t table_stride, const int32_t *lens,
+                          const int32_t *cu_groups, int64_t groups, const int32_t *prefix_len, float scale,
+                          float softcap, const float *slopes, void *out, float *lse, int32_t *err_flag, void *ws,
+                          size_t ws_bytes, void *stream, const wsw_launch_opts *opts);
+
+/*
  * wsw_bounded_wait_check -- run the bounded mbarrier wait of the tensor-core kernels
  * on its own, one thread of one CTA.  The library has no device-side fault injection:
  * this call is how the give-up path of a wait is exercised on a GPU.

@@ -122,3 +122,30 @@ def test_beam_select_rejects_on_host(lib):
     assert need(0, 4, 10, 0) == 0 and need(1, 33, 10, 0) == 0 and need(1, 16, 1000, 2) == 0
     assert _beam(lib, ws_bytes=need(2, 4, 1000, 1) - 1) == WORKSPACE
     assert _beam(lib, requests=0, logits=N, ws=N) == 0
+
+
+def _attend(lib, **change):
+    c = _cache()
+    a = dict(q=A, dtype=2, requests=4, q_heads=8, cache=ctypes.byref(c), table=A, width=8, stride=8, lens=A, cu=A, groups=2,
+             prefix=A, scale=ctypes.c_float(0.1), softcap=ctypes.c_float(0), slopes=N, out=A, lse=N, err=N, ws=A,
+             ws_bytes=1 << 40)
+    a.update(change)
+    return lib.wsw_attn_paged_prefix(*a.values(), None, None)
+
+
+def test_attn_prefix_rejects_on_host(lib):
+    for name in ("q", "cache", "table", "lens", "cu", "prefix", "out", "ws"):
+        assert _attend(lib, **{name: N}) == INVALID, name
+    for name in ("q", "table", "lens", "cu", "prefix", "slopes", "out", "lse", "err", "ws"):
+        assert _attend(lib, **{name: P(4098)}) == MISALIGNED, name
+    for change in ({"requests": -1}, {"q_heads": 7}, {"groups": 0}, {"groups": -1}, {"stride": 7}, {"width": -1},
+                   {"scale": ctypes.c_float(float("inf"))}, {"softcap": ctypes.c_float(-1)}):
+        assert _attend(lib, **change) == INVALID, change
+    for change in ({"dtype": 3}, {"requests": 65536}, {"groups": 16385}, {"cache": ctypes.byref(_cache(head_dim=256))},
+                   {"requests": 60000, "q_heads": 32768}, {"width": 1 << 27, "stride": 1 << 27},
+                   {"groups": 16384, "width": 1 << 20, "stride": 1 << 20}):
+        assert _attend(lib, **change) == UNSUPPORTED, change
+    need = lib.wsw_attn_paged_prefix_workspace_bytes
+    assert need(4, 0, 8, 2, 64) == 0 and need(4, 2, 8, 2, 256) == 0 and need(4, 16385, 8, 2, 64) == 0
+    assert _attend(lib, ws_bytes=need(4, 2, 8, 2, 64) - 1) == WORKSPACE
+    assert _attend(lib, requests=0, q=N, out=N, ws=N) == 0

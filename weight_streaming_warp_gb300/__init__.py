@@ -26,7 +26,7 @@ __all__ = [
     "rope_table", "rope_kv_write", "attn_paged_decode", "attn_paged_decode_workspace_bytes", "TokenLogprobs",
     "token_logprobs", "token_logprobs_out", "token_logprobs_workspace_bytes", "PageCopies", "KvFork", "kv_page_fork",
     "kv_page_copy", "KvCompact", "kv_page_compact", "kv_page_compact_workspace_bytes", "BeamStep", "beam_select",
-    "beam_select_out", "beam_select_workspace_bytes",
+    "beam_select_out", "beam_select_workspace_bytes", "attn_paged_prefix", "attn_paged_prefix_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -144,7 +144,11 @@ def load():
     L.wsw_beam_select_workspace_bytes.restype = ctypes.c_size_t
     L.wsw_beam_select.argtypes = [_p, _i32, _i64, _i64, _i64, _i64, _p, _p, _i64, _f32, _p, _p, _p, _p, _p, _p, _p,
                                   ctypes.c_size_t, _p, _p]
-    for f in ("wsw_beam_select", "wsw_kv_page_fork", "wsw_kv_page_copy", "wsw_kv_page_compact", "wsw_kv_page_plan", "wsw_rope_table", "wsw_rope_kv_write", "wsw_attn_paged_decode",
+    L.wsw_attn_paged_prefix_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i64]
+    L.wsw_attn_paged_prefix_workspace_bytes.restype = ctypes.c_size_t
+    L.wsw_attn_paged_prefix.argtypes = [_p, _i32, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _i64, _p, _f32, _f32, _p, _p, _p,
+                                        _p, _p, ctypes.c_size_t, _p, _p]
+    for f in ("wsw_attn_paged_prefix", "wsw_beam_select", "wsw_kv_page_fork", "wsw_kv_page_copy", "wsw_kv_page_compact", "wsw_kv_page_plan", "wsw_rope_table", "wsw_rope_kv_write", "wsw_attn_paged_decode",
               "wsw_token_logprobs"):
         getattr(L, f).restype = ctypes.c_int
     for f in ("wsw_quantize_q8", "wsw_gemv_bf16", "wsw_gemv_bf16_chain", "wsw_gemv_q8_0", "wsw_quantize_gemv_q8_0",
@@ -934,6 +938,46 @@ def beam_select(logits, scores, end_tokens=(), scale=1.0, out=None, ws=None, opt
         _packed(score, _F32, "score", dev, shape), _packed(end_parent, _I32, "end_parent", dev, shape),
         _packed(end_token, _I32, "end_token", dev, shape), _packed(end_score, _F32, "end_score", dev, shape),
         _packed(ws, _U8, "ws", dev), ws.numel(), _raw_stream(dev), _opts(opts)), "beam_select")
+    return out
+
+
+def attn_paged_prefix_workspace_bytes(requests, groups, q_heads, kv_heads, head_dim) -> int:
+    return int(load().wsw_attn_paged_prefix_workspace_bytes(requests, groups, q_heads, kv_heads, head_dim))
+
+
+def attn_paged_prefix(q, kv, table, lens, groups, prefix, scale=None, softcap=0.0, slopes=None, out=None, lse=None,
+                      err_flag=None, ws=None, opts=None):
+    """attn_paged_decode for a batch in which groups of requests share a prefix, read once for each
+    group: requests groups[g] .. groups[g + 1] - 1 (int32 [n + 1], ascending) have the same keys
+    and values at their first prefix[g] (int32 [n]) positions.  head_dim 64 or 128, no window; the
+    other arguments and the result are attn_paged_decode's.  ws: a uint8 device tensor of at least
+    attn_paged_prefix_workspace_bytes(...) bytes, zero-filled before its first use (every call
+    leaves it ready for the next), allocated if None."""
+    code, dev = _float_dev(q, "q")
+    if q.dim() != 3 or not q.is_contiguous():
+        raise WswError("q must be a contiguous [requests][q_heads][head_dim] tensor")
+    shape = q.shape
+    n, heads, hd = shape
+    if hd != kv.head_dim or heads % kv.heads != 0:
+        raise WswError("q must have the cache's head_dim and a multiple of its heads")
+    tp, width, row = _table(table, n, dev)
+    pp = _packed(prefix, _I32, "prefix", dev)
+    count = prefix.numel()
+    if scale is None:
+        scale = 1.0 / float(hd) ** 0.5
+    if out is None:
+        out = torch.empty_like(q)
+    if ws is None:
+        ws = torch.zeros(attn_paged_prefix_workspace_bytes(n, count, heads, kv.heads, hd), dtype=torch.uint8,
+                         device=q.device)
+    _check(load().wsw_attn_paged_prefix(
+        q.data_ptr(), code, n, heads, kv._ref if kv._device == dev else _elsewhere(kv, dev), tp, width, row,
+        _packed(lens, _I32, "lens", dev, (n,)), _packed(groups, _I32, "groups", dev, (count + 1,)), count, pp, scale,
+        softcap, None if slopes is None else _packed(slopes, _F32, "slopes", dev, (heads,)),
+        _packed(out, q.dtype, "out", dev, shape),
+        None if lse is None else _packed(lse, _F32, "lse", dev, (n, heads)),
+        None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev),
+        _packed(ws, _U8, "ws", dev), ws.numel(), _raw_stream(dev), _opts(opts)), "attn_paged_prefix")
     return out
 
 

@@ -34,18 +34,16 @@ extern "C" size_t wsw_attn_paged_decode_workspace_bytes(int64_t requests, int64_
                                record_bytes(rows_of(q_heads / kv_heads), head_dim);
 }
 
-extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t requests, int64_t q_heads,
-                                     const wsw_kv_cache *cache, const int32_t *table, int64_t max_pages,
-                                     int64_t table_stride, const int32_t *lens, float scale, float softcap,
-                                     int64_t window, const float *slopes, void *out, float *lse, int32_t *err_flag,
-                                     void *ws, size_t ws_bytes, void *stream, const wsw_launch_opts *opts) {
-    using namespace wsw;
-    using namespace wsw::paged;
-    Opts o;
-    int st = resolve_opts(opts, &o);
-    if (st != WSW_OK) return st;
-    Args a;
-    st = check_kv_cache(cache, &a.kv);
+namespace wsw {
+namespace paged {
+
+int prepare(const void *q, int32_t dtype, int64_t requests, int64_t q_heads, const wsw_kv_cache *cache,
+            const int32_t *table, int64_t max_pages, int64_t table_stride, const int32_t *lens, float scale,
+            float softcap, int64_t window, const float *slopes, void *out, float *lse, int32_t *err_flag, Args *args,
+            int *rows, int64_t *tiles) {
+    Args &a = *args;
+    a = Args{};
+    int st = check_kv_cache(cache, &a.kv);
     if (st != WSW_OK) return st;
     if (dtype != WSW_F32 && dtype != WSW_F16 && dtype != WSW_BF16) return WSW_ERR_UNSUPPORTED;
     if (requests < 0 || q_heads < 1 || q_heads % a.kv.heads != 0 || max_pages < 0 || table_stride < max_pages ||
@@ -60,13 +58,11 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
         max_pages > most || (max_pages << a.kv.page_shift) > most || window >= lim)
         return WSW_ERR_UNSUPPORTED;
     if (requests == 0) return WSW_OK;
-    if (!q || !out || !lens || !ws || (max_pages > 0 && !table)) return WSW_ERR_INVALID_ARG;
-    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(ws)) & 15) ||
+    if (!q || !out || !lens || (max_pages > 0 && !table)) return WSW_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) ||
         ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(lse) |
           reinterpret_cast<uintptr_t>(slopes) | reinterpret_cast<uintptr_t>(err_flag)) & 3))
         return WSW_ERR_MISALIGNED;
-    if (ws_bytes < wsw_attn_paged_decode_workspace_bytes(requests, q_heads, cache->heads, cache->head_dim))
-        return WSW_ERR_WORKSPACE;
     a.q = q;
     a.out = out;
     a.lse = lse;
@@ -85,26 +81,58 @@ extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t reque
     a.requests = static_cast<int>(requests);
     a.q_heads = static_cast<int>(q_heads);
     a.group = static_cast<int>(q_heads / cache->heads);
-    const int rows = rows_of(a.group);
-    a.passes = (a.group + rows - 1) / rows;
+    *rows = rows_of(a.group);
+    a.passes = (a.group + *rows - 1) / *rows;
     a.max_len = static_cast<int>(max_pages << a.kv.page_shift);
     a.window = window > 0 ? static_cast<int>(window) : 0x7fffffff;
-    a.dtype = dtype;
-    unsigned char *w = static_cast<unsigned char *>(ws);
-    a.cnt = reinterpret_cast<unsigned *>(w);
-    a.rec = reinterpret_cast<float *>(w + kCounterBytes);
-    a.wrec = a.rec + static_cast<size_t>(kCtas) * 2 * record_bytes(rows, cache->head_dim) / 4;
+    a.dtype = a.out_dtype = dtype;
     // the longest possible list
     const int64_t seen = a.max_len < a.window ? a.max_len : a.window;
-    const int64_t tiles = requests * cache->heads * a.passes * ((seen + 15) / 16 + kPair);
-    if (tiles >= lim - 65536) return WSW_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
+    *tiles = requests * cache->heads * a.passes * ((seen + 15) / 16 + kPair);
+    if (*tiles >= lim - 65536) return WSW_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
+    return WSW_OK;
+}
+
+void place(Args *a, void *ws, int rows) {
+    unsigned char *w = static_cast<unsigned char *>(ws);
+    a->cnt = reinterpret_cast<unsigned *>(w);
+    a->rec = reinterpret_cast<float *>(w + kCounterBytes);
+    a->wrec = a->rec + static_cast<size_t>(kCtas) * 2 * record_bytes(rows, a->kv.head_dim) / 4;
+}
+
+cudaError_t launch_paged(const Args &a, int cache_dtype, int rows, int64_t tiles, cudaStream_t s, bool pdl) {
+    if (cache_dtype == WSW_F16) return launch_type<WSW_F16, false>(a, rows, s, pdl, tiles);
+    if (cache_dtype == WSW_Q8_0) return launch_type<WSW_Q8_0, false>(a, rows, s, pdl, tiles);
+    if (a.dtype == WSW_F32) return launch_type<WSW_BF16, true>(a, rows, s, pdl, tiles);
+    return launch_type<WSW_BF16, false>(a, rows, s, pdl, tiles);
+}
+
+}  // namespace paged
+}  // namespace wsw
+
+extern "C" int wsw_attn_paged_decode(const void *q, int32_t dtype, int64_t requests, int64_t q_heads,
+                                     const wsw_kv_cache *cache, const int32_t *table, int64_t max_pages,
+                                     int64_t table_stride, const int32_t *lens, float scale, float softcap,
+                                     int64_t window, const float *slopes, void *out, float *lse, int32_t *err_flag,
+                                     void *ws, size_t ws_bytes, void *stream, const wsw_launch_opts *opts) {
+    using namespace wsw;
+    using namespace wsw::paged;
+    Opts o;
+    int st = resolve_opts(opts, &o);
+    if (st != WSW_OK) return st;
+    Args a;
+    int rows = 0;
+    int64_t tiles = 0;
+    st = prepare(q, dtype, requests, q_heads, cache, table, max_pages, table_stride, lens, scale, softcap, window, slopes,
+                 out, lse, err_flag, &a, &rows, &tiles);
+    if (st != WSW_OK || requests == 0) return st;
+    if (!ws) return WSW_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(ws) & 15) return WSW_ERR_MISALIGNED;
+    if (ws_bytes < wsw_attn_paged_decode_workspace_bytes(requests, q_heads, cache->heads, cache->head_dim))
+        return WSW_ERR_WORKSPACE;
+    place(&a, ws, rows);
     DeviceInfo di;
     if (!device_info(&di, &st)) return st;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (cache->dtype == WSW_F16) e = launch_type<WSW_F16, false>(a, rows, s, o.pdl, tiles);
-    else if (cache->dtype == WSW_Q8_0) e = launch_type<WSW_Q8_0, false>(a, rows, s, o.pdl, tiles);
-    else if (dtype == WSW_F32) e = launch_type<WSW_BF16, true>(a, rows, s, o.pdl, tiles);
-    else e = launch_type<WSW_BF16, false>(a, rows, s, o.pdl, tiles);
+    const cudaError_t e = launch_paged(a, cache->dtype, rows, tiles, static_cast<cudaStream_t>(stream), o.pdl);
     return e == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
 }

@@ -80,7 +80,12 @@ struct Args {
     float cap_out;    // softcap log2 e
     int requests, q_heads, group, passes;  // passes = ceil(group / rows)
     int max_len, window;                   // window > 0
-    int dtype;                             // of q and out
+    int dtype;                             // of q
+    int out_dtype;                         // of out
+    // NULL, or for callers that join the result with another part of the positions: only those from
+    // first[r] on are seen, and a row's maximum and sum are left, too
+    const int32_t *first;
+    float2 *ml;  // [requests][q_heads]
 };
 
 // Shape of one variant: cache type, head_dim, query rows (8 or 16), third parts of q and the weights
@@ -212,14 +217,19 @@ __device__ __forceinline__ uint32_t pack16(int dtype, float x, float y) {
     return dtype == WSW_BF16 ? *reinterpret_cast<const uint32_t *>(&b) : *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ void store_out4(const Args &a, int64_t i, float4 v) {
-    if (a.dtype == WSW_F32)
+    if (a.out_dtype == WSW_F32)
         *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i) = v;
     else
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + i) =
-            make_uint2(pack16(a.dtype, v.x, v.y), pack16(a.dtype, v.z, v.w));
+            make_uint2(pack16(a.out_dtype, v.x, v.y), pack16(a.out_dtype, v.z, v.w));
 }
 __device__ __forceinline__ float lse_of(float m, float l, float shift) {
     return l == 0.f ? -INFINITY : (m + log2f(l) - shift) * kLn2;
+}
+template <typename C>
+__device__ __forceinline__ void leave_sum(const Args &a, int64_t head, float m, float l) {
+    if (a.lse) a.lse[head] = lse_of(m, l, C::shift);
+    if (a.ml) a.ml[head] = make_float2(m - C::shift, l);
 }
 // weight of a record with maximum m against the common maximum
 __device__ __forceinline__ float weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
@@ -240,17 +250,23 @@ __device__ __forceinline__ int clipped_len(const Args &a, int r) {
     const int n = a.lens[r];
     return n < 0 ? 0 : n > a.max_len ? a.max_len : n;
 }
+// the first position that request r of length len sees
+__device__ __forceinline__ int start_of(const Args &a, int r, int len) {
+    int start = len > a.window ? len - a.window : 0;
+    if (a.first) start = max(start, min(a.first[r], len));
+    return start;
+}
 template <int T>
-__device__ __forceinline__ int tiles_of(const Args &a, int len) {
-    const int seen = len < a.window ? len : a.window;
+__device__ __forceinline__ int tiles_of(const Args &a, int r, int len) {
+    const int seen = len - start_of(a, r, len);
     return seen / T + (seen % T != 0);
 }
 template <int T>
 __device__ __forceinline__ void set_request(const Args &a, Cursor &c, int r) {
     c.r = r;
     c.len = clipped_len(a, r);
-    c.nt = tiles_of<T>(a, c.len);
-    c.start = c.len > a.window ? c.len - a.window : 0;
+    c.nt = tiles_of<T>(a, r, c.len);
+    c.start = start_of(a, r, c.len);
 }
 // The next tile of the list; the caller knows that there is one.
 template <int T>
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
     for (int r = r0; r < r1; ++r) {
         const int n = a.lens[r], clipped = min(max(n, 0), a.max_len);
         cut_len |= n != clipped;
-        const int nt = tiles_of<T>(a, clipped);
+        const int nt = tiles_of<T>(a, r, clipped);
         if (r == r0) nt0 = nt;
         mine += nt * HP;
         mine_n += nt > 0 ? HP : 0;
@@ -339,7 +355,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
 #pragma unroll 1
         while (s >= at + counted(nt) * HP) {
             at += counted(nt) * HP;
-            nt = tiles_of<T>(a, clipped_len(a, ++r));
+            ++r;
+            nt = tiles_of<T>(a, r, clipped_len(a, r));
         }
         p = Place{r, s - at, nt};
     };
@@ -367,12 +384,15 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
     // requests that see nothing
 #pragma unroll 1
     for (int r = cta; r < a.requests; r += gridDim.x) {
-        if (clipped_len(a, r) > 0) continue;
+        const int n = clipped_len(a, r);
+        if (start_of(a, r, n) < n) continue;
         const int64_t head = static_cast<int64_t>(r) * a.q_heads;
 #pragma unroll 1
         for (int i = tid; i < a.q_heads * (D / 4); i += NT) store_out4(a, head * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
 #pragma unroll 1
         for (int i = tid; a.lse && i < a.q_heads; i += NT) a.lse[head + i] = -INFINITY;
+#pragma unroll 1
+        for (int i = tid; a.ml && i < a.q_heads; i += NT) a.ml[head + i] = make_float2(-INFINITY, 0.f);
     }
     __syncthreads();
     if (n_cta == 0) return;
@@ -871,10 +891,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                     for (int x = 0; x < 2; ++x) v[n][x] = (RT == 8 ? o[n][x] + o[n][2 + x] : o[n][2 * y + x]) * f;
                 if (tq == 0) {
                     if (!whole) piece_ml[2 * warp + run_end][row] = make_float2(m[y], l[y]);
-                    else if (a.lse) a.lse[head] = lse_of(m[y], l[y], C::shift);
+                    else leave_sum<C>(a, head, m[y], l[y]);
                 }
                 // lane tq's dimensions: 2 tq, 2 tq + 1 of every eight, or (q8_0) 4 tq .. 4 tq + 3 of sixteen
-                if (!whole || a.dtype == WSW_F32) {
+                if (!whole || a.out_dtype == WSW_F32) {
                     float *dst = whole ? static_cast<float *>(a.out) + head * D : rec + row * C::srec;
                     dst += C::q8 ? 4 * tq : 2 * tq;
 #pragma unroll
@@ -890,9 +910,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                     for (int n = 0; n < D / 8; n += C::q8 ? 2 : 1) {
                         if constexpr (C::q8)
                             *reinterpret_cast<uint2 *>(dst + 8 * n) =
-                                make_uint2(pack16(a.dtype, v[n][0], v[n + 1][0]), pack16(a.dtype, v[n][1], v[n + 1][1]));
+                                make_uint2(pack16(a.out_dtype, v[n][0], v[n + 1][0]),
+                                           pack16(a.out_dtype, v[n][1], v[n + 1][1]));
                         else
-                            *reinterpret_cast<uint32_t *>(dst + 8 * n) = pack16(a.dtype, v[n][0], v[n][1]);
+                            *reinterpret_cast<uint32_t *>(dst + 8 * n) = pack16(a.out_dtype, v[n][0], v[n][1]);
                     }
                 }
             }
@@ -991,7 +1012,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                 const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
                 const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
                 store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
-                if (c4 == 0 && a.lse) a.lse[head] = lse_of(ml.x, ml.y, C::shift);
+                if (c4 == 0) leave_sum<C>(a, head, ml.x, ml.y);
             } else {
                 float *r = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec + row * C::rec;
                 *reinterpret_cast<float4 *>(r + 4 + 4 * c4) = s;
@@ -1105,7 +1126,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                     const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
                     const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
                     store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
-                    if (c4 == 0 && a.lse) a.lse[head] = lse_of(ml.x, ml.y, C::shift);
+                    if (c4 == 0) leave_sum<C>(a, head, ml.x, ml.y);
                 } else {
                     // the group's record takes the place of its first CTA's: this thread has read
                     // what it writes, and everyone the (m, l)
@@ -1125,6 +1146,15 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
 
 template <int CT, bool X3>
 cudaError_t launch_type(const Args &a, int rows, cudaStream_t s, bool pdl, int64_t tiles);
+
+// attn_paged.cu: checks a call's arguments but its workspace and fills everything but a.cnt, a.rec and
+// a.wrec; rows and tiles are launch_paged()'s.  A status.
+int prepare(const void *q, int32_t dtype, int64_t requests, int64_t q_heads, const wsw_kv_cache *cache,
+            const int32_t *table, int64_t max_pages, int64_t table_stride, const int32_t *lens, float scale,
+            float softcap, int64_t window, const float *slopes, void *out, float *lse, int32_t *err_flag, Args *a,
+            int *rows, int64_t *tiles);
+void place(Args *a, void *ws, int rows);  // the parts of the workspace
+cudaError_t launch_paged(const Args &a, int cache_dtype, int rows, int64_t tiles, cudaStream_t s, bool pdl);
 
 template <int CT, int D, int RT, bool X3>
 cudaError_t launch_one(const Args &a, cudaStream_t s, bool pdl, int64_t tiles) {

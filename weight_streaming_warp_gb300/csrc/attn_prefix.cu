@@ -1,0 +1,330 @@
+// attn_prefix.cu -- host entry of the attention over shared prefixes, its plan and its join.
+//
+// Four launches, each behind the one before: the plan (which requests share what, and the list
+// of tiles), the prefixes (attn_prefix.cuh), the rest of each request's positions
+// (attn_paged.cuh, from first[r] on) and the join:
+//   M = max_i m_i;  out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i;  lse = ln 2 (M + log2 sum_i ...)
+// over the pieces i of a row's prefix and the rest.  A row reads its pieces' (m, l) first, a lane each,
+// then their sums; a piece's maximum and sum stay apart until here, so that no logarithm is rounded
+// in between.
+#include "attn_prefix.cuh"
+#include "kv_rows.cuh"
+
+namespace wsw {
+namespace prefix {
+
+#define WSW_PREFIX_DECLARE(CT) template <> cudaError_t launch_prefix<CT>(const Args &, int, cudaStream_t, int);
+WSW_PREFIX_DECLARE(WSW_F16)
+WSW_PREFIX_DECLARE(WSW_BF16)
+WSW_PREFIX_DECLARE(WSW_Q8_0)
+
+namespace {
+
+constexpr int kMaxGroups = 16384;  // two words of shared memory each
+constexpr int kPlanThreads = 1024;
+
+// Parts of q (and whether P is one part: 128 positions a tile) by types.
+int q_parts(int dtype, int cache) {
+    if (dtype == WSW_F32) return cache == WSW_BF16 ? 3 : 2;
+    return dtype == WSW_F16 && cache == WSW_BF16 ? 2 : 1;
+}
+int tile_of(int dtype) { return dtype == WSW_F32 ? 64 : 128; }
+int row_tiles(int64_t requests, int64_t group, int64_t groups, int parts) {
+    return parts == 1 && requests * group > 128 * groups ? 2 : 1;
+}
+
+struct PlanArgs {
+    const int32_t *cu, *prefix, *lens;
+    int *begin, *off, *used, *rep, *run;  // as Plan
+    int *first, *group_of;                // [requests] where the rest begins, whose prefix it shares
+    int32_t *err;
+    int requests, groups, max_len, heads, group, unit_rows, tile;
+};
+
+__global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const PlanArgs a) {
+    extern __shared__ int sm[];
+    __shared__ int scan_sm[33];
+    int *begin = sm, *used = sm + a.groups + 1;
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    // ---- the groups' bounds: cu cut to [0, requests], and never below the one before
+    const int per = (a.groups + nt) / nt;  // of groups + 1
+    const int i0 = min(tid * per, a.groups + 1), i1 = min(i0 + per, a.groups + 1);
+    int err = 0, most = 0;
+    for (int i = i0; i < i1; ++i) most = max(most, min(max(a.cu[i], 0), a.requests));
+    int upto = most;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(WSW_FULL_MASK, upto, d);
+        if (lane >= d) upto = max(upto, y);
+    }
+    if (lane == 31) scan_sm[warp] = upto;
+    __syncthreads();
+    int before = __shfl_up_sync(WSW_FULL_MASK, upto, 1);
+    if (lane == 0) before = 0;
+    for (int w = 0; w < warp; ++w) before = max(before, scan_sm[w]);
+    for (int i = i0; i < i1; ++i) {
+        const int x = a.cu[i];
+        before = max(before, min(max(x, 0), a.requests));
+        if (before != x) err |= 4;
+        begin[i] = before;
+    }
+    __syncthreads();
+    // ---- the prefixes
+    const int g0 = min(i0, a.groups), g1 = min(i1, a.groups);
+    int sum = 0;
+    auto tiles = [&](int g, int n) {
+        const int rows = (begin[g + 1] - begin[g]) * a.group;
+        return a.heads * ((rows + a.unit_rows - 1) / a.unit_rows) * ((n + a.tile - 1) / a.tile);
+    };
+    for (int g = g0; g < g1; ++g) {
+        const int x = a.prefix[g], n = min(max(x, 0), a.max_len);
+        if (n != x) err |= 4;
+        int r = begin[g];
+        const int e = begin[g + 1];
+        // one request has nobody to share with
+        const bool shares = n > 0 && e - r > 1;
+        while (shares && r < e && min(a.lens[r], a.max_len) < n) ++r;
+        used[g] = shares && r < e ? n : 0;
+        a.used[g] = used[g];
+        a.rep[g] = r < a.requests ? r : 0;
+        sum += tiles(g, used[g]);
+    }
+    int total;
+    int at = block_scan(sum, 0x7fffffff, scan_sm, &total);
+    for (int g = g0; g < g1; ++g) {
+        a.off[g] = at;
+        a.begin[g] = begin[g];
+        at += tiles(g, used[g]);
+    }
+    if (tid == 0) {
+        a.off[a.groups] = total;
+        a.begin[a.groups] = begin[a.groups];
+        *a.run = max((total + kCtas - 1) / kCtas, 1);
+    }
+    if (err && a.err) atomicOr(a.err, err);
+    // ---- each request's part (used and begin are complete: the scan has barriers)
+    for (int r = tid; r < a.requests; r += nt) {
+        int lo = 0, n = a.groups;  // the last group that begins at r or before
+        while (n > 1) {
+            const int half = n >> 1;
+            if (begin[lo + half] <= r) lo += half;
+            n -= half;
+        }
+        const bool in = r >= begin[0] && r < begin[a.groups];
+        const bool shares = in && used[lo] > 0 && min(a.lens[r], a.max_len) >= used[lo];
+        a.first[r] = shares ? used[lo] : 0;
+        a.group_of[r] = shares ? lo : -1;
+    }
+}
+
+struct JoinArgs {
+    Plan plan;
+    const int *group_of;
+    const float *rec, *whole;
+    const float *rest;   // [rows][D]
+    const float2 *ml;    // [rows]
+    void *out;
+    float *lse;
+    int64_t rows;        // requests * q_heads
+    int q_heads, group, row_tiles, tile, dtype;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) prefix_join_kernel(const JoinArgs a) {
+    constexpr int N = D / 32, kRec = D + 4;  // values of a lane
+    using V = std::conditional_t<N == 4, float4, float2>;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    pdl_launch_dependents();
+    pdl_wait();
+    if (row >= a.rows) return;
+    const int req = static_cast<int>(row / a.q_heads), head = static_cast<int>(row - static_cast<int64_t>(req) * a.q_heads);
+    const int g = a.group_of[req];
+    const V rest = *reinterpret_cast<const V *>(a.rest + row * D + lane * N);
+    const float2 ml = a.ml[row];
+    float s[N], m = ml.x, l = ml.y;
+    const float *r = reinterpret_cast<const float *>(&rest);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = r[i] * l;  // the rest comes divided by its sum
+    if (g >= 0) {
+        const int unit_rows = 128 * a.row_tiles;
+        const int rows = (a.plan.begin[g + 1] - a.plan.begin[g]) * a.group;
+        const int nt = (a.plan.used[g] + a.tile - 1) / a.tile, run = *a.plan.run;
+        const int kv = head / a.group, in = (req - a.plan.begin[g]) * a.group + head - kv * a.group;
+        const int unit = kv * ((rows + unit_rows - 1) / unit_rows) + in / unit_rows;
+        const int first = a.plan.off[g] + unit * nt, c0 = first / run, c1 = (first + nt - 1) / run;
+        const int n = c1 - c0 + 1;
+        // piece k: a unit that one CTA has whole, or of CTA c0 + k its last piece (k = 0) or its first
+        const int64_t apart = static_cast<int64_t>(2) * unit_rows * kRec;
+        const float *one = n == 1 ? a.whole + row * kRec
+                                  : a.rec + (static_cast<int64_t>(c0) * 2 * unit_rows + in % unit_rows) * kRec;
+        auto piece = [&](int k) {
+            return n == 1 ? one : one + k * apart + (k == 0 ? static_cast<int64_t>(unit_rows) * kRec : 0);
+        };
+        float mx = m;
+        for (int k = lane; k < n; k += 32) mx = fmaxf(mx, piece(k)[0]);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
+        const float f = paged::weight(m, mx);
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = f == 0.f ? 0.f : s[i] * f;
+        l *= f;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float *p = piece(k);
+            const float2 pml = *reinterpret_cast<const float2 *>(p);
+            const V v = *reinterpret_cast<const V *>(p + 4 + lane * N);
+            const float w = paged::weight(pml.x, mx);
+            const float *x = reinterpret_cast<const float *>(&v);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = w == 0.f ? s[i] : fmaf(x[i], w, s[i]);
+            l = fmaf(pml.y, w, l);
+        }
+        m = mx;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * paged::kLn2;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] *= inv;
+    const int64_t at = row * D + lane * N;
+    if (a.dtype == WSW_F32) {
+        *reinterpret_cast<V *>(static_cast<float *>(a.out) + at) = *reinterpret_cast<const V *>(s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + at + i) = paged::pack16(a.dtype, s[i], s[i + 1]);
+    }
+}
+
+size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// The workspace: the paged attention's part first (its counters stay at the beginning whatever the sizes),
+// the plan, the prefixes' pieces and whole units, the rest's results.
+struct Room {
+    size_t plan, rec, whole, rest, ml, bytes;
+};
+Room room(int64_t requests, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    Room w;
+    const size_t rows = static_cast<size_t>(requests) * q_heads, rec = static_cast<size_t>(head_dim + 4) * 4;
+    // two row tiles by the rule for one part of q: the most that any types need
+    const int rt = row_tiles(requests, q_heads / kv_heads, groups, 1);
+    w.plan = align256(wsw_attn_paged_decode_workspace_bytes(requests, q_heads, kv_heads, head_dim));
+    w.rec = w.plan + align256((4 * (static_cast<size_t>(groups) + 1) + 1 + 2 * static_cast<size_t>(requests)) * 4);
+    w.whole = w.rec + static_cast<size_t>(kCtas) * 2 * rt * 128 * rec;
+    w.rest = w.whole + align256(rows * rec);
+    w.ml = w.rest + align256(rows * head_dim * 4);
+    w.bytes = w.ml + rows * 8;
+    return w;
+}
+
+}  // namespace
+}  // namespace prefix
+}  // namespace wsw
+
+extern "C" size_t wsw_attn_paged_prefix_workspace_bytes(int64_t requests, int64_t groups, int64_t q_heads,
+                                                        int64_t kv_heads, int64_t head_dim) {
+    using namespace wsw::prefix;
+    if (requests < 0 || groups < 1 || groups > kMaxGroups || (head_dim != 64 && head_dim != 128) ||
+        wsw_attn_paged_decode_workspace_bytes(requests, q_heads, kv_heads, head_dim) == 0)
+        return 0;
+    return room(requests, groups, q_heads, kv_heads, head_dim).bytes;
+}
+
+extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t requests, int64_t q_heads,
+                                     const wsw_kv_cache *cache, const int32_t *table, int64_t max_pages,
+                                     int64_t table_stride, const int32_t *lens, const int32_t *cu_groups,
+                                     int64_t groups, const int32_t *prefix_len, float scale, float softcap,
+                                     const float *slopes, void *out, float *lse, int32_t *err_flag, void *ws,
+                                     size_t ws_bytes, void *stream, const wsw_launch_opts *opts) {
+    using namespace wsw;
+    using namespace wsw::prefix;
+    Opts o;
+    int st = resolve_opts(opts, &o);
+    if (st != WSW_OK) return st;
+    paged::Args rest;
+    int rows = 0;
+    int64_t list = 0;
+    st = paged::prepare(q, dtype, requests, q_heads, cache, table, max_pages, table_stride, lens, scale, softcap, 0, slopes,
+                        out, lse, err_flag, &rest, &rows, &list);
+    if (st != WSW_OK) return st;
+    if (groups < 1) return WSW_ERR_INVALID_ARG;
+    if (groups > kMaxGroups || rest.kv.head_dim == 256) return WSW_ERR_UNSUPPORTED;
+    if (requests == 0) return WSW_OK;
+    if (!cu_groups || !prefix_len || !ws) return WSW_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(cu_groups) | reinterpret_cast<uintptr_t>(prefix_len)) & 3) ||
+        (reinterpret_cast<uintptr_t>(ws) & 15))
+        return WSW_ERR_MISALIGNED;
+    const int64_t kv_heads = cache->heads, group = rest.group;
+    // the longest list: tiles are counted in 32 bits
+    const int64_t units = kv_heads * (requests * group / 128 + groups), longest = (rest.max_len + 63) / 64;
+    if (requests * q_heads > (int64_t(1) << 30) || units * (longest + 1) >= (int64_t(1) << 31) - 65536)
+        return WSW_ERR_UNSUPPORTED;
+    const Room w = room(requests, groups, q_heads, kv_heads, cache->head_dim);
+    if (ws_bytes < w.bytes) return WSW_ERR_WORKSPACE;
+    DeviceInfo di;
+    if (!device_info(&di, &st)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    unsigned char *base = static_cast<unsigned char *>(ws);
+
+    const int rt = row_tiles(requests, group, groups, q_parts(dtype, cache->dtype));
+    PlanArgs p;
+    p.cu = cu_groups; p.prefix = prefix_len; p.lens = lens; p.err = err_flag;
+    p.begin = reinterpret_cast<int *>(base + w.plan);
+    p.off = p.begin + groups + 1;
+    p.used = p.off + groups + 1;
+    p.rep = p.used + groups + 1;
+    p.run = p.rep + groups + 1;
+    p.first = p.run + 1;
+    p.group_of = p.first + requests;
+    p.requests = rest.requests; p.groups = static_cast<int>(groups); p.max_len = rest.max_len;
+    p.heads = rest.kv.heads; p.group = rest.group; p.unit_rows = 128 * rt; p.tile = tile_of(dtype);
+    const int plan_smem = static_cast<int>((2 * groups + 1) * 4);
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(prefix_plan_kernel), (2 * kMaxGroups + 1) * 4);
+    if (e == cudaSuccess)
+        e = launch(prefix_plan_kernel, dim3(1), dim3(requests > 256 || groups > 256 ? kPlanThreads : 256), plan_smem, s, o.pdl, p);
+    if (e != cudaSuccess) return WSW_ERR_CUDA;
+
+    Args a;
+    a.q = q; a.slopes = slopes; a.table = table; a.lens = lens; a.err = err_flag;
+    a.plan = Plan{p.begin, p.off, p.used, p.rep, p.run};
+    a.rec = reinterpret_cast<float *>(base + w.rec);
+    a.whole = reinterpret_cast<float *>(base + w.whole);
+    a.kv = rest.kv;
+    a.table_stride = table_stride;
+    a.scale2 = std::fabs(rest.scale2);
+    a.cap_in = std::fabs(rest.cap_in);
+    a.cap_out = rest.cap_out;
+    a.q_heads = rest.q_heads; a.group = rest.group; a.groups = p.groups; a.max_len = rest.max_len;
+    a.dtype = dtype;
+    a.negative = scale < 0.f;
+    const int64_t most = units * longest;
+    const int ctas = static_cast<int>(most < kCtas ? (most < 1 ? 1 : most) : kCtas);
+    if (cache->dtype == WSW_F16) e = launch_prefix<WSW_F16>(a, rt, s, ctas);
+    else if (cache->dtype == WSW_BF16) e = launch_prefix<WSW_BF16>(a, rt, s, ctas);
+    else e = launch_prefix<WSW_Q8_0>(a, rt, s, ctas);
+    if (e != cudaSuccess) return WSW_ERR_CUDA;
+
+    paged::place(&rest, ws, rows);
+    rest.first = p.first;
+    rest.out = base + w.rest;
+    rest.out_dtype = WSW_F32;
+    rest.lse = nullptr;
+    rest.ml = reinterpret_cast<float2 *>(base + w.ml);
+    e = paged::launch_paged(rest, cache->dtype, rows, list, s, true);
+    if (e != cudaSuccess) return WSW_ERR_CUDA;
+
+    JoinArgs j;
+    j.plan = a.plan;
+    j.group_of = p.group_of;
+    j.rec = a.rec; j.whole = a.whole;
+    j.rest = reinterpret_cast<const float *>(rest.out); j.ml = rest.ml;
+    j.out = out; j.lse = lse;
+    j.rows = requests * q_heads;
+    j.q_heads = rest.q_heads; j.group = rest.group; j.row_tiles = rt; j.tile = p.tile; j.dtype = dtype;
+    const dim3 grid(static_cast<unsigned>((j.rows + 7) / 8));
+    e = rest.kv.head_dim == 64 ? launch(prefix_join_kernel<64>, grid, dim3(256), 0, s, true, j)
+                               : launch(prefix_join_kernel<128>, grid, dim3(256), 0, s, true, j);
+    return e == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
+}

@@ -1,0 +1,725 @@
+// attn_prefix.cuh -- attention of the requests of a group over the prefix that they share: K and V read
+// once for all of them, on the fifth-generation tensor cores.
+//
+//   x = scale q . K_p (capped by softcap tanh(. / softcap), minus slope (n - 1 - p)), log2 units
+//   m = max_p x,  l = sum_p 2^(x - m),  O = sum_p 2^(x - m) V_p       over the positions p < prefix
+// The rest of each request's positions is the paged decode attention's (attn_paged.cuh), and a last
+// kernel joins the parts (attn_prefix.cu).
+//
+// The query heads of all of a group's requests that share a KV head are the rows of one product:
+// 4 D flops per row and position against 4 D bytes (16 bits) per position, so that a few hundred rows are
+// bound by the tensor cores, a few by HBM.
+//
+//  * A unit is a tile of rows (kv head, 128 or 256 of a group's rows); the position tiles of all units,
+//    in order, are one list that is cut into equal runs for 152 CTAs, one on an SM.  A CTA leaves
+//    (m, l, O) of each piece of a unit; pieces are joined in tile order, so that results depend on
+//    the sizes alone.
+//  * Two softmax warpgroups, a thread for each row, each with its own scores S and value sums O in
+//    tensor memory.  With more than 128 rows in a group they have 128 rows each and the same K and V
+//    (half the reads); else the same rows, and take the tiles in turn; their sums are joined
+//    when the piece ends.  One's softmax runs while the tensor cores work for the other.
+//  * The weights P go back to tensor memory over the scores, whose thread has read them; S of the next
+//    tile is issued behind the P V that reads them, and one thread's MMAs complete in order.
+//  * Four warps copy K and V rows with cp.async into a ring of tiles, swizzled as the MMAs want them:
+//    16-byte pieces by the block table, so that any page size, layout and stride is the same code (a TMA box
+//    cannot cross a page, and pages may have one position).  q8_0 codes become binary16(scale * code)
+//    on the way.  A tile is signalled two tiles later, when its copies have landed.
+//  * q, scores, sums and l are fp32 or parts: q over its own 16-bit type is exact, a bf16 or fp32 row
+//    over binary16 takes the power of two that brings its largest value to 2^14 .. 2^15 and, fp32, a second
+//    part (22 bits); fp16 over bf16 is two parts, fp32 over bf16 three, both exact.  Under 16-bit queries P is
+//    rounded to the cache's 16-bit type: 2^-9 (bf16) or 2^-12 of each weight against the result's own
+//    rounding of 2^-9 or 2^-12; under fp32 queries P is two (binary16) or three (bf16) parts.
+//  * The maximum in use is raised, and O rescaled, only when a tile exceeds it by more than kLazy.
+//  * Every wait is bounded; a role whose wait ran out stops, and the rows' l is NaN.
+#pragma once
+
+#include "attn_paged.cuh"
+#include "tc_util.cuh"
+
+namespace wsw {
+namespace prefix {
+
+using paged::cp16;
+using paged::cp_commit;
+using paged::cp_wait;
+using paged::ex2;
+using paged::kLazy;
+using paged::kLog2e;
+using paged::split;
+using paged::split3;
+
+constexpr int kCtas = 152;     // runs of the tile list
+constexpr int kLoaders = 4;    // warps
+constexpr int kMmaWarp = 8 + kLoaders;
+constexpr int kThreads = 512;  // whole warpgroups: three warps beside the MMAs' are idle
+// registers of a thread, by role; launched with 128 each
+constexpr int kSoftRegs = 176, kLoadRegs = 96, kMmaRegs = 64;
+static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs == 4 * 65536 / kThreads, "no more than the block was launched with");
+constexpr int kSeen = 16;      // tiles whose visible positions are kept
+constexpr int kTileBytes = 224 * 1024;
+constexpr uint32_t kTmemCols = 512;
+
+// What the plan kernel leaves: [groups + 1] each but `run`.
+struct Plan {
+    const int *begin;  // first request of a group
+    const int *off;    // its tiles' place in the list
+    const int *used;   // its prefix's positions
+    const int *rep;    // the request whose table row holds its pages
+    const int *run;    // [1] tiles of a CTA
+};
+
+struct Args {
+    const void *q;
+    const float *slopes;
+    const int32_t *table, *lens;
+    int32_t *err;
+    Plan plan;
+    float *rec;    // [kCtas][2][rows of a unit][D + 4]: (m - shift, l, -, -, O) of pieces
+    float *whole;  // [requests * q_heads][D + 4]: of units that one CTA has whole
+    KvView kv;
+    int64_t table_stride;
+    float scale2;  // |scale| log2 e
+    float cap_in;  // |scale| / softcap, 0: not capped
+    float cap_out; // softcap log2 e
+    int q_heads, group, groups, max_len;
+    int dtype, negative;  // of q; scale < 0
+};
+
+// Shape of one variant: cache type, head_dim, parts of q and of P, row tiles of a unit.
+template <int CT, int D_, int QP_, int PP_, int RT_>
+struct Cfg {
+    static constexpr int D = D_, QP = QP_, PP = PP_, RT = RT_;
+    static constexpr bool q8 = CT == WSW_Q8_0, bf16 = CT == WSW_BF16;
+    // several parts of P: 64 positions, whose scores a thread keeps while the parts overwrite them
+    static constexpr int TP = PP == 1 ? 128 : 64;
+    static constexpr int stage = TP * D * 2;               // a K or V tile
+    static constexpr int q_part = 128 * D * 2;             // of a row tile
+    static constexpr int q_bytes = RT * QP * q_part;
+    static constexpr int fit = (kTileBytes - q_bytes) / stage;
+    static constexpr int stages = fit < 8 ? fit : 8;
+    static constexpr int ahead = RT == 1 ? 2 : 1;          // K tiles before their V tiles
+    static constexpr int s_cols = PP == 3 ? 96 : TP;       // of a slot: scores, then P's parts
+    static constexpr uint32_t o_col = 2 * s_cols;
+    static constexpr float shift = bf16 ? -kLazy : 7.f;    // log2 of the weights' scale
+    static constexpr int rec = D + 4;
+    static_assert(2 * s_cols + 2 * D <= 512 && stages >= 4 && kSeen >= stages + 4, "room");
+    static constexpr int smem = q_bytes + stages * stage + 2048 + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory");
+};
+
+struct Control {
+    uint64_t full[8], empty[8];
+    uint64_t s_full[2], p_full[2];
+    uint64_t q_full, o_done;
+    uint32_t seen[kSeen][4];
+    float2 ml[128];
+    uint32_t tmem;
+    int at[2];  // the first tile's group and its place there
+};
+static_assert(sizeof(Control) <= 2048 && kTileBytes + 2048 + 1024 <= 227 * 1024, "control");
+
+// The pieces of a CTA's run, in order; every role walks them.
+template <typename C>
+struct Walk {
+    const Args &a;
+    int pos, end;                 // places in the list
+    int g, in;                    // group, place in its part
+    int begin, rows, used, rep;   // of the group: first request, query rows per KV head, positions
+    int nt, per_head;             // tiles and row tiles
+    // the piece
+    int head, tile, t0, n;        // KV head, unit of the head, first tile, tiles
+
+    __device__ Walk(const Args &a_, int pos_, int end_, int g_, int in_) : a(a_), pos(pos_), end(end_), g(g_), in(in_) {
+        if (pos < end) group();
+    }
+    __device__ void group() {
+        begin = a.plan.begin[g];
+        rows = (a.plan.begin[g + 1] - begin) * a.group;
+        used = a.plan.used[g];
+        rep = a.plan.rep[g];
+        nt = (used + C::TP - 1) / C::TP;
+        per_head = (rows + 128 * C::RT - 1) / (128 * C::RT);
+    }
+    __device__ bool next() {
+        if (pos >= end) return false;
+        while (in >= nt * per_head * a.kv.heads) {  // the next group with tiles: there is one
+            do ++g;
+            while (a.plan.off[g + 1] == a.plan.off[g]);
+            in = 0;
+            group();
+        }
+        const int unit = in / nt;
+        t0 = in - unit * nt;
+        head = unit / per_head;
+        tile = unit - head * per_head;
+        n = min(nt - t0, end - pos);
+        pos += n;
+        in += n;
+        return true;
+    }
+    __device__ bool whole() const { return n == nt; }
+};
+
+__device__ __forceinline__ bool mbar_test(uint64_t *b, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done) : "r"(tc::saddr(b)), "r"(parity) : "memory");
+    return done;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+// The two softmax warpgroups' barrier; whether all their threads say yes.
+__device__ __forceinline__ bool both_agree(bool yes) {
+    uint32_t all;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, 256, p;\n"
+                 " selp.u32 %0, 1, 0, q;\n}" : "=r"(all) : "r"(static_cast<uint32_t>(yes)) : "memory");
+    return all;
+}
+// byte address of 16-byte piece c of row r in a swizzled tile of boxes of 64 values
+__device__ __forceinline__ uint32_t swizzled(int r, int c, int rows) {
+    return static_cast<uint32_t>((c >> 3) * rows * 128 + r * 128 + ((c & 7) ^ (r & 7)) * 16);
+}
+
+template <int CT, int D, int QP, int PP, int RT>
+__global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_constant__ Args a) {
+    using namespace tc;
+    using C = Cfg<CT, D, QP, PP, RT>;
+    constexpr int TP = C::TP, S = C::stages;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                             ~static_cast<uintptr_t>(1023));
+    unsigned char *q_sm = tiles, *ring = tiles + C::q_bytes;
+    Control &ct = *reinterpret_cast<Control *>(ring + S * C::stage);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&ct.full[i], kLoaders);
+            mbar_init(&ct.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ct.s_full[i], 1);
+            mbar_init(&ct.p_full[i], 4);
+        }
+        mbar_init(&ct.q_full, 8);
+        mbar_init(&ct.o_done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&ct.tmem)),
+                     "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    const int total = a.plan.off[a.groups], run = *a.plan.run;
+    const int pos = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * run, static_cast<int64_t>(total)));
+    const int end = min(pos + run, total);
+    if (warp == 0 && pos < end) {  // the last group that begins at pos or before
+        int lo = 0, n = a.groups;
+        while (n > 1) {
+            const int step = (n + 31) / 32;
+            const bool before = lane * step < n && a.plan.off[lo + lane * step] <= pos;
+            const int at = (__popc(__ballot_sync(WSW_FULL_MASK, before)) - 1) * step;
+            lo += at;
+            n = min(step, n - at);
+        }
+        if (lane == 0) {
+            ct.at[0] = lo;
+            ct.at[1] = pos - a.plan.off[lo];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ct.tmem;
+    bool ok = true;
+
+    if (warp >= 8 && warp < kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+        Walk<C> w(a, pos, end, ct.at[0], ct.at[1]);
+        // ---- K and V tiles: K_0 .. K_(ahead - 1), then V_j, K_(j + ahead), ...
+        const int lw = warp - 8;
+        constexpr int RW = TP / kLoaders;                // rows of a warp
+        constexpr int kPieces = C::q8 ? D / 16 : D / 8;  // 16-byte pieces of a row
+        constexpr int kRows = 32 / kPieces, kSteps = RW / kRows;
+        const int c = lane % kPieces, rr = lane / kPieces;
+        const int page_mask = (1 << a.kv.page_shift) - 1;
+        int item = 0, signalled = 0, k_tiles = 0;        // of the whole run
+        // tiles below `upto` have landed: for the tensor cores to see
+        auto signal = [&](int upto) {
+            fence_async_shared();
+            __syncwarp();
+            for (; signalled < upto; ++signalled)
+                if (lane == 0) mbar_arrive(&ct.full[signalled % S]);
+        };
+        while (ok && w.next()) {
+            const int32_t *row = a.table + static_cast<int64_t>(w.rep) * a.table_stride;
+            const int items = 2 * w.n;
+            // tile of the i-th item and whether it is V
+            auto tile_of = [&](int i, bool &v) {
+                const int lead = min(C::ahead, w.n);
+                if (i < lead) { v = false; return i; }
+                i -= lead;
+                // V_0, K_lead, V_1, K_(lead + 1), ... and the last V's alone
+                const int pairs = w.n - lead;
+                if (i < 2 * pairs) { v = (i & 1) == 0; return v ? i >> 1 : lead + (i >> 1); }
+                v = true;
+                return i - pairs;
+            };
+            auto page_of = [&](int i) {
+                bool v;
+                const int p = (w.t0 + tile_of(i, v)) * TP + lw * RW + lane;
+                return lane < RW && p < w.used ? row[p >> a.kv.page_shift] : -1;
+            };
+            int page = page_of(0);
+            for (int i = 0; i < items; ++i, ++item) {
+                bool v;
+                const int p = (w.t0 + tile_of(i, v)) * TP + lw * RW + lane;
+                const bool in = lane < RW && p < w.used;
+                const bool there = in && static_cast<unsigned>(page) < static_cast<unsigned>(a.kv.num_pages);
+                if (in && !there && a.err) atomicOr(a.err, 1);
+                const uint32_t valid = __ballot_sync(WSW_FULL_MASK, there);
+                const int64_t at = there ? page * a.kv.page_stride + (p & page_mask) * a.kv.pos_stride : 0;
+                const int64_t dat = C::q8 && there ? page * a.kv.d_page_stride + (p & page_mask) * a.kv.d_pos_stride : 0;
+                if (i + 1 < items) page = page_of(i + 1);
+                const unsigned char *base = (v ? a.kv.v : a.kv.k) + w.head * a.kv.head_stride;
+                const int st = item % S;
+                const uint32_t dst = saddr(ring + st * C::stage);
+                uint4 code[C::q8 ? kSteps : 1];
+                uint16_t scale[C::q8 ? kSteps : 1];
+                if constexpr (C::q8) {  // on their way before the stage is free
+                    const unsigned char *dbase = (v ? a.kv.vd : a.kv.kd) + w.head * a.kv.d_head_stride;
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        const int r = k * kRows + rr;
+                        const int64_t o = __shfl_sync(WSW_FULL_MASK, at, r), d = __shfl_sync(WSW_FULL_MASK, dat, r);
+                        const bool there_r = (valid >> r) & 1;
+                        code[k] = there_r ? __ldg(reinterpret_cast<const uint4 *>(base + o) + c) : make_uint4(0u, 0u, 0u, 0u);
+                        scale[k] = there_r ? __ldg(reinterpret_cast<const uint16_t *>(dbase + d) + (c >> 1)) : 0;
+                    }
+                }
+                if (item >= S) {
+                    const uint32_t parity = ((item / S) - 1) & 1u;
+                    if (signalled < item && !__all_sync(WSW_FULL_MASK, mbar_test(&ct.empty[st], parity))) {
+                        // nothing to copy: wait for what is on its way
+                        cp_wait<0>();
+                        signal(item);
+                    }
+                    if (!__all_sync(WSW_FULL_MASK, mbar_wait(&ct.empty[st], parity))) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (!v) {
+                    if (lane == 0) {
+                        if constexpr (RW == 32) ct.seen[k_tiles % kSeen][lw] = valid;
+                        else reinterpret_cast<uint16_t *>(ct.seen[k_tiles % kSeen])[lw] = static_cast<uint16_t>(valid);
+                    }
+                    ++k_tiles;
+                }
+                if constexpr (C::q8) {
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        const int r = k * kRows + rr;
+                        const __half2 d2 = __half2half2(__ushort_as_half(scale[k]));
+                        const uint32_t u[4] = {code[k].x ^ 0x80808080u, code[k].y ^ 0x80808080u, code[k].z ^ 0x80808080u,
+                                               code[k].w ^ 0x80808080u};
+                        uint32_t h[8];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            h[2 * x] = paged::dequant2(u[x], 0x4140, d2);
+                            h[2 * x + 1] = paged::dequant2(u[x], 0x4342, d2);
+                        }
+                        if (!((valid >> r) & 1)) {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) h[x] = 0u;
+                        }
+                        unsigned char *to = ring + st * C::stage;
+                        *reinterpret_cast<uint4 *>(to + swizzled(lw * RW + r, 2 * c, TP)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4 *>(to + swizzled(lw * RW + r, 2 * c + 1, TP)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
+                    signal(item + 1);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        const int r = k * kRows + rr;
+                        const int64_t o = __shfl_sync(WSW_FULL_MASK, at, r);
+                        cp16(dst + swizzled(lw * RW + r, c, TP), base + o + c * 16, (valid >> r) & 1);
+                    }
+                    cp_commit();
+                    if (item >= 2 && signalled < item - 1) {
+                        cp_wait<2>();
+                        signal(item - 1);
+                    }
+                }
+            }
+        }
+        cp_wait<0>();
+        signal(item);
+        __syncwarp();
+    } else if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        if (warp == kMmaWarp && lane == 0) {
+            Walk<C> w(a, pos, end, ct.at[0], ct.at[1]);
+            constexpr uint32_t id_s = instr_desc(128, TP, C::bf16);
+            constexpr uint32_t id_pv = instr_desc(128, D, C::bf16) | (1u << 16);  // B (V) MN-major
+            int item = 0, piece = 0;
+            uint32_t p_phase[2] = {0, 0};
+            auto landed = [&](int i) { return mbar_wait(&ct.full[i % S], (i / S) & 1u); };
+            auto scores = [&](int slot, int k) {
+                const uint32_t kt = saddr(ring + (k % S) * C::stage), qt = saddr(q_sm + (RT == 2 ? slot : 0) * QP * C::q_part);
+                tc_fence_after();
+#pragma unroll
+                for (int part = 0; part < QP; ++part)
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b) {
+                        const uint64_t dq = sw128_desc(qt + part * C::q_part + b * 128 * 128), dk = sw128_desc(kt + b * TP * 128);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_bf16(tmem + slot * C::s_cols, dq + 2 * kk, dk + 2 * kk, id_s, (part | b | kk) != 0);
+                    }
+            };
+            auto values = [&](int slot, int v, bool more) {
+                const uint64_t dv = sw128_mn_desc(saddr(ring + (v % S) * C::stage), TP * 128);
+#pragma unroll
+                for (int part = 0; part < PP; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < TP / 16; ++kk)
+                        mma_ts(tmem + C::o_col + slot * D, tmem + slot * C::s_cols + part * (TP / 2) + 8 * kk, dv + 128 * kk,
+                               id_pv, more || (part | kk) != 0);
+            };
+            while (ok && w.next()) {
+                ok = mbar_wait(&ct.q_full, piece & 1u);
+                ++piece;
+                if (!ok) break;
+                const int lead = min(C::ahead, w.n);
+                for (int j = 0; j < lead; ++j) {
+                    if (!(ok = landed(item))) break;
+                    for (int s = 0; s < RT; ++s) {
+                        const int slot = RT == 2 ? s : j;
+                        scores(slot, item);
+                        mma_commit(&ct.s_full[slot]);
+                    }
+                    mma_commit(&ct.empty[item % S]);
+                    ++item;
+                }
+                for (int j = 0; j < w.n && ok; ++j) {
+                    const bool more_k = j + lead < w.n;
+                    const int v = item++, k = more_k ? item++ : 0;
+                    for (int s = 0; s < RT; ++s) {
+                        const int slot = RT == 2 ? s : j & 1;
+                        if (!(ok = mbar_wait(&ct.p_full[slot], p_phase[slot]))) break;
+                        p_phase[slot] ^= 1u;
+                        if (s == 0 && !(ok = landed(v))) break;
+                        tc_fence_after();
+                        values(slot, v, RT == 2 ? j > 0 : j > 1);
+                        if (s == RT - 1) mma_commit(&ct.empty[v % S]);
+                        if (!more_k) continue;
+                        if (s == 0 && !(ok = landed(k))) break;
+                        scores(slot, k);
+                        mma_commit(&ct.s_full[slot]);
+                        if (s == RT - 1) mma_commit(&ct.empty[k % S]);
+                    }
+                }
+                if (ok) mma_commit(&ct.o_done);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: slot and row of this thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        Walk<C> w(a, pos, end, ct.at[0], ct.at[1]);
+        const int slot = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        const uint32_t s_base = lane_base + slot * C::s_cols, o_base = lane_base + C::o_col + slot * D;
+        uint32_t s_phase = 0;
+        int piece = 0, k_tiles = 0;
+        while (ok && w.next()) {
+            const int in_group = (w.tile * RT + (RT == 2 ? slot : 0)) * 128 + r;
+            const bool real = in_group < w.rows;
+            const int req = w.begin + (real ? in_group : 0) / a.group, gq = (real ? in_group : 0) % a.group;
+            const int64_t head = static_cast<int64_t>(req) * a.q_heads + w.head * a.group + gq;
+            // ---- q: this thread's row, or its half of the row that both warpgroups have
+            float unit = a.cap_in != 0.f ? a.cap_in : a.scale2;  // of a score's product sum, over softcap if capped
+            {
+                const bool wide = a.dtype == WSW_F32;
+                // eight values of the row, 16 (32) bytes
+                auto load8 = [&](int ch, float (&x)[8]) {
+                    if (wide) {
+                        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + head * D + 8 * ch);
+                        const float4 u = src[0], v = src[1];
+                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+                        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+                    } else {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + head * D + 8 * ch);
+                        const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = a.dtype == WSW_BF16 ? make_float2(bf16lo(y[i]), bf16hi(y[i]))
+                                                                 : __half22float2(*reinterpret_cast<const __half2 *>(&y[i]));
+                            x[2 * i] = f.x;
+                            x[2 * i + 1] = f.y;
+                        }
+                    }
+                    if (!real) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                    }
+                };
+                float up = a.negative ? -1.f : 1.f;
+                if constexpr (!C::bf16) {
+                    if (a.dtype != WSW_F16) {
+                        float top = 0.f;
+#pragma unroll 4
+                        for (int ch = 0; ch < D / 8; ++ch) {
+                            float x[8];
+                            load8(ch, x);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+                        }
+                        const int e = max(static_cast<int>(__float_as_uint(top) >> 23), 15);
+                        up *= __uint_as_float((268u - e) << 23);
+                        unit *= __uint_as_float((e - 14u) << 23);
+                    }
+                }
+                unsigned char *to = q_sm + (RT == 2 ? slot : 0) * QP * C::q_part;
+                const int ch0 = RT == 2 ? 0 : slot * (D / 16), ch1 = RT == 2 ? D / 8 : ch0 + D / 16;
+#pragma unroll 4
+                for (int ch = ch0; ch < ch1; ++ch) {
+                    float x[8];
+                    load8(ch, x);
+                    uint32_t part[3][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float u = x[2 * i] * up, v = x[2 * i + 1] * up;
+                        if constexpr (QP == 1) part[0][i] = pack2<C::bf16>(u, v);
+                        else if constexpr (QP == 2) split<CT>(u, v, part[0][i], part[1][i]);
+                        else split3(u, v, part[0][i], part[1][i], part[2][i]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < QP; ++k)
+                        *reinterpret_cast<uint4 *>(to + k * C::q_part + swizzled(r, ch, 128)) =
+                            make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
+                }
+                fence_async_shared();
+                tc_fence_before();  // O of the piece before has been read
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ct.q_full);
+            }
+            const float slope = a.slopes && real ? a.slopes[w.head * a.group + gq] * kLog2e : 0.f;
+            const int last = real && a.slopes ? min(max(a.lens[req], 0), a.max_len) - 1 : 0;
+            float m = -INFINITY, l = 0.f;
+            const int step = RT == 2 ? 1 : 2;
+            for (int j = RT == 2 ? 0 : slot; j < w.n; j += step) {
+                if (!__all_sync(WSW_FULL_MASK, mbar_wait(&ct.s_full[slot], s_phase))) {
+                    ok = false;
+                    break;
+                }
+                s_phase ^= 1u;
+                tc_fence_after();
+                const uint32_t *seen = ct.seen[(k_tiles + j) % kSeen];
+                const bool all = TP == 128 ? (seen[0] & seen[1] & seen[2] & seen[3]) == 0xffffffffu
+                                           : (seen[0] & seen[1]) == 0xffffffffu;
+                const bool plain = all && a.cap_in == 0.f && !a.slopes;
+                const int p0 = (w.t0 + j) * TP;
+                // 32 scores of a chunk, in log2 units where the tile is not plain
+                auto finish = [&](uint32_t (&v)[32], int chunk) {
+                    if (plain) return;
+                    const uint32_t mask = seen[chunk];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * unit);
+                    if (a.cap_in != 0.f) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(a.cap_out * tanhf(__uint_as_float(v[i])));
+                    }
+                    if (a.slopes) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __float_as_uint(fmaf(-slope, static_cast<float>(last - (p0 + 32 * chunk + i)),
+                                                        __uint_as_float(v[i])));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = (mask >> i) & 1 ? v[i] : 0xff800000u;
+                };
+                auto top = [&](const uint32_t (&v)[32], float mx) {
+                    float q4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) q4[i & 3] = fmaxf(q4[i & 3], __uint_as_float(v[i]));
+                    return fmaxf(fmaxf(q4[0], q4[1]), fmaxf(q4[2], q4[3]));
+                };
+                uint32_t va[32], vb[32];
+                float mx = -INFINITY;
+                if constexpr (TP == 128) {  // the second half's maximum; it is read again for the weights
+                    tmem_ld32(s_base + 64, va);
+                    tmem_ld32(s_base + 96, vb);
+                    tmem_wait_ld();
+                    finish(va, 2);
+                    finish(vb, 3);
+                    mx = top(vb, top(va, mx));
+                }
+                tmem_ld32(s_base, va);
+                tmem_ld32(s_base + 32, vb);
+                tmem_wait_ld();
+                finish(va, 0);
+                finish(vb, 1);
+                mx = top(vb, top(va, mx));
+                const float mul = plain ? unit : 1.f;
+                const float mt = mx * mul;
+                const bool raise = mt > m + kLazy;  // m = -inf: by anything visible
+                if (j >= step && __any_sync(WSW_FULL_MASK, raise)) {
+                    // the S that was waited for was issued behind the last P V: O is complete
+                    const float al = raise ? ex2(m - mt) : 1.f;
+                    l *= al;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o_base + 32 * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                        tmem_st32(o_base + 32 * c, o);
+                    }
+                }
+                if (raise) m = mt;
+                const float ref = m == -INFINITY ? 0.f : m - C::shift;  // nothing seen yet: all weights 0
+                const uint64_t mul2 = f2_pack(mul, mul), ref2 = f2_pack(-ref, -ref);
+                uint64_t l2a = 0ull, l2b = 0ull;  // a tile's sum by itself: l gets one rounding a tile
+                auto weights = [&](const uint32_t (&v)[32], uint32_t (&part)[PP][16]) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        uint64_t t = f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(t) : "l"(mul2), "l"(ref2));
+                        float t0, t1;
+                        f2_unpack(t, t0, t1);
+                        const float w0 = ex2(t0), w1 = ex2(t1);
+                        if (i & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(l2b) : "l"(f2_pack(w0, w1)));
+                        else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(l2a) : "l"(f2_pack(w0, w1)));
+                        if constexpr (PP == 1) part[0][i] = pack2<C::bf16>(w0, w1);
+                        else if constexpr (PP == 2) split<CT>(w0, w1, part[0][i], part[1][i]);
+                        else split3(w0, w1, part[0][i], part[1][i], part[2][i]);
+                    }
+                };
+                auto put = [&](const uint32_t (&v)[32], int chunk) {
+                    uint32_t part[PP][16];
+                    weights(v, part);
+#pragma unroll
+                    for (int k = 0; k < PP; ++k) tmem_st16(s_base + k * (TP / 2) + 16 * chunk, part[k]);
+                };
+                put(va, 0);
+                put(vb, 1);
+                if constexpr (TP == 128) {
+                    tmem_ld32(s_base + 64, va);
+                    tmem_ld32(s_base + 96, vb);
+                    tmem_wait_ld();
+                    finish(va, 2);
+                    finish(vb, 3);
+                    put(va, 2);
+                    put(vb, 3);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ct.p_full[slot]);
+                float l0, l1, l2, l3;
+                f2_unpack(l2a, l0, l1);
+                f2_unpack(l2b, l2, l3);
+                l += (l0 + l1) + (l2 + l3);
+            }
+            k_tiles += w.n;
+            // ---- the piece's (m, l, O)
+            ok = ok && mbar_wait(&ct.o_done, piece & 1u);
+            ++piece;
+            if (RT == 1 && slot == 1) ct.ml[r] = make_float2(m, l);
+            const bool have = both_agree(ok);
+            ok = have;
+            tc_fence_after();
+            if (!have) l = __int_as_float(0x7fc00000);
+            float *rec = w.whole() ? a.whole + head * C::rec
+                                   : a.rec + ((static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 == 0)) * RT +
+                                              (RT == 2 ? slot : 0)) * 128 * C::rec + r * C::rec;
+            float f0 = 1.f, f1 = 0.f, mj = m;
+            float *other = reinterpret_cast<float *>(q_sm);  // [32][128] of the second warpgroup's O: q has been read
+            const bool two = RT == 1 && w.n > 1;
+            if (two && slot == 0) {  // both warpgroups have these rows
+                const float2 o = ct.ml[r];
+                mj = fmaxf(m, o.x);
+                f0 = m == -INFINITY ? 0.f : ex2(m - mj);
+                f1 = o.x == -INFINITY ? 0.f : ex2(o.x - mj);
+                l = l * f0 + o.y * f1;
+            }
+            const bool writes = real && (RT == 2 || slot == 0);
+            if (writes) *reinterpret_cast<float2 *>(rec) = make_float2(mj == -INFINITY ? -INFINITY : mj - C::shift, l);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                const bool mine = RT == 2 || slot == 0 || two;
+                if (mine && have) {
+                    tmem_ld32(o_base + 32 * c, o);
+                    tmem_wait_ld();
+                }
+                if (two) {
+                    if (slot == 1) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) other[i * 128 + r] = __uint_as_float(o[i]);
+                    }
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    if (slot == 0) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            // a part without weights holds nothing (0 times what its rows hold may be NaN)
+                            const float x = f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
+                            o[i] = __float_as_uint(f1 == 0.f ? x : fmaf(other[i * 128 + r], f1, x));
+                        }
+                    }
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                }
+                if (writes) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4 *>(rec + 4 + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+template <int CT, int D, int QP, int PP, int RT>
+cudaError_t launch_one(const Args &a, cudaStream_t s, int ctas) {
+    using C = Cfg<CT, D, QP, PP, RT>;
+    const auto kernel = attn_prefix_kernel<CT, D, QP, PP, RT>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), C::smem);
+    if (e != cudaSuccess) return e;
+    return launch(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), C::smem, s, true, a);
+}
+
+// Row tiles of a unit: two (the warpgroups share K and V) where a group has more than 128 rows on average
+// and q is one part.
+template <int CT>
+cudaError_t launch_prefix(const Args &a, int row_tiles, cudaStream_t s, int ctas);
+
+#define WSW_PREFIX_ONE(CT, QP, PP, RT)                                                   \
+    (a.kv.head_dim == 64 ? launch_one<CT, 64, QP, PP, RT>(a, s, ctas) : launch_one<CT, 128, QP, PP, RT>(a, s, ctas))
+
+}  // namespace prefix
+}  // namespace wsw
