@@ -728,7 +728,7 @@ int wsw_kv_page_copy(const int32_t *src, const int32_t *dst, const int32_t *fill
  *               max_pages entries (the row lists nothing).
  *   ws          device workspace of ws_bytes >= wsw_kv_page_compact_workspace_bytes(num_pages),
  *               16-byte aligned, overwritten.
- *   requests <= 65535;  num_pages <= 2^26;  max_pages <= 2^31 - 2^20;  page_size a power of two
+ *   requests <= 65535;  num_pages <= 2^22;  max_pages <= 2^31 - 2^20;  page_size a power of two
  *   <= 65536;  max_moves < 2^31.
  */
 size_t wsw_kv_page_compact_workspace_bytes(int64_t num_pages);

@@ -88,11 +88,11 @@ def test_compact_rejects_on_host(lib):
     for change in ({"requests": -1}, {"width": -1}, {"stride": 7}, {"out_stride": 7}, {"page": 0}, {"pool": 0},
                    {"moves": -1}, {"out": P((3 << 20) + 4)}, {"out": P(3 << 20), "out_stride": 9}):
         assert _compact(lib, **change) == INVALID, change
-    for change in ({"requests": 65536}, {"page": 24}, {"page": 1 << 17}, {"pool": (1 << 26) + 1}, {"moves": 1 << 31},
+    for change in ({"requests": 65536}, {"page": 24}, {"page": 1 << 17}, {"pool": (1 << 22) + 1}, {"moves": 1 << 31},
                    {"stride": 1 << 50}, {"width": 1 << 31, "stride": 1 << 31, "out_stride": 1 << 31}):
         assert _compact(lib, **change) == UNSUPPORTED, change
     need = lib.wsw_kv_page_compact_workspace_bytes
-    assert need(0) == 0 and need((1 << 26) + 1) == 0 and need(100) >= 100 + 400
+    assert need(0) == 0 and need((1 << 22) + 1) == 0 and need(100) >= 100 + 400
     assert _compact(lib, ws_bytes=need(100) - 1) == WORKSPACE
 
 

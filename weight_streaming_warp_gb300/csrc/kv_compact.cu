@@ -7,10 +7,14 @@
 //   free list: the pages not live then, in ascending order, in the last places of `free_pages`
 //
 // Nothing is counted from one call to the next: what is free is what the rows do not list.  Bytes:
-// the entries in (and out, with moves), a mark and a held byte a page, the free list; two passes over the
-// tables and three over the marks with barriers in between, so one cluster (a CTA alone for little), whose
-// barriers cost half a microsecond.  With pages' prefix counts of live, moving and filled ones a
-// free page's place needs no scan of its own: p - live(p) + moved(p) - filled(p) lie below it.
+// the entries in (and out, with moves), a held byte a page, the free list.  One cluster, of which each CTA has
+// a run of the pages as bits in shared memory: it reads all entries and marks those of its own
+// run (marks as bytes in memory, each CTA's entries scattered over them, took 9 us of 16 for 64 rows
+// of 380 entries: an SM sends a scattered store every 8 cycles or so; all CTAs' reads are 1 us).  A warp
+// takes 32 pages at a time, a lane each, so that ranks are ballots; with the counts of live, moving and
+// filled pages before a page its place in the free list needs no scan of its own: p - live + moved -
+// filled pages lie below it.  The CTAs exchange their counts through the workspace, a barrier
+// of the cluster (1 us) for each exchange.
 #include "kv_rows.cuh"
 
 namespace wsw {
@@ -18,30 +22,20 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kSegment = 256;  // entries of a row that a warp takes
-constexpr int64_t kMaxPages = int64_t(1) << 26;
+constexpr int64_t kMaxPages = int64_t(1) << 22;  // two bits each in the shared memory of 8 CTAs
 
 struct CompactArgs {
     const int32_t *seq, *table;
     const uint8_t *held;
     int32_t *table_out, *free_pages, *head, *src, *dst, *count, *err;
-    uint8_t *mark;       // [pages rounded up to 16]
-    int32_t *to;         // [pages] where each page goes (with moves)
+    int32_t *to;         // [pages] where a page that may move goes
     int *sums;           // [3][16] of the CTAs
     int64_t table_stride, out_stride;
-    int rows, shift, max_pages, pages, max_moves;
+    int rows, shift, max_pages, pages, max_moves, run;  // run: pages of a warp, a multiple of 32
 };
 
-__device__ __forceinline__ unsigned bytes_set(unsigned w) {  // of bytes 0 or 1
-    return __popc(w & 0x01010101u);
-}
-__device__ __forceinline__ unsigned nonzero(unsigned w) {    // bytes to 0 or 1
-    w |= w >> 4;
-    w |= w >> 2;
-    w |= w >> 1;
-    return w & 0x01010101u;
-}
-
 __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const CompactArgs a) {
+    extern __shared__ uint32_t bits[];  // [words of the CTA] listed pages, then held ones
     __shared__ int scan_sm[33];
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
     const int cta = blockIdx.x, ncta = gridDim.x;
@@ -49,23 +43,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const CompactAr
         if (ncta > 1) cluster_barrier();
         else __syncthreads();
     };
+    const int own_words = a.run / 32 * (nt >> 5);
+    uint32_t *listed_bits = bits, *held_bits = bits + own_words;
+    const unsigned first_page = static_cast<unsigned>(cta) * (a.run * (nt >> 5)), own_pages = 32u * own_words;
+    for (int i = tid; i < own_words; i += nt) listed_bits[i] = 0u;
     pdl_launch_dependents();
     pdl_wait();
-    // a thread has `per` times sixteen consecutive pages
-    const int vecs = (a.pages + 15) >> 4, threads = ncta * nt, me = cta * nt + tid;
-    const int per = (vecs + threads - 1) / threads;
-    const int v0 = min(me * per, vecs), v1 = min(v0 + per, vecs);
-    uint4 *marks = reinterpret_cast<uint4 *>(a.mark);
-    for (int v = me; v < vecs; v += threads) marks[v] = make_uint4(0u, 0u, 0u, 0u);
-    barrier();
+    const int64_t start = static_cast<int64_t>(first_page) + static_cast<int64_t>(tid >> 5) * a.run;
+    const int p0 = static_cast<int>(min(start, static_cast<int64_t>(a.pages)));
+    const int p1 = static_cast<int>(min(start + a.run, static_cast<int64_t>(a.pages)));
+    uint32_t *listed_run = listed_bits + (tid >> 5) * (a.run / 32), *held_run = held_bits + (tid >> 5) * (a.run / 32);
+    for (int base = p0, w = 0; base < p1; base += 128, w += 4) {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = base + 32 * i + lane;
+            h[i] = a.held && p < p1 ? a.held[p] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = __ballot_sync(WSW_FULL_MASK, h[i]);
+            if (lane == 0 && base + 32 * i < p1) held_run[w + i] = h[i];
+        }
+    }
+    __syncthreads();
 
     // ---- marks
     int err = 0;
-    const int segments = (a.max_pages + kSegment - 1) / kSegment;
+    const int segments = max((a.max_pages + kSegment - 1) / kSegment, 1);  // one for the lengths at least
     const int64_t tasks = static_cast<int64_t>(a.rows) * segments;
-    // every entry that a row uses: f(row's offsets in and out, entry's number, entry)
-    auto entries = [&](auto f) {
-        for (int64_t t = me >> 5; t < tasks; t += threads >> 5) {
+    // every entry that a row uses, shared among warps first, first + step, ...: f(row, entry's number, entry)
+    auto entries = [&](int64_t from, int step, auto f) {
+        for (int64_t t = from; t < tasks; t += step) {
             // neighbouring warps take neighbouring rows: the long ones' ends spread
             const int s = static_cast<int>(t / a.rows), r = static_cast<int>(t - static_cast<int64_t>(s) * a.rows);
             const int n = a.seq[r];
@@ -89,93 +98,66 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const CompactAr
             }
         }
     };
-    entries([&](int, int, int page) {
-        if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pages)) a.mark[page] = 1;
-        else err |= 1;
+    entries(tid >> 5, nt >> 5, [&](int, int, int page) {
+        const unsigned at = static_cast<unsigned>(page) - first_page;
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.pages)) err |= 1;
+        else if (at < own_pages) atomicOr(&listed_bits[at >> 5], 1u << (at & 31));
     });
-    if (err && a.err) atomicOr(a.err, err);
-    barrier();
+    if (err && a.err && cta == 0) atomicOr(a.err, err);
+    __syncthreads();
+
+    // f(page, whether a row lists it, whether it is held) for the warp's pages, all lanes together
+    auto pages = [&](auto f) {
+        for (int base = p0, w = 0; base < p1; base += 32, ++w)
+            f(base + lane, (listed_run[w] >> lane) & 1u, (held_run[w] >> lane) & 1u);
+    };
+    const uint32_t below = (1u << lane) - 1;
+    auto count = [&](bool x) { return __popc(__ballot_sync(WSW_FULL_MASK, x)); };
+    auto rank = [&](bool x) { return __popc(__ballot_sync(WSW_FULL_MASK, x) & below); };
+    // what the block's earlier warps and the earlier CTAs have of a warp's count, and all
+    auto exchange = [&](int which, int mine, int *before) {
+        int total;
+        const int own = block_scan(lane == 0 ? mine : 0, 0x7fffffff, scan_sm, &total);
+        *before = __shfl_sync(WSW_FULL_MASK, own, 0);
+        if (tid == 0) a.sums[which * 16 + cta] = total;
+    };
+    auto collect = [&](int which, int *before, int *all) {
+        const int x = lane < ncta ? __ldcg(a.sums + which * 16 + lane) : 0;
+        *before += __reduce_add_sync(WSW_FULL_MASK, lane < cta ? x : 0);
+        *all = __reduce_add_sync(WSW_FULL_MASK, x);
+    };
 
     // ---- live pages
-    auto held16 = [&](int v) {  // 0 or 1 in each byte; a page past the last one reads as held, not live
-        uint4 h = make_uint4(0u, 0u, 0u, 0u);
-        if (!a.held) return h;
-        if (16 * v + 16 <= a.pages && (reinterpret_cast<uintptr_t>(a.held) & 15) == 0) {
-            h = reinterpret_cast<const uint4 *>(a.held)[v];
-            h.x = nonzero(h.x); h.y = nonzero(h.y); h.z = nonzero(h.z); h.w = nonzero(h.w);
-        } else {
-            unsigned w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (16 * v + i < a.pages) w[i >> 2] |= (a.held[16 * v + i] != 0 ? 1u : 0u) << (8 * (i & 3));
-            h = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        return h;
-    };
-    int live = 0, total;
-    for (int v = v0; v < v1; ++v) {
-        const uint4 m = __ldcg(marks + v), h = held16(v);
-        live += bytes_set(m.x | h.x) + bytes_set(m.y | h.y) + bytes_set(m.z | h.z) + bytes_set(m.w | h.w);
-    }
-    constexpr int kNoCap = 0x7fffffff;
-    int live_before = block_scan(live, kNoCap, scan_sm, &total);
-    // the other CTAs' totals: what came before, and all
-    auto exchange = [&](int which, int mine, int *before, int *all) {
-        if (tid == 0) a.sums[which * 16 + cta] = mine;
-        barrier();
-        *before = *all = 0;
-        for (int i = 0; i < ncta; ++i) {
-            const int x = __ldcg(a.sums + which * 16 + i);
-            if (i < cta) *before += x;
-            *all += x;
-        }
-    };
-    int before, many;
-    exchange(0, total, &before, &many);
-    live_before += before;
+    int live = 0, live_before, many;
+    for (int w = lane; w < (p1 - p0 + 31) / 32; w += 32) live += __popc(listed_run[w] | held_run[w]);
+    live = __reduce_add_sync(WSW_FULL_MASK, live);
+    exchange(0, live, &live_before);
+    barrier();
+    collect(0, &live_before, &many);
 
     // ---- moves
-    auto is = [](const uint4 &w, int i) {
-        const unsigned x = i < 4 ? w.x : i < 8 ? w.y : i < 12 ? w.z : w.w;
-        return (x >> (8 * (i & 3))) & 1u;
-    };
     int out_before = 0, in_before = 0, moves = 0;
     if (a.max_moves > 0) {
-        int out = 0, in = 0;
-        for (int v = v0; v < v1; ++v) {
-            const uint4 m = __ldcg(marks + v), h = held16(v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int p = 16 * v + i;
-                const bool held = is(h, i), listed = is(m, i);
-                out += listed && !held && p >= many;
-                in += !listed && !held && p < many;
-            }
-        }
-        int out_total, in_total, ignore, all_in;
-        out_before = block_scan(out, kNoCap, scan_sm, &out_total);
-        in_before = block_scan(in, kNoCap, scan_sm, &in_total);
-        if (tid == 0) a.sums[32 + cta] = in_total;
-        exchange(1, out_total, &before, &moves);
-        out_before += before;
-        ignore = all_in = 0;
-        for (int i = 0; i < ncta; ++i) {
-            const int x = __ldcg(a.sums + 32 + i);
-            if (i < cta) ignore += x;
-            all_in += x;
-        }
-        in_before += ignore;
-        moves = min(min(moves, all_in), a.max_moves);
+        int out = 0, in = 0, holes;
+        pages([&](int p, bool listed, bool held) {
+            out += count(listed && !held && p >= many);
+            in += count(!listed && !held && p < many);
+        });
+        exchange(1, out, &out_before);
+        exchange(2, in, &in_before);
+        barrier();
+        collect(1, &out_before, &moves);
+        collect(2, &in_before, &holes);
+        moves = min(min(moves, holes), a.max_moves);
         int o = out_before, k = in_before;
-        for (int v = v0; v < v1; ++v) {
-            const uint4 m = __ldcg(marks + v), h = held16(v);
-            for (int i = 0; i < 16; ++i) {
-                const int p = 16 * v + i;
-                const bool held = is(h, i), listed = is(m, i);
-                if (listed && !held && p >= many && o < moves) a.src[o++] = p;
-                else if (!listed && !held && p < many && k < moves) a.dst[k++] = p;
-            }
-        }
+        pages([&](int p, bool listed, bool held) {
+            const bool goes = listed && !held && p >= many, fills = !listed && !held && p < many;
+            const int ro = o + rank(goes), rk = k + rank(fills);
+            if (goes && ro < moves) a.src[ro] = p;
+            if (fills && rk < moves) a.dst[rk] = p;
+            o += count(goes);
+            k += count(fills);
+        });
     }
     if (cta == 0 && tid == 0) {
         *a.head = many;
@@ -184,34 +166,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const CompactAr
     if (moves > 0) barrier();  // src and dst
 
     // ---- the free list, and where each page goes
-    const int first_free = many;  // the list's last pages - many places
-    int l = live_before, o = min(out_before, moves), k = min(in_before, moves);
-    for (int v = v0; v < v1; ++v) {
-        const uint4 m = __ldcg(marks + v), h = held16(v);
-        for (int i = 0; i < 16; ++i) {
-            const int p = 16 * v + i;
-            if (p >= a.pages) break;
-            const bool held = is(h, i), listed = is(m, i), lives = held || listed;
-            const bool goes = listed && !held && p >= many && o < moves;
-            const bool filled = !lives && p < many && k < moves;
-            if (goes || (!lives && !filled)) a.free_pages[first_free + p - l + o - k] = p;
-            if (moves > 0) a.to[p] = goes ? __ldcg(a.dst + o) : p;
-            l += lives;
-            o += goes;
-            k += filled;
+    int l = live_before, o = out_before, k = in_before;
+    pages([&](int p, bool listed, bool held) {
+        const bool lives = listed || held;
+        const bool out = listed && !held && p >= many, in = !lives && p < many;
+        const int rl = l + rank(lives), ro = o + rank(out), rk = k + rank(in);
+        const bool goes = out && ro < moves, filled = in && rk < moves;
+        if (p < a.pages) {
+            // in the list's last pages - many places
+            if (goes || (!lives && !filled)) a.free_pages[many + p - rl + min(ro, moves) - min(rk, moves)] = p;
+            if (moves > 0 && out) a.to[p] = goes ? __ldcg(a.dst + ro) : p;
         }
-    }
+        l += count(lives);
+        o += count(out);
+        k += count(in);
+    });
     if (a.max_moves == 0) return;
 
-    // ---- the tables
+    // ---- the tables: pages below N stay, as do held ones
     if (moves > 0) barrier();
-    entries([&](int r, int j, int page) {
-        const bool ok = moves > 0 && static_cast<unsigned>(page) < static_cast<unsigned>(a.pages);
-        a.table_out[r * a.out_stride + j] = ok ? __ldcg(a.to + page) : page;
+    entries(cta * (nt >> 5) + (tid >> 5), ncta * (nt >> 5), [&](int r, int j, int page) {
+        int to = page;
+        if (moves > 0 && page >= many && page < a.pages && !(a.held && a.held[page])) to = __ldcg(a.to + page);
+        a.table_out[r * a.out_stride + j] = to;
     });
 }
 
-size_t mark_bytes(int64_t pages) { return (static_cast<size_t>(pages) + 15) / 16 * 16; }
 constexpr size_t kSumBytes = 3 * 16 * 4;
 
 }  // namespace
@@ -220,7 +200,7 @@ constexpr size_t kSumBytes = 3 * 16 * 4;
 extern "C" size_t wsw_kv_page_compact_workspace_bytes(int64_t num_pages) {
     using namespace wsw;
     if (num_pages < 1 || num_pages > kMaxPages) return 0;
-    return kSumBytes + mark_bytes(num_pages) + static_cast<size_t>(num_pages) * 4;
+    return kSumBytes + static_cast<size_t>(num_pages) * 4;
 }
 
 extern "C" int wsw_kv_page_compact(const int32_t *seq_len, int64_t requests, const int32_t *table, int64_t max_pages,
@@ -264,8 +244,7 @@ extern "C" int wsw_kv_page_compact(const int32_t *seq_len, int64_t requests, con
     a.src = src; a.dst = dst; a.count = count; a.err = err_flag;
     unsigned char *w = static_cast<unsigned char *>(ws);
     a.sums = reinterpret_cast<int *>(w);
-    a.mark = w + kSumBytes;
-    a.to = reinterpret_cast<int32_t *>(a.mark + mark_bytes(num_pages));
+    a.to = reinterpret_cast<int32_t *>(w + kSumBytes);
     a.table_stride = table_stride; a.out_stride = out_stride;
     a.rows = static_cast<int>(requests);
     a.shift = 0;
@@ -275,11 +254,17 @@ extern "C" int wsw_kv_page_compact(const int32_t *seq_len, int64_t requests, con
     a.max_moves = static_cast<int>(max_moves);
     static ClusterChoice choice;
     unsigned ncta = 1;
-    if (cluster_ctas(choice, reinterpret_cast<const void *>(kv_compact_kernel), kThreads, 0, di.device, &ncta) !=
+    constexpr int kMost = static_cast<int>(kMaxPages / 8 * 2 / 8);  // bytes of bits with 8 CTAs
+    static_assert(kMost <= 200 * 1024, "shared memory");
+    if (cluster_ctas(choice, reinterpret_cast<const void *>(kv_compact_kernel), kThreads, kMost + 2048, di.device, &ncta) !=
         cudaSuccess)
         return WSW_ERR_CUDA;
-    if (requests * max_pages <= 8192 && num_pages <= 8192) ncta = 1;
-    const cudaError_t e = launch_cluster(kv_compact_kernel, ncta, ncta, kThreads, 0, static_cast<cudaStream_t>(stream),
+    // little is done sooner without barriers between CTAs
+    if (requests * max_pages <= 4096 && num_pages <= 8192) ncta = 1;
+    const int64_t warps = static_cast<int64_t>(ncta) * (kThreads / 32);
+    a.run = static_cast<int>(((num_pages + warps - 1) / warps + 31) / 32 * 32);
+    const size_t smem = static_cast<size_t>(a.run) / 32 * (kThreads / 32) * 2 * 4;
+    const cudaError_t e = launch_cluster(kv_compact_kernel, ncta, ncta, kThreads, smem, static_cast<cudaStream_t>(stream),
                                          o.pdl, a);
     return e == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
 }

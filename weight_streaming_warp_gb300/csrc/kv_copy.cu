@@ -53,35 +53,51 @@ __device__ __forceinline__ void move(const unsigned char *from, unsigned char *t
     }
 }
 
+// A unit of work: copy, cache, K, V or their scales, part.
+struct Unit {
+    int src, dst, fill, layer, kind, part;
+};
+
 __global__ void __launch_bounds__(kThreads, 4) kv_copy_kernel(const __grid_constant__ CopyArgs a) {
     pdl_launch_dependents();
     pdl_wait();
     const int n = min(max(*a.count, 0), a.most);
     const int64_t each = static_cast<int64_t>(a.layers) * a.kinds * a.parts, units = n * each;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    auto fetch = [&](int64_t u) {
+        Unit x{};
+        if (u >= units) return x;
         const int e = static_cast<int>(u / each);
         int in = static_cast<int>(u - e * each);
-        const int part = in % a.parts;
+        x.src = a.src[e];
+        x.dst = a.dst[e];
+        x.fill = a.fill ? a.fill[e] : 1 << a.shift;
+        x.part = in % a.parts;
         in /= a.parts;
-        const int kind = in % a.kinds;  // K, V, K's scales, V's scales
-        const Layer &l = a.layer[in / a.kinds];
-        if (kind >= 2 && !l.q8) continue;
-        const int src = a.src[e], dst = a.dst[e];
-        const bool ok = static_cast<unsigned>(src) < static_cast<unsigned>(l.num_pages) &&
-                        static_cast<unsigned>(dst) < static_cast<unsigned>(l.num_pages);
+        x.kind = in % a.kinds;
+        x.layer = in / a.kinds;
+        return x;
+    };
+    Unit next = fetch(blockIdx.x);
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const Unit x = next;
+        next = fetch(u + gridDim.x);  // its pages' numbers on their way during this unit's copies
+        const Layer &l = a.layer[x.layer];
+        const bool scales = x.kind >= 2;
+        if (scales && !l.q8) continue;
+        const bool ok = static_cast<unsigned>(x.src) < static_cast<unsigned>(l.num_pages) &&
+                        static_cast<unsigned>(x.dst) < static_cast<unsigned>(l.num_pages);
         if (!ok && a.err && threadIdx.x == 0) atomicOr(a.err, 1);
-        if (!ok || src == dst) continue;
-        const int filled = a.fill ? min(max(a.fill[e], 0), 1 << a.shift) : 1 << a.shift;
-        const bool scales = kind >= 2;
-        unsigned char *base = scales ? (kind == 2 ? l.kd : l.vd) : (kind == 0 ? l.k : l.v);
+        if (!ok || x.src == x.dst) continue;
+        const int filled = min(max(x.fill, 0), 1 << a.shift);
+        unsigned char *base = scales ? (x.kind == 2 ? l.kd : l.vd) : (x.kind == 0 ? l.k : l.v);
         const int64_t page = scales ? l.d_page_stride : l.page_stride;
         const int64_t pos = scales ? l.d_pos_stride : l.pos_stride, head = scales ? l.d_head_stride : l.head_stride;
-        const unsigned char *from = base + src * page;
-        unsigned char *to = base + dst * page;
+        const unsigned char *from = base + x.src * page;
+        unsigned char *to = base + x.dst * page;
         const int width = scales ? l.row / 16 : 16;             // of a vector; a row's scales are one
         const int vs = scales ? 0 : 31 - __clz(l.row / 16);
         const int64_t all = (static_cast<int64_t>(filled) * l.heads) << vs;
-        const int64_t v0 = all * part / a.parts, v1 = all * (part + 1) / a.parts;
+        const int64_t v0 = all * x.part / a.parts, v1 = all * (x.part + 1) / a.parts;
         if (width == 16) move<uint4>(from, to, pos, head, l.heads, filled, vs, v0, v1);
         else if (width == 8) move<uint2>(from, to, pos, head, l.heads, filled, vs, v0, v1);
         else move<uint32_t>(from, to, pos, head, l.heads, filled, vs, v0, v1);

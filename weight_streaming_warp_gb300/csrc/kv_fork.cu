@@ -109,11 +109,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_fork_kernel(const ForkArgs a) 
 #pragma unroll 1
     for (int j0 = cta << a.col_shift; j0 < columns; j0 += static_cast<int>(gridDim.x) << a.col_shift) {
         const int c = tid & (width - 1), j = j0 + c, step = nt >> a.col_shift;
-#pragma unroll 4
+#pragma unroll 8
         for (int r = tid >> a.col_shift; r < a.rows; r += step)
             if (j < columns) stage[(r << a.col_shift) + c] = a.table[r * a.table_stride + j];
         __syncthreads();
-#pragma unroll 4
+#pragma unroll 2
         for (int i = tid >> a.col_shift; i < a.children; i += step) {
             if (j >= columns) continue;
             const int need = pages_of(len[i], a.shift), k = rank[i];
@@ -184,9 +184,10 @@ extern "C" int wsw_kv_page_fork(const int32_t *parent, int64_t children, const i
     a.n_free = static_cast<int>(n_free); a.max_pages = static_cast<int>(max_pages);
     a.shift = 0;
     while ((int64_t(1) << a.shift) < page_size) ++a.shift;
-    // the widest tile that fits, a line of 32 entries at most
+    // a sector of 8 entries wide, so that there are many tiles (64 x 8 rows of 130 pages: ___ us, lines of 32 16 us),
+    // and narrower for many rows
     const int64_t words = 3 * children + requests;
-    a.col_shift = 5;
+    a.col_shift = 3;
     while (a.col_shift > 0 && (words + (requests << a.col_shift)) * 4 > kMaxSmem) --a.col_shift;
     const size_t smem = static_cast<size_t>(words + (requests << a.col_shift)) * 4;
     static_assert((4 * kMaxRows + 2 * kMaxRows) * 4 <= kMaxSmem, "tile");
