@@ -100,7 +100,8 @@ def beam(logits, scores, ends, scale=1.0):
         m = x.max()
         if not np.isfinite(m) or np.isnan(x).any() or not scores[b] < np.inf:
             continue
-        total[b] = scores[b] + (x - (m + math.log(np.exp(x - m).sum())))
+        # x - m first: it stays exact where m + ln S itself is huge (a row at the type's lowest value)
+        total[b] = scores[b] + ((x - m) - math.log(np.exp(x - m).sum()))
     flat = total.ravel()
     order = np.lexsort((np.arange(flat.size), -flat))
     nxt, ended = [], []

@@ -145,7 +145,7 @@ def test_one_workspace_serves_calls_of_different_sizes():
     for turn in range(2):
         for i, (n, beams, vocab) in enumerate(sizes):
             _check(wsw, _logits(i + turn, n, beams, vocab), _scores(i, n, beams), [1], ws=ws, opts={"pdl": turn})
-    assert (ws[:2048 + 4 * 16384] == 0).all()
+    assert (ws[:4 * 16384] == 0).all()
 
 
 def test_results_are_the_same_in_a_graph_and_on_another_stream():

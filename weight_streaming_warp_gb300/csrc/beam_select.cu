@@ -6,18 +6,19 @@
 // Nothing beyond a row's k = beams * (1 + end tokens) largest logits can be chosen: an end token
 // takes one place in each row at most.  So a row is streamed once, as for its log probabilities
 // (topk_rows.cuh), with its sum and its k best kept; rows are split over CTAs when there are few.
-// The last CTA of a row joins its splits, the last row of a request merges the rows' lists: a lane
-// holds the head of each beam's list, and a step finds the best head with two warp-wide
-// maxima.
+// Each CTA leaves its part's maximum, sum and k best keys; the last CTA of a request merges the lists of
+// all its beams' parts: a score that enough candidates reach comes from the heads of the lists,
+// whatever reaches it is ranked, and the ranks answer.  (Rows joined first, then the request: 3 us more.)
 //
 // The order of near candidates of different beams hangs on the difference of their lse, so that more
 // than fp32 of it counts: a thread's sum of some hundred terms is fp32 (the errors of single terms,
-// 2^-22 at most, have no common sign), the sums of threads and CTAs, the logarithm and the
-// scores are 64 bits.  lse is off by some 1e-8, and by what the rounding of scale log2 e to
+// 2^-22 at most, have no common sign); the sums of threads and CTAs, the logarithm and the
+// scores are pairs of fp32 (some 45 bits: FP64 has a hundredth of fp32's rate here, and 900 scores
+// of four operations took 5 us).  lse is off by some 1e-8, and by what the rounding of scale log2 e to
 // fp32 (6e-8 at most) makes of the mean of the log probabilities, which all beams have nearly in
-// common.  Rows of different alignment are summed in another order: beams whose k best are the
-// same logits of the same tokens, and whose sums differ by less than 2^-20, count as equal,
-// so that copies of a beam tie and rank by index.
+// common.  Rows of different alignment are summed in another order: beams whose largest logit is the
+// same value of the same token, and whose ln S differ by less than 2^-20, count as copies of each
+// other: they share the first one's, so that they tie and rank by index.
 //
 // Bound: the logits once; as the log probabilities with alternatives, by the selection's dependent steps
 // for few rows and by instructions for 16-bit logits.
@@ -37,148 +38,279 @@ struct BeamArgs {
     const float *scores;
     int32_t *parent, *token, *end_parent, *end_token;
     float *score, *end_score;
-    unsigned *row_cnt, *req_cnt;  // arrival counters, zero between calls
+    unsigned *cnt;                // [requests] arrival counters, zero between calls
     float *part;                  // [rows][splits][rec]: maximum, sum (64 bits), keys
-    uint64_t *lists;              // [rows][1 + k]: lse (64 bits), keys
     int64_t ld;
-    double scale;
-    float c;                      // scale log2 e
-    int vocab, beams, k, splits, chunk, rec, n_ends;
+    float scale, c;               // c = scale log2 e
+    int vocab, beams, want, k, splits, chunk, rec, n_ends;  // want: candidates that can matter, k: of a row
     int32_t ends[kMaxEnds];
 };
 
+// A value as the sum of two fp32, |l| at most half a step of h.
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {  // a + b, exact
+    const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+    return Two{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
+}
+__device__ __forceinline__ Two renorm(float h, float l) {   // |l| <= |h|
+    const float s = __fadd_rn(h, l);
+    return Two{s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    const Two s = two_sum(a.h, b.h);
+    return renorm(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Two operator*(Two a, float f) {
+    const float p = __fmul_rn(a.h, f);
+    return renorm(p, __fmaf_rn(a.l, f, __fmaf_rn(a.h, f, -p)));
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    const float p = __fmul_rn(a.h, b.h);
+    return renorm(p, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.h, -p))));
+}
+// a / b of positive values: the quotient's remainder, divided again
+__device__ __forceinline__ Two operator/(Two a, Two b) {
+    const float q = __fdiv_rn(a.h, b.h);
+    const Two r = a + b * -q;
+    return renorm(q, __fdiv_rn(__fadd_rn(r.h, r.l), b.h));
+}
+// ln x, x >= 1 or 0 or NaN: x = 2^e f with f in [0.7, 1.42), ln f = 2 (t + t^3 / 3 + t^5 / 5 + ...), t = (f - 1) / (f + 1),
+// |t| < 0.18; the terms from t^5 on need fp32 alone, and end where they are below 2^-45.
+__device__ __forceinline__ Two ln(Two x) {
+    if (!(x.h > 0.f) || !(x.h < INFINITY)) return Two{x.h == 0.f ? -INFINITY : NAN, 0.f};
+    int e = static_cast<int>(__float_as_uint(x.h) >> 23) - 127;
+    if ((__float_as_uint(x.h) & 0x7fffffu) > 0x350000u) ++e;  // from 1.414 on
+    const float unit = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    const Two f{x.h * unit, x.l * unit};
+    const Two t = (f + Two{-1.f, 0.f}) / (f + Two{1.f, 0.f});
+    const Two t2 = t * t;
+    const float y = t2.h;
+    float p = 1.f / 15.f;
+    p = fmaf(p, y, 1.f / 13.f);
+    p = fmaf(p, y, 1.f / 11.f);
+    p = fmaf(p, y, 1.f / 9.f);
+    p = fmaf(p, y, 1.f / 7.f);
+    p = fmaf(p, y, 1.f / 5.f);
+    // 1 / 3 and ln 2 in two parts
+    const Two series = Two{1.f, 0.f} + t2 * (Two{0.33333334f, -9.934108e-9f} + Two{p * y, 0.f});
+    return Two{0.69314718f, -1.9046543e-9f} * static_cast<float>(e) + t * series * 2.f;
+}
+
 struct BeamShared {
-    Shared top;
-    uint64_t cand[kMaxBeams * kMaxTop];  // order-preserving scores, 0: no candidate
-    double sum[kWarps];
-    double lse[kMaxBeams];
-    float max[kWarps];
-    int last;
+    Shared top;                // its buf holds the lists' keys in the end
+    uint64_t score[kCap];      // of each key, 0: no candidate
+    uint16_t at[kCap];         // the places of those that reach the threshold
+    uint64_t best[2][kMaxTop]; // the best so far, in order: scores, and their
+    int2 tag[2][kMaxTop];      // lists and tokens; two sets in turn
+    uint64_t head[kMaxBeams];  // each beam's largest logit's key
+    uint64_t group[kWarps][32];
+    Two sum[kMaxBeams], base[kMaxBeams];
+    float max[kMaxBeams], ln_s[kMaxBeams];
+    int last, n;
 };
 
-__device__ __forceinline__ uint64_t ord64(double s) {
-    if (!(s > -INFINITY) || !(s < INFINITY)) return 0;  // -inf, NaN
-    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(s + 0.0));
-    return (u >> 63) ? ~u : u | (1ull << 63);
-}
-__device__ __forceinline__ float unord64(uint64_t k) {
-    return static_cast<float>(__longlong_as_double(static_cast<long long>((k >> 63) ? k & ~(1ull << 63) : ~k)));
+// order-preserving bits of a finite score; 0: no candidate
+__device__ __forceinline__ uint64_t ord2(Two s) {
+    if (!(s.h > -INFINITY) || !(s.h < INFINITY)) return 0;  // -inf, NaN
+    return (static_cast<uint64_t>(ord(s.h)) << 32) | ord(s.l);
 }
 
-// Arrive at a counter; whether this is the last of `expected` arrivals.  The block barrier before
-// orders the block's writes before thread 0's arrival, whose release publishes them; the last
-// one's acquire, and the barrier after, order the reads behind every arrival.
-__device__ __forceinline__ bool arrive(unsigned *cnt, int expected, int *flag) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        unsigned old;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(cnt) : "memory");
-        *flag = old == static_cast<unsigned>(expected - 1);
-        if (*flag) *cnt = 0u;  // ready for the next call
-    }
-    __syncthreads();
-    return *flag;
+// (m, s) of a set raised to the maximum mx
+__device__ __forceinline__ Two raised(const BeamArgs &a, float m, Two s, float mx) {
+    return s.h == 0.f ? Two{0.f, 0.f} : s * ex2((m - mx) * a.c);  // before the first value the difference may be -inf
+}
+// The maximum and sum of groups of W lanes; every lane gets its group's.
+template <int W = 32>
+__device__ __forceinline__ void warp_total(const BeamArgs &a, float &m, Two &s) {
+    float mx = m;
+#pragma unroll
+    for (int d = W / 2; d >= 1; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
+    s = raised(a, m, s, mx);
+    m = mx;
+#pragma unroll
+    for (int d = W / 2; d >= 1; d >>= 1)
+        s = s + Two{__shfl_xor_sync(WSW_FULL_MASK, s.h, d), __shfl_xor_sync(WSW_FULL_MASK, s.l, d)};
 }
 
-// The block's maximum and sum from the threads' (m, s), the sum in 64 bits; all threads get them.
-__device__ __forceinline__ void block_total(const BeamArgs &a, BeamShared &sm, float m, double s, float &mx, double &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    mx = m;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
-    if (lane == 0) sm.max[warp] = mx;
-    __syncthreads();
-    mx = sm.max[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) mx = max_nan(mx, sm.max[w]);
-    total = s == 0. ? 0. : s * static_cast<double>(ex2((m - mx) * a.c));
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(WSW_FULL_MASK, total, d);
-    if (lane == 0) sm.sum[warp] = total;
-    __syncthreads();
-    total = 0.;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += sm.sum[w];
-}
-
-// The request's answer, once all its rows' lists are there.  Every thread calls it.
-__device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t request) {
-    const int tid = threadIdx.x, k = a.k, n = a.beams * k;
-    uint64_t *keys = sm.top.buf;
-    static_assert(kMaxBeams * kMaxTop <= kCap, "keys");
-    const uint64_t *lists = a.lists + request * a.beams * (1 + k);
-    for (int i = tid; i < n; i += kThreads) {
-        const int b = i / k;
-        keys[i] = __ldcg(lists + i + b + 1);
-    }
-    if (tid < a.beams) sm.lse[tid] = __longlong_as_double(static_cast<long long>(__ldcg(lists + tid * (1 + k))));
-    __syncthreads();
-    // copies of a beam: the first one's lse
-    double lse = 0.;
-    if (tid < a.beams) {
-        lse = sm.lse[tid];
-        for (int b = 0; b < tid; ++b) {
-            if (!(fabs(sm.lse[b] - lse) <= 9.5367431640625e-7)) continue;
-            int i = 0;
-            while (i < k && keys[b * k + i] == keys[tid * k + i]) ++i;
-            if (i < k) continue;
-            lse = sm.lse[b];
-            break;
-        }
-    }
-    __syncthreads();
-    if (tid < a.beams) sm.lse[tid] = lse;
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-        const int b = i / k;
-        const double x = static_cast<double>(unord(static_cast<uint32_t>(keys[i] >> 32)));
-        const double sc = static_cast<double>(a.scores[request * a.beams + b]);
-        sm.cand[i] = keys[i] ? ord64(sc + (a.scale * x - sm.lse[b])) : 0;
-    }
-    __syncthreads();
-    if (tid >= 32) return;
-    const int64_t out = request * a.beams;
-    int at = 0, alive = 0, ended = 0;
-    uint64_t own = tid < a.beams ? sm.cand[tid * k] : 0;
+// Each of the request's beams: score - ln S, its maximum and first key, from its parts.
+__device__ __forceinline__ void beam_sums(const BeamArgs &a, BeamShared &sm, const float *recs, int64_t request) {
+    const int tid = threadIdx.x, lane = tid & 31;
 #pragma unroll 1
-    for (int rank = 0; alive < a.beams; ++rank) {
-        const unsigned hi = static_cast<unsigned>(own >> 32);
-        const unsigned mh = __reduce_max_sync(WSW_FULL_MASK, hi);
-        if (mh == 0) break;  // no candidate is left (one has its highest bit or the next ones set)
-        const unsigned lo = hi == mh ? static_cast<unsigned>(own) : 0;
-        const unsigned ml = __reduce_max_sync(WSW_FULL_MASK, lo);
-        const int best = __ffs(__ballot_sync(WSW_FULL_MASK, hi == mh && lo == ml)) - 1;  // ties: the lowest beam
-        int token = 0;
-        bool ends = false;
-        if (tid == best) {
-            token = static_cast<int>(~static_cast<uint32_t>(keys[tid * k + at]));
-            for (int i = 0; i < a.n_ends; ++i) ends |= token == a.ends[i];
+    for (int b = tid >> 5; b < a.beams; b += kWarps) {
+        float m = -FLT_MAX;
+        Two sum{0.f, 0.f};
+        uint64_t head = 0;
+#pragma unroll 1
+        for (int i = lane; i < a.splits; i += 32) {
+            const float *r = recs + (static_cast<int64_t>(b) * a.splits + i) * a.rec;
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(r));
+            const uint64_t key = __ldcg(reinterpret_cast<const uint64_t *>(r) + 2);
+            const float mn = max_nan(m, v.x);
+            sum = raised(a, m, sum, mn) + raised(a, v.x, Two{v.z, v.w}, mn);
+            m = mn;
+            head = max(head, key);
         }
-        ends = __any_sync(WSW_FULL_MASK, ends);
-        if (tid == best) {
-            const int32_t row = static_cast<int32_t>(out + tid);
-            if (!ends) {
-                a.parent[out + alive] = row;
-                a.token[out + alive] = token;
-                a.score[out + alive] = unord64(own);
-            } else if (rank < a.beams) {
-                a.end_parent[out + ended] = row;
-                a.end_token[out + ended] = token;
-                a.end_score[out + ended] = unord64(own);
+        if (a.splits > 1) {
+            warp_total(a, m, sum);
+#pragma unroll 1
+            for (int d = 16; d >= 1; d >>= 1) head = max(head, __shfl_xor_sync(WSW_FULL_MASK, head, d));
+        }
+        if (lane == 0) {
+            sm.max[b] = m;
+            sm.sum[b] = sum;
+            sm.head[b] = head;
+        }
+    }
+    __syncthreads();
+    // a row of nothing but -inf, with a NaN or with +inf has no candidate: ln S -inf or NaN
+    if (tid >= 32) return;  // a barrier follows
+    const int b = min(lane, a.beams - 1);
+    Two l = ln(sm.sum[b]);
+    sm.ln_s[b] = l.h;
+    __syncwarp();
+    int first = b;  // of the copies of this beam
+    for (int o = b - 1; o >= 0; --o)
+        if (sm.head[o] == sm.head[b] && fabsf(sm.ln_s[o] - l.h) <= 9.5367431640625e-7f) first = o;
+    l.h = __shfl_sync(WSW_FULL_MASK, l.h, first);
+    l.l = __shfl_sync(WSW_FULL_MASK, l.l, first);
+    if (lane < a.beams) sm.base[lane] = Two{a.scores[request * a.beams + lane], 0.f} + Two{-l.h, -l.l};
+}
+
+// The request's answer, once all its rows' parts are there.  Every thread calls it.  (The loops are not
+// unrolled: of code that runs once, fetching is the larger part.)
+__device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t request) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k, want = a.want;
+    const int lists = a.beams * a.splits;  // at most kTargetCtas, or kMaxBeams
+    static_assert(kMaxBeams <= kThreads && kTargetCtas <= kCap, "keys in buf");
+    const float *recs = a.part + request * lists * a.rec;
+    uint64_t *keys = sm.top.buf;
+    // the first keys of each list: three a thread, which is enough almost always
+    constexpr int kEach = 3;
+    const int some = min(k, max(1, kEach * kThreads / lists)), here = lists * some;
+    auto key_at = [&](int i, int d0) {
+        const int list = i / some, d = d0 + i - list * some;
+        return d < k ? __ldcg(reinterpret_cast<const uint64_t *>(recs + static_cast<int64_t>(list) * a.rec + 4) + d) : 0;
+    };
+    uint64_t got[kEach];  // on their way while the sums are taken
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) got[u] = tid + u * kThreads < here ? key_at(tid + u * kThreads, 0) : 0;
+    if (tid == 0) sm.n = 0;
+    beam_sums(a, sm, recs, request);
+    int set = 0, have = 0;  // the best so far
+    uint64_t thr = 1;       // a score that a candidate has to reach
+    for (int d0 = 0;; d0 += some) {
+#pragma unroll
+        for (int u = 0; u < kEach; ++u)
+            if (tid + u * kThreads < here) keys[tid + u * kThreads] = got[u];
+#pragma unroll 1
+        for (int i = tid + kEach * kThreads; i < here; i += kThreads) keys[i] = key_at(i, d0);  // more lists than that
+        __syncthreads();
+#pragma unroll 1
+        for (int i = tid; i < here; i += kThreads) {
+            const int b = i / some / a.splits;
+            const uint64_t key = keys[i];
+            // score - ln S + scale (x - m): the difference and its product are exact pairs
+            const Two d = two_sum(unord(static_cast<uint32_t>(key >> 32)), -sm.max[b]);
+            const Two p = d * a.scale;
+            sm.score[i] = key && p.h > -INFINITY ? ord2(sm.base[b] + p) : 0;
+        }
+        __syncthreads();
+        if (d0 == 0) {
+            // a score that `want` candidates reach, from 32 candidates: the heads of 32 groups of lists,
+            // or the first few of fewer lists
+            const int depth = lists >= 32 ? 1 : min(32 / lists, some);
+            uint64_t own = 0;
+#pragma unroll 1
+            for (int i = tid; i < lists * depth; i += kThreads) own = max(own, sm.score[i / depth * some + i % depth]);
+            sm.group[warp][lane] = own;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) own = max(own, sm.group[w][lane]);
+            int more = 0;
+#pragma unroll 4
+            for (int j = 0; j < 32; ++j) {
+                const uint64_t o = __shfl_sync(WSW_FULL_MASK, own, j);
+                more += o > own || (o == own && j < lane);
             }
-            own = ++at < k ? sm.cand[tid * k + at] : 0;
+            thr = __shfl_sync(WSW_FULL_MASK, own, __ffs(__ballot_sync(WSW_FULL_MASK, more == want - 1)) - 1);
+            thr = max(thr, static_cast<uint64_t>(1));  // 0: fewer candidates than that
         }
-        alive += !ends;
-        ended += ends && rank < a.beams;
+        // ---- the candidates that reach it, ranked
+#pragma unroll 1
+        for (int i = tid; i < here; i += kThreads)
+            if (sm.score[i] >= thr) sm.at[atomicAdd(&sm.n, 1)] = static_cast<uint16_t>(i);
+        __syncthreads();
+        const int n = sm.n, all = n + have;
+        auto score_of = [&](int i) { return i < n ? sm.score[sm.at[i]] : sm.best[set][i - n]; };
+        // Equal scores: the lower beam, then the lower token.  Lists are in the order of beams and tokens, and
+        // each in its own, so that it is the lower list, then the one before in it (an earlier round's).
+        auto list_of = [&](int i) { return i < n ? sm.at[i] / some : sm.tag[set][i - n].x; };
+        auto comes_first = [&](int j, int i) {
+            if ((j < n) == (i < n)) return j < n ? sm.at[j] < sm.at[i] : j < i;
+            return j < n ? list_of(j) < list_of(i) : list_of(j) <= list_of(i);
+        };
+#pragma unroll 1
+        for (int i = tid; i < all; i += kThreads) {
+            const uint64_t mine = score_of(i);
+            int before = 0;
+#pragma unroll 2
+            for (int j = 0; j < all; ++j) {
+                const uint64_t o = score_of(j);
+                before += o > mine;
+                if (o == mine && j != i) before += comes_first(j, i);
+            }
+            if (before < want) {
+                sm.best[set ^ 1][before] = mine;
+                sm.tag[set ^ 1][before] = i < n ? make_int2(list_of(i), static_cast<int>(~static_cast<uint32_t>(keys[sm.at[i]])))
+                                                : sm.tag[set][i - n];
+            }
+        }
+        __syncthreads();
+        set ^= 1;
+        have = min(all, want);
+        if (have == want) thr = max(thr, sm.best[set][want - 1]);
+        // again where a list's last key here reaches it, too
+        bool again = false;
+#pragma unroll 1
+        for (int i = tid; i < lists; i += kThreads) again |= sm.score[i * some + some - 1] >= thr;
+        if (d0 + some >= k || !__syncthreads_or(again)) break;
+        if (tid == 0) sm.n = 0;
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) got[u] = tid + u * kThreads < here ? key_at(tid + u * kThreads, d0 + some) : 0;
+    }
+    if (tid >= 32) return;
+    // ---- in order: a lane for each of the best
+    const int64_t out = request * a.beams;
+    const bool there = lane < have;
+    const int2 tag = there ? sm.tag[set][lane] : make_int2(0, 0);
+    const int token = tag.y, row = static_cast<int>(out) + tag.x / a.splits;
+    bool ends = false;
+#pragma unroll 1
+    for (int i = 0; i < a.n_ends; ++i) ends |= there && token == a.ends[i];
+    const uint32_t alive = __ballot_sync(WSW_FULL_MASK, there && !ends), ended = __ballot_sync(WSW_FULL_MASK, ends && lane < a.beams);
+    const uint32_t below = (1u << lane) - 1;
+    const int at = __popc(alive & below), at_end = __popc(ended & below);
+    const float s = there ? unord(static_cast<uint32_t>(sm.best[set][lane] >> 32)) : 0.f;
+    if (there && !ends && at < a.beams) {
+        a.parent[out + at] = row;
+        a.token[out + at] = token;
+        a.score[out + at] = s;
+    }
+    if (ends && lane < a.beams) {
+        a.end_parent[out + at_end] = row;
+        a.end_token[out + at_end] = token;
+        a.end_score[out + at_end] = s;
     }
     // the places without a candidate
-    for (int i = alive + tid; i < a.beams; i += 32) {
-        a.parent[out + i] = a.token[out + i] = -1;
-        a.score[out + i] = -INFINITY;
+    if (lane < a.beams && lane >= __popc(alive)) {
+        a.parent[out + lane] = a.token[out + lane] = -1;
+        a.score[out + lane] = -INFINITY;
     }
-    for (int i = ended + tid; a.end_parent && i < a.beams; i += 32) {
-        a.end_parent[out + i] = a.end_token[out + i] = -1;
-        a.end_score[out + i] = -INFINITY;
+    if (a.end_parent && lane < a.beams && lane >= __popc(ended)) {
+        a.end_parent[out + lane] = a.end_token[out + lane] = -1;
+        a.end_score[out + lane] = -INFINITY;
     }
 }
 
@@ -302,50 +434,40 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
         __syncthreads();
         cut(top, k);
     }
-    float mx;
-    double total;
-    block_total(a, sm, m, static_cast<double>(s), mx, total);
-    if (a.splits > 1) {
-        float *rec = a.part + (row * a.splits + split) * a.rec;
-        if (tid == 0) {
-            rec[0] = mx;
-            reinterpret_cast<double *>(rec)[1] = total;
-        }
-        if (tid < k) reinterpret_cast<uint64_t *>(rec + 4)[tid] = tid < top.n ? top.best[tid] : 0;
-        if (!arrive(a.row_cnt + row, a.splits, &sm.last)) return;
-        const float *recs = a.part + row * a.splits * a.rec;
-        m = -FLT_MAX;
-        double sum = 0.;
-        static_assert(kTargetCtas / 2 >= kThreads, "several splits a thread");
-        for (int i = tid; i < a.splits; i += kThreads) {
-            const float *r = recs + static_cast<int64_t>(i) * a.rec;
-            const float rm = __ldcg(r);
-            const double rs = __ldcg(reinterpret_cast<const double *>(r) + 1);
-            const float mn = max_nan(m, rm);
-            sum = (sum == 0. ? 0. : sum * static_cast<double>(ex2((m - mn) * a.c))) +
-                  (rs == 0. ? 0. : rs * static_cast<double>(ex2((rm - mn) * a.c)));
-            m = mn;
-        }
-        join_keys(top, recs, a.rec, a.splits, k);
-        block_total(a, sm, m, sum, mx, total);
+    // the block's maximum and sum
+    Two sum{s, 0.f};
+    warp_total(a, m, sum);
+    if ((tid & 31) == 0) {
+        sm.max[tid >> 5] = m;
+        sm.sum[tid >> 5] = sum;
     }
-    // the row's list; a row of nothing but -inf, with a NaN or with +inf has no candidate: lse -inf or NaN
-    uint64_t *list = a.lists + row * (1 + k);
-    if (tid == 0) list[0] = static_cast<uint64_t>(__double_as_longlong(a.scale * static_cast<double>(mx) + log(total)));
-    if (tid < k) list[1 + tid] = tid < min(top.n, kCap) ? top.best[tid] : 0;
+    __syncthreads();
+    float *rec = a.part + (row * a.splits + split) * a.rec;
+    if (tid < 32) {
+        m = sm.max[tid % kWarps];
+        sum = sm.sum[tid % kWarps];
+        warp_total<kWarps>(a, m, sum);
+        if (tid == 0) *reinterpret_cast<float4 *>(rec) = make_float4(m, 0.f, sum.h, sum.l);
+    }
+    if (tid < k) reinterpret_cast<uint64_t *>(rec + 4)[tid] = tid < top.n ? top.best[tid] : 0;
+    // the block barrier orders the record before thread 0's arrival, whose release publishes
+    // it; the last arrival's acquire orders the reads behind it after every record
+    __syncthreads();
     const int64_t request = row / a.beams;
-    if (arrive(a.req_cnt + request, a.beams, &sm.last)) merge(a, sm, request);
+    if (tid == 0) {
+        unsigned old;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.cnt + request) : "memory");
+        sm.last = old == static_cast<unsigned>(a.beams * a.splits - 1);
+        if (sm.last) a.cnt[request] = 0u;  // ready for the next call
+    }
+    __syncthreads();
+    if (sm.last) merge(a, sm, request);
 }
 
-constexpr size_t kRowCounters = 2048;
-static_assert(kTargetCtas / 2 * 4 <= kRowCounters, "counters");
-// the counters' places do not depend on the sizes: one workspace serves calls of different sizes in turn
-constexpr size_t kCounterBytes = kRowCounters + kMaxRequests * 4;
+// the counters' place does not depend on the sizes: one workspace serves calls of different sizes in turn
+constexpr size_t kCounterBytes = kMaxRequests * 4;
 
-int64_t list_length(int64_t beams, int64_t vocab, int64_t n_ends) {
-    const int64_t k = beams * (1 + n_ends);
-    return k < vocab ? k : vocab;
-}
+int64_t list_length(int64_t want, int64_t vocab) { return want < vocab ? want : vocab; }
 
 }  // namespace
 }  // namespace wsw
@@ -357,10 +479,9 @@ extern "C" size_t wsw_beam_select_workspace_bytes(int64_t requests, int64_t beam
         n_ends < 0 || n_ends > kMaxEnds || beams * (1 + n_ends) > kMaxTop)
         return 0;
     int splits, chunk;
-    const int64_t rows = requests * beams, k = list_length(beams, vocab, n_ends);
+    const int64_t rows = requests * beams, k = list_length(beams * (1 + n_ends), vocab);
     split_rows(rows, vocab, &splits, &chunk);
-    const size_t records = splits > 1 ? static_cast<size_t>(rows) * splits * record_floats(k) * 4 : 0;
-    return kCounterBytes + records + static_cast<size_t>(rows) * (1 + k) * 8;
+    return kCounterBytes + static_cast<size_t>(rows) * splits * record_floats(k) * 4;
 }
 
 extern "C" int wsw_beam_select(const void *logits, int32_t dtype, int64_t requests, int64_t beams, int64_t vocab,
@@ -398,22 +519,20 @@ extern "C" int wsw_beam_select(const void *logits, int32_t dtype, int64_t reques
     a.parent = parent; a.token = token; a.score = score;
     a.end_parent = end_parent; a.end_token = end_token; a.end_score = end_score;
     a.ld = ld;
-    a.scale = static_cast<double>(scale);
-    a.c = static_cast<float>(a.scale * 1.4426950408889634);
+    a.scale = scale;
+    a.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     a.vocab = static_cast<int>(vocab);
     a.beams = static_cast<int>(beams);
-    a.k = static_cast<int>(list_length(beams, vocab, n_ends));
+    a.want = static_cast<int>(beams * (1 + n_ends));
+    a.k = static_cast<int>(list_length(a.want, vocab));
     a.n_ends = static_cast<int>(n_ends);
     for (int64_t i = 0; i < n_ends; ++i) a.ends[i] = end_tokens[i];
     const int64_t rows = requests * beams;
     split_rows(rows, vocab, &a.splits, &a.chunk);
     a.rec = record_floats(a.k);
     unsigned char *w = static_cast<unsigned char *>(ws);
-    a.row_cnt = reinterpret_cast<unsigned *>(w);
-    a.req_cnt = reinterpret_cast<unsigned *>(w + kRowCounters);
+    a.cnt = reinterpret_cast<unsigned *>(w);
     a.part = reinterpret_cast<float *>(w + kCounterBytes);
-    a.lists = reinterpret_cast<uint64_t *>(w + kCounterBytes +
-                                           (a.splits > 1 ? static_cast<size_t>(rows) * a.splits * a.rec * 4 : 0));
     const dim3 grid(static_cast<unsigned>(rows * a.splits));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
