@@ -23,7 +23,7 @@
 //  * Four warps copy K and V rows with cp.async into a ring of tiles, swizzled as the MMAs want them:
 //    16-byte pieces by the block table, so that any page size, layout and stride is the same code (a TMA box
 //    cannot cross a page, and pages may have one position).  q8_0 codes become binary16(scale * code)
-//    on the way.  A tile is signalled two tiles later, when its copies have landed.
+//    on the way.  A tile's barrier counts the threads whose copies have landed.
 //  * q, scores, sums and l are fp32 or parts: q over its own 16-bit type is exact, a bf16 or fp32 row
 //    over binary16 takes the power of two that brings its largest value to 2^14 .. 2^15 and, fp32, a second
 //    part (22 bits); fp16 over bf16 is two parts, fp32 over bf16 three, both exact.  Under 16-bit queries P is
@@ -40,8 +40,6 @@ namespace wsw {
 namespace prefix {
 
 using paged::cp16;
-using paged::cp_commit;
-using paged::cp_wait;
 using paged::ex2;
 using paged::kLazy;
 using paged::kLog2e;
@@ -52,9 +50,6 @@ constexpr int kCtas = 152;     // runs of the tile list
 constexpr int kLoaders = 4;    // warps
 constexpr int kMmaWarp = 8 + kLoaders;
 constexpr int kThreads = 512;  // whole warpgroups: three warps beside the MMAs' are idle
-// registers of a thread, by role; launched with 128 each
-constexpr int kSoftRegs = 176, kLoadRegs = 96, kMmaRegs = 64;
-static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs == 4 * 65536 / kThreads, "no more than the block was launched with");
 constexpr int kSeen = 16;      // tiles whose visible positions are kept
 constexpr int kTileBytes = 224 * 1024;
 constexpr uint32_t kTmemCols = 512;
@@ -95,21 +90,26 @@ struct Cfg {
     static constexpr int stage = TP * D * 2;               // a K or V tile
     static constexpr int q_part = 128 * D * 2;             // of a row tile
     static constexpr int q_bytes = RT * QP * q_part;
-    static constexpr int fit = (kTileBytes - q_bytes) / stage;
+    // q8_0 rows land as codes and scales, a few tiles deep, and become tiles from there
+    static constexpr int raw = q8 ? TP * (D + D / 16) : 0, raw_stages = TP == 128 ? 3 : 4;
+    static constexpr int fit = (kTileBytes - q_bytes - raw_stages * raw) / stage;
     static constexpr int stages = fit < 8 ? fit : 8;
     static constexpr int ahead = RT == 1 ? 2 : 1;          // K tiles before their V tiles
     static constexpr int s_cols = PP == 3 ? 96 : TP;       // of a slot: scores, then P's parts
     static constexpr uint32_t o_col = 2 * s_cols;
     static constexpr float shift = bf16 ? -kLazy : 7.f;    // log2 of the weights' scale
     static constexpr int rec = D + 4;
-    static_assert(2 * s_cols + 2 * D <= 512 && stages >= 4 && kSeen >= stages + 4, "room");
-    static constexpr int smem = q_bytes + stages * stage + 2048 + 1024;
+    // registers of a thread, by role; launched with 128 each
+    static constexpr int soft_regs = q8 ? 176 : 184, load_regs = q8 ? 96 : 80, mma_regs = 64;
+    static_assert(2 * soft_regs + load_regs + mma_regs == 4 * 65536 / kThreads, "what the block was launched with");
+    static_assert(2 * s_cols + 2 * D <= 512 && stages >= 3 && kSeen >= stages + 4 + (q8 ? raw_stages : 0), "room");
+    static constexpr int smem = q_bytes + stages * stage + raw_stages * raw + 2048 + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
 };
 
 struct Control {
     uint64_t full[8], empty[8];
-    uint64_t s_full[2], p_full[2];
+    uint64_t s_full[2], p_full[2];  // of a slot
     uint64_t q_full, o_done;
     uint32_t seen[kSeen][4];
     float2 ml[128];
@@ -129,9 +129,8 @@ struct Walk {
     // the piece
     int head, tile, t0, n;        // KV head, unit of the head, first tile, tiles
 
-    __device__ Walk(const Args &a_, int pos_, int end_, int g_, int in_) : a(a_), pos(pos_), end(end_), g(g_), in(in_) {
-        if (pos < end) group();
-    }
+    __device__ Walk(const Args &a_, int pos_, int end_, int g_, int in_) : a(a_), pos(pos_), end(end_), g(g_), in(in_) {}
+    // read again for each piece (from L1): not kept in registers meanwhile
     __device__ void group() {
         begin = a.plan.begin[g];
         rows = (a.plan.begin[g + 1] - begin) * a.group;
@@ -142,6 +141,7 @@ struct Walk {
     }
     __device__ bool next() {
         if (pos >= end) return false;
+        group();
         while (in >= nt * per_head * a.kv.heads) {  // the next group with tiles: there is one
             do ++g;
             while (a.plan.off[g + 1] == a.plan.off[g]);
@@ -160,11 +160,15 @@ struct Walk {
     __device__ bool whole() const { return n == nt; }
 };
 
-__device__ __forceinline__ bool mbar_test(uint64_t *b, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-                 : "=r"(done) : "r"(tc::saddr(b)), "r"(parity) : "memory");
-    return done;
+__device__ __forceinline__ void cp16_all(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -203,12 +207,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                              ~static_cast<uintptr_t>(1023));
     unsigned char *q_sm = tiles, *ring = tiles + C::q_bytes;
-    Control &ct = *reinterpret_cast<Control *>(ring + S * C::stage);
+    unsigned char *raw_ring = ring + S * C::stage;
+    Control &ct = *reinterpret_cast<Control *>(raw_ring + C::raw_stages * C::raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&ct.full[i], kLoaders);
+            mbar_init(&ct.full[i], C::q8 ? kLoaders : 32 * kLoaders);
             mbar_init(&ct.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
     bool ok = true;
 
     if (warp >= 8 && warp < kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::load_regs));
         Walk<C> w(a, pos, end, ct.at[0], ct.at[1]);
         // ---- K and V tiles: K_0 .. K_(ahead - 1), then V_j, K_(j + ahead), ...
         const int lw = warp - 8;
@@ -259,14 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
         constexpr int kRows = 32 / kPieces, kSteps = RW / kRows;
         const int c = lane % kPieces, rr = lane / kPieces;
         const int page_mask = (1 << a.kv.page_shift) - 1;
-        int item = 0, signalled = 0, k_tiles = 0;        // of the whole run
-        // tiles below `upto` have landed: for the tensor cores to see
-        auto signal = [&](int upto) {
-            fence_async_shared();
-            __syncwarp();
-            for (; signalled < upto; ++signalled)
-                if (lane == 0) mbar_arrive(&ct.full[signalled % S]);
-        };
+        constexpr int kTurn = 8 / kRows > 1 ? 8 / kRows : 1;  // steps after which the swizzle repeats
+        uint32_t to_row[kTurn];
+#pragma unroll
+        for (int k = 0; k < kTurn; ++k) to_row[k] = swizzled(lw * RW + k * kRows + rr, c, TP);
+        int item = 0, k_tiles = 0;                       // of the whole run
         while (ok && w.next()) {
             const int32_t *row = a.table + static_cast<int64_t>(w.rep) * a.table_stride;
             const int items = 2 * w.n;
@@ -286,125 +288,179 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                 const int p = (w.t0 + tile_of(i, v)) * TP + lw * RW + lane;
                 return lane < RW && p < w.used ? row[p >> a.kv.page_shift] : -1;
             };
+            const int first = item;
             int page = page_of(0);
-            for (int i = 0; i < items; ++i, ++item) {
+            auto wait_empty = [&](int it) {
+                return it < S || __all_sync(WSW_FULL_MASK, mbar_wait(&ct.empty[it % S], ((it / S) - 1) & 1u));
+            };
+            // a tile's rows to where they lie: lane's row, for all lanes
+            struct Rows {
+                const unsigned char *base;  // of K or V, the head's
+                int64_t at, dat;
+                uint32_t valid;
                 bool v;
-                const int p = (w.t0 + tile_of(i, v)) * TP + lw * RW + lane;
+            };
+            auto rows_of = [&](int i) {
+                Rows x;
+                const int p = (w.t0 + tile_of(i, x.v)) * TP + lw * RW + lane;
                 const bool in = lane < RW && p < w.used;
                 const bool there = in && static_cast<unsigned>(page) < static_cast<unsigned>(a.kv.num_pages);
                 if (in && !there && a.err) atomicOr(a.err, 1);
-                const uint32_t valid = __ballot_sync(WSW_FULL_MASK, there);
-                const int64_t at = there ? page * a.kv.page_stride + (p & page_mask) * a.kv.pos_stride : 0;
-                const int64_t dat = C::q8 && there ? page * a.kv.d_page_stride + (p & page_mask) * a.kv.d_pos_stride : 0;
+                x.valid = __ballot_sync(WSW_FULL_MASK, there);
+                x.at = there ? page * a.kv.page_stride + (p & page_mask) * a.kv.pos_stride : 0;
+                x.dat = C::q8 && there ? page * a.kv.d_page_stride + (p & page_mask) * a.kv.d_pos_stride : 0;
+                x.base = (x.v ? a.kv.v : a.kv.k) + w.head * a.kv.head_stride;
                 if (i + 1 < items) page = page_of(i + 1);
-                const unsigned char *base = (v ? a.kv.v : a.kv.k) + w.head * a.kv.head_stride;
-                const int st = item % S;
-                const uint32_t dst = saddr(ring + st * C::stage);
-                uint4 code[C::q8 ? kSteps : 1];
-                uint16_t scale[C::q8 ? kSteps : 1];
-                if constexpr (C::q8) {  // on their way before the stage is free
-                    const unsigned char *dbase = (v ? a.kv.vd : a.kv.kd) + w.head * a.kv.d_head_stride;
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        const int r = k * kRows + rr;
-                        const int64_t o = __shfl_sync(WSW_FULL_MASK, at, r), d = __shfl_sync(WSW_FULL_MASK, dat, r);
-                        const bool there_r = (valid >> r) & 1;
-                        code[k] = there_r ? __ldg(reinterpret_cast<const uint4 *>(base + o) + c) : make_uint4(0u, 0u, 0u, 0u);
-                        scale[k] = there_r ? __ldg(reinterpret_cast<const uint16_t *>(dbase + d) + (c >> 1)) : 0;
-                    }
-                }
-                if (item >= S) {
-                    const uint32_t parity = ((item / S) - 1) & 1u;
-                    if (signalled < item && !__all_sync(WSW_FULL_MASK, mbar_test(&ct.empty[st], parity))) {
-                        // nothing to copy: wait for what is on its way
-                        cp_wait<0>();
-                        signal(item);
-                    }
-                    if (!__all_sync(WSW_FULL_MASK, mbar_wait(&ct.empty[st], parity))) {
-                        ok = false;
-                        break;
-                    }
-                }
-                if (!v) {
+                if (!x.v) {
                     if (lane == 0) {
-                        if constexpr (RW == 32) ct.seen[k_tiles % kSeen][lw] = valid;
-                        else reinterpret_cast<uint16_t *>(ct.seen[k_tiles % kSeen])[lw] = static_cast<uint16_t>(valid);
+                        if constexpr (RW == 32) ct.seen[k_tiles % kSeen][lw] = x.valid;
+                        else reinterpret_cast<uint16_t *>(ct.seen[k_tiles % kSeen])[lw] = static_cast<uint16_t>(x.valid);
                     }
                     ++k_tiles;
                 }
-                if constexpr (C::q8) {
+                return x;
+            };
+            if constexpr (!C::q8) {
+                for (int i = 0; i < items; ++i, ++item) {
+                    const int st = item % S;
+                    if (!wait_empty(item)) {
+                        ok = false;
+                        break;
+                    }
+                    const Rows x = rows_of(i);
+                    const uint32_t dst = saddr(ring + st * C::stage);
+                    if (x.valid == (RW == 32 ? 0xffffffffu : 0xffffu) && a.kv.page_shift >= 4) {
+                        // sixteen rows of a page at a time, pos_stride apart: few instructions, since this warp issues
+                        // in between the softmax's (shuffles for each row: the MMAs waited 600 cycles a tile)
+                        const int64_t pitch = kRows * a.kv.pos_stride;
 #pragma unroll
+                        for (int g = 0; g < RW / 16; ++g) {
+                            const unsigned char *src = x.base + __shfl_sync(WSW_FULL_MASK, x.at, 16 * g) + rr * a.kv.pos_stride + c * 16;
+#pragma unroll
+                            for (int k = 0; k < 16 / kRows; ++k) {
+                                cp16_all(dst + to_row[k % kTurn] + (16 * g + k / kTurn * 8) * 128, src);
+                                src += pitch;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            const int r = k * kRows + rr;
+                            const int64_t o = __shfl_sync(WSW_FULL_MASK, x.at, r);
+                            cp16(dst + swizzled(lw * RW + r, c, TP), x.base + o + c * 16, (x.valid >> r) & 1);
+                        }
+                    }
+                    // this thread arrives once its copies have landed (the MMAs' warp has the proxy fence)
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(saddr(&ct.full[st])) : "memory");
+                }
+            } else {
+                // codes and scales of the warp's own rows on their way, raw_stages - 1 tiles ahead
+                constexpr int kScale = D / 16;  // bytes of a row's scales
+                auto raw_of = [&](int it) { return raw_ring + it % C::raw_stages * C::raw; };
+                auto issue = [&](int i) {
+                    if (i < items) {
+                        const Rows x = rows_of(i);
+                        unsigned char *to = raw_of(first + i);
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            const int r = k * kRows + rr;
+                            const int64_t o = __shfl_sync(WSW_FULL_MASK, x.at, r);
+                            cp16(saddr(to) + (lw * RW + r) * D + c * 16, x.base + o + c * 16, (x.valid >> r) & 1);
+                        }
+                        if (lane < RW)
+                            paged::cp_small<kScale>(saddr(to) + TP * D + (lw * RW + lane) * kScale,
+                                                    (x.v ? a.kv.vd : a.kv.kd) + w.head * a.kv.d_head_stride + x.dat,
+                                                    (x.valid >> lane) & 1);
+                    }
+                    paged::cp_commit();  // a group for each turn, empty past the end
+                };
+#pragma unroll
+                for (int i = 0; i < C::raw_stages - 1; ++i) issue(i);
+                for (int i = 0; i < items; ++i, ++item) {
+                    __syncwarp();  // every lane has read the place that the next copies reuse
+                    issue(i + C::raw_stages - 1);
+                    paged::cp_wait<C::raw_stages - 1>();
+                    __syncwarp();  // the rows that every lane copied
+                    const int st = item % S;
+                    if (!wait_empty(item)) {
+                        ok = false;
+                        break;
+                    }
+                    const unsigned char *from = raw_of(item);
+                    unsigned char *to = ring + st * C::stage;
+#pragma unroll 2
                     for (int k = 0; k < kSteps; ++k) {
-                        const int r = k * kRows + rr;
-                        const __half2 d2 = __half2half2(__ushort_as_half(scale[k]));
-                        const uint32_t u[4] = {code[k].x ^ 0x80808080u, code[k].y ^ 0x80808080u, code[k].z ^ 0x80808080u,
-                                               code[k].w ^ 0x80808080u};
-                        uint32_t h[8];
+                        const int r = lw * RW + k * kRows + rr;
+                        const uint4 code = *reinterpret_cast<const uint4 *>(from + r * D + c * 16);
+                        const __half2 d2 = __half2half2(*reinterpret_cast<const __half *>(from + TP * D + r * kScale + (c >> 1) * 2));
+                        const uint32_t u[4] = {code.x ^ 0x80808080u, code.y ^ 0x80808080u, code.z ^ 0x80808080u, code.w ^ 0x80808080u};
+                        uint32_t h[8];  // rows that are not there are zeros: codes and scales
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             h[2 * x] = paged::dequant2(u[x], 0x4140, d2);
                             h[2 * x + 1] = paged::dequant2(u[x], 0x4342, d2);
                         }
-                        if (!((valid >> r) & 1)) {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) h[x] = 0u;
-                        }
-                        unsigned char *to = ring + st * C::stage;
-                        *reinterpret_cast<uint4 *>(to + swizzled(lw * RW + r, 2 * c, TP)) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4 *>(to + swizzled(lw * RW + r, 2 * c + 1, TP)) = make_uint4(h[4], h[5], h[6], h[7]);
+                        *reinterpret_cast<uint4 *>(to + swizzled(r, 2 * c, TP)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4 *>(to + swizzled(r, 2 * c + 1, TP)) = make_uint4(h[4], h[5], h[6], h[7]);
                     }
-                    signal(item + 1);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        const int r = k * kRows + rr;
-                        const int64_t o = __shfl_sync(WSW_FULL_MASK, at, r);
-                        cp16(dst + swizzled(lw * RW + r, c, TP), base + o + c * 16, (valid >> r) & 1);
-                    }
-                    cp_commit();
-                    if (item >= 2 && signalled < item - 1) {
-                        cp_wait<2>();
-                        signal(item - 1);
-                    }
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ct.full[st]);
                 }
             }
         }
-        cp_wait<0>();
-        signal(item);
+        cp_wait_all();
         __syncwarp();
     } else if (warp >= kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-        if (warp == kMmaWarp && lane == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma_regs));
+        if (warp == kMmaWarp) {
+            // The whole warp walks, so that addresses and descriptors are uniform values; one elected lane issues.
+            // (With one lane walking alone an MMA was issued every 115 cycles.)
             Walk<C> w(a, pos, end, ct.at[0], ct.at[1]);
             constexpr uint32_t id_s = instr_desc(128, TP, C::bf16);
             constexpr uint32_t id_pv = instr_desc(128, D, C::bf16) | (1u << 16);  // B (V) MN-major
             int item = 0, piece = 0;
             uint32_t p_phase[2] = {0, 0};
-            auto landed = [&](int i) { return mbar_wait(&ct.full[i % S], (i / S) & 1u); };
+            auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(WSW_FULL_MASK, mbar_wait(b, parity)) != 0; };
+            auto landed = [&](int i) {
+                const bool yes = wait(&ct.full[i % S], (i / S) & 1u);
+                fence_async_shared();  // what the copies wrote, for the tensor cores
+                return yes;
+            };
+            auto commit = [&](uint64_t *b) {
+                if (elect_one()) mma_commit(b);
+            };
             auto scores = [&](int slot, int k) {
                 const uint32_t kt = saddr(ring + (k % S) * C::stage), qt = saddr(q_sm + (RT == 2 ? slot : 0) * QP * C::q_part);
+                const uint64_t dq = sw128_desc(qt), dk = sw128_desc(kt);
+                const uint32_t d = tmem + slot * C::s_cols;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int part = 0; part < QP; ++part)
+                    for (int part = 0; part < QP; ++part)
 #pragma unroll
-                    for (int b = 0; b < D / 64; ++b) {
-                        const uint64_t dq = sw128_desc(qt + part * C::q_part + b * 128 * 128), dk = sw128_desc(kt + b * TP * 128);
+                        for (int b = 0; b < D / 64; ++b)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16(tmem + slot * C::s_cols, dq + 2 * kk, dk + 2 * kk, id_s, (part | b | kk) != 0);
-                    }
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_bf16(d, dq + ((part * C::q_part + b * 128 * 128) >> 4) + 2 * kk,
+                                         dk + ((b * TP * 128) >> 4) + 2 * kk, id_s, (part | b | kk) != 0);
+                }
+                __syncwarp();
             };
             auto values = [&](int slot, int v, bool more) {
                 const uint64_t dv = sw128_mn_desc(saddr(ring + (v % S) * C::stage), TP * 128);
+                const uint32_t d = tmem + C::o_col + slot * D, p = tmem + slot * C::s_cols;
+                if (elect_one()) {
 #pragma unroll
-                for (int part = 0; part < PP; ++part)
+                    for (int part = 0; part < PP; ++part)
 #pragma unroll
-                    for (int kk = 0; kk < TP / 16; ++kk)
-                        mma_ts(tmem + C::o_col + slot * D, tmem + slot * C::s_cols + part * (TP / 2) + 8 * kk, dv + 128 * kk,
-                               id_pv, more || (part | kk) != 0);
+                        for (int kk = 0; kk < TP / 16; ++kk)
+                            mma_ts(d, p + part * (TP / 2) + 8 * kk, dv + 128 * kk, id_pv, more || (part | kk) != 0);
+                }
+                __syncwarp();
             };
             while (ok && w.next()) {
-                ok = mbar_wait(&ct.q_full, piece & 1u);
+                ok = wait(&ct.q_full, piece & 1u);
                 ++piece;
                 if (!ok) break;
                 const int lead = min(C::ahead, w.n);
@@ -413,9 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                     for (int s = 0; s < RT; ++s) {
                         const int slot = RT == 2 ? s : j;
                         scores(slot, item);
-                        mma_commit(&ct.s_full[slot]);
+                        commit(&ct.s_full[slot]);
                     }
-                    mma_commit(&ct.empty[item % S]);
+                    commit(&ct.empty[item % S]);
                     ++item;
                 }
                 for (int j = 0; j < w.n && ok; ++j) {
@@ -423,26 +479,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                     const int v = item++, k = more_k ? item++ : 0;
                     for (int s = 0; s < RT; ++s) {
                         const int slot = RT == 2 ? s : j & 1;
-                        if (!(ok = mbar_wait(&ct.p_full[slot], p_phase[slot]))) break;
+                        if (!(ok = wait(&ct.p_full[slot], p_phase[slot]))) break;
                         p_phase[slot] ^= 1u;
                         if (s == 0 && !(ok = landed(v))) break;
                         tc_fence_after();
                         values(slot, v, RT == 2 ? j > 0 : j > 1);
-                        if (s == RT - 1) mma_commit(&ct.empty[v % S]);
+                        if (s == RT - 1) commit(&ct.empty[v % S]);
                         if (!more_k) continue;
                         if (s == 0 && !(ok = landed(k))) break;
                         scores(slot, k);
-                        mma_commit(&ct.s_full[slot]);
-                        if (s == RT - 1) mma_commit(&ct.empty[k % S]);
+                        commit(&ct.s_full[slot]);
+                        if (s == RT - 1) commit(&ct.empty[k % S]);
                     }
                 }
-                if (ok) mma_commit(&ct.o_done);
+                if (ok) commit(&ct.o_done);
             }
         }
-        __syncwarp();
     } else {
         // ---- softmax: slot and row of this thread
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
         Walk<C> w(a, pos, end, ct.at[0], ct.at[1]);
         const int slot = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
@@ -536,70 +591,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                 const bool all = TP == 128 ? (seen[0] & seen[1] & seen[2] & seen[3]) == 0xffffffffu
                                            : (seen[0] & seen[1]) == 0xffffffffu;
                 const bool plain = all && a.cap_in == 0.f && !a.slopes;
-                const int p0 = (w.t0 + j) * TP;
-                // 32 scores of a chunk, in log2 units where the tile is not plain
-                auto finish = [&](uint32_t (&v)[32], int chunk) {
-                    if (plain) return;
-                    const uint32_t mask = seen[chunk];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * unit);
-                    if (a.cap_in != 0.f) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(a.cap_out * tanhf(__uint_as_float(v[i])));
-                    }
-                    if (a.slopes) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = __float_as_uint(fmaf(-slope, static_cast<float>(last - (p0 + 32 * chunk + i)),
-                                                        __uint_as_float(v[i])));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = (mask >> i) & 1 ? v[i] : 0xff800000u;
-                };
-                auto top = [&](const uint32_t (&v)[32], float mx) {
+                uint64_t l2a = 0ull, l2b = 0ull;  // a tile's sum by itself: l gets one rounding a tile
+                auto top = [](const uint32_t (&v)[32], float mx) {
                     float q4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) q4[i & 3] = fmaxf(q4[i & 3], __uint_as_float(v[i]));
+                    for (int i = 0; i < 32; i += 2)
+                        asm("max.f32 %0, %0, %1, %2;" : "+f"(q4[(i >> 1) & 3]) : "f"(__uint_as_float(v[i])), "f"(__uint_as_float(v[i + 1])));
                     return fmaxf(fmaxf(q4[0], q4[1]), fmaxf(q4[2], q4[3]));
                 };
-                uint32_t va[32], vb[32];
-                float mx = -INFINITY;
-                if constexpr (TP == 128) {  // the second half's maximum; it is read again for the weights
-                    tmem_ld32(s_base + 64, va);
-                    tmem_ld32(s_base + 96, vb);
-                    tmem_wait_ld();
-                    finish(va, 2);
-                    finish(vb, 3);
-                    mx = top(vb, top(va, mx));
-                }
-                tmem_ld32(s_base, va);
-                tmem_ld32(s_base + 32, vb);
-                tmem_wait_ld();
-                finish(va, 0);
-                finish(vb, 1);
-                mx = top(vb, top(va, mx));
-                const float mul = plain ? unit : 1.f;
-                const float mt = mx * mul;
-                const bool raise = mt > m + kLazy;  // m = -inf: by anything visible
-                if (j >= step && __any_sync(WSW_FULL_MASK, raise)) {
-                    // the S that was waited for was issued behind the last P V: O is complete
-                    const float al = raise ? ex2(m - mt) : 1.f;
-                    l *= al;
+                // the maximum in use, with the tile's mt in mind
+                auto raise_to = [&](float mt) {
+                    const bool raise = mt > m + kLazy;  // m = -inf: by anything visible
+                    if (j >= step && __any_sync(WSW_FULL_MASK, raise)) {
+                        // the S that was waited for was issued behind the last P V: O is complete
+                        const float al = raise ? ex2(m - mt) : 1.f;
+                        l *= al;
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(o_base + 32 * c, o);
-                        tmem_wait_ld();
+                        for (int c = 0; c < D / 16; ++c) {
+                            float o[16];
+                            tmem_ld16(o_base + 16 * c, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                        tmem_st32(o_base + 32 * c, o);
+                            for (int i = 0; i < 16; ++i) o[i] *= al;
+                            tmem_st16(o_base + 16 * c, reinterpret_cast<const uint32_t (&)[16]>(o));
+                        }
                     }
-                }
-                if (raise) m = mt;
-                const float ref = m == -INFINITY ? 0.f : m - C::shift;  // nothing seen yet: all weights 0
-                const uint64_t mul2 = f2_pack(mul, mul), ref2 = f2_pack(-ref, -ref);
-                uint64_t l2a = 0ull, l2b = 0ull;  // a tile's sum by itself: l gets one rounding a tile
-                auto weights = [&](const uint32_t (&v)[32], uint32_t (&part)[PP][16]) {
+                    if (raise) m = mt;
+                };
+                // weights 2^(x mul - ref) of a chunk of 32 scores, into tensor memory
+                auto put = [&](const uint32_t (&v)[32], int chunk, float mul, float ref) {
+                    const uint64_t mul2 = f2_pack(mul, mul), ref2 = f2_pack(-ref, -ref);
+                    uint32_t part[PP][16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         uint64_t t = f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
@@ -613,23 +634,82 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                         else if constexpr (PP == 2) split<CT>(w0, w1, part[0][i], part[1][i]);
                         else split3(w0, w1, part[0][i], part[1][i], part[2][i]);
                     }
-                };
-                auto put = [&](const uint32_t (&v)[32], int chunk) {
-                    uint32_t part[PP][16];
-                    weights(v, part);
 #pragma unroll
                     for (int k = 0; k < PP; ++k) tmem_st16(s_base + k * (TP / 2) + 16 * chunk, part[k]);
                 };
-                put(va, 0);
-                put(vb, 1);
-                if constexpr (TP == 128) {
-                    tmem_ld32(s_base + 64, va);
-                    tmem_ld32(s_base + 96, vb);
+                auto ref_of = [&] { return m == -INFINITY ? 0.f : m - C::shift; };  // nothing seen yet: all weights 0
+                if (plain) {
+                    // three chunks of scores stay in registers, the fourth is read twice
+                    constexpr int kStay = TP == 128 ? 3 : 2;
+                    uint32_t v[kStay][32];
+                    float mx = -INFINITY;
+                    if constexpr (TP == 128) {
+                        tmem_ld32(s_base + 96, v[0]);
+                        tmem_wait_ld();
+                        mx = top(v[0], mx);
+                    }
+#pragma unroll
+                    for (int c = 0; c < kStay; ++c) tmem_ld32(s_base + 32 * c, v[c]);
                     tmem_wait_ld();
-                    finish(va, 2);
-                    finish(vb, 3);
-                    put(va, 2);
-                    put(vb, 3);
+#pragma unroll
+                    for (int c = 0; c < kStay; ++c) mx = top(v[c], mx);
+                    raise_to(mx * unit);
+                    const float ref = ref_of();
+#pragma unroll
+                    for (int c = 0; c < kStay; ++c) put(v[c], c, unit, ref);
+                    if constexpr (TP == 128) {
+                        tmem_ld32(s_base + 96, v[0]);
+                        tmem_wait_ld();
+                        put(v[0], 3, unit, ref);
+                    }
+                } else {
+                    const int p0 = (w.t0 + j) * TP;
+                    // 32 scores of a chunk in log2 units
+                    auto read = [&](uint32_t (&v)[32], int chunk) {
+                        tmem_ld32(s_base + 32 * chunk, v);
+                        tmem_wait_ld();
+                        const uint32_t mask = seen[chunk];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * unit);
+                        if (a.cap_in != 0.f) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(a.cap_out * tanhf(__uint_as_float(v[i])));
+                        }
+                        if (a.slopes) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = __float_as_uint(fmaf(-slope, static_cast<float>(last - (p0 + 32 * chunk + i)),
+                                                            __uint_as_float(v[i])));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = (mask >> i) & 1 ? v[i] : 0xff800000u;
+                    };
+                    // the second half's maximum comes first (it is read again for the weights), since the first half's
+                    // weights take the place of scores that have been read; several parts of the weights take all
+                    // scores' places, which two chunks hold
+                    float mx = -INFINITY;
+                    uint32_t va[32], vb[32];
+                    if constexpr (TP == 128) {
+#pragma unroll 1
+                        for (int c = 2; c < 4; ++c) {
+                            read(va, c);
+                            mx = top(va, mx);
+                        }
+                    }
+                    read(va, 0);
+                    read(vb, 1);
+                    mx = top(vb, top(va, mx));
+                    raise_to(mx);
+                    const float ref = ref_of();
+                    put(va, 0, 1.f, ref);
+                    put(vb, 1, 1.f, ref);
+                    if constexpr (TP == 128) {
+#pragma unroll 1
+                        for (int c = 2; c < 4; ++c) {
+                            read(va, c);
+                            put(va, c, 1.f, ref);
+                        }
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
