@@ -794,7 +794,7 @@ int wsw_beam_select(const void *logits, int32_t dtype, int64_t requests, int64_t
  *               and sets bit 2 of *err_flag; bits 0 and 1 as wsw_attn_paged_decode's.
  *   head_dim    64 or 128.
  *   ws          device workspace of ws_bytes >= wsw_attn_paged_prefix_workspace_bytes(...) bytes,
- *               16-byte aligned, zero-filled before its first use and then reused, as
+ *               256-byte aligned, zero-filled before its first use and then reused, as
  *               wsw_attn_paged_decode's.
  *   1 <= groups <= 16384;  requests * q_heads <= 2^30;
  *   kv heads * (requests * group / 128 + groups) * (max_pages * page_size / 64 + 2) < 2^31 - 65536.

@@ -145,6 +145,7 @@ def test_attn_prefix_rejects_on_host(lib):
                    {"requests": 60000, "q_heads": 32768}, {"width": 1 << 27, "stride": 1 << 27},
                    {"groups": 16384, "width": 1 << 20, "stride": 1 << 20}):
         assert _attend(lib, **change) == UNSUPPORTED, change
+    assert _attend(lib, ws=P(4096 + 128)) == MISALIGNED
     need = lib.wsw_attn_paged_prefix_workspace_bytes
     assert need(4, 0, 8, 2, 64) == 0 and need(4, 2, 8, 2, 256) == 0 and need(4, 16385, 8, 2, 64) == 0
     assert _attend(lib, ws_bytes=need(4, 2, 8, 2, 64) - 1) == WORKSPACE

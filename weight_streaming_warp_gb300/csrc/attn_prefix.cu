@@ -20,7 +20,7 @@ WSW_PREFIX_DECLARE(WSW_Q8_0)
 
 namespace {
 
-constexpr int kMaxGroups = 16384;  // two words of shared memory each
+constexpr int kMaxGroups = 16384;  // three words of shared memory each
 constexpr int kPlanThreads = 1024;
 
 // Parts of q (and whether P is one part: 128 positions a tile) by types.
@@ -36,6 +36,7 @@ int row_tiles(int64_t requests, int64_t group, int64_t groups, int parts) {
 struct PlanArgs {
     const int32_t *cu, *prefix, *lens;
     int *begin, *off, *used, *rep, *run;  // as Plan
+    int2 *start;
     int *first, *group_of;                // [requests] where the rest begins, whose prefix it shares
     int32_t *err;
     int requests, groups, max_len, heads, group, unit_rows, tile;
@@ -44,7 +45,7 @@ struct PlanArgs {
 __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const PlanArgs a) {
     extern __shared__ int sm[];
     __shared__ int scan_sm[33];
-    int *begin = sm, *used = sm + a.groups + 1;
+    int *begin = sm, *used = begin + a.groups + 1, *off = used + a.groups;
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
     pdl_wait();
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const Plan
     int total;
     int at = block_scan(sum, 0x7fffffff, scan_sm, &total);
     for (int g = g0; g < g1; ++g) {
-        a.off[g] = at;
+        a.off[g] = off[g] = at;
         a.begin[g] = begin[g];
         at += tiles(g, used[g]);
     }
@@ -104,7 +105,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const Plan
         *a.run = max((total + kCtas - 1) / kCtas, 1);
     }
     if (err && a.err) atomicOr(a.err, err);
-    // ---- each request's part (used and begin are complete: the scan has barriers)
+    __syncthreads();
+    // ---- where each CTA begins: the last group whose part begins there or before
+    const int run = max((total + kCtas - 1) / kCtas, 1);
+    for (int c = tid; c < kCtas; c += nt) {
+        const int64_t pos = static_cast<int64_t>(c) * run;
+        int lo = 0, n = a.groups;
+        while (n > 1) {
+            const int half = n >> 1;
+            if (off[lo + half] <= pos) lo += half;
+            n -= half;
+        }
+        a.start[c] = pos < total ? make_int2(lo, static_cast<int>(pos) - off[lo]) : make_int2(-1, 0);
+    }
+    // ---- each request's part
     for (int r = tid; r < a.requests; r += nt) {
         int lo = 0, n = a.groups;  // the last group that begins at r or before
         while (n > 1) {
@@ -133,7 +147,7 @@ struct JoinArgs {
 
 template <int D>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const JoinArgs a) {
-    constexpr int N = D / 32, kRec = D + 4;  // values of a lane
+    constexpr int N = D / 32, kRec = D + kHead;  // values of a lane
     using V = std::conditional_t<N == 4, float4, float2>;
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -175,7 +189,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const JoinArgs a) {
         for (int k = 0; k < n; ++k) {
             const float *p = piece(k);
             const float2 pml = *reinterpret_cast<const float2 *>(p);
-            const V v = *reinterpret_cast<const V *>(p + 4 + lane * N);
+            const V v = *reinterpret_cast<const V *>(p + kHead + lane * N);
             const float w = paged::weight(pml.x, mx);
             const float *x = reinterpret_cast<const float *>(&v);
 #pragma unroll
@@ -207,11 +221,11 @@ struct Room {
 };
 Room room(int64_t requests, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
     Room w;
-    const size_t rows = static_cast<size_t>(requests) * q_heads, rec = static_cast<size_t>(head_dim + 4) * 4;
+    const size_t rows = static_cast<size_t>(requests) * q_heads, rec = static_cast<size_t>(head_dim + kHead) * 4;
     // two row tiles by the rule for one part of q: the most that any types need
     const int rt = row_tiles(requests, q_heads / kv_heads, groups, 1);
     w.plan = align256(wsw_attn_paged_decode_workspace_bytes(requests, q_heads, kv_heads, head_dim));
-    w.rec = w.plan + align256((4 * (static_cast<size_t>(groups) + 1) + 1 + 2 * static_cast<size_t>(requests)) * 4);
+    w.rec = w.plan + align256((2 * kCtas + 4 * (static_cast<size_t>(groups) + 1) + 1 + 2 * static_cast<size_t>(requests)) * 4);
     w.whole = w.rec + static_cast<size_t>(kCtas) * 2 * rt * 128 * rec;
     w.rest = w.whole + align256(rows * rec);
     w.ml = w.rest + align256(rows * head_dim * 4);
@@ -254,7 +268,7 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     if (requests == 0) return WSW_OK;
     if (!cu_groups || !prefix_len || !ws) return WSW_ERR_INVALID_ARG;
     if (((reinterpret_cast<uintptr_t>(cu_groups) | reinterpret_cast<uintptr_t>(prefix_len)) & 3) ||
-        (reinterpret_cast<uintptr_t>(ws) & 15))
+        (reinterpret_cast<uintptr_t>(ws) & 255))
         return WSW_ERR_MISALIGNED;
     const int64_t kv_heads = cache->heads, group = rest.group;
     // the longest list: tiles are counted in 32 bits
@@ -271,7 +285,8 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     const int rt = row_tiles(requests, group, groups, q_parts(dtype, cache->dtype));
     PlanArgs p;
     p.cu = cu_groups; p.prefix = prefix_len; p.lens = lens; p.err = err_flag;
-    p.begin = reinterpret_cast<int *>(base + w.plan);
+    p.start = reinterpret_cast<int2 *>(base + w.plan);
+    p.begin = reinterpret_cast<int *>(p.start + kCtas);
     p.off = p.begin + groups + 1;
     p.used = p.off + groups + 1;
     p.rep = p.used + groups + 1;
@@ -280,15 +295,15 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     p.group_of = p.first + requests;
     p.requests = rest.requests; p.groups = static_cast<int>(groups); p.max_len = rest.max_len;
     p.heads = rest.kv.heads; p.group = rest.group; p.unit_rows = 128 * rt; p.tile = tile_of(dtype);
-    const int plan_smem = static_cast<int>((2 * groups + 1) * 4);
-    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(prefix_plan_kernel), (2 * kMaxGroups + 1) * 4);
+    const int plan_smem = static_cast<int>((3 * groups + 1) * 4);
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(prefix_plan_kernel), (3 * kMaxGroups + 1) * 4);
     if (e == cudaSuccess)
         e = launch(prefix_plan_kernel, dim3(1), dim3(requests > 256 || groups > 256 ? kPlanThreads : 256), plan_smem, s, o.pdl, p);
     if (e != cudaSuccess) return WSW_ERR_CUDA;
 
     Args a;
     a.q = q; a.slopes = slopes; a.table = table; a.lens = lens; a.err = err_flag;
-    a.plan = Plan{p.begin, p.off, p.used, p.rep, p.run};
+    a.plan = Plan{p.begin, p.off, p.used, p.rep, p.run, p.start};
     a.rec = reinterpret_cast<float *>(base + w.rec);
     a.whole = reinterpret_cast<float *>(base + w.whole);
     a.kv = rest.kv;

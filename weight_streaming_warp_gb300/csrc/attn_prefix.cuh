@@ -51,8 +51,9 @@ constexpr int kLoaders = 4;    // warps
 constexpr int kMmaWarp = 8 + kLoaders;
 constexpr int kThreads = 512;  // whole warpgroups: three warps beside the MMAs' are idle
 constexpr int kSeen = 16;      // tiles whose visible positions are kept
-constexpr int kTileBytes = 224 * 1024;
+constexpr int kControl = 2048, kTileBytes = 227 * 1024 - kControl - 1024;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kHead = 8;       // floats before a record's O, which keeps 32-byte alignment
 
 // What the plan kernel leaves: [groups + 1] each but `run`.
 struct Plan {
@@ -61,6 +62,7 @@ struct Plan {
     const int *used;   // its prefix's positions
     const int *rep;    // the request whose table row holds its pages
     const int *run;    // [1] tiles of a CTA
+    const int2 *start; // [kCtas] group and place in its part where a CTA's run begins; group -1: nothing
 };
 
 struct Args {
@@ -69,8 +71,8 @@ struct Args {
     const int32_t *table, *lens;
     int32_t *err;
     Plan plan;
-    float *rec;    // [kCtas][2][rows of a unit][D + 4]: (m - shift, l, -, -, O) of pieces
-    float *whole;  // [requests * q_heads][D + 4]: of units that one CTA has whole
+    float *rec;    // [kCtas][2][rows of a unit][D + kHead]: (m - shift, l, - ..., O) of pieces
+    float *whole;  // [requests * q_heads][D + kHead]: of units that one CTA has whole
     KvView kv;
     int64_t table_stride;
     float scale2;  // |scale| log2 e
@@ -98,12 +100,12 @@ struct Cfg {
     static constexpr int s_cols = PP == 3 ? 96 : TP;       // of a slot: scores, then P's parts
     static constexpr uint32_t o_col = 2 * s_cols;
     static constexpr float shift = bf16 ? -kLazy : 7.f;    // log2 of the weights' scale
-    static constexpr int rec = D + 4;
+    static constexpr int rec = D + kHead;
     // registers of a thread, by role; launched with 128 each
     static constexpr int soft_regs = q8 ? 176 : 184, load_regs = q8 ? 96 : 80, mma_regs = 64;
     static_assert(2 * soft_regs + load_regs + mma_regs == 4 * 65536 / kThreads, "what the block was launched with");
     static_assert(2 * s_cols + 2 * D <= 512 && stages >= 3 && kSeen >= stages + 4 + (q8 ? raw_stages : 0), "room");
-    static constexpr int smem = q_bytes + stages * stage + raw_stages * raw + 2048 + 1024;
+    static constexpr int smem = q_bytes + stages * stage + raw_stages * raw + kControl + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
 };
 
@@ -112,11 +114,10 @@ struct Control {
     uint64_t s_full[2], p_full[2];  // of a slot
     uint64_t q_full, o_done;
     uint32_t seen[kSeen][4];
-    float2 ml[128];
+    float unit[256];    // of the rows' scores
     uint32_t tmem;
-    int at[2];  // the first tile's group and its place there
 };
-static_assert(sizeof(Control) <= 2048 && kTileBytes + 2048 + 1024 <= 227 * 1024, "control");
+static_assert(sizeof(Control) <= kControl && kTileBytes + kControl + 1024 <= 227 * 1024, "control");
 
 // The pieces of a CTA's run, in order; every role walks them.
 template <typename C>
@@ -162,6 +163,11 @@ struct Walk {
 
 __device__ __forceinline__ void cp16_all(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 32 bytes at a 32-byte boundary: a whole sector
+__device__ __forceinline__ void st32(float *p, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // one lane of the (converged) warp
@@ -231,23 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
     }
     pdl_launch_dependents();
     pdl_wait();
+    const int2 start = a.plan.start[blockIdx.x];
     const int total = a.plan.off[a.groups], run = *a.plan.run;
-    const int pos = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * run, static_cast<int64_t>(total)));
-    const int end = min(pos + run, total);
-    if (warp == 0 && pos < end) {  // the last group that begins at pos or before
-        int lo = 0, n = a.groups;
-        while (n > 1) {
-            const int step = (n + 31) / 32;
-            const bool before = lane * step < n && a.plan.off[lo + lane * step] <= pos;
-            const int at = (__popc(__ballot_sync(WSW_FULL_MASK, before)) - 1) * step;
-            lo += at;
-            n = min(step, n - at);
-        }
-        if (lane == 0) {
-            ct.at[0] = lo;
-            ct.at[1] = pos - a.plan.off[lo];
-        }
-    }
+    const int pos = start.x < 0 ? total : static_cast<int>(blockIdx.x) * run;
+    const int end = start.x < 0 ? total : min(pos + run, total);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -256,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
 
     if (warp >= 8 && warp < kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::load_regs));
-        Walk<C> w(a, pos, end, ct.at[0], ct.at[1]);
+        Walk<C> w(a, pos, end, start.x, start.y);
         // ---- K and V tiles: K_0 .. K_(ahead - 1), then V_j, K_(j + ahead), ...
         const int lw = warp - 8;
         constexpr int RW = TP / kLoaders;                // rows of a warp
@@ -416,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
         if (warp == kMmaWarp) {
             // The whole warp walks, so that addresses and descriptors are uniform values; one elected lane issues.
             // (With one lane walking alone an MMA was issued every 115 cycles.)
-            Walk<C> w(a, pos, end, ct.at[0], ct.at[1]);
+            Walk<C> w(a, pos, end, start.x, start.y);
             constexpr uint32_t id_s = instr_desc(128, TP, C::bf16);
             constexpr uint32_t id_pv = instr_desc(128, D, C::bf16) | (1u << 16);  // B (V) MN-major
             int item = 0, piece = 0;
@@ -498,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
     } else {
         // ---- softmax: slot and row of this thread
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
-        Walk<C> w(a, pos, end, ct.at[0], ct.at[1]);
+        Walk<C> w(a, pos, end, start.x, start.y);
         const int slot = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t s_base = lane_base + slot * C::s_cols, o_base = lane_base + C::o_col + slot * D;
@@ -509,72 +502,86 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
             const bool real = in_group < w.rows;
             const int req = w.begin + (real ? in_group : 0) / a.group, gq = (real ? in_group : 0) % a.group;
             const int64_t head = static_cast<int64_t>(req) * a.q_heads + w.head * a.group + gq;
-            // ---- q: this thread's row, or its half of the row that both warpgroups have
+            // ---- q.  A warp has 32 rows of its slot, or 16 of those that both slots share: sixteen (D 64: eight) lanes
+            // load a row, eight values each.  (A thread for each row took 4 us with 16-bit rows and 10 with fp32.)
             float unit = a.cap_in != 0.f ? a.cap_in : a.scale2;  // of a score's product sum, over softcap if capped
             {
-                const bool wide = a.dtype == WSW_F32;
-                // eight values of the row, 16 (32) bytes
-                auto load8 = [&](int ch, float (&x)[8]) {
-                    if (wide) {
-                        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + head * D + 8 * ch);
-                        const float4 u = src[0], v = src[1];
-                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-                        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-                    } else {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + head * D + 8 * ch);
-                        const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+                constexpr int kLanes = D / 8, kPer = 32 / kLanes, kRowsOfWarp = RT == 2 ? 32 : 16;
+                const int ch = lane % kLanes, r0 = (warp & 3) * 32 + (RT == 2 ? 0 : slot * 16) + lane / kLanes;
+                const int first_in_group = (w.tile * RT + (RT == 2 ? slot : 0)) * 128;
+                unsigned char *to = q_sm + (RT == 2 ? slot : 0) * QP * C::q_part;
+                constexpr int kTurns = kRowsOfWarp / kPer, kAtOnce = 4;
+#pragma unroll 1
+                for (int t = 0; t < kTurns; t += kAtOnce) {
+                    uint4 raw[kAtOnce][QP == 1 || (C::bf16 && QP == 2) ? 1 : 2];  // fp32 rows are twice as wide
+                    constexpr bool kMayBeWide = QP == 3 || (!C::bf16 && QP == 2);
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        const int in = first_in_group + r0 + (t + u) * kPer;
+                        const int64_t h = static_cast<int64_t>(w.begin + (in < w.rows ? in : 0) / a.group) * a.q_heads +
+                                          w.head * a.group + (in < w.rows ? in : 0) % a.group;
+                        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(a.q) +
+                                                                           (h * D + 8 * ch) * (kMayBeWide ? 4 : 2));
+#pragma unroll
+                        for (int k = 0; k < (kMayBeWide ? 2 : 1); ++k)
+                            raw[u][k] = in < w.rows ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        const int row = r0 + (t + u) * kPer;
+                        float x[8];
+#pragma unroll
+                        for (int k = 0; k < (kMayBeWide ? 2 : 1); ++k) {
+                            const uint32_t y[4] = {raw[u][k].x, raw[u][k].y, raw[u][k].z, raw[u][k].w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if constexpr (kMayBeWide) {
+                                    x[4 * k + i] = __uint_as_float(y[i]);
+                                } else {
+                                    const float2 f = a.dtype == WSW_BF16 ? make_float2(bf16lo(y[i]), bf16hi(y[i]))
+                                                                         : __half22float2(*reinterpret_cast<const __half2 *>(&y[i]));
+                                    x[2 * i] = f.x;
+                                    x[2 * i + 1] = f.y;
+                                }
+                            }
+                        }
+                        float up = a.negative ? -1.f : 1.f;
+                        if constexpr (!C::bf16) {
+                            if (a.dtype != WSW_F16) {
+                                float top = 0.f;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+                                for (int d = kLanes / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(WSW_FULL_MASK, top, d));
+                                const int e = max(static_cast<int>(__float_as_uint(top) >> 23), 15);
+                                up *= __uint_as_float((268u - e) << 23);
+                                if (ch == 0) ct.unit[(RT == 2 ? slot * 128 : 0) + row] = __uint_as_float((e - 14u) << 23);
+                            }
+                        }
+                        uint32_t part[3][4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 f = a.dtype == WSW_BF16 ? make_float2(bf16lo(y[i]), bf16hi(y[i]))
-                                                                 : __half22float2(*reinterpret_cast<const __half2 *>(&y[i]));
-                            x[2 * i] = f.x;
-                            x[2 * i + 1] = f.y;
+                            const float x0 = x[2 * i] * up, x1 = x[2 * i + 1] * up;
+                            if constexpr (QP == 1) part[0][i] = pack2<C::bf16>(x0, x1);
+                            else if constexpr (QP == 2) split<CT>(x0, x1, part[0][i], part[1][i]);
+                            else split3(x0, x1, part[0][i], part[1][i], part[2][i]);
                         }
-                    }
-                    if (!real) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                        for (int k = 0; k < QP; ++k)
+                            *reinterpret_cast<uint4 *>(to + k * C::q_part + swizzled(row, ch, 128)) =
+                                make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
                     }
-                };
-                float up = a.negative ? -1.f : 1.f;
-                if constexpr (!C::bf16) {
-                    if (a.dtype != WSW_F16) {
-                        float top = 0.f;
-#pragma unroll 4
-                        for (int ch = 0; ch < D / 8; ++ch) {
-                            float x[8];
-                            load8(ch, x);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-                        }
-                        const int e = max(static_cast<int>(__float_as_uint(top) >> 23), 15);
-                        up *= __uint_as_float((268u - e) << 23);
-                        unit *= __uint_as_float((e - 14u) << 23);
-                    }
-                }
-                unsigned char *to = q_sm + (RT == 2 ? slot : 0) * QP * C::q_part;
-                const int ch0 = RT == 2 ? 0 : slot * (D / 16), ch1 = RT == 2 ? D / 8 : ch0 + D / 16;
-#pragma unroll 4
-                for (int ch = ch0; ch < ch1; ++ch) {
-                    float x[8];
-                    load8(ch, x);
-                    uint32_t part[3][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = x[2 * i] * up, v = x[2 * i + 1] * up;
-                        if constexpr (QP == 1) part[0][i] = pack2<C::bf16>(u, v);
-                        else if constexpr (QP == 2) split<CT>(u, v, part[0][i], part[1][i]);
-                        else split3(u, v, part[0][i], part[1][i], part[2][i]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < QP; ++k)
-                        *reinterpret_cast<uint4 *>(to + k * C::q_part + swizzled(r, ch, 128)) =
-                            make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
                 }
                 fence_async_shared();
                 tc_fence_before();  // O of the piece before has been read
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ct.q_full);
+                if constexpr (!C::bf16) {
+                    if (a.dtype != WSW_F16) {
+                        if (RT == 1) asm volatile("bar.sync 1, 256;" ::: "memory");
+                        unit *= ct.unit[(RT == 2 ? slot * 128 : 0) + r];
+                    }
+                }
             }
             const float slope = a.slopes && real ? a.slopes[w.head * a.group + gq] * kLog2e : 0.f;
             const int last = real && a.slopes ? min(max(a.lens[req], 0), a.max_len) - 1 : 0;
@@ -724,7 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
             // ---- the piece's (m, l, O)
             ok = ok && mbar_wait(&ct.o_done, piece & 1u);
             ++piece;
-            if (RT == 1 && slot == 1) ct.ml[r] = make_float2(m, l);
+            float2 *ml = reinterpret_cast<float2 *>(q_sm);  // [2][128] of both slots' rows: q has been read
+            if (RT == 1) ml[slot * 128 + r] = make_float2(m, l);
             const bool have = both_agree(ok);
             ok = have;
             tc_fence_after();
@@ -732,48 +740,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
             float *rec = w.whole() ? a.whole + head * C::rec
                                    : a.rec + ((static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 == 0)) * RT +
                                               (RT == 2 ? slot : 0)) * 128 * C::rec + r * C::rec;
-            float f0 = 1.f, f1 = 0.f, mj = m;
-            float *other = reinterpret_cast<float *>(q_sm);  // [32][128] of the second warpgroup's O: q has been read
-            const bool two = RT == 1 && w.n > 1;
-            if (two && slot == 0) {  // both warpgroups have these rows
-                const float2 o = ct.ml[r];
-                mj = fmaxf(m, o.x);
-                f0 = m == -INFINITY ? 0.f : ex2(m - mj);
-                f1 = o.x == -INFINITY ? 0.f : ex2(o.x - mj);
-                l = l * f0 + o.y * f1;
+            // both slots' sums of the same rows: a warp reaches its quarter's rows of either, so each warpgroup
+            // joins half of the columns
+            float f0 = 1.f, f1 = 0.f;
+            if (RT == 1 && have) {
+                const float2 x = ml[r], y = ml[128 + r];
+                m = fmaxf(x.x, y.x);
+                f0 = x.x == -INFINITY ? 0.f : ex2(x.x - m);
+                f1 = y.x == -INFINITY ? 0.f : ex2(y.x - m);
+                l = x.y * f0 + y.y * f1;
             }
-            const bool writes = real && (RT == 2 || slot == 0);
-            if (writes) *reinterpret_cast<float2 *>(rec) = make_float2(mj == -INFINITY ? -INFINITY : mj - C::shift, l);
+            if (real && (RT == 2 || slot == 0)) *reinterpret_cast<float2 *>(rec) = make_float2(m == -INFINITY ? m : m - C::shift, l);
+            constexpr int kCols = RT == 2 ? D : D / 2;
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < kCols / 32; ++c) {
+                const int col = (RT == 2 ? 0 : slot * kCols) + 32 * c;
                 uint32_t o[32];
-                const bool mine = RT == 2 || slot == 0 || two;
-                if (mine && have) {
-                    tmem_ld32(o_base + 32 * c, o);
-                    tmem_wait_ld();
-                }
-                if (two) {
-                    if (slot == 1) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) other[i * 128 + r] = __uint_as_float(o[i]);
-                    }
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
-                    if (slot == 0) {
+                if (have) {
+                    if constexpr (RT == 2) {
+                        tmem_ld32(o_base + col, o);
+                        tmem_wait_ld();
+                    } else {
+                        uint32_t y[32];
+                        tmem_ld32(lane_base + C::o_col + col, o);
+                        if (w.n > 1) tmem_ld32(lane_base + C::o_col + D + col, y);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             // a part without weights holds nothing (0 times what its rows hold may be NaN)
                             const float x = f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
-                            o[i] = __float_as_uint(f1 == 0.f ? x : fmaf(other[i * 128 + r], f1, x));
+                            o[i] = __float_as_uint(w.n > 1 && f1 != 0.f ? fmaf(__uint_as_float(y[i]), f1, x) : x);
                         }
                     }
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
                 }
-                if (writes) {
+                if (real) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<uint4 *>(rec + 4 + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    for (int i = 0; i < 32; i += 8) st32(rec + kHead + col + i, o + i);
                 }
             }
+            // both have read the sums and O before the next piece's
+            if (RT == 1) asm volatile("bar.sync 1, 256;" ::: "memory");
         }
     }
     tc_fence_before();
