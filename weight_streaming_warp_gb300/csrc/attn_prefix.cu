@@ -23,12 +23,11 @@ namespace {
 constexpr int kMaxGroups = 16384;  // three words of shared memory each
 constexpr int kPlanThreads = 1024;
 
-// Parts of q (and whether P is one part: 128 positions a tile) by types.
+// Parts of q by types.
 int q_parts(int dtype, int cache) {
     if (dtype == WSW_F32) return cache == WSW_BF16 ? 3 : 2;
     return dtype == WSW_F16 && cache == WSW_BF16 ? 2 : 1;
 }
-int tile_of(int dtype) { return dtype == WSW_F32 ? 64 : 128; }
 int row_tiles(int64_t requests, int64_t group, int64_t groups, int parts) {
     return parts == 1 && requests * group > 128 * groups ? 2 : 1;
 }
@@ -294,7 +293,7 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     p.first = p.run + 1;
     p.group_of = p.first + requests;
     p.requests = rest.requests; p.groups = static_cast<int>(groups); p.max_len = rest.max_len;
-    p.heads = rest.kv.heads; p.group = rest.group; p.unit_rows = 128 * rt; p.tile = tile_of(dtype);
+    p.heads = rest.kv.heads; p.group = rest.group; p.unit_rows = 128 * rt; p.tile = tile_positions(dtype == WSW_F32 ? 2 : 1, cache->dtype, rt);
     const int plan_smem = static_cast<int>((3 * groups + 1) * 4);
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(prefix_plan_kernel), (3 * kMaxGroups + 1) * 4);
     if (e == cudaSuccess)

@@ -47,9 +47,7 @@ using paged::split;
 using paged::split3;
 
 constexpr int kCtas = 152;     // runs of the tile list
-constexpr int kLoaders = 4;    // warps
-constexpr int kMmaWarp = 8 + kLoaders;
-constexpr int kThreads = 512;  // whole warpgroups: three warps beside the MMAs' are idle
+constexpr int kLoaders = 4;    // warps that share a tile
 constexpr int kSeen = 16;      // tiles whose visible positions are kept
 constexpr int kControl = 2048, kTileBytes = 227 * 1024 - kControl - 1024;
 constexpr uint32_t kTmemCols = 512;
@@ -82,30 +80,42 @@ struct Args {
     int dtype, negative;  // of q; scale < 0
 };
 
+// Positions of a tile.  Several parts of P: 64, whose scores a thread keeps while the parts overwrite
+// them; q8_0 under two row tiles: 64, for room.
+constexpr int tile_positions(int p_parts, int cache, int row_tiles) {
+    return p_parts == 1 && !(cache == WSW_Q8_0 && row_tiles == 2) ? 128 : 64;
+}
+
 // Shape of one variant: cache type, head_dim, parts of q and of P, row tiles of a unit.
 template <int CT, int D_, int QP_, int PP_, int RT_>
 struct Cfg {
     static constexpr int D = D_, QP = QP_, PP = PP_, RT = RT_;
     static constexpr bool q8 = CT == WSW_Q8_0, bf16 = CT == WSW_BF16;
-    // several parts of P: 64 positions, whose scores a thread keeps while the parts overwrite them
-    static constexpr int TP = PP == 1 ? 128 : 64;
+    static constexpr int TP = tile_positions(PP, CT, RT);
     static constexpr int stage = TP * D * 2;               // a K or V tile
     static constexpr int q_part = 128 * D * 2;             // of a row tile
     static constexpr int q_bytes = RT * QP * q_part;
-    // q8_0 rows land as codes and scales, a few tiles deep, and become tiles from there
-    static constexpr int raw = q8 ? TP * (D + D / 16) : 0, raw_stages = TP == 128 ? 3 : 4;
-    static constexpr int fit = (kTileBytes - q_bytes - raw_stages * raw) / stage;
+    // q8_0 rows land as codes and scales, a few tiles of K and of V deep, and become tiles from there
+    static constexpr int raw = q8 ? TP * (D + D / 16) : 0, raw_stages = 2 + (TP == 64);
+    static constexpr int fit = (kTileBytes - q_bytes - 2 * raw_stages * raw) / stage;
     static constexpr int stages = fit < 8 ? fit : 8;
     static constexpr int ahead = RT == 1 ? 2 : 1;          // K tiles before their V tiles
     static constexpr int s_cols = PP == 3 ? 96 : TP;       // of a slot: scores, then P's parts
     static constexpr uint32_t o_col = 2 * s_cols;
     static constexpr float shift = bf16 ? -kLazy : 7.f;    // log2 of the weights' scale
     static constexpr int rec = D + kHead;
-    // registers of a thread, by role; launched with 128 each
-    static constexpr int soft_regs = q8 ? 176 : 184, load_regs = q8 ? 96 : 80, mma_regs = 64;
-    static_assert(2 * soft_regs + load_regs + mma_regs == 4 * 65536 / kThreads, "what the block was launched with");
+    // Warpgroups: two of softmax, one or (q8_0, whose codes become values on the way) two of loaders, K's and V's, and
+    // the MMAs' warp with three idle ones.
+    static constexpr int load_groups = q8 ? 2 : 1;
+    static constexpr int mma_warp = 8 + 4 * load_groups, threads = 32 * (mma_warp + 4);
+    // registers of a thread, as launched and by role
+    static constexpr int regs = q8 ? 96 : 128;
+    static constexpr int soft_regs = q8 ? 128 : 184, load_regs = 80, mma_regs = 64;
+    static_assert(2 * soft_regs + load_groups * load_regs + mma_regs == (3 + load_groups) * regs && regs * threads <= 65536,
+                  "what the block was launched with");
+    static constexpr int stay = TP == 64 ? 2 : q8 ? 2 : 3;  // chunks of 32 scores that a thread keeps
     static_assert(2 * s_cols + 2 * D <= 512 && stages >= 3 && kSeen >= stages + 4 + (q8 ? raw_stages : 0), "room");
-    static constexpr int smem = q_bytes + stages * stage + raw_stages * raw + kControl + 1024;
+    static constexpr int smem = q_bytes + stages * stage + 2 * raw_stages * raw + kControl + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
 };
 
@@ -205,7 +215,7 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c, int rows) {
 }
 
 template <int CT, int D, int QP, int PP, int RT>
-__global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefix_kernel(const __grid_constant__ Args a) {
     using namespace tc;
     using C = Cfg<CT, D, QP, PP, RT>;
     constexpr int TP = C::TP, S = C::stages;
@@ -214,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                                                              ~static_cast<uintptr_t>(1023));
     unsigned char *q_sm = tiles, *ring = tiles + C::q_bytes;
     unsigned char *raw_ring = ring + S * C::stage;
-    Control &ct = *reinterpret_cast<Control *>(raw_ring + C::raw_stages * C::raw);
+    Control &ct = *reinterpret_cast<Control *>(raw_ring + 2 * C::raw_stages * C::raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
@@ -230,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
         mbar_init(&ct.o_done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMmaWarp) {
+    if (warp == C::mma_warp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&ct.tmem)),
                      "r"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -247,11 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
     const uint32_t tmem = ct.tmem;
     bool ok = true;
 
-    if (warp >= 8 && warp < kMmaWarp) {
+    if (warp >= 8 && warp < C::mma_warp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::load_regs));
         Walk<C> w(a, pos, end, start.x, start.y);
         // ---- K and V tiles: K_0 .. K_(ahead - 1), then V_j, K_(j + ahead), ...
-        const int lw = warp - 8;
+        const int lw = warp & 3;
         constexpr int RW = TP / kLoaders;                // rows of a warp
         constexpr int kPieces = C::q8 ? D / 16 : D / 8;  // 16-byte pieces of a row
         constexpr int kRows = 32 / kPieces, kSteps = RW / kRows;
@@ -264,10 +274,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
         int item = 0, k_tiles = 0;                       // of the whole run
         while (ok && w.next()) {
             const int32_t *row = a.table + static_cast<int64_t>(w.rep) * a.table_stride;
-            const int items = 2 * w.n;
+            // q8_0: this warpgroup's items are the K tiles, or the V tiles
+            const bool only_v = C::q8 && warp >= 12;
+            const int items = C::q8 ? w.n : 2 * w.n, lead = min(C::ahead, w.n);
             // tile of the i-th item and whether it is V
             auto tile_of = [&](int i, bool &v) {
-                const int lead = min(C::ahead, w.n);
+                if constexpr (C::q8) {
+                    v = only_v;
+                    return i;
+                }
                 if (i < lead) { v = false; return i; }
                 i -= lead;
                 // V_0, K_lead, V_1, K_(lead + 1), ... and the last V's alone
@@ -281,7 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                 const int p = (w.t0 + tile_of(i, v)) * TP + lw * RW + lane;
                 return lane < RW && p < w.used ? row[p >> a.kv.page_shift] : -1;
             };
-            const int first = item;
             int page = page_of(0);
             auto wait_empty = [&](int it) {
                 return it < S || __all_sync(WSW_FULL_MASK, mbar_wait(&ct.empty[it % S], ((it / S) - 1) & 1u));
@@ -349,11 +363,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
             } else {
                 // codes and scales of the warp's own rows on their way, raw_stages - 1 tiles ahead
                 constexpr int kScale = D / 16;  // bytes of a row's scales
-                auto raw_of = [&](int it) { return raw_ring + it % C::raw_stages * C::raw; };
+                // this kind's place in the ring: K_0 .. K_(lead - 1), V_0, K_lead, V_1, ..., the last V's alone
+                auto place = [&](int i) {
+                    return item + (only_v ? (i < w.n - lead ? lead + 2 * i : w.n + i) : i < lead ? i : 2 * i - lead + 1);
+                };
+                auto raw_of = [&](int i) { return raw_ring + (only_v * C::raw_stages + i % C::raw_stages) * C::raw; };
                 auto issue = [&](int i) {
                     if (i < items) {
                         const Rows x = rows_of(i);
-                        unsigned char *to = raw_of(first + i);
+                        unsigned char *to = raw_of(i);
 #pragma unroll
                         for (int k = 0; k < kSteps; ++k) {
                             const int r = k * kRows + rr;
@@ -367,21 +385,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                     }
                     paged::cp_commit();  // a group for each turn, empty past the end
                 };
+                __syncwarp();  // every lane has read the last piece's rows
 #pragma unroll
                 for (int i = 0; i < C::raw_stages - 1; ++i) issue(i);
-                for (int i = 0; i < items; ++i, ++item) {
+                for (int i = 0; i < items; ++i) {
                     __syncwarp();  // every lane has read the place that the next copies reuse
                     issue(i + C::raw_stages - 1);
                     paged::cp_wait<C::raw_stages - 1>();
                     __syncwarp();  // the rows that every lane copied
-                    const int st = item % S;
-                    if (!wait_empty(item)) {
+                    const int at = place(i), st = at % S;
+                    if (!wait_empty(at)) {
                         ok = false;
                         break;
                     }
-                    const unsigned char *from = raw_of(item);
+                    const unsigned char *from = raw_of(i);
                     unsigned char *to = ring + st * C::stage;
-#pragma unroll 2
+#pragma unroll
                     for (int k = 0; k < kSteps; ++k) {
                         const int r = lw * RW + k * kRows + rr;
                         const uint4 code = *reinterpret_cast<const uint4 *>(from + r * D + c * 16);
@@ -400,13 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ct.full[st]);
                 }
+                item += 2 * w.n;
             }
         }
         cp_wait_all();
         __syncwarp();
-    } else if (warp >= kMmaWarp) {
+    } else if (warp >= C::mma_warp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::mma_regs));
-        if (warp == kMmaWarp) {
+        if (warp == C::mma_warp) {
             // The whole warp walks, so that addresses and descriptors are uniform values; one elected lane issues.
             // (With one lane walking alone an MMA was issued every 115 cycles.)
             Walk<C> w(a, pos, end, start.x, start.y);
@@ -646,12 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                 };
                 auto ref_of = [&] { return m == -INFINITY ? 0.f : m - C::shift; };  // nothing seen yet: all weights 0
                 if (plain) {
-                    // three chunks of scores stay in registers, the fourth is read twice
-                    constexpr int kStay = TP == 128 ? 3 : 2;
+                    // some chunks of scores stay in registers, the others are read twice (weights take the place of
+                    // the first ones' only)
+                    constexpr int kStay = C::stay;
                     uint32_t v[kStay][32];
                     float mx = -INFINITY;
-                    if constexpr (TP == 128) {
-                        tmem_ld32(s_base + 96, v[0]);
+#pragma unroll
+                    for (int c = kStay; c < TP / 32; ++c) {
+                        tmem_ld32(s_base + 32 * c, v[0]);
                         tmem_wait_ld();
                         mx = top(v[0], mx);
                     }
@@ -664,10 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
                     const float ref = ref_of();
 #pragma unroll
                     for (int c = 0; c < kStay; ++c) put(v[c], c, unit, ref);
-                    if constexpr (TP == 128) {
-                        tmem_ld32(s_base + 96, v[0]);
+#pragma unroll
+                    for (int c = kStay; c < TP / 32; ++c) {
+                        tmem_ld32(s_base + 32 * c, v[0]);
                         tmem_wait_ld();
-                        put(v[0], 3, unit, ref);
+                        put(v[0], c, unit, ref);
                     }
                 } else {
                     const int p0 = (w.t0 + j) * TP;
@@ -784,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefix_kernel(const __grid_c
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == C::mma_warp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
@@ -796,7 +819,13 @@ cudaError_t launch_one(const Args &a, cudaStream_t s, int ctas) {
     const auto kernel = attn_prefix_kernel<CT, D, QP, PP, RT>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), C::smem);
     if (e != cudaSuccess) return e;
-    return launch(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), C::smem, s, true, a);
+    // the roles' registers are shared out of what the block is launched with: with less, a role would wait for them
+    static const int regs = [kernel] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, reinterpret_cast<const void *>(kernel)) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs < C::regs) return cudaErrorLaunchOutOfResources;
+    return launch(kernel, dim3(static_cast<unsigned>(ctas)), dim3(C::threads), C::smem, s, true, a);
 }
 
 // Row tiles of a unit: two (the warpgroups share K and V) where a group has more than 128 rows on average
