@@ -792,21 +792,24 @@ int wsw_beam_select(const void *logits, int32_t dtype, int64_t requests, int64_t
  *   cu_groups   int32 [groups + 1], ascending within [0, requests];  prefix_len int32 [groups], within
  *               [0, max_pages * page_size].  A bound that is not is moved to the nearest one that is,
  *               and sets bit 2 of *err_flag; bits 0 and 1 as wsw_attn_paged_decode's.
+ *   share       1: always in this way.  0: batches whose cached positions have 128 MB at most (requests *
+ *               max_pages * page_size of them) are attended as wsw_attn_paged_decode does, in one
+ *               launch and without a look at the groups, which is sooner.
  *   head_dim    64 or 128.
  *   ws          device workspace of ws_bytes >= wsw_attn_paged_prefix_workspace_bytes(...) bytes,
  *               256-byte aligned, zero-filled before its first use and then reused, as
  *               wsw_attn_paged_decode's.
  *   1 <= groups <= 16384;  requests * q_heads <= 2^30;
- *   kv heads * (requests * group / 128 + groups) * (max_pages * page_size / 64 + 2) < 2^31 - 65536.
+ *   kv heads * (requests * group / 128 + groups) * (max_pages * page_size / 16 + 9) < 2^31 - 65536.
  *   Other arguments and limits as wsw_attn_paged_decode.  Four launches.
  */
 size_t wsw_attn_paged_prefix_workspace_bytes(int64_t requests, int64_t groups, int64_t q_heads, int64_t kv_heads,
                                              int64_t head_dim);
 int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t requests, int64_t q_heads, const wsw_kv_cache *cache,
                           const int32_t *table, int64_t max_pages, int64_t table_stride, const int32_t *lens,
-                          const int32_t *cu_groups, int64_t groups, const int32_t *prefix_len, float scale,
-                          float softcap, const float *slopes, void *out, float *lse, int32_t *err_flag, void *ws,
-                          size_t ws_bytes, void *stream, const wsw_launch_opts *opts);
+                          const int32_t *cu_groups, int64_t groups, const int32_t *prefix_len, int32_t share,
+                          float scale, float softcap, const float *slopes, void *out, float *lse, int32_t *err_flag,
+                          void *ws, size_t ws_bytes, void *stream, const wsw_launch_opts *opts);
 
 /*
  * wsw_bounded_wait_check -- run the bounded mbarrier wait of the tensor-core kernels

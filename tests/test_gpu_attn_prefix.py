@@ -98,7 +98,7 @@ class Case:
         lse = torch.full((n, self.kvh * self.group), 7.0, device="cuda")
         out = torch.full((n, self.kvh * self.group, self.d), 7.0, device="cuda", dtype=DT[self.qt])
         self.wsw.attn_paged_prefix(self.q.cuda(), self.kv, self.table_d, self.lens_d, self.cu_d, self.prefix_d, scale=scale,
-                                   lse=lse, out=out, **kw)
+                                   lse=lse, out=out, **{"share": True, **kw})
         return out, lse
 
     def check(self, scale=None, softcap=0.0, slopes=None, hidden=None, **kw):
@@ -271,9 +271,34 @@ def test_one_workspace_graphs_streams_and_repeated_calls():
     q, out, lse = c.q.cuda(), torch.empty_like(want[1][0]), torch.empty_like(want[1][1])
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        wsw.attn_paged_prefix(q, c.kv, c.table_d, c.lens_d, c.cu_d, c.prefix_d, out=out, lse=lse, ws=ws)
+        wsw.attn_paged_prefix(q, c.kv, c.table_d, c.lens_d, c.cu_d, c.prefix_d, out=out, lse=lse, ws=ws, share=True)
     for _ in range(3):
         out.fill_(5)
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want[1][0]) and torch.equal(lse, want[1][1])
+
+
+@pytest.mark.parametrize("q,cache", [("bf16", "bf16"), ("fp32", "q8_0")])
+def test_a_small_batch_goes_the_paged_way(q, cache):
+    """Without `share` the result is attn_paged_decode's, bit for bit, and the groups are not looked at."""
+    wsw = need_gpu()
+    c = Case(wsw, [(300, _lens(300, 1, 60, 7))], kvh=2, group=4, q=q, cache=cache)
+    c.cu_d.fill_(77)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = c.check(share=False, err_flag=err)
+    want_lse = torch.empty_like(lse)
+    want = wsw.attn_paged_decode(c.q.cuda(), c.kv, c.table_d, c.lens_d, lse=want_lse)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and int(err) == 0
+
+
+def test_a_large_batch_is_shared():
+    """A block table of more than 128 MB of positions, all but the first few unused."""
+    wsw = need_gpu()
+    c = Case(wsw, [(300, _lens(300, 1, 60, 7))], kvh=2, group=4, page=16)
+    wide = torch.full((3, 1 << 16), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.table_d.shape[1]] = c.table_d
+    small, _ = c.check()
+    c.table_d = wide
+    out, _ = c.check(share=False)
+    assert torch.equal(out, small)

@@ -127,7 +127,7 @@ def test_beam_select_rejects_on_host(lib):
 def _attend(lib, **change):
     c = _cache()
     a = dict(q=A, dtype=2, requests=4, q_heads=8, cache=ctypes.byref(c), table=A, width=8, stride=8, lens=A, cu=A, groups=2,
-             prefix=A, scale=ctypes.c_float(0.1), softcap=ctypes.c_float(0), slopes=N, out=A, lse=N, err=N, ws=A,
+             prefix=A, share=1, scale=ctypes.c_float(0.1), softcap=ctypes.c_float(0), slopes=N, out=A, lse=N, err=N, ws=A,
              ws_bytes=1 << 40)
     a.update(change)
     return lib.wsw_attn_paged_prefix(*a.values(), None, None)
@@ -138,7 +138,7 @@ def test_attn_prefix_rejects_on_host(lib):
         assert _attend(lib, **{name: N}) == INVALID, name
     for name in ("q", "table", "lens", "cu", "prefix", "slopes", "out", "lse", "err", "ws"):
         assert _attend(lib, **{name: P(4098)}) == MISALIGNED, name
-    for change in ({"requests": -1}, {"q_heads": 7}, {"groups": 0}, {"groups": -1}, {"stride": 7}, {"width": -1},
+    for change in ({"requests": -1}, {"q_heads": 7}, {"groups": 0}, {"groups": -1}, {"share": 2}, {"stride": 7}, {"width": -1},
                    {"scale": ctypes.c_float(float("inf"))}, {"softcap": ctypes.c_float(-1)}):
         assert _attend(lib, **change) == INVALID, change
     for change in ({"dtype": 3}, {"requests": 65536}, {"groups": 16385}, {"cache": ctypes.byref(_cache(head_dim=256))},

@@ -146,8 +146,8 @@ def load():
                                   ctypes.c_size_t, _p, _p]
     L.wsw_attn_paged_prefix_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i64]
     L.wsw_attn_paged_prefix_workspace_bytes.restype = ctypes.c_size_t
-    L.wsw_attn_paged_prefix.argtypes = [_p, _i32, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _i64, _p, _f32, _f32, _p, _p, _p,
-                                        _p, _p, ctypes.c_size_t, _p, _p]
+    L.wsw_attn_paged_prefix.argtypes = [_p, _i32, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _i64, _p, _i32, _f32, _f32, _p,
+                                        _p, _p, _p, _p, ctypes.c_size_t, _p, _p]
     for f in ("wsw_attn_paged_prefix", "wsw_beam_select", "wsw_kv_page_fork", "wsw_kv_page_copy", "wsw_kv_page_compact", "wsw_kv_page_plan", "wsw_rope_table", "wsw_rope_kv_write", "wsw_attn_paged_decode",
               "wsw_token_logprobs"):
         getattr(L, f).restype = ctypes.c_int
@@ -946,11 +946,12 @@ def attn_paged_prefix_workspace_bytes(requests, groups, q_heads, kv_heads, head_
 
 
 def attn_paged_prefix(q, kv, table, lens, groups, prefix, scale=None, softcap=0.0, slopes=None, out=None, lse=None,
-                      err_flag=None, ws=None, opts=None):
+                      err_flag=None, ws=None, share=False, opts=None):
     """attn_paged_decode for a batch in which groups of requests share a prefix, read once for each
     group: requests groups[g] .. groups[g + 1] - 1 (int32 [n + 1], ascending) have the same keys
     and values at their first prefix[g] (int32 [n]) positions.  head_dim 64 or 128, no window; the
-    other arguments and the result are attn_paged_decode's.  ws: a uint8 device tensor of at least
+    other arguments and the result are attn_paged_decode's.  Small batches (128 MB of cached
+    positions by the table's size) go attn_paged_decode's way unless share is true.  ws: a uint8 device tensor of at least
     attn_paged_prefix_workspace_bytes(...) bytes, zero-filled before its first use (every call
     leaves it ready for the next), allocated if None."""
     code, dev = _float_dev(q, "q")
@@ -972,8 +973,8 @@ def attn_paged_prefix(q, kv, table, lens, groups, prefix, scale=None, softcap=0.
                          device=q.device)
     _check(load().wsw_attn_paged_prefix(
         q.data_ptr(), code, n, heads, kv._ref if kv._device == dev else _elsewhere(kv, dev), tp, width, row,
-        _packed(lens, _I32, "lens", dev, (n,)), _packed(groups, _I32, "groups", dev, (count + 1,)), count, pp, scale,
-        softcap, None if slopes is None else _packed(slopes, _F32, "slopes", dev, (heads,)),
+        _packed(lens, _I32, "lens", dev, (n,)), _packed(groups, _I32, "groups", dev, (count + 1,)), count, pp,
+        1 if share else 0, scale, softcap, None if slopes is None else _packed(slopes, _F32, "slopes", dev, (heads,)),
         _packed(out, q.dtype, "out", dev, shape),
         None if lse is None else _packed(lse, _F32, "lse", dev, (n, heads)),
         None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev),

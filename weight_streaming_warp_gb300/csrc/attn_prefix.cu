@@ -22,6 +22,9 @@ namespace {
 
 constexpr int kMaxGroups = 16384;  // three words of shared memory each
 constexpr int kPlanThreads = 1024;
+constexpr int64_t kEachBytes = int64_t(128) << 20;
+constexpr int kPiece = 7;           // tiles
+constexpr int kSingleGroups = 16;   // groups for which the cut into single pieces is looked for
 
 // Parts of q by types.
 int q_parts(int dtype, int cache) {
@@ -34,9 +37,10 @@ int row_tiles(int64_t requests, int64_t group, int64_t groups, int parts) {
 
 struct PlanArgs {
     const int32_t *cu, *prefix, *lens;
-    int *begin, *off, *used, *rep, *run;  // as Plan
+    int *begin, *off, *used, *rep, *stride, *run;  // as Plan
     int2 *start;
-    int *first, *group_of;                // [requests] where the rest begins, whose prefix it shares
+    int *first;    // [requests] where the rest begins
+    int4 *pieces;  // [requests] what the join needs of its group (Pieces); rows 0: it shares nothing
     int32_t *err;
     int requests, groups, max_len, heads, group, unit_rows, tile;
 };
@@ -73,11 +77,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const Plan
     __syncthreads();
     // ---- the prefixes
     const int g0 = min(i0, a.groups), g1 = min(i1, a.groups);
-    int sum = 0;
-    auto tiles = [&](int g, int n) {
-        const int rows = (begin[g + 1] - begin[g]) * a.group;
-        return a.heads * ((rows + a.unit_rows - 1) / a.unit_rows) * ((n + a.tile - 1) / a.tile);
+    auto units = [&](int g) {  // of a KV head
+        return ((begin[g + 1] - begin[g]) * a.group + a.unit_rows - 1) / a.unit_rows;
     };
+    auto tiles = [&](int g) { return (used[g] + a.tile - 1) / a.tile; };
+    int sum = 0, count = 0;
     for (int g = g0; g < g1; ++g) {
         const int x = a.prefix[g], n = min(max(x, 0), a.max_len);
         if (n != x) err |= 4;
@@ -89,24 +93,53 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const Plan
         used[g] = shares && r < e ? n : 0;
         a.used[g] = used[g];
         a.rep[g] = r < a.requests ? r : 0;
-        sum += tiles(g, used[g]);
+        if (used[g] > 0) {
+            count += a.heads * units(g);
+            sum += a.heads * units(g) * tiles(g);
+        }
     }
-    int total;
+    // ---- the list.  A piece of a unit costs its CTA kPiece tiles beside its own: either units have as many
+    // places more, or (few groups) a CTA has one piece alone, of `run` tiles at most: the least of 32 lengths for
+    // which there are CTAs enough.
+    int total, all_units;
+    block_scan(sum, 0x7fffffff, scan_sm, &total);
+    block_scan(count, 0x7fffffff, scan_sm, &all_units);
+    int run = (total + kPiece * all_units + kCtas - 1) / kCtas;
+    bool single = false;
+    if (a.groups <= kSingleGroups) {  // every warp works it out
+        const int least = (total + kCtas - 1) / kCtas, mine = max(least + lane * max(least / 16, 1), 1);
+        int ctas = 0;
+        for (int g = 0; g < a.groups; ++g)
+            if (used[g] > 0) ctas += a.heads * units(g) * ((tiles(g) + mine - 1) / mine);
+        const uint32_t fit = __ballot_sync(WSW_FULL_MASK, ctas <= kCtas);
+        const int one = __shfl_sync(WSW_FULL_MASK, mine, fit ? __ffs(fit) - 1 : 0);
+        if (fit && one <= run) {
+            run = one;
+            single = true;
+        }
+    }
+    run = max(run, 1);
+    auto stride = [&](int g) {
+        return used[g] == 0 ? 0 : single ? (tiles(g) + run - 1) / run * run : tiles(g) + kPiece;
+    };
+    sum = 0;
+    for (int g = g0; g < g1; ++g) sum += a.heads * units(g) * stride(g);
     int at = block_scan(sum, 0x7fffffff, scan_sm, &total);
     for (int g = g0; g < g1; ++g) {
         a.off[g] = off[g] = at;
         a.begin[g] = begin[g];
-        at += tiles(g, used[g]);
+        a.stride[g] = stride(g);
+        at += a.heads * units(g) * stride(g);
     }
     if (tid == 0) {
         a.off[a.groups] = total;
         a.begin[a.groups] = begin[a.groups];
-        *a.run = max((total + kCtas - 1) / kCtas, 1);
+        a.run[0] = run;
+        a.run[1] = single;
     }
     if (err && a.err) atomicOr(a.err, err);
     __syncthreads();
     // ---- where each CTA begins: the last group whose part begins there or before
-    const int run = max((total + kCtas - 1) / kCtas, 1);
     for (int c = tid; c < kCtas; c += nt) {
         const int64_t pos = static_cast<int64_t>(c) * run;
         int lo = 0, n = a.groups;
@@ -128,74 +161,84 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const Plan
         const bool in = r >= begin[0] && r < begin[a.groups];
         const bool shares = in && used[lo] > 0 && min(a.lens[r], a.max_len) >= used[lo];
         a.first[r] = shares ? used[lo] : 0;
-        a.group_of[r] = shares ? lo : -1;
+        a.pieces[r] = shares ? make_int4((begin[lo + 1] - begin[lo]) * a.group, (r - begin[lo]) * a.group, off[lo], used[lo])
+                             : make_int4(0, 0, 0, 0);
     }
 }
 
 struct JoinArgs {
-    Plan plan;
-    const int *group_of;
+    const int *run;      // [2] places of a CTA, whether it has single pieces
+    const int4 *pieces;  // [requests]: query rows of its group per KV head, its own ones' place there, the group's place
+                         // in the list, its prefix's positions
     const float *rec, *whole;
     const float *rest;   // [rows][D]
     const float2 *ml;    // [rows]
     void *out;
     float *lse;
-    int64_t rows;        // requests * q_heads
-    int q_heads, group, row_tiles, tile, dtype;
+    int q_heads, group, row_shift, tile_shift, dtype;  // log2 of a unit's rows, of a tile's positions
 };
 
+// A warp for each query head of a request.
 template <int D>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const JoinArgs a) {
     constexpr int N = D / 32, kRec = D + kHead;  // values of a lane
     using V = std::conditional_t<N == 4, float4, float2>;
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int req = blockIdx.y, head = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t row = static_cast<int64_t>(req) * a.q_heads + head;
     pdl_launch_dependents();
     pdl_wait();
-    if (row >= a.rows) return;
-    const int req = static_cast<int>(row / a.q_heads), head = static_cast<int>(row - static_cast<int64_t>(req) * a.q_heads);
-    const int g = a.group_of[req];
+    if (head >= a.q_heads) return;
+    const int4 of = a.pieces[req];
+    const int run = *a.run;
     const V rest = *reinterpret_cast<const V *>(a.rest + row * D + lane * N);
     const float2 ml = a.ml[row];
     float s[N], m = ml.x, l = ml.y;
     const float *r = reinterpret_cast<const float *>(&rest);
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] = r[i] * l;  // the rest comes divided by its sum
-    if (g >= 0) {
-        const int unit_rows = 128 * a.row_tiles;
-        const int rows = (a.plan.begin[g + 1] - a.plan.begin[g]) * a.group;
-        const int nt = (a.plan.used[g] + a.tile - 1) / a.tile, run = *a.plan.run;
-        const int kv = head / a.group, in = (req - a.plan.begin[g]) * a.group + head - kv * a.group;
-        const int unit = kv * ((rows + unit_rows - 1) / unit_rows) + in / unit_rows;
-        const int first = a.plan.off[g] + unit * nt, c0 = first / run, c1 = (first + nt - 1) / run;
+    if (of.x > 0) {
+        const int unit_rows = 1 << a.row_shift, nt = ((of.w - 1) >> a.tile_shift) + 1;
+        const int kv = head / a.group, in = of.y + head - kv * a.group;
+        const int unit = kv * (((of.x - 1) >> a.row_shift) + 1) + (in >> a.row_shift);
+        const int stride = a.run[1] ? (nt + run - 1) / run * run : nt + kPiece;
+        const int first = of.z + unit * stride, c0 = first / run, c1 = (first + nt - 1) / run;
         const int n = c1 - c0 + 1;
         // piece k: a unit that one CTA has whole, or of CTA c0 + k its last piece (k = 0) or its first
         const int64_t apart = static_cast<int64_t>(2) * unit_rows * kRec;
         const float *one = n == 1 ? a.whole + row * kRec
-                                  : a.rec + (static_cast<int64_t>(c0) * 2 * unit_rows + in % unit_rows) * kRec;
-        auto piece = [&](int k) {
-            return n == 1 ? one : one + k * apart + (k == 0 ? static_cast<int64_t>(unit_rows) * kRec : 0);
-        };
-        float mx = m;
-        for (int k = lane; k < n; k += 32) mx = fmaxf(mx, piece(k)[0]);
+                                  : a.rec + (static_cast<int64_t>(c0) * 2 * unit_rows + (in & (unit_rows - 1))) * kRec;
+        // four at a time: their sums and values on their way together, then raised to a common maximum
+        for (int k0 = 0; k0 < n; k0 += 4) {
+            float2 pml[4];
+            V v[4];
+            float mx = m;
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(WSW_FULL_MASK, mx, d));
-        const float f = paged::weight(m, mx);
+            for (int k = 0; k < 4; ++k) {
+                const float *p = n == 1 ? one : one + (k0 + k) * apart + (k0 + k == 0 ? static_cast<int64_t>(unit_rows) * kRec : 0);
+                pml[k] = make_float2(-INFINITY, 0.f);
+                if (k0 + k < n) {
+                    pml[k] = *reinterpret_cast<const float2 *>(p);
+                    v[k] = *reinterpret_cast<const V *>(p + kHead + lane * N);
+                }
+            }
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = f == 0.f ? 0.f : s[i] * f;
-        l *= f;
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float *p = piece(k);
-            const float2 pml = *reinterpret_cast<const float2 *>(p);
-            const V v = *reinterpret_cast<const V *>(p + kHead + lane * N);
-            const float w = paged::weight(pml.x, mx);
-            const float *x = reinterpret_cast<const float *>(&v);
+            for (int k = 0; k < 4; ++k) mx = fmaxf(mx, pml[k].x);
+            const float f = paged::weight(m, mx);
+            l *= f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) s[i] = w == 0.f ? s[i] : fmaf(x[i], w, s[i]);
-            l = fmaf(pml.y, w, l);
+            for (int i = 0; i < N; ++i) s[i] = f == 0.f ? 0.f : s[i] * f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k0 + k >= n) break;
+                const float w = paged::weight(pml[k].x, mx);
+                const float *x = reinterpret_cast<const float *>(&v[k]);
+#pragma unroll
+                for (int i = 0; i < N; ++i) s[i] = w == 0.f ? s[i] : fmaf(x[i], w, s[i]);
+                l = fmaf(pml[k].y, w, l);
+            }
+            m = mx;
         }
-        m = mx;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * paged::kLn2;
@@ -224,7 +267,8 @@ Room room(int64_t requests, int64_t groups, int64_t q_heads, int64_t kv_heads, i
     // two row tiles by the rule for one part of q: the most that any types need
     const int rt = row_tiles(requests, q_heads / kv_heads, groups, 1);
     w.plan = align256(wsw_attn_paged_decode_workspace_bytes(requests, q_heads, kv_heads, head_dim));
-    w.rec = w.plan + align256((2 * kCtas + 4 * (static_cast<size_t>(groups) + 1) + 1 + 2 * static_cast<size_t>(requests)) * 4);
+    w.rec = w.plan + align256((2 * kCtas + 4 * static_cast<size_t>(requests) + 5 * (static_cast<size_t>(groups) + 1) + 2 +
+                               static_cast<size_t>(requests)) * 4);
     w.whole = w.rec + static_cast<size_t>(kCtas) * 2 * rt * 128 * rec;
     w.rest = w.whole + align256(rows * rec);
     w.ml = w.rest + align256(rows * head_dim * 4);
@@ -248,8 +292,8 @@ extern "C" size_t wsw_attn_paged_prefix_workspace_bytes(int64_t requests, int64_
 extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t requests, int64_t q_heads,
                                      const wsw_kv_cache *cache, const int32_t *table, int64_t max_pages,
                                      int64_t table_stride, const int32_t *lens, const int32_t *cu_groups,
-                                     int64_t groups, const int32_t *prefix_len, float scale, float softcap,
-                                     const float *slopes, void *out, float *lse, int32_t *err_flag, void *ws,
+                                     int64_t groups, const int32_t *prefix_len, int32_t share, float scale,
+                                     float softcap, const float *slopes, void *out, float *lse, int32_t *err_flag, void *ws,
                                      size_t ws_bytes, void *stream, const wsw_launch_opts *opts) {
     using namespace wsw;
     using namespace wsw::prefix;
@@ -262,7 +306,7 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     st = paged::prepare(q, dtype, requests, q_heads, cache, table, max_pages, table_stride, lens, scale, softcap, 0, slopes,
                         out, lse, err_flag, &rest, &rows, &list);
     if (st != WSW_OK) return st;
-    if (groups < 1) return WSW_ERR_INVALID_ARG;
+    if (groups < 1 || (share != 0 && share != 1)) return WSW_ERR_INVALID_ARG;
     if (groups > kMaxGroups || rest.kv.head_dim == 256) return WSW_ERR_UNSUPPORTED;
     if (requests == 0) return WSW_OK;
     if (!cu_groups || !prefix_len || !ws) return WSW_ERR_INVALID_ARG;
@@ -272,7 +316,7 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     const int64_t kv_heads = cache->heads, group = rest.group;
     // the longest list: tiles are counted in 32 bits
     const int64_t units = kv_heads * (requests * group / 128 + groups), longest = (rest.max_len + 63) / 64;
-    if (requests * q_heads > (int64_t(1) << 30) || units * (longest + 1) >= (int64_t(1) << 31) - 65536)
+    if (requests * q_heads > (int64_t(1) << 30) || units * (4 * longest + kPiece + 1) >= (int64_t(1) << 31) - 65536)
         return WSW_ERR_UNSUPPORTED;
     const Room w = room(requests, groups, q_heads, kv_heads, cache->head_dim);
     if (ws_bytes < w.bytes) return WSW_ERR_WORKSPACE;
@@ -280,18 +324,26 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     if (!device_info(&di, &st)) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned char *base = static_cast<unsigned char *>(ws);
+    paged::place(&rest, ws, rows);
+    // What all requests list of a prefix comes from HBM once anyhow while it stays in L2, and four launches cost 9 us
+    // more than one: 4 heads of 128, bf16, group 8, one prefix of 8192 for 8 / 16 requests (135 / 271 MB in all) 33 / 34 us
+    // shared and 27 / 40 each on its own; 16 prefixes of 1024 for 4 each (143 MB) 27 and 29.
+    const int64_t row_bytes = 2 * kv_heads * (cache->dtype == WSW_Q8_0 ? cache->head_dim * 17 / 16 : cache->head_dim * 2);
+    if (!share && requests * static_cast<int64_t>(rest.max_len) <= kEachBytes / row_bytes)
+        return paged::launch_paged(rest, cache->dtype, rows, list, s, o.pdl) == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
 
     const int rt = row_tiles(requests, group, groups, q_parts(dtype, cache->dtype));
     PlanArgs p;
     p.cu = cu_groups; p.prefix = prefix_len; p.lens = lens; p.err = err_flag;
-    p.start = reinterpret_cast<int2 *>(base + w.plan);
+    p.pieces = reinterpret_cast<int4 *>(base + w.plan);
+    p.start = reinterpret_cast<int2 *>(p.pieces + requests);
     p.begin = reinterpret_cast<int *>(p.start + kCtas);
     p.off = p.begin + groups + 1;
     p.used = p.off + groups + 1;
     p.rep = p.used + groups + 1;
-    p.run = p.rep + groups + 1;
-    p.first = p.run + 1;
-    p.group_of = p.first + requests;
+    p.stride = p.rep + groups + 1;
+    p.run = p.stride + groups + 1;
+    p.first = p.run + 2;
     p.requests = rest.requests; p.groups = static_cast<int>(groups); p.max_len = rest.max_len;
     p.heads = rest.kv.heads; p.group = rest.group; p.unit_rows = 128 * rt; p.tile = tile_positions(dtype == WSW_F32 ? 2 : 1, cache->dtype, rt);
     const int plan_smem = static_cast<int>((3 * groups + 1) * 4);
@@ -302,7 +354,7 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
 
     Args a;
     a.q = q; a.slopes = slopes; a.table = table; a.lens = lens; a.err = err_flag;
-    a.plan = Plan{p.begin, p.off, p.used, p.rep, p.run, p.start};
+    a.plan = Plan{p.begin, p.off, p.used, p.rep, p.stride, p.run, p.start};
     a.rec = reinterpret_cast<float *>(base + w.rec);
     a.whole = reinterpret_cast<float *>(base + w.whole);
     a.kv = rest.kv;
@@ -320,7 +372,6 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     else e = launch_prefix<WSW_Q8_0>(a, rt, s, ctas);
     if (e != cudaSuccess) return WSW_ERR_CUDA;
 
-    paged::place(&rest, ws, rows);
     rest.first = p.first;
     rest.out = base + w.rest;
     rest.out_dtype = WSW_F32;
@@ -330,14 +381,15 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     if (e != cudaSuccess) return WSW_ERR_CUDA;
 
     JoinArgs j;
-    j.plan = a.plan;
-    j.group_of = p.group_of;
+    j.run = p.run;
+    j.pieces = p.pieces;
     j.rec = a.rec; j.whole = a.whole;
     j.rest = reinterpret_cast<const float *>(rest.out); j.ml = rest.ml;
     j.out = out; j.lse = lse;
-    j.rows = requests * q_heads;
-    j.q_heads = rest.q_heads; j.group = rest.group; j.row_tiles = rt; j.tile = p.tile; j.dtype = dtype;
-    const dim3 grid(static_cast<unsigned>((j.rows + 7) / 8));
+    j.q_heads = rest.q_heads; j.group = rest.group; j.dtype = dtype;
+    j.row_shift = rt == 2 ? 8 : 7;
+    j.tile_shift = p.tile == 128 ? 7 : 6;
+    const dim3 grid(static_cast<unsigned>((q_heads + 7) / 8), static_cast<unsigned>(requests));
     e = rest.kv.head_dim == 64 ? launch(prefix_join_kernel<64>, grid, dim3(256), 0, s, true, j)
                                : launch(prefix_join_kernel<128>, grid, dim3(256), 0, s, true, j);
     return e == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;

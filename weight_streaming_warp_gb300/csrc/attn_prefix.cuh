@@ -51,7 +51,7 @@ constexpr int kLoaders = 4;    // warps that share a tile
 constexpr int kSeen = 16;      // tiles whose visible positions are kept
 constexpr int kControl = 2048, kTileBytes = 227 * 1024 - kControl - 1024;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kHead = 8;       // floats before a record's O, which keeps 32-byte alignment
+constexpr int kHead = 8;       // floats before a record's O: whole sectors
 
 // What the plan kernel leaves: [groups + 1] each but `run`.
 struct Plan {
@@ -59,7 +59,8 @@ struct Plan {
     const int *off;    // its tiles' place in the list
     const int *used;   // its prefix's positions
     const int *rep;    // the request whose table row holds its pages
-    const int *run;    // [1] tiles of a CTA
+    const int *stride; // places that each of its units has in the list, its tiles at least
+    const int *run;    // [1] places of a CTA
     const int2 *start; // [kCtas] group and place in its part where a CTA's run begins; group -1: nothing
 };
 
@@ -136,7 +137,7 @@ struct Walk {
     int pos, end;                 // places in the list
     int g, in;                    // group, place in its part
     int begin, rows, used, rep;   // of the group: first request, query rows per KV head, positions
-    int nt, per_head;             // tiles and row tiles
+    int nt, stride, per_head;     // tiles and places of a unit, units of a KV head
     // the piece
     int head, tile, t0, n;        // KV head, unit of the head, first tile, tiles
 
@@ -148,21 +149,31 @@ struct Walk {
         used = a.plan.used[g];
         rep = a.plan.rep[g];
         nt = (used + C::TP - 1) / C::TP;
+        stride = a.plan.stride[g];
         per_head = (rows + 128 * C::RT - 1) / (128 * C::RT);
     }
     __device__ bool next() {
         if (pos >= end) return false;
         group();
-        while (in >= nt * per_head * a.kv.heads) {  // the next group with tiles: there is one
-            do ++g;
-            while (a.plan.off[g + 1] == a.plan.off[g]);
-            in = 0;
-            group();
+        for (;;) {
+            while (in >= stride * per_head * a.kv.heads) {  // the next group with tiles
+                do ++g;
+                while (g < a.groups && a.plan.off[g + 1] == a.plan.off[g]);
+                if (g >= a.groups) return false;
+                in = 0;
+                group();
+            }
+            const int unit = in / stride;
+            t0 = in - unit * stride;
+            if (t0 < nt) {
+                head = unit / per_head;
+                tile = unit - head * per_head;
+                break;
+            }
+            pos += stride - t0;  // places without tiles
+            in += stride - t0;
+            if (pos >= end) return false;
         }
-        const int unit = in / nt;
-        t0 = in - unit * nt;
-        head = unit / per_head;
-        tile = unit - head * per_head;
         n = min(nt - t0, end - pos);
         pos += n;
         in += n;
@@ -175,9 +186,13 @@ __device__ __forceinline__ void cp16_all(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // 32 bytes at a 32-byte boundary: a whole sector
-__device__ __forceinline__ void st32(float *p, const uint32_t *r) {
+__device__ __forceinline__ void st32(float *p, const uint32_t (&r)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
                  "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // one lane of the (converged) warp
@@ -298,6 +313,9 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
             };
             int page = page_of(0);
             auto wait_empty = [&](int it) {
+                // The first queries come before most of the first tiles: behind a ring full of copies a load takes
+                // 4 us.
+                if (it == 2 && !__all_sync(WSW_FULL_MASK, mbar_wait(&ct.q_full, 0))) return false;
                 return it < S || __all_sync(WSW_FULL_MASK, mbar_wait(&ct.empty[it % S], ((it / S) - 1) & 1u));
             };
             // a tile's rows to where they lie: lane's row, for all lanes
@@ -531,20 +549,43 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                 const int first_in_group = (w.tile * RT + (RT == 2 ? slot : 0)) * 128;
                 unsigned char *to = q_sm + (RT == 2 ? slot : 0) * QP * C::q_part;
                 constexpr int kTurns = kRowsOfWarp / kPer, kAtOnce = 4;
+                // the lane's rows in turn, as request and head of the group
+                int in = first_in_group + r0, rq = in / a.group, rg = in - rq * a.group;
+                auto source = [&](int esize) {
+                    return static_cast<const unsigned char *>(a.q) +
+                           ((static_cast<int64_t>(w.begin + rq) * a.q_heads + w.head * a.group + rg) * D + 8 * ch) * esize;
+                };
+                auto step_row = [&] {
+                    in += kPer;
+                    rg += kPer;
+                    while (rg >= a.group) {
+                        rg -= a.group;
+                        ++rq;
+                    }
+                };
+                // 16-bit rows of the cache's own type as they are
+                const bool as_is = QP == 1 && a.dtype == (C::bf16 ? WSW_BF16 : WSW_F16) && !a.negative;
+                if (as_is) {
 #pragma unroll 1
-                for (int t = 0; t < kTurns; t += kAtOnce) {
+                    for (int t = 0; t < kTurns; ++t) {
+                        const bool there = in < w.rows;
+                        cp16(saddr(to) + swizzled(r0 + t * kPer, ch, 128), there ? source(2) : static_cast<const unsigned char *>(a.q),
+                             there);
+                        step_row();
+                    }
+                    cp_wait_all();
+                }
+#pragma unroll 1
+                for (int t = 0; t < kTurns && !as_is; t += kAtOnce) {
                     uint4 raw[kAtOnce][QP == 1 || (C::bf16 && QP == 2) ? 1 : 2];  // fp32 rows are twice as wide
                     constexpr bool kMayBeWide = QP == 3 || (!C::bf16 && QP == 2);
 #pragma unroll
                     for (int u = 0; u < kAtOnce; ++u) {
-                        const int in = first_in_group + r0 + (t + u) * kPer;
-                        const int64_t h = static_cast<int64_t>(w.begin + (in < w.rows ? in : 0) / a.group) * a.q_heads +
-                                          w.head * a.group + (in < w.rows ? in : 0) % a.group;
-                        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(a.q) +
-                                                                           (h * D + 8 * ch) * (kMayBeWide ? 4 : 2));
+                        const uint4 *src = reinterpret_cast<const uint4 *>(source(kMayBeWide ? 4 : 2));
 #pragma unroll
                         for (int k = 0; k < (kMayBeWide ? 2 : 1); ++k)
                             raw[u][k] = in < w.rows ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                        step_row();
                     }
 #pragma unroll
                     for (int u = 0; u < kAtOnce; ++u) {
@@ -600,6 +641,19 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                     if (a.dtype != WSW_F16) {
                         if (RT == 1) asm volatile("bar.sync 1, 256;" ::: "memory");
                         unit *= ct.unit[(RT == 2 ? slot * 128 : 0) + r];
+                    }
+                }
+            }
+            // the next piece's queries into L1 before its tiles fill the way to memory
+            {
+                Walk<C> nx = w;
+                if (nx.next()) {
+                    const int rows = min(nx.rows - nx.tile * RT * 128, RT * 128), row_bytes = D * (a.dtype == WSW_F32 ? 4 : 2);
+                    const int lines = row_bytes / 128;
+                    for (int i = tid; i < rows * lines; i += 256) {
+                        const int in = nx.tile * RT * 128 + i / lines;
+                        const int64_t h = static_cast<int64_t>(nx.begin + in / a.group) * a.q_heads + nx.head * a.group + in % a.group;
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const unsigned char *>(a.q) + h * row_bytes + i % lines * 128));
                     }
                 }
             }
@@ -774,32 +828,25 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                 l = x.y * f0 + y.y * f1;
             }
             if (real && (RT == 2 || slot == 0)) *reinterpret_cast<float2 *>(rec) = make_float2(m == -INFINITY ? m : m - C::shift, l);
+            // (a rolled loop of few instructions: code that runs once a piece is mostly waited for)
             constexpr int kCols = RT == 2 ? D : D / 2;
+            const int col0 = RT == 2 ? 0 : slot * kCols;
+            const uint32_t from = RT == 2 ? o_base : lane_base + C::o_col + col0;
 #pragma unroll 1
-            for (int c = 0; c < kCols / 32; ++c) {
-                const int col = (RT == 2 ? 0 : slot * kCols) + 32 * c;
-                uint32_t o[32];
-                if (have) {
-                    if constexpr (RT == 2) {
-                        tmem_ld32(o_base + col, o);
-                        tmem_wait_ld();
-                    } else {
-                        uint32_t y[32];
-                        tmem_ld32(lane_base + C::o_col + col, o);
-                        if (w.n > 1) tmem_ld32(lane_base + C::o_col + D + col, y);
-                        tmem_wait_ld();
+            for (int c = 0; c < kCols; c += 8) {
+                uint32_t o[8], y[8];
+                tmem_ld8(from + c, o);
+                if (RT == 1) tmem_ld8(from + D + c, y);
+                tmem_wait_ld();
+                if (RT == 1) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            // a part without weights holds nothing (0 times what its rows hold may be NaN)
-                            const float x = f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
-                            o[i] = __float_as_uint(w.n > 1 && f1 != 0.f ? fmaf(__uint_as_float(y[i]), f1, x) : x);
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        // a part without weights holds nothing (0 times what its rows hold may be NaN)
+                        const float x = f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
+                        o[i] = __float_as_uint(f1 == 0.f ? x : fmaf(__uint_as_float(y[i]), f1, x));
                     }
                 }
-                if (real) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) st32(rec + kHead + col + i, o + i);
-                }
+                if (real) st32(rec + kHead + col0 + c, o);
             }
             // both have read the sums and O before the next piece's
             if (RT == 1) asm volatile("bar.sync 1, 256;" ::: "memory");
