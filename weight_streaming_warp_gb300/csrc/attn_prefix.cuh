@@ -122,7 +122,7 @@ struct Cfg {
 
 struct Control {
     uint64_t full[8], empty[8];
-    uint64_t s_full[2], p_full[2];  // of a slot
+    uint64_t s_full[2], p_full[2][2];  // of a slot; of each half of its weights
     uint64_t q_full, o_done;
     uint32_t seen[kSeen][4];
     float unit[256];    // of the rows' scores
@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ct.s_full[i], 1);
-            mbar_init(&ct.p_full[i], 4);
+            mbar_init(&ct.p_full[i][0], 4);
+            mbar_init(&ct.p_full[i][1], 4);
         }
         mbar_init(&ct.q_full, 8);
         mbar_init(&ct.o_done, 1);
@@ -478,14 +479,15 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                 }
                 __syncwarp();
             };
-            auto values = [&](int slot, int v, bool more) {
-                const uint64_t dv = sw128_mn_desc(saddr(ring + (v % S) * C::stage), TP * 128);
-                const uint32_t d = tmem + C::o_col + slot * D, p = tmem + slot * C::s_cols;
+            // half of a tile's positions: the first half's products run while the other half's weights are made
+            auto values = [&](int slot, int v, int half, bool more) {
+                const uint64_t dv = sw128_mn_desc(saddr(ring + (v % S) * C::stage), TP * 128) + half * (TP / 32) * 128;
+                const uint32_t d = tmem + C::o_col + slot * D, p = tmem + slot * C::s_cols + half * (TP / 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int part = 0; part < PP; ++part)
 #pragma unroll
-                        for (int kk = 0; kk < TP / 16; ++kk)
+                        for (int kk = 0; kk < TP / 32; ++kk)
                             mma_ts(d, p + part * (TP / 2) + 8 * kk, dv + 128 * kk, id_pv, more || (part | kk) != 0);
                 }
                 __syncwarp();
@@ -510,11 +512,14 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                     const int v = item++, k = more_k ? item++ : 0;
                     for (int s = 0; s < RT; ++s) {
                         const int slot = RT == 2 ? s : j & 1;
-                        if (!(ok = wait(&ct.p_full[slot], p_phase[slot]))) break;
-                        p_phase[slot] ^= 1u;
+                        if (!(ok = wait(&ct.p_full[slot][0], p_phase[slot]))) break;
                         if (s == 0 && !(ok = landed(v))) break;
                         tc_fence_after();
-                        values(slot, v, RT == 2 ? j > 0 : j > 1);
+                        values(slot, v, 0, RT == 2 ? j > 0 : j > 1);
+                        if (!(ok = wait(&ct.p_full[slot][1], p_phase[slot]))) break;
+                        p_phase[slot] ^= 1u;
+                        tc_fence_after();
+                        values(slot, v, 1, true);
                         if (s == RT - 1) commit(&ct.empty[v % S]);
                         if (!more_k) continue;
                         if (s == 0 && !(ok = landed(k))) break;
@@ -718,6 +723,12 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
 #pragma unroll
                     for (int k = 0; k < PP; ++k) tmem_st16(s_base + k * (TP / 2) + 16 * chunk, part[k]);
                 };
+                auto ready = [&](int half) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ct.p_full[slot][half]);
+                };
                 auto ref_of = [&] { return m == -INFINITY ? 0.f : m - C::shift; };  // nothing seen yet: all weights 0
                 if (plain) {
                     // some chunks of scores stay in registers, the others are read twice (weights take the place of
@@ -739,7 +750,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                     raise_to(mx * unit);
                     const float ref = ref_of();
 #pragma unroll
-                    for (int c = 0; c < kStay; ++c) put(v[c], c, unit, ref);
+                    for (int c = 0; c < kStay; ++c) {
+                        put(v[c], c, unit, ref);
+                        if (c == TP / 64 - 1) ready(0);
+                    }
 #pragma unroll
                     for (int c = kStay; c < TP / 32; ++c) {
                         tmem_ld32(s_base + 32 * c, v[0]);
@@ -786,8 +800,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                     raise_to(mx);
                     const float ref = ref_of();
                     put(va, 0, 1.f, ref);
+                    if constexpr (TP == 64) ready(0);
                     put(vb, 1, 1.f, ref);
                     if constexpr (TP == 128) {
+                        ready(0);
 #pragma unroll 1
                         for (int c = 2; c < 4; ++c) {
                             read(va, c);
@@ -795,10 +811,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                         }
                     }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ct.p_full[slot]);
+                ready(1);
                 float l0, l1, l2, l3;
                 f2_unpack(l2a, l0, l1);
                 f2_unpack(l2b, l2, l3);
