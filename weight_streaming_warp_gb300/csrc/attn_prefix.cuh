@@ -111,10 +111,9 @@ struct Cfg {
     static constexpr int mma_warp = 8 + 4 * load_groups, threads = 32 * (mma_warp + 4);
     // registers of a thread, as launched and by role
     static constexpr int regs = q8 ? 96 : 128;
-    static constexpr int soft_regs = q8 ? 128 : 184, load_regs = 80, mma_regs = 64;
+    static constexpr int soft_regs = q8 ? 128 : 144, load_regs = q8 ? 80 : 112, mma_regs = q8 ? 64 : 112;
     static_assert(2 * soft_regs + load_groups * load_regs + mma_regs == (3 + load_groups) * regs && regs * threads <= 65536,
                   "what the block was launched with");
-    static constexpr int stay = TP == 64 ? 2 : q8 ? 2 : 3;  // chunks of 32 scores that a thread keeps
     static_assert(2 * s_cols + 2 * D <= 512 && stages >= 3 && kSeen >= stages + 4 + (q8 ? raw_stages : 0), "room");
     static constexpr int smem = q_bytes + stages * stage + 2 * raw_stages * raw + kControl + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
@@ -731,31 +730,28 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                 };
                 auto ref_of = [&] { return m == -INFINITY ? 0.f : m - C::shift; };  // nothing seen yet: all weights 0
                 if (plain) {
-                    // some chunks of scores stay in registers, the others are read twice (weights take the place of
-                    // the first ones' only)
-                    constexpr int kStay = C::stay;
-                    uint32_t v[kStay][32];
+                    // Two chunks of scores stay in registers, the others are read twice, a chunk at a time (weights take the
+                    // place of the first two's only).  256 requests behind 32768 positions: 157 us; three chunks 162, four 163,
+                    // the second half on its way while the first half's weights are made 163.
+                    uint32_t v[2][32];
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int c = kStay; c < TP / 32; ++c) {
+                    for (int c = 2; c < TP / 32; ++c) {
                         tmem_ld32(s_base + 32 * c, v[0]);
                         tmem_wait_ld();
                         mx = top(v[0], mx);
                     }
-#pragma unroll
-                    for (int c = 0; c < kStay; ++c) tmem_ld32(s_base + 32 * c, v[c]);
+                    tmem_ld32(s_base, v[0]);
+                    tmem_ld32(s_base + 32, v[1]);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < kStay; ++c) mx = top(v[c], mx);
-                    raise_to(mx * unit);
+                    raise_to(top(v[1], top(v[0], mx)) * unit);
                     const float ref = ref_of();
+                    put(v[0], 0, unit, ref);
+                    if constexpr (TP == 64) ready(0);
+                    put(v[1], 1, unit, ref);
+                    if constexpr (TP == 128) ready(0);
 #pragma unroll
-                    for (int c = 0; c < kStay; ++c) {
-                        put(v[c], c, unit, ref);
-                        if (c == TP / 64 - 1) ready(0);
-                    }
-#pragma unroll
-                    for (int c = kStay; c < TP / 32; ++c) {
+                    for (int c = 2; c < TP / 32; ++c) {
                         tmem_ld32(s_base + 32 * c, v[0]);
                         tmem_wait_ld();
                         put(v[0], c, unit, ref);
