@@ -302,3 +302,15 @@ def test_a_large_batch_is_shared():
     c.table_d = wide
     out, _ = c.check(share=False)
     assert torch.equal(out, small)
+
+
+@pytest.mark.parametrize("q,cache", [("bf16", "bf16"), ("fp32", "q8_0"), ("fp32", "bf16"), ("fp16", "fp16")])
+@pytest.mark.parametrize("prefix", [1, 40, 64, 128])
+def test_pieces_of_one_tile(q, cache, prefix):
+    """Several pieces of one tile (two, of 64 positions) to a block: a ring place of the first tiles belongs
+    to a later piece, whose queries come while the loads of the one before may still be behind."""
+    c = Case(need_gpu(), [(prefix, _lens(prefix, 0, 1))] * 400, d=64, q=q, cache=cache, group=2)
+    out, lse = c.check()
+    for _ in range(20):
+        o, l = c.run()
+        assert torch.equal(o, out) and torch.equal(l, lse)

@@ -312,10 +312,12 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                 return lane < RW && p < w.used ? row[p >> a.kv.page_shift] : -1;
             };
             int page = page_of(0);
+            const bool first_piece = item == 0;
             auto wait_empty = [&](int it) {
                 // The first queries come before most of the first tiles: behind a ring full of copies a load takes
-                // 4 us.
-                if (it == 2 && !__all_sync(WSW_FULL_MASK, mbar_wait(&ct.q_full, 0))) return false;
+                // 4 us.  In the first piece alone: the barrier's next phase needs all of that piece's tiles, so it
+                // cannot pass while this waits; behind a first piece of one tile it could.
+                if (first_piece && it == 2 && !__all_sync(WSW_FULL_MASK, mbar_wait(&ct.q_full, 0))) return false;
                 return it < S || __all_sync(WSW_FULL_MASK, mbar_wait(&ct.empty[it % S], ((it / S) - 1) & 1u));
             };
             // a tile's rows to where they lie: lane's row, for all lanes
