@@ -772,19 +772,60 @@ def token_logprobs(logits, tokens=None, top=0, scale=1.0, out=None, ws=None, opt
 
 # ------------------------------------------------------ rows that continue one prompt ----
 
-class PageCopies(NamedTuple):
-    """Copies of pages for kv_page_copy; the first `count` of them are there."""
-    src: torch.Tensor             # int32 [most]
-    dst: torch.Tensor             # int32 [most]
-    fill: Optional[torch.Tensor]  # int32 [most] positions of each, or None: whole pages
-    count: torch.Tensor           # int32 [1]
+class _Held:
+    """Tensors that a program makes once and passes to call after call: checked here, held by the
+    object, their addresses kept."""
+    __slots__ = ("_device", "_at")
+    _names = ()
+
+    def __iter__(self):
+        return iter([getattr(self, n) for n in self._names])
+
+    def __setattr__(self, name, value):
+        if name in self._names and hasattr(self, name):
+            raise AttributeError("the tensors of a %s stay those that it was made with" % type(self).__name__)
+        object.__setattr__(self, name, value)
+
+    def _hold(self, first, checks):
+        """checks: (tensor, type, name, shape) of each, all on the first one's device."""
+        if not isinstance(first, _Tensor) or not first.is_cuda:
+            raise WswError("%s must be a CUDA tensor" % checks[0][2])
+        self._device = first.get_device()
+        self._at = tuple([None if t is None else _packed(t, d, n, self._device, s) for t, d, n, s in checks])
+
+    def _on_device(self, dev):
+        if self._device != dev:
+            raise WswError("the %s is on cuda:%d, the call's device is cuda:%d" % (type(self).__name__, self._device, dev))
+        return self._at
 
 
-class KvFork(NamedTuple):
-    table: torch.Tensor    # int32 [children][max_pages]
-    seq_len: torch.Tensor  # int32 [children]
-    head: torch.Tensor     # int32 [1]
-    copies: PageCopies     # room for one of each child
+class PageCopies(_Held):
+    """Copies of pages for kv_page_copy: the first `count` (int32 [1]) of src and dst (int32 [most]) are
+    there, of fill (int32 [most], or None: whole pages) positions each."""
+    __slots__ = ("src", "dst", "fill", "count", "most")
+    _names = ("src", "dst", "fill", "count")
+
+    def __init__(self, src, dst, fill, count):
+        self.src, self.dst, self.fill, self.count = src, dst, fill, count
+        self.most = src.numel() if isinstance(src, _Tensor) else 0
+        n = (self.most,)
+        self._hold(src, [(src, _I32, "copies.src", n), (dst, _I32, "copies.dst", n), (fill, _I32, "copies.fill", n),
+                         (count, _I32, "copies.count", (1,))])
+
+
+class KvFork(_Held):
+    """What kv_page_fork fills: table int32 [children][max_pages], seq_len int32 [children], head int32
+    [1], copies (a PageCopies with room for one of each child)."""
+    __slots__ = ("table", "seq_len", "head", "copies", "_table")
+    _names = ("table", "seq_len", "head", "copies")
+
+    def __init__(self, table, seq_len, head, copies):
+        self.table, self.seq_len, self.head, self.copies = table, seq_len, head, copies
+        self._hold(seq_len, [(seq_len, _I32, "seq_len (out)", None), (head, _I32, "head (out)", (1,))])
+        self._table = _table(table, seq_len.numel(), self._device)
+        if copies.fill is None or copies.most != seq_len.numel():
+            raise WswError("copies must have room for one copy of each child")
+        self._at += copies._on_device(self._device)
 
 
 def _page_copies(n, device, fill):
@@ -806,19 +847,16 @@ def kv_page_fork(parent, seq_len, free_pages, head, table, page_size, out=None, 
     rows = seq_len.numel()
     tp, width, row = _table(table, rows, dev)
     if out is None:
-        out = KvFork(table.new_full((n, width), -1), torch.empty_like(parent), torch.empty_like(head),
+        out = KvFork(table.new_full((n, width), -1), parent.new_empty(n), torch.empty_like(head),
                      _page_copies(n, parent.device, True))
-    op, out_width, out_row = _table(out.table, n, dev)
-    if out_width != width:
-        raise WswError("the new table must have as many entries in a row as the old one")
-    c = out.copies
+    lens_out, head_out, src, dst, fill, count = out._on_device(dev)
+    op, out_width, out_row = out._table
+    if out_width != width or out.copies.most != n:
+        raise WswError("the new table must be [children][max_pages], with the old one's max_pages")
     _check(load().wsw_kv_page_fork(
         pp, n, sp, rows, _packed(free_pages, _I32, "free_pages", dev), free_pages.numel(),
-        _packed(head, _I32, "head", dev, (1,)), page_size, tp, width, row, op, out_row,
-        _packed(out.seq_len, _I32, "seq_len (out)", dev, (n,)), _packed(out.head, _I32, "head (out)", dev, (1,)),
-        _packed(c.src, _I32, "copies.src", dev, (n,)), _packed(c.dst, _I32, "copies.dst", dev, (n,)),
-        _packed(c.fill, _I32, "copies.fill", dev, (n,)), _packed(c.count, _I32, "copies.count", dev, (1,)),
-        None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _raw_stream(dev), _opts(opts)),
+        _packed(head, _I32, "head", dev, (1,)), page_size, tp, width, row, op, out_row, lens_out, head_out, src, dst, fill,
+        count, None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _raw_stream(dev), _opts(opts)),
         "kv_page_fork")
     return out
 
@@ -827,27 +865,34 @@ def kv_page_copy(copies, caches, err_flag=None, opts=None):
     """Carries out copies (a PageCopies, as kv_page_fork and kv_page_compact give them) in each
     of caches, the PagedKV of every layer that shares the block table, in one launch for up to 32
     of them.  A copy that names a page outside a cache is left out there (err_flag, bit 0)."""
-    dev = _home(copies.src, "copies.src")
-    sp = _packed(copies.src, _I32, "copies.src", dev)
-    n = copies.src.numel()
+    dev = copies._device
+    if dev != _current_device():
+        _home(copies.src, "copies.src")
+    src, dst, fill, count = copies._at
     caches = (caches,) if isinstance(caches, PagedKV) else caches
     for kv in caches:
         if kv._device != dev:
             _elsewhere(kv, dev)
     refs = (_p * max(len(caches), 1))(*[kv._ref for kv in caches])
     _check(load().wsw_kv_page_copy(
-        sp, _packed(copies.dst, _I32, "copies.dst", dev, (n,)),
-        None if copies.fill is None else _packed(copies.fill, _I32, "copies.fill", dev, (n,)),
-        _packed(copies.count, _I32, "copies.count", dev, (1,)), n, refs, len(caches),
+        src, dst, fill, count, copies.most, refs, len(caches),
         None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _raw_stream(dev), _opts(opts)),
         "kv_page_copy")
 
 
-class KvCompact(NamedTuple):
-    table: torch.Tensor       # int32 [requests][max_pages]
-    free_pages: torch.Tensor  # int32 [num_pages]: the free ones from head on
-    head: torch.Tensor        # int32 [1]
-    copies: PageCopies        # room for max_moves whole pages
+class KvCompact(_Held):
+    """What kv_page_compact fills: table int32 [requests][max_pages], free_pages int32 [num_pages] (the free
+    ones from head, int32 [1], on), copies (a PageCopies with room for max_moves whole pages)."""
+    __slots__ = ("table", "free_pages", "head", "copies", "_table")
+    _names = ("table", "free_pages", "head", "copies")
+
+    def __init__(self, table, free_pages, head, copies):
+        self.table, self.free_pages, self.head, self.copies = table, free_pages, head, copies
+        self._hold(free_pages, [(free_pages, _I32, "free_pages", None), (head, _I32, "head", (1,))])
+        self._table = _table(table, table.shape[0] if isinstance(table, _Tensor) and table.dim() == 2 else -1, self._device)
+        if copies.fill is not None:
+            raise WswError("whole pages move: copies.fill must be None")
+        self._at += copies._on_device(self._device)
 
 
 def kv_page_compact_workspace_bytes(num_pages) -> int:
@@ -871,32 +916,31 @@ def kv_page_compact(seq_len, table, page_size, num_pages, held=None, max_moves=0
         out = KvCompact(table, torch.full((num_pages,), -1, dtype=torch.int32, device=seq_len.device),
                         torch.empty(1, dtype=torch.int32, device=seq_len.device),
                         _page_copies(max_moves, seq_len.device, False))
-    op, out_width, out_row = _table(out.table, n, dev)
-    if out_width != width:
-        raise WswError("the new table must have as many entries in a row as the old one")
-    c = out.copies
-    if c.fill is not None:
-        raise WswError("whole pages move: copies.fill must be None")
+    free_pages, head, src, dst, _, count = out._on_device(dev)
+    op, out_width, out_row = out._table
+    if out_width != width or out.table.shape[0] != n or out.free_pages.numel() != num_pages or out.copies.most != max_moves:
+        raise WswError("out must have a table of the old one's shape, num_pages free pages and max_moves copies")
     if ws is None:
         ws = torch.empty(kv_page_compact_workspace_bytes(num_pages), dtype=torch.uint8, device=seq_len.device)
     _check(load().wsw_kv_page_compact(
         sp, n, tp, width, row, page_size, num_pages,
-        None if held is None else _packed(held, _U8, "held", dev, (num_pages,)), max_moves, op, out_row,
-        _packed(out.free_pages, _I32, "free_pages", dev, (num_pages,)), _packed(out.head, _I32, "head", dev, (1,)),
-        _packed(c.src, _I32, "copies.src", dev, (max_moves,)), _packed(c.dst, _I32, "copies.dst", dev, (max_moves,)),
-        _packed(c.count, _I32, "copies.count", dev, (1,)),
-        None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev), _packed(ws, _U8, "ws", dev), ws.numel(),
-        _raw_stream(dev), _opts(opts)), "kv_page_compact")
+        None if held is None else _packed(held, _U8, "held", dev, (num_pages,)), max_moves, op, out_row, free_pages, head,
+        src, dst, count, None if err_flag is None else _packed(err_flag, _I32, "err_flag", dev),
+        _packed(ws, _U8, "ws", dev), ws.numel(), _raw_stream(dev), _opts(opts)), "kv_page_compact")
     return out
 
 
-class BeamStep(NamedTuple):
-    parent: torch.Tensor      # int32 [requests][beams]: rows of the logits
-    token: torch.Tensor       # int32 [requests][beams]
-    score: torch.Tensor       # fp32 [requests][beams]
-    end_parent: torch.Tensor  # the same of the candidates that end
-    end_token: torch.Tensor
-    end_score: torch.Tensor
+class BeamStep(_Held):
+    """What beam_select fills, each [requests][beams]: parent int32 (rows of the logits), token int32 and
+    score fp32 of the next beams, and the same of the candidates that end."""
+    __slots__ = ("parent", "token", "score", "end_parent", "end_token", "end_score", "_shape")
+    _names = ("parent", "token", "score", "end_parent", "end_token", "end_score")
+
+    def __init__(self, parent, token, score, end_parent, end_token, end_score):
+        self.parent, self.token, self.score = parent, token, score
+        self.end_parent, self.end_token, self.end_score = end_parent, end_token, end_score
+        self._shape = parent.shape if isinstance(parent, _Tensor) else None
+        self._hold(parent, [(t, _F32 if n.endswith("score") else _I32, n, self._shape) for n, t in zip(self._names, self)])
 
 
 def beam_select_workspace_bytes(requests, beams, vocab, ends=0) -> int:
@@ -931,12 +975,11 @@ def beam_select(logits, scores, end_tokens=(), scale=1.0, out=None, ws=None, opt
     if ws is None:
         ws = torch.zeros(beam_select_workspace_bytes(n, beams, vocab, len(end_tokens)), dtype=torch.uint8,
                          device=logits.device)
-    parent, token, score, end_parent, end_token, end_score = out
+    at = out._on_device(dev)
+    if out._shape != shape:
+        raise WswError("out must be [requests][beams] as scores")
     _check(load().wsw_beam_select(
-        logits.data_ptr(), code, n, beams, vocab, ld, sp, ends, len(end_tokens), scale,
-        _packed(parent, _I32, "parent", dev, shape), _packed(token, _I32, "token", dev, shape),
-        _packed(score, _F32, "score", dev, shape), _packed(end_parent, _I32, "end_parent", dev, shape),
-        _packed(end_token, _I32, "end_token", dev, shape), _packed(end_score, _F32, "end_score", dev, shape),
+        logits.data_ptr(), code, n, beams, vocab, ld, sp, ends, len(end_tokens), scale, *at,
         _packed(ws, _U8, "ws", dev), ws.numel(), _raw_stream(dev), _opts(opts)), "beam_select")
     return out
 
@@ -951,9 +994,9 @@ def attn_paged_prefix(q, kv, table, lens, groups, prefix, scale=None, softcap=0.
     group: requests groups[g] .. groups[g + 1] - 1 (int32 [n + 1], ascending) have the same keys
     and values at their first prefix[g] (int32 [n]) positions.  head_dim 64 or 128, no window; the
     other arguments and the result are attn_paged_decode's.  Small batches (128 MB of cached
-    positions by the table's size) go attn_paged_decode's way unless share is true.  ws: a uint8 device tensor of at least
-    attn_paged_prefix_workspace_bytes(...) bytes, zero-filled before its first use (every call
-    leaves it ready for the next), allocated if None."""
+    positions by the table's size) go attn_paged_decode's way unless share is true.  ws: a uint8
+    device tensor of at least attn_paged_prefix_workspace_bytes(...) bytes, zero-filled before its
+    first use (every call leaves it ready for the next), allocated if None."""
     code, dev = _float_dev(q, "q")
     if q.dim() != 3 or not q.is_contiguous():
         raise WswError("q must be a contiguous [requests][q_heads][head_dim] tensor")
