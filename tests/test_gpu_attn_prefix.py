@@ -314,3 +314,39 @@ def test_pieces_of_one_tile(q, cache, prefix):
     for _ in range(20):
         o, l = c.run()
         assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "q8_0"])
+def test_pages_far_into_a_large_cache(cache):
+    """Element offsets past 2^32 in K and V: the same result as in a small cache."""
+    wsw = need_gpu()
+    c = Case(wsw, [(600, _lens(600, 0, 30, 1))], kvh=8, group=4, page=256, q="bf16", cache=cache, junk=0.0)
+    want, want_lse = c.check()
+    pages = (1 << 32) // (256 * 8 * 128) + 2
+    few = c.kv.num_pages
+    small = [x for x in (c.kv.k, c.kv.v, c.kv.kd, c.kv.vd) if x is not None]
+    big = [torch.empty((pages + few,) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda") for x in small]
+    for b, x in zip(big, small):
+        b[pages:] = x
+    c.kv = wsw.PagedKV(*big)
+    c.table_d = torch.where(c.table_d >= 0, c.table_d + pages, c.table_d)
+    out, lse = c.run()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_two_streams_at_once():
+    """Each call with its own workspace: the results of calls alone."""
+    wsw = need_gpu()
+    cases = [Case(wsw, [(3000, _lens(3000, *range(24)))], kvh=4, group=8, q="bf16", cache="bf16", seed=s) for s in (1, 2)]
+    want = [c.run() for c in cases]
+    ws = [torch.zeros(wsw.attn_paged_prefix_workspace_bytes(24, 1, 32, 4, 128), dtype=torch.uint8, device="cuda") for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    qs = [c.q.cuda() for c in cases]
+    outs = [torch.empty_like(w[0]) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for c, q, o, w, s in zip(cases, qs, outs, ws, streams):
+            with torch.cuda.stream(s):
+                wsw.attn_paged_prefix(q, c.kv, c.table_d, c.lens_d, c.cu_d, c.prefix_d, out=o, ws=w, share=True)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w[0]) for o, w in zip(outs, want))

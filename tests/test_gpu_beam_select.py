@@ -169,3 +169,23 @@ def test_results_are_the_same_in_a_graph_and_on_another_stream():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_two_streams_at_once():
+    """Each call with its own workspace: the results of calls alone."""
+    wsw = need_gpu()
+    g = torch.Generator(device="cuda").manual_seed(0)
+    jobs = []
+    for n in (3, 70):
+        x, s = torch.randn(n * 4, 60000, generator=g, device="cuda") * 2, torch.zeros(n, 4, device="cuda")
+        want = [t.clone() for t in wsw.beam_select(x, s, [5])]
+        ws = torch.zeros(wsw.beam_select_workspace_bytes(n, 4, 60000, 1), dtype=torch.uint8, device="cuda")
+        jobs.append((x, s, want, ws, wsw.beam_select_out(n, 4), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for x, s, _, ws, out, stream in jobs:
+            with torch.cuda.stream(stream):
+                wsw.beam_select(x, s, [5], out=out, ws=ws)
+    torch.cuda.synchronize()
+    for _, _, want, _, out, _ in jobs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))

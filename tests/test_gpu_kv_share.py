@@ -274,3 +274,81 @@ def test_a_step_of_fork_copy_and_compact_replays_in_a_graph():
         table, seq, rows = plain(table, seq, par, rows)
         assert np.array_equal(tab.cpu().numpy(), table) and lens.tolist() == seq.tolist() and int(err) == 0
         assert torch.equal(full[0], rows)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8_0"])
+def test_copies_far_into_a_large_cache(kind):
+    """Element offsets past 2^32 in K and V."""
+    wsw = need_gpu()
+    page, heads, dim = 256, 8, 128
+    pages = (1 << 32) // (page * heads * dim) + 40
+    shape = (pages, page, heads, dim)
+    parts = [torch.empty(shape, dtype=torch.int8 if kind == "q8_0" else torch.bfloat16, device="cuda") for _ in range(2)]
+    if kind == "q8_0":
+        parts += [torch.empty(shape[:3] + (dim // 32,), dtype=torch.float16, device="cuda") for _ in range(2)]
+    src, dst, fill = [pages - 1, 3, pages - 2], [5, pages - 3, pages - 4], [page, 100, 7]
+    for x in parts:
+        for p in src + dst:
+            x[p] = torch.randint(-9, 9, x[p].shape, device="cuda").to(x.dtype)
+    want = [[x[d].clone() for d in dst] for x in parts]
+    for w, x in zip(want, parts):
+        for i, (s, n) in enumerate(zip(src, fill)):
+            w[i][:n] = x[s, :n]
+    err = _i32([0])
+    wsw.kv_page_copy(wsw.PageCopies(_i32(src), _i32(dst), _i32(fill), _i32([3])), wsw.PagedKV(*parts), err_flag=err)
+    assert int(err) == 0
+    for w, x in zip(want, parts):
+        assert all(torch.equal(a, x[d]) for a, d in zip(w, dst))
+
+
+@pytest.mark.parametrize("n,width", [(64, 300), (8192, 40), (3, 70000)])
+def test_tables_with_room_between_their_rows(n, width):
+    """Strided views of wider tables, whose other entries stay."""
+    wsw = need_gpu()
+    g = np.random.default_rng(n)
+    page = 4
+    wide_in, wide_out = g.integers(0, 10 ** 6, (n, width + 5)), np.full((n, width + 9), 55)
+    seq, parent = g.integers(0, width * page + 1, n), g.integers(-1, n, n)
+    free = np.arange(n) + 2 * 10 ** 6
+    want = ref.fork(parent, seq, free, 0, wide_in[:, 2:width + 2], page, wide_out[:, 3:width + 3])
+    t, o = _i32(wide_in), _i32(wide_out)
+    out = wsw.KvFork(o[:, 3:width + 3], _i32(np.zeros(n)), _i32([0]),
+                     wsw.PageCopies(*[_i32(np.zeros(n)) for _ in range(3)], _i32([0])))
+    wsw.kv_page_fork(_i32(parent), _i32(seq), _i32(free), _i32([0]), t[:, 2:width + 2], page, out=out)
+    got = o.cpu().numpy()
+    assert np.array_equal(got[:, 3:width + 3], want[0]) and (got[:, :3] == 55).all() and (got[:, width + 3:] == 55).all()
+    assert int(out.head) == want[2] and out.seq_len.tolist() == want[1].tolist()
+
+
+def test_the_largest_pool():
+    wsw = need_gpu()
+    g = np.random.default_rng(0)
+    pool = 1 << 22
+    table = g.permutation(pool)[:200 * 1000].reshape(200, 1000)
+    _compact(wsw, g.integers(0, 16001, 200), table, 16, pool, None, 1 << 20, True)
+
+
+def test_two_streams_at_once():
+    """Each with its own workspace and tensors."""
+    wsw = need_gpu()
+    g = np.random.default_rng(1)
+    pool, jobs = 50000, []
+    for i in range(2):
+        seq, table = g.integers(0, 8000, 64), g.permutation(pool)[:64 * 500].reshape(64, 500)
+        out = wsw.KvCompact(_i32(table), _i32(np.full(pool, -1)), _i32([0]),
+                            wsw.PageCopies(_i32(np.zeros(pool)), _i32(np.zeros(pool)), None, _i32([0])))
+        ws = torch.zeros(wsw.kv_page_compact_workspace_bytes(pool), dtype=torch.uint8, device="cuda")
+        jobs.append((seq, table, _i32(seq), _i32(table), out, ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for seq, table, seq_d, table_d, out, ws, stream in jobs:
+            with torch.cuda.stream(stream):
+                wsw.kv_page_compact(seq_d, table_d, 16, pool, max_moves=pool, out=out, ws=ws)
+    torch.cuda.synchronize()
+    for seq, table, _, _, out, _, _ in jobs:
+        want = ref.compact(seq, table, 16, pool, None, pool)
+        got = out.table.cpu().numpy()
+        for r, n in enumerate(seq):
+            k = ref.pages(int(n), 16)
+            assert np.array_equal(got[r, :k], want[0][r, :k])
+        assert int(out.head) == want[2] and out.free_pages.tolist()[want[2]:] == want[1]
