@@ -189,3 +189,17 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for _, _, want, _, out, _ in jobs:
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("vocab", [40, 30011])
+@pytest.mark.parametrize("beams,ends", [(1, 8), (2, 8), (4, 7), (8, 3), (10, 2), (16, 1)])
+def test_end_tokens_lead_every_row(vocab, beams, ends):
+    """The end tokens are each row's largest: all places of a request's first candidates may be theirs."""
+    wsw = need_gpu()
+    x = _logits(beams, 5, beams, vocab)
+    tokens = [(7 * i + 3) % vocab for i in range(ends)]
+    x[:3, :, tokens] += 15
+    x[3, :beams // 2 + 1, tokens] += 15
+    decided = _check(wsw, x, _scores(0, 5, beams), tokens)[1]
+    decided += _check(wsw, x, np.zeros((5, beams)), tokens + [vocab + 5] if ends < 8 and beams * (2 + ends) <= 32 else tokens)[1]
+    assert decided >= 2

@@ -3,8 +3,8 @@
 //   s[b][j] = score[b] + scale x[b][j] - lse_b,  lse_b = ln sum_i exp(scale x[b][i])
 //   the candidates (b, j) in order of s; the first `beams` that do not end become the beams
 //
-// Nothing beyond a row's k = beams * (1 + end tokens) largest logits can be chosen: an end token
-// takes one place in each row at most.  So a row is streamed once, as for its log probabilities
+// Nothing beyond a row's k = beams + end tokens largest logits can matter: an end token takes one place
+// in each row, and behind `beams` others nothing is chosen or reported.  So a row is streamed once, as for its log probabilities
 // (topk_rows.cuh), with its sum and its k best kept; rows are split over CTAs when there are few.
 // Each CTA leaves its part's maximum, sum and k best keys; the last CTA of a request merges the lists of
 // all its beams' parts: a score that enough candidates reach comes from the heads of the lists,
@@ -134,6 +134,13 @@ __device__ __forceinline__ void warp_total(const BeamArgs &a, float &m, Two &s) 
         s = s + Two{__shfl_xor_sync(WSW_FULL_MASK, s.h, d), __shfl_xor_sync(WSW_FULL_MASK, s.l, d)};
 }
 
+__device__ __forceinline__ bool is_end(const BeamArgs &a, int token) {
+    bool ends = false;
+#pragma unroll 1
+    for (int i = 0; i < a.n_ends; ++i) ends |= token == a.ends[i];
+    return ends;
+}
+
 // Each of the request's beams: score - ln S, its maximum and first key, from its parts.
 __device__ __forceinline__ void beam_sums(const BeamArgs &a, BeamShared &sm, const float *recs, int64_t request) {
     const int tid = threadIdx.x, lane = tid & 31;
@@ -218,12 +225,15 @@ __device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t
         }
         __syncthreads();
         if (d0 == 0) {
-            // a score that `want` candidates reach, from 32 candidates: the heads of 32 groups of lists,
-            // or the first few of fewer lists
+            // a score that `beams` candidates that do not end reach (what is below it is neither chosen nor
+            // reported), from 32 candidates: the heads of 32 groups of lists, or the first few of fewer lists
             const int depth = lists >= 32 ? 1 : min(32 / lists, some);
             uint64_t own = 0;
 #pragma unroll 1
-            for (int i = tid; i < lists * depth; i += kThreads) own = max(own, sm.score[i / depth * some + i % depth]);
+            for (int i = tid; i < lists * depth; i += kThreads) {
+                const int at = i / depth * some + i % depth;
+                if (!is_end(a, static_cast<int>(~static_cast<uint32_t>(keys[at])))) own = max(own, sm.score[at]);
+            }
             sm.group[warp][lane] = own;
             __syncthreads();
 #pragma unroll
@@ -234,7 +244,7 @@ __device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t
                 const uint64_t o = __shfl_sync(WSW_FULL_MASK, own, j);
                 more += o > own || (o == own && j < lane);
             }
-            thr = __shfl_sync(WSW_FULL_MASK, own, __ffs(__ballot_sync(WSW_FULL_MASK, more == want - 1)) - 1);
+            thr = __shfl_sync(WSW_FULL_MASK, own, __ffs(__ballot_sync(WSW_FULL_MASK, more == a.beams - 1)) - 1);
             thr = max(thr, static_cast<uint64_t>(1));  // 0: fewer candidates than that
         }
         // ---- the candidates that reach it, ranked
@@ -286,9 +296,7 @@ __device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t
     const bool there = lane < have;
     const int2 tag = there ? sm.tag[set][lane] : make_int2(0, 0);
     const int token = tag.y, row = static_cast<int>(out) + tag.x / a.splits;
-    bool ends = false;
-#pragma unroll 1
-    for (int i = 0; i < a.n_ends; ++i) ends |= there && token == a.ends[i];
+    const bool ends = there && is_end(a, token);
     const uint32_t alive = __ballot_sync(WSW_FULL_MASK, there && !ends), ended = __ballot_sync(WSW_FULL_MASK, ends && lane < a.beams);
     const uint32_t below = (1u << lane) - 1;
     const int at = __popc(alive & below), at_end = __popc(ended & below);
@@ -467,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
 // the counters' place does not depend on the sizes: one workspace serves calls of different sizes in turn
 constexpr size_t kCounterBytes = kMaxRequests * 4;
 
-int64_t list_length(int64_t want, int64_t vocab) { return want < vocab ? want : vocab; }
+int64_t list_length(int64_t beams, int64_t n_ends, int64_t vocab) { return beams + n_ends < vocab ? beams + n_ends : vocab; }
 
 }  // namespace
 }  // namespace wsw
@@ -479,7 +487,7 @@ extern "C" size_t wsw_beam_select_workspace_bytes(int64_t requests, int64_t beam
         n_ends < 0 || n_ends > kMaxEnds || beams * (1 + n_ends) > kMaxTop)
         return 0;
     int splits, chunk;
-    const int64_t rows = requests * beams, k = list_length(beams * (1 + n_ends), vocab);
+    const int64_t rows = requests * beams, k = list_length(beams, n_ends, vocab);
     split_rows(rows, vocab, &splits, &chunk);
     return kCounterBytes + static_cast<size_t>(rows) * splits * record_floats(k) * 4;
 }
@@ -524,7 +532,7 @@ extern "C" int wsw_beam_select(const void *logits, int32_t dtype, int64_t reques
     a.vocab = static_cast<int>(vocab);
     a.beams = static_cast<int>(beams);
     a.want = static_cast<int>(beams * (1 + n_ends));
-    a.k = static_cast<int>(list_length(a.want, vocab));
+    a.k = static_cast<int>(list_length(beams, n_ends, vocab));
     a.n_ends = static_cast<int>(n_ends);
     for (int64_t i = 0; i < n_ends; ++i) a.ends[i] = end_tokens[i];
     const int64_t rows = requests * beams;
