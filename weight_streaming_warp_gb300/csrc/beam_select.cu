@@ -105,7 +105,8 @@ struct BeamShared {
     uint64_t best[2][kMaxTop]; // the best so far, in order: scores, and their
     int2 tag[2][kMaxTop];      // lists and tokens; two sets in turn
     uint64_t head[kMaxBeams];  // each beam's largest logit's key
-    uint64_t group[kWarps][32];
+    alignas(16) uint32_t group[kThreads];
+    uint32_t reach;
     Two sum[kMaxBeams], base[kMaxBeams];
     float max[kMaxBeams], ln_s[kMaxBeams];
     int last, n;
@@ -226,25 +227,28 @@ __device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t
         __syncthreads();
         if (d0 == 0) {
             // a score that `beams` candidates that do not end reach (what is below it is neither chosen nor
-            // reported), from 32 candidates: the heads of 32 groups of lists, or the first few of fewer lists
-            const int depth = lists >= 32 ? 1 : min(32 / lists, some);
+            // reported), from a candidate a thread: the heads of 128 groups of lists, or the first few of fewer lists
+            const int depth = lists >= kThreads ? 1 : min(kThreads / lists, some);
             uint64_t own = 0;
 #pragma unroll 1
             for (int i = tid; i < lists * depth; i += kThreads) {
                 const int at = i / depth * some + i % depth;
                 if (!is_end(a, static_cast<int>(~static_cast<uint32_t>(keys[at])))) own = max(own, sm.score[at]);
             }
-            sm.group[warp][lane] = own;
+            // their order by a word each, whose last bits keep them apart: the bound is that much lower
+            static_assert(kThreads == 128, "seven bits");
+            const uint32_t word = (static_cast<uint32_t>(own >> 32) & ~127u) | (127 - tid);
+            sm.group[tid] = word;
             __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) own = max(own, sm.group[w][lane]);
             int more = 0;
 #pragma unroll 4
-            for (int j = 0; j < 32; ++j) {
-                const uint64_t o = __shfl_sync(WSW_FULL_MASK, own, j);
-                more += o > own || (o == own && j < lane);
+            for (int j = 0; j < kThreads / 4; ++j) {
+                const uint4 o = reinterpret_cast<const uint4 *>(sm.group)[j];
+                more += (o.x > word) + (o.y > word) + (o.z > word) + (o.w > word);
             }
-            thr = __shfl_sync(WSW_FULL_MASK, own, __ffs(__ballot_sync(WSW_FULL_MASK, more == a.beams - 1)) - 1);
+            if (more == a.beams - 1) sm.reach = word & ~127u;
+            __syncthreads();
+            thr = static_cast<uint64_t>(sm.reach) << 32;
             thr = max(thr, static_cast<uint64_t>(1));  // 0: fewer candidates than that
         }
         // ---- the candidates that reach it, ranked
