@@ -4,7 +4,7 @@ Tolerance.  A score's error, in units of the largest sum A = scale sum |q k| of 
 (exact in q's own type, for fp16 over bf16 and for fp32 over bf16 pages within a prefix; 2^-22 over binary16;
 2^-17 for fp32 or fp16 over bf16 in the rest, which the paged attention has, but exact there too under fp32),
 parts * head_dim / 16 + 2 fp32 sums and products (2^-23 each: tensor-core sums may cut), softcap's tanh
-(2^-22 of softcap), the slope's product and sum (2^-22 of slope distance), the exponential (2^-22).  A relative
+(7 2^-24 of softcap), the slope's product and sum (2^-22 of slope distance), the exponential (2^-22).  A relative
 error e of every weight moves an output by at most 2 e times its weighted magnitude M = sum w |v| / sum w.
 Under 16-bit queries a weight is rounded once, U = 2^-8 (bf16 cache) or 2^-11 of itself, and binary16 weights
 are off by 2^-32 of the largest (below their normal range), n 2^-32 max |v| in sum; under fp32 queries U = 2^-22 over
@@ -124,7 +124,7 @@ class Case:
             exact = self.qt == ("bf16" if half else "fp16") or wide and half
             parts = 3 if wide and half else 2 if wide or half and self.qt == "fp16" else 1
             e = a * ((0 if exact else 2.0 ** -17 if half else 2.0 ** -22) + (parts * self.d / 16 + 2) * 2.0 ** -23)
-            e += softcap * 2.0 ** -22 + (0 if fs is None else fs.max() * dist.max() * 2.0 ** -22) + 2.0 ** -22
+            e += softcap * 7 * 2.0 ** -24 + (0 if fs is None else fs.max() * dist.max() * 2.0 ** -22) + 2.0 ** -22
             u = (0 if half else 2.0 ** -22) if wide else 2.0 ** -8 if half else 2.0 ** -11
             sums = (len(p) / 16 * parts + 32 + 160) * 2.0 ** -23
             lim = mag * (2 * e + u + sums) + (0 if half else len(p) * 2.0 ** -32 * np.abs(v).max())
