@@ -190,13 +190,13 @@ __device__ __forceinline__ void beam_sums(const BeamArgs &a, BeamShared &sm, con
 // unrolled: of code that runs once, fetching is the larger part.)
 __device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t request) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k, want = a.want;
-    const int lists = a.beams * a.splits;  // at most kTargetCtas, or kMaxBeams
-    static_assert(kMaxBeams <= kThreads && kTargetCtas <= kCap, "keys in buf");
+    const int lists = a.beams * a.splits;  // at most kThreads
+    static_assert(kMaxBeams <= kThreads && 3 * kThreads <= kCap, "keys in buf");
     const float *recs = a.part + request * lists * a.rec;
     uint64_t *keys = sm.top.buf;
-    // the first keys of each list: three a thread, which is enough almost always
+    // the first keys of each list, three a thread
     constexpr int kEach = 3;
-    const int some = min(k, max(1, kEach * kThreads / lists)), here = lists * some;
+    const int some = min(k, kEach * kThreads / lists), here = lists * some;
     auto key_at = [&](int i, int d0) {
         const int list = i / some, d = d0 + i - list * some;
         return d < k ? __ldcg(reinterpret_cast<const uint64_t *>(recs + static_cast<int64_t>(list) * a.rec + 4) + d) : 0;
@@ -212,8 +212,6 @@ __device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t
 #pragma unroll
         for (int u = 0; u < kEach; ++u)
             if (tid + u * kThreads < here) keys[tid + u * kThreads] = got[u];
-#pragma unroll 1
-        for (int i = tid + kEach * kThreads; i < here; i += kThreads) keys[i] = key_at(i, d0);  // more lists than that
         __syncthreads();
 #pragma unroll 1
         for (int i = tid; i < here; i += kThreads) {
@@ -227,14 +225,10 @@ __device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t
         __syncthreads();
         if (d0 == 0) {
             // a score that `beams` candidates that do not end reach (what is below it is neither chosen nor
-            // reported), from a candidate a thread: the heads of 128 groups of lists, or the first few of fewer lists
-            const int depth = lists >= kThreads ? 1 : min(kThreads / lists, some);
+            // reported), from a candidate a thread, the first few of each list
+            const int depth = min(kThreads / lists, some), at = tid / depth * some + tid % depth;
             uint64_t own = 0;
-#pragma unroll 1
-            for (int i = tid; i < lists * depth; i += kThreads) {
-                const int at = i / depth * some + i % depth;
-                if (!is_end(a, static_cast<int>(~static_cast<uint32_t>(keys[at])))) own = max(own, sm.score[at]);
-            }
+            if (tid < lists * depth && !is_end(a, static_cast<int>(~static_cast<uint32_t>(keys[at])))) own = sm.score[at];
             // their order by a word each, whose last bits keep them apart: the bound is that much lower
             static_assert(kThreads == 128, "seven bits");
             const uint32_t word = (static_cast<uint32_t>(own >> 32) & ~127u) | (127 - tid);
@@ -479,6 +473,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
 // the counters' place does not depend on the sizes: one workspace serves calls of different sizes in turn
 constexpr size_t kCounterBytes = kMaxRequests * 4;
 
+// A row's splits: those of the log probabilities, but no more than 128 lists of a request, so that the merge
+// fetches three keys of each at once.  152064 fp32 logits with an end token, us with up to 608 lists and with 128: 1 x 4
+// 11.7 and 11.3, 1 x 8 19.2 and 15.6, 4 x 8 19.3 and 17.1, 1 x 16 31.6 and 29.3, 2 x 16 35.0 and 35.5 (64 lists: 13.0,
+// 18.5, 19.3, 31.7 and 33.1).
+void beam_splits(int64_t rows, int64_t beams, int64_t vocab, int *splits, int *chunk) {
+    split_rows(rows, vocab, splits, chunk);
+    const int64_t most = kThreads / beams;  // 4 at least
+    if (*splits <= most) return;
+    const int64_t ch = ((vocab + most - 1) / most + 31) / 32 * 32;
+    *chunk = static_cast<int>(ch);
+    *splits = static_cast<int>((vocab + ch - 1) / ch);
+}
+
 int64_t list_length(int64_t beams, int64_t n_ends, int64_t vocab) { return beams + n_ends < vocab ? beams + n_ends : vocab; }
 
 }  // namespace
@@ -492,7 +499,7 @@ extern "C" size_t wsw_beam_select_workspace_bytes(int64_t requests, int64_t beam
         return 0;
     int splits, chunk;
     const int64_t rows = requests * beams, k = list_length(beams, n_ends, vocab);
-    split_rows(rows, vocab, &splits, &chunk);
+    beam_splits(rows, beams, vocab, &splits, &chunk);
     return kCounterBytes + static_cast<size_t>(rows) * splits * record_floats(k) * 4;
 }
 
@@ -540,7 +547,7 @@ extern "C" int wsw_beam_select(const void *logits, int32_t dtype, int64_t reques
     a.n_ends = static_cast<int>(n_ends);
     for (int64_t i = 0; i < n_ends; ++i) a.ends[i] = end_tokens[i];
     const int64_t rows = requests * beams;
-    split_rows(rows, vocab, &a.splits, &a.chunk);
+    beam_splits(rows, beams, vocab, &a.splits, &a.chunk);
     a.rec = record_floats(a.k);
     unsigned char *w = static_cast<unsigned char *>(ws);
     a.cnt = reinterpret_cast<unsigned *>(w);
