@@ -350,3 +350,12 @@ def test_two_streams_at_once():
                 wsw.attn_paged_prefix(q, c.kv, c.table_d, c.lens_d, c.cu_d, c.prefix_d, out=o, ws=w, share=True)
     torch.cuda.synchronize()
     assert all(torch.equal(o, w[0]) for o, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("groups", [1, 15, 16, 17, 20, 60, 160, 5000])
+@pytest.mark.parametrize("q,cache", [("bf16", "bf16"), ("fp32", "fp16")])
+def test_short_tables_of_many_groups(groups, q, cache):
+    """Fewer tiles than SMs, whose pieces still have their places in the list."""
+    c = Case(need_gpu(), [(20 + g % 13, _lens(20 + g % 13, 0, 2)) for g in range(groups)], kvh=1, group=1, d=64, q=q, cache=cache)
+    assert c.table.shape[1] * c.page <= 64
+    c.check()

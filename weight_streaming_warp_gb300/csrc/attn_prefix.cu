@@ -365,8 +365,8 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     a.q_heads = rest.q_heads; a.group = rest.group; a.groups = p.groups; a.max_len = rest.max_len;
     a.dtype = dtype;
     a.negative = scale < 0.f;
-    const int64_t most = units * longest;
-    const int ctas = static_cast<int>(most < kCtas ? (most < 1 ? 1 : most) : kCtas);
+    const int64_t most = units * (longest + kPiece);  // places of the list
+    const int ctas = static_cast<int>(most < kCtas ? most : kCtas);
     if (cache->dtype == WSW_F16) e = launch_prefix<WSW_F16>(a, rt, s, ctas);
     else if (cache->dtype == WSW_BF16) e = launch_prefix<WSW_BF16>(a, rt, s, ctas);
     else e = launch_prefix<WSW_Q8_0>(a, rt, s, ctas);
