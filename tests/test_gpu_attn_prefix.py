@@ -102,7 +102,19 @@ class Case:
         return out, lse
 
     def check(self, scale=None, softcap=0.0, slopes=None, hidden=None, **kw):
-        """hidden: {request: positions that a bad table entry hides}."""
+        """hidden: {request: positions that a bad table entry hides}.  Where a group's rows would fill two row tiles, a
+        second time in a table with room for rows so long that they do."""
+        rows, narrow = len(self.lens) * self.group, self.table_d
+        if rows > 128 * len(self.prefix) and kw.get("share", True):
+            width = (21 * 152 * 128 // (self.kvh * (rows // 128)) + 128) // self.page + 1
+            if width > narrow.shape[1]:
+                self.table_d = torch.full((len(self.lens), width), -1, dtype=torch.int32, device="cuda")
+                self.table_d[:, :narrow.shape[1]] = narrow
+                self._check(scale, softcap, slopes, hidden, **kw)
+                self.table_d = narrow
+        return self._check(scale, softcap, slopes, hidden, **kw)
+
+    def _check(self, scale, softcap, slopes, hidden, **kw):
         scale = 1 / math.sqrt(self.d) if scale is None else scale
         sl = None if slopes is None else torch.tensor(slopes, dtype=torch.float32, device="cuda")
         out, lse = self.run(scale, softcap=softcap, slopes=sl, **kw)
@@ -359,3 +371,12 @@ def test_short_tables_of_many_groups(groups, q, cache):
     c = Case(need_gpu(), [(20 + g % 13, _lens(20 + g % 13, 0, 2)) for g in range(groups)], kvh=1, group=1, d=64, q=q, cache=cache)
     assert c.table.shape[1] * c.page <= 64
     c.check()
+
+
+@pytest.mark.parametrize("q,cache,d", [("bf16", "bf16", 128), ("fp16", "fp16", 64), ("bf16", "q8_0", 128)])
+def test_both_row_tilings(q, cache, d):
+    """More than 128 rows of a group, with cap, slopes and a negative scale."""
+    c = Case(need_gpu(), [(700, _lens(700, *range(40))), (1300, _lens(1300, *range(3)))], kvh=2, group=8, d=d, q=q, cache=cache)
+    c.check()
+    c.check(-0.2, softcap=20.0)
+    c.check(softcap=30.0, slopes=[2.0 ** -(i % 8 + 1) for i in range(16)])

@@ -23,16 +23,25 @@ namespace {
 constexpr int kMaxGroups = 16384;  // three words of shared memory each
 constexpr int kPlanThreads = 1024;
 constexpr int64_t kEachBytes = int64_t(128) << 20;
-constexpr int kPiece = 7;           // tiles
-constexpr int kSingleGroups = 16;   // groups for which the cut into single pieces is looked for
+// Tiles that a piece costs.  16 x 4 requests of 4 x 8 heads behind 4096 positions, bf16: 55 us with none, 53 with 3, 51 with 7 and 14;
+// 1 x 256 behind 8192, q8_0: 84, 81, 78, 80.  (CTAs with a single piece each, where there are enough for that: 16 x 4 51 us, 45
+// without, for the longer plan alone 3 us.)
+constexpr int kPiece = 7;
 
 // Parts of q by types.
 int q_parts(int dtype, int cache) {
     if (dtype == WSW_F32) return cache == WSW_BF16 ? 3 : 2;
     return dtype == WSW_F16 && cache == WSW_BF16 ? 2 : 1;
 }
-int row_tiles(int64_t requests, int64_t group, int64_t groups, int parts) {
-    return parts == 1 && requests * group > 128 * groups ? 2 : 1;
+// Row tiles of a unit.  Two read K and V half as often, for groups of more than 128 rows a head (several parts of q would leave
+// no room for the ring), but an SM's two slots then work on one tile: they pay from some kRowTiles tiles of 128 rows and
+// 128 positions for each SM.  4 heads of 128, bf16, group 8, us with one and with two: 32 requests behind 8192 / 32768
+// positions 29 / 46 and 35 / 54 (3 / 13 tiles), 64 behind 32768 59.5 and 58.8 (27), 128 behind 8192 / 16384 / 32768 38 / 55 / 88
+// and 40 / 52 / 77 (13 / 27 / 54), 256 behind 32768 152 and 123 (108).
+constexpr int kRowTiles = 20;
+int row_tiles(int64_t requests, int64_t group, int64_t groups, int parts, int64_t heads, int64_t max_len) {
+    const int64_t rows = requests * group;
+    return parts == 1 && rows > 128 * groups && heads * (rows / 128) * (max_len / 128) > kRowTiles * kCtas ? 2 : 1;
 }
 
 struct PlanArgs {
@@ -98,30 +107,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const Plan
             sum += a.heads * units(g) * tiles(g);
         }
     }
-    // ---- the list.  A piece of a unit costs its CTA kPiece tiles beside its own: either units have as many
-    // places more, or (few groups) a CTA has one piece alone, of `run` tiles at most: the least of 32 lengths for
-    // which there are CTAs enough.
+    // ---- the list: a piece of a unit costs its CTA kPiece tiles beside its own (start, queries, its sums' way out), so
+    // that units have as many places more
     int total, all_units;
     block_scan(sum, 0x7fffffff, scan_sm, &total);
     block_scan(count, 0x7fffffff, scan_sm, &all_units);
     int run = (total + kPiece * all_units + kCtas - 1) / kCtas;
-    bool single = false;
-    if (a.groups <= kSingleGroups) {  // every warp works it out
-        const int least = (total + kCtas - 1) / kCtas, mine = max(least + lane * max(least / 16, 1), 1);
-        int ctas = 0;
-        for (int g = 0; g < a.groups; ++g)
-            if (used[g] > 0) ctas += a.heads * units(g) * ((tiles(g) + mine - 1) / mine);
-        const uint32_t fit = __ballot_sync(WSW_FULL_MASK, ctas <= kCtas);
-        const int one = __shfl_sync(WSW_FULL_MASK, mine, fit ? __ffs(fit) - 1 : 0);
-        if (fit && one <= run) {
-            run = one;
-            single = true;
-        }
-    }
     run = max(run, 1);
-    auto stride = [&](int g) {
-        return used[g] == 0 ? 0 : single ? (tiles(g) + run - 1) / run * run : tiles(g) + kPiece;
-    };
+    auto stride = [&](int g) { return used[g] == 0 ? 0 : tiles(g) + kPiece; };
     sum = 0;
     for (int g = g0; g < g1; ++g) sum += a.heads * units(g) * stride(g);
     int at = block_scan(sum, 0x7fffffff, scan_sm, &total);
@@ -135,7 +128,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const Plan
         a.off[a.groups] = total;
         a.begin[a.groups] = begin[a.groups];
         a.run[0] = run;
-        a.run[1] = single;
     }
     if (err && a.err) atomicOr(a.err, err);
     __syncthreads();
@@ -167,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const Plan
 }
 
 struct JoinArgs {
-    const int *run;      // [2] places of a CTA, whether it has single pieces
+    const int *run;      // [1] places of a CTA
     const int4 *pieces;  // [requests]: query rows of its group per KV head, its own ones' place there, the group's place
                          // in the list, its prefix's positions
     const float *rec, *whole;
@@ -201,7 +193,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const JoinArgs a) {
         const int unit_rows = 1 << a.row_shift, nt = ((of.w - 1) >> a.tile_shift) + 1;
         const int kv = head / a.group, in = of.y + head - kv * a.group;
         const int unit = kv * (((of.x - 1) >> a.row_shift) + 1) + (in >> a.row_shift);
-        const int stride = a.run[1] ? (nt + run - 1) / run * run : nt + kPiece;
+        const int stride = nt + kPiece;
         const int first = of.z + unit * stride, c0 = first / run, c1 = (first + nt - 1) / run;
         const int n = c1 - c0 + 1;
         // piece k: a unit that one CTA has whole, or of CTA c0 + k its last piece (k = 0) or its first
@@ -264,10 +256,10 @@ struct Room {
 Room room(int64_t requests, int64_t groups, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
     Room w;
     const size_t rows = static_cast<size_t>(requests) * q_heads, rec = static_cast<size_t>(head_dim + kHead) * 4;
-    // two row tiles by the rule for one part of q: the most that any types need
-    const int rt = row_tiles(requests, q_heads / kv_heads, groups, 1);
+    // the most that any types and lengths need
+    const int rt = row_tiles(requests, q_heads / kv_heads, groups, 1, kv_heads, int64_t(1) << 31);
     w.plan = align256(wsw_attn_paged_decode_workspace_bytes(requests, q_heads, kv_heads, head_dim));
-    w.rec = w.plan + align256((2 * kCtas + 4 * static_cast<size_t>(requests) + 5 * (static_cast<size_t>(groups) + 1) + 2 +
+    w.rec = w.plan + align256((2 * kCtas + 4 * static_cast<size_t>(requests) + 5 * (static_cast<size_t>(groups) + 1) + 1 +
                                static_cast<size_t>(requests)) * 4);
     w.whole = w.rec + static_cast<size_t>(kCtas) * 2 * rt * 128 * rec;
     w.rest = w.whole + align256(rows * rec);
@@ -332,7 +324,7 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     if (!share && requests * static_cast<int64_t>(rest.max_len) <= kEachBytes / row_bytes)
         return paged::launch_paged(rest, cache->dtype, rows, list, s, o.pdl) == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;
 
-    const int rt = row_tiles(requests, group, groups, q_parts(dtype, cache->dtype));
+    const int rt = row_tiles(requests, group, groups, q_parts(dtype, cache->dtype), kv_heads, rest.max_len);
     PlanArgs p;
     p.cu = cu_groups; p.prefix = prefix_len; p.lens = lens; p.err = err_flag;
     p.pieces = reinterpret_cast<int4 *>(base + w.plan);
@@ -343,7 +335,7 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     p.rep = p.used + groups + 1;
     p.stride = p.rep + groups + 1;
     p.run = p.stride + groups + 1;
-    p.first = p.run + 2;
+    p.first = p.run + 1;
     p.requests = rest.requests; p.groups = static_cast<int>(groups); p.max_len = rest.max_len;
     p.heads = rest.kv.heads; p.group = rest.group; p.unit_rows = 128 * rt; p.tile = tile_positions(dtype == WSW_F32 ? 2 : 1, cache->dtype, rt);
     const int plan_smem = static_cast<int>((3 * groups + 1) * 4);
