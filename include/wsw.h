@@ -785,9 +785,9 @@ int wsw_beam_select(const void *logits, int32_t dtype, int64_t requests, int64_t
  * one request, and a request outside all groups are attended as wsw_attn_paged_decode does.
  *
  * A prefix's products run on the tensor cores with fp32 sums.  Under 16-bit queries the softmax
- * weights are rounded to the cache's 16-bit type (binary16 for q8_0), 2^-9 (bf16) or 2^-12 of each
- * at most on average half of that; under fp32 queries they and q keep 22 bits over binary16 and q8_0 and
- * all 24 over bf16, as there.
+ * weights are rounded to the cache's 16-bit type (binary16 for q8_0), by 2^-8 (bf16) or 2^-11 of each
+ * at most; under fp32 queries they and q keep 22 bits over binary16 and q8_0 and all 24 over bf16, as
+ * there.  softcap's tanh is off by 7 2^-24 at most.
  *
  *   cu_groups   int32 [groups + 1], ascending within [0, requests];  prefix_len int32 [groups], within
  *               [0, max_pages * page_size].  A bound that is not is moved to the nearest one that is,

@@ -306,7 +306,7 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
         (reinterpret_cast<uintptr_t>(ws) & 255))
         return WSW_ERR_MISALIGNED;
     const int64_t kv_heads = cache->heads, group = rest.group;
-    // the longest list: tiles are counted in 32 bits
+    // the longest list, of tiles of 64 positions or more: places are counted in 32 bits
     const int64_t units = kv_heads * (requests * group / 128 + groups), longest = (rest.max_len + 63) / 64;
     if (requests * q_heads > (int64_t(1) << 30) || units * (4 * longest + kPiece + 1) >= (int64_t(1) << 31) - 65536)
         return WSW_ERR_UNSUPPORTED;
@@ -318,8 +318,9 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     unsigned char *base = static_cast<unsigned char *>(ws);
     paged::place(&rest, ws, rows);
     // What all requests list of a prefix comes from HBM once anyhow while it stays in L2, and four launches cost 9 us
-    // more than one: 4 heads of 128, bf16, group 8, one prefix of 8192 for 8 / 16 requests (135 / 271 MB in all) 33 / 34 us
-    // shared and 27 / 40 each on its own; 16 prefixes of 1024 for 4 each (143 MB) 27 and 29.
+    // more than one: 4 heads of 128, bf16, group 8, one prefix of 8192 for 4 / 8 / 16 requests (68 / 135 / 271 MB in all) 29 /
+    // 30 / 31 us shared and 21 / 27 / 40 each on its own; 16 prefixes of 1024 / 2048 for 4 each (143 / 277 MB) 28 / 32 and 28.5 /
+    // 42; fp32 over q8_0, 8 requests behind 8192 (72 MB) 41 and 31.
     const int64_t row_bytes = 2 * kv_heads * (cache->dtype == WSW_Q8_0 ? cache->head_dim * 17 / 16 : cache->head_dim * 2);
     if (!share && requests * static_cast<int64_t>(rest.max_len) <= kEachBytes / row_bytes)
         return paged::launch_paged(rest, cache->dtype, rows, list, s, o.pdl) == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;

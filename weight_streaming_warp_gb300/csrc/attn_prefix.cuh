@@ -8,27 +8,32 @@
 //
 // The query heads of all of a group's requests that share a KV head are the rows of one product:
 // 4 D flops per row and position against 4 D bytes (16 bits) per position, so that a few hundred rows are
-// bound by the tensor cores, a few by HBM.
+// bound by the tensor cores, a few by HBM.  256 requests of 4 x 8 heads behind 32768 positions, bf16: 95 us of this
+// kernel, 1.4 PFLOP/s; a tile of 128 rows and 128 positions takes 3100 cycles where its products take 2048: the two
+// slots' softmax (one exponential for each score, 16 a cycle) and products do not overlap all the time.
 //
 //  * A unit is a tile of rows (kv head, 128 or 256 of a group's rows); the position tiles of all units,
-//    in order, are one list that is cut into equal runs for 152 CTAs, one on an SM.  A CTA leaves
+//    in order, are one list that is cut into equal runs for 152 CTAs, one on an SM (attn_prefix.cu has the rules).  A CTA leaves
 //    (m, l, O) of each piece of a unit; pieces are joined in tile order, so that results depend on
 //    the sizes alone.
 //  * Two softmax warpgroups, a thread for each row, each with its own scores S and value sums O in
-//    tensor memory.  With more than 128 rows in a group they have 128 rows each and the same K and V
-//    (half the reads); else the same rows, and take the tiles in turn; their sums are joined
-//    when the piece ends.  One's softmax runs while the tensor cores work for the other.
+//    tensor memory.  With two row tiles in a unit they have 128 rows each and the same K and V (half the
+//    reads); with one the same rows, and take the tiles in turn; their sums are joined when the
+//    piece ends.  One's softmax runs while the tensor cores work for the other.
 //  * The weights P go back to tensor memory over the scores, whose thread has read them; S of the next
-//    tile is issued behind the P V that reads them, and one thread's MMAs complete in order.
+//    tile is issued behind the P V that reads them, and one thread's MMAs complete in order.  The P V of a tile's
+//    first half runs while the second half's weights are made (170 us for the case above without, 162 with).
 //  * Four warps copy K and V rows with cp.async into a ring of tiles, swizzled as the MMAs want them:
 //    16-byte pieces by the block table, so that any page size, layout and stride is the same code (a TMA box
-//    cannot cross a page, and pages may have one position).  q8_0 codes become binary16(scale * code)
-//    on the way.  A tile's barrier counts the threads whose copies have landed.
+//    cannot cross a page, and pages may have one position).  Over q8_0 four warps have K and four have V: codes
+//    and scales land in rings of their own, two or three tiles deep, and become binary16(scale * code) on the way to the
+//    tile (33 fp32 requests of 4 x 8 heads behind 32768 positions: 117 us with one set of loaders, 101 so).  A tile's
+//    barrier counts the threads whose copies have landed.
 //  * q, scores, sums and l are fp32 or parts: q over its own 16-bit type is exact, a bf16 or fp32 row
 //    over binary16 takes the power of two that brings its largest value to 2^14 .. 2^15 and, fp32, a second
 //    part (22 bits); fp16 over bf16 is two parts, fp32 over bf16 three, both exact.  Under 16-bit queries P is
-//    rounded to the cache's 16-bit type: 2^-9 (bf16) or 2^-12 of each weight against the result's own
-//    rounding of 2^-9 or 2^-12; under fp32 queries P is two (binary16) or three (bf16) parts.
+//    rounded to the cache's 16-bit type: 2^-8 (bf16) or 2^-11 of each weight at most, as the result's own
+//    rounding; under fp32 queries P is two (binary16) or three (bf16) parts.
 //  * The maximum in use is raised, and O rescaled, only when a tile exceeds it by more than kLazy.
 //  * Every wait is bounded; a role whose wait ran out stops, and the rows' l is NaN.
 #pragma once
@@ -658,19 +663,6 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                     if (a.dtype != WSW_F16) {
                         if (RT == 1) asm volatile("bar.sync 1, 256;" ::: "memory");
                         unit *= ct.unit[(RT == 2 ? slot * 128 : 0) + r];
-                    }
-                }
-            }
-            // the next piece's queries into L1 before its tiles fill the way to memory
-            {
-                Walk<C> nx = w;
-                if (nx.next()) {
-                    const int rows = min(nx.rows - nx.tile * RT * 128, RT * 128), row_bytes = D * (a.dtype == WSW_F32 ? 4 : 2);
-                    const int lines = row_bytes / 128;
-                    for (int i = tid; i < rows * lines; i += 256) {
-                        const int in = nx.tile * RT * 128 + i / lines;
-                        const int64_t h = static_cast<int64_t>(nx.begin + in / a.group) * a.q_heads + nx.head * a.group + in % a.group;
-                        asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const unsigned char *>(a.q) + h * row_bytes + i % lines * 128));
                     }
                 }
             }

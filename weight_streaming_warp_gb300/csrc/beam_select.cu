@@ -21,7 +21,8 @@
 // other: they share the first one's, so that they tie and rank by index.
 //
 // Bound: the logits once; as the log probabilities with alternatives, by the selection's dependent steps
-// for few rows and by instructions for 16-bit logits.
+// for few rows (1 x 4 x 152064 fp32 10.9 us; the logits alone are 0.4) and by instructions and the selection's
+// barriers for many (60 x 10 x 50021 bf16 25 us, 2.4 TB/s; 150 x 4 x 50000 fp32 34 us, 3.5 TB/s).
 #include "topk_rows.cuh"
 
 namespace wsw {

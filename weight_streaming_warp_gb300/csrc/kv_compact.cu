@@ -14,7 +14,8 @@
 // takes 32 pages at a time, a lane each, so that ranks are ballots; with the counts of live, moving and
 // filled pages before a page its place in the free list needs no scan of its own: p - live + moved -
 // filled pages lie below it.  The CTAs exchange their counts through the workspace, a barrier
-// of the cluster (1 us) for each exchange.
+// of the cluster (1 us) for each exchange.  Bound: these dependent steps (64 rows of 380 entries, freeing only, 9.6 us;
+// 40 rows of 88 entries with their moves 14 us under a profiler's serialised launches).
 #include "kv_rows.cuh"
 
 namespace wsw {

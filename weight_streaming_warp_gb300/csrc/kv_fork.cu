@@ -184,7 +184,7 @@ extern "C" int wsw_kv_page_fork(const int32_t *parent, int64_t children, const i
     a.n_free = static_cast<int>(n_free); a.max_pages = static_cast<int>(max_pages);
     a.shift = 0;
     while ((int64_t(1) << a.shift) < page_size) ++a.shift;
-    // a sector of 8 entries wide, so that there are many tiles (64 x 8 rows of 130 pages: ___ us, lines of 32 16 us),
+    // a sector of 8 entries wide, so that there are many tiles (64 x 8 rows of 130 pages: 8.1 us, lines of 32 16 us),
     // and narrower for many rows
     const int64_t words = 3 * children + requests;
     a.col_shift = 3;
