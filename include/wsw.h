@@ -784,10 +784,9 @@ int wsw_beam_select(const void *logits, int32_t dtype, int64_t requests, int64_t
  * with lens[r] >= prefix_len[g]; a shorter request (or an unused row of length 0), a group of
  * one request, and a request outside all groups are attended as wsw_attn_paged_decode does.
  *
- * A prefix's products run on the tensor cores with fp32 sums.  Under 16-bit queries the softmax
- * weights are rounded to the cache's 16-bit type (binary16 for q8_0), by 2^-8 (bf16) or 2^-11 of each
- * at most; under fp32 queries they and q keep 22 bits over binary16 and q8_0 and all 24 over bf16, as
- * there.  softcap's tanh is off by 7 2^-24 at most.
+ * A prefix's products run on the tensor cores with fp32 sums.  The softmax weights keep 22 bits over
+ * binary16 and q8_0 and 16 over bf16 (under fp32 queries all 24), as there; q keeps 22 bits over binary16 and
+ * q8_0 (its own binary16 all of them), and all of them over bf16.  softcap's tanh is off by 7 2^-24 at most.
  *
  *   cu_groups   int32 [groups + 1], ascending within [0, requests];  prefix_len int32 [groups], within
  *               [0, max_pages * page_size].  A bound that is not is moved to the nearest one that is,

@@ -338,7 +338,7 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     p.run = p.stride + groups + 1;
     p.first = p.run + 1;
     p.requests = rest.requests; p.groups = static_cast<int>(groups); p.max_len = rest.max_len;
-    p.heads = rest.kv.heads; p.group = rest.group; p.unit_rows = 128 * rt; p.tile = tile_positions(dtype == WSW_F32 ? 2 : 1, cache->dtype, rt);
+    p.heads = rest.kv.heads; p.group = rest.group; p.unit_rows = 128 * rt; p.tile = tile_positions(dtype == WSW_F32, cache->dtype, rt);
     const int plan_smem = static_cast<int>((3 * groups + 1) * 4);
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(prefix_plan_kernel), (3 * kMaxGroups + 1) * 4);
     if (e == cudaSuccess)

@@ -31,9 +31,11 @@
 //    barrier counts the threads whose copies have landed.
 //  * q, scores, sums and l are fp32 or parts: q over its own 16-bit type is exact, a bf16 or fp32 row
 //    over binary16 takes the power of two that brings its largest value to 2^14 .. 2^15 and, fp32, a second
-//    part (22 bits); fp16 over bf16 is two parts, fp32 over bf16 three, both exact.  Under 16-bit queries P is
-//    rounded to the cache's 16-bit type: 2^-8 (bf16) or 2^-11 of each weight at most, as the result's own
-//    rounding; under fp32 queries P is two (binary16) or three (bf16) parts.
+//    part (22 bits); fp16 over bf16 is two parts, fp32 over bf16 three, both exact.  P is two parts, 16 (bf16) or 22 bits
+//    (binary16), under fp32 queries over bf16 three, as in attn_paged.cuh, so that which of the two kernels attends
+//    a position does not show in the result.  (With one part the weights' rounding was as large as a bf16 result's
+//    own, 2.3e-3 in the root mean square instead of 1.7e-3; the call for the case above, with rests of 16
+//    positions, took 155 us with one part and 187 so.)
 //  * The maximum in use is raised, and O rescaled, only when a tile exceeds it by more than kLazy.
 //  * Every wait is bounded; a role whose wait ran out stops, and the rows' l is NaN.
 #pragma once
@@ -86,10 +88,9 @@ struct Args {
     int dtype, negative;  // of q; scale < 0
 };
 
-// Positions of a tile.  Several parts of P: 64, whose scores a thread keeps while the parts overwrite
-// them; q8_0 under two row tiles: 64, for room.
-constexpr int tile_positions(int p_parts, int cache, int row_tiles) {
-    return p_parts == 1 && !(cache == WSW_Q8_0 && row_tiles == 2) ? 128 : 64;
+// Positions of a tile.  fp32 queries and q8_0 under two row tiles: 64, for room.
+constexpr int tile_positions(bool wide, int cache, int row_tiles) {
+    return !wide && !(cache == WSW_Q8_0 && row_tiles == 2) ? 128 : 64;
 }
 
 // cap tanh(x) of v = 2 log2(e) x:  1 - 2 / (1 + e^2|x|) with x's sign.  Off by 7 2^-24 of cap at most: the power's 2^-22
@@ -103,12 +104,14 @@ __device__ __forceinline__ float capped(float v, float cap) {
     return copysignf(fmaf(-2.f * cap, r, cap), v);
 }
 
-// Shape of one variant: cache type, head_dim, parts of q and of P, row tiles of a unit.
-template <int CT, int D_, int QP_, int PP_, int RT_>
+// Shape of one variant: cache type, head_dim, parts of q, row tiles of a unit.
+template <int CT, int D_, int QP_, int RT_>
 struct Cfg {
-    static constexpr int D = D_, QP = QP_, PP = PP_, RT = RT_;
+    static constexpr int D = D_, QP = QP_, RT = RT_;
     static constexpr bool q8 = CT == WSW_Q8_0, bf16 = CT == WSW_BF16;
-    static constexpr int TP = tile_positions(PP, CT, RT);
+    static constexpr bool wide = QP == (bf16 ? 3 : 2);     // fp32 queries
+    static constexpr int PP = QP == 3 ? 3 : 2;             // parts of P
+    static constexpr int TP = tile_positions(wide, CT, RT);
     static constexpr int stage = TP * D * 2;               // a K or V tile
     static constexpr int q_part = 128 * D * 2;             // of a row tile
     static constexpr int q_bytes = RT * QP * q_part;
@@ -117,7 +120,13 @@ struct Cfg {
     static constexpr int fit = (kTileBytes - q_bytes - 2 * raw_stages * raw) / stage;
     static constexpr int stages = fit < 8 ? fit : 8;
     static constexpr int ahead = RT == 1 ? 2 : 1;          // K tiles before their V tiles
-    static constexpr int s_cols = PP == 3 ? 96 : TP;       // of a slot: scores, then P's parts
+    // of a slot: scores, then P's parts.  Two parts of 32 weights take the place of their own scores, side by side; three
+    // take more, and all scores' places, which a thread keeps meanwhile.
+    static constexpr int s_cols = PP == 3 ? 96 : TP;
+    // the column of part k of the weights of 16 positions, of P's first
+    static constexpr int p_col(int k, int sixteen) {
+        return PP == 3 ? k * (TP / 2) + 8 * sixteen : (sixteen >> 1) * 32 + 16 * k + 8 * (sixteen & 1);
+    }
     static constexpr uint32_t o_col = 2 * s_cols;
     static constexpr float shift = bf16 ? -kLazy : 7.f;    // log2 of the weights' scale
     static constexpr int rec = D + kHead;
@@ -244,11 +253,11 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c, int rows) {
     return static_cast<uint32_t>((c >> 3) * rows * 128 + r * 128 + ((c & 7) ^ (r & 7)) * 16);
 }
 
-template <int CT, int D, int QP, int PP, int RT>
-__global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefix_kernel(const __grid_constant__ Args a) {
+template <int CT, int D, int QP, int RT>
+__global__ void __launch_bounds__(Cfg<CT, D, QP, RT>::threads, 1) attn_prefix_kernel(const __grid_constant__ Args a) {
     using namespace tc;
-    using C = Cfg<CT, D, QP, PP, RT>;
-    constexpr int TP = C::TP, S = C::stages;
+    using C = Cfg<CT, D, QP, RT>;
+    constexpr int TP = C::TP, S = C::stages, PP = C::PP;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *tiles = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                              ~static_cast<uintptr_t>(1023));
@@ -499,13 +508,13 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
             // half of a tile's positions: the first half's products run while the other half's weights are made
             auto values = [&](int slot, int v, int half, bool more) {
                 const uint64_t dv = sw128_mn_desc(saddr(ring + (v % S) * C::stage), TP * 128) + half * (TP / 32) * 128;
-                const uint32_t d = tmem + C::o_col + slot * D, p = tmem + slot * C::s_cols + half * (TP / 4);
+                const uint32_t d = tmem + C::o_col + slot * D, p = tmem + slot * C::s_cols;
                 if (elect_one()) {
 #pragma unroll
                     for (int part = 0; part < PP; ++part)
 #pragma unroll
                         for (int kk = 0; kk < TP / 32; ++kk)
-                            mma_ts(d, p + part * (TP / 2) + 8 * kk, dv + 128 * kk, id_pv, more || (part | kk) != 0);
+                            mma_ts(d, p + C::p_col(part, half * (TP / 32) + kk), dv + 128 * kk, id_pv, more || (part | kk) != 0);
                 }
                 __syncwarp();
             };
@@ -599,13 +608,12 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                 }
 #pragma unroll 1
                 for (int t = 0; t < kTurns && !as_is; t += kAtOnce) {
-                    uint4 raw[kAtOnce][QP == 1 || (C::bf16 && QP == 2) ? 1 : 2];  // fp32 rows are twice as wide
-                    constexpr bool kMayBeWide = QP == 3 || (!C::bf16 && QP == 2);
+                    uint4 raw[kAtOnce][C::wide ? 2 : 1];  // fp32 rows are twice as wide
 #pragma unroll
                     for (int u = 0; u < kAtOnce; ++u) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(source(kMayBeWide ? 4 : 2));
+                        const uint4 *src = reinterpret_cast<const uint4 *>(source(C::wide ? 4 : 2));
 #pragma unroll
-                        for (int k = 0; k < (kMayBeWide ? 2 : 1); ++k)
+                        for (int k = 0; k < (C::wide ? 2 : 1); ++k)
                             raw[u][k] = in < w.rows ? src[k] : make_uint4(0u, 0u, 0u, 0u);
                         step_row();
                     }
@@ -614,11 +622,11 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                         const int row = r0 + (t + u) * kPer;
                         float x[8];
 #pragma unroll
-                        for (int k = 0; k < (kMayBeWide ? 2 : 1); ++k) {
+                        for (int k = 0; k < (C::wide ? 2 : 1); ++k) {
                             const uint32_t y[4] = {raw[u][k].x, raw[u][k].y, raw[u][k].z, raw[u][k].w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                if constexpr (kMayBeWide) {
+                                if constexpr (C::wide) {
                                     x[4 * k + i] = __uint_as_float(y[i]);
                                 } else {
                                     const float2 f = a.dtype == WSW_BF16 ? make_float2(bf16lo(y[i]), bf16hi(y[i]))
@@ -720,12 +728,11 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                         const float w0 = ex2(t0), w1 = ex2(t1);
                         if (i & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(l2b) : "l"(f2_pack(w0, w1)));
                         else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(l2a) : "l"(f2_pack(w0, w1)));
-                        if constexpr (PP == 1) part[0][i] = pack2<C::bf16>(w0, w1);
-                        else if constexpr (PP == 2) split<CT>(w0, w1, part[0][i], part[1][i]);
+                        if constexpr (PP == 2) split<CT>(w0, w1, part[0][i], part[1][i]);
                         else split3(w0, w1, part[0][i], part[1][i], part[2][i]);
                     }
 #pragma unroll
-                    for (int k = 0; k < PP; ++k) tmem_st16(s_base + k * (TP / 2) + 16 * chunk, part[k]);
+                    for (int k = 0; k < PP; ++k) tmem_st16(s_base + C::p_col(k, 2 * chunk), part[k]);
                 };
                 auto ready = [&](int half) {
                     tmem_wait_st();
@@ -735,8 +742,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
                 };
                 auto ref_of = [&] { return m == -INFINITY ? 0.f : m - C::shift; };  // nothing seen yet: all weights 0
                 if (plain) {
-                    // Two chunks of scores stay in registers, the others are read twice, a chunk at a time (weights take the
-                    // place of the first two's only).  256 requests behind 32768 positions: 157 us; three chunks 162, four 163,
+                    // Two chunks of scores stay in registers, the others are read twice, a chunk at a time (weights take no
+                    // other chunk's place, or both chunks' of 64 positions).  With P in one part, 256 requests behind 32768 positions: 157 us; three chunks 162, four 163,
                     // the second half on its way while the first half's weights are made 163.
                     uint32_t v[2][32];
                     float mx = -INFINITY;
@@ -783,9 +790,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = (mask >> i) & 1 ? v[i] : 0xff800000u;
                     };
-                    // the second half's maximum comes first (its scores go back for the weights), since the first half's
-                    // weights take the place of scores that have been read; several parts of the weights take all
-                    // scores' places, which two chunks hold
+                    // the second half's maximum comes first (its scores go back for the weights); weights take their own
+                    // scores' places or, in three parts, those of two chunks that have been read
                     float mx = -INFINITY;
                     uint32_t va[32], vb[32];
                     if constexpr (TP == 128) {
@@ -876,10 +882,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, PP, RT>::threads, 1) attn_prefi
     }
 }
 
-template <int CT, int D, int QP, int PP, int RT>
+template <int CT, int D, int QP, int RT>
 cudaError_t launch_one(const Args &a, cudaStream_t s, int ctas) {
-    using C = Cfg<CT, D, QP, PP, RT>;
-    const auto kernel = attn_prefix_kernel<CT, D, QP, PP, RT>;
+    using C = Cfg<CT, D, QP, RT>;
+    const auto kernel = attn_prefix_kernel<CT, D, QP, RT>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), C::smem);
     if (e != cudaSuccess) return e;
     // the roles' registers are shared out of what the block is launched with: with less, a role would wait for them
@@ -896,8 +902,8 @@ cudaError_t launch_one(const Args &a, cudaStream_t s, int ctas) {
 template <int CT>
 cudaError_t launch_prefix(const Args &a, int row_tiles, cudaStream_t s, int ctas);
 
-#define WSW_PREFIX_ONE(CT, QP, PP, RT)                                                   \
-    (a.kv.head_dim == 64 ? launch_one<CT, 64, QP, PP, RT>(a, s, ctas) : launch_one<CT, 128, QP, PP, RT>(a, s, ctas))
+#define WSW_PREFIX_ONE(CT, QP, RT)                                                   \
+    (a.kv.head_dim == 64 ? launch_one<CT, 64, QP, RT>(a, s, ctas) : launch_one<CT, 128, QP, RT>(a, s, ctas))
 
 }  // namespace prefix
 }  // namespace wsw

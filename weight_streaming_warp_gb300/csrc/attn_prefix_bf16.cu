@@ -7,9 +7,9 @@ namespace prefix {
 
 template <>
 cudaError_t launch_prefix<WSW_BF16>(const Args &a, int row_tiles, cudaStream_t s, int ctas) {
-    if (a.dtype == WSW_F32) return WSW_PREFIX_ONE(WSW_BF16, 3, 3, 1);
-    if (a.dtype == WSW_F16) return WSW_PREFIX_ONE(WSW_BF16, 2, 1, 1);
-    return row_tiles == 2 ? WSW_PREFIX_ONE(WSW_BF16, 1, 1, 2) : WSW_PREFIX_ONE(WSW_BF16, 1, 1, 1);
+    if (a.dtype == WSW_F32) return WSW_PREFIX_ONE(WSW_BF16, 3, 1);
+    if (a.dtype == WSW_F16) return WSW_PREFIX_ONE(WSW_BF16, 2, 1);
+    return row_tiles == 2 ? WSW_PREFIX_ONE(WSW_BF16, 1, 2) : WSW_PREFIX_ONE(WSW_BF16, 1, 1);
 }
 
 }  // namespace prefix
