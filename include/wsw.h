@@ -786,7 +786,7 @@ int wsw_beam_select(const void *logits, int32_t dtype, int64_t requests, int64_t
  *
  * A prefix's products run on the tensor cores with fp32 sums.  The softmax weights keep 22 bits over
  * binary16 and q8_0 and 16 over bf16 (under fp32 queries all 24), as there; q keeps 22 bits over binary16 and
- * q8_0 (its own binary16 all of them), and all of them over bf16.  softcap's tanh is off by 7 2^-24 at most.
+ * q8_0 (its own binary16 all of them), and all of them over bf16.  softcap's tanh is off by 24 2^-24 of itself at most.
  *
  *   cu_groups   int32 [groups + 1], ascending within [0, requests];  prefix_len int32 [groups], within
  *               [0, max_pages * page_size].  A bound that is not is moved to the nearest one that is,
