@@ -16,13 +16,15 @@
 // scores are pairs of fp32 (some 45 bits: FP64 has a hundredth of fp32's rate here, and 900 scores
 // of four operations took 5 us).  lse is off by some 1e-8, and by what the rounding of scale log2 e to
 // fp32 (6e-8 at most) makes of the mean of the log probabilities, which all beams have nearly in
-// common.  Rows of different alignment are summed in another order: beams whose largest logit is the
-// same value of the same token, and whose ln S differ by less than 2^-20, count as copies of each
-// other: they share the first one's, so that they tie and rank by index.
+// common.  Value i of every row is the same thread's in the same order, whatever the row's alignment, so that equal rows have
+// equal sums, bit for bit: copies of a beam tie and rank by index.  Rows that do not lie on 16 bytes take a vector from
+// two loads, the second from L1.  (60 x 10 x 50021, of which seven bf16 rows in eight and three fp32 rows in four do not:
+// 30.8 and 43.6 us; with the vectors of each row as they lie in memory 26.6 and 35.8, and sums of copies that differ.  The
+// second vector by shuffles: 33.4 and 61.)
 //
 // Bound: the logits once; as the log probabilities with alternatives, by the selection's dependent steps
-// for few rows (1 x 4 x 152064 fp32 10.9 us; the logits alone are 0.4) and by instructions and the selection's
-// barriers for many (60 x 10 x 50021 bf16 25 us, 2.4 TB/s; 150 x 4 x 50000 fp32 34 us, 3.5 TB/s).
+// for few rows (1 x 4 x 152064 fp32 10.6 us; the logits alone are 0.4) and by instructions and the selection's
+// barriers for many (60 x 10 x 50024 bf16 26 us, 2.3 TB/s; 150 x 4 x 50000 fp32 32 us, 3.7 TB/s).
 #include "topk_rows.cuh"
 
 namespace wsw {
@@ -105,11 +107,10 @@ struct BeamShared {
     uint16_t at[kCap];         // the places of those that reach the threshold
     uint64_t best[2][kMaxTop]; // the best so far, in order: scores, and their
     int2 tag[2][kMaxTop];      // lists and tokens; two sets in turn
-    uint64_t head[kMaxBeams];  // each beam's largest logit's key
     alignas(16) uint32_t group[kThreads];
     uint32_t reach;
     Two sum[kMaxBeams], base[kMaxBeams];
-    float max[kMaxBeams], ln_s[kMaxBeams];
+    float max[kMaxBeams];
     int last, n;
 };
 
@@ -143,48 +144,32 @@ __device__ __forceinline__ bool is_end(const BeamArgs &a, int token) {
     return ends;
 }
 
-// Each of the request's beams: score - ln S, its maximum and first key, from its parts.
+// Each of the request's beams: score - ln S and its maximum, from its parts.
 __device__ __forceinline__ void beam_sums(const BeamArgs &a, BeamShared &sm, const float *recs, int64_t request) {
     const int tid = threadIdx.x, lane = tid & 31;
 #pragma unroll 1
     for (int b = tid >> 5; b < a.beams; b += kWarps) {
         float m = -FLT_MAX;
         Two sum{0.f, 0.f};
-        uint64_t head = 0;
 #pragma unroll 1
         for (int i = lane; i < a.splits; i += 32) {
             const float *r = recs + (static_cast<int64_t>(b) * a.splits + i) * a.rec;
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(r));
-            const uint64_t key = __ldcg(reinterpret_cast<const uint64_t *>(r) + 2);
             const float mn = max_nan(m, v.x);
             sum = raised(a, m, sum, mn) + raised(a, v.x, Two{v.z, v.w}, mn);
             m = mn;
-            head = max(head, key);
         }
-        if (a.splits > 1) {
-            warp_total(a, m, sum);
-#pragma unroll 1
-            for (int d = 16; d >= 1; d >>= 1) head = max(head, __shfl_xor_sync(WSW_FULL_MASK, head, d));
-        }
+        if (a.splits > 1) warp_total(a, m, sum);
         if (lane == 0) {
             sm.max[b] = m;
             sm.sum[b] = sum;
-            sm.head[b] = head;
         }
     }
     __syncthreads();
     // a row of nothing but -inf, with a NaN or with +inf has no candidate: ln S -inf or NaN
-    if (tid >= 32) return;  // a barrier follows
-    const int b = min(lane, a.beams - 1);
-    Two l = ln(sm.sum[b]);
-    sm.ln_s[b] = l.h;
-    __syncwarp();
-    int first = b;  // of the copies of this beam
-    for (int o = b - 1; o >= 0; --o)
-        if (sm.head[o] == sm.head[b] && fabsf(sm.ln_s[o] - l.h) <= 9.5367431640625e-7f) first = o;
-    l.h = __shfl_sync(WSW_FULL_MASK, l.h, first);
-    l.l = __shfl_sync(WSW_FULL_MASK, l.l, first);
-    if (lane < a.beams) sm.base[lane] = Two{a.scores[request * a.beams + lane], 0.f} + Two{-l.h, -l.l};
+    if (tid >= a.beams) return;  // a barrier follows
+    const Two l = ln(sm.sum[tid]);
+    sm.base[tid] = Two{a.scores[request * a.beams + tid], 0.f} + Two{-l.h, -l.l};
 }
 
 // The request's answer, once all its rows' parts are there.  Every thread calls it.  (The loops are not
@@ -321,6 +306,37 @@ __device__ __forceinline__ void merge(const BeamArgs &a, BeamShared &sm, int64_t
     }
 }
 
+// 16 bytes at any multiple of T's size, `behind` bytes behind a multiple of 16: of one or two vectors there, both of
+// which hold some of them.
+struct LoadAnywhere {
+    int behind;
+    __device__ __forceinline__ static uint4 first(const void *p, int behind) {
+        return __ldg(reinterpret_cast<const uint4 *>(static_cast<const unsigned char *>(p) - behind));
+    }
+    // the bytes from `behind` on of a and the vector b after it
+    __device__ __forceinline__ static uint4 join(const uint4 &a, const uint4 &b, int behind) {
+        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (behind & 8) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (behind & 4) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        if (behind & 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ uint4 operator()(const void *p) const {
+        const uint4 a = first(p, behind);
+        if (behind == 0) return a;
+        return join(a, first(static_cast<const unsigned char *>(p) + 16, behind), behind);
+    }
+};
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(const __grid_constant__ BeamArgs a) {
     constexpr int V = Elem<T>::kVec;
@@ -333,11 +349,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
     pdl_launch_dependents();
     pdl_wait();
     const T *x = static_cast<const T *>(a.x) + row * a.ld;
-    // The row as 16-byte vectors behind `lead` values: the split takes the vectors of [lo, hi); the first
-    // split also the values before them, the last one those after the last whole vector.
-    const int lead = min(static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)), a.vocab);
-    const int64_t begin = lead + static_cast<int64_t>(split) * a.chunk;
-    const int whole = lead + (a.vocab - lead) / V * V;
+    // The row as vectors of 16 bytes: the split takes those of [lo, hi), the last one also the values behind the last
+    // whole vector.
+    const int behind = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15);
+    const int64_t begin = static_cast<int64_t>(split) * a.chunk;
+    const int whole = a.vocab / V * V;
     const int lo = static_cast<int>(min(begin, static_cast<int64_t>(whole)));
     const int hi = static_cast<int>(min(begin + a.chunk, static_cast<int64_t>(whole)));
     const int k = a.k;
@@ -348,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
         for (int u = 0; u < kUnroll; ++u) {
             const int at = tile0 + (u * kThreads + tid) * V;
             raw[u] = make_uint4(Elem<T>::kLow, Elem<T>::kLow, Elem<T>::kLow, Elem<T>::kLow);
-            if (at < hi) raw[u] = __ldg(reinterpret_cast<const uint4 *>(x + at));
+            if (at < hi) raw[u] = LoadAnywhere::first(x + at, behind);
         }
     };
     fetch(lo);
@@ -358,18 +374,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
         top.thr = -INFINITY;
     }
     __syncthreads();
-    {
-        int i = -1;
-        if (split == 0 && tid < lead) i = tid;
-        if (split == a.splits - 1 && tid >= 32 && tid - 32 < a.vocab - whole) i = whole + tid - 32;
-        if (i >= 0) {
-            const float v = Elem<T>::get(x, i);
-            if (!(v == -INFINITY)) {
-                m = fmaxf(v, -FLT_MAX);
-                s = v != v || v == INFINITY ? NAN : 1.f;
-            }
-            push(top, key_of(v, i));
+    if (split == a.splits - 1 && tid >= 32 && tid - 32 < a.vocab - whole) {
+        const int i = whole + tid - 32;
+        const float v = Elem<T>::get(x, i);
+        if (!(v == -INFINITY)) {
+            m = fmaxf(v, -FLT_MAX);
+            s = v != v || v == INFINITY ? NAN : 1.f;
         }
+        push(top, key_of(v, i));
     }
     const uint64_t c2 = f2(a.c, a.c);
 
@@ -380,6 +392,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
     for (int tile0 = lo; tile0 < hi; tile0 += kTile) {
         float v[kUnroll][V];
         float vm[kUnroll];
+        if (behind) {
+            uint4 next[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int at = tile0 + (u * kThreads + tid) * V;
+                next[u] = raw[u];
+                if (at < hi) next[u] = LoadAnywhere::first(x + at + V, behind);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) raw[u] = LoadAnywhere::join(raw[u], next[u], behind);
+        }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) Elem<T>::unpack(raw[u], v[u]);
         if (tile0 + kTile < hi) fetch(tile0 + kTile);  // in flight during this tile's arithmetic
@@ -430,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
         const bool last = tile0 + kTile >= hi;
         if (__syncthreads_or(filled > kKeep || last || (first && k > 8))) {
             const int end = min(tile0 + kTile, hi);
-            select(top, x, group0, end, thr, k);
+            select(top, x, group0, end, thr, k, LoadAnywhere{behind});
             group0 = end;
             thr = after_cut(top, end, k);
         }

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) logprobs_ker
         const bool last = tile0 + kTile >= hi;
         if (__syncthreads_or(filled > kKeep || last || (first && k > 8))) {
             const int end = min(tile0 + kTile, hi);
-            select(sm, x, group0, end, thr, k);
+            select(sm, x, group0, end, thr, k, LoadAligned{});
             group0 = end;
             thr = after_cut(sm, end, k);
         }

@@ -253,13 +253,19 @@ __device__ __forceinline__ void thin(Shared &sm, int n, int k) {
     __syncthreads();
 }
 
+// 16 bytes at a 16-byte boundary
+struct LoadAligned {
+    template <typename T>
+    __device__ __forceinline__ uint4 operator()(const T *p) const { return __ldg(reinterpret_cast<const uint4 *>(p)); }
+};
+
 // The candidates' values from thr up become keys, and the keys are cut.  When there were too many
 // vectors for their place, the values [from, end) of the row are read again: those that the k-th
 // largest of 32 groups' maxima reaches, which some tens do in any order of distinct values; what
 // many equal ones still overflow goes in pieces that cannot, a cut before each.  Every thread calls it
-// after a barrier behind the candidates.
-template <typename T>
-__device__ __forceinline__ void select(Shared &sm, const T *x, int from, int end, float thr, int k) {
+// after a barrier behind the candidates.  load(p): the 16 bytes of values from p on.
+template <typename T, typename Load>
+__device__ __forceinline__ void select(Shared &sm, const T *x, int from, int end, float thr, int k, Load load) {
     constexpr int V = Elem<T>::kVec;
     const int tid = threadIdx.x, n0 = sm.n, nvec = sm.nvec;
     if (nvec <= kVecs) {
@@ -273,7 +279,7 @@ __device__ __forceinline__ void select(Shared &sm, const T *x, int from, int end
         float v[V];
 #pragma unroll 2
         for (int i = tid; i < nv; i += kThreads) {
-            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(x + from) + i), v);
+            Elem<T>::unpack(load(x + from + i * V), v);
 #pragma unroll
             for (int u = 0; u < V; ++u) mx = fmaxf(mx, v[u]);
         }
@@ -281,7 +287,7 @@ __device__ __forceinline__ void select(Shared &sm, const T *x, int from, int end
         bool full = !(mx >= bound);
 #pragma unroll 1
         for (int i = tid; i < nv && !full; i += kThreads) {
-            Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(x + from) + i), v);
+            Elem<T>::unpack(load(x + from + i * V), v);
 #pragma unroll
             for (int u = 0; u < V; ++u) {
                 if (!(v[u] >= bound)) continue;
