@@ -751,9 +751,9 @@ int wsw_kv_page_compact(const int32_t *seq_len, int64_t requests, const int32_t 
  *   end_parent, end_token, end_score   the same of the ended ones, in order
  * Places without a candidate hold -1, -1 and -inf.  A forbidden token (logit -inf), a beam whose
  * score is not finite, and every beam whose row holds a NaN or +inf have no candidates.
- * Sums are fp32 within a thread and 64 bits above, scores are compared in 64 bits: s is off by
- * some 1e-7, differences between the beams of a request by some 1e-8.  parent is what
- * wsw_kv_page_fork takes.
+ * Sums are fp32 within a thread's tile and pairs of fp32 above, scores are compared as pairs: s is off by some
+ * 1e-8 as a rule and 2^-18 at most, before its rounding.  Equal rows have equal sums, whatever their
+ * alignment.  parent is what wsw_kv_page_fork takes.
  *
  *   logits      `dtype` (WSW_F32, WSW_F16 or WSW_BF16) [requests * beams][ld], ld >= vocab,
  *               aligned to its element.

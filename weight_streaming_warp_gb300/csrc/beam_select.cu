@@ -11,20 +11,26 @@
 // whatever reaches it is ranked, and the ranks answer.  (Rows joined first, then the request: 3 us more.)
 //
 // The order of near candidates of different beams hangs on the difference of their lse, so that more
-// than fp32 of it counts: a thread's sum of some hundred terms is fp32 (the errors of single terms,
-// 2^-22 at most, have no common sign); the sums of threads and CTAs, the logarithm and the
-// scores are pairs of fp32 (some 45 bits: FP64 has a hundredth of fp32's rate here, and 900 scores
-// of four operations took 5 us).  lse is off by some 1e-8, and by what the rounding of scale log2 e to
-// fp32 (6e-8 at most) makes of the mean of the log probabilities, which all beams have nearly in
-// common.  Value i of every row is the same thread's in the same order, whatever the row's alignment, so that equal rows have
+// than fp32 of it counts.  A tile's terms, 8 or 16 of each half of a pair, are added in fp32; the sums of tiles, threads
+// and CTAs, their factors when a maximum is raised, the logarithm and the scores are pairs of fp32 (some 45 bits: FP64 has
+// a hundredth of fp32's rate here, and 900 scores of four operations took 5 us), and scale log2 e is one.  (A thread's sum in
+// fp32 lost what was below half its last place tile after tile, always downward: 1.4e-6 of a row of 152064 behind a peak of
+// 20.)  lse is off by 2^-22 (a term's power), 15 2^-24 (a tile's additions), and 2 2^-24 ln 2 |t| (the two roundings of a
+// term's exponent t; its mean is below the entropy and kLag, 26): 2^-18 at most.  Nearly all of it comes
+// with either sign: rows of 152064 normal values, flat, rising, behind a peak or but two, are off by 5e-9 to 5e-8 in the root
+// mean square and 2e-7 at most, the beams' differences by half of that (5e-8 to 1.4e-6 and 2.4e-6 with fp32 sums and factors,
+// at 1 us less of 30).  Value i of every row is the same thread's in the same order, whatever the row's alignment, so that equal rows have
 // equal sums, bit for bit: copies of a beam tie and rank by index.  Rows that do not lie on 16 bytes take a vector from
 // two loads, the second from L1.  (60 x 10 x 50021, of which seven bf16 rows in eight and three fp32 rows in four do not:
-// 30.8 and 43.6 us; with the vectors of each row as they lie in memory 26.6 and 35.8, and sums of copies that differ.  The
-// second vector by shuffles: 33.4 and 61.)
+// 32.6 and 45.1 us; with the vectors of each row as they lie in memory 4 and 8 less, and sums of copies that differ.  The
+// second vector by shuffles: 3 and 17 more.)
 //
 // Bound: the logits once; as the log probabilities with alternatives, by the selection's dependent steps
-// for few rows (1 x 4 x 152064 fp32 10.6 us; the logits alone are 0.4) and by instructions and the selection's
-// barriers for many (60 x 10 x 50024 bf16 26 us, 2.3 TB/s; 150 x 4 x 50000 fp32 32 us, 3.7 TB/s).
+// for few rows (1 x 4 x 152064 fp32 11.3 us; the logits alone are 0.4) and by instructions and the selection's
+// barriers for many (60 x 10 x 50024 bf16 27.5 us, 2.2 TB/s; 150 x 4 x 50000 fp32 33 us, 3.7 TB/s).
+#include <algorithm>
+#include <limits>
+
 #include "topk_rows.cuh"
 
 namespace wsw {
@@ -44,7 +50,7 @@ struct BeamArgs {
     unsigned *cnt;                // [requests] arrival counters, zero between calls
     float *part;                  // [rows][splits][rec]: maximum, sum (64 bits), keys
     int64_t ld;
-    float scale, c;               // c = scale log2 e
+    float scale, c, c_lo;         // c + c_lo = scale log2 e, c_lo > 0
     int vocab, beams, want, k, splits, chunk, rec, n_ends;  // want: candidates that can matter, k: of a row
     int32_t ends[kMaxEnds];
 };
@@ -114,15 +120,34 @@ struct BeamShared {
     int last, n;
 };
 
+// The maximum in use lags behind a thread's by up to so much (log2), so that factors, which are pairs, are rare.
+constexpr float kLag = 8.f;
+
 // order-preserving bits of a finite score; 0: no candidate
 __device__ __forceinline__ uint64_t ord2(Two s) {
     if (!(s.h > -INFINITY) || !(s.h < INFINITY)) return 0;  // -inf, NaN
     return (static_cast<uint64_t>(ord(s.h)) << 32) | ord(s.l);
 }
 
-// (m, s) of a set raised to the maximum mx
+// (m, s) of a set raised to the maximum mx: s 2^y of y = (m - mx) scale log2 e = i + f, |f| <= 0.5, by the exponential series
+// of z = f ln 2: the terms from z^3 on, 0.007 at most, need fp32 alone, and end where they are below 2^-32.
 __device__ __forceinline__ Two raised(const BeamArgs &a, float m, Two s, float mx) {
-    return s.h == 0.f ? Two{0.f, 0.f} : s * ex2((m - mx) * a.c);  // before the first value the difference may be -inf
+    if (s.h == 0.f || m == mx) return s;
+    const Two d = two_sum(m, -mx);
+    if (!(d.h * a.c > -125.f)) return m != m || mx != mx ? Two{NAN, 0.f} : Two{0.f, 0.f};
+    const Two y = d * Two{a.c, a.c_lo};
+    const float i = rintf(y.h);
+    const Two z = renorm(y.h - i, y.l) * Two{0.69314718f, -1.9046543e-9f}, z2 = z * z;
+    const float x = z.h;
+    float p = 1.f / 40320.f;
+    p = fmaf(p, x, 1.f / 5040.f);
+    p = fmaf(p, x, 1.f / 720.f);
+    p = fmaf(p, x, 1.f / 120.f);
+    p = fmaf(p, x, 1.f / 24.f);
+    p = fmaf(p, x, 1.f / 6.f);
+    const Two power = Two{1.f, 0.f} + (z + Two{z2.h * 0.5f, z2.l * 0.5f} + Two{p * x * z2.h, 0.f});
+    const float unit = __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(i)) << 23);
+    return s * Two{power.h * unit, power.l * unit};
 }
 // The maximum and sum of groups of W lanes; every lane gets its group's.
 template <int W = 32>
@@ -368,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
         }
     };
     fetch(lo);
-    float m = -FLT_MAX, s = 0.f;  // m >= -FLT_MAX: x - m is never (-inf) - (-inf)
+    float m = -FLT_MAX;  // m >= -FLT_MAX: x - m is never (-inf) - (-inf)
+    Two sum{0.f, 0.f};
     if (tid == 0) {
         top.n = top.nvec = 0;
         top.thr = -INFINITY;
@@ -379,11 +405,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
         const float v = Elem<T>::get(x, i);
         if (!(v == -INFINITY)) {
             m = fmaxf(v, -FLT_MAX);
-            s = v != v || v == INFINITY ? NAN : 1.f;
+            sum.h = v != v || v == INFINITY ? NAN : 1.f;
         }
         push(top, key_of(v, i));
     }
-    const uint64_t c2 = f2(a.c, a.c);
+    const uint64_t c2 = f2(a.c, a.c), c2_lo = f2(a.c_lo, a.c_lo);
 
     int since = 0, filled = 0;  // tiles since the buffer was looked at, candidates known then
     int group0 = lo;
@@ -414,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
             for (int i = 2; i < V; i += 2) vm[u] = max3(vm[u], v[u][i], v[u][i + 1]);
             tm = fmaxf(tm, vm[u]);
         }
-        if (tm > m) {
-            s = s == 0.f ? 0.f : s * ex2((m - tm) * a.c);  // before the first value the difference may be -inf
+        if ((tm - m) * a.c > kLag) {
+            sum = raised(a, m, sum, tm);
             m = tm;
         }
         const uint64_t nm2 = f2(-m, -m);
@@ -426,7 +452,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
             for (int i = 0; i < V; i += 2) {
                 uint64_t d2 = f2(v[u][i], v[u][i + 1]);
                 asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d2) : "l"(nm2));
-                asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d2) : "l"(c2));
+                uint64_t lo;  // of a masked value (-inf) as d2 c is, since c_lo > 0
+                asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(lo) : "l"(d2), "l"(c2_lo));
+                asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(d2) : "l"(c2), "l"(lo));
                 float d0, d1;
                 asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d2));
                 asm("add.rn.f32x2 %0, %0, %1;" : "+l"(ss) : "l"(f2(ex2(d0), ex2(d1))));
@@ -434,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
         {
             float x0, x1;
             asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(ss));
-            s += x0 + x1;
+            sum = sum + two_sum(x0, x1);
         }
         // what reaches the first tile's bound; after a cut, only what beats the k-th best
         if (first) thr = reached_by(top, tm, k);
@@ -465,7 +493,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 6) beam_kernel(
         cut(top, k);
     }
     // the block's maximum and sum
-    Two sum{s, 0.f};
     warp_total(a, m, sum);
     if ((tid & 31) == 0) {
         sm.max[tid >> 5] = m;
@@ -563,7 +590,10 @@ extern "C" int wsw_beam_select(const void *logits, int32_t dtype, int64_t reques
     a.end_parent = end_parent; a.end_token = end_token; a.end_score = end_score;
     a.ld = ld;
     a.scale = scale;
-    a.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    const double c = static_cast<double>(scale) * 1.4426950408889634;
+    a.c = static_cast<float>(c);
+    if (static_cast<double>(a.c) >= c) a.c = std::nextafter(a.c, 0.f);
+    a.c_lo = std::max(static_cast<float>(c - a.c), std::numeric_limits<float>::denorm_min());
     a.vocab = static_cast<int>(vocab);
     a.beams = static_cast<int>(beams);
     a.want = static_cast<int>(beams * (1 + n_ends));
