@@ -7,10 +7,13 @@
 namespace wsw {
 namespace paged {
 
-template <> cudaError_t launch_type<WSW_F16, false>(const Args &, int, cudaStream_t, bool, int64_t);
-template <> cudaError_t launch_type<WSW_BF16, false>(const Args &, int, cudaStream_t, bool, int64_t);
-template <> cudaError_t launch_type<WSW_BF16, true>(const Args &, int, cudaStream_t, bool, int64_t);
-template <> cudaError_t launch_type<WSW_Q8_0, false>(const Args &, int, cudaStream_t, bool, int64_t);
+#define WSW_PAGED_DECLARE(CT, X3)                                                                       \
+    template <> cudaError_t launch_type<CT, X3, false>(const Args &, int, cudaStream_t, bool, int64_t); \
+    template <> cudaError_t launch_type<CT, X3, true>(const Args &, int, cudaStream_t, bool, int64_t);
+WSW_PAGED_DECLARE(WSW_F16, false)
+WSW_PAGED_DECLARE(WSW_BF16, false)
+WSW_PAGED_DECLARE(WSW_BF16, true)
+WSW_PAGED_DECLARE(WSW_Q8_0, false)
 
 namespace {
 constexpr size_t kCounterBytes = 2048;
@@ -85,7 +88,7 @@ int prepare(const void *q, int32_t dtype, int64_t requests, int64_t q_heads, con
     a.passes = (a.group + *rows - 1) / *rows;
     a.max_len = static_cast<int>(max_pages << a.kv.page_shift);
     a.window = window > 0 ? static_cast<int>(window) : 0x7fffffff;
-    a.dtype = a.out_dtype = dtype;
+    a.dtype = dtype;
     // the longest possible list
     const int64_t seen = a.max_len < a.window ? a.max_len : a.window;
     *tiles = requests * cache->heads * a.passes * ((seen + 15) / 16 + kPair);
@@ -100,11 +103,15 @@ void place(Args *a, void *ws, int rows) {
     a->wrec = a->rec + static_cast<size_t>(kCtas) * 2 * record_bytes(rows, a->kv.head_dim) / 4;
 }
 
+template <bool Rest>
+cudaError_t launch_cache(const Args &a, int cache_dtype, int rows, int64_t tiles, cudaStream_t s, bool pdl) {
+    if (cache_dtype == WSW_F16) return launch_type<WSW_F16, false, Rest>(a, rows, s, pdl, tiles);
+    if (cache_dtype == WSW_Q8_0) return launch_type<WSW_Q8_0, false, Rest>(a, rows, s, pdl, tiles);
+    if (a.dtype == WSW_F32) return launch_type<WSW_BF16, true, Rest>(a, rows, s, pdl, tiles);
+    return launch_type<WSW_BF16, false, Rest>(a, rows, s, pdl, tiles);
+}
 cudaError_t launch_paged(const Args &a, int cache_dtype, int rows, int64_t tiles, cudaStream_t s, bool pdl) {
-    if (cache_dtype == WSW_F16) return launch_type<WSW_F16, false>(a, rows, s, pdl, tiles);
-    if (cache_dtype == WSW_Q8_0) return launch_type<WSW_Q8_0, false>(a, rows, s, pdl, tiles);
-    if (a.dtype == WSW_F32) return launch_type<WSW_BF16, true>(a, rows, s, pdl, tiles);
-    return launch_type<WSW_BF16, false>(a, rows, s, pdl, tiles);
+    return a.ml ? launch_cache<true>(a, cache_dtype, rows, tiles, s, pdl) : launch_cache<false>(a, cache_dtype, rows, tiles, s, pdl);
 }
 
 }  // namespace paged

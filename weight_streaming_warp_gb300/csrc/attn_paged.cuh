@@ -80,13 +80,15 @@ struct Args {
     float cap_out;    // softcap log2 e
     int requests, q_heads, group, passes;  // passes = ceil(group / rows)
     int max_len, window;                   // window > 0
-    int dtype;                             // of q
-    int out_dtype;                         // of out
-    // NULL, or for callers that join the result with another part of the positions: only those from
-    // first[r] on are seen, and a row's maximum and sum are left, too
-    const int32_t *first;
-    float2 *ml;  // [requests][q_heads]
+    int dtype;                             // of q and out
+    // of the Rest variant (below) alone
+    const int32_t *first;  // [requests]
+    float2 *ml;            // [requests][q_heads]
 };
+
+// Rest: for callers that join the result with another part of the positions.  Only those from first[r] on are seen, out is
+// fp32, and a row's maximum and sum are left, too.  (A variant of its own: asked at run time it cost attn_paged_decode
+// 0.1 us of 8.7 for three short requests, 0.9 of 114.3 for 64 ragged ones.)
 
 // Shape of one variant: cache type, head_dim, query rows (8 or 16), third parts of q and the weights
 // (bf16 pages under fp32 queries).
@@ -216,20 +218,21 @@ __device__ __forceinline__ uint32_t pack16(int dtype, float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
     return dtype == WSW_BF16 ? *reinterpret_cast<const uint32_t *>(&b) : *reinterpret_cast<const uint32_t *>(&h);
 }
+template <bool Rest>
 __device__ __forceinline__ void store_out4(const Args &a, int64_t i, float4 v) {
-    if (a.out_dtype == WSW_F32)
+    if (Rest || a.dtype == WSW_F32)
         *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i) = v;
     else
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + i) =
-            make_uint2(pack16(a.out_dtype, v.x, v.y), pack16(a.out_dtype, v.z, v.w));
+            make_uint2(pack16(a.dtype, v.x, v.y), pack16(a.dtype, v.z, v.w));
 }
 __device__ __forceinline__ float lse_of(float m, float l, float shift) {
     return l == 0.f ? -INFINITY : (m + log2f(l) - shift) * kLn2;
 }
-template <typename C>
-__device__ __forceinline__ void leave_sum(const Args &a, int64_t head, float m, float l) {
-    if (a.lse) a.lse[head] = lse_of(m, l, C::shift);
-    if (a.ml) a.ml[head] = make_float2(m - C::shift, l);
+template <bool Rest>
+__device__ __forceinline__ void leave_sum(const Args &a, int64_t head, float m, float l, float shift) {
+    if constexpr (Rest) a.ml[head] = make_float2(m - shift, l);
+    else if (a.lse) a.lse[head] = lse_of(m, l, shift);
 }
 // weight of a record with maximum m against the common maximum
 __device__ __forceinline__ float weight(float m, float mx) { return m == -INFINITY ? 0.f : ex2(m - mx); }
@@ -250,26 +253,26 @@ __device__ __forceinline__ int clipped_len(const Args &a, int r) {
     const int n = a.lens[r];
     return n < 0 ? 0 : n > a.max_len ? a.max_len : n;
 }
-// the first position that request r of length len sees
+// the first position that request r of length len sees; there is no window in front of a rest
+template <bool Rest>
 __device__ __forceinline__ int start_of(const Args &a, int r, int len) {
-    int start = len > a.window ? len - a.window : 0;
-    if (a.first) start = max(start, min(a.first[r], len));
-    return start;
+    if constexpr (Rest) return min(a.first[r], len);
+    return len > a.window ? len - a.window : 0;
 }
-template <int T>
+template <int T, bool Rest>
 __device__ __forceinline__ int tiles_of(const Args &a, int r, int len) {
-    const int seen = len - start_of(a, r, len);
+    const int seen = Rest ? len - start_of<Rest>(a, r, len) : len < a.window ? len : a.window;
     return seen / T + (seen % T != 0);
 }
-template <int T>
+template <int T, bool Rest>
 __device__ __forceinline__ void set_request(const Args &a, Cursor &c, int r) {
     c.r = r;
     c.len = clipped_len(a, r);
-    c.nt = tiles_of<T>(a, r, c.len);
-    c.start = start_of(a, r, c.len);
+    c.nt = tiles_of<T, Rest>(a, r, c.len);
+    c.start = start_of<Rest>(a, r, c.len);
 }
 // The next tile of the list; the caller knows that there is one.
-template <int T>
+template <int T, bool Rest>
 __device__ __forceinline__ void advance(const Args &a, Cursor &c, int extra) {
     ++c.g;
     if (++c.t < c.nt) return;
@@ -278,11 +281,11 @@ __device__ __forceinline__ void advance(const Args &a, Cursor &c, int extra) {
     if (++c.hp < a.kv.heads * a.passes) return;
     c.hp = 0;
     int r = c.r;
-    do set_request<T>(a, c, ++r);
+    do set_request<T, Rest>(a, c, ++r);
     while (c.nt == 0 && r + 1 < a.requests);
 }
 
-template <int CT, int D, int RT, bool X3>
+template <int CT, int D, int RT, bool X3, bool Rest>
 __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_kernel(const __grid_constant__ Args a) {
     using C = Cfg<CT, D, RT, X3>;
     constexpr int W = C::warps, NT = C::threads, T = C::tile;
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
     for (int r = r0; r < r1; ++r) {
         const int n = a.lens[r], clipped = min(max(n, 0), a.max_len);
         cut_len |= n != clipped;
-        const int nt = tiles_of<T>(a, r, clipped);
+        const int nt = tiles_of<T, Rest>(a, r, clipped);
         if (r == r0) nt0 = nt;
         mine += nt * HP;
         mine_n += nt > 0 ? HP : 0;
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
         while (s >= at + counted(nt) * HP) {
             at += counted(nt) * HP;
             ++r;
-            nt = tiles_of<T>(a, r, clipped_len(a, r));
+            nt = tiles_of<T, Rest>(a, r, clipped_len(a, r));
         }
         p = Place{r, s - at, nt};
     };
@@ -385,14 +388,15 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
 #pragma unroll 1
     for (int r = cta; r < a.requests; r += gridDim.x) {
         const int n = clipped_len(a, r);
-        if (start_of(a, r, n) < n) continue;
+        if (Rest ? start_of<Rest>(a, r, n) < n : n > 0) continue;
         const int64_t head = static_cast<int64_t>(r) * a.q_heads;
 #pragma unroll 1
-        for (int i = tid; i < a.q_heads * (D / 4); i += NT) store_out4(a, head * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int i = tid; i < a.q_heads * (D / 4); i += NT) store_out4<Rest>(a, head * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
 #pragma unroll 1
-        for (int i = tid; a.lse && i < a.q_heads; i += NT) a.lse[head + i] = -INFINITY;
-#pragma unroll 1
-        for (int i = tid; a.ml && i < a.q_heads; i += NT) a.ml[head + i] = make_float2(-INFINITY, 0.f);
+        for (int i = tid; (Rest || a.lse) && i < a.q_heads; i += NT) {
+            if constexpr (Rest) a.ml[head + i] = make_float2(-INFINITY, 0.f);
+            else a.lse[head + i] = -INFINITY;
+        }
     }
     __syncthreads();
     if (n_cta == 0) return;
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
     if (wb < we) {
         Cursor uc;  // the tile in use
         const Place at_first = place[warp];
-        set_request<T>(a, uc, at_first.req);
+        set_request<T, Rest>(a, uc, at_first.req);
         {
             const int n = counted(uc.nt);
             uc.hp = at_first.off / n;
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                 if (ic.g + 1 + (ic.t == ic.nt - 1 ? extra : 0) >= we) {
                     ic.g = we;
                 } else {
-                    advance<T>(a, ic, extra);
+                    advance<T, Rest>(a, ic, extra);
                     look_up();
                     if (ic.t == 0) {  // a new pair: its queries on their way to L1
                         const int hn = a.passes == 1 ? ic.hp : ic.hp / a.passes, gn = (ic.hp - hn * a.passes) * RT;
@@ -891,10 +895,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                     for (int x = 0; x < 2; ++x) v[n][x] = (RT == 8 ? o[n][x] + o[n][2 + x] : o[n][2 * y + x]) * f;
                 if (tq == 0) {
                     if (!whole) piece_ml[2 * warp + run_end][row] = make_float2(m[y], l[y]);
-                    else leave_sum<C>(a, head, m[y], l[y]);
+                    else leave_sum<Rest>(a, head, m[y], l[y], C::shift);
                 }
                 // lane tq's dimensions: 2 tq, 2 tq + 1 of every eight, or (q8_0) 4 tq .. 4 tq + 3 of sixteen
-                if (!whole || a.out_dtype == WSW_F32) {
+                if (Rest || !whole || a.dtype == WSW_F32) {
                     float *dst = whole ? static_cast<float *>(a.out) + head * D : rec + row * C::srec;
                     dst += C::q8 ? 4 * tq : 2 * tq;
 #pragma unroll
@@ -910,15 +914,14 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                     for (int n = 0; n < D / 8; n += C::q8 ? 2 : 1) {
                         if constexpr (C::q8)
                             *reinterpret_cast<uint2 *>(dst + 8 * n) =
-                                make_uint2(pack16(a.out_dtype, v[n][0], v[n + 1][0]),
-                                           pack16(a.out_dtype, v[n][1], v[n + 1][1]));
+                                make_uint2(pack16(a.dtype, v[n][0], v[n + 1][0]), pack16(a.dtype, v[n][1], v[n + 1][1]));
                         else
-                            *reinterpret_cast<uint32_t *>(dst + 8 * n) = pack16(a.out_dtype, v[n][0], v[n][1]);
+                            *reinterpret_cast<uint32_t *>(dst + 8 * n) = pack16(a.dtype, v[n][0], v[n][1]);
                     }
                 }
             }
             if (run_end) break;
-            advance<T>(a, uc, extra);
+            advance<T, Rest>(a, uc, extra);
         }
         // the first piece's record joins the last one's in the ring
         if (first_left) {
@@ -1011,8 +1014,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
             if (pc.pstart >= b && pc.pstart + pc.nt <= e) {
                 const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
                 const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-                store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
-                if (c4 == 0) leave_sum<C>(a, head, ml.x, ml.y);
+                store_out4<Rest>(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
+                if (c4 == 0) leave_sum<Rest>(a, head, ml.x, ml.y, C::shift);
             } else {
                 float *r = a.rec + static_cast<int64_t>(cta * 2 + (pc.pstart < b ? 0 : 1)) * RT * C::rec + row * C::rec;
                 *reinterpret_cast<float4 *>(r + 4 + 4 * c4) = s;
@@ -1125,8 +1128,8 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
                 if (final) {
                     const int64_t head = static_cast<int64_t>(pc.r) * a.q_heads + h * a.group + g0 + row;
                     const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-                    store_out4(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
-                    if (c4 == 0) leave_sum<C>(a, head, ml.x, ml.y);
+                    store_out4<Rest>(a, head * D + 4 * c4, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
+                    if (c4 == 0) leave_sum<Rest>(a, head, ml.x, ml.y, C::shift);
                 } else {
                     // the group's record takes the place of its first CTA's: this thread has read
                     // what it writes, and everyone the (m, l)
@@ -1144,7 +1147,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, RT, X3>::threads, 1) attn_paged_ker
     }
 }
 
-template <int CT, bool X3>
+template <int CT, bool X3, bool Rest>
 cudaError_t launch_type(const Args &a, int rows, cudaStream_t s, bool pdl, int64_t tiles);
 
 // attn_paged.cu: checks a call's arguments but its workspace and fills everything but a.cnt, a.rec and
@@ -1154,12 +1157,13 @@ int prepare(const void *q, int32_t dtype, int64_t requests, int64_t q_heads, con
             float softcap, int64_t window, const float *slopes, void *out, float *lse, int32_t *err_flag, Args *a,
             int *rows, int64_t *tiles);
 void place(Args *a, void *ws, int rows);  // the parts of the workspace
+// a.ml: of the rest
 cudaError_t launch_paged(const Args &a, int cache_dtype, int rows, int64_t tiles, cudaStream_t s, bool pdl);
 
-template <int CT, int D, int RT, bool X3>
+template <int CT, int D, int RT, bool X3, bool Rest>
 cudaError_t launch_one(const Args &a, cudaStream_t s, bool pdl, int64_t tiles) {
     using C = Cfg<CT, D, RT, X3>;
-    const auto kernel = attn_paged_kernel<CT, D, RT, X3>;
+    const auto kernel = attn_paged_kernel<CT, D, RT, X3, Rest>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), C::smem);
     if (e != cudaSuccess) return e;
     // no more CTAs than `tiles`, the most that there can be, fill
@@ -1167,17 +1171,18 @@ cudaError_t launch_one(const Args &a, cudaStream_t s, bool pdl, int64_t tiles) {
     return launch(kernel, dim3(static_cast<unsigned>(ctas)), dim3(C::threads), C::smem, s, pdl, a);
 }
 
-#define WSW_PAGED_TYPE(CT, X3)                                                                       \
-    template <>                                                                                      \
-    cudaError_t launch_type<CT, X3>(const Args &a, int rows, cudaStream_t s, bool pdl, int64_t tiles) {   \
-        switch (a.kv.head_dim * 2 + (rows == 16)) {                                                  \
-            case 128: return launch_one<CT, 64, 8, X3>(a, s, pdl, tiles);                             \
-            case 129: return launch_one<CT, 64, 16, X3>(a, s, pdl, tiles);                            \
-            case 256: return launch_one<CT, 128, 8, X3>(a, s, pdl, tiles);                            \
-            case 257: return launch_one<CT, 128, 16, X3>(a, s, pdl, tiles);                           \
-            case 512: return launch_one<CT, 256, 8, X3>(a, s, pdl, tiles);                            \
-            default: return launch_one<CT, 256, 16, X3>(a, s, pdl, tiles);                            \
-        }                                                                                            \
+#define WSW_PAGED_TYPE(CT, X3, Rest)                                                                       \
+    template <>                                                                                            \
+    cudaError_t launch_type<CT, X3, Rest>(const Args &a, int rows, cudaStream_t s, bool pdl, int64_t tiles) {  \
+        constexpr int wide = Rest ? 128 : 256;  /* a prefix's head_dim is 128 at most */                   \
+        switch (a.kv.head_dim * 2 + (rows == 16)) {                                                        \
+            case 128: return launch_one<CT, 64, 8, X3, Rest>(a, s, pdl, tiles);                            \
+            case 129: return launch_one<CT, 64, 16, X3, Rest>(a, s, pdl, tiles);                           \
+            case 256: return launch_one<CT, 128, 8, X3, Rest>(a, s, pdl, tiles);                           \
+            case 257: return launch_one<CT, 128, 16, X3, Rest>(a, s, pdl, tiles);                          \
+            case 512: return launch_one<CT, wide, 8, X3, Rest>(a, s, pdl, tiles);                          \
+            default: return launch_one<CT, wide, 16, X3, Rest>(a, s, pdl, tiles);                          \
+        }                                                                                                  \
     }
 
 }  // namespace paged

@@ -4,6 +4,6 @@
 
 namespace wsw {
 namespace paged {
-WSW_PAGED_TYPE(WSW_BF16, true)
+WSW_PAGED_TYPE(WSW_BF16, true, false)
 }  // namespace paged
 }  // namespace wsw

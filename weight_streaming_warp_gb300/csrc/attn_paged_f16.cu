@@ -4,6 +4,6 @@
 
 namespace wsw {
 namespace paged {
-WSW_PAGED_TYPE(WSW_F16, false)
+WSW_PAGED_TYPE(WSW_F16, false, false)
 }  // namespace paged
 }  // namespace wsw

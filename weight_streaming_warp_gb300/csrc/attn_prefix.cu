@@ -367,8 +367,6 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
 
     rest.first = p.first;
     rest.out = base + w.rest;
-    rest.out_dtype = WSW_F32;
-    rest.lse = nullptr;
     rest.ml = reinterpret_cast<float2 *>(base + w.ml);
     e = paged::launch_paged(rest, cache->dtype, rows, list, s, true);
     if (e != cudaSuccess) return WSW_ERR_CUDA;

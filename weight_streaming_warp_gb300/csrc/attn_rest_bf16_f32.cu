@@ -1,0 +1,9 @@
+// attn_rest_bf16_f32.cu -- the paged decode attention behind a shared prefix, over bf16 pages, fp32 queries (one
+// translation unit each: they compile side by side).
+#include "attn_paged.cuh"
+
+namespace wsw {
+namespace paged {
+WSW_PAGED_TYPE(WSW_BF16, true, true)
+}  // namespace paged
+}  // namespace wsw
