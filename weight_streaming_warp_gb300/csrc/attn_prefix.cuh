@@ -28,7 +28,7 @@
 //    cannot cross a page, and pages may have one position).  Over q8_0 four warps have K and four have V: codes
 //    and scales land in rings of their own, two or three tiles deep, and become binary16(scale * code) on the way to the
 //    tile (33 fp32 requests of 4 x 8 heads behind 32768 positions: 117 us with one set of loaders, 101 so).  A tile's
-//    barrier counts the threads whose copies have landed.
+//    barrier counts the threads whose copies have landed, and each warp's word of the tile's visible positions.
 //  * q, scores, sums and l are fp32 or parts: q over its own 16-bit type is exact, a bf16 or fp32 row
 //    over binary16 takes the power of two that brings its largest value to 2^14 .. 2^15 and, fp32, a second
 //    part (22 bits); fp16 over bf16 is two parts, fp32 over bf16 three, both exact.  P is two parts, 16 (bf16) or 22 bits
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, RT>::threads, 1) attn_prefix_ke
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&ct.full[i], C::q8 ? kLoaders : 32 * kLoaders);
+            mbar_init(&ct.full[i], C::q8 ? kLoaders : 33 * kLoaders);
             mbar_init(&ct.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -412,8 +412,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, RT>::threads, 1) attn_prefix_ke
                             cp16(dst + swizzled(lw * RW + r, c, TP), x.base + o + c * 16, (x.valid >> r) & 1);
                         }
                     }
-                    // this thread arrives once its copies have landed (the MMAs' warp has the proxy fence)
+                    // this thread arrives once its copies have landed (the MMAs' warp has the proxy fence), and the lane
+                    // that wrote the visible positions for that store, which is no copy
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(saddr(&ct.full[st])) : "memory");
+                    if (lane == 0) mbar_arrive(&ct.full[st]);
                 }
             } else {
                 // codes and scales of the warp's own rows on their way, raw_stages - 1 tiles ahead
