@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(const Plan
 }
 
 struct JoinArgs {
-    const int *run;      // [1] places of a CTA
+    const int *run;      // [1] places of a CTA; 0: a wait ran out
     const int4 *pieces;  // [requests]: query rows of its group per KV head, its own ones' place there, the group's place
                          // in the list, its prefix's positions
     const float *rec, *whole;
@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const JoinArgs a) {
     const float *r = reinterpret_cast<const float *>(&rest);
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] = r[i] * l;  // the rest comes divided by its sum
-    if (of.x > 0) {
+    if (of.x > 0 && run == 0) l = __int_as_float(0x7fc00000);
+    if (of.x > 0 && run > 0) {
         const int unit_rows = 1 << a.row_shift, nt = ((of.w - 1) >> a.tile_shift) + 1;
         const int kv = head / a.group, in = of.y + head - kv * a.group;
         const int unit = kv * (((of.x - 1) >> a.row_shift) + 1) + (in >> a.row_shift);

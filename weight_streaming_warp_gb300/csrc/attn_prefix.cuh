@@ -37,7 +37,9 @@
 //    own, 2.3e-3 in the root mean square instead of 1.7e-3; the call for the case above, with rests of 16
 //    positions, took 155 us with one part and 187 so.)
 //  * The maximum in use is raised, and O rescaled, only when a tile exceeds it by more than kLazy.
-//  * Every wait is bounded; a role whose wait ran out stops, and the rows' l is NaN.
+//  * Every wait is bounded; a role whose wait ran out stops once its own copies or MMAs have ended.  The block's later pieces
+//    are then missing, so that a word says so (blocks that start later have nothing to do) and the join makes all rows
+//    behind a prefix NaN.
 #pragma once
 
 #include "attn_paged.cuh"
@@ -67,7 +69,7 @@ struct Plan {
     const int *used;   // its prefix's positions
     const int *rep;    // the request whose table row holds its pages
     const int *stride; // places that each of its units has in the list, its tiles at least
-    const int *run;    // [1] places of a CTA
+    int *run;          // [1] places of a CTA; 0 once a wait ran out
     const int2 *start; // [kCtas] group and place in its part where a CTA's run begins; group -1: nothing
 };
 
@@ -157,7 +159,7 @@ struct Cfg {
 struct Control {
     uint64_t full[8], empty[8];
     uint64_t s_full[2], p_full[2][2];  // of a slot; of each half of its weights
-    uint64_t q_full, o_done;
+    uint64_t q_full, o_done, stopped;
     uint32_t seen[kSeen][4];
     float unit[256];    // of the rows' scores
     uint32_t tmem;
@@ -288,6 +290,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, RT>::threads, 1) attn_prefix_ke
         }
         mbar_init(&ct.q_full, 8);
         mbar_init(&ct.o_done, 1);
+        mbar_init(&ct.stopped, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == C::mma_warp) {
@@ -567,6 +570,10 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, RT>::threads, 1) attn_prefix_ke
                     }
                 }
                 if (ok) commit(&ct.o_done);
+            }
+            if (!ok) {  // what was issued reads shared memory and writes tensor memory
+                commit(&ct.stopped);
+                wait(&ct.stopped, 0);
             }
         }
     } else {
@@ -855,7 +862,6 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, RT>::threads, 1) attn_prefix_ke
             const bool have = both_agree(ok);
             ok = have;
             tc_fence_after();
-            if (!have) l = __int_as_float(0x7fc00000);
             float *rec = w.whole() ? a.whole + head * C::rec
                                    : a.rec + ((static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 == 0)) * RT +
                                               (RT == 2 ? slot : 0)) * 128 * C::rec + r * C::rec;
@@ -893,6 +899,7 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, RT>::threads, 1) attn_prefix_ke
             // both have read the sums and O before the next piece's
             if (RT == 1) asm volatile("bar.sync 1, 256;" ::: "memory");
         }
+        if (!ok && tid == 0) *a.plan.run = 0;
     }
     tc_fence_before();
     __syncthreads();
