@@ -21,3 +21,12 @@ def test_many_groups_of_short_first_rows():
     c = Case(need_gpu(), [(20 + g % 40, [g % 19] * (g % 5) + _lens(20 + g % 40, 1, g % 3)) for g in range(700)], kvh=1, group=1, d=64,
              q="fp16", cache="fp16")
     c.check()
+
+
+def test_heads_and_groups_near_the_limit():
+    """11900 KV heads and room for 16384 groups, of which one has requests: within the stated limit for 32 positions."""
+    c = Case(need_gpu(), [(8, [10, 12])], kvh=11900, group=1, d=64, q="fp16", cache="fp16")
+    assert c.table.shape[1] * c.page == 32
+    c.cu_d = torch.cat([c.cu_d, c.cu_d[-1:].expand(16383)]).contiguous()
+    c.prefix_d = torch.cat([c.prefix_d, c.prefix_d.expand(16383)]).contiguous()
+    c.check()

@@ -325,9 +325,10 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
         (reinterpret_cast<uintptr_t>(ws) & 255))
         return WSW_ERR_MISALIGNED;
     const int64_t kv_heads = cache->heads, group = rest.group;
-    // the longest list, of tiles of 64 positions or more: places are counted in 32 bits
+    // places of the longest list, units * (longest + kPiece) of tiles of 64 positions or more, are counted in 32 bits; the limit
+    // is above them, longest <= max_len / 64 + 1
     const int64_t units = kv_heads * (requests * group / 128 + groups), longest = (rest.max_len + 63) / 64;
-    if (requests * q_heads > (int64_t(1) << 30) || units * (4 * longest + kPiece + 1) >= (int64_t(1) << 31) - 65536)
+    if (requests * q_heads > (int64_t(1) << 30) || units * (rest.max_len / 16 + 9) >= (int64_t(1) << 31) - 65536)
         return WSW_ERR_UNSUPPORTED;
     const Room w = room(requests, groups, q_heads, kv_heads, cache->head_dim);
     if (ws_bytes < w.bytes) return WSW_ERR_WORKSPACE;
