@@ -50,3 +50,25 @@ def test_a_cap_far_above_the_scores_changes_nothing():
     for softcap in (1e6, 1e8, 1e12):
         out, lse = c.run(0.1, softcap=softcap)
         assert float((out - want).abs().max()) < 2e-4 and float((lse - want_lse).abs().max()) < 1e-4
+
+
+@pytest.mark.parametrize("softcap", [1e-30, 1e-37, 5e-38, 1e-39, 1e-44])
+@pytest.mark.parametrize("q,cache", [("fp32", "fp16"), ("bf16", "bf16"), ("bf16", "q8_0")])
+def test_caps_below_every_score(softcap, q, cache):
+    """Every score is +-softcap, next to nothing, or 0: the values' mean, for queries of zeros, too."""
+    wsw = need_gpu()
+    c = Case(wsw, [(300, [300 + i for i in (0, 3, 40)])], kvh=2, group=4, q=q, cache=cache, seed=7)
+    c.q[1] = 0
+    c.q[2, 3] = 0
+    for scale in (0.1, -3.0):
+        for share in (True, False):
+            out, lse = c.run(scale, softcap=softcap, share=share)
+            for r, n in enumerate(c.lens):
+                p = np.arange(n)
+                rows = c.table[r].numpy()[p // c.page] * c.page + p % c.page
+                want = np.repeat(c.vals[1][rows].mean(0), c.group, 0)
+                mag = np.abs(c.vals[1][rows]).mean(0).max()
+                # weights and their sums: (300 / 16 + 192) 2^-23 and 2^-16 for the parts; then the result's rounding
+                lim = mag * (211 * 2.0 ** -23 + 2.0 ** -16) + n * 2.0 ** -32 * mag
+                assert (np.abs(out[r].double().cpu().numpy() - want) <= lim + STEP[q] * (np.abs(want) + lim)).all(), r
+                assert (np.abs(lse[r].double().cpu().numpy() - np.log(n)) <= 211 * 2.0 ** -23 + 2.0 ** -22 * 6).all(), r

@@ -77,7 +77,10 @@ int prepare(const void *q, int32_t dtype, int64_t requests, int64_t q_heads, con
     a.scale2 = scale * kLog2e;
     // A cap so large that softcap log2 e or scale / softcap leaves fp32's normal range bends only scores of
     // |q . K| above 2^114: none.  (As a cap, inf * tanh(0) made every result NaN.)
-    const float in = softcap > 0.f ? scale / softcap : 0.f;
+    // A cap so small that scale / softcap, or its product with 2 log2 e, leaves it at the other end cuts every score but 0, to +-
+    // softcap: a quarter of the largest value does the same.  (As it was, 0 * inf made rows of zeros NaN.)
+    const float most_in = FLT_MAX / 4;
+    const float in = softcap > 0.f ? std::fmin(std::fmax(scale / softcap, -most_in), most_in) : 0.f;
     const bool capped = std::isfinite(softcap * kLog2e) && std::fabs(in) >= FLT_MIN;
     a.cap_in = capped ? in : 0.f;
     a.cap_out = capped ? softcap * kLog2e : 0.f;
