@@ -970,6 +970,8 @@ def beam_select(logits, scores, end_tokens=(), scale=1.0, out=None, ws=None, opt
         raise WswError("scores must be [requests][beams], logits [requests * beams][vocab]")
     n, beams = shape
     ends = (_i32 * len(end_tokens))(*end_tokens) if end_tokens else None
+    if ends and ends[:] != list(end_tokens):
+        raise WswError("end tokens must fit into 32 bits")
     if out is None:
         out = beam_select_out(n, beams, logits.device)
     if ws is None:
