@@ -906,7 +906,7 @@ def kv_page_compact(seq_len, table, page_size, num_pages, held=None, max_moves=0
     up to max_moves live pages behind the others also move into the gaps, the table follows and
     copies names the pages, which kv_page_copy has to copy before the cache is used again.
     Returns a KvCompact, whose table is `table` itself, updated in place; out = one to fill, in
-    which table may lie elsewhere.  ws: a uint8 device tensor of at least
+    which table may lie elsewhere (it is written when max_moves is not 0).  ws: a uint8 device tensor of at least
     kv_page_compact_workspace_bytes(num_pages) bytes, allocated if None."""
     dev = _home(seq_len, "seq_len")
     sp = _packed(seq_len, _I32, "seq_len", dev)

@@ -23,9 +23,9 @@ namespace {
 constexpr int kMaxGroups = 16384;  // three words of shared memory each
 constexpr int kPlanThreads = 1024;
 constexpr int64_t kEachBytes = int64_t(128) << 20;
-// Tiles that a piece costs.  16 x 4 requests of 4 x 8 heads behind 4096 positions, bf16: 55 us with none, 53 with 3, 51 with 7 and 14;
-// 1 x 256 behind 8192, q8_0: 84, 81, 78, 80.  (CTAs with a single piece each, where there are enough for that: 16 x 4 51 us, 45
-// without, for the longer plan alone 3 us.)
+// Tiles that a piece costs.  16 x 4 requests of 4 x 8 heads behind 4096 positions, bf16: 57 us with none, 56 with 3, 54 with 7, 55 with
+// 14; 1 x 256 behind 8192, q8_0: 89, 85, 84, 85.  (CTAs with a single piece each, where there are enough for that, lengthened
+// the plan: 6 us more for 16 x 4.)
 constexpr int kPiece = 7;
 
 // Parts of q by types.
@@ -36,8 +36,8 @@ int q_parts(int dtype, int cache) {
 // Row tiles of a unit.  Two read K and V half as often, for groups of more than 128 rows a head (several parts of q would leave
 // no room for the ring), but an SM's two slots then work on one tile: they pay from some kRowTiles tiles of 128 rows and
 // 128 positions for each SM.  4 heads of 128, bf16, group 8, us with one and with two: 32 requests behind 8192 / 32768
-// positions 29 / 46 and 35 / 54 (3 / 13 tiles), 64 behind 32768 59.5 and 58.8 (27), 128 behind 8192 / 16384 / 32768 38 / 55 / 88
-// and 40 / 52 / 77 (13 / 27 / 54), 256 behind 32768 152 and 123 (108).
+// positions 31 / 50 and 37 / 58 (3 / 13 tiles), 64 behind 32768 65 and 66 (27), 128 behind 8192 / 16384 / 32768 41 / 59 / 96
+// and 44 / 59 / 92 (13 / 27 / 54), 256 behind 32768 166 and 153 (108).
 constexpr int kRowTiles = 20;
 int row_tiles(int64_t requests, int64_t group, int64_t groups, int parts, int64_t heads, int64_t max_len) {
     const int64_t rows = requests * group;
@@ -338,9 +338,10 @@ extern "C" int wsw_attn_paged_prefix(const void *q, int32_t dtype, int64_t reque
     unsigned char *base = static_cast<unsigned char *>(ws);
     paged::place(&rest, ws, rows);
     // What all requests list of a prefix comes from HBM once anyhow while it stays in L2, and four launches cost 9 us
-    // more than one: 4 heads of 128, bf16, group 8, one prefix of 8192 for 4 / 8 / 16 requests (68 / 135 / 271 MB in all) 29 /
-    // 30 / 31 us shared and 21 / 27 / 40 each on its own; 16 prefixes of 1024 / 2048 for 4 each (143 / 277 MB) 28 / 32 and 28.5 /
-    // 42; fp32 over q8_0, 8 requests behind 8192 (72 MB) 41 and 31.
+    // more than one: 4 heads of 128, bf16, group 8, one prefix of 8192 for 4 / 8 / 16 requests (68 / 135 / 271 MB in all) 30 /
+    // 31 / 32 us shared and 22 / 25 / 39 each on its own; 16 prefixes of 1024 / 2048 / 4096 for 4 each (143 / 277 / 546 MB) 31 /
+    // 37 / 53 and 25 / 38 / 60; fp32 over q8_0, 8 / 16 / 32 requests behind 8192 (72 / 143 / 286 MB) 39 / 41 / 42 and 31 / 42 / 65.
+    // Lengths stay on the device: the table's width stands for them.
     const int64_t row_bytes = 2 * kv_heads * (cache->dtype == WSW_Q8_0 ? cache->head_dim * 17 / 16 : cache->head_dim * 2);
     if (!share && requests * static_cast<int64_t>(rest.max_len) <= kEachBytes / row_bytes)
         return paged::launch_paged(rest, cache->dtype, rows, list, s, o.pdl) == cudaSuccess ? WSW_OK : WSW_ERR_CUDA;

@@ -8,9 +8,10 @@
 //
 // The query heads of all of a group's requests that share a KV head are the rows of one product:
 // 4 D flops per row and position against 4 D bytes (16 bits) per position, so that a few hundred rows are
-// bound by the tensor cores, a few by HBM.  256 requests of 4 x 8 heads behind 32768 positions, bf16: 95 us of this
-// kernel, 1.4 PFLOP/s; a tile of 128 rows and 128 positions takes 3100 cycles where its products take 2048: the two
-// slots' softmax (one exponential for each score, 16 a cycle) and products do not overlap all the time.
+// bound by the tensor cores, a few by HBM.  256 requests of 4 x 8 heads behind 32768 positions, bf16: some 128 us of this
+// kernel, 1.6 PFLOP/s with the weights' second part counted; two tiles of 128 rows by 128 positions take 4400 cycles under a
+// profiler where their products take 3072: the two slots' softmax (one exponential for each score, 16 a cycle) and products do
+// not overlap all the time.
 //
 //  * A unit is a tile of rows (kv head, 128 or 256 of a group's rows); the position tiles of all units,
 //    in order, are one list that is cut into equal runs for 152 CTAs, one on an SM (attn_prefix.cu has the rules).  A CTA leaves
@@ -22,12 +23,12 @@
 //    piece ends.  One's softmax runs while the tensor cores work for the other.
 //  * The weights P go back to tensor memory over the scores, whose thread has read them; S of the next
 //    tile is issued behind the P V that reads them, and one thread's MMAs complete in order.  The P V of a tile's
-//    first half runs while the second half's weights are made (170 us for the case above without, 162 with).
+//    first half runs while the second half's weights are made (with P in one part, 170 us for the case above without, 162 with).
 //  * Four warps copy K and V rows with cp.async into a ring of tiles, swizzled as the MMAs want them:
 //    16-byte pieces by the block table, so that any page size, layout and stride is the same code (a TMA box
 //    cannot cross a page, and pages may have one position).  Over q8_0 four warps have K and four have V: codes
 //    and scales land in rings of their own, two or three tiles deep, and become binary16(scale * code) on the way to the
-//    tile (33 fp32 requests of 4 x 8 heads behind 32768 positions: 117 us with one set of loaders, 101 so).  A tile's
+//    tile (33 fp32 requests of 4 x 8 heads behind 32768 positions: 117 us with one set of loaders, 101 so, and 91 since).  A tile's
 //    barrier counts the threads whose copies have landed, and each warp's word of the tile's visible positions.
 //  * q, scores, sums and l are fp32 or parts: q over its own 16-bit type is exact, a bf16 or fp32 row
 //    over binary16 takes the power of two that brings its largest value to 2^14 .. 2^15 and, fp32, a second
@@ -762,8 +763,9 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, RT>::threads, 1) attn_prefix_ke
                 auto ref_of = [&] { return m == -INFINITY ? 0.f : m - C::shift; };  // nothing seen yet: all weights 0
                 if (plain) {
                     // Two chunks of scores stay in registers, the others are read twice, a chunk at a time (weights take no
-                    // other chunk's place, or both chunks' of 64 positions).  With P in one part, 256 requests behind 32768 positions: 157 us; three chunks 162, four 163,
-                    // the second half on its way while the first half's weights are made 163.
+                    // other chunk's place, or both chunks' of 64 positions).  With P in one part, 256 requests behind 32768
+                    // positions: 157 us; three chunks 162, four 163, the second half on its way while the first half's
+                    // weights are made 163.
                     uint32_t v[2][32];
                     float mx = -INFINITY;
 #pragma unroll
