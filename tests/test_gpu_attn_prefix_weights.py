@@ -52,3 +52,30 @@ def test_weights_in_two_parts(q, cache, per, group, wide):
             lim = mag * (2 * e + (2.0 ** -16 if half else 2.0 ** -22) + sums) + n * 2.0 ** -32 * np.abs(v).max()
             bad = np.abs(got[r] - want) - (lim + STEP[q] * (np.abs(want) + lim) + 2.0 ** -25)
             assert (bad <= 0).all(), "request %d: over by %.3g of %.3g" % (r, bad.max(), lim.max())
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_positive_products(cache, d):
+    """fp32 queries enter in two or three parts, the small ones first.  Sums of positive products grow evenly over the n = d / 16
+    steps of the large part, to k / n of the score behind step k.  A step cuts its sum to fp32's bits (that it cuts half a
+    last place in the mean does not hold: its addends are cut before they are added), so that it is off by less than a last
+    place, 2^-23 of the sum so far: (1 + 2 + .. + n) / n = (n + 1) / 2 times 2^-23 of the score.  Were the small parts added
+    behind, each of their n or 2 n steps would cut the whole score.  The lse's other roundings have either sign: their mean
+    over 256 rows is below 2^-24."""
+    wsw = need_gpu()
+    c = Case(wsw, [(100, [100] * 32)], kvh=2, group=4, d=d, q="fp32", cache=cache, junk=0.0)
+    c.q = c.q.abs() + 0.5
+    k = c.kv.k.view(-1, 2, d)
+    k.copy_(k.abs() + 0.5)
+    vals = k.double().cpu().numpy()
+    rows = c.table[0].numpy()[np.arange(100) // c.page] * c.page + np.arange(100) % c.page
+    q = c.q.double().numpy().reshape(32, 2, 4, d)
+    scale = 40.0 / float(np.einsum("rhgd,phd->rhgp", q, vals[rows]).mean())
+    _, lse = c.run(scale)
+    scale = float(np.float32(scale))
+    x = np.einsum("rhgd,phd->rhgp", q, vals[rows]) * scale
+    m = x.max(-1, keepdims=True)
+    want = (m[..., 0] + np.log(np.exp(x - m).sum(-1))).reshape(32, 8)
+    off = (lse.double().cpu().numpy() - want) / want
+    assert abs(off.mean()) <= (d / 16 + 1) / 2 * 2.0 ** -23 + 2.0 ** -24, off.mean() * 2.0 ** 24

@@ -509,15 +509,16 @@ __global__ void __launch_bounds__(Cfg<CT, D, QP, RT>::threads, 1) attn_prefix_ke
                 const uint64_t dq = sw128_desc(qt), dk = sw128_desc(kt);
                 const uint32_t d = tmem + slot * C::s_cols;
                 tc_fence_after();
+                // q's last part first: an MMA's sum is cut to fp32's bits, which costs nothing while the sum is small
                 if (elect_one()) {
 #pragma unroll
-                    for (int part = 0; part < QP; ++part)
+                    for (int part = QP - 1; part >= 0; --part)
 #pragma unroll
                         for (int b = 0; b < D / 64; ++b)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 mma_bf16(d, dq + ((part * C::q_part + b * 128 * 128) >> 4) + 2 * kk,
-                                         dk + ((b * TP * 128) >> 4) + 2 * kk, id_s, (part | b | kk) != 0);
+                                         dk + ((b * TP * 128) >> 4) + 2 * kk, id_s, part < QP - 1 || (b | kk) != 0);
                 }
                 __syncwarp();
             };
