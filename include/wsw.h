@@ -742,7 +742,7 @@ int wsw_kv_page_compact(const int32_t *seq_len, int64_t requests, const int32_t 
  * wsw_beam_select -- the next beams of every request from the logits of all its beams, in one
  * pass.  With x[b] the row of beam b (row request * beams + b of the logits), y = scale * x,
  *   s[b][j] = scores[b] + y[b][j] - ln sum_i exp(y[b][i])
- * The candidates (b, j) with finite s are taken in descending order of s, equal ones by the
+ * The candidates (b, j) with s finite in fp32 are taken in descending order of s, equal ones by the
  * lower b, then the lower j, until `beams` of them do not end: those are the next beams, in that
  * order.  A candidate ends if its token is one of end_tokens; it is reported as an ended one
  * if fewer than `beams` candidates come before it.

@@ -61,3 +61,27 @@ def test_uneven_rows_at_every_alignment(kind, order):
     else:
         x[..., 20000:23000] += 6
     _check(wsw, x.to(T[kind]).contiguous(), _scores(2, 1, 9), [vocab - 1])
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_masks_of_the_lowest_value(kind):
+    """Tokens masked by the type's lowest value are candidates behind all others while their scores are finite in fp32, by
+    the lower token; a scale above 1 takes them out of fp32's range: none."""
+    wsw = need_gpu()
+    low = torch.finfo(T[kind]).min
+    x = torch.full((6, 5000), low, dtype=T[kind], device="cuda")
+    x[:, 4000], x[:, 17] = 3, 1
+    s = torch.tensor([[-1.0, -2, -3], [-1.0, -1, -1]], device="cuda")
+    r = wsw.beam_select(x[:3, :600], s[:1])  # one token of each row is allowed
+    assert r.parent.tolist() == [[0, 1, 2]] and r.token.tolist() == [[17] * 3] and r.score.tolist() == [[-1, -2, -3]]
+    one = x.clone()
+    one[1:3], one[4:] = low, low
+    s[0, 1:] = -math.inf
+    r = wsw.beam_select(one, s)
+    assert r.token[0].tolist() == [4000, 17, 0] and float(r.score[0, 2]) < -3e38 and r.parent[0].tolist() == [0] * 3
+    # rows of nothing else are even: ln 5000 below their scores
+    assert r.parent[1].tolist() == [3, 3, 4] and r.token[1].tolist() == [4000, 17, 0]
+    assert abs(float(r.score[1, 2]) + 1 + math.log(5000)) < 1e-5
+    r = wsw.beam_select(one, s, scale=2.0)
+    assert r.token[0].tolist() == [4000, 17, -1] and r.parent[0].tolist() == [0, 0, -1] and float(r.score[0, 2]) == -math.inf
+    assert r.parent[1].tolist() == [3, 3, 4] and r.token[1].tolist() == [4000, 17, 0]
