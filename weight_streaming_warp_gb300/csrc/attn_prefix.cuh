@@ -9,9 +9,9 @@
 // The query heads of all of a group's requests that share a KV head are the rows of one product:
 // 4 D flops per row and position against 4 D bytes (16 bits) per position, so that a few hundred rows are
 // bound by the tensor cores, a few by HBM.  256 requests of 4 x 8 heads behind 32768 positions, bf16: some 128 us of this
-// kernel, 1.6 PFLOP/s with the weights' second part counted; two tiles of 128 rows by 128 positions take 4400 cycles under a
-// profiler where their products take 3072: the two slots' softmax (one exponential for each score, 16 a cycle) and products do
-// not overlap all the time.
+// kernel, 1.6 PFLOP/s with the weights' second part counted; the products keep the tensor cores busy for 70% of the
+// cycles under a profiler: the two slots' softmax (one exponential for each score, 16 a cycle) and products do not overlap
+// all the time.
 //
 //  * A unit is a tile of rows (kv head, 128 or 256 of a group's rows); the position tiles of all units,
 //    in order, are one list that is cut into equal runs for 152 CTAs, one on an SM (attn_prefix.cu has the rules).  A CTA leaves
